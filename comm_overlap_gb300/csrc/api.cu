@@ -9,6 +9,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <functional>
 #include <string>
 #include <vector>
 
@@ -85,7 +86,8 @@ struct NvtxChunk {
 const char* kernel_kind_name(int kind) {
   static const char* const names[DOMINO_K_COUNT] = {"gemm_fwd1", "gemm_fwd2", "shard_sum", "layernorm",
                                                      "gemm_dgrad_h", "gemm_wgrad_b", "gemm_dgrad_x", "gemm_wgrad_a",
-                                                     "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj"};
+                                                     "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj",
+                                                     "ln_affine", "ln_affine_bwd"};
   return (kind >= 0 && kind < DOMINO_K_COUNT) ? names[kind] : "kernel";
 }
 
@@ -982,6 +984,11 @@ void set_last_error(const std::string& msg) { t_last_error = msg; }
 // The handle checks every entry point starts with (non-null, bound to the current device), for
 // other translation units of the library.
 domino_status check_handle(domino_handle H) { return ready(H); }
+int handle_sms(domino_handle H) { return H->num_sms; }
+domino_status launch_on(domino_handle H, int kind, cudaStream_t st, const char* what,
+                        const std::function<cudaError_t()>& fn) {
+  return launch(H, kind, st, what, fn);
+}
 }  // namespace dm
 
 // =============================================================================================

@@ -21,9 +21,11 @@ ACT_NONE, ACT_RELU, ACT_GELU, ACT_SWIGLU, ACT_BILINEAR = 0, 1, 2, 3, 4
 SCHED_SERIAL, SCHED_INTRA, SCHED_INTER, SCHED_FUSED = 0, 1, 2, 3
 PASS_FWD, PASS_BWD, PASS_STACK, PASS_STACK_BWD, PASS_ATTN, PASS_BLOCK, PASS_FWD_FP8 = 0, 1, 2, 3, 4, 5, 6
 (K_GEMM_FWD1, K_GEMM_FWD2, K_SHARD_SUM, K_LAYERNORM, K_GEMM_DGRAD_H, K_GEMM_WGRAD_B, K_GEMM_DGRAD_X,
- K_GEMM_WGRAD_A, K_LN_BWD, K_GEMM_QKV, K_ATTN, K_GEMM_OPROJ) = range(12)
+ K_GEMM_WGRAD_A, K_LN_BWD, K_GEMM_QKV, K_ATTN, K_GEMM_OPROJ, K_LN_AFFINE,
+ K_LN_AFFINE_BWD) = range(14)
 KERNEL_NAMES = ["gemm_fwd1", "gemm_fwd2", "shard_sum", "layernorm", "gemm_dgrad_h", "gemm_wgrad_b",
-                "gemm_dgrad_x", "gemm_wgrad_a", "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj"]
+                "gemm_dgrad_x", "gemm_wgrad_a", "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj",
+                "ln_affine", "ln_affine_bwd"]
 
 
 class DominoError(RuntimeError):
@@ -49,6 +51,8 @@ _lib = None
 _lock = threading.Lock()
 _P = ctypes.c_void_p
 _S = ctypes.c_int32
+_I64 = ctypes.c_int64
+_N = ctypes.c_size_t
 
 _SIGS = {
     "domino_create": [ctypes.POINTER(ctypes.c_void_p)],
@@ -69,6 +73,10 @@ _SIGS = {
     "domino_block_fwd": [_P, ctypes.POINTER(domino_cfg), _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "domino_shard_sum": [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, _P,
                          ctypes.c_int64, _P],
+    "domino_layernorm_fwd": [_P, _P, _I64, _P, _P, ctypes.c_float, _P, _I64, _P, _P, _I64, _I64, _P],
+    "domino_layernorm_bwd_workspace_size": [_I64, _I64, ctypes.POINTER(_N)],
+    "domino_layernorm_bwd": [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _I64, _I64, _P, _N,
+                             _P],
     "domino_act_eval": [ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_int64, _P],
     "domino_device_status": [_P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)],
     "domino_timing_enable": [_P, ctypes.c_int32],
@@ -222,6 +230,25 @@ def domino_stack_bwd(handle, cfg, A, B, save, gZ_out, gZ_in, gA, gB, workspace, 
 
 def domino_shard_sum(P, t, rows, cols, residual, ld_res, Y, ld_y, stream=None) -> None:
     _check(lib().domino_shard_sum(_ptr(P), t, rows, cols, _ptr(residual), ld_res, _ptr(Y), ld_y, _stream(stream)))
+
+
+def domino_layernorm_fwd(handle, X, ld_x, gamma, beta, eps, Y, ld_y, mean, rstd, rows, h, stream=None) -> None:
+    _check(lib().domino_layernorm_fwd(handle, _ptr(X), ld_x, _ptr(gamma), _ptr(beta), eps, _ptr(Y), ld_y, _ptr(mean),
+                                      _ptr(rstd), rows, h, _stream(stream)))
+
+
+def domino_layernorm_bwd_workspace_size(rows, h) -> int:
+    n = _N()
+    _check(lib().domino_layernorm_bwd_workspace_size(rows, h, ctypes.byref(n)))
+    return n.value
+
+
+def domino_layernorm_bwd(handle, gY, ld_gy, X, ld_x, gamma, mean, rstd, gres, ld_gres, gX, ld_gx, ggamma, gbeta,
+                         accumulate, rows, h, workspace, workspace_bytes=None, stream=None) -> None:
+    _check(lib().domino_layernorm_bwd(handle, _ptr(gY), ld_gy, _ptr(X), ld_x, _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                      _ptr(gres), ld_gres, _ptr(gX), ld_gx, _ptr(ggamma), _ptr(gbeta), accumulate,
+                                      rows, h, _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                      _stream(stream)))
 
 
 def domino_act_eval(act, a, b, out, da, db, n, stream=None) -> None:

@@ -1,0 +1,179 @@
+"""PyTorch functions and modules around the sublayer operators (argument marshalling only).
+
+The operators of a pre-LN block outside the sharded MLP: LayerNorm with weight and bias.  Each has
+plain functions that allocate their outputs and call the C ABI (`layer_norm_fwd`, `layer_norm_bwd`),
+a differentiable function (`layer_norm`) and a module (`DominoLayerNorm`).  Every step of the
+computation runs in the library's kernels; tensors must be on one CUDA device, matrices bf16.
+
+Calls run on the current stream of the tensors' device.  Workspaces come from PyTorch's allocator for
+each call, so calls on several streams, and several captured graphs, share none.  One library handle
+per device serves all threads; a lock is held while a call enqueues its kernels.
+"""
+from __future__ import annotations
+
+import threading
+
+import torch
+
+from . import domino as dm
+
+_handles: dict[int, int] = {}
+_lock = threading.Lock()
+
+
+class _call:
+    """The device of `x` made current, its handle, and the lock under which handles are used."""
+
+    def __init__(self, x: torch.Tensor):
+        self.device = torch.cuda.device(x.device)
+
+    def __enter__(self) -> int:
+        _lock.acquire()
+        try:
+            self.device.__enter__()
+            index = torch.cuda.current_device()
+            h = _handles.get(index)
+            if h is None:
+                h = _handles[index] = dm.domino_create()
+            return h
+        except BaseException:
+            _lock.release()
+            raise
+
+    def __exit__(self, *exc):
+        self.device.__exit__(*exc)
+        _lock.release()
+        return False
+
+
+def _check(name: str, x: torch.Tensor, like: torch.Tensor | None = None, shape=None, dtype=torch.bfloat16) -> None:
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {x.dtype}")
+    if like is not None and x.device != like.device:
+        raise ValueError(f"{name} is on {x.device}, not on {like.device}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+
+
+def _rows(x: torch.Tensor) -> tuple[torch.Tensor, int]:
+    """A 2-D tensor whose rows the library can stride over, and that stride: `x` itself where its rows
+    are contiguous, 16-byte aligned and do not overlap, else a copy."""
+    n, c = x.shape
+    if (c <= 1 or x.stride(1) == 1) and x.data_ptr() % 16 == 0:
+        if n <= 1:
+            return x, c
+        if x.stride(0) >= c and x.stride(0) % 8 == 0:
+            return x, x.stride(0)
+    return x.clone(memory_format=torch.contiguous_format), c
+
+
+def _vec(x: torch.Tensor | None) -> torch.Tensor | None:
+    """A vector the library can read: contiguous and 16-byte aligned."""
+    if x is None or (x.is_contiguous() and x.data_ptr() % 16 == 0):
+        return x
+    return x.clone(memory_format=torch.contiguous_format)
+
+
+def _matrix(name: str, x: torch.Tensor) -> None:
+    _check(name, x)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {x.dim()}")
+
+
+# ---- LayerNorm -----------------------------------------------------------------------------------
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
+    """LayerNorm of each row of x [rows, h] (bf16) with weight and bias (bf16): (y, mean, rstd), the last
+    two fp32, for `layer_norm_bwd`."""
+    _matrix("x", x)
+    rows, h = x.shape
+    _check("weight", weight, x, (h,))
+    if bias is not None:
+        _check("bias", bias, x, (h,))
+    x, ld = _rows(x)
+    weight, bias = _vec(weight), _vec(bias)
+    y = torch.empty((rows, h), dtype=torch.bfloat16, device=x.device)
+    mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    with _call(x) as handle:
+        dm.domino_layernorm_fwd(handle, x, ld, weight, bias, eps, y, h, mean, rstd, rows, h)
+    return y, mean, rstd
+
+
+def layer_norm_bwd(gy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                   gres: torch.Tensor | None = None, grads: tuple | None = None, bias_grad: bool = True):
+    """Gradients of `layer_norm_fwd`: (gx, gweight, gbias), gx bf16 (with `gres`, the gradient of a
+    residual connection around the LayerNorm, added before its rounding), the others fp32.  `grads`, a
+    pair of fp32 buffers, is added to instead of allocated (main_grad accumulation)."""
+    _matrix("gy", gy)
+    _matrix("x", x)
+    rows, h = x.shape
+    _check("gy", gy, x, (rows, h))
+    _check("weight", weight, x, (h,))
+    _check("mean", mean, x, (rows,), torch.float32)
+    _check("rstd", rstd, x, (rows,), torch.float32)
+    if gres is not None:
+        _check("gres", gres, x, (rows, h))
+    if grads is not None:
+        gw, gb = grads
+        for name, g in (("weight", gw), ("bias", gb)):
+            if g is None and name == "bias":
+                continue
+            _check(f"the {name}'s gradient buffer", g, x, (h,), torch.float32)
+            if not g.is_contiguous() or g.data_ptr() % 16:
+                raise ValueError(f"the {name}'s gradient buffer must be contiguous and 16-byte aligned")
+    else:
+        gw = torch.empty(h, dtype=torch.float32, device=x.device)
+        gb = torch.empty(h, dtype=torch.float32, device=x.device) if bias_grad else None
+    gy, ld_gy = _rows(gy)
+    x, ld_x = _rows(x)
+    ld_r = h
+    if gres is not None:
+        gres, ld_r = _rows(gres)
+    weight, mean, rstd = _vec(weight), _vec(mean), _vec(rstd)
+    gx = torch.empty((rows, h), dtype=torch.bfloat16, device=x.device)
+    n = dm.domino_layernorm_bwd_workspace_size(rows, h)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    with _call(x) as handle:
+        dm.domino_layernorm_bwd(handle, gy, ld_gy, x, ld_x, weight, mean, rstd, gres, ld_r, gx, h, gw, gb,
+                                int(grads is not None), rows, h, ws, n)
+    return gx, gw, gb
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        y, mean, rstd = layer_norm_fwd(x, weight, bias, eps)
+        ctx.save_for_backward(x, weight, mean, rstd)
+        ctx.bias = bias is not None
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        x, weight, mean, rstd = ctx.saved_tensors
+        gx, gw, gb = layer_norm_bwd(gy, x, weight, mean, rstd, bias_grad=ctx.bias)
+        return gx, gw.to(weight.dtype), gb.to(weight.dtype) if ctx.bias else None, None
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
+    """Differentiable LayerNorm over the last dimension of x [..., h] (bf16)."""
+    _check("x", x)
+    return _LayerNorm.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps).view(x.shape)
+
+
+class DominoLayerNorm(torch.nn.Module):
+    """LayerNorm over the last dimension with bf16 weight and bias."""
+
+    def __init__(self, h: int, eps: float = 1e-5, bias: bool = True, device: str | torch.device = "cuda"):
+        super().__init__()
+        self.h, self.eps = h, eps
+        self.weight = torch.nn.Parameter(torch.ones(h, dtype=torch.bfloat16, device=device))
+        self.bias = torch.nn.Parameter(torch.zeros(h, dtype=torch.bfloat16, device=device)) if bias else None
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        if x.shape[-1] != self.h:
+            raise ValueError(f"x must have {self.h} columns")
+        return layer_norm(x, self.weight, self.bias, self.eps)

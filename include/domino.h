@@ -272,6 +272,31 @@ DOMINO_API domino_status domino_block_fwd(domino_handle handle, const domino_cfg
                                           const uint16_t* B, uint16_t* Z_out, void* workspace,
                                           size_t workspace_bytes, void* stream);
 
+/* LayerNorm with weight and bias, each row on its own:
+ *   Y = (X - mean) rstd gamma + beta,  rstd = 1 / sqrt(var + eps)  (biased variance),
+ * in fp32 with one rounding to bf16.  X, Y: rows x h with row strides ld_x, ld_y (elements, multiples
+ * of 8); Y may be X.  gamma, beta: h bf16 (beta nullable: no bias).  mean, rstd (nullable): rows fp32
+ * each, what domino_layernorm_bwd needs.  h: a multiple of 8, at most 16384; rows may be 0. */
+DOMINO_API domino_status domino_layernorm_fwd(domino_handle handle, const uint16_t* X, int64_t ld_x,
+                                              const uint16_t* gamma, const uint16_t* beta, float eps, uint16_t* Y,
+                                              int64_t ld_y, float* mean, float* rstd, int64_t rows, int64_t h,
+                                              void* stream);
+
+/* Backward of domino_layernorm_fwd.  With n = (X - mean) rstd and u = gY gamma:
+ *   gX = bf16( gres + rstd (u - mean(u) - n mean(u n)) )   (gres, the gradient arriving through a
+ *        residual connection, is nullable; gX may be gY or gres),
+ *   ggamma = sum over rows of gY n,  gbeta = sum over rows of gY   (fp32, h each; gbeta nullable),
+ * written (accumulate = 0) or added to what the buffers hold (accumulate = 1).  The sums' order is
+ * fixed: equal inputs give equal bits.  With rows = 0 the sums are zero.  Workspace:
+ * domino_layernorm_bwd_workspace_size() bytes. */
+DOMINO_API domino_status domino_layernorm_bwd_workspace_size(int64_t rows, int64_t h, size_t* bytes);
+DOMINO_API domino_status domino_layernorm_bwd(domino_handle handle, const uint16_t* gY, int64_t ld_gy,
+                                              const uint16_t* X, int64_t ld_x, const uint16_t* gamma,
+                                              const float* mean, const float* rstd, const uint16_t* gres,
+                                              int64_t ld_gres, uint16_t* gX, int64_t ld_gx, float* ggamma,
+                                              float* gbeta, int32_t accumulate, int64_t rows, int64_t h,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* The reduction step alone (the AllReduce stand-in):
  *   Y[r, c] = bf16( (residual[r, c]) + (((P_0[r,c] + P_1[r,c]) + ...) + P_{t-1}[r,c]) )
  * P: t slices of rows x cols fp32, slice i at P + i*rows*cols, row stride cols.
@@ -309,7 +334,9 @@ typedef enum {
   DOMINO_K_GEMM_QKV = 9,    /* fused query/key/value projection of the attention sublayer */
   DOMINO_K_ATTN = 10,       /* causal multi-head attention */
   DOMINO_K_GEMM_OPROJ = 11, /* attention output projection -> fp32 shard partials (FUSED: + shard-sum) */
-  DOMINO_K_COUNT = 12
+  DOMINO_K_LN_AFFINE = 12,  /* domino_layernorm_fwd */
+  DOMINO_K_LN_AFFINE_BWD = 13, /* domino_layernorm_bwd (its two kernels) */
+  DOMINO_K_COUNT = 14
 } domino_kernel_kind;
 DOMINO_API domino_status domino_timing_enable(domino_handle handle, int32_t enable);
 DOMINO_API domino_status domino_timing_reset(domino_handle handle);
