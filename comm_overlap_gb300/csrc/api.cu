@@ -17,6 +17,7 @@
 
 #include "../../include/domino.h"
 #include "kernels.h"
+#include "ops.h"
 
 using dm::GemmArgs;
 
@@ -87,7 +88,8 @@ const char* kernel_kind_name(int kind) {
   static const char* const names[DOMINO_K_COUNT] = {"gemm_fwd1", "gemm_fwd2", "shard_sum", "layernorm",
                                                      "gemm_dgrad_h", "gemm_wgrad_b", "gemm_dgrad_x", "gemm_wgrad_a",
                                                      "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj",
-                                                     "ln_affine", "ln_affine_bwd"};
+                                                     "ln_affine", "ln_affine_bwd", "linear_fwd", "linear_gz", "linear_gx",
+                                                     "linear_gw"};
   return (kind >= 0 && kind < DOMINO_K_COUNT) ? names[kind] : "kernel";
 }
 
@@ -1375,12 +1377,13 @@ domino_status domino_device_status(domino_handle H, domino_status* out, int32_t*
   DM_TRY(ready(H));
   if (!out) return fail(DOMINO_ERR_INVALID_ARG, "out is NULL");
   DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
-  int c1 = 0, c2 = 0, c3 = 0, c4 = 0;
+  int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0;
   DM_CUDA(dm::take_gemm_fwd_error(&c1), "reading the device error word");
   DM_CUDA(dm::take_gemm_bwd_error(&c2), "reading the device error word");
   DM_CUDA(dm::take_attn_error(&c3), "reading the device error word");
   DM_CUDA(dm::take_gemm_fp8_error(&c4), "reading the device error word");
-  const int code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : c4));
+  DM_CUDA(dm::take_linear_error(&c5), "reading the device error word");
+  const int code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : (c4 ? c4 : c5)));
   *out = code ? DOMINO_ERR_TIMEOUT : DOMINO_OK;
   if (site) *site = code;
   return DOMINO_OK;

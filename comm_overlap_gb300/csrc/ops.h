@@ -1,5 +1,5 @@
 // ops.h -- host-side interface between the C ABI of the sublayer operators (ops_api.cu) and their
-// kernels: LayerNorm with parameters (norm.cu).
+// kernels: LayerNorm with parameters (norm.cu), the linear layer (linear.cu).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -50,5 +50,43 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, int sms, cudaStream_t st);
 int ln_bwd_blocks(int64_t rows, int64_t h, int sms);
 cudaError_t launch_ln_bwd(const LnBwdArgs& a, float* part, int sms, cudaStream_t st);
 cudaError_t launch_ln_cols(const LnBwdArgs& a, const float* part, int sms, cudaStream_t st);
+
+// ---- linear layer (linear.cu): D (M x N) = A . B^T over k_blocks steps of 64
+constexpr int kLinPairs = 76;  // CTA pairs of a GB300; more are not used
+enum LinKind : int {
+  LIN_FWD = 0,  // A, B contiguous along the reduction: X . W^T
+  LIN_GX = 1,   // B contiguous along its rows: gZ . W
+  LIN_GW = 2,   // both contiguous along their rows: gZ^T . X
+};
+// Maps (all with a third dimension of one): operands in boxes of 64 (reduction) x 128 rows, or, contiguous
+// along their rows, 64 (rows) x 64 (reduction), 128-byte swizzle; y, z (z only with save) in boxes of
+// 32 x 32, 64-byte swizzle.
+struct LinMaps {
+  CUtensorMap a, b, y, z;
+};
+struct LinArgs {
+  int32_t M, N, m_tiles, n_tiles, k_blocks, act, save, err_site;
+  const uint16_t* bias;  // nullable
+  const uint16_t* R;     // nullable
+  int64_t ld_r;
+  // set by the launcher
+  int32_t round, share;  // tiles in a whole round; steps of the last round that a pair computes
+  uint8_t* part;
+  uint32_t* flags;
+};
+int64_t lin_scratch_bytes(int64_t m, int64_t n, int64_t k);
+cudaError_t launch_linear(int kind, const LinMaps& m, LinArgs a, void* scratch, cudaStream_t st);
+struct LinGzArgs {
+  const uint16_t* gY;
+  const uint16_t* Z;  // with an activation
+  uint16_t* gZ;       // with an activation; contiguous
+  float* part;        // nullable: lin_gz_row_blocks() rows of N floats
+  int64_t M, N, ld_gy, ld_z;
+  int32_t act;
+};
+int lin_gz_row_blocks(int64_t m, int64_t n);
+cudaError_t launch_lin_gz(const LinGzArgs& a, cudaStream_t st);
+cudaError_t launch_lin_gbias(const float* part, int64_t m, int64_t n, float* gbias, int accumulate, cudaStream_t st);
+cudaError_t take_linear_error(int* code);
 
 }  // namespace dm

@@ -72,6 +72,59 @@ domino_status check_ln(int64_t rows, int64_t h) {
 
 size_t ln_bwd_bytes(int64_t rows, int64_t h) { return size_t(dm::ln_bwd_blocks(rows, h, kGb300Sms)) * 2 * h * 4; }
 
+// Tensor map of a row-major rows x cols matrix with row stride ld (elements), a third dimension of one.
+domino_status map2(CUtensorMap* m, int elem_bytes, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                   uint32_t box_cols, uint32_t box_rows, int swizzle) {
+  const uint64_t dims[3] = {uint64_t(cols), uint64_t(rows), 1};
+  const uint64_t strides[2] = {uint64_t(ld) * elem_bytes, uint64_t(ld) * uint64_t(rows) * elem_bytes};
+  const uint32_t box[3] = {box_cols, box_rows, 1};
+  std::string err;
+  if (!dm::make_map(m, elem_bytes, base, 3, dims, strides, box, &err, swizzle)) return refuse(DOMINO_ERR_CUDA, err);
+  return DOMINO_OK;
+}
+
+constexpr size_t kSlice = 1024;
+size_t slice_up(size_t n) { return (n + kSlice - 1) / kSlice * kSlice; }
+
+domino_status check_linear(int64_t m, int64_t n, int64_t k, int32_t act) {
+  if (m < 0 || n <= 0 || k <= 0) return refuse(DOMINO_ERR_INVALID_ARG, "need M >= 0, N > 0 and K > 0");
+  if (act < DOMINO_ACT_NONE || act > DOMINO_ACT_BILINEAR) return refuse(DOMINO_ERR_INVALID_ARG, "unknown activation");
+  if (act > DOMINO_ACT_GELU)
+    return refuse(DOMINO_ERR_UNSUPPORTED, "the linear layer takes no gated activation (domino_mlp_fwd does)");
+  if (n % 8 != 0 || k % 8 != 0) return refuse(DOMINO_ERR_ALIGNMENT, "N and K must be multiples of 8 (16-byte rows)");
+  if (m > (int64_t(1) << 31) - 257 || n > (int64_t(1) << 20) || k > (int64_t(1) << 20))
+    return refuse(DOMINO_ERR_UNSUPPORTED, "linear layer: M beyond 2^31 - 257, or N or K beyond 2^20");
+  if (((m + 255) / 256) * ((n + 255) / 256) >= int64_t(1) << 30)
+    return refuse(DOMINO_ERR_UNSUPPORTED, "linear layer: more output tiles than one launch covers");
+  return DOMINO_OK;
+}
+
+// Workspace of the backward: the products' scratch (one at a time), gZ, and the bias gradient's partial sums.
+struct LinBwdPlan {
+  size_t scratch, off_gz, off_part, total;
+};
+LinBwdPlan linear_bwd_plan(int64_t m, int64_t n, int64_t k, int32_t act) {
+  LinBwdPlan p = {};
+  const int64_t gx = dm::lin_scratch_bytes(m, k, n), gw = dm::lin_scratch_bytes(n, k, m);
+  p.scratch = slice_up(size_t(gx > gw ? gx : gw));
+  p.off_gz = p.scratch;
+  p.off_part = p.off_gz + (act == DOMINO_ACT_NONE ? 0 : slice_up(size_t(m) * n * 2));
+  p.total = p.off_part + slice_up(size_t(dm::lin_gz_row_blocks(m, n)) * n * 4);
+  if (m == 0) p.total = 0;
+  return p;
+}
+
+dm::LinArgs linear_args(int64_t m, int64_t n, int64_t k, int site) {
+  dm::LinArgs a = {};
+  a.M = int32_t(m);
+  a.N = int32_t(n);
+  a.m_tiles = int32_t((m + 255) / 256);
+  a.n_tiles = int32_t((n + 255) / 256);
+  a.k_blocks = int32_t((k + 63) / 64);
+  a.err_site = site << 4;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -144,6 +197,143 @@ domino_status domino_layernorm_bwd(domino_handle H, const uint16_t* gY, int64_t 
                            [&] { return dm::launch_ln_bwd(a, part, op_sms(H), st); }));
     return dm::launch_on(H, DOMINO_K_LN_AFFINE_BWD, st, "LayerNorm gradient sums launch",
                          [&] { return dm::launch_ln_cols(a, part, op_sms(H), st); });
+  });
+}
+
+domino_status domino_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act, int32_t pass,
+                                           size_t* bytes) {
+  return guarded([&]() -> domino_status {
+    if (!bytes) return refuse(DOMINO_ERR_INVALID_ARG, "bytes is NULL");
+    DM_TRY(check_linear(M, N, K, act));
+    if (pass != DOMINO_PASS_FWD && pass != DOMINO_PASS_BWD)
+      return refuse(DOMINO_ERR_INVALID_ARG, "pass must be DOMINO_PASS_FWD or DOMINO_PASS_BWD");
+    *bytes = pass == DOMINO_PASS_FWD ? size_t(dm::lin_scratch_bytes(M, N, K)) : linear_bwd_plan(M, N, K, act).total;
+    return DOMINO_OK;
+  });
+}
+
+domino_status domino_linear_fwd(domino_handle H, const uint16_t* X, int64_t ld_x, const uint16_t* W,
+                                const uint16_t* bias, int32_t act, const uint16_t* R, int64_t ld_r, uint16_t* Y,
+                                int64_t ld_y, uint16_t* Z, int64_t ld_z, int64_t M, int64_t N, int64_t K,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> domino_status {
+    DM_TRY(check_linear(M, N, K, act));
+    DM_TRY(check_ld(ld_x, K, "ld_x"));
+    DM_TRY(check_ld(ld_y, N, "ld_y"));
+    if (R) DM_TRY(check_ld(ld_r, N, "ld_r"));
+    if (Z) DM_TRY(check_ld(ld_z, N, "ld_z"));
+    DM_TRY(check_ptr(W, "W"));
+    DM_TRY(check_ptr(bias, "bias", true));
+    if (M > 0) {
+      DM_TRY(check_ptr(X, "X"));
+      DM_TRY(check_ptr(Y, "Y"));
+      DM_TRY(check_ptr(R, "R", true));
+      DM_TRY(check_ptr(Z, "Z", true));
+      DM_TRY(check_ws(workspace, workspace_bytes, size_t(dm::lin_scratch_bytes(M, N, K))));
+    }
+    DM_TRY(dm::check_handle(H));
+    if (M == 0) return DOMINO_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    dm::LinMaps m = {};
+    DM_TRY(map2(&m.a, 2, X, K, M, ld_x, 64, 128, 128));
+    DM_TRY(map2(&m.b, 2, W, K, N, K, 64, 128, 128));
+    DM_TRY(map2(&m.y, 2, Y, N, M, ld_y, 32, 32, 64));
+    if (Z) DM_TRY(map2(&m.z, 2, Z, N, M, ld_z, 32, 32, 64));
+    dm::LinArgs a = linear_args(M, N, K, 0x20);
+    a.act = act;
+    a.save = Z != nullptr;
+    a.bias = bias;
+    a.R = R;
+    a.ld_r = ld_r;
+    return dm::launch_on(H, DOMINO_K_LINEAR_FWD, st, "linear layer launch",
+                         [&] { return dm::launch_linear(dm::LIN_FWD, m, a, workspace, st); });
+  });
+}
+
+domino_status domino_linear_bwd(domino_handle H, const uint16_t* gY, int64_t ld_gy, const uint16_t* X, int64_t ld_x,
+                                const uint16_t* W, const uint16_t* Z, int64_t ld_z, int32_t act, uint16_t* gX,
+                                int64_t ld_gx, uint16_t* gW, float* gW_main, float* gbias, int32_t accumulate,
+                                int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  return guarded([&]() -> domino_status {
+    DM_TRY(check_linear(M, N, K, act));
+    if (accumulate != 0 && accumulate != 1) return refuse(DOMINO_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+    if (gW && gW_main) return refuse(DOMINO_ERR_INVALID_ARG, "gW and gW_main exclude each other");
+    DM_TRY(check_ld(ld_gy, N, "ld_gy"));
+    const bool want_gw = gW || gW_main, has_act = act != DOMINO_ACT_NONE;
+    if (want_gw) DM_TRY(check_ld(ld_x, K, "ld_x"));
+    if (gX) DM_TRY(check_ld(ld_gx, K, "ld_gx"));
+    if (has_act) DM_TRY(check_ld(ld_z, N, "ld_z"));
+    DM_TRY(check_ptr(gW, "gW", true));
+    DM_TRY(check_ptr(gW_main, "gW_main", true));
+    DM_TRY(check_ptr(gbias, "gbias", true));
+    const LinBwdPlan P = linear_bwd_plan(M, N, K, act);
+    if (M > 0) {
+      DM_TRY(check_ptr(gY, "gY"));
+      DM_TRY(check_ptr(gX, "gX", true));
+      if (want_gw) DM_TRY(check_ptr(X, "X"));
+      if (gX) DM_TRY(check_ptr(W, "W"));
+      if (has_act) DM_TRY(check_ptr(Z, "Z"));
+      DM_TRY(check_ws(workspace, workspace_bytes, P.total));
+    }
+    DM_TRY(dm::check_handle(H));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M == 0) {  // empty sums
+      if (gW && cudaMemsetAsync(gW, 0, size_t(N) * K * 2, st) != cudaSuccess)
+        return refuse(DOMINO_ERR_CUDA, "cudaMemsetAsync failed");
+      if (gbias && !accumulate && cudaMemsetAsync(gbias, 0, size_t(N) * 4, st) != cudaSuccess)
+        return refuse(DOMINO_ERR_CUDA, "cudaMemsetAsync failed");
+      return DOMINO_OK;
+    }
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    uint16_t* gz_buf = reinterpret_cast<uint16_t*>(ws + P.off_gz);
+    float* part = reinterpret_cast<float*>(ws + P.off_part);
+    if (has_act || gbias) {
+      const dm::LinGzArgs g = {gY, Z, gz_buf, gbias ? part : nullptr, M, N, ld_gy, ld_z, act};
+      DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GZ, st, "linear layer gZ launch", [&] { return dm::launch_lin_gz(g, st); }));
+      if (gbias)
+        DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GZ, st, "linear layer bias gradient launch",
+                             [&] { return dm::launch_lin_gbias(part, M, N, gbias, accumulate, st); }));
+    }
+    const uint16_t* gZ = has_act ? gz_buf : gY;
+    const int64_t ld_gz = has_act ? N : ld_gy;
+    if (gX) {
+      dm::LinMaps m = {};
+      DM_TRY(map2(&m.a, 2, gZ, N, M, ld_gz, 64, 128, 128));
+      DM_TRY(map2(&m.b, 2, W, K, N, K, 64, 64, 128));
+      DM_TRY(map2(&m.y, 2, gX, K, M, ld_gx, 32, 32, 64));
+      const dm::LinArgs a = linear_args(M, K, N, 0x21);
+      DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GX, st, "linear layer gX launch",
+                           [&] { return dm::launch_linear(dm::LIN_GX, m, a, ws, st); }));
+    }
+    if (want_gw) {
+      dm::LinMaps m = {};
+      DM_TRY(map2(&m.a, 2, gZ, N, M, ld_gz, 64, 64, 128));
+      DM_TRY(map2(&m.b, 2, X, K, M, ld_x, 64, 64, 128));
+      if (gW) {
+        DM_TRY(map2(&m.y, 2, gW, K, N, K, 32, 32, 64));
+        const dm::LinArgs a = linear_args(N, K, M, 0x22);
+        DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
+                             [&] { return dm::launch_linear(dm::LIN_GW, m, a, ws, st); }));
+      } else {
+        const dm::LinArgs l = linear_args(N, K, M, 0x22);
+        dm::GemmArgs a = {};
+        a.batches = 1;
+        a.m_tiles = l.m_tiles;
+        a.n_tiles = l.n_tiles;
+        a.k_blocks = l.k_blocks;
+        a.M = l.M;
+        a.N = l.N;
+        a.err_site = l.err_site;
+        a.alpha = a.out_scale = 1.0f;
+        a.out0 = gW_main;
+        a.ld0 = K;
+        const dm::EpiMaps none = {};
+        DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
+                             [&] { return dm::launch_gemm_bwd(dm::GV_WGRAD, m.a, m.b, none, a, st); }));
+      }
+    }
+    return DOMINO_OK;
   });
 }
 

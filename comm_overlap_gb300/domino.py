@@ -22,10 +22,10 @@ SCHED_SERIAL, SCHED_INTRA, SCHED_INTER, SCHED_FUSED = 0, 1, 2, 3
 PASS_FWD, PASS_BWD, PASS_STACK, PASS_STACK_BWD, PASS_ATTN, PASS_BLOCK, PASS_FWD_FP8 = 0, 1, 2, 3, 4, 5, 6
 (K_GEMM_FWD1, K_GEMM_FWD2, K_SHARD_SUM, K_LAYERNORM, K_GEMM_DGRAD_H, K_GEMM_WGRAD_B, K_GEMM_DGRAD_X,
  K_GEMM_WGRAD_A, K_LN_BWD, K_GEMM_QKV, K_ATTN, K_GEMM_OPROJ, K_LN_AFFINE,
- K_LN_AFFINE_BWD) = range(14)
+ K_LN_AFFINE_BWD, K_LINEAR_FWD, K_LINEAR_GZ, K_LINEAR_GX, K_LINEAR_GW) = range(18)
 KERNEL_NAMES = ["gemm_fwd1", "gemm_fwd2", "shard_sum", "layernorm", "gemm_dgrad_h", "gemm_wgrad_b",
                 "gemm_dgrad_x", "gemm_wgrad_a", "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj",
-                "ln_affine", "ln_affine_bwd"]
+                "ln_affine", "ln_affine_bwd", "linear_fwd", "linear_gz", "linear_gx", "linear_gw"]
 
 
 class DominoError(RuntimeError):
@@ -77,6 +77,10 @@ _SIGS = {
     "domino_layernorm_bwd_workspace_size": [_I64, _I64, ctypes.POINTER(_N)],
     "domino_layernorm_bwd": [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _I64, _I64, _P, _N,
                              _P],
+    "domino_linear_workspace_size": [_I64, _I64, _I64, _S, _S, ctypes.POINTER(_N)],
+    "domino_linear_fwd": [_P, _P, _I64, _P, _P, _S, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _N, _P],
+    "domino_linear_bwd": [_P, _P, _I64, _P, _I64, _P, _P, _I64, _S, _P, _I64, _P, _P, _P, _S, _I64, _I64, _I64, _P,
+                          _N, _P],
     "domino_act_eval": [ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_int64, _P],
     "domino_device_status": [_P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)],
     "domino_timing_enable": [_P, ctypes.c_int32],
@@ -249,6 +253,26 @@ def domino_layernorm_bwd(handle, gY, ld_gy, X, ld_x, gamma, mean, rstd, gres, ld
                                       _ptr(gres), ld_gres, _ptr(gX), ld_gx, _ptr(ggamma), _ptr(gbeta), accumulate,
                                       rows, h, _ptr(workspace), _nbytes(workspace, workspace_bytes),
                                       _stream(stream)))
+
+
+def domino_linear_workspace_size(M, N, K, act, pass_) -> int:
+    n = _N()
+    _check(lib().domino_linear_workspace_size(M, N, K, act, pass_, ctypes.byref(n)))
+    return n.value
+
+
+def domino_linear_fwd(handle, X, ld_x, W, bias, act, R, ld_r, Y, ld_y, Z, ld_z, M, N, K, workspace,
+                      workspace_bytes=None, stream=None) -> None:
+    _check(lib().domino_linear_fwd(handle, _ptr(X), ld_x, _ptr(W), _ptr(bias), act, _ptr(R), ld_r, _ptr(Y), ld_y,
+                                   _ptr(Z), ld_z, M, N, K, _ptr(workspace), _nbytes(workspace, workspace_bytes),
+                                   _stream(stream)))
+
+
+def domino_linear_bwd(handle, gY, ld_gy, X, ld_x, W, Z, ld_z, act, gX, ld_gx, gW, gW_main, gbias, accumulate, M, N, K,
+                      workspace, workspace_bytes=None, stream=None) -> None:
+    _check(lib().domino_linear_bwd(handle, _ptr(gY), ld_gy, _ptr(X), ld_x, _ptr(W), _ptr(Z), ld_z, act, _ptr(gX),
+                                   ld_gx, _ptr(gW), _ptr(gW_main), _ptr(gbias), accumulate, M, N, K, _ptr(workspace),
+                                   _nbytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def domino_act_eval(act, a, b, out, da, db, n, stream=None) -> None:

@@ -1,8 +1,9 @@
 """PyTorch functions and modules around the sublayer operators (argument marshalling only).
 
-The operators of a pre-LN block outside the sharded MLP: LayerNorm with weight and bias.  Each has
-plain functions that allocate their outputs and call the C ABI (`layer_norm_fwd`, `layer_norm_bwd`),
-a differentiable function (`layer_norm`) and a module (`DominoLayerNorm`).  Every step of the
+The operators of a pre-LN block outside the sharded MLP: LayerNorm with weight and bias, and the linear
+layer with bias, activation and residual.  Each has plain functions that allocate their outputs and call
+the C ABI (`layer_norm_fwd`, `layer_norm_bwd`, `linear_fwd`, `linear_bwd`), a differentiable function
+(`layer_norm`, `linear`) and a module (`DominoLayerNorm`, `DominoLinear`).  Every step of the
 computation runs in the library's kernels; tensors must be on one CUDA device, matrices bf16.
 
 Calls run on the current stream of the tensors' device.  Workspaces come from PyTorch's allocator for
@@ -177,3 +178,141 @@ class DominoLayerNorm(torch.nn.Module):
         if x.shape[-1] != self.h:
             raise ValueError(f"x must have {self.h} columns")
         return layer_norm(x, self.weight, self.bias, self.eps)
+
+
+# ---- linear layer ----------------------------------------------------------------------------------
+
+ACTS = {"none": dm.ACT_NONE, "relu": dm.ACT_RELU, "gelu": dm.ACT_GELU}
+
+
+def _act(act) -> int:
+    code = ACTS.get(act, act)
+    if code not in ACTS.values():
+        raise ValueError(f"act must be one of {sorted(ACTS)}")
+    return code
+
+
+def _linear_shapes(x: torch.Tensor, weight: torch.Tensor) -> tuple[int, int, int]:
+    _matrix("x", x)
+    _matrix("weight", weight)
+    n, k = weight.shape
+    _check("weight", weight, x, (n, x.shape[1]))
+    return x.shape[0], n, k
+
+
+def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act="none",
+               residual: torch.Tensor | None = None, save: bool = False):
+    """y = act(x weight^T + bias) + residual for x [m, k], weight [n, k] (bf16): (y, z), z the
+    pre-activation that `linear_bwd` needs, or None without `save`."""
+    m, n, k = _linear_shapes(x, weight)
+    act = _act(act)
+    if bias is not None:
+        _check("bias", bias, x, (n,))
+    ld_r = n
+    if residual is not None:
+        _check("residual", residual, x, (m, n))
+        residual, ld_r = _rows(residual)
+    x, ld_x = _rows(x)
+    weight, bias = _vec(weight), _vec(bias)
+    y = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
+    z = torch.empty_like(y) if save else None
+    size = dm.domino_linear_workspace_size(m, n, k, act, dm.PASS_FWD)
+    ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+    with _call(x) as handle:
+        dm.domino_linear_fwd(handle, x, ld_x, weight, bias, act, residual, ld_r, y, n, z, n, m, n, k, ws, size)
+    return y, z
+
+
+def linear_bwd(gy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, z: torch.Tensor | None = None, act="none",
+               x_grad: bool = True, weight_grad: bool = True, bias_grad: bool = True, main_grad: torch.Tensor | None = None,
+               bias_main_grad: torch.Tensor | None = None):
+    """Gradients of `linear_fwd`: (gx, gweight, gbias), gx and gweight bf16, gbias fp32; None where not
+    asked for.  With `main_grad` (fp32, like weight) the weight's gradient is added to it instead of
+    returned; with `bias_main_grad` the bias's.  `z`: what the forward kept (act "none" needs none)."""
+    m, n, k = _linear_shapes(x, weight)
+    act = _act(act)
+    _check("gy", gy, x, (m, n))
+    ld_z = n
+    if act != dm.ACT_NONE:
+        if z is None:
+            raise ValueError("the activation's gradient needs z")
+        _check("z", z, x, (m, n))
+        z, ld_z = _rows(z)
+    else:
+        z = None
+    for name, g, shape in (("main_grad", main_grad, (n, k)), ("bias_main_grad", bias_main_grad, (n,))):
+        if g is not None:
+            _check(name, g, x, shape, torch.float32)
+            if not g.is_contiguous() or g.data_ptr() % 16:
+                raise ValueError(f"{name} must be contiguous and 16-byte aligned")
+    gy, ld_gy = _rows(gy)
+    x, ld_x = _rows(x)
+    weight = _vec(weight)
+    gx = torch.empty((m, k), dtype=torch.bfloat16, device=x.device) if x_grad else None
+    gw = torch.empty((n, k), dtype=torch.bfloat16, device=x.device) if weight_grad and main_grad is None else None
+    gb = bias_main_grad
+    if gb is None and bias_grad:
+        gb = torch.empty(n, dtype=torch.float32, device=x.device)
+    size = dm.domino_linear_workspace_size(m, n, k, act, dm.PASS_BWD)
+    ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
+    with _call(x) as handle:
+        dm.domino_linear_bwd(handle, gy, ld_gy, x, ld_x, weight, z, ld_z, act, gx, k, gw,
+                             main_grad if weight_grad else None, gb, int(bias_main_grad is not None), m, n, k, ws, size)
+    return gx, gw, gb
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, act, main_grad, bias_main_grad):
+        y, z = linear_fwd(x, weight, bias, act, residual, save=act != dm.ACT_NONE)
+        ctx.save_for_backward(x, weight, z)
+        ctx.act, ctx.bias, ctx.main = act, bias is not None, (main_grad, bias_main_grad)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gy):
+        x, weight, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        main, bias_main = ctx.main
+        gx, gw, gb = linear_bwd(gy, x, weight, z, ctx.act, need[0], need[1], ctx.bias and need[2], main if need[1] else None,
+                                bias_main if ctx.bias and need[2] else None)
+        if bias_main is not None:
+            gb = None
+        return gx, gw, gb.to(weight.dtype) if gb is not None else None, gy if need[3] else None, None, None, None
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act="none",
+           residual: torch.Tensor | None = None) -> torch.Tensor:
+    """Differentiable y = act(x weight^T + bias) + residual for x [..., k] (bf16).  Where weight (bias)
+    has an fp32 `main_grad`, its gradient is accumulated there and its `.grad` stays None."""
+    _check("x", x)
+    r = residual.reshape(-1, weight.shape[0]) if residual is not None else None
+    y = _Linear.apply(x.reshape(-1, x.shape[-1]), weight, bias, r, _act(act), getattr(weight, "main_grad", None),
+                      getattr(bias, "main_grad", None))
+    return y.view(*x.shape[:-1], weight.shape[0])
+
+
+class DominoLinear(torch.nn.Module):
+    """y = act(x weight^T + bias) + residual with bf16 parameters; with `fuse_wgrad` their gradients are
+    accumulated in fp32 `main_grad` buffers, as in `DominoMLP`."""
+
+    def __init__(self, k: int, n: int, bias: bool = True, act="none", fuse_wgrad: bool = False, init_std: float = 0.02,
+                 device: str | torch.device = "cuda"):
+        super().__init__()
+        self.act = _act(act)
+        self.weight = torch.nn.Parameter(torch.empty((n, k), dtype=torch.bfloat16, device=device))
+        self.bias = torch.nn.Parameter(torch.zeros(n, dtype=torch.bfloat16, device=device)) if bias else None
+        with torch.no_grad():
+            self.weight.normal_(0.0, init_std)
+        if fuse_wgrad:
+            for p in self.parameters():
+                p.main_grad = torch.zeros(p.shape, dtype=torch.float32, device=device)
+
+    def zero_main_grad(self) -> None:
+        for p in self.parameters():
+            if hasattr(p, "main_grad"):
+                p.main_grad.zero_()
+
+    def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
+        return linear(x, self.weight, self.bias, self.act, residual)

@@ -297,6 +297,37 @@ DOMINO_API domino_status domino_layernorm_bwd(domino_handle handle, const uint16
                                               float* gbeta, int32_t accumulate, int64_t rows, int64_t h,
                                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* Linear layer:  Z = X . W^T + bias,  Y = act(Z) + R.
+ *   X: M x K (row stride ld_x); W: N x K, contiguous (nn.Linear [out, in]); bias (nullable): N;
+ *   R (nullable, the residual): M x N (row stride ld_r); Y: M x N (row stride ld_y; may be R).
+ *   Z (nullable): M x N (row stride ld_z), the pre-activation that domino_linear_bwd needs.
+ * bf16 operands, fp32 accumulation; bias, activation and residual are applied in fp32 and Y and Z are
+ * each rounded once.  act: NONE, RELU or GELU.  N and K are multiples of 8, at most 2^20; M >= 0.
+ * The order of every sum depends on the sizes alone: equal inputs give equal bits.  Workspace:
+ * domino_linear_workspace_size(..., DOMINO_PASS_FWD); its contents need no initialisation. */
+DOMINO_API domino_status domino_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act, int32_t pass,
+                                                      size_t* bytes);
+DOMINO_API domino_status domino_linear_fwd(domino_handle handle, const uint16_t* X, int64_t ld_x, const uint16_t* W,
+                                           const uint16_t* bias, int32_t act, const uint16_t* R, int64_t ld_r,
+                                           uint16_t* Y, int64_t ld_y, uint16_t* Z, int64_t ld_z, int64_t M,
+                                           int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/* Backward of domino_linear_fwd (the residual's gradient is gY itself):
+ *   gZ = gY act'(Z)                 (fp32; rounded to bf16 where it enters the products)
+ *   gX = gZ . W                     (nullable; M x K, row stride ld_gx)
+ *   gW = gZ^T . X                   (N x K; nullable) as bf16, rounded once, or instead
+ *   gW_main += gZ^T . X             (N x K fp32, the main_grad buffer; nullable)
+ *   gbias = sum over rows of gZ     (N fp32, unrounded gZ; nullable), added to the buffer with
+ *                                   accumulate = 1.
+ * Z is what the forward kept (unused with act = NONE); W is needed for gX, X for gW.  Workspace:
+ * domino_linear_workspace_size(..., DOMINO_PASS_BWD). */
+DOMINO_API domino_status domino_linear_bwd(domino_handle handle, const uint16_t* gY, int64_t ld_gy,
+                                           const uint16_t* X, int64_t ld_x, const uint16_t* W, const uint16_t* Z,
+                                           int64_t ld_z, int32_t act, uint16_t* gX, int64_t ld_gx, uint16_t* gW,
+                                           float* gW_main, float* gbias, int32_t accumulate, int64_t M, int64_t N,
+                                           int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
 /* The reduction step alone (the AllReduce stand-in):
  *   Y[r, c] = bf16( (residual[r, c]) + (((P_0[r,c] + P_1[r,c]) + ...) + P_{t-1}[r,c]) )
  * P: t slices of rows x cols fp32, slice i at P + i*rows*cols, row stride cols.
@@ -336,7 +367,11 @@ typedef enum {
   DOMINO_K_GEMM_OPROJ = 11, /* attention output projection -> fp32 shard partials (FUSED: + shard-sum) */
   DOMINO_K_LN_AFFINE = 12,  /* domino_layernorm_fwd */
   DOMINO_K_LN_AFFINE_BWD = 13, /* domino_layernorm_bwd (its two kernels) */
-  DOMINO_K_COUNT = 14
+  DOMINO_K_LINEAR_FWD = 14, /* domino_linear_fwd */
+  DOMINO_K_LINEAR_GZ = 15,  /* domino_linear_bwd: gZ and the bias gradient (its two kernels) */
+  DOMINO_K_LINEAR_GX = 16,  /* domino_linear_bwd: gZ . W */
+  DOMINO_K_LINEAR_GW = 17,  /* domino_linear_bwd: gZ^T . X */
+  DOMINO_K_COUNT = 18
 } domino_kernel_kind;
 DOMINO_API domino_status domino_timing_enable(domino_handle handle, int32_t enable);
 DOMINO_API domino_status domino_timing_reset(domino_handle handle);

@@ -74,3 +74,63 @@ def test_functions_refuse_what_they_cannot_take():
         ops.layer_norm_bwd(x, x, w, w, w)
     with pytest.raises(ValueError, match="columns"):
         ops.DominoLayerNorm(128, device="cpu")(x)
+
+
+def lin_fwd(**kw):
+    a = dict(handle=None, X=P, ld_x=64, W=P, bias=P, act=dm.ACT_GELU, R=P, ld_r=128, Y=P, ld_y=128, Z=P, ld_z=128, M=4, N=128,
+             K=64, workspace=P, workspace_bytes=1 << 30, stream=0)
+    dm.domino_linear_fwd(**{**a, **kw})
+
+
+def lin_bwd(**kw):
+    a = dict(handle=None, gY=P, ld_gy=128, X=P, ld_x=64, W=P, Z=P, ld_z=128, act=dm.ACT_GELU, gX=P, ld_gx=64, gW=P, gW_main=None,
+             gbias=P, accumulate=0, M=4, N=128, K=64, workspace=P, workspace_bytes=1 << 30, stream=0)
+    dm.domino_linear_bwd(**{**a, **kw})
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(M=-1), INVALID), (dict(N=0), INVALID), (dict(K=0), INVALID), (dict(act=5), INVALID), (dict(act=-1), INVALID),
+    (dict(act=dm.ACT_SWIGLU), UNSUPPORTED), (dict(act=dm.ACT_BILINEAR), UNSUPPORTED), (dict(N=132), ALIGNMENT),
+    (dict(K=60), ALIGNMENT), (dict(N=(1 << 20) + 8), UNSUPPORTED), (dict(M=(1 << 31) - 256), UNSUPPORTED),
+    (dict(M=(1 << 31) - 257, N=1 << 16, ld_y=1 << 16, ld_r=1 << 16, ld_z=1 << 16), UNSUPPORTED), (dict(ld_x=56), INVALID),
+    (dict(ld_x=68), ALIGNMENT), (dict(ld_y=120), INVALID), (dict(ld_r=64), INVALID), (dict(ld_z=130), ALIGNMENT),
+    (dict(X=None), INVALID), (dict(W=None), INVALID), (dict(Y=None), INVALID), (dict(W=P + 8), ALIGNMENT), (dict(bias=P + 2), ALIGNMENT),
+    (dict(R=P + 2), ALIGNMENT), (dict(Z=P + 4), ALIGNMENT), (dict(K=4096, ld_x=4096, workspace=None), WORKSPACE),
+    (dict(K=4096, ld_x=4096, workspace=P + 128), WORKSPACE), (dict(K=4096, ld_x=4096, workspace_bytes=1 << 20), WORKSPACE),
+    (dict(), INVALID), (dict(bias=None, R=None, Z=None, workspace=None), INVALID)])
+def test_linear_forward(kw, code):
+    assert status(lin_fwd, **kw) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(act=dm.ACT_SWIGLU), UNSUPPORTED), (dict(N=100), ALIGNMENT), (dict(accumulate=3), INVALID),
+    (dict(gW_main=P), INVALID), (dict(gW=None, gW_main=P + 4), ALIGNMENT), (dict(gY=None), INVALID), (dict(X=None), INVALID),
+    (dict(W=None), INVALID), (dict(Z=None), INVALID), (dict(ld_z=64), INVALID), (dict(ld_gy=120), INVALID), (dict(ld_gx=8), INVALID),
+    (dict(gX=P + 2), ALIGNMENT), (dict(gbias=P + 4), ALIGNMENT), (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=64), WORKSPACE),
+    (dict(), INVALID), (dict(gX=None, W=None, gbias=None), INVALID), (dict(gW=None, X=None, ld_x=0), INVALID)])
+def test_linear_backward(kw, code):
+    assert status(lin_bwd, **kw) == code
+
+
+def test_linear_workspace_size():
+    size = dm.domino_linear_workspace_size
+    assert size(4, 128, 512, dm.ACT_NONE, dm.PASS_FWD) == 0  # too short a reduction to cut
+    assert size(0, 128, 4096, dm.ACT_NONE, dm.PASS_FWD) == 0 and size(0, 128, 4096, dm.ACT_GELU, dm.PASS_BWD) == 0
+    assert size(4, 128, 4096, dm.ACT_NONE, dm.PASS_FWD) == 76 * (256 * 256 * 4 + 64)
+    assert size(4, 128, 64, dm.ACT_GELU, dm.PASS_BWD) == 1024 + 1024  # gZ, one row of partial sums
+    assert status(size, M=4, N=128, K=64, act=dm.ACT_NONE, pass_=dm.PASS_STACK) == INVALID
+    assert status(size, M=4, N=128, K=64, act=dm.ACT_SWIGLU, pass_=dm.PASS_FWD) == UNSUPPORTED
+
+
+def test_linear_functions_refuse_what_they_cannot_take():
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(128, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.linear_fwd(x, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.linear(x, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.linear_bwd(x, x, w)
+    with pytest.raises(ValueError, match="act"):
+        ops.DominoLinear(64, 128, act="tanh", device="cpu")
+    with pytest.raises(ValueError, match="act"):
+        ops.DominoLinear(64, 128, act=dm.ACT_SWIGLU, device="cpu")
