@@ -114,6 +114,18 @@ LinBwdPlan linear_bwd_plan(int64_t m, int64_t n, int64_t k, int32_t act) {
   return p;
 }
 
+domino_status check_packed(int64_t tq, int64_t n, int32_t heads, int32_t kv_heads, int64_t tk) {
+  if (tq < 0 || n < 0 || tk < 0 || heads < 1 || kv_heads < 1)
+    return refuse(DOMINO_ERR_INVALID_ARG, "need tq, n, tk >= 0, heads >= 1 and kv_heads >= 1");
+  if (heads % kv_heads != 0) return refuse(DOMINO_ERR_INVALID_ARG, "heads must be a multiple of kv_heads");
+  if (heads / kv_heads > 128 || heads > 4096)
+    return refuse(DOMINO_ERR_UNSUPPORTED, "packed attention: more than 128 heads per key head, or than 4096 heads");
+  const int64_t most = (int64_t(1) << 31) - 1024;
+  if (tq > most || tk > most || n > (int64_t(1) << 24) || (tq + n + 1024) * kv_heads > most)
+    return refuse(DOMINO_ERR_UNSUPPORTED, "packed attention: more tokens or sequences than one call covers");
+  return DOMINO_OK;
+}
+
 dm::LinArgs linear_args(int64_t m, int64_t n, int64_t k, int site) {
   dm::LinArgs a = {};
   a.M = int32_t(m);
@@ -333,6 +345,90 @@ domino_status domino_linear_bwd(domino_handle H, const uint16_t* gY, int64_t ld_
                              [&] { return dm::launch_gemm_bwd(dm::GV_WGRAD, m.a, m.b, none, a, st); }));
       }
     }
+    return DOMINO_OK;
+  });
+}
+
+domino_status domino_attn_packed_workspace_size(int64_t tq, int64_t n, int32_t heads, int32_t kv_heads, int64_t tk,
+                                                size_t* bytes) {
+  return guarded([&]() -> domino_status {
+    if (!bytes) return refuse(DOMINO_ERR_INVALID_ARG, "bytes is NULL");
+    DM_TRY(check_packed(tq, n, heads, kv_heads, tk));
+    *bytes = tq == 0 || n == 0 ? 0 : size_t(dm::packed_scratch_bytes(tq, n, heads, kv_heads, tk));
+    return DOMINO_OK;
+  });
+}
+
+domino_status domino_attn_packed_fwd(domino_handle H, const uint16_t* Q, int64_t ld_q, const uint16_t* K, int64_t ld_k,
+                                     const uint16_t* V, int64_t ld_v, const int32_t* cu_q, const int32_t* k_start,
+                                     const int32_t* k_len, float scale, uint16_t* O, int64_t ld_o, float* lse,
+                                     int64_t tq, int64_t n, int32_t heads, int32_t kv_heads, int64_t tk,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> domino_status {
+    DM_TRY(check_packed(tq, n, heads, kv_heads, tk));
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return refuse(DOMINO_ERR_INVALID_ARG, "scale must be finite and > 0");
+    DM_TRY(check_ld(ld_q, int64_t(heads) * 128, "ld_q"));
+    DM_TRY(check_ld(ld_k, int64_t(kv_heads) * 128, "ld_k"));
+    DM_TRY(check_ld(ld_v, int64_t(kv_heads) * 128, "ld_v"));
+    DM_TRY(check_ld(ld_o, int64_t(heads) * 128, "ld_o"));
+    const bool work = tq > 0 && n > 0;
+    if (work) {
+      DM_TRY(check_ptr(Q, "Q"));
+      DM_TRY(check_ptr(K, "K", tk == 0));
+      DM_TRY(check_ptr(V, "V", tk == 0));
+      DM_TRY(check_ptr(O, "O"));
+      DM_TRY(check_ptr(lse, "lse", true));
+      const int32_t* lists[] = {cu_q, k_start, k_len};
+      static const char* const names[] = {"cu_q", "k_start", "k_len"};
+      for (int i = 0; i < 3; ++i) {
+        if (!lists[i]) return refuse(DOMINO_ERR_INVALID_ARG, std::string(names[i]) + " is NULL");
+        if (reinterpret_cast<uintptr_t>(lists[i]) & 3u)
+          return refuse(DOMINO_ERR_ALIGNMENT, std::string(names[i]) + " is not 4-byte aligned");
+      }
+      DM_TRY(check_ws(workspace, workspace_bytes, size_t(dm::packed_scratch_bytes(tq, n, heads, kv_heads, tk))));
+    }
+    DM_TRY(dm::check_handle(H));
+    if (!work) return DOMINO_OK;
+    dm::PackedArgs a = {};
+    a.cu_q = cu_q;
+    a.k_start = k_start;
+    a.k_len = k_len;
+    a.O = O;
+    a.lse = lse;
+    a.ld_o = ld_o;
+    a.n = int32_t(n);
+    a.tq = int32_t(tq);
+    a.tk = int32_t(tk);
+    a.hq = heads;
+    a.hkv = kv_heads;
+    a.group = heads / kv_heads;
+    a.tokens = 128 / a.group;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.err_site = 0x23 << 4;
+    std::string err;
+    CUtensorMap mq, mk, mv;
+    {
+      const uint64_t dims[4] = {128, uint64_t(a.group), uint64_t(kv_heads), uint64_t(tq)};
+      const uint64_t strides[3] = {256, uint64_t(a.group) * 256, uint64_t(ld_q) * 2};
+      const uint32_t box[4] = {64, uint32_t(a.group), 1, uint32_t(a.tokens)};
+      if (!dm::make_map(&mq, 2, Q, 4, dims, strides, box, &err)) return refuse(DOMINO_ERR_CUDA, err);
+    }
+    for (int i = 0; i < 2; ++i) {
+      // without keys nothing is loaded: the maps describe Q's first row
+      const uint64_t dims[3] = {128, uint64_t(kv_heads), uint64_t(tk > 0 ? tk : 1)};
+      const uint64_t strides[2] = {256, uint64_t(i ? ld_v : ld_k) * 2};
+      const uint32_t box[3] = {64, 1, 128};
+      if (!dm::make_map(i ? &mv : &mk, 2, tk > 0 ? (i ? V : K) : Q, 3, dims, strides, box, &err))
+        return refuse(DOMINO_ERR_CUDA, err);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_PACKED, st, "packed attention plan launch",
+                         [&] { return dm::launch_packed_plan(a, workspace, st); }));
+    DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_PACKED, st, "packed attention launch",
+                         [&] { return dm::launch_packed_attention(mq, mk, mv, a, workspace, op_sms(H), st); }));
+    if (dm::packed_may_cut(a))
+      DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_PACKED, st, "packed attention combine launch",
+                           [&] { return dm::launch_packed_combine(a, workspace, st); }));
     return DOMINO_OK;
   });
 }

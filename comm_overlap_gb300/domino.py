@@ -22,10 +22,12 @@ SCHED_SERIAL, SCHED_INTRA, SCHED_INTER, SCHED_FUSED = 0, 1, 2, 3
 PASS_FWD, PASS_BWD, PASS_STACK, PASS_STACK_BWD, PASS_ATTN, PASS_BLOCK, PASS_FWD_FP8 = 0, 1, 2, 3, 4, 5, 6
 (K_GEMM_FWD1, K_GEMM_FWD2, K_SHARD_SUM, K_LAYERNORM, K_GEMM_DGRAD_H, K_GEMM_WGRAD_B, K_GEMM_DGRAD_X,
  K_GEMM_WGRAD_A, K_LN_BWD, K_GEMM_QKV, K_ATTN, K_GEMM_OPROJ, K_LN_AFFINE,
- K_LN_AFFINE_BWD, K_LINEAR_FWD, K_LINEAR_GZ, K_LINEAR_GX, K_LINEAR_GW) = range(18)
+ K_LN_AFFINE_BWD, K_LINEAR_FWD, K_LINEAR_GZ, K_LINEAR_GX, K_LINEAR_GW,
+ K_ATTN_PACKED) = range(19)
 KERNEL_NAMES = ["gemm_fwd1", "gemm_fwd2", "shard_sum", "layernorm", "gemm_dgrad_h", "gemm_wgrad_b",
                 "gemm_dgrad_x", "gemm_wgrad_a", "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj",
-                "ln_affine", "ln_affine_bwd", "linear_fwd", "linear_gz", "linear_gx", "linear_gw"]
+                "ln_affine", "ln_affine_bwd", "linear_fwd", "linear_gz", "linear_gx", "linear_gw",
+                "attn_packed"]
 
 
 class DominoError(RuntimeError):
@@ -81,6 +83,9 @@ _SIGS = {
     "domino_linear_fwd": [_P, _P, _I64, _P, _P, _S, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _N, _P],
     "domino_linear_bwd": [_P, _P, _I64, _P, _I64, _P, _P, _I64, _S, _P, _I64, _P, _P, _P, _S, _I64, _I64, _I64, _P,
                           _N, _P],
+    "domino_attn_packed_workspace_size": [_I64, _I64, _S, _S, _I64, ctypes.POINTER(_N)],
+    "domino_attn_packed_fwd": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, ctypes.c_float, _P, _I64, _P, _I64, _I64,
+                               _S, _S, _I64, _P, _N, _P],
     "domino_act_eval": [ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_int64, _P],
     "domino_device_status": [_P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)],
     "domino_timing_enable": [_P, ctypes.c_int32],
@@ -273,6 +278,22 @@ def domino_linear_bwd(handle, gY, ld_gy, X, ld_x, W, Z, ld_z, act, gX, ld_gx, gW
     _check(lib().domino_linear_bwd(handle, _ptr(gY), ld_gy, _ptr(X), ld_x, _ptr(W), _ptr(Z), ld_z, act, _ptr(gX),
                                    ld_gx, _ptr(gW), _ptr(gW_main), _ptr(gbias), accumulate, M, N, K, _ptr(workspace),
                                    _nbytes(workspace, workspace_bytes), _stream(stream)))
+
+
+BAD_LENGTHS_SITE = 0x7E0
+
+
+def domino_attn_packed_workspace_size(tq, n, heads, kv_heads, tk) -> int:
+    size = _N()
+    _check(lib().domino_attn_packed_workspace_size(tq, n, heads, kv_heads, tk, ctypes.byref(size)))
+    return size.value
+
+
+def domino_attn_packed_fwd(handle, Q, ld_q, K, ld_k, V, ld_v, cu_q, k_start, k_len, scale, O, ld_o, lse, tq, n, heads,
+                           kv_heads, tk, workspace, workspace_bytes=None, stream=None) -> None:
+    _check(lib().domino_attn_packed_fwd(handle, _ptr(Q), ld_q, _ptr(K), ld_k, _ptr(V), ld_v, _ptr(cu_q), _ptr(k_start),
+                                        _ptr(k_len), scale, _ptr(O), ld_o, _ptr(lse), tq, n, heads, kv_heads, tk,
+                                        _ptr(workspace), _nbytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def domino_act_eval(act, a, b, out, da, db, n, stream=None) -> None:

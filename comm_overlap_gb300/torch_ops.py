@@ -1,9 +1,10 @@
 """PyTorch functions and modules around the sublayer operators (argument marshalling only).
 
-The operators of a pre-LN block outside the sharded MLP: LayerNorm with weight and bias, and the linear
-layer with bias, activation and residual.  Each has plain functions that allocate their outputs and call
-the C ABI (`layer_norm_fwd`, `layer_norm_bwd`, `linear_fwd`, `linear_bwd`), a differentiable function
-(`layer_norm`, `linear`) and a module (`DominoLayerNorm`, `DominoLinear`).  Every step of the
+The operators of a pre-LN block outside the sharded MLP: LayerNorm with weight and bias, the linear layer
+with bias, activation and residual, and causal attention over packed sequences with grouped heads.  The
+first two have plain functions that allocate their outputs and call the C ABI (`layer_norm_fwd`,
+`layer_norm_bwd`, `linear_fwd`, `linear_bwd`), a differentiable function (`layer_norm`, `linear`) and a
+module (`DominoLayerNorm`, `DominoLinear`); the attention (`packed_attention`) is forward only.  Every step of the
 computation runs in the library's kernels; tensors must be on one CUDA device, matrices bf16.
 
 Calls run on the current stream of the tensors' device.  Workspaces come from PyTorch's allocator for
@@ -316,3 +317,87 @@ class DominoLinear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, residual: torch.Tensor | None = None) -> torch.Tensor:
         return linear(x, self.weight, self.bias, self.act, residual)
+
+
+# ---- attention over packed sequences ---------------------------------------------------------------
+
+HEAD_DIM = 128
+
+
+def _heads(name: str, x: torch.Tensor) -> tuple[torch.Tensor, int]:
+    """A [tokens, heads, 128] tensor with its heads one after the other, and its token stride."""
+    t, h, d = x.shape
+    if x.data_ptr() % 16 == 0 and x.stride(2) == 1 and (h <= 1 or x.stride(1) == d):
+        if t <= 1:
+            return x, h * d
+        if x.stride(0) >= h * d and x.stride(0) % 8 == 0:
+            return x, x.stride(0)
+    return x.clone(memory_format=torch.contiguous_format), h * d
+
+
+def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                     k_start: torch.Tensor | None = None, k_len: torch.Tensor | None = None, scale: float | None = None,
+                     return_lse: bool = False, out: torch.Tensor | None = None):
+    """Causal attention of n packed sequences, q [tq, heads, 128], k and v [tk, kv_heads, 128] (bf16).
+
+    Sequence s has the queries cu_q[s] .. cu_q[s + 1] - 1 and the k_len[s] keys from row k_start[s]; its last
+    query sees all of them, the one before all but the last, and so on (int32 tensors on the device, of n + 1,
+    n and n values).  Without k_start and k_len the keys are the sequence's own rows, as in prompts.  The scale
+    is 1 / sqrt(128) unless given.  Returns o, or (o, lse) with lse [tq, heads] fp32.  Rows that belong to no
+    sequence are left as they were in `out` (undefined without it).  Lengths that leave the tensors are not
+    raised here: they are read on the device, and `device_status` reports them.  Forward only."""
+    for name, x in (("q", q), ("k", k), ("v", v)):
+        _check(name, x, q)
+        if x.dim() != 3 or x.shape[2] != HEAD_DIM:
+            raise ValueError(f"{name} must have shape [tokens, heads, {HEAD_DIM}], not {tuple(x.shape)}")
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        raise ValueError("packed_attention has no backward: call it under torch.no_grad(), or detach its inputs")
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    tq, hq, _ = q.shape
+    tk, hkv, _ = k.shape
+    if hkv == 0 or hq == 0 or hq % hkv:
+        raise ValueError("the query heads must be a multiple of the key heads")
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be a vector of n + 1 values")
+    n = cu_q.numel() - 1
+    if (k_start is None) != (k_len is None):
+        raise ValueError("k_start and k_len go together")
+    _check("cu_q", cu_q, q, (n + 1,), torch.int32)
+    if k_start is None:
+        if tk != tq:
+            raise ValueError("without k_start and k_len, q and k must have the same rows")
+        k_start, k_len = cu_q[:-1], cu_q.diff()
+    _check("k_start", k_start, q, (n,), torch.int32)
+    _check("k_len", k_len, q, (n,), torch.int32)
+    q, ld_q = _heads("q", q)
+    k, ld_k = _heads("k", k)
+    v, ld_v = _heads("v", v)
+    cu_q, k_start, k_len = (t.contiguous() for t in (cu_q, k_start, k_len))
+    if out is None:
+        out = torch.empty((tq, hq, HEAD_DIM), dtype=torch.bfloat16, device=q.device)
+        ld_o = hq * HEAD_DIM
+    else:
+        _check("out", out, q, (tq, hq, HEAD_DIM))
+        same, ld_o = _heads("out", out)
+        if same is not out:
+            raise ValueError("out must have contiguous, 16-byte aligned tokens that do not overlap")
+    lse = torch.empty((tq, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    size = dm.domino_attn_packed_workspace_size(tq, n, hq, hkv, tk)
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    with _call(q) as handle:
+        dm.domino_attn_packed_fwd(handle, q, ld_q, k, ld_k, v, ld_v, cu_q, k_start, k_len,
+                                  HEAD_DIM ** -0.5 if scale is None else scale, out, ld_o, lse, tq, n, hq, hkv, tk, ws, size)
+    return (out, lse) if return_lse else out
+
+
+def device_status(device: torch.device | int | None = None) -> None:
+    """Synchronises the device and raises DominoError if a call of this module's since the last look ran out
+    of a wait or met lengths that leave their tensors."""
+    x = torch.empty(0, device="cuda" if device is None else device)
+    with _call(x) as handle:
+        status, site = dm.domino_device_status(handle)
+    if status != dm.DOMINO_OK:
+        what = "packed_attention met lengths that leave its tensors" if site == dm.BAD_LENGTHS_SITE else \
+            f"a device-side wait ran out (site {site:#x})"
+        raise dm.DominoError(status, what)

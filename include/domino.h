@@ -328,6 +328,33 @@ DOMINO_API domino_status domino_linear_bwd(domino_handle handle, const uint16_t*
                                            float* gW_main, float* gbias, int32_t accumulate, int64_t M, int64_t N,
                                            int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Causal attention of packed sequences with grouped heads, head dimension 128: whole prompts, chunks of
+ * prompts over a cache, and single tokens over a cache, in any mixture.
+ *   Q: tq x heads x 128, K, V: tk x kv_heads x 128, O: tq x heads x 128; row strides ld_q, ld_k, ld_v, ld_o
+ *      (elements, multiples of 8), so that Q, K, V may be slices of a fused projection and K, V a cache.
+ *   heads is a multiple of kv_heads; query head j uses key head j / (heads / kv_heads).
+ *   cu_q (n + 1), k_start, k_len (n each): device int32.  Sequence s has the query rows cu_q[s] ..
+ *      cu_q[s + 1] - 1 and the key rows k_start[s] .. k_start[s] + k_len[s] - 1; its last query sees all its
+ *      keys, the one before all but the last, and so on.
+ *   O = softmax(scale Q K^T over the keys a query sees) V, P rounded to bf16 for its product, O once from
+ *      fp32.  lse (nullable): tq x heads fp32, the logarithm of each softmax's denominator.  A query that
+ *      sees no key (k_len < its position's need, or 0) gets zeros and -inf.
+ * Rows of K and V outside a sequence's keys, and their values, have no effect on it.  Within a sequence a
+ * NaN or infinity in V at a position that a query does not see may still reach it as NaN (0 x inf) when it
+ * is in the query's last block of 128 keys.  Rows of O and lse that belong to no sequence keep what they
+ * held.  Lengths are read on the device: a sequence whose rows leave the tensors is skipped and recorded
+ * (domino_device_status gives DOMINO_ERR_INVALID_ARG); query rows shared by two sequences have undefined
+ * results.  Equal inputs give equal bits.  O may not overlap Q, K or V.
+ * Workspace: domino_attn_packed_workspace_size() bytes, without initialisation. */
+DOMINO_API domino_status domino_attn_packed_workspace_size(int64_t tq, int64_t n, int32_t heads, int32_t kv_heads,
+                                                           int64_t tk, size_t* bytes);
+DOMINO_API domino_status domino_attn_packed_fwd(domino_handle handle, const uint16_t* Q, int64_t ld_q,
+                                                const uint16_t* K, int64_t ld_k, const uint16_t* V, int64_t ld_v,
+                                                const int32_t* cu_q, const int32_t* k_start, const int32_t* k_len,
+                                                float scale, uint16_t* O, int64_t ld_o, float* lse, int64_t tq,
+                                                int64_t n, int32_t heads, int32_t kv_heads, int64_t tk,
+                                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* The reduction step alone (the AllReduce stand-in):
  *   Y[r, c] = bf16( (residual[r, c]) + (((P_0[r,c] + P_1[r,c]) + ...) + P_{t-1}[r,c]) )
  * P: t slices of rows x cols fp32, slice i at P + i*rows*cols, row stride cols.
@@ -345,8 +372,10 @@ DOMINO_API domino_status domino_act_eval(int32_t act, const float* a, const floa
                                          float* db, int64_t n, void* stream);
 
 /* Reads and clears the device error word of every kernel of this library.  *out is
- * DOMINO_OK or DOMINO_ERR_TIMEOUT; *site (nullable) receives the code of the wait that
- * expired.  Synchronises the device. */
+ * DOMINO_OK, DOMINO_ERR_TIMEOUT, or DOMINO_ERR_INVALID_ARG when domino_attn_packed_fwd met lengths that
+ * leave its tensors; *site (nullable) receives the code of the wait that expired (or
+ * DOMINO_BAD_LENGTHS_SITE).  Synchronises the device. */
+#define DOMINO_BAD_LENGTHS_SITE 0x7E0
 DOMINO_API domino_status domino_device_status(domino_handle handle, domino_status* out, int32_t* site);
 
 /* Per-kernel timing: when enabled, each launch is bracketed by CUDA events on the stream it
@@ -371,7 +400,8 @@ typedef enum {
   DOMINO_K_LINEAR_GZ = 15,  /* domino_linear_bwd: gZ and the bias gradient (its two kernels) */
   DOMINO_K_LINEAR_GX = 16,  /* domino_linear_bwd: gZ . W */
   DOMINO_K_LINEAR_GW = 17,  /* domino_linear_bwd: gZ^T . X */
-  DOMINO_K_COUNT = 18
+  DOMINO_K_ATTN_PACKED = 18, /* domino_attn_packed_fwd (its two or three kernels) */
+  DOMINO_K_COUNT = 19
 } domino_kernel_kind;
 DOMINO_API domino_status domino_timing_enable(domino_handle handle, int32_t enable);
 DOMINO_API domino_status domino_timing_reset(domino_handle handle);

@@ -134,3 +134,38 @@ def test_linear_functions_refuse_what_they_cannot_take():
         ops.DominoLinear(64, 128, act="tanh", device="cpu")
     with pytest.raises(ValueError, match="act"):
         ops.DominoLinear(64, 128, act=dm.ACT_SWIGLU, device="cpu")
+
+
+def attn(**kw):
+    a = dict(handle=None, Q=P, ld_q=1024, K=P, ld_k=256, V=P, ld_v=256, cu_q=P, k_start=P, k_len=P, scale=0.1, O=P, ld_o=1024, lse=P,
+             tq=4, n=2, heads=8, kv_heads=2, tk=100, workspace=P, workspace_bytes=1 << 30, stream=0)
+    dm.domino_attn_packed_fwd(**{**a, **kw})
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tq=-1), INVALID), (dict(n=-1), INVALID), (dict(tk=-1), INVALID), (dict(heads=0), INVALID), (dict(kv_heads=0), INVALID),
+    (dict(kv_heads=3), INVALID), (dict(heads=129, kv_heads=1), UNSUPPORTED), (dict(heads=8192, kv_heads=8192), UNSUPPORTED),
+    (dict(tq=1 << 31), UNSUPPORTED), (dict(tk=(1 << 31) - 1023), UNSUPPORTED), (dict(n=1 << 25), UNSUPPORTED),
+    (dict(tq=1 << 30, heads=8, kv_heads=8), UNSUPPORTED), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(ld_q=1016), INVALID), (dict(ld_k=260), ALIGNMENT),
+    (dict(ld_v=128), INVALID), (dict(ld_o=1025), ALIGNMENT), (dict(Q=None), INVALID), (dict(K=None), INVALID), (dict(V=P + 2), ALIGNMENT),
+    (dict(O=P + 8), ALIGNMENT), (dict(lse=P + 4), ALIGNMENT), (dict(cu_q=None), INVALID), (dict(k_start=None), INVALID),
+    (dict(k_len=P + 2), ALIGNMENT), (dict(workspace=None), WORKSPACE), (dict(workspace=P + 64), WORKSPACE),
+    (dict(workspace_bytes=1000), WORKSPACE), (dict(), INVALID), (dict(cu_q=P + 4, lse=None, K=None, V=None, tk=0), INVALID)])
+def test_packed_attention(kw, code):
+    assert status(attn, **kw) == code
+
+
+def test_packed_attention_workspace_size():
+    size = dm.domino_attn_packed_workspace_size
+    assert size(0, 4, 8, 2, 100) == 0 and size(4, 0, 8, 2, 100) == 0
+    # keys too few to be cut: the list of work alone
+    assert size(64, 64, 8, 2, 512) < 1 << 16
+    assert size(64, 64, 8, 2, 1 << 20) > 8 * 152 * 128 * 128 * 4
+    assert status(size, tq=1, n=1, heads=3, kv_heads=2, tk=1) == INVALID
+
+
+def test_packed_attention_function_refuses_what_it_cannot_take():
+    q, cu = torch.zeros(4, 8, 128, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.packed_attention(q, q, q, cu)
