@@ -3,19 +3,17 @@
 // pre-activation, applies an activation, adds a residual and rounds once to bf16; and the column
 // pass of the backward (gZ = gY act'(Z), bias gradient).
 //
-// The product runs on CTA pairs (cluster of 2, tcgen05.mma.cta_group::2, 256 x 256 tiles, 64 elements
-// of the reduction a step through a 6-stage TMA ring), one pair per two SMs:
-//   warp 0 (one lane)  TMA producer of this CTA's 128 rows of A and its 128 rows of B
+// The product runs on CTA pairs (tcgen05.mma.cta_group::2, tiles of 256 rows and `width` columns, 64
+// elements of the reduction a step through a 5-stage TMA ring):
+//   warp 0 (one lane)  TMA producer of this CTA's 128 rows of A and its width / 2 rows of B
 //   warp 1 (one lane of the leader)  MMA issuer, two 256-column accumulators in TMEM
-//   warps 2-9          epilogue, two per TMEM lane quarter with 128 columns each, one row a thread
-// Work split: while whole rounds of tiles (one per pair) remain, a pair takes tiles unit, unit + units,
-// ...  The last round's `rest` tiles, if they would leave pairs idle, are laid end to end along the
-// reduction and cut into equal shares of `q` steps, one per pair; a share covers the end of one tile
-// and perhaps the beginning of the next.  The pair that computes a tile's end adds the other shares'
-// fp32 partials (in memory, one slot a pair) in their order along the reduction and runs the
-// epilogue, so results do not depend on timing.  A pair publishes its partial before it does
-// anything else and waits, last of all, only for pairs of lower index, which were launched before
-// it: no two pairs wait for each other, whatever else occupies the GPU.
+//   warps 2-9          epilogue, two per TMEM lane quarter taking alternate 32-column chunks, one row a
+//                      thread
+// The launcher lays the work over the GPU (lin_plan): pairs take tiles unit, unit + units, ...; the width
+// (64 to 256 columns) is chosen so that the last round leaves few pairs idle; a product with few tiles is
+// also cut along the reduction over the 2 or 4 pairs of a larger cluster, whose fp32 partials meet in
+// shared memory and are added in their order, each pair finishing a part of the rows.  No sum's
+// order depends on timing.
 #include "gemm.cuh"
 #include "ops.h"
 
@@ -24,55 +22,13 @@ namespace dm {
 namespace {
 
 constexpr int kLinThreads = 320;
-constexpr int kLinStages = 6;
-constexpr int kLinStageBytes = 32768;  // 128 x 64 bf16 of A, then of B
-constexpr int kLinWarpBytes = 4096;    // an epilogue warp's boxes: Y, Z (32 x 32 bf16 each)
-constexpr int kLinSmem = 1024 + kCtrlBytes + kLinStages * kLinStageBytes + 8 * kLinWarpBytes;
+constexpr int kLinRing = 5 * 32768;  // the operand ring: stages of 64 elements of a_rows rows of A and the B rows
+constexpr int kLinMaxStages = 16;    // as many as fit, at least 5 (128 rows of A and of B)
+constexpr int kLinBox = 2048;          // 32 x 32 bf16
+constexpr int kLinWarpBytes = 4 * kLinBox;  // an epilogue warp's boxes: a Y for each of its chunks, or two Y and Z
+constexpr int kLinSmem = 1024 + kCtrlBytes + kLinRing + 8 * kLinWarpBytes;
 static_assert(kLinSmem <= 232448, "shared memory beyond the per-CTA limit");
-
-// A pair's share of the last round: [k0, k1) of one tile.
-struct LinSeg {
-  int tile, k0, k1;
-};
-
-struct LinWork {
-  int units, unit, full, kb;
-  LinSeg pub, fin;  // the part published for another pair (k1 > k0), the part finished here
-  int helpers;      // pairs unit - helpers .. unit - 1 hold the partials of fin's tile
-
-  __device__ LinWork(const LinArgs& a, int unit_, int units_) : units(units_), unit(unit_), kb(a.k_blocks) {
-    const int tiles = a.m_tiles * a.n_tiles;
-    full = tiles / a.round;
-    const int rest = tiles - full * a.round;
-    const int total = rest * kb, i0 = unit * a.share, i1 = min(i0 + a.share, total);
-    pub = fin = LinSeg{0, 0, 0};
-    helpers = 0;
-    if (i0 >= i1) return;
-    const int t = i0 / kb, lo = i0 - t * kb, end = (t + 1) * kb;
-    const LinSeg first{full * a.round + t, lo, min(i1, end) - t * kb};
-    if (first.k1 < kb) {
-      pub = first;
-    } else {
-      fin = first;
-      helpers = unit - t * kb / a.share;
-      if (i1 > end) pub = LinSeg{first.tile + 1, 0, i1 - end};
-    }
-  }
-  // segments in the order every role walks them: the published part, whole tiles, the finished part
-  __device__ int count() const { return (pub.k1 > 0 ? 1 : 0) + full + (fin.k1 > 0 ? 1 : 0); }
-  __device__ LinSeg at(int i, bool& publish) const {
-    publish = false;
-    if (pub.k1 > 0) {
-      if (i == 0) {
-        publish = true;
-        return pub;
-      }
-      --i;
-    }
-    if (i < full) return LinSeg{unit + i * units, 0, kb};
-    return fin;
-  }
-};
+static_assert(128 * 256 * 4 <= kLinRing, "a partial fits the idle ring");
 
 // Tiles in groups of 8 rows of tiles, so that the operands of concurrent tiles stay in L2.
 __device__ __forceinline__ void lin_tile(const LinArgs& a, int tile, int& mt, int& nt) {
@@ -82,38 +38,112 @@ __device__ __forceinline__ void lin_tile(const LinArgs& a, int tile, int& mt, in
   nt = in / size;
 }
 
-// Waits until the warp of the same place in pair u has written its block of u's partial slot.
-__device__ __forceinline__ bool wait_flag(const uint32_t* flag, volatile int* abort_flag, int* err, int site,
-                                          int lane) {
-  bool ok = true;
-  if (lane == 0) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 0; ld_acquire_u32(flag) == 0; ++it) {
-      if ((it & 63u) == 63u) {
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (*abort_flag || now - t0 > kWaitTimeoutNs) {
-          if (!*abort_flag) atomicCAS(err, 0, site);
-          *abort_flag = 1;
-          ok = false;
-          break;
-        }
-      }
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// drain_pair_ring (gemm.cuh) for a ring of `stages` stages.
+__device__ __forceinline__ void drain_ring(uint32_t full_bar0, uint32_t stages, uint32_t own, uint32_t peer,
+                                           uint32_t peer_bytes) {
+  const uint32_t end = own > peer ? own : peer;
+#pragma unroll 1
+  for (uint32_t s = 0; s < stages && s < end; ++s) {
+    const uint32_t j = s + (end - 1u - s) / stages * stages;  // last use of stage s below `end`
+    if (j < own && j >= peer)
+      mbar_complete_tx(full_bar0 + 8u * s, peer_bytes);
+    else if (j >= own && j < peer)
+      mbar_arrive_expect_tx(full_bar0 + 8u * s, peer_bytes);
+    mbar_wait_drain(full_bar0 + 8u * s, (j / stages) & 1u);
+  }
+}
+
+// Bias and residual of a 32-column chunk (first column col) for one row; zero outside D.
+struct LinIn {
+  uint4 bias[4], res[4];
+  __device__ __forceinline__ void load(const LinArgs& a, int row, int col) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = col + 8 * q < a.N;
+      bias[q] = in && a.bias ? *reinterpret_cast<const uint4*>(a.bias + col + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
+      res[q] = in && a.R && row < a.M
+                   ? *reinterpret_cast<const uint4*>(a.R + static_cast<int64_t>(row) * a.ld_r + col + 8 * q)
+                   : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
-  if (ok) (void)ld_acquire_u32(flag);
-  return ok;
+};
+
+// Epilogue of one 32-column chunk (first column col) of the rows row0 + lane, r: the sums.
+__device__ __forceinline__ void lin_chunk(const LinArgs& a, const CUtensorMap* tmY, const CUtensorMap* tmZ,
+                                          const uint32_t (&r)[32], const LinIn& in, int row0, int col, int lane,
+                                          uint32_t boxes, uint32_t& n_stored) {
+  // Z = D + bias; Y = act(Z) + R, each rounded once from fp32
+  uint32_t y[16], z[16];
+  auto finish = [&](auto act) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t bw[4] = {in.bias[q].x, in.bias[q].y, in.bias[q].z, in.bias[q].w};
+      const uint32_t rw[4] = {in.res[q].x, in.res[q].y, in.res[q].z, in.res[q].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float z0 = __uint_as_float(r[8 * q + 2 * e]) + bf16lo(bw[e]);
+        const float z1 = __uint_as_float(r[8 * q + 2 * e + 1]) + bf16hi(bw[e]);
+        z[4 * q + e] = pack_bf16x2(z0, z1);
+        y[4 * q + e] = pack_bf16x2(act_fwd(decltype(act)::value, z0) + bf16lo(rw[e]),
+                                   act_fwd(decltype(act)::value, z1) + bf16hi(rw[e]));
+      }
+    }
+  };
+  if (a.act == ACT_GELU)
+    finish(std::integral_constant<int, ACT_GELU>{});
+  else if (a.act == ACT_RELU)
+    finish(std::integral_constant<int, ACT_RELU>{});
+  else
+    finish(std::integral_constant<int, ACT_NONE>{});
+  // the boxes in turn (32 x 64 bytes, 16-byte piece j of row r at j ^ (r / 2 % 4)): four Y, or two pairs
+  const uint32_t box = boxes + (a.save ? (n_stored & 1u) * 2u : (n_stored & 3u)) * kLinBox;
+  if (lane == 0) {
+    if (a.save) bulk_wait_group_read<1>();
+    else bulk_wait_group_read<3>();
+  }
+  __syncwarp();
+  const uint32_t at = box + static_cast<uint32_t>(lane) * 64u, x = (static_cast<uint32_t>(lane) >> 1) & 3u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t off = (static_cast<uint32_t>(j) ^ x) << 4;
+    st_shared_v4(at + off, y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+    if (a.save) st_shared_v4(at + kLinBox + off, z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(tmY, box, col, row0, 0);
+    if (a.save) tma_store_3d(tmZ, box + kLinBox, col, row0, 0);
+    bulk_commit_group();
+  }
+  ++n_stored;
 }
 
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmZ, const LinArgs a) {
-  constexpr int S = kLinStages;
-  constexpr uint32_t kIdesc = idesc_bf16_f32(256, 256, A_MN, B_MN);
+  constexpr int S = kLinMaxStages;
   constexpr int kFull = 0, kEmpty = S, kAccFull = 2 * S, kAccEmpty = 2 * S + 2, kDrain = 2 * S + 4,
                 kPeerCount = 2 * S + 5;
+  static_assert(8 * (kPeerCount + 1) <= 512, "barriers overlap the TMEM slot");
+  const uint32_t stages = static_cast<uint32_t>(a.stages), stage_bytes = static_cast<uint32_t>(a.stage_bytes),
+                 b_at = static_cast<uint32_t>(a.a_rows) * 128u;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -124,9 +154,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  // CTA `crank` of the cluster: half `rank` of pair `part`, which computes part `part` of the reduction
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
+  const int part = static_cast<int>(crank >> 1);
   const bool leader = rank == 0;
-  const int unit = static_cast<int>(blockIdx.x >> 1), units = static_cast<int>(gridDim.x >> 1);
+  const int unit = static_cast<int>(blockIdx.x) / (2 * a.parts), units = static_cast<int>(gridDim.x) / (2 * a.parts);
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
+  const int k_first = part * a.k_blocks / a.parts, k_last = (part + 1) * a.k_blocks / a.parts;
+  const int tiles = a.m_tiles * a.n_tiles;
   int* err = &g_gemm_err;
 
   if (threadIdx.x == 0) {
@@ -153,220 +188,219 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish_pair();
   }
+  pdl_launch();
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const LinWork w(a, unit, units);
-  const int nseg = w.count();
+  pdl_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer
+    {
+      // ---------------- TMA producer (the warp walks the loop, one elected lane issues)
+      const bool one = elect_one();
       uint32_t s = 0, ph = 0, issued = 0;
-      bool ok = true, pub;
-      for (int i = 0; ok && i < nseg; ++i) {
-        const LinSeg g = w.at(i, pub);
+      bool ok = true;
+      const uint32_t full_lead = mapa_shared(bar(kFull), lead);
+      const uint32_t b_rows = static_cast<uint32_t>(a.width) / 2;
+      const uint32_t b_bytes = (B_MN ? (b_rows + 63u) / 64u * 64u : b_rows) * 128u;
+      // with at most 128 rows of A the second CTA has none: it loads none, and its accumulator is not read
+      const bool has_a = leader || a.M > 128;
+      const uint32_t a_bytes = static_cast<uint32_t>(a.a_rows) * 128u;
+      const uint32_t peer_bytes = (a.M > 128 ? a_bytes : 0u) + b_bytes;
+      for (int tile = unit; ok && tile < tiles; tile += units) {
         int mt, nt;
-        lin_tile(a, g.tile, mt, nt);
-        const int m0 = mt * 256 + static_cast<int>(rank) * 128, n0 = nt * 256 + static_cast<int>(rank) * 128;
-        for (int kb = g.k0; kb < g.k1; ++kb) {
-          if (!mbar_wait(bar(kEmpty + s), ph ^ 1u, abort_flag, err, a.err_site + 1)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = stage0 + s * kLinStageBytes, sb = sa + kLinStageBytes / 2;
-          const uint32_t fb = mapa_shared(bar(kFull + s), 0);  // the leader's barrier counts both CTAs' bytes
+        lin_tile(a, tile, mt, nt);
+        const int m0 = mt * 256 + static_cast<int>(rank) * 128, n0 = nt * a.width + static_cast<int>(rank * b_rows);
+        for (int kb = k_first; kb < k_last; ++kb) {
+          ok = mbar_wait(bar(kEmpty + s), ph ^ 1u, abort_flag, err, a.err_site + 1);
+          if (!ok) break;
+          const uint32_t sa = stage0 + s * stage_bytes, sb = sa + b_at;
+          const uint32_t fb = full_lead + 8u * s;  // the leader's barrier counts both CTAs' bytes
           const int k0 = kb * kBK;
-          if (leader) mbar_arrive_expect_tx(bar(kFull + s), 2u * kLinStageBytes);
-          if constexpr (!A_MN) {
-            tma_load_3d_pair(sa, &tmA, fb, k0, m0, 0);
-          } else {
-            tma_load_3d_pair(sa, &tmA, fb, m0, k0, 0);
-            tma_load_3d_pair(sa + 8192, &tmA, fb, m0 + 64, k0, 0);
+          if (one) {
+          if (leader) mbar_arrive_expect_tx(bar(kFull + s), a_bytes + b_bytes + peer_bytes);
+          if (has_a) {
+            if constexpr (!A_MN) {
+              tma_load_3d_pair(sa, &tmA, fb, k0, m0, 0);
+            } else {
+              tma_load_3d_pair(sa, &tmA, fb, m0, k0, 0);
+              tma_load_3d_pair(sa + 8192, &tmA, fb, m0 + 64, k0, 0);
+            }
           }
           if constexpr (!B_MN) {
             tma_load_3d_pair(sb, &tmB, fb, k0, n0, 0);
           } else {
             tma_load_3d_pair(sb, &tmB, fb, n0, k0, 0);
-            tma_load_3d_pair(sb + 8192, &tmB, fb, n0 + 64, k0, 0);
+            if (b_rows > 64) tma_load_3d_pair(sb + 8192, &tmB, fb, n0 + 64, k0, 0);
+          }
           }
           ++issued;
-          if (++s == S) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
       // both CTAs' copies have landed before the pair leaves, also after an abort (gemm.cuh)
-      if (!leader) {
-        st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(peer_issued)), 0), issued);
-        mbar_arrive_cluster(mapa_shared(bar(kPeerCount), 0));
+      if (!one) {
+      } else if (!leader) {
+        st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(peer_issued)), lead), issued);
+        mbar_arrive_cluster(mapa_shared(bar(kPeerCount), lead));
       } else if (mbar_wait_cluster_acquire(bar(kPeerCount), 0, kPeerCountTimeoutNs)) {
         const uint32_t peer = *peer_issued;
-        if (!ok || peer != issued || *abort_flag) drain_pair_ring<S>(bar(kFull), issued, peer, kLinStageBytes);
+        if (!ok || peer != issued || *abort_flag) drain_ring(bar(kFull), stages, issued, peer, peer_bytes);
       } else {
         const uint64_t t0 = global_timer_ns();
         while (global_timer_ns() - t0 < kPeerCopyGraceNs) {
         }
       }
     }
+    __syncwarp();
+    if (a.parts > 1) {  // the epilogue's two
+      cluster_sync();
+      cluster_sync();
+    }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ---------------- MMA issuer for both CTAs
+    if (leader) {
+      // ---------------- MMA issuer for both CTAs.  The whole warp walks the loop and one elected lane issues:
+      // the operands are then warp-uniform, and a product's issue costs a fraction of what it costs a thread of
+      // a diverged warp (measured: 134 clocks, as long as a 256 x 256 x 16 product takes).
+      const bool one = elect_one();
       uint32_t s = 0, ph = 0;
-      bool ok = true, pub;
-      for (int i = 0; ok && i < nseg; ++i) {
-        const LinSeg g = w.at(i, pub);
+      bool ok = true;
+      const uint32_t idesc = idesc_bf16_f32(256, a.width, A_MN, B_MN);
+      const uint64_t a_desc = A_MN ? sdesc_sw128(stage0, 8192, 1024) : sdesc_sw128(stage0, 16, 1024);
+      const uint64_t b_desc = B_MN ? sdesc_sw128(stage0 + b_at, 8192, 1024) : sdesc_sw128(stage0 + b_at, 16, 1024);
+      int i = 0;
+      for (int tile = unit; ok && tile < tiles; tile += units, ++i) {
         const int acc = i & 1;
-        if (!mbar_wait(bar(kAccEmpty + acc), ((static_cast<uint32_t>(i) >> 1) & 1u) ^ 1u, abort_flag, err,
-                       a.err_site + 2))
-          break;
+        ok = mbar_wait(bar(kAccEmpty + acc), ((static_cast<uint32_t>(i) >> 1) & 1u) ^ 1u, abort_flag, err,
+                       a.err_site + 2);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
-        for (int kb = g.k0; kb < g.k1; ++kb) {
-          if (!mbar_wait(bar(kFull + s), ph, abort_flag, err, a.err_site + 3)) {
-            ok = false;
-            break;
-          }
+        for (int kb = k_first; kb < k_last; ++kb) {
+          ok = mbar_wait(bar(kFull + s), ph, abort_flag, err, a.err_site + 3);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = stage0 + s * kLinStageBytes, sb = sa + kLinStageBytes / 2;
+          const uint64_t off = static_cast<uint64_t>(s * stage_bytes >> 4);
+          if (one) {
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            const uint64_t ad = A_MN ? sdesc_sw128(sa + kk * 2048, 8192, 1024) : sdesc_sw128(sa + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? sdesc_sw128(sb + kk * 2048, 8192, 1024) : sdesc_sw128(sb + kk * 32, 16, 1024);
-            umma_bf16_pair(d, ad, bd, kIdesc, static_cast<uint32_t>(kb != g.k0 || kk != 0));
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              umma_bf16_pair(d, a_desc + off + (A_MN ? kk * 128 : kk * 2), b_desc + off + (B_MN ? kk * 128 : kk * 2), idesc,
+                             static_cast<uint32_t>(kb != k_first || kk != 0));
+            umma_commit_pair_multicast(bar(kEmpty + s), pair_mask);
           }
-          umma_commit_pair_multicast(bar(kEmpty + s), 0x3);
-          if (++s == S) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair_multicast(bar(kAccFull + acc), 0x3);
+        if (one) umma_commit_pair_multicast(bar(kAccFull + acc), pair_mask);
       }
-      umma_commit_pair(bar(kDrain));
+      if (one) umma_commit_pair(bar(kDrain));
+      __syncwarp();
       mbar_wait_drain(bar(kDrain), 0);
     }
+    __syncwarp();
+    if (a.parts > 1) {  // the epilogue's two
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
-    // ---------------- epilogue: rows of the warp's TMEM lane quarter, 128 of the tile's columns
+    // ---------------- epilogue: rows of the warp's TMEM lane quarter, every other 32-column chunk
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
-    const uint32_t box_y = stage0 + S * kLinStageBytes + static_cast<uint32_t>(ew) * kLinWarpBytes, box_z = box_y + 2048u;
-    const uint32_t rsw = static_cast<uint32_t>(lane) * 64u, rx = (static_cast<uint32_t>(lane) >> 1) & 3u;
-    const uint32_t tq = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
-    // this warp's block in a partial slot: 32 pieces of 16 bytes a lane, 512 bytes a piece
-    const int64_t wofs = static_cast<int64_t>(rank * 8 + static_cast<uint32_t>(ew)) * kSlotWarpBytes + lane * 16;
-    const uint32_t wflag = rank * 8 + static_cast<uint32_t>(ew);
-    auto slot = [&](int u) { return a.part + static_cast<int64_t>(u) * kSlotBytes + wofs; };
-    bool stored = false, pub, ok = true;
-    for (int i = 0; ok && i < nseg; ++i) {
-      const LinSeg g = w.at(i, pub);
-      int mt, nt;
-      lin_tile(a, g.tile, mt, nt);
-      const int row0 = mt * 256 + static_cast<int>(rank) * 128 + quarter * 32, row = row0 + lane;
-      const int colw = nt * 256 + half * 128;
-      const int acc = i & 1;
-      ok = mbar_wait(bar(kAccFull + acc), (static_cast<uint32_t>(i) >> 1) & 1u, abort_flag, err, a.err_site + 4);
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t tacc = tq + static_cast<uint32_t>(acc * kBN);
-      const bool live = row0 < a.M && colw < a.N;  // something of this warp's part is inside D
-      const int nhelp = (!pub && i == nseg - 1 && w.fin.k1 > 0) ? w.helpers : 0;
-      for (int u = unit - nhelp; ok && live && u < unit; ++u)
-        ok = wait_flag(a.flags + u * 16 + wflag, abort_flag, err, a.err_site + 6, lane);
-      if (!ok) break;
+    const uint32_t boxes = stage0 + kLinRing + static_cast<uint32_t>(ew) * kLinWarpBytes;
+    const uint32_t tq = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t n_stored = 0;
+    if (a.parts == 1) {
+      int i = 0;
+      for (int tile = unit; tile < tiles; tile += units, ++i) {
+        int mt, nt;
+        lin_tile(a, tile, mt, nt);
+        const int row0 = mt * 256 + static_cast<int>(rank) * 128 + quarter * 32;
+        const int acc = i & 1;
+        // a chunk's bias and residual are loaded before the previous one is finished (the first's while the
+        // products run)
+        LinIn in;
+        in.load(a, row0 + lane, nt * a.width + 32 * half);
+        const bool ok = mbar_wait(bar(kAccFull + acc), (static_cast<uint32_t>(i) >> 1) & 1u, abort_flag, err, a.err_site + 4);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
+        const uint32_t tacc = tq + static_cast<uint32_t>(acc * kBN);
 #pragma unroll 1
-      for (int cc = 0; cc < 128; cc += 32) {
-        const int col = colw + cc;
-        if (!live || col >= a.N) break;
-        uint32_t r[32];
-        tmem_ld32(tacc + static_cast<uint32_t>(cc), r);
-        if (pub) {
+        for (int cc = 32 * half; cc < a.width; cc += 64) {
+          const int col = nt * a.width + cc;
+          if (row0 >= a.M || col >= a.N) break;
+          uint32_t r[32];
+          tmem_ld32(tacc + static_cast<uint32_t>(cc), r);
+          const LinIn now = in;
+          if (cc + 64 < a.width) in.load(a, row0 + lane, col + 64);
           tmem_ld_wait();
-          if (row < a.M) {
-            uint4* p = reinterpret_cast<uint4*>(slot(unit)) + cc / 4 * 32;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              __stcg(p + q * 32, make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]));
-          }
-          continue;
+          lin_chunk(a, &tmY, &tmZ, r, now, row0, col, lane, boxes, n_stored);
         }
-        uint4 bias[4], res[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bool in = col + 8 * q < a.N;
-          bias[q] = in && a.bias ? *reinterpret_cast<const uint4*>(a.bias + col + 8 * q) : make_uint4(0u, 0u, 0u, 0u);
-          res[q] = in && a.R && row < a.M
-                       ? *reinterpret_cast<const uint4*>(a.R + static_cast<int64_t>(row) * a.ld_r + col + 8 * q)
-                       : make_uint4(0u, 0u, 0u, 0u);
-        }
-        tmem_ld_wait();
-        for (int u = unit - nhelp; u < unit; ++u) {
-          if (row >= a.M) break;
-          const uint4* p = reinterpret_cast<const uint4*>(slot(u)) + cc / 4 * 32;
-          uint4 v[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = __ldcg(p + q * 32);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + __uint_as_float(v[q].x));
-            r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + __uint_as_float(v[q].y));
-            r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + __uint_as_float(v[q].z));
-            r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + __uint_as_float(v[q].w));
-          }
-        }
-        // Z = D + bias; Y = act(Z) + R, each rounded once from fp32
-        uint32_t yz[2][16];
-        auto finish = [&](auto act) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t bw[4] = {bias[q].x, bias[q].y, bias[q].z, bias[q].w};
-            const uint32_t rw[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float z0 = __uint_as_float(r[8 * q + 2 * e]) + bf16lo(bw[e]);
-              const float z1 = __uint_as_float(r[8 * q + 2 * e + 1]) + bf16hi(bw[e]);
-              yz[1][4 * q + e] = pack_bf16x2(z0, z1);
-              yz[0][4 * q + e] = pack_bf16x2(act_fwd(decltype(act)::value, z0) + bf16lo(rw[e]),
-                                             act_fwd(decltype(act)::value, z1) + bf16hi(rw[e]));
-            }
-          }
-        };
-        if (a.act == ACT_GELU)
-          finish(std::integral_constant<int, ACT_GELU>{});
-        else if (a.act == ACT_RELU)
-          finish(std::integral_constant<int, ACT_RELU>{});
-        else
-          finish(std::integral_constant<int, ACT_NONE>{});
-        if (lane == 0 && stored) bulk_wait_group_read<0>();
+        tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(bar(kAccEmpty + acc), lead));
+      }
+    } else {
+      // one tile a cluster: each pair sends its fp32 partial of lane quarter qd to the pair that finishes it,
+      // qd / (4 / parts), into that CTA's ring, block `part` (4 / parts x 32 rows, 16-byte piece j of row r
+      // at j ^ (r % 8)); the finishing pair adds the blocks in their order
+      int mt, nt;
+      lin_tile(a, unit, mt, nt);
+      const int row_cta = mt * 256 + static_cast<int>(rank) * 128, rows4 = 4 / a.parts;
+      const uint32_t row_bytes = static_cast<uint32_t>(a.width) * 4u, key = static_cast<uint32_t>(lane) & 7u;
+      const uint32_t block = static_cast<uint32_t>(rows4) * 32u * row_bytes;
+      const bool got = mbar_wait(bar(kAccFull), 0, abort_flag, err, a.err_site + 4);
+      const bool ok = __all_sync(0xFFFFFFFFu, got);
+      tc_fence_after();
+      cluster_sync();  // every ring of the cluster is idle (after an abort: nothing is sent or read)
+      if (ok && row_cta + quarter * 32 < a.M) {
+        const uint32_t p = mapa_shared(stage0, static_cast<uint32_t>(quarter / rows4 * 2) + rank) + static_cast<uint32_t>(part) * block +
+                           static_cast<uint32_t>(quarter % rows4 * 32 + lane) * row_bytes;
+#pragma unroll 1
+        for (int cc = 32 * half; cc < a.width; cc += 64) {
+          uint32_t r[32];
+          tmem_ld32(tq + static_cast<uint32_t>(cc), r);
+          tmem_ld_wait();
+          if (row_cta + quarter * 32 + lane < a.M) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t off = rsw + ((static_cast<uint32_t>(j) ^ rx) << 4);
-          st_shared_v4(box_y + off, yz[0][4 * j], yz[0][4 * j + 1], yz[0][4 * j + 2], yz[0][4 * j + 3]);
-          if (a.save) st_shared_v4(box_z + off, yz[1][4 * j], yz[1][4 * j + 1], yz[1][4 * j + 2], yz[1][4 * j + 3]);
+            for (uint32_t j = 0; j < 8; ++j)
+              st_shared_cluster_v4(p + (((static_cast<uint32_t>(cc) / 4u + j) ^ key) << 4), r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tmY, box_y, col, row0, 0);
-          if (a.save) tma_store_3d(&tmZ, box_z, col, row0, 0);
-          bulk_commit_group();
-        }
-        stored = true;
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (pub) {
-          __threadfence();
-          asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flags + unit * 16 + wflag), "r"(1u) : "memory");
+      cluster_sync();  // every block has arrived
+      if (ok) {
+        const int chunks = a.width / 32;
+#pragma unroll 1
+        for (int c = ew; c < rows4 * chunks; c += 8) {
+          const int qd = c / chunks, cc = (c - qd * chunks) * 32;
+          const int row0 = row_cta + (part * rows4 + qd) * 32, col = nt * a.width + cc;
+          if (row0 >= a.M || col >= a.N) continue;
+          const uint32_t p = stage0 + static_cast<uint32_t>(qd * 32 + lane) * row_bytes;
+          uint32_t r[32];
+          LinIn in;
+          in.load(a, row0 + lane, col);
+#pragma unroll 1
+          for (int q = 0; q < a.parts; ++q) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 v = ld_shared_v4(p + static_cast<uint32_t>(q) * block +
+                                           (((static_cast<uint32_t>(cc) / 4u + static_cast<uint32_t>(j)) ^ key) << 4));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                r[4 * j + e] = q == 0 ? w[e] : __float_as_uint(__uint_as_float(r[4 * j + e]) + __uint_as_float(w[e]));
+            }
+          }
+          lin_chunk(a, &tmY, &tmZ, r, in, row0, col, lane, boxes, n_stored);
         }
-        mbar_arrive_cluster_relaxed(mapa_shared(bar(kAccEmpty + acc), 0));
       }
     }
     if (lane == 0) bulk_wait_group_all();
@@ -382,74 +416,29 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   }
 }
 
-// Steps of the reduction below which a share of the last round is not cut further.
-constexpr int kMinShare = 8;
-
-// How a product of `tiles` tiles of `kb` steps is laid over at most `pairs` pairs.
-struct LinSplit {
-  int units, round, share;
-  bool split;
-};
-LinSplit lin_split(int64_t tiles, int kb, int pairs) {
-  LinSplit s;
-  s.round = pairs;
-  const int64_t full = tiles / pairs, rest = tiles - full * pairs;
-  int64_t q = (rest * kb + pairs - 1) / pairs;
-  if (q < kMinShare) q = kMinShare;
-  if (rest == 0 || q * 8 > int64_t(kb) * 7) q = kb;  // little to gain: whole tiles
-  s.share = static_cast<int>(q);
-  const int64_t parts = (rest * kb + q - 1) / q;
-  s.units = static_cast<int>(full > 0 ? pairs : parts);
-  s.split = rest > 0 && q < kb;
-  return s;
-}
-
 template <bool A_MN, bool B_MN>
-cudaError_t launch_linear_t(const LinMaps& m, LinArgs a, cudaStream_t st) {
+cudaError_t launch_linear_t(const LinMaps& m, const LinArgs& a, cudaStream_t st) {
   auto fn = linear_kernel<A_MN, B_MN>;
-  static std::atomic<int> pairs_of[kMaxDevices];  // co-resident pairs per device; 0 = not set up
+  static std::atomic<bool> ready_of[kMaxDevices];  // the shared-memory opt-in, per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = kLinSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int pairs = pairs_of[dev].load(std::memory_order_acquire);
-  if (pairs == 0) {
+  if (!ready_of[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kLinSmem);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(2);
-    e = cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg);
-    if (e != cudaSuccess) return e;
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
-    if (pairs > kLinPairs) pairs = kLinPairs;  // what the workspace is sized for
-    pairs_of[dev].store(pairs, std::memory_order_release);
+    ready_of[dev].store(true, std::memory_order_release);
   }
-  const LinSplit s = lin_split(int64_t(a.m_tiles) * a.n_tiles, a.k_blocks, pairs);
-  if (s.units == 0) return cudaSuccess;
-  a.round = s.round;
-  a.share = s.share;
-  if (s.split) {
-    e = cudaMemsetAsync(a.flags, 0, kLinPairs * 64, st);
-    if (e != cudaSuccess) return e;
-  }
-  cfg.gridDim = dim3(2 * s.units);
-  return cudaLaunchKernelEx(&cfg, fn, m.a, m.b, m.y, m.z, a);
+  return launch_pdl(fn, dim3(static_cast<unsigned>(2 * a.parts * a.units)), dim3(kLinThreads), kLinSmem, 2 * a.parts, st,
+                    m.a, m.b, m.y, m.z, a);
 }
 
 // ---- gZ = gY act'(Z) and the columns' sums of gZ (before its rounding).  A block owns 256 columns
 // and a range of rows; lane l of each of its 8 warps owns columns 8 l .. 8 l + 7.
 __global__ void __launch_bounds__(256) lin_gz_kernel(const LinGzArgs a) {
   __shared__ float sums[8][256];
+  pdl_launch();
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + lane * 8;
   const int64_t per = (a.M + gridDim.y - 1) / gridDim.y, r0 = per * blockIdx.y;
@@ -516,6 +505,8 @@ __global__ void __launch_bounds__(256) lin_gz_kernel(const LinGzArgs a) {
 // The row ranges' sums in order, written or added to gbias.
 __global__ void __launch_bounds__(256) lin_gbias_kernel(const float* __restrict__ part, int parts, int64_t n,
                                                         float* gbias, int accumulate) {
+  pdl_launch();
+  pdl_wait();
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= n) return;
   float s = 0.0f;
@@ -526,15 +517,37 @@ __global__ void __launch_bounds__(256) lin_gbias_kernel(const float* __restrict_
 
 }  // namespace
 
-int64_t lin_scratch_bytes(int64_t m, int64_t n, int64_t k) {
-  const int64_t tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  // a device may keep fewer pairs resident than kLinPairs: any last round may then be split
-  return tiles == 0 || k <= kMinShare * kBK ? 0 : int64_t(kLinPairs) * (kSlotBytes + 64);
+// Estimated clocks of a product: a step of the reduction takes about 250 + 1.25 width (measured over two rounds
+// of 152 tiles with 32 and 64 steps: 333 at 64 columns, 399 at 128, 488 at 192, 575 at 256), a round's change
+// of tiles 8 and the last epilogue 20 a column, the start 4500, and joining cut reductions as below.  The
+// choices it makes are within 5 % of the best of all widths and cuts at the shapes tried.
+LinPlan lin_plan(int64_t m, int64_t n, int64_t k) {
+  constexpr int kLinQuads = 36, kLinOctets = 15;  // clusters of 4 and 8 CTAs that a GB300 keeps resident
+  const int64_t m_tiles = (m + 255) / 256, kb = (k + 63) / 64;
+  LinPlan best = {256, 1, 0};
+  double least = 1e300;
+  for (int width = 256; width >= 64; width -= 32) {
+    const int64_t tiles = m_tiles * ((n + width - 1) / width);
+    for (int parts = 1; parts <= 4; parts *= 2) {
+      if (parts > 1 && (tiles > (parts == 2 ? kLinQuads : kLinOctets) || kb < 4 * parts)) break;
+      const int64_t rounds = parts > 1 ? 1 : (tiles + kLinPairs - 1) / kLinPairs;
+      const double steps = double((kb + parts - 1) / parts);
+      double cost = double(rounds) * (steps * (250 + 1.25 * width) + 8.0 * width) + 20.0 * width;
+      if (parts > 1) cost += (parts == 2 ? 1200.0 : 3000.0) + 45.0 * width * double(m < 256 ? m : 256) / 256;
+      if (cost < least) {
+        least = cost;
+        best = {width, parts, static_cast<int>(parts > 1 || tiles < kLinPairs ? tiles : kLinPairs)};
+      }
+    }
+  }
+  return best;
 }
 
-cudaError_t launch_linear(int kind, const LinMaps& m, LinArgs a, void* scratch, cudaStream_t st) {
-  a.part = static_cast<uint8_t*>(scratch);
-  a.flags = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(scratch) + int64_t(kLinPairs) * kSlotBytes);
+cudaError_t launch_linear(int kind, const LinMaps& m, LinArgs a, cudaStream_t st) {
+  if (a.units == 0) return cudaSuccess;
+  const int b_rows = kind == LIN_FWD ? a.width / 2 : (a.width / 2 + 63) / 64 * 64;
+  a.stage_bytes = (a.a_rows + b_rows) * 128;  // both multiples of 8 rows: swizzle atoms stay aligned
+  a.stages = kLinRing / a.stage_bytes < kLinMaxStages ? kLinRing / a.stage_bytes : kLinMaxStages;
   switch (kind) {
     case LIN_FWD: return launch_linear_t<false, false>(m, a, st);
     case LIN_GX: return launch_linear_t<false, true>(m, a, st);
@@ -552,14 +565,12 @@ int lin_gz_row_blocks(int64_t m, int64_t n) {
 cudaError_t launch_lin_gz(const LinGzArgs& a, cudaStream_t st) {
   const int rb = lin_gz_row_blocks(a.M, a.N);
   if (rb == 0 || a.N == 0) return cudaSuccess;
-  lin_gz_kernel<<<dim3(static_cast<unsigned>((a.N + 255) / 256), static_cast<unsigned>(rb)), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(lin_gz_kernel, dim3(static_cast<unsigned>((a.N + 255) / 256), static_cast<unsigned>(rb)), dim3(256), 0, 1, st, a);
 }
 
 cudaError_t launch_lin_gbias(const float* part, int64_t m, int64_t n, float* gbias, int accumulate, cudaStream_t st) {
-  lin_gbias_kernel<<<static_cast<unsigned>((n + 255) / 256), 256, 0, st>>>(part, lin_gz_row_blocks(m, n), n, gbias,
-                                                                            accumulate);
-  return cudaGetLastError();
+  return launch_pdl(lin_gbias_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, 1, st, part,
+                    lin_gz_row_blocks(m, n), n, gbias, accumulate);
 }
 
 cudaError_t take_linear_error(int* code) { return take_error_word(code); }

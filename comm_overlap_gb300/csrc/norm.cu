@@ -63,6 +63,8 @@ __device__ __forceinline__ void load_row(uint4 (&w)[NPT], const uint16_t* p, int
 // registers), y = (x - mean) rstd gamma + beta.
 template <int NPT>
 __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a, const int tpr) {
+  pdl_launch();
+  pdl_wait();
   __shared__ float2 red_all[8][32];
   const int team = threadIdx.x / tpr, t = threadIdx.x - team * tpr, warps = tpr >> 5;
   const int teams = blockDim.x / tpr;
@@ -142,6 +144,8 @@ template <int NPT, bool PREFETCH>
 __global__ void __launch_bounds__(kTeamThreads) ln_bwd_kernel(const LnBwdArgs a, float* __restrict__ part,
                                                               const int tpr) {
   extern __shared__ float cols[];  // teams x 2 h (only with several teams)
+  pdl_launch();
+  pdl_wait();
   __shared__ float2 red_all[8][32];
   const int team = threadIdx.x / tpr, t = threadIdx.x - team * tpr, warps = tpr >> 5;
   const int teams = blockDim.x / tpr;
@@ -278,6 +282,8 @@ __global__ void __launch_bounds__(kTeamThreads) ln_bwd_kernel(const LnBwdArgs a,
 // groups in order.  Columns 0 .. h-1 go to ggamma, the others to gbeta (nullable).
 __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__ part, int parts, int64_t h,
                                                        float* ggamma, float* gbeta, int accumulate) {
+  pdl_launch();
+  pdl_wait();
   __shared__ float4 sums[32][32];
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * 4;
@@ -306,55 +312,39 @@ __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__
   *reinterpret_cast<float4*>(o) = s;
 }
 
+int pieces_per_thread(int64_t h) { return h <= 2048 ? 1 : (h <= 8192 ? 2 : 4); }
 int team_threads(int64_t h, int npt) { return static_cast<int>(((h / 8 + npt - 1) / npt + 31) / 32 * 32); }
 
 }  // namespace
 
 int ln_bwd_blocks(int64_t rows, int64_t h, int sms) {
-  const int npt = h <= 2048 ? 1 : (h <= 8192 ? 2 : 4);
-  const int tpr = team_threads(h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
+  const int tpr = team_threads(h, pieces_per_thread(h)), teams = tpr >= 256 ? 1 : 256 / tpr;
   const int64_t need = (rows + 4 * teams - 1) / (4 * teams), most = 2 * int64_t(sms);
   return static_cast<int>(need < most ? need : most);
 }
 
 cudaError_t launch_ln_fwd(const LnFwdArgs& a, int sms, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
-  const int npt = a.h <= 2048 ? 1 : (a.h <= 8192 ? 2 : 4);
-  const int tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
+  const int npt = pieces_per_thread(a.h), tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
   const int64_t need = (a.rows + teams - 1) / teams, most = int64_t(sms) * (2048 / (teams * tpr));
-  const int grid = static_cast<int>(need < most ? need : most);
-  if (npt == 1)
-    ln_fwd_kernel<1><<<grid, teams * tpr, 0, st>>>(a, tpr);
-  else if (npt == 2)
-    ln_fwd_kernel<2><<<grid, teams * tpr, 0, st>>>(a, tpr);
-  else
-    ln_fwd_kernel<4><<<grid, teams * tpr, 0, st>>>(a, tpr);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(static_cast<unsigned>(teams * tpr));
+  return launch_pdl(npt == 1 ? ln_fwd_kernel<1> : npt == 2 ? ln_fwd_kernel<2> : ln_fwd_kernel<4>, grid, block, 0, 1, st, a, tpr);
 }
 
 cudaError_t launch_ln_bwd(const LnBwdArgs& a, float* part, int sms, cudaStream_t st) {
   const int grid = ln_bwd_blocks(a.rows, a.h, sms);
   if (grid == 0) return cudaSuccess;
-  {
-    const int npt = a.h <= 2048 ? 1 : (a.h <= 8192 ? 2 : 4);
-    const int tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
-    // several teams only for h <= 2048 (npt 1, at most 8 teams x 2 h floats with teams x h <= 2048)
-    const size_t smem = teams > 1 ? size_t(teams) * 2 * a.h * 4 : 0;
-    if (npt == 1)
-      ln_bwd_kernel<1, true><<<grid, teams * tpr, smem, st>>>(a, part, tpr);
-    else if (npt == 2)
-      ln_bwd_kernel<2, true><<<grid, teams * tpr, smem, st>>>(a, part, tpr);
-    else
-      ln_bwd_kernel<4, false><<<grid, teams * tpr, smem, st>>>(a, part, tpr);
-  }
-  return cudaGetLastError();
+  const int npt = pieces_per_thread(a.h), tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
+  // several teams only for h <= 1024 (at most 8 teams x 2 h floats with teams x h <= 2048)
+  const size_t smem = teams > 1 ? size_t(teams) * 2 * a.h * 4 : 0;
+  return launch_pdl(npt == 1 ? ln_bwd_kernel<1, true> : npt == 2 ? ln_bwd_kernel<2, true> : ln_bwd_kernel<4, false>, dim3(grid),
+                    dim3(static_cast<unsigned>(teams * tpr)), smem, 1, st, a, part, tpr);
 }
 
 cudaError_t launch_ln_cols(const LnBwdArgs& a, const float* part, int sms, cudaStream_t st) {
   const int grid = ln_bwd_blocks(a.rows, a.h, sms);
   const int cgrid = static_cast<int>((2 * a.h + 127) / 128);
-  ln_cols_kernel<<<cgrid, 1024, 0, st>>>(part, grid, a.h, a.ggamma, a.gbeta, a.accumulate);
-  return cudaGetLastError();
+  return launch_pdl(ln_cols_kernel, dim3(cgrid), dim3(1024), 0, 1, st, part, grid, a.h, a.ggamma, a.gbeta, a.accumulate);
 }
 
 }  // namespace dm

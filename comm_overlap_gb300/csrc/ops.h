@@ -7,6 +7,7 @@
 
 #include <functional>
 #include <string>
+#include <utility>
 
 #include "../../include/domino.h"
 #include "kernels.h"
@@ -20,6 +21,34 @@ int handle_sms(domino_handle H);
 // One launch through the handle: launch count, per-kernel timing, failure injection, NVTX range.
 domino_status launch_on(domino_handle H, int kind, cudaStream_t st, const char* what,
                         const std::function<cudaError_t()>& fn);
+
+// ---- programmatic dependent launch: a kernel may be placed on SMs that its predecessor in the stream has left, and
+// sets itself up there; before it touches memory that others use it waits, in every thread's path, for the
+// predecessor's end (pdl_wait).  Saves 2 - 3 us between the short kernels of these operators.
+#ifdef __CUDACC__
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... Params, class... Args>
+cudaError_t launch_pdl(void (*fn)(Params...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
+                       Args&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fn, static_cast<Params>(std::forward<Args>(args))...);
+}
+#endif
 
 // ---- LayerNorm with weight and bias (norm.cu); h a multiple of 8, at most kLnMaxH
 constexpr int64_t kLnMaxH = 16384;
@@ -59,24 +88,28 @@ enum LinKind : int {
   LIN_GX = 1,   // B contiguous along its rows: gZ . W
   LIN_GW = 2,   // both contiguous along their rows: gZ^T . X
 };
-// Maps (all with a third dimension of one): operands in boxes of 64 (reduction) x 128 rows, or, contiguous
-// along their rows, 64 (rows) x 64 (reduction), 128-byte swizzle; y, z (z only with save) in boxes of
-// 32 x 32, 64-byte swizzle.
+// How a product is laid over the GPU: tiles of 256 x width, each computed by `parts` pairs along the
+// reduction, by `units` pairs (groups of `parts` pairs).
+struct LinPlan {
+  int width, parts, units;
+};
+LinPlan lin_plan(int64_t m, int64_t n, int64_t k);
+// Maps (all with a third dimension of one): operands in boxes of 64 (reduction) x a_rows, or x width / 2 for
+// B, or, contiguous along their rows, 64 (rows) x 64 (reduction), 128-byte swizzle; y, z (z only with save) in
+// boxes of 32 x 32, 64-byte swizzle.
 struct LinMaps {
   CUtensorMap a, b, y, z;
 };
 struct LinArgs {
   int32_t M, N, m_tiles, n_tiles, k_blocks, act, save, err_site;
-  const uint16_t* bias;  // nullable
-  const uint16_t* R;     // nullable
+  int32_t width, parts, units;  // lin_plan
+  int32_t a_rows;               // rows of a box of A: 128, or fewer when A is smaller
+  int32_t stages, stage_bytes;  // set by the launcher: the operand ring
+  const uint16_t* bias;         // nullable
+  const uint16_t* R;            // nullable
   int64_t ld_r;
-  // set by the launcher
-  int32_t round, share;  // tiles in a whole round; steps of the last round that a pair computes
-  uint8_t* part;
-  uint32_t* flags;
 };
-int64_t lin_scratch_bytes(int64_t m, int64_t n, int64_t k);
-cudaError_t launch_linear(int kind, const LinMaps& m, LinArgs a, void* scratch, cudaStream_t st);
+cudaError_t launch_linear(int kind, const LinMaps& m, LinArgs a, cudaStream_t st);
 struct LinGzArgs {
   const uint16_t* gY;
   const uint16_t* Z;  // with an activation

@@ -99,15 +99,12 @@ domino_status check_linear(int64_t m, int64_t n, int64_t k, int32_t act) {
   return DOMINO_OK;
 }
 
-// Workspace of the backward: the products' scratch (one at a time), gZ, and the bias gradient's partial sums.
+// Workspace of the backward: gZ, and the bias gradient's partial sums.
 struct LinBwdPlan {
-  size_t scratch, off_gz, off_part, total;
+  size_t off_gz, off_part, total;
 };
-LinBwdPlan linear_bwd_plan(int64_t m, int64_t n, int64_t k, int32_t act) {
+LinBwdPlan linear_bwd_plan(int64_t m, int64_t n, int32_t act) {
   LinBwdPlan p = {};
-  const int64_t gx = dm::lin_scratch_bytes(m, k, n), gw = dm::lin_scratch_bytes(n, k, m);
-  p.scratch = slice_up(size_t(gx > gw ? gx : gw));
-  p.off_gz = p.scratch;
   p.off_part = p.off_gz + (act == DOMINO_ACT_NONE ? 0 : slice_up(size_t(m) * n * 2));
   p.total = p.off_part + slice_up(size_t(dm::lin_gz_row_blocks(m, n)) * n * 4);
   if (m == 0) p.total = 0;
@@ -126,15 +123,25 @@ domino_status check_packed(int64_t tq, int64_t n, int32_t heads, int32_t kv_head
   return DOMINO_OK;
 }
 
-dm::LinArgs linear_args(int64_t m, int64_t n, int64_t k, int site) {
-  dm::LinArgs a = {};
-  a.M = int32_t(m);
-  a.N = int32_t(n);
-  a.m_tiles = int32_t((m + 255) / 256);
-  a.n_tiles = int32_t((n + 255) / 256);
-  a.k_blocks = int32_t((k + 63) / 64);
-  a.err_site = site << 4;
-  return a;
+// Arguments and operand maps of D (m x n) = A . B^T over k: A m x k and B n x k, each contiguous along the
+// reduction or (a_mn, b_mn) given as its transpose, with row strides ld_a, ld_b.
+domino_status linear_product(dm::LinMaps* maps, dm::LinArgs* a, const uint16_t* A, int64_t ld_a, bool a_mn,
+                             const uint16_t* B, int64_t ld_b, bool b_mn, int64_t m, int64_t n, int64_t k, int site) {
+  const dm::LinPlan p = dm::lin_plan(m, n, k);
+  *a = {};
+  a->M = int32_t(m);
+  a->N = int32_t(n);
+  a->m_tiles = int32_t((m + 255) / 256);
+  a->n_tiles = int32_t((n + p.width - 1) / p.width);
+  a->k_blocks = int32_t((k + 63) / 64);
+  a->err_site = site << 4;
+  a->width = p.width;
+  a->parts = p.parts;
+  a->units = p.units;
+  a->a_rows = a_mn || m >= 128 ? 128 : int32_t((m + 7) / 8 * 8);
+  DM_TRY(a_mn ? map2(&maps->a, 2, A, m, k, ld_a, 64, 64, 128) : map2(&maps->a, 2, A, k, m, ld_a, 64, uint32_t(a->a_rows), 128));
+  DM_TRY(b_mn ? map2(&maps->b, 2, B, n, k, ld_b, 64, 64, 128) : map2(&maps->b, 2, B, k, n, ld_b, 64, uint32_t(p.width / 2), 128));
+  return DOMINO_OK;
 }
 
 }  // namespace
@@ -212,14 +219,11 @@ domino_status domino_layernorm_bwd(domino_handle H, const uint16_t* gY, int64_t 
   });
 }
 
-domino_status domino_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act, int32_t pass,
-                                           size_t* bytes) {
+domino_status domino_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act, size_t* bytes) {
   return guarded([&]() -> domino_status {
     if (!bytes) return refuse(DOMINO_ERR_INVALID_ARG, "bytes is NULL");
     DM_TRY(check_linear(M, N, K, act));
-    if (pass != DOMINO_PASS_FWD && pass != DOMINO_PASS_BWD)
-      return refuse(DOMINO_ERR_INVALID_ARG, "pass must be DOMINO_PASS_FWD or DOMINO_PASS_BWD");
-    *bytes = pass == DOMINO_PASS_FWD ? size_t(dm::lin_scratch_bytes(M, N, K)) : linear_bwd_plan(M, N, K, act).total;
+    *bytes = linear_bwd_plan(M, N, act).total;
     return DOMINO_OK;
   });
 }
@@ -227,7 +231,7 @@ domino_status domino_linear_workspace_size(int64_t M, int64_t N, int64_t K, int3
 domino_status domino_linear_fwd(domino_handle H, const uint16_t* X, int64_t ld_x, const uint16_t* W,
                                 const uint16_t* bias, int32_t act, const uint16_t* R, int64_t ld_r, uint16_t* Y,
                                 int64_t ld_y, uint16_t* Z, int64_t ld_z, int64_t M, int64_t N, int64_t K,
-                                void* workspace, size_t workspace_bytes, void* stream) {
+                                void* stream) {
   return guarded([&]() -> domino_status {
     DM_TRY(check_linear(M, N, K, act));
     DM_TRY(check_ld(ld_x, K, "ld_x"));
@@ -241,24 +245,22 @@ domino_status domino_linear_fwd(domino_handle H, const uint16_t* X, int64_t ld_x
       DM_TRY(check_ptr(Y, "Y"));
       DM_TRY(check_ptr(R, "R", true));
       DM_TRY(check_ptr(Z, "Z", true));
-      DM_TRY(check_ws(workspace, workspace_bytes, size_t(dm::lin_scratch_bytes(M, N, K))));
     }
     DM_TRY(dm::check_handle(H));
     if (M == 0) return DOMINO_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     dm::LinMaps m = {};
-    DM_TRY(map2(&m.a, 2, X, K, M, ld_x, 64, 128, 128));
-    DM_TRY(map2(&m.b, 2, W, K, N, K, 64, 128, 128));
+    dm::LinArgs a;
+    DM_TRY(linear_product(&m, &a, X, ld_x, false, W, K, false, M, N, K, 0x20));
     DM_TRY(map2(&m.y, 2, Y, N, M, ld_y, 32, 32, 64));
     if (Z) DM_TRY(map2(&m.z, 2, Z, N, M, ld_z, 32, 32, 64));
-    dm::LinArgs a = linear_args(M, N, K, 0x20);
     a.act = act;
     a.save = Z != nullptr;
     a.bias = bias;
     a.R = R;
     a.ld_r = ld_r;
     return dm::launch_on(H, DOMINO_K_LINEAR_FWD, st, "linear layer launch",
-                         [&] { return dm::launch_linear(dm::LIN_FWD, m, a, workspace, st); });
+                         [&] { return dm::launch_linear(dm::LIN_FWD, m, a, st); });
   });
 }
 
@@ -279,7 +281,7 @@ domino_status domino_linear_bwd(domino_handle H, const uint16_t* gY, int64_t ld_
     DM_TRY(check_ptr(gW, "gW", true));
     DM_TRY(check_ptr(gW_main, "gW_main", true));
     DM_TRY(check_ptr(gbias, "gbias", true));
-    const LinBwdPlan P = linear_bwd_plan(M, N, K, act);
+    const LinBwdPlan P = linear_bwd_plan(M, N, act);
     if (M > 0) {
       DM_TRY(check_ptr(gY, "gY"));
       DM_TRY(check_ptr(gX, "gX", true));
@@ -311,38 +313,35 @@ domino_status domino_linear_bwd(domino_handle H, const uint16_t* gY, int64_t ld_
     const int64_t ld_gz = has_act ? N : ld_gy;
     if (gX) {
       dm::LinMaps m = {};
-      DM_TRY(map2(&m.a, 2, gZ, N, M, ld_gz, 64, 128, 128));
-      DM_TRY(map2(&m.b, 2, W, K, N, K, 64, 64, 128));
+      dm::LinArgs a;
+      DM_TRY(linear_product(&m, &a, gZ, ld_gz, false, W, K, true, M, K, N, 0x21));
       DM_TRY(map2(&m.y, 2, gX, K, M, ld_gx, 32, 32, 64));
-      const dm::LinArgs a = linear_args(M, K, N, 0x21);
       DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GX, st, "linear layer gX launch",
-                           [&] { return dm::launch_linear(dm::LIN_GX, m, a, ws, st); }));
+                           [&] { return dm::launch_linear(dm::LIN_GX, m, a, st); }));
     }
     if (want_gw) {
       dm::LinMaps m = {};
-      DM_TRY(map2(&m.a, 2, gZ, N, M, ld_gz, 64, 64, 128));
-      DM_TRY(map2(&m.b, 2, X, K, M, ld_x, 64, 64, 128));
+      dm::LinArgs a;
+      DM_TRY(linear_product(&m, &a, gZ, ld_gz, true, X, ld_x, true, N, K, M, 0x22));
       if (gW) {
         DM_TRY(map2(&m.y, 2, gW, K, N, K, 32, 32, 64));
-        const dm::LinArgs a = linear_args(N, K, M, 0x22);
         DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
-                             [&] { return dm::launch_linear(dm::LIN_GW, m, a, ws, st); }));
-      } else {
-        const dm::LinArgs l = linear_args(N, K, M, 0x22);
-        dm::GemmArgs a = {};
-        a.batches = 1;
-        a.m_tiles = l.m_tiles;
-        a.n_tiles = l.n_tiles;
-        a.k_blocks = l.k_blocks;
-        a.M = l.M;
-        a.N = l.N;
-        a.err_site = l.err_site;
-        a.alpha = a.out_scale = 1.0f;
-        a.out0 = gW_main;
-        a.ld0 = K;
+                             [&] { return dm::launch_linear(dm::LIN_GW, m, a, st); }));
+      } else {  // the MLP's weight-gradient product, tiles of 256 x 256
+        dm::GemmArgs g = {};
+        g.batches = 1;
+        g.m_tiles = a.m_tiles;
+        g.n_tiles = int32_t((K + 255) / 256);
+        g.k_blocks = a.k_blocks;
+        g.M = a.M;
+        g.N = a.N;
+        g.err_site = a.err_site;
+        g.alpha = g.out_scale = 1.0f;
+        g.out0 = gW_main;
+        g.ld0 = K;
         const dm::EpiMaps none = {};
         DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
-                             [&] { return dm::launch_gemm_bwd(dm::GV_WGRAD, m.a, m.b, none, a, st); }));
+                             [&] { return dm::launch_gemm_bwd(dm::GV_WGRAD, m.a, m.b, none, g, st); }));
       }
     }
     return DOMINO_OK;

@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
   __shared__ int bins[kBins];
   __shared__ unsigned long long s_total;
   __shared__ int s_max, s_slots, s_splits, s_entries;
+  pdl_launch();
+  pdl_wait();
   const int tid = threadIdx.x, span = 2 * a.tokens;
   if (tid == 0) {
     s_total = 0;
@@ -390,6 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  pdl_launch();
+  pdl_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -778,6 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Block (split, key/value head, tile): with m = max m_p and c_p = 2^(m_p - m) over the parts p in order,
 // O = sum c_p O_p / sum c_p l_p, lse = ln 2 (m + log2(sum c_p l_p)).
 __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a, const PackedWork w) {
+  pdl_launch();
+  pdl_wait();
   if (static_cast<int>(blockIdx.x) >= w.head->splits) return;
   const PackedSplit s = w.splits[blockIdx.x];
   const int hk = blockIdx.y, x = blockIdx.z;
@@ -837,8 +843,7 @@ int64_t packed_scratch_bytes(int64_t tq, int64_t n, int hq, int hkv, int64_t tk)
 }
 
 cudaError_t launch_packed_plan(const PackedArgs& a, void* ws, cudaStream_t st) {
-  packed_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, packed_work(a, ws));
-  return cudaGetLastError();
+  return launch_pdl(packed_plan_kernel, dim3(1), dim3(kPlanThreads), 0, 1, st, a, packed_work(a, ws));
 }
 
 cudaError_t launch_packed_attention(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
@@ -856,8 +861,7 @@ cudaError_t launch_packed_attention(const CUtensorMap& q, const CUtensorMap& k, 
   const PackedWork w = packed_work(a, ws);
   const int64_t most = int64_t(w.cap_entries) * a.hkv;
   const int grid = static_cast<int>(most < sms ? most : sms);
-  packed_attention_kernel<<<grid, kThreads, kSmem, st>>>(q, k, v, a, w);
-  return cudaGetLastError();
+  return launch_pdl(packed_attention_kernel, dim3(grid), dim3(kThreads), kSmem, 1, st, q, k, v, a, w);
 }
 
 bool packed_may_cut(const PackedArgs& a) {
@@ -866,8 +870,8 @@ bool packed_may_cut(const PackedArgs& a) {
 
 cudaError_t launch_packed_combine(const PackedArgs& a, void* ws, cudaStream_t st) {
   const PackedWork w = packed_work(a, ws);
-  packed_combine_kernel<<<dim3(static_cast<unsigned>(w.cap_splits), static_cast<unsigned>(a.hkv), 2), 256, 0, st>>>(a, w);
-  return cudaGetLastError();
+  return launch_pdl(packed_combine_kernel, dim3(static_cast<unsigned>(w.cap_splits), static_cast<unsigned>(a.hkv), 2), dim3(256), 0, 1,
+                    st, a, w);
 }
 
 cudaError_t take_packed_error(int* code) {

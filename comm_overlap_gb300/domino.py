@@ -79,8 +79,8 @@ _SIGS = {
     "domino_layernorm_bwd_workspace_size": [_I64, _I64, ctypes.POINTER(_N)],
     "domino_layernorm_bwd": [_P, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P, _S, _I64, _I64, _P, _N,
                              _P],
-    "domino_linear_workspace_size": [_I64, _I64, _I64, _S, _S, ctypes.POINTER(_N)],
-    "domino_linear_fwd": [_P, _P, _I64, _P, _P, _S, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P, _N, _P],
+    "domino_linear_bwd_workspace_size": [_I64, _I64, _I64, _S, ctypes.POINTER(_N)],
+    "domino_linear_fwd": [_P, _P, _I64, _P, _P, _S, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _P],
     "domino_linear_bwd": [_P, _P, _I64, _P, _I64, _P, _P, _I64, _S, _P, _I64, _P, _P, _P, _S, _I64, _I64, _I64, _P,
                           _N, _P],
     "domino_attn_packed_workspace_size": [_I64, _I64, _S, _S, _I64, ctypes.POINTER(_N)],
@@ -260,17 +260,15 @@ def domino_layernorm_bwd(handle, gY, ld_gy, X, ld_x, gamma, mean, rstd, gres, ld
                                       _stream(stream)))
 
 
-def domino_linear_workspace_size(M, N, K, act, pass_) -> int:
-    n = _N()
-    _check(lib().domino_linear_workspace_size(M, N, K, act, pass_, ctypes.byref(n)))
-    return n.value
-
-
-def domino_linear_fwd(handle, X, ld_x, W, bias, act, R, ld_r, Y, ld_y, Z, ld_z, M, N, K, workspace,
-                      workspace_bytes=None, stream=None) -> None:
+def domino_linear_fwd(handle, X, ld_x, W, bias, act, R, ld_r, Y, ld_y, Z, ld_z, M, N, K, stream=None) -> None:
     _check(lib().domino_linear_fwd(handle, _ptr(X), ld_x, _ptr(W), _ptr(bias), act, _ptr(R), ld_r, _ptr(Y), ld_y,
-                                   _ptr(Z), ld_z, M, N, K, _ptr(workspace), _nbytes(workspace, workspace_bytes),
-                                   _stream(stream)))
+                                   _ptr(Z), ld_z, M, N, K, _stream(stream)))
+
+
+def domino_linear_bwd_workspace_size(M, N, K, act) -> int:
+    n = _N()
+    _check(lib().domino_linear_bwd_workspace_size(M, N, K, act, ctypes.byref(n)))
+    return n.value
 
 
 def domino_linear_bwd(handle, gY, ld_gy, X, ld_x, W, Z, ld_z, act, gX, ld_gx, gW, gW_main, gbias, accumulate, M, N, K,

@@ -217,10 +217,8 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     weight, bias = _vec(weight), _vec(bias)
     y = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
     z = torch.empty_like(y) if save else None
-    size = dm.domino_linear_workspace_size(m, n, k, act, dm.PASS_FWD)
-    ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
     with _call(x) as handle:
-        dm.domino_linear_fwd(handle, x, ld_x, weight, bias, act, residual, ld_r, y, n, z, n, m, n, k, ws, size)
+        dm.domino_linear_fwd(handle, x, ld_x, weight, bias, act, residual, ld_r, y, n, z, n, m, n, k)
     return y, z
 
 
@@ -254,7 +252,7 @@ def linear_bwd(gy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, z: torch
     gb = bias_main_grad
     if gb is None and bias_grad:
         gb = torch.empty(n, dtype=torch.float32, device=x.device)
-    size = dm.domino_linear_workspace_size(m, n, k, act, dm.PASS_BWD)
+    size = dm.domino_linear_bwd_workspace_size(m, n, k, act)
     ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
     with _call(x) as handle:
         dm.domino_linear_bwd(handle, gy, ld_gy, x, ld_x, weight, z, ld_z, act, gx, k, gw,

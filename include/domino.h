@@ -303,15 +303,11 @@ DOMINO_API domino_status domino_layernorm_bwd(domino_handle handle, const uint16
  *   Z (nullable): M x N (row stride ld_z), the pre-activation that domino_linear_bwd needs.
  * bf16 operands, fp32 accumulation; bias, activation and residual are applied in fp32 and Y and Z are
  * each rounded once.  act: NONE, RELU or GELU.  N and K are multiples of 8, at most 2^20; M >= 0.
- * The order of every sum depends on the sizes alone: equal inputs give equal bits.  Workspace:
- * domino_linear_workspace_size(..., DOMINO_PASS_FWD); its contents need no initialisation. */
-DOMINO_API domino_status domino_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act, int32_t pass,
-                                                      size_t* bytes);
+ * The order of every sum depends on the sizes alone: equal inputs give equal bits. */
 DOMINO_API domino_status domino_linear_fwd(domino_handle handle, const uint16_t* X, int64_t ld_x, const uint16_t* W,
                                            const uint16_t* bias, int32_t act, const uint16_t* R, int64_t ld_r,
                                            uint16_t* Y, int64_t ld_y, uint16_t* Z, int64_t ld_z, int64_t M,
-                                           int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
-                                           void* stream);
+                                           int64_t N, int64_t K, void* stream);
 
 /* Backward of domino_linear_fwd (the residual's gradient is gY itself):
  *   gZ = gY act'(Z)                 (fp32; rounded to bf16 where it enters the products)
@@ -321,7 +317,9 @@ DOMINO_API domino_status domino_linear_fwd(domino_handle handle, const uint16_t*
  *   gbias = sum over rows of gZ     (N fp32, unrounded gZ; nullable), added to the buffer with
  *                                   accumulate = 1.
  * Z is what the forward kept (unused with act = NONE); W is needed for gX, X for gW.  Workspace:
- * domino_linear_workspace_size(..., DOMINO_PASS_BWD). */
+ * domino_linear_bwd_workspace_size() bytes. */
+DOMINO_API domino_status domino_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act,
+                                                          size_t* bytes);
 DOMINO_API domino_status domino_linear_bwd(domino_handle handle, const uint16_t* gY, int64_t ld_gy,
                                            const uint16_t* X, int64_t ld_x, const uint16_t* W, const uint16_t* Z,
                                            int64_t ld_z, int32_t act, uint16_t* gX, int64_t ld_gx, uint16_t* gW,

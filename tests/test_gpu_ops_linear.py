@@ -53,8 +53,8 @@ def check_fwd(x, w, b, act, r, y, z):
     close(y, yd, sy, what="y")
 
 
-# one step of the reduction and fewer; tiles' edges in every direction; one row to several tiles; a last round that is
-# cut along the reduction (more than 8 steps of 64) alone, and after whole rounds
+# one step of the reduction and fewer; tiles' edges in every direction and width; one row to several rounds of tiles; few
+# tiles, whose reduction is cut over clusters of two and four pairs
 SIZES = [(1, 8, 8), (2, 40, 56), (31, 248, 72), (33, 264, 512), (127, 256, 520), (129, 512, 576), (255, 8, 1096),
          (257, 2560, 264), (1, 4096, 4096), (5, 16384, 1024), (300, 768, 8192), (777, 2560, 2560), (5000, 2056, 264),
          (5000, 2056, 1096), (4864, 4096, 128)]
@@ -157,14 +157,14 @@ def test_strides_and_outputs_left_alone(ops):
     big = torch.full((m + 2, n + 16), 7.0, dtype=torch.bfloat16, device="cuda")
     out = big[1:-1, 8:8 + n]
     with ops._call(x) as h:
-        dm.domino_linear_fwd(h, x, xw.shape[1], w, None, dm.ACT_GELU, r, rw.shape[1], out, big.shape[1], None, 0, m, n, k, None, 0)
+        dm.domino_linear_fwd(h, x, xw.shape[1], w, None, dm.ACT_GELU, r, rw.shape[1], out, big.shape[1], None, 0, m, n, k)
     assert torch.equal(out, y)
     big[1:-1, 8:8 + n] = 7.0
     assert (big == 7.0).all()
     # the residual's buffer as the output
     r2 = r.clone()
     with ops._call(x) as h:
-        dm.domino_linear_fwd(h, x, xw.shape[1], w, None, dm.ACT_GELU, r2, n, r2, n, None, 0, m, n, k, None, 0)
+        dm.domino_linear_fwd(h, x, xw.shape[1], w, None, dm.ACT_GELU, r2, n, r2, n, None, 0, m, n, k)
     assert torch.equal(r2, y)
     # an output gradient broadcast over its rows
     e = r[:1].expand(m, n)

@@ -78,7 +78,7 @@ def test_functions_refuse_what_they_cannot_take():
 
 def lin_fwd(**kw):
     a = dict(handle=None, X=P, ld_x=64, W=P, bias=P, act=dm.ACT_GELU, R=P, ld_r=128, Y=P, ld_y=128, Z=P, ld_z=128, M=4, N=128,
-             K=64, workspace=P, workspace_bytes=1 << 30, stream=0)
+             K=64, stream=0)
     dm.domino_linear_fwd(**{**a, **kw})
 
 
@@ -95,9 +95,7 @@ def lin_bwd(**kw):
     (dict(M=(1 << 31) - 257, N=1 << 16, ld_y=1 << 16, ld_r=1 << 16, ld_z=1 << 16), UNSUPPORTED), (dict(ld_x=56), INVALID),
     (dict(ld_x=68), ALIGNMENT), (dict(ld_y=120), INVALID), (dict(ld_r=64), INVALID), (dict(ld_z=130), ALIGNMENT),
     (dict(X=None), INVALID), (dict(W=None), INVALID), (dict(Y=None), INVALID), (dict(W=P + 8), ALIGNMENT), (dict(bias=P + 2), ALIGNMENT),
-    (dict(R=P + 2), ALIGNMENT), (dict(Z=P + 4), ALIGNMENT), (dict(K=4096, ld_x=4096, workspace=None), WORKSPACE),
-    (dict(K=4096, ld_x=4096, workspace=P + 128), WORKSPACE), (dict(K=4096, ld_x=4096, workspace_bytes=1 << 20), WORKSPACE),
-    (dict(), INVALID), (dict(bias=None, R=None, Z=None, workspace=None), INVALID)])
+    (dict(R=P + 2), ALIGNMENT), (dict(Z=P + 4), ALIGNMENT), (dict(), INVALID), (dict(bias=None, R=None, Z=None), INVALID)])
 def test_linear_forward(kw, code):
     assert status(lin_fwd, **kw) == code
 
@@ -113,13 +111,11 @@ def test_linear_backward(kw, code):
 
 
 def test_linear_workspace_size():
-    size = dm.domino_linear_workspace_size
-    assert size(4, 128, 512, dm.ACT_NONE, dm.PASS_FWD) == 0  # too short a reduction to cut
-    assert size(0, 128, 4096, dm.ACT_NONE, dm.PASS_FWD) == 0 and size(0, 128, 4096, dm.ACT_GELU, dm.PASS_BWD) == 0
-    assert size(4, 128, 4096, dm.ACT_NONE, dm.PASS_FWD) == 76 * (256 * 256 * 4 + 64)
-    assert size(4, 128, 64, dm.ACT_GELU, dm.PASS_BWD) == 1024 + 1024  # gZ, one row of partial sums
-    assert status(size, M=4, N=128, K=64, act=dm.ACT_NONE, pass_=dm.PASS_STACK) == INVALID
-    assert status(size, M=4, N=128, K=64, act=dm.ACT_SWIGLU, pass_=dm.PASS_FWD) == UNSUPPORTED
+    size = dm.domino_linear_bwd_workspace_size
+    assert size(0, 128, 4096, dm.ACT_GELU) == 0
+    assert size(4, 128, 64, dm.ACT_GELU) == 1024 + 1024  # gZ, one row of partial sums
+    assert size(4, 128, 64, dm.ACT_NONE) == 1024
+    assert status(size, M=4, N=128, K=64, act=dm.ACT_SWIGLU) == UNSUPPORTED
 
 
 def test_linear_functions_refuse_what_they_cannot_take():
