@@ -29,6 +29,17 @@ domino_status launch_on(domino_handle H, int kind, cudaStream_t st, const char* 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 template <class... Params, class... Args>
 cudaError_t launch_pdl(void (*fn)(Params...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
                        Args&&... args) {

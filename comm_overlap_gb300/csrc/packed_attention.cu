@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1 || warp == kIssuer1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer of tile x.  In items where both tiles work the issuers alternate: each
+    {
+      // ---------------- MMA issuer of tile x (the warp walks the work, one elected lane issues).  In items where both tiles work the issuers alternate: each
       // first Q K^T, then per block P V and the next Q K^T; a tile that has no work left in a block passes
       // its turn on.  Elsewhere the one with work needs no turn.
       const uint32_t x = warp == 1 ? 0u : 1u;
@@ -470,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dQ = sdesc_sw128(sQ + x * kTile, 16, 1024), dK0 = sdesc_sw128(sK, 16, 1024),
                      dV0 = sdesc_sw128(sV, kHalf, 1024);
       const uint32_t tS = tmem_base + 128u * x, tO = tmem_base + 256u + 128u * x;
+      const bool one = elect_one();
       auto qk = [=](uint32_t kb) {
         const uint64_t dk = dK0 + ((static_cast<uint64_t>(kb) * kTile) >> 4);
 #pragma unroll
@@ -506,15 +507,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          qk(gb & 1u);
-          if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
-          umma_commit(bar(B_S_FULL + x));
-          umma_commit(bar(B_K_EMPTY + 2 * x + (gb & 1u)));
-          if (b0 + 1 == e) umma_commit(bar(B_Q_EMPTY + x));
+          if (one) {
+            qk(gb & 1u);
+            if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
+            umma_commit(bar(B_S_FULL + x));
+            umma_commit(bar(B_K_EMPTY + 2 * x + (gb & 1u)));
+            if (b0 + 1 == e) umma_commit(bar(B_Q_EMPTY + x));
+          }
           for (int j = b0; ok && j < last; ++j) {
             if (j >= e) {  // the other tile alone
               ok = take_turn(two);
-              if (ok && two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
+              if (ok && two && one) mbar_arrive(bar(B_TURN + (x ^ 1u)));
               continue;
             }
             const uint32_t r = gb + static_cast<uint32_t>(j - b0), r1 = r + 1u;
@@ -529,12 +532,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
+            ++np;
+            if (!one) continue;
             pv(r & 1u, j == b0);
             if (j + 1 < e) qk(r1 & 1u);  // overwrites P only after the product above (issue order)
             if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
             umma_commit(bar(B_PV_DONE + x));
             umma_commit(bar(B_V_EMPTY + 2 * x + (r & 1u)));
-            ++np;
             if (j + 1 < e) {
               umma_commit(bar(B_S_FULL + x));
               umma_commit(bar(B_K_EMPTY + 2 * x + (r1 & 1u)));
@@ -546,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         shared_before |= two;
         gb += static_cast<uint32_t>(last - b0);
       }
-      umma_commit(bar(B_DRAIN + x));
+      if (one) umma_commit(bar(B_DRAIN + x));
       const uint64_t t0 = global_timer_ns();
       while (!mbar_try_wait(bar(B_DRAIN + x), 0) && global_timer_ns() - t0 <= kDrainNs) {
       }
