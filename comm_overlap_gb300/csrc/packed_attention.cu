@@ -38,8 +38,11 @@ constexpr int kBlk = 128;                     // rows of a tile, keys of a block
 constexpr uint32_t kTile = kBlk * kD * 2;     // 32 KiB: one Q, K or V tile
 constexpr uint32_t kHalf = kTile / 2;         // one 64-column (128-byte) swizzle panel
 constexpr uint32_t kOBox = 32 * 64 * 2;       // 4 KiB: one warp's 32 rows x 64 columns of O
-constexpr int kThreads = 352;
-constexpr int kIssuer1 = 10;                  // issues tile 1's products (tile 0's: warp 1)
+constexpr int kThreads = 384;                 // warps: 0 producer, 1 and 2 issuers, 3 idle, 4-7 and 8-11 softmax
+// Registers a thread after the split: launched with 168, the first warpgroup gives up 72 and the softmax
+// warpgroups take 32 each (96 x 128 + 200 x 256 <= 168 x 384).
+constexpr int kRegsRoles = 96, kRegsSoftmax = 200;
+static_assert(kRegsRoles * 128 + kRegsSoftmax * 256 <= 168 * kThreads, "more registers than the block was launched with");
 constexpr int kSmem = 1024 + 1024 + 6 * static_cast<int>(kTile) + 8 * static_cast<int>(kOBox);
 static_assert(kSmem <= 232448, "shared memory beyond the per-CTA limit");
 constexpr uint32_t kTmemCols = 512;
@@ -295,10 +298,34 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// the largest of three, NaN if one is
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// 2^y of two finite values on the FMA units: y = i + r, |r| <= 1/2, i by adding 1.5 x 2^23, 2^r by a polynomial of
+// degree 5 (least maximal relative error over [-1/2, 1/2], fitted by reweighted least squares; 2.1e-7 with
+// its fp32 evaluation), i added to the exponent.  Below 2^-126 it stays there.
+__device__ __forceinline__ uint64_t exp2_fma(uint64_t y) {
+  constexpr float kShift = 12582912.0f;
+  float a, b;
+  f2_split(y, a, b);
+  y = f2(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+  const uint64_t t = add_f2(y, f2(kShift, kShift));
+  const uint64_t r = fma_f2(add_f2(t, f2(-kShift, -kShift)), f2(-1.0f, -1.0f), y);
+  uint64_t p = f2(0x1.5c08e2p-10f, 0x1.5c08e2p-10f);
+  p = fma_f2(p, r, f2(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
+  p = fma_f2(p, r, f2(0x1.c6b6e6p-5f, 0x1.c6b6e6p-5f));
+  p = fma_f2(p, r, f2(0x1.ebf918p-3f, 0x1.ebf918p-3f));
+  p = fma_f2(p, r, f2(0x1.62e428p-1f, 0x1.62e428p-1f));
+  p = fma_f2(p, r, f2(0x1.000002p+0f, 0x1.000002p+0f));
+  float t0, t1, p0, p1;
+  f2_split(t, t0, t1);
+  f2_split(p, p0, p1);
+  return f2(__uint_as_float(__float_as_uint(t0) * 0x800000u + __float_as_uint(p0)),
+            __uint_as_float(__float_as_uint(t1) * 0x800000u + __float_as_uint(p1)));
 }
 
 // As mbar_wait (bounded), but polling: the thread is never suspended.
@@ -400,6 +427,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int total = w.head->entries * a.hkv;
 
+  if (warp < 4)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer
@@ -459,12 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 1 || warp == kIssuer1) {
+  } else if (warp < 3) {
     {
       // ---------------- MMA issuer of tile x (the warp walks the work, one elected lane issues).  In items where both tiles work the issuers alternate: each
       // first Q K^T, then per block P V and the next Q K^T; a tile that has no work left in a block passes
       // its turn on.  Elsewhere the one with work needs no turn.
-      const uint32_t x = warp == 1 ? 0u : 1u;
+      const uint32_t x = static_cast<uint32_t>(warp) - 1u;
       constexpr uint32_t kIdQK = idesc_bf16_f32(kBlk, kBlk, false, false);
       constexpr uint32_t kIdPV = idesc_bf16_f32(kBlk, kD, false, true);
       const uint64_t dQ = sdesc_sw128(sQ + x * kTile, 16, 1024), dK0 = sdesc_sw128(sK, 16, 1024),
@@ -556,12 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ---------------- softmax warps of tile x, one row a thread
-    const int x = (warp - 2) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int x = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lq = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem_base + lq + 128u * x, tO = tmem_base + lq + 256u + 128u * x;
-    const uint32_t obox = sO + static_cast<uint32_t>(warp - 2) * kOBox;
+    const uint32_t obox = sO + static_cast<uint32_t>(warp - 4) * kOBox;
     const int rows = a.tokens * a.group;
     // row / group for rows below 128 (exact: the rounding of the factor adds less than 1 / group)
     const uint32_t inv_group = (65536u + static_cast<uint32_t>(a.group) - 1u) / static_cast<uint32_t>(a.group);
@@ -587,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32u * i, sr[i]);
         tmem_ld_wait();
         const int rel = lim - j * kBlk;  // columns above it are masked
-        if (__any_sync(0xFFFFFFFFu, rel < kBlk - 1)) {
+        const bool masked = __any_sync(0xFFFFFFFFu, rel < kBlk - 1);
+        if (masked) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c > rel) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
@@ -599,14 +632,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 128; c += 2)
           m8[(c >> 1) & 7] = max3(m8[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
                                   __uint_as_float(sr[c >> 5][(c & 31) + 1]));
-#pragma unroll
-        for (int i = 4; i > 0; i >>= 1)
-#pragma unroll
-          for (int n = 0; n < i; ++n) m8[n] = fmaxf(m8[n], m8[n + i]);
+        const float top = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), max3(m8[6], m8[7], m8[7]));
         // running maximum in the log2 domain, raised when some row of the warp would pass it by more than
         // 8 (p <= 2^8 otherwise); O and the sum are then rescaled.  A row that has seen no key keeps
         // -inf, and zero stands in for it so that its p are 0 and not NaN.
-        const float cand = fmaxf(m_run, m8[0] * a.scale_log2);
+        const float cand = fmaxf(m_run, top * a.scale_log2);
         const bool raise = __any_sync(0xFFFFFFFFu, cand > m_run + 8.0f) || j == b0;
         const float mx = raise ? cand : m_run;
         const float base = mx == -INFINITY ? 0.0f : mx;
@@ -616,16 +646,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) l4[i] = f2(0.0f, 0.0f);
         const uint64_t sc2 = f2(a.scale_log2, a.scale_log2), nmx2 = f2(-base, -base);
         uint32_t pk[2][32];
+        // p = 2^(score - maximum) in pairs; `some`: one pair in four on the FMA units, which relieves the
+        // exponential units (finite, unmasked scores only)
+        auto exponentials = [&](auto some) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const int i = 2 * c;
-          float y0, y1;
-          f2_split(fma_f2(f2(__uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1])), sc2, nmx2),
-                   y0, y1);
-          const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
-          l4[c & 3] = add_f2(l4[c & 3], f2(p0, p1));
-          pk[c >> 5][c & 31] = pack_bf16x2(p0, p1);
-        }
+          for (int c = 0; c < 64; ++c) {
+            const int i = 2 * c;
+            const uint64_t y = fma_f2(f2(__uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1])), sc2, nmx2);
+            float p0, p1;
+            if (decltype(some)::value && (c & 3) == 3) {
+              f2_split(exp2_fma(y), p0, p1);
+            } else {
+              f2_split(y, p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+            }
+            l4[c & 3] = add_f2(l4[c & 3], f2(p0, p1));
+            pk[c >> 5][c & 31] = pack_bf16x2(p0, p1);
+          }
+        };
+        if (masked || __any_sync(0xFFFFFFFFu, !(fabsf(top) < INFINITY)))
+          exponentials(std::false_type{});
+        else
+          exponentials(std::true_type{});
         float l8[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) f2_split(l4[i], l8[2 * i], l8[2 * i + 1]);
