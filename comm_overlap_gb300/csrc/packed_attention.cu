@@ -39,9 +39,10 @@ constexpr uint32_t kTile = kBlk * kD * 2;     // 32 KiB: one Q, K or V tile
 constexpr uint32_t kHalf = kTile / 2;         // one 64-column (128-byte) swizzle panel
 constexpr uint32_t kOBox = 32 * 64 * 2;       // 4 KiB: one warp's 32 rows x 64 columns of O
 constexpr int kThreads = 384;                 // warps: 0 producer, 1 and 2 issuers, 3 idle, 4-7 and 8-11 softmax
-// Registers a thread after the split: launched with 168, the first warpgroup gives up 72 and the softmax
-// warpgroups take 32 each (96 x 128 + 200 x 256 <= 168 x 384).
-constexpr int kRegsRoles = 96, kRegsSoftmax = 200;
+// Registers a thread after the split: launched with 168, the first warpgroup gives up 104 and the softmax
+// warpgroups take 48 each (64 x 128 + 216 x 256 <= 168 x 384): a row's 128 scores and 64 packed p stay in
+// registers (16384-token prompt: 2420 us with 168 for all and a softmax that spills, 1510 us so).
+constexpr int kRegsRoles = 64, kRegsSoftmax = 216;
 static_assert(kRegsRoles * 128 + kRegsSoftmax * 256 <= 168 * kThreads, "more registers than the block was launched with");
 constexpr int kSmem = 1024 + 1024 + 6 * static_cast<int>(kTile) + 8 * static_cast<int>(kOBox);
 static_assert(kSmem <= 232448, "shared memory beyond the per-CTA limit");
@@ -298,34 +299,11 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// the largest of three, NaN if one is
+// the largest of three (a NaN score makes its own p NaN and need not show in the maximum)
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// 2^y of two finite values on the FMA units: y = i + r, |r| <= 1/2, i by adding 1.5 x 2^23, 2^r by a polynomial of
-// degree 5 (least maximal relative error over [-1/2, 1/2], fitted by reweighted least squares; 2.1e-7 with
-// its fp32 evaluation), i added to the exponent.  Below 2^-126 it stays there.
-__device__ __forceinline__ uint64_t exp2_fma(uint64_t y) {
-  constexpr float kShift = 12582912.0f;
-  float a, b;
-  f2_split(y, a, b);
-  y = f2(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
-  const uint64_t t = add_f2(y, f2(kShift, kShift));
-  const uint64_t r = fma_f2(add_f2(t, f2(-kShift, -kShift)), f2(-1.0f, -1.0f), y);
-  uint64_t p = f2(0x1.5c08e2p-10f, 0x1.5c08e2p-10f);
-  p = fma_f2(p, r, f2(0x1.3d0c52p-7f, 0x1.3d0c52p-7f));
-  p = fma_f2(p, r, f2(0x1.c6b6e6p-5f, 0x1.c6b6e6p-5f));
-  p = fma_f2(p, r, f2(0x1.ebf918p-3f, 0x1.ebf918p-3f));
-  p = fma_f2(p, r, f2(0x1.62e428p-1f, 0x1.62e428p-1f));
-  p = fma_f2(p, r, f2(0x1.000002p+0f, 0x1.000002p+0f));
-  float t0, t1, p0, p1;
-  f2_split(t, t0, t1);
-  f2_split(p, p0, p1);
-  return f2(__uint_as_float(__float_as_uint(t0) * 0x800000u + __float_as_uint(p0)),
-            __uint_as_float(__float_as_uint(t1) * 0x800000u + __float_as_uint(p1)));
 }
 
 // As mbar_wait (bounded), but polling: the thread is never suspended.
@@ -619,8 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32u * i, sr[i]);
         tmem_ld_wait();
         const int rel = lim - j * kBlk;  // columns above it are masked
-        const bool masked = __any_sync(0xFFFFFFFFu, rel < kBlk - 1);
-        if (masked) {
+        if (__any_sync(0xFFFFFFFFu, rel < kBlk - 1)) {
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c > rel) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
@@ -646,29 +623,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) l4[i] = f2(0.0f, 0.0f);
         const uint64_t sc2 = f2(a.scale_log2, a.scale_log2), nmx2 = f2(-base, -base);
         uint32_t pk[2][32];
-        // p = 2^(score - maximum) in pairs; `some`: one pair in four on the FMA units, which relieves the
-        // exponential units (finite, unmasked scores only)
-        auto exponentials = [&](auto some) {
+        // p = 2^(score - maximum), two columns at a time
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const int i = 2 * c;
-            const uint64_t y = fma_f2(f2(__uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1])), sc2, nmx2);
-            float p0, p1;
-            if (decltype(some)::value && (c & 3) == 3) {
-              f2_split(exp2_fma(y), p0, p1);
-            } else {
-              f2_split(y, p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-            }
-            l4[c & 3] = add_f2(l4[c & 3], f2(p0, p1));
-            pk[c >> 5][c & 31] = pack_bf16x2(p0, p1);
-          }
-        };
-        if (masked || __any_sync(0xFFFFFFFFu, !(fabsf(top) < INFINITY)))
-          exponentials(std::false_type{});
-        else
-          exponentials(std::true_type{});
+        for (int c = 0; c < 64; ++c) {
+          const int i = 2 * c;
+          float p0, p1;
+          f2_split(fma_f2(f2(__uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1])), sc2, nmx2), p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          l4[c & 3] = add_f2(l4[c & 3], f2(p0, p1));
+          pk[c >> 5][c & 31] = pack_bf16x2(p0, p1);
+        }
         float l8[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) f2_split(l4[i], l8[2 * i], l8[2 * i + 1]);
