@@ -48,7 +48,7 @@ constexpr int kSmem = 1024 + 1024 + 6 * static_cast<int>(kTile) + 8 * static_cas
 static_assert(kSmem <= 232448, "shared memory beyond the per-CTA limit");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kDrainNs = 200000000ull;
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;  // as many as the sort has bins
 
 enum : int {
   B_Q_FULL = 0, B_Q_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = 6, B_V_FULL = 10, B_V_EMPTY = 12, B_S_FULL = 16,
@@ -89,7 +89,7 @@ __host__ inline PackedLayout packed_layout(int64_t tq, int64_t n, int tokens, in
   l.cap_slots = cut ? 8 * kSms : 0;
   l.cap_entries = static_cast<int>(pairs + (cut ? 4 * kSms / hkv + 1 : 0));
   l.prefix = sizeof(PackedHeader);
-  l.entries = up(l.prefix + (n + 1) * 4, 256);
+  l.entries = up(l.prefix + (n > kPlanThreads ? n * 4 : 0), 256);
   l.splits = up(l.entries + int64_t(l.cap_entries) * sizeof(PackedEntry), 256);
   l.o = up(l.splits + int64_t(l.cap_splits) * sizeof(PackedSplit), 1024);
   l.ml = l.o + int64_t(l.cap_slots) * kBlk * kD * 4;
@@ -153,54 +153,74 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {  
   return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
 }
 
+// A pair of tiles: its sequence's lengths, its first token, the key blocks it sees.
+struct PackedPair {
+  int q0, qlen, k0, klen, tok0, e;
+};
+
+// The kernel is a chain of short dependent steps, so each thread keeps its first pair in registers, the totals are
+// added by warp before they meet in shared memory, and the sequences' offsets are searched there when they
+// fit (9 - 17 us before, with a pair's lengths looked up for each step and one atomic a pair).
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedArgs a, const PackedWork w) {
   constexpr int kBins = 1024;
   __shared__ int warp_sums[32];
   __shared__ int bins[kBins];
+  __shared__ int near_prefix[kPlanThreads];
   __shared__ unsigned long long s_total;
-  __shared__ int s_max, s_slots, s_splits, s_entries;
-  pdl_launch();
-  pdl_wait();
+  __shared__ int s_max, s_slots, s_splits, s_bad;
   const int tid = threadIdx.x, span = 2 * a.tokens;
   if (tid == 0) {
     s_total = 0;
-    s_max = s_slots = s_splits = s_entries = 0;
+    s_max = s_slots = s_splits = s_bad = 0;
   }
   for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
+  pdl_launch();
+  pdl_wait();
   // pairs of tiles before each sequence
+  const bool near = a.n <= kPlanThreads;
   int pairs = 0;
   for (int base = 0; base < a.n; base += kPlanThreads) {
     const int s = base + tid;
     int q0, qlen = 0, k0, klen;
     if (s < a.n) seq_lengths(a, s, q0, qlen, k0, klen);
     int total;
-    const int before = block_scan((qlen + span - 1) / span, warp_sums, total);
-    if (s < a.n) w.prefix[s] = pairs + before;
+    const int before = pairs + block_scan((qlen + span - 1) / span, warp_sums, total);
+    if (s < a.n) (near ? near_prefix : w.prefix)[s] = before;
     pairs += total;
   }
-  if (tid == 0) w.prefix[a.n] = pairs;
   __syncthreads();
-  // pair i: its sequence (the last one that begins at or before i and has pairs) and its blocks
-  auto pair_of = [&](int i, int& q0, int& qlen, int& k0, int& klen, int& tok0) {
+  const int* prefix = near ? near_prefix : w.prefix;
+  // pair i belongs to the last sequence that begins at or before it
+  auto pair_of = [&](int i) {
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (w.prefix[mid] <= i) lo = mid; else hi = mid - 1;
+      if (prefix[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    seq_lengths(a, lo, q0, qlen, k0, klen);
-    tok0 = (i - w.prefix[lo]) * span;
-    return seen_blocks(qlen, klen, tok0 + span);
+    PackedPair p;
+    seq_lengths(a, lo, p.q0, p.qlen, p.k0, p.klen);
+    p.tok0 = (i - prefix[lo]) * span;
+    p.e = seen_blocks(p.qlen, p.klen, p.tok0 + span);
+    return p;
   };
-  unsigned long long mine = 0;
-  int most = 0;
-  for (int i = tid; i < pairs; i += kPlanThreads) {
-    int q0, qlen, k0, klen, tok0;
-    const int e = pair_of(i, q0, qlen, k0, klen, tok0);
+  PackedPair first = {};
+  if (tid < pairs) first = pair_of(tid);
+  unsigned long long mine = static_cast<unsigned long long>(first.e);
+  int most = first.e;
+  for (int i = tid + kPlanThreads; i < pairs; i += kPlanThreads) {
+    const int e = pair_of(i).e;
     mine += static_cast<unsigned long long>(e);
     most = max(most, e);
   }
-  if (mine) atomicAdd(&s_total, mine);
-  if (most) atomicMax(&s_max, most);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  }
+  if ((tid & 31) == 0 && most > 0) {
+    atomicAdd(&s_total, mine);
+    atomicMax(&s_max, most);
+  }
   __syncthreads();
   // even share of the blocks, twice per SM; parts of at least kPackedMinPart blocks
   const unsigned long long total = s_total * static_cast<unsigned long long>(a.hkv);
@@ -209,34 +229,37 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
   if (share < kPackedMinPart) share = kPackedMinPart;
   if (w.cap_slots == 0) share = 0x7FFFFFFF;
   auto parts_of = [&](int e, int& len) {
-    const int parts = e > share ? (e + share - 1) / share : 1;
-    len = parts > 1 ? (e + parts - 1) / parts : e;
-    return parts > 1 ? (e + len - 1) / len : 1;
+    len = e;
+    if (e <= share) return 1;
+    const int parts = (e + share - 1) / share;
+    len = (e + parts - 1) / parts;
+    return (e + len - 1) / len;
   };
   int shift = 0;
   while ((min(s_max, share) >> shift) >= kBins) ++shift;
   // longest first: counting sort by blocks (order within a bin is of no consequence)
   for (int i = tid; i < pairs; i += kPlanThreads) {
-    int q0, qlen, k0, klen, tok0, len;
-    const int e = pair_of(i, q0, qlen, k0, klen, tok0), parts = parts_of(e, len);
+    const int e = i == tid ? first.e : pair_of(i).e;
+    int len;
+    const int parts = parts_of(e, len);
     if (parts > 1) atomicAdd(&bins[kBins - 1 - (len >> shift)], parts - 1);
     atomicAdd(&bins[kBins - 1 - ((e - (parts - 1) * len) >> shift)], 1);
   }
   __syncthreads();
   int count;
-  const int v = tid < kBins ? bins[tid] : 0;
-  const int start = block_scan(v, warp_sums, count);
-  if (tid < kBins) bins[tid] = start;
+  const int start = block_scan(bins[tid], warp_sums, count);
+  bins[tid] = start;
   __syncthreads();
   for (int i = tid; i < pairs; i += kPlanThreads) {
-    int q0, qlen, k0, klen, tok0, len;
-    const int e = pair_of(i, q0, qlen, k0, klen, tok0), parts = parts_of(e, len);
+    const PackedPair p = i == tid ? first : pair_of(i);
+    int len;
+    const int parts = parts_of(p.e, len);
     PackedEntry en;
-    en.q_row = q0 + tok0;
-    en.qn = qlen - tok0;
-    en.k_row = k0;
-    en.klen = klen;
-    en.pos0 = klen - qlen + tok0;
+    en.q_row = p.q0 + p.tok0;
+    en.qn = p.qlen - p.tok0;
+    en.k_row = p.k0;
+    en.klen = p.klen;
+    en.pos0 = p.klen - p.qlen + p.tok0;
     int slot = -1;
     if (parts > 1) {
       slot = atomicAdd(&s_slots, parts * 2 * a.hkv);
@@ -249,28 +272,28 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
         ps.len = len;
         ps.slot = slot;
         w.splits[sp] = ps;
-      } else {  // beyond the bounds above: only overlapping (refused) lengths get here
-        atomicCAS(&g_packed_err, 0, kPackedBadLengths);
+      } else {
+        s_bad = 1;
         continue;
       }
     }
-    for (int p = 0; p < parts; ++p) {
-      en.b0 = p * len;
-      en.b1 = min(e, en.b0 + len);
-      en.slot = parts > 1 ? slot + p * 2 * a.hkv : -1;
+    for (int k = 0; k < parts; ++k) {
+      en.b0 = k * len;
+      en.b1 = min(p.e, en.b0 + len);
+      en.slot = parts > 1 ? slot + k * 2 * a.hkv : -1;
       const int at = atomicAdd(&bins[kBins - 1 - ((en.b1 - en.b0) >> shift)], 1);
-      if (at < w.cap_entries) {
+      if (at < w.cap_entries)
         w.entries[at] = en;
-        atomicAdd(&s_entries, 1);
-      } else {
-        atomicCAS(&g_packed_err, 0, kPackedBadLengths);
-      }
+      else
+        s_bad = 1;
     }
   }
   __syncthreads();
   if (tid == 0) {
-    w.head->entries = count <= w.cap_entries && s_entries == count ? count : 0;
-    w.head->splits = w.head->entries ? min(s_splits, w.cap_splits) : 0;
+    // beyond the bounds of the workspace only with overlapping sequences, which are refused
+    if (s_bad) atomicCAS(&g_packed_err, 0, kPackedBadLengths);
+    w.head->entries = s_bad ? 0 : count;
+    w.head->splits = s_bad ? 0 : s_splits;
   }
 }
 
