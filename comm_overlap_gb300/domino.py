@@ -118,20 +118,22 @@ def lib() -> ctypes.CDLL:
 
 
 def _check(status: int):
-    if status != DOMINO_OK:
+    if status:
         raise DominoError(status, lib().domino_last_error().decode())
 
 
 def _ptr(x):
     """Device pointer of a tensor (or an int address, or None)."""
-    if x is None:
-        return None
+    if x is None or x.__class__ is int:
+        return x
     if isinstance(x, int):
         return x
     return x.data_ptr()
 
 
 def _stream(stream):
+    if stream.__class__ is int:
+        return stream
     if stream is None:
         import torch
         return torch.cuda.current_stream().cuda_stream

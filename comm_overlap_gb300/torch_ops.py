@@ -21,34 +21,32 @@ from . import domino as dm
 
 _handles: dict[int, int] = {}
 _lock = threading.Lock()
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+# The current stream's handle as an integer and the current device, without the objects that torch.cuda builds
+# around them (3 us a call on a Grace core).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-class _call:
-    """The device of `x` made current, its handle, and the lock under which handles are used."""
-
-    def __init__(self, x: torch.Tensor):
-        self.device = torch.cuda.device(x.device)
-
-    def __enter__(self) -> int:
-        _lock.acquire()
-        try:
-            self.device.__enter__()
-            index = torch.cuda.current_device()
-            h = _handles.get(index)
-            if h is None:
-                h = _handles[index] = dm.domino_create()
-            return h
-        except BaseException:
-            _lock.release()
-            raise
-
-    def __exit__(self, *exc):
-        self.device.__exit__(*exc)
-        _lock.release()
-        return False
+def _call(fn, x: torch.Tensor, *args) -> None:
+    """fn(handle, *args, stream) on the device of `x` and its current stream, under the lock."""
+    index = x.get_device()
+    if _device() != index:
+        with torch.cuda.device(index):
+            return _call(fn, x, *args)
+    with _lock:
+        handle = _handles.get(index)
+        if handle is None:
+            handle = _handles[index] = dm.domino_create()
+        fn(handle, *args, stream=_raw_stream(index))
 
 
-def _check(name: str, x: torch.Tensor, like: torch.Tensor | None = None, shape=None, dtype=torch.bfloat16) -> None:
+def _check(name: str, x: torch.Tensor, like: torch.Tensor | None = None, shape=None, dtype=_BF16) -> None:
+    """Refuses a tensor that is not on the GPU (that of `like`), or not of the shape or type."""
+    if (isinstance(x, torch.Tensor) and x.dtype is dtype and x.is_cuda and (shape is None or x.shape == shape)
+            and (like is None or x.get_device() == like.get_device())):
+        return
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.dtype != dtype:
@@ -63,11 +61,12 @@ def _rows(x: torch.Tensor) -> tuple[torch.Tensor, int]:
     """A 2-D tensor whose rows the library can stride over, and that stride: `x` itself where its rows
     are contiguous, 16-byte aligned and do not overlap, else a copy."""
     n, c = x.shape
-    if (c <= 1 or x.stride(1) == 1) and x.data_ptr() % 16 == 0:
+    ld, one = x.stride()
+    if (one == 1 or c <= 1) and x.data_ptr() % 16 == 0:
         if n <= 1:
             return x, c
-        if x.stride(0) >= c and x.stride(0) % 8 == 0:
-            return x, x.stride(0)
+        if ld >= c and ld % 8 == 0:
+            return x, ld
     return x.clone(memory_format=torch.contiguous_format), c
 
 
@@ -96,11 +95,10 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
         _check("bias", bias, x, (h,))
     x, ld = _rows(x)
     weight, bias = _vec(weight), _vec(bias)
-    y = torch.empty((rows, h), dtype=torch.bfloat16, device=x.device)
-    mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    with _call(x) as handle:
-        dm.domino_layernorm_fwd(handle, x, ld, weight, bias, eps, y, h, mean, rstd, rows, h)
+    y = torch.empty((rows, h), dtype=_BF16, device=x.device)
+    mean = torch.empty(rows, dtype=_F32, device=x.device)
+    rstd = torch.empty(rows, dtype=_F32, device=x.device)
+    _call(dm.domino_layernorm_fwd, x, x, ld, weight, bias, eps, y, h, mean, rstd, rows, h)
     return y, mean, rstd
 
 
@@ -127,20 +125,19 @@ def layer_norm_bwd(gy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean
             if not g.is_contiguous() or g.data_ptr() % 16:
                 raise ValueError(f"the {name}'s gradient buffer must be contiguous and 16-byte aligned")
     else:
-        gw = torch.empty(h, dtype=torch.float32, device=x.device)
-        gb = torch.empty(h, dtype=torch.float32, device=x.device) if bias_grad else None
+        gw = torch.empty(h, dtype=_F32, device=x.device)
+        gb = torch.empty(h, dtype=_F32, device=x.device) if bias_grad else None
     gy, ld_gy = _rows(gy)
     x, ld_x = _rows(x)
     ld_r = h
     if gres is not None:
         gres, ld_r = _rows(gres)
     weight, mean, rstd = _vec(weight), _vec(mean), _vec(rstd)
-    gx = torch.empty((rows, h), dtype=torch.bfloat16, device=x.device)
+    gx = torch.empty((rows, h), dtype=_BF16, device=x.device)
     n = dm.domino_layernorm_bwd_workspace_size(rows, h)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-    with _call(x) as handle:
-        dm.domino_layernorm_bwd(handle, gy, ld_gy, x, ld_x, weight, mean, rstd, gres, ld_r, gx, h, gw, gb,
-                                int(grads is not None), rows, h, ws, n)
+    _call(dm.domino_layernorm_bwd, x, gy, ld_gy, x, ld_x, weight, mean, rstd, gres, ld_r, gx, h, gw, gb,
+          int(grads is not None), rows, h, ws, n)
     return gx, gw, gb
 
 
@@ -215,10 +212,9 @@ def linear_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
         residual, ld_r = _rows(residual)
     x, ld_x = _rows(x)
     weight, bias = _vec(weight), _vec(bias)
-    y = torch.empty((m, n), dtype=torch.bfloat16, device=x.device)
+    y = torch.empty((m, n), dtype=_BF16, device=x.device)
     z = torch.empty_like(y) if save else None
-    with _call(x) as handle:
-        dm.domino_linear_fwd(handle, x, ld_x, weight, bias, act, residual, ld_r, y, n, z, n, m, n, k)
+    _call(dm.domino_linear_fwd, x, x, ld_x, weight, bias, act, residual, ld_r, y, n, z, n, m, n, k)
     return y, z
 
 
@@ -247,16 +243,15 @@ def linear_bwd(gy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, z: torch
     gy, ld_gy = _rows(gy)
     x, ld_x = _rows(x)
     weight = _vec(weight)
-    gx = torch.empty((m, k), dtype=torch.bfloat16, device=x.device) if x_grad else None
-    gw = torch.empty((n, k), dtype=torch.bfloat16, device=x.device) if weight_grad and main_grad is None else None
+    gx = torch.empty((m, k), dtype=_BF16, device=x.device) if x_grad else None
+    gw = torch.empty((n, k), dtype=_BF16, device=x.device) if weight_grad and main_grad is None else None
     gb = bias_main_grad
     if gb is None and bias_grad:
-        gb = torch.empty(n, dtype=torch.float32, device=x.device)
+        gb = torch.empty(n, dtype=_F32, device=x.device)
     size = dm.domino_linear_bwd_workspace_size(m, n, k, act)
     ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
-    with _call(x) as handle:
-        dm.domino_linear_bwd(handle, gy, ld_gy, x, ld_x, weight, z, ld_z, act, gx, k, gw,
-                             main_grad if weight_grad else None, gb, int(bias_main_grad is not None), m, n, k, ws, size)
+    _call(dm.domino_linear_bwd, x, gy, ld_gy, x, ld_x, weight, z, ld_z, act, gx, k, gw,
+          main_grad if weight_grad else None, gb, int(bias_main_grad is not None), m, n, k, ws, size)
     return gx, gw, gb
 
 
@@ -383,9 +378,8 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     lse = torch.empty((tq, hq), dtype=torch.float32, device=q.device) if return_lse else None
     size = dm.domino_attn_packed_workspace_size(tq, n, hq, hkv, tk)
     ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
-    with _call(q) as handle:
-        dm.domino_attn_packed_fwd(handle, q, ld_q, k, ld_k, v, ld_v, cu_q, k_start, k_len,
-                                  HEAD_DIM ** -0.5 if scale is None else scale, out, ld_o, lse, tq, n, hq, hkv, tk, ws, size)
+    _call(dm.domino_attn_packed_fwd, q, q, ld_q, k, ld_k, v, ld_v, cu_q, k_start, k_len,
+          HEAD_DIM ** -0.5 if scale is None else scale, out, ld_o, lse, tq, n, hq, hkv, tk, ws, size)
     return (out, lse) if return_lse else out
 
 
@@ -393,8 +387,13 @@ def device_status(device: torch.device | int | None = None) -> None:
     """Synchronises the device and raises DominoError if a call of this module's since the last look ran out
     of a wait or met lengths that leave their tensors."""
     x = torch.empty(0, device="cuda" if device is None else device)
-    with _call(x) as handle:
+    status, site = 0, 0
+
+    def read(handle, stream):
+        nonlocal status, site
         status, site = dm.domino_device_status(handle)
+
+    _call(read, x)
     if status != dm.DOMINO_OK:
         what = "packed_attention met lengths that leave its tensors" if site == dm.BAD_LENGTHS_SITE else \
             f"a device-side wait ran out (site {site:#x})"

@@ -156,15 +156,13 @@ def test_strides_and_outputs_left_alone(ops):
     check_fwd(x, w, None, "gelu", r, y, z)
     big = torch.full((m + 2, n + 16), 7.0, dtype=torch.bfloat16, device="cuda")
     out = big[1:-1, 8:8 + n]
-    with ops._call(x) as h:
-        dm.domino_linear_fwd(h, x, xw.shape[1], w, None, dm.ACT_GELU, r, rw.shape[1], out, big.shape[1], None, 0, m, n, k)
+    ops._call(dm.domino_linear_fwd, x, x, xw.shape[1], w, None, dm.ACT_GELU, r, rw.shape[1], out, big.shape[1], None, 0, m, n, k)
     assert torch.equal(out, y)
     big[1:-1, 8:8 + n] = 7.0
     assert (big == 7.0).all()
     # the residual's buffer as the output
     r2 = r.clone()
-    with ops._call(x) as h:
-        dm.domino_linear_fwd(h, x, xw.shape[1], w, None, dm.ACT_GELU, r2, n, r2, n, None, 0, m, n, k)
+    ops._call(dm.domino_linear_fwd, x, x, xw.shape[1], w, None, dm.ACT_GELU, r2, n, r2, n, None, 0, m, n, k)
     assert torch.equal(r2, y)
     # an output gradient broadcast over its rows
     e = r[:1].expand(m, n)
