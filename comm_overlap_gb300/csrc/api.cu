@@ -1377,14 +1377,15 @@ domino_status domino_device_status(domino_handle H, domino_status* out, int32_t*
   DM_TRY(ready(H));
   if (!out) return fail(DOMINO_ERR_INVALID_ARG, "out is NULL");
   DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
-  int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0;
+  int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0, c7 = 0;
   DM_CUDA(dm::take_gemm_fwd_error(&c1), "reading the device error word");
   DM_CUDA(dm::take_gemm_bwd_error(&c2), "reading the device error word");
   DM_CUDA(dm::take_attn_error(&c3), "reading the device error word");
   DM_CUDA(dm::take_gemm_fp8_error(&c4), "reading the device error word");
   DM_CUDA(dm::take_linear_error(&c5), "reading the device error word");
   DM_CUDA(dm::take_packed_error(&c6), "reading the device error word");
-  const int code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : (c4 ? c4 : (c5 ? c5 : c6))));
+  DM_CUDA(dm::take_norm_error(&c7), "reading the device error word");
+  const int code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : (c4 ? c4 : (c5 ? c5 : (c6 ? c6 : c7)))));
   *out = code == 0 ? DOMINO_OK : (code == dm::kPackedBadLengths ? DOMINO_ERR_INVALID_ARG : DOMINO_ERR_TIMEOUT);
   if (site) *site = code;
   return DOMINO_OK;

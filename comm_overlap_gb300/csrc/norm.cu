@@ -8,8 +8,12 @@
 // the next row's pieces are loaded before the current row is reduced, which keeps memory busy across
 // the reductions.  All arithmetic is fp32; the one rounding to bf16 is the output's.
 // Bound: memory (forward 4 bytes, backward 6, with a residual gradient 8 bytes an element).
+#include <atomic>
+
 #include "actfn.cuh"
+#include "f32x2.cuh"
 #include "ops.h"
+#include "ptx.cuh"
 
 namespace dm {
 
@@ -49,6 +53,13 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
+__device__ __forceinline__ void unpack8(const uint4& w, uint64_t (&v)[4]) {
+  v[0] = f2(bf16lo(w.x), bf16hi(w.x));
+  v[1] = f2(bf16lo(w.y), bf16hi(w.y));
+  v[2] = f2(bf16lo(w.z), bf16hi(w.z));
+  v[3] = f2(bf16lo(w.w), bf16hi(w.w));
+}
+
 template <int NPT>
 __device__ __forceinline__ void load_row(uint4 (&w)[NPT], const uint16_t* p, int t, int tpr, int nv) {
   const uint4* q = reinterpret_cast<const uint4*>(p);
@@ -61,7 +72,7 @@ __device__ __forceinline__ void load_row(uint4 (&w)[NPT], const uint16_t* p, int
 
 // mean and 1 / sqrt(var + eps) of the row (variance of the centred values, as a second pass over the
 // registers), y = (x - mean) rstd gamma + beta.
-template <int NPT>
+template <int NPT, bool KEEP>
 __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a, const int tpr) {
   pdl_launch();
   pdl_wait();
@@ -76,17 +87,26 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
   int flip = 0;
   const float inv_h = 1.0f / static_cast<float>(a.h);
   uint4 w[NPT], ga[NPT], be[NPT];
-  load_row<NPT>(w, a.X + r * a.ld_x, t, tpr, nv);
-#pragma unroll
-  for (int i = 0; i < NPT; ++i) {
+  auto gamma_at = [&](int i) {
     const int v = t + i * tpr;
-    ga[i] = v < nv ? reinterpret_cast<const uint4*>(a.gamma)[v] : make_uint4(0u, 0u, 0u, 0u);
-    be[i] = v < nv && a.beta ? reinterpret_cast<const uint4*>(a.beta)[v] : make_uint4(0u, 0u, 0u, 0u);
+    return v < nv ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + v) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto beta_at = [&](int i) {
+    const int v = t + i * tpr;
+    return v < nv && a.beta ? __ldg(reinterpret_cast<const uint4*>(a.beta) + v) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  load_row<NPT>(w, a.X + r * a.ld_x, t, tpr, nv);
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int i = 0; i < NPT; ++i) {
+      ga[i] = gamma_at(i);
+      be[i] = beta_at(i);
+    }
   }
   for (; r < a.rows; r += stride) {
     uint4 next[NPT];
     const bool more = r + stride < a.rows;
-    if (more) load_row<NPT>(next, a.X + (r + stride) * a.ld_x, t, tpr, nv);
+    if (KEEP && more) load_row<NPT>(next, a.X + (r + stride) * a.ld_x, t, tpr, nv);
     // mean and variance of the row times c
     auto stats = [&](float c, float& mean, float& var) {
       float s = 0.0f;
@@ -125,17 +145,201 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
       if (t + i * tpr >= nv) continue;
       float x[8], g[8], b[8];
       unpack8(w[i], x);
-      unpack8(ga[i], g);
-      unpack8(be[i], b);
+      unpack8(KEEP ? ga[i] : gamma_at(i), g);
+      unpack8(KEEP ? be[i] : beta_at(i), b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = fmaf((x[e] * c - mean) * rstd, g[e], b[e]);
       y[t + i * tpr] = pack8(x);
     }
     if (more) {
+      if constexpr (KEEP) {
 #pragma unroll
-      for (int i = 0; i < NPT; ++i) w[i] = next[i];
+        for (int i = 0; i < NPT; ++i) w[i] = next[i];
+      } else {
+        load_row<NPT>(w, a.X + (r + stride) * a.ld_x, t, tpr, nv);
+      }
     }
   }
+}
+
+// ---- forward of many rows: each team of `wpr` warps streams rows through its own `depth` buffers in shared memory
+// with bulk copies, so that memory never waits for a reduction and no team for another.  The row is
+// normalised in place and stored from there; a buffer is refilled one row after its store was issued.
+// Same arithmetic as above up to the order of the sums.  32768 x 4096: 135 us above, 88 us here (0.90 of the copy
+// bandwidth; the same copies without arithmetic take 86 us).
+__device__ int g_norm_err;
+
+__device__ __forceinline__ void bulk_load_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, bytes);
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_row(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(src),
+               "r"(bytes)
+               : "memory");
+}
+
+constexpr int kStreamMaxWarps = 16, kStreamMaxDepth = 3;
+constexpr int kStreamCtrl = 1024;
+
+__global__ void __launch_bounds__(32 * kStreamMaxWarps) ln_fwd_stream_kernel(const LnFwdArgs a, const int depth, const int wpr) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, teams = (blockDim.x >> 5) / wpr;
+  const int team = warp / wpr, wt = warp - team * wpr, tt = wt * 32 + lane, width = wpr * 32;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.h) * 2u, pitch = (row_bytes + 127u) & ~127u;
+  const uint32_t bar0 = smem_u32(smem) + static_cast<uint32_t>(team * kStreamMaxDepth) * 8u;
+  float* joint = reinterpret_cast<float*>(smem + 512);  // a team's warps: mean and sum of squares each
+  // gamma and beta in shared memory: beside buffers of this size L1 is too small to hold them (101 -> 88 us)
+  const uint32_t sg = smem_u32(smem) + kStreamCtrl, sb = sg + pitch;
+  const uint32_t buf0 = sg + (2u + static_cast<uint32_t>(team * depth)) * pitch;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kStreamCtrl - 4);
+  if (tt == 0) {
+    for (int d = 0; d < depth; ++d) mbar_init(bar0 + 8u * d, 1);
+    if (team == 0) *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_launch();
+  pdl_wait();
+  const int nv = static_cast<int>(a.h >> 3);
+  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+    const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.gamma) + v);
+    const uint4 b = a.beta ? __ldg(reinterpret_cast<const uint4*>(a.beta) + v) : make_uint4(0u, 0u, 0u, 0u);
+    st_shared_v4(sg + 16u * v, g.x, g.y, g.z, g.w);
+    st_shared_v4(sb + 16u * v, b.x, b.y, b.z, b.w);
+  }
+  __syncthreads();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * teams, r0 = static_cast<int64_t>(blockIdx.x) * teams + team;
+  if (tt == 0)
+    for (int d = 0; d < depth; ++d)
+      if (r0 + d * stride < a.rows) bulk_load_row(buf0 + d * pitch, a.X + (r0 + d * stride) * a.ld_x, row_bytes, bar0 + 8u * d);
+  auto team_sync = [&] {
+    if (wpr > 1)
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(width) : "memory");
+    else
+      __syncwarp();
+  };
+  auto pieces = [&](int thread) { return static_cast<float>(thread < nv ? (nv - 1 - thread) / width + 1 : 0); };
+  // the values (in eights) that each warp of the team holds
+  auto held = [&](int w) {
+    const int full = nv / width, rest = nv - full * width - w * 32;
+    return static_cast<float>(full * 32 + (rest < 0 ? 0 : rest > 32 ? 32 : rest));
+  };
+  const float inv_h = 1.0f / static_cast<float>(a.h);
+  int d = 0;
+  uint32_t phase = 0;
+  for (int64_t r = r0; r < a.rows; r += stride) {
+    const uint32_t buf = buf0 + static_cast<uint32_t>(d) * pitch;
+    // (a wait that runs out raises the abort flag; the row is then not stored)
+    bool ok = mbar_wait(bar0 + 8u * d, phase, abort_flag, &g_norm_err, 0x250);
+    // mean and variance of the row times c in one pass: each thread's sums are taken relative to the mean of its
+    // first eight values (so that their squares do not cancel), then joined pairwise in the warp and in warp order
+    auto stats = [&](float c, float& mean, float& var) {
+      float n = pieces(tt), m2 = 0.0f;
+      mean = 0.0f;
+      if (tt < nv) {
+        uint64_t x[4];
+        unpack8(ld_shared_v4(buf + 16u * tt), x);
+        const uint64_t c2 = f2(c, c);
+        float lo, hi;
+        f2_split(add_f2(add_f2(mul_f2(x[0], c2), mul_f2(x[1], c2)), add_f2(mul_f2(x[2], c2), mul_f2(x[3], c2))), lo, hi);
+        const float shift = (lo + hi) * 0.125f;
+        const uint64_t neg = f2(-shift, -shift);
+        uint64_t s[2] = {0, 0}, q[2] = {0, 0};
+#pragma unroll 4
+        for (int v = tt; v < nv; v += width) {
+          unpack8(ld_shared_v4(buf + 16u * v), x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t d2 = fma_f2(x[e], c2, neg);
+            s[e & 1] = add_f2(s[e & 1], d2);
+            q[e & 1] = fma_f2(d2, d2, q[e & 1]);
+          }
+        }
+        f2_split(add_f2(s[0], s[1]), lo, hi);
+        const float off = (lo + hi) / (8.0f * n);
+        mean = shift + off;
+        f2_split(add_f2(q[0], q[1]), lo, hi);
+        m2 = (lo + hi) - off * off * (8.0f * n);
+      }
+      // (n, mean, m2) and (nb, mb, qb) together; n counts eights
+      auto join = [](float& n, float& mean, float& m2, float nb, float mb, float qb) {
+        const float both = n + nb, w = both > 0.0f ? nb / both : 0.0f, diff = mb - mean;
+        m2 = m2 + qb + diff * diff * (8.0f * n * w);
+        mean = mean + diff * w;
+        n = both;
+      };
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float nb = __shfl_xor_sync(0xFFFFFFFFu, n, o), mb = __shfl_xor_sync(0xFFFFFFFFu, mean, o);
+        join(n, mean, m2, nb, mb, __shfl_xor_sync(0xFFFFFFFFu, m2, o));
+      }
+      if (wpr > 1) {
+        if (lane == 0) {
+          joint[2 * warp] = mean;
+          joint[2 * warp + 1] = m2;
+        }
+        team_sync();
+        const float* j = joint + 2 * team * wpr;
+        n = held(0);
+        mean = j[0];
+        m2 = j[1];
+        for (int w = 1; w < wpr; ++w) join(n, mean, m2, held(w), j[2 * w], j[2 * w + 1]);
+      } else {  // lanes may differ in the last bit
+        mean = __shfl_sync(0xFFFFFFFFu, mean, 0);
+        m2 = __shfl_sync(0xFFFFFFFFu, m2, 0);
+      }
+      var = fmaxf(m2 * inv_h, 0.0f);
+    };
+    float c = 1.0f, mean, var;
+    stats(1.0f, mean, var);
+    if (!(var < INFINITY) || !(fabsf(mean) < INFINITY)) {  // as in ln_fwd_kernel; the same in the whole team
+      c = 0x1p-80f;
+      team_sync();  // the first sums are read
+      stats(c, mean, var);
+    }
+    const float rstd = 1.0f / sqrtf(var + a.eps * c * c);
+    if (tt == 0) {
+      if (a.mean) a.mean[r] = mean / c;
+      if (a.rstd) a.rstd[r] = rstd * c;
+    }
+    const uint64_t c2 = f2(c, c), neg = f2(-mean, -mean), r2 = f2(rstd, rstd);
+#pragma unroll 4
+    for (int v = tt; v < nv; v += width) {
+      uint64_t x[4], g[4], b[4];
+      unpack8(ld_shared_v4(buf + 16u * v), x);
+      unpack8(ld_shared_v4(sg + 16u * v), g);
+      unpack8(ld_shared_v4(sb + 16u * v), b);
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float lo, hi;
+        f2_split(fma_f2(mul_f2(fma_f2(x[e], c2, neg), r2), g[e], b[e]), lo, hi);
+        y[e] = pack_bf16x2(lo, hi);
+      }
+      st_shared_v4(buf + 16u * v, y[0], y[1], y[2], y[3]);
+    }
+    fence_proxy_async_smem();
+    team_sync();  // the row is written, and the joint sums are read
+    if (tt == 0 && ok && !*abort_flag) {
+      bulk_store_row(a.Y + r * a.ld_y, buf, row_bytes);
+      bulk_commit_group();
+      // the previous row's buffer: its store has read it once at most this row's is pending
+      const int64_t next = r + (depth - 1) * stride;
+      if (r != r0 && next < a.rows) {
+        bulk_wait_group_read<1>();
+        const int pd = d == 0 ? depth - 1 : d - 1;
+        bulk_load_row(buf0 + static_cast<uint32_t>(pd) * pitch, a.X + next * a.ld_x, row_bytes, bar0 + 8u * pd);
+      }
+    }
+    if (++d == depth) {
+      d = 0;
+      phase ^= 1u;
+    }
+  }
+  if (tt == 0) bulk_wait_group_all();
+  __syncwarp();
 }
 
 // With u = gy gamma and n = (x - mean) rstd:  gx = rstd (u - mean(u) - n mean(u n)) (+ gres);
@@ -312,6 +516,11 @@ __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__
   *reinterpret_cast<float4*>(o) = s;
 }
 
+constexpr int kMaxSmem = 232448;  // a CTA's
+// Rows are streamed from 768 columns and 2.2 M values on: at 1024 columns the two cross at about 1800 rows (3.2 us
+// teams, 4.3 streamed at 1216; 5.5 and 4.3 at 2432), at 4096 at 650 (11.0 and 6.5 at 1216); at 512 columns teams
+// stay ahead (20.9 and 27.8 us at 32768 rows).
+constexpr int64_t kStreamMinH = 768, kStreamMinValues = 2200000;
 int pieces_per_thread(int64_t h) { return h <= 2048 ? 1 : (h <= 8192 ? 2 : 4); }
 int team_threads(int64_t h, int npt) { return static_cast<int>(((h / 8 + npt - 1) / npt + 31) / 32 * 32); }
 
@@ -323,12 +532,36 @@ int ln_bwd_blocks(int64_t rows, int64_t h, int sms) {
   return static_cast<int>(need < most ? need : most);
 }
 
+namespace {
+cudaError_t launch_ln_fwd_stream(const LnFwdArgs& a, int sms, cudaStream_t st) {
+  static std::atomic<bool> ready_of[kMaxDevices];  // the shared-memory opt-in, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready_of[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(ln_fwd_stream_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    ready_of[dev].store(true, std::memory_order_release);
+  }
+  // as many teams as rows fit beside gamma and beta, sixteen warps among them
+  const int64_t pitch = (a.h * 2 + 127) / 128 * 128;
+  const int depth = pitch > 16384 ? 2 : 3;
+  const int64_t fit = (kMaxSmem - kStreamCtrl - 2 * pitch) / (pitch * depth);
+  const int teams = static_cast<int>(fit < kStreamMaxWarps ? fit : kStreamMaxWarps);
+  const int wpr = teams > 8 ? 1 : teams > 4 ? 2 : teams > 2 ? 4 : 8;
+  return launch_pdl(ln_fwd_stream_kernel, dim3(static_cast<unsigned>(sms)), dim3(static_cast<unsigned>(32 * wpr * teams)),
+                    size_t(kStreamCtrl + pitch * (2 + depth * teams)), 1, st, a, depth, wpr);
+}
+}  // namespace
+
 cudaError_t launch_ln_fwd(const LnFwdArgs& a, int sms, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
+  if (a.h >= kStreamMinH && a.rows * a.h >= kStreamMinValues) return launch_ln_fwd_stream(a, sms, st);
   const int npt = pieces_per_thread(a.h), tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
   const int64_t need = (a.rows + teams - 1) / teams, most = int64_t(sms) * (2048 / (teams * tpr));
   const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(static_cast<unsigned>(teams * tpr));
-  return launch_pdl(npt == 1 ? ln_fwd_kernel<1> : npt == 2 ? ln_fwd_kernel<2> : ln_fwd_kernel<4>, grid, block, 0, 1, st, a, tpr);
+  return launch_pdl(npt == 1 ? ln_fwd_kernel<1, true> : npt == 2 ? ln_fwd_kernel<2, true> : ln_fwd_kernel<4, true>, grid, block, 0, 1, st, a, tpr);
 }
 
 cudaError_t launch_ln_bwd(const LnBwdArgs& a, float* part, int sms, cudaStream_t st) {
@@ -345,6 +578,18 @@ cudaError_t launch_ln_cols(const LnBwdArgs& a, const float* part, int sms, cudaS
   const int grid = ln_bwd_blocks(a.rows, a.h, sms);
   const int cgrid = static_cast<int>((2 * a.h + 127) / 128);
   return launch_pdl(ln_cols_kernel, dim3(cgrid), dim3(1024), 0, 1, st, part, grid, a.h, a.ggamma, a.gbeta, a.accumulate);
+}
+
+cudaError_t take_norm_error(int* code) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_norm_err, sizeof(int));
+  if (e != cudaSuccess) return e;
+  *code = v;
+  if (v != 0) {
+    const int zero = 0;
+    e = cudaMemcpyToSymbol(g_norm_err, &zero, sizeof(int));
+  }
+  return e;
 }
 
 }  // namespace dm

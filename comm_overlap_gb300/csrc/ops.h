@@ -90,6 +90,7 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, int sms, cudaStream_t st);
 // `part`: ln_bwd_blocks() rows of 2 h floats, written by the backward and summed by launch_ln_cols.
 int ln_bwd_blocks(int64_t rows, int64_t h, int sms);
 cudaError_t launch_ln_bwd(const LnBwdArgs& a, float* part, int sms, cudaStream_t st);
+cudaError_t take_norm_error(int* code);
 cudaError_t launch_ln_cols(const LnBwdArgs& a, const float* part, int sms, cudaStream_t st);
 
 // ---- linear layer (linear.cu): D (M x N) = A . B^T over k_blocks steps of 64
