@@ -51,9 +51,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kDrainNs = 200000000ull;
 constexpr int kPlanThreads = 1024;  // as many as the sort has bins
 
+// per tile: Q, O free, drain, turn; per ring slot: K, V; per tile and ring slot (2 x + slot): their releases; per tile and
+// score buffer (2 x + buffer, which half blocks use in turn): S, P, P V done.  (Two P V may be outstanding when a
+// softmax warp waits for the later one: with one barrier for both, its parity could not tell them apart.)
 enum : int {
   B_Q_FULL = 0, B_Q_EMPTY = 2, B_K_FULL = 4, B_K_EMPTY = 6, B_V_FULL = 10, B_V_EMPTY = 12, B_S_FULL = 16,
-  B_P_FULL = 18, B_PV_DONE = 20, B_O_FREE = 22, B_DRAIN = 24, B_TURN = 26, B_COUNT = 28
+  B_P_FULL = 20, B_PV_DONE = 24, B_O_FREE = 28, B_DRAIN = 30, B_TURN = 32, B_COUNT = 34
 };
 
 // ---- work list, in the workspace
@@ -336,11 +339,11 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatil
 
 struct Item {
   int hk, q_row, qn, k_row, klen, pos0, b0, slot;
-  int e0, e1;   // tile x attends to key blocks b0 .. e_x - 1 (none: e_x <= b0)
+  int e0, e1;   // tile x attends to half blocks (64 keys) 2 b0 .. e_x - 1 (none: e_x <= 2 b0)
   int last;     // blocks b0 .. last - 1 are loaded
   __device__ int e(int x) const { return x ? e1 : e0; }
-  __device__ bool active(int x) const { return e(x) > b0; }
-  __device__ bool both() const { return e0 > b0 && e1 > b0; }
+  __device__ bool active(int x) const { return e(x) > 2 * b0; }
+  __device__ bool both() const { return e0 > 2 * b0 && e1 > 2 * b0; }
 };
 
 // The k-th item of this CTA: the list in rounds of gridDim.x, every other round backwards.
@@ -361,9 +364,9 @@ __device__ __forceinline__ bool item_at(const PackedArgs& a, const PackedWork& w
   it.slot = v.w < 0 ? -1 : v.w + 2 * it.hk;
   // the last position that each tile's queries see
   const int l0 = it.pos0 + min(a.tokens, it.qn) - 1, l1 = it.pos0 + min(2 * a.tokens, it.qn) - 1;
-  it.e0 = min(v.z, l0 < 0 ? 0 : (l0 >> 7) + 1);
-  it.e1 = it.qn > a.tokens ? min(v.z, l1 < 0 ? 0 : (l1 >> 7) + 1) : 0;
-  it.last = max(it.e0, it.e1);
+  it.e0 = min(2 * v.z, l0 < 0 ? 0 : (l0 >> 6) + 1);
+  it.e1 = it.qn > a.tokens ? min(2 * v.z, l1 < 0 ? 0 : (l1 >> 6) + 1) : 0;
+  it.last = (max(it.e0, it.e1) + 1) >> 1;
   if (it.last < it.b0) it.last = it.b0;
   return true;
 }
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bar(i), (i == B_P_FULL || i == B_P_FULL + 1 || i == B_O_FREE || i == B_O_FREE + 1) ? 4 : 1);
+      mbar_init(bar(i), ((i >= B_P_FULL && i < B_PV_DONE) || i == B_O_FREE || i == B_O_FREE + 1) ? 4 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(bar(B_V_FULL + b), kTile);
           tma_load_3d(sV + b * kTile, &tmV, bar(B_V_FULL + b), 0, it.hk, row);
           tma_load_3d(sV + b * kTile + kHalf, &tmV, bar(B_V_FULL + b), 64, it.hk, row);
-          const uint32_t users = (j < it.e0 ? 1u : 0u) | (j < it.e1 ? 2u : 0u);
+          const uint32_t users = (2 * j < it.e0 ? 1u : 0u) | (2 * j < it.e1 ? 2u : 0u);
           cons = (cons & ~(3u << (2 * b))) | (users << (2 * b));
           upar ^= users << (2 * b);
         }
@@ -472,32 +475,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < 3) {
     {
-      // ---------------- MMA issuer of tile x (the warp walks the work, one elected lane issues).  In items where both tiles work the issuers alternate: each
-      // first Q K^T, then per block P V and the next Q K^T; a tile that has no work left in a block passes
-      // its turn on.  Elsewhere the one with work needs no turn.
+      // ---------------- MMA issuer of tile x (the warp walks the work, one elected lane issues).  Scores are made
+      // in half blocks of 64 keys, two of them in flight (buffers of 64 TMEM columns, P in the first 32), so that
+      // the softmax of one runs while the tensor core makes the next: S of half blocks 0 and 1 first, then for
+      // each half block n P V of it and S of n + 2, in the same buffer.  In items where both tiles work the
+      // issuers alternate, half block by half block; a tile that has no work left passes its turn on.  Elsewhere
+      // the one with work needs no turn.
       const uint32_t x = static_cast<uint32_t>(warp) - 1u;
-      constexpr uint32_t kIdQK = idesc_bf16_f32(kBlk, kBlk, false, false);
+      constexpr uint32_t kIdQK = idesc_bf16_f32(kBlk, 64, false, false);
       constexpr uint32_t kIdPV = idesc_bf16_f32(kBlk, kD, false, true);
       const uint64_t dQ = sdesc_sw128(sQ + x * kTile, 16, 1024), dK0 = sdesc_sw128(sK, 16, 1024),
                      dV0 = sdesc_sw128(sV, kHalf, 1024);
       const uint32_t tS = tmem_base + 128u * x, tO = tmem_base + 256u + 128u * x;
       const bool one = elect_one();
-      auto qk = [=](uint32_t kb) {
-        const uint64_t dk = dK0 + ((static_cast<uint64_t>(kb) * kTile) >> 4);
+      uint32_t gb = 0, nq = 0, np = 0, turns = 0;  // ring position; items and half blocks of this tile; turns received
+      // S of half block h (of ring position gb) into the buffer of half block count n
+      auto qk = [&](int h, uint32_t n) {
+        const uint64_t dk = dK0 + ((static_cast<uint64_t>((gb + (static_cast<uint32_t>(h) >> 1)) & 1u) * kTile + (h & 1) * 8192u) >> 4);
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint64_t off = (static_cast<uint64_t>(kk >> 2) * kHalf + static_cast<uint64_t>(kk & 3) * 32u) >> 4;
-          umma_bf16(tS, dQ + off, dk + off, kIdQK, static_cast<uint32_t>(kk != 0));
+          umma_bf16(tS + 64u * (n & 1u), dQ + off, dk + off, kIdQK, static_cast<uint32_t>(kk != 0));
         }
       };
-      auto pv = [=](uint32_t vb, bool first) {
-        const uint64_t dv = dV0 + ((static_cast<uint64_t>(vb) * kTile) >> 4);
+      auto pv = [&](int h, uint32_t n, bool first) {
+        const uint64_t dv = dV0 + ((static_cast<uint64_t>((gb + (static_cast<uint32_t>(h) >> 1)) & 1u) * kTile + (h & 1) * 8192u) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kBlk / 16; ++kk)
-          umma_bf16_tmem_a(tO, tS + 8u * kk, dv + ((static_cast<uint64_t>(kk) * 2048u) >> 4), kIdPV,
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16_tmem_a(tO, tS + 64u * (n & 1u) + 8u * kk, dv + ((static_cast<uint64_t>(kk) * 2048u) >> 4), kIdPV,
                            static_cast<uint32_t>(!first || kk != 0));
       };
-      uint32_t gb = 0, nq = 0, np = 0, turns = 0;  // ring position; items and blocks of this tile; turns received
       bool ok = true, shared_before = false;
       auto take_turn = [&](bool needed) -> bool {
         if (!needed) return true;
@@ -505,61 +512,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++turns;
         return true;
       };
+      auto k_ready = [&](int h) {
+        const uint32_t r = gb + (static_cast<uint32_t>(h) >> 1);
+        return mbar_wait(bar(B_K_FULL + (r & 1u)), (r >> 1) & 1u, abort_flag, err, a.err_site + 6);
+      };
       Item it;
       for (int k = 0; ok && item_at(a, w, total, k, it); ++k) {
-        const bool two = it.both(), mine = it.active(static_cast<int>(x));
-        const int b0 = it.b0, e = it.e(static_cast<int>(x)), last = it.last;
-        if (mine) {
-          if (!mbar_wait(bar(B_Q_FULL + x), nq & 1u, abort_flag, err, a.err_site + 5) ||
-              !mbar_wait(bar(B_K_FULL + (gb & 1u)), (gb >> 1) & 1u, abort_flag, err, a.err_site + 6) ||
-              // the first turn ever is tile 0's
+        const bool two = it.both();
+        const int n = it.e(static_cast<int>(x)) - 2 * it.b0, most = max(it.e0, it.e1) - 2 * it.b0;  // half blocks: this tile's, all
+        const uint32_t blocks = static_cast<uint32_t>(it.last - it.b0);
+        if (n > 0) {
+          // after S of half block h: its block is released once its last half block of this tile is done
+          auto made_s = [&](int h, uint32_t c) {
+            umma_commit(bar(B_S_FULL + 2 * x + (c & 1u)));
+            if ((h & 1) || h == n - 1) umma_commit(bar(B_K_EMPTY + 2 * x + ((gb + (static_cast<uint32_t>(h) >> 1)) & 1u)));
+            if (h == n - 1) umma_commit(bar(B_Q_EMPTY + x));
+          };
+          // the first turn ever is tile 0's
+          if (!mbar_wait(bar(B_Q_FULL + x), nq & 1u, abort_flag, err, a.err_site + 5) || !k_ready(0) ||
               !take_turn(two && (x == 1 || shared_before))) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (one) {
-            qk(gb & 1u);
+            qk(0, np);
+            made_s(0, np);
+            if (n > 1) {
+              qk(1, np + 1);
+              made_s(1, np + 1);
+            }
             if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
-            umma_commit(bar(B_S_FULL + x));
-            umma_commit(bar(B_K_EMPTY + 2 * x + (gb & 1u)));
-            if (b0 + 1 == e) umma_commit(bar(B_Q_EMPTY + x));
           }
-          for (int j = b0; ok && j < last; ++j) {
-            if (j >= e) {  // the other tile alone
+          for (int h = 0; ok && h < most; ++h) {
+            if (h >= n) {  // the other tile alone
               ok = take_turn(two);
               if (ok && two && one) mbar_arrive(bar(B_TURN + (x ^ 1u)));
               continue;
             }
-            const uint32_t r = gb + static_cast<uint32_t>(j - b0), r1 = r + 1u;
+            const uint32_t r = gb + (static_cast<uint32_t>(h) >> 1);
             // the waits that are usually over first, the softmax hand-off (the critical path) last
             if (!mbar_wait(bar(B_V_FULL + (r & 1u)), (r >> 1) & 1u, abort_flag, err, a.err_site + 7) ||
-                (j + 1 < e &&
-                 !mbar_wait(bar(B_K_FULL + (r1 & 1u)), (r1 >> 1) & 1u, abort_flag, err, a.err_site + 6)) ||
+                (h + 2 < n && !k_ready(h + 2)) ||
                 // the item's first P V overwrites O: the previous item's must be read
-                (j == b0 && nq > 0 && !mbar_wait(bar(B_O_FREE + x), (nq - 1) & 1u, abort_flag, err, a.err_site + 8)) ||
-                !take_turn(two) || !mbar_poll(bar(B_P_FULL + x), np & 1u, abort_flag, err, a.err_site + 9)) {
+                (h == 0 && nq > 0 && !mbar_wait(bar(B_O_FREE + x), (nq - 1) & 1u, abort_flag, err, a.err_site + 8)) ||
+                !take_turn(two) || !mbar_poll(bar(B_P_FULL + 2 * x + (np & 1u)), (np >> 1) & 1u, abort_flag, err, a.err_site + 9)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            ++np;
-            if (!one) continue;
-            pv(r & 1u, j == b0);
-            if (j + 1 < e) qk(r1 & 1u);  // overwrites P only after the product above (issue order)
-            if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
-            umma_commit(bar(B_PV_DONE + x));
-            umma_commit(bar(B_V_EMPTY + 2 * x + (r & 1u)));
-            if (j + 1 < e) {
-              umma_commit(bar(B_S_FULL + x));
-              umma_commit(bar(B_K_EMPTY + 2 * x + (r1 & 1u)));
-              if (j + 2 == e) umma_commit(bar(B_Q_EMPTY + x));
+            if (one) {
+              pv(h, np, h == 0);
+              umma_commit(bar(B_PV_DONE + 2 * x + (np & 1u)));
+              if ((h & 1) || h == n - 1) umma_commit(bar(B_V_EMPTY + 2 * x + (r & 1u)));
+              if (h + 2 < n) {
+                qk(h + 2, np);  // overwrites P only after the product above (issue order)
+                made_s(h + 2, np);
+              }
+              if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
             }
+            ++np;
           }
           ++nq;
         }
         shared_before |= two;
-        gb += static_cast<uint32_t>(last - b0);
+        gb += blocks;
       }
       if (one) umma_commit(bar(B_DRAIN + x));
       const uint64_t t0 = global_timer_ns();
@@ -578,44 +595,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t inv_group = (65536u + static_cast<uint32_t>(a.group) - 1u) / static_cast<uint32_t>(a.group);
     auto token_of = [inv_group](int r) { return static_cast<int>((static_cast<uint32_t>(r) * inv_group) >> 16); };
     const int tok = token_of(row);
-    uint32_t cb = 0, gb = 0;  // key blocks this tile has processed; ring position
+    uint32_t cb = 0, gb = 0;  // half blocks this tile has processed; ring position
     bool ok = true;
     Item it;
     for (int k = 0; ok && item_at(a, w, total, k, it); ++k) {
-      const int e = it.e(x), b0 = it.b0, klen = it.klen;
+      const int e = it.e(x), first = 2 * it.b0, klen = it.klen;
       // the last key position that this row sees (none for rows outside)
       const int lim = row < rows && tok < it.qn - x * a.tokens ? min(it.pos0 + x * a.tokens + tok, klen - 1) : -1;
       float m_run = -INFINITY, l_run = 0.0f;
-      for (int j = b0; ok && j < e; ++j, ++cb) {
-        ok = mbar_wait(bar(B_S_FULL + x), cb & 1u, abort_flag, err, a.err_site + 10);
+      for (int j = first; ok && j < e; ++j, ++cb) {
+        const uint32_t tB = tS + 64u * (cb & 1u);
+        ok = mbar_wait(bar(B_S_FULL + 2 * x + (cb & 1u)), (cb >> 1) & 1u, abort_flag, err, a.err_site + 10);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(tS + 32u * i, sr[i]);
+        uint32_t sr[2][32];
+        tmem_ld32(tB, sr[0]);
+        tmem_ld32(tB + 32u, sr[1]);
         tmem_ld_wait();
-        const int rel = lim - j * kBlk;  // columns above it are masked
-        if (__any_sync(0xFFFFFFFFu, rel < kBlk - 1)) {
+        const int rel = lim - j * 64;  // columns above it are masked
+        if (__any_sync(0xFFFFFFFFu, rel < 63)) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
+          for (int c = 0; c < 64; ++c)
             if (c > rel) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
         }
-        float m8[8];
+        float m4[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
+        for (int i = 0; i < 4; ++i) m4[i] = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 128; c += 2)
-          m8[(c >> 1) & 7] = max3(m8[(c >> 1) & 7], __uint_as_float(sr[c >> 5][c & 31]),
+        for (int c = 0; c < 64; c += 2)
+          m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
                                   __uint_as_float(sr[c >> 5][(c & 31) + 1]));
-        const float top = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), max3(m8[6], m8[7], m8[7]));
+        const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
         // running maximum in the log2 domain, raised when some row of the warp would pass it by more than
         // 8 (p <= 2^8 otherwise); O and the sum are then rescaled.  A row that has seen no key keeps
         // -inf, and zero stands in for it so that its p are 0 and not NaN.
         const float cand = fmaxf(m_run, top * a.scale_log2);
-        const bool raise = __any_sync(0xFFFFFFFFu, cand > m_run + 8.0f) || j == b0;
+        const bool raise = __any_sync(0xFFFFFFFFu, cand > m_run + 8.0f) || j == first;
         const float mx = raise ? cand : m_run;
         const float base = mx == -INFINITY ? 0.0f : mx;
         const float alpha = raise ? ex2_approx(m_run - base) : 1.0f;
@@ -623,32 +641,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) l4[i] = f2(0.0f, 0.0f);
         const uint64_t sc2 = f2(a.scale_log2, a.scale_log2), nmx2 = f2(-base, -base);
-        uint32_t pk[2][32];
+        uint32_t pk[32];
         // p = 2^(score - maximum), two columns at a time
 #pragma unroll
-        for (int c = 0; c < 64; ++c) {
+        for (int c = 0; c < 32; ++c) {
           const int i = 2 * c;
           float p0, p1;
           f2_split(fma_f2(f2(__uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1])), sc2, nmx2), p0, p1);
           p0 = ex2_approx(p0);
           p1 = ex2_approx(p1);
           l4[c & 3] = add_f2(l4[c & 3], f2(p0, p1));
-          pk[c >> 5][c & 31] = pack_bf16x2(p0, p1);
+          pk[c] = pack_bf16x2(p0, p1);
         }
-        float l8[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f2_split(l4[i], l8[2 * i], l8[2 * i + 1]);
-#pragma unroll
-        for (int i = 4; i > 0; i >>= 1)
-#pragma unroll
-          for (int n = 0; n < i; ++n) l8[n] += l8[n + i];
-        l_run = l_run * alpha + l8[0];
+        tmem_st32(tB, pk);  // P -> the first 32 columns of its scores
+        float l0, l1;
+        f2_split(add_f2(add_f2(l4[0], l4[1]), add_f2(l4[2], l4[3])), l0, l1);
+        l_run = l_run * alpha + (l0 + l1);
         m_run = mx;
-        // P -> the first 64 columns of S; they and O are free: the previous block's P V was issued
-        // before this block's Q K^T by the same thread, so it has completed once S_FULL has
-        tmem_st32(tS, pk[0]);
-        tmem_st32(tS + 32u, pk[1]);
-        if (j > b0 && raise) {
+        if (j > first && raise) {
+          // O is free once the previous half block's P V has completed
+          ok = mbar_wait(bar(B_PV_DONE + 2 * x + ((cb - 1u) & 1u)), ((cb - 1u) >> 1) & 1u, abort_flag, err, a.err_site + 13);
+          if (!__all_sync(0xFFFFFFFFu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
@@ -665,16 +682,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(tO + static_cast<uint32_t>(c * 32), o);
           }
         }
-        if ((j + 1) * kBlk > klen) {
-          // the value tile's rows past the sequence: cleared before the product reads them (0 x NaN)
-          const uint32_t r = gb + static_cast<uint32_t>(j - b0);
+        if ((j + 1) * 64 > klen) {
+          // the half block's value rows past the sequence: cleared before the product reads them (0 x NaN)
+          const uint32_t r = gb + (static_cast<uint32_t>(j - first) >> 1);
           ok = mbar_wait(bar(B_V_FULL + (r & 1u)), (r >> 1) & 1u, abort_flag, err, a.err_site + 11);
           if (!__all_sync(0xFFFFFFFFu, ok)) {
             ok = false;
             break;
           }
-          const uint32_t v = sV + (r & 1u) * kTile;
-          for (int c = klen - j * kBlk + (row >> 3); c < kBlk; c += 16)
+          const uint32_t v = sV + (r & 1u) * kTile + static_cast<uint32_t>(j & 1) * 8192u;
+          for (int c = klen - j * 64 + (row >> 3); c < 64; c += 16)
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h)
               st_shared_v4(v + h * kHalf + static_cast<uint32_t>(c) * 128u + (static_cast<uint32_t>(row) & 7u) * 16u, 0u, 0u, 0u, 0u);
@@ -683,15 +700,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_P_FULL + x));
+        if (lane == 0) mbar_arrive(bar(B_P_FULL + 2 * x + (cb & 1u)));
       }
       if (!ok) break;
       item_at(a, w, total, k, it);  // again, rather than kept in registers through the blocks
-      gb += static_cast<uint32_t>(it.last - b0);
+      gb += static_cast<uint32_t>(it.last - it.b0);
       const int live = min(a.tokens, it.qn - x * a.tokens);  // tokens of the tile that exist
       const bool row_ok = row < rows && tok < live;
-      if (e > b0) {
-        ok = mbar_wait(bar(B_PV_DONE + x), (cb - 1u) & 1u, abort_flag, err, a.err_site + 12);
+      if (e > first) {
+        ok = mbar_wait(bar(B_PV_DONE + 2 * x + ((cb - 1u) & 1u)), ((cb - 1u) >> 1) & 1u, abort_flag, err, a.err_site + 12);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
@@ -739,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int h2 = 0; h2 < 2; ++h2) {
         uint32_t o[2][32];
-        if (e > b0 && any) {
+        if (e > first && any) {
           tmem_ld32(tO + static_cast<uint32_t>(h2 * 64), o[0]);
           tmem_ld32(tO + static_cast<uint32_t>(h2 * 64 + 32), o[1]);
           tmem_ld_wait();
@@ -747,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[0][i] = o[1][i] = 0u;
         }
-        if (h2 == 1 && e > b0) {
+        if (h2 == 1 && e > first) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_O_FREE + x));
