@@ -136,7 +136,7 @@ cudaError_t launch_lin_gbias(const float* part, int64_t m, int64_t n, float* gbi
 cudaError_t take_linear_error(int* code);
 
 // ---- causal attention over packed sequences (packed_attention.cu), head dimension 128
-constexpr int kPackedMinPart = 4;          // key blocks of 128 below which an item is not cut further
+constexpr int kPackedMinPart = 4;          // key blocks of 128 in the smallest part of a cut item
 constexpr int kPackedBadLengths = 0x7E0;   // error word: a sequence's rows leave the tensors
 struct PackedArgs {
   const int32_t* cu_q;     // n + 1
@@ -146,16 +146,18 @@ struct PackedArgs {
   float* lse;              // nullable: tq x hq
   int64_t ld_o;
   int32_t n, tq, tk, hq, hkv, group, tokens;  // group = hq / hkv query heads share a key head; tokens = 128 / group
+  int32_t heads_abreast, subgroups, groups;   // packed_groups: key heads of a group of CTAs, hkv / that, groups
   float scale_log2;        // scale x log2(e)
   int32_t err_site;
 };
 // Maps, bf16 with 128-byte swizzle: q (128, group, hkv, tq) in boxes (64, group, 1, tokens); k, v (128, hkv,
 // tk) in boxes (64, 1, 128).
 int64_t packed_scratch_bytes(int64_t tq, int64_t n, int hq, int hkv, int64_t tk);
+void packed_groups(PackedArgs* a, int sms);
 bool packed_may_cut(const PackedArgs& a);
 cudaError_t launch_packed_plan(const PackedArgs& a, void* ws, cudaStream_t st);
 cudaError_t launch_packed_attention(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                                    const PackedArgs& a, void* ws, int sms, cudaStream_t st);
+                                    const PackedArgs& a, void* ws, cudaStream_t st);
 cudaError_t launch_packed_combine(const PackedArgs& a, void* ws, cudaStream_t st);
 cudaError_t take_packed_error(int* code);
 

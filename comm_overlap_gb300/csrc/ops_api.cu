@@ -404,6 +404,7 @@ domino_status domino_attn_packed_fwd(domino_handle H, const uint16_t* Q, int64_t
     a.tokens = 128 / a.group;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err_site = 0x23 << 4;
+    dm::packed_groups(&a, op_sms(H));
     std::string err;
     CUtensorMap mq, mk, mv;
     {
@@ -424,7 +425,7 @@ domino_status domino_attn_packed_fwd(domino_handle H, const uint16_t* Q, int64_t
     DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_PACKED, st, "packed attention plan launch",
                          [&] { return dm::launch_packed_plan(a, workspace, st); }));
     DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_PACKED, st, "packed attention launch",
-                         [&] { return dm::launch_packed_attention(mq, mk, mv, a, workspace, op_sms(H), st); }));
+                         [&] { return dm::launch_packed_attention(mq, mk, mv, a, workspace, st); }));
     if (dm::packed_may_cut(a))
       DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_PACKED, st, "packed attention combine launch",
                            [&] { return dm::launch_packed_combine(a, workspace, st); }));

@@ -7,13 +7,16 @@
 // head, so that a key block is read once for all G heads, and one decoded token fills G rows.
 //
 // Three kernels:
-//  plan     (one block) checks the lengths, lists the work and sorts it, longest first.  An item is two
-//           tiles (2 TQ tokens) of a sequence for one key/value head, over its key blocks of 128.  Items
-//           longer than twice an even share of the whole work are cut along the keys into parts.
-//  attend   (persistent, one CTA an SM) walks the list in a fixed back-and-forth order: O = softmax(scale Q
-//           K^T + mask) V with an online softmax over the key blocks, as in attention.cu: scores and O in
-//           TMEM, P in bf16 in the scores' columns, one MMA issuer per tile taking turns.
-//  combine  adds the parts of cut items: each part left its unnormalised O, maximum and sum.
+//  plan     (one block) checks the lengths and lists the pairs of tiles (2 TQ tokens) with the key blocks of 128 that
+//           each sees, laid end to end for all key/value heads: a pair weighs its blocks and kPackedItemCost.
+//  attend   (persistent) computes O = softmax(scale Q K^T + mask) V with an online softmax over the key blocks,
+//           as in attention.cu: scores and O in TMEM, P in bf16 in the scores' columns.  Where that is even enough, the
+//           CTAs are dealt whole pairs, heaviest first, back and forth.  Elsewhere (few long caches) the work is cut
+//           into equal ranges, one for each group of CTAs (one CTA for each of up to 8 heads, which read neighbouring
+//           cache rows at the same time); a range may begin and end inside a pair, at a block.  Whole / cut, us:
+//           eight prompts of 11000 tokens 140 / 165, 16 heads of four prompts 89 / 104, 64 cached tokens 196 / 188,
+//           one token of 30000 keys 440 / 46 (whole, estimated from its blocks).
+//  combine  adds the parts of pairs that were cut: each left its unnormalised O, maximum and sum.
 // Only keys of the sequence count: scores of rows past its end are masked by position and its last value
 // tile is cleared past its end in shared memory, so whatever lies there (NaN included) has no effect.
 //
@@ -49,9 +52,9 @@ constexpr int kSmem = 1024 + 1024 + 6 * static_cast<int>(kTile) + 8 * static_cas
 static_assert(kSmem <= 232448, "shared memory beyond the per-CTA limit");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kDrainNs = 200000000ull;
-constexpr int kPlanThreads = 1024;  // as many as the sort has bins
+constexpr int kPlanThreads = 1024;
 
-// per tile: Q, O free, drain, turn; per ring slot: K, V; per tile and ring slot (2 x + slot): their releases; per tile and
+// turn; per tile: Q, O free, drain; per ring slot: K, V; per tile and ring slot (2 x + slot): their releases; per tile and
 // score buffer (2 x + buffer, which half blocks use in turn): S, P, P V done.  (Two P V may be outstanding when a
 // softmax warp waits for the later one: with one barrier for both, its parity could not tell them apart.)
 enum : int {
@@ -61,55 +64,64 @@ enum : int {
 
 // ---- work list, in the workspace
 struct PackedHeader {
-  int entries, splits, pad[62];
+  int64_t work, per;  // total weight; that of a group's range
+  int pairs, whole;   // whole: pairs are not cut, and dealt out by weight
+  int pad[58];
 };
-// One pair of tiles (or a part of it) for every key/value head.
-struct __align__(16) PackedEntry {
+// A pair of tiles of one sequence, for every key/value head.
+struct __align__(16) PackedPair {
   int q_row, qn;      // first query row; queries of the sequence from there on
   int k_row, klen;    // first key row, keys
-  int pos0, b0, b1;   // key position of query q_row; key blocks b0 .. b1 - 1
-  int slot;           // -1, or the first partial slot: head h, tile x use slot + 2 h + x
+  int pos0, eh;       // key position of query q_row; half blocks (64 keys) that the pair sees
+  int64_t at;         // where it begins in the work (its head subgroups follow each other, eh + kPackedItemCost each)
 };
-// A pair of tiles that was cut: parts of `len` blocks, part p in slots slot + p 2 Hkv + 2 h + x.
-struct __align__(16) PackedSplit {
-  int q_row, qn, pos0, len, slot, pad[3];
-};
+
+// What cutting costs (parts' items, ranges that end at whole blocks, the combination), in half blocks: pairs stay
+// whole where that leaves the longest share at most so much above the mean.
+constexpr int kPackedCutCost = 16;
+// What an item costs beside its half blocks (its first loads and products, its output), in half blocks: 2.5 us against
+// 0.84 in eight ragged prompts.
+constexpr int kPackedItemCost = 3;
 
 __host__ __device__ inline int64_t up(int64_t n, int64_t a) { return (n + a - 1) / a * a; }
 
 struct PackedLayout {
-  int64_t prefix, entries, splits, o, ml, total;
-  int cap_entries, cap_splits, cap_slots;
+  int64_t starts, pairs, order, prefix, o, ml, total;
+  int cap_pairs, slots;
 };
-// Bounds: the pairs of tiles of all sequences are at most Tq / (2 TQ) + n.  With an even share of
-// total / (2 kSms) blocks (total over all heads), fewer than 2 kSms / Hkv pairs are longer than a share, and
-// their parts over all heads are at most 4 kSms (a pair of e > share blocks has at most 2 e / share).
-constexpr int kSms = 152;
-__host__ inline PackedLayout packed_layout(int64_t tq, int64_t n, int tokens, int hkv, int64_t tk) {
+constexpr int kSms = 152;  // CTAs that the workspace is sized for, at most
+__host__ inline PackedLayout packed_layout(int64_t tq, int64_t n, int tokens, int64_t tk) {
   PackedLayout l;
-  const int64_t pairs = tq / (2 * tokens) + n;
-  const bool cut = (tk + kBlk - 1) / kBlk > kPackedMinPart;
-  l.cap_splits = cut ? static_cast<int>(pairs < 2 * kSms / hkv + 1 ? pairs : 2 * kSms / hkv + 1) : 0;
-  l.cap_slots = cut ? 8 * kSms : 0;
-  l.cap_entries = static_cast<int>(pairs + (cut ? 4 * kSms / hkv + 1 : 0));
-  l.prefix = sizeof(PackedHeader);
-  l.entries = up(l.prefix + (n > kPlanThreads ? n * 4 : 0), 256);
-  l.splits = up(l.entries + int64_t(l.cap_entries) * sizeof(PackedEntry), 256);
-  l.o = up(l.splits + int64_t(l.cap_splits) * sizeof(PackedSplit), 1024);
-  l.ml = l.o + int64_t(l.cap_slots) * kBlk * kD * 4;
-  l.total = l.ml + int64_t(l.cap_slots) * 2 * kBlk * 4;
+  const bool cut = (tk + kBlk - 1) / kBlk >= 2 * kPackedMinPart;
+  l.cap_pairs = static_cast<int>(tq / (2 * tokens) + n);  // of sequences that do not overlap
+  l.slots = cut ? 4 * kSms : 0;                           // a CTA's first and last part, two tiles each
+  l.starts = sizeof(PackedHeader);
+  l.pairs = up(l.starts + kSms * 4, 256);
+  l.order = up(l.pairs + int64_t(l.cap_pairs) * sizeof(PackedPair), 256);
+  l.prefix = up(l.order + int64_t(l.cap_pairs) * 4, 256);
+  l.o = up(l.prefix + (n > kPlanThreads ? n * 4 : 0), 1024);
+  l.ml = l.o + int64_t(l.slots) * kBlk * kD * 4;
+  l.total = l.ml + int64_t(l.slots) * 2 * kBlk * 4;
   return l;
 }
 
 struct PackedWork {
   PackedHeader* head;
-  int* prefix;
-  PackedEntry* entries;
-  PackedSplit* splits;
-  float* o;    // slot: [column / 4][row][4]
-  float* ml;   // slot: maximum (log2 domain) of the 128 rows, then their sums
-  int cap_entries, cap_splits, cap_slots;
+  int* starts;         // the pair in which each group's range begins
+  PackedPair* pairs;
+  int* order;          // the pairs, heaviest first (where they are not cut)
+  int* prefix;         // pairs before each sequence, where there are more sequences than threads
+  float* o;            // slot: [column / 4][row][4]
+  float* ml;           // slot: maximum (log2 domain) of the 128 rows, then their sums
+  int cap_pairs;
 };
+
+// The block at which a range's border `off` into an item of eh half blocks cuts it: no part is shorter than
+// kPackedMinPart (0 or all of its blocks: not cut).
+__device__ __forceinline__ int cut_at(int64_t off, int eh) {
+  const int e = (eh + 1) >> 1, b = off < eh ? static_cast<int>(off) >> 1 : e;
+  return b < kPackedMinPart ? 0 : e - b < kPackedMinPart ? e : b;
+}
 
 // ---- plan -----------------------------------------------------------------------------------------
 
@@ -126,178 +138,152 @@ __device__ __forceinline__ void seq_lengths(const PackedArgs& a, int s, int& q0,
   }
 }
 
-// Key blocks that the queries [tok0, tok1) of a sequence see.
-__device__ __forceinline__ int seen_blocks(int qlen, int klen, int tok1) {
+// Half blocks of keys that the queries before tok1 of a sequence see.
+__device__ __forceinline__ int seen_halves(int qlen, int klen, int tok1) {
   const int last = klen - qlen + min(tok1, qlen) - 1;
-  return last < 0 ? 0 : (last >> 7) + 1;
+  return last < 0 ? 0 : (last >> 6) + 1;
 }
 
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {  // exclusive
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {  // exclusive
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    const T y = __shfl_up_sync(0xFFFFFFFFu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();  // the previous call's sums are read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int s = warp_sums[lane];
+    T s = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      const T y = __shfl_up_sync(0xFFFFFFFFu, s, o);
       if (lane >= o) s += y;
     }
     warp_sums[lane] = s;
   }
   __syncthreads();
   total = warp_sums[31];
-  return x - v + (warp > 0 ? warp_sums[warp - 1] : 0);
+  return x - v + (warp > 0 ? warp_sums[warp - 1] : T(0));
 }
 
-// A pair of tiles: its sequence's lengths, its first token, the key blocks it sees.
-struct PackedPair {
-  int q0, qlen, k0, klen, tok0, e;
-};
-
-// The kernel is a chain of short dependent steps, so each thread keeps its first pair in registers, the totals are
-// added by warp before they meet in shared memory, and the sequences' offsets are searched there when they
-// fit (9 - 17 us before, with a pair's lengths looked up for each step and one atomic a pair).
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedArgs a, const PackedWork w) {
-  constexpr int kBins = 1024;
-  __shared__ int warp_sums[32];
-  __shared__ int bins[kBins];
+  __shared__ int sums[32];
+  __shared__ long long sums64[32];
   __shared__ int near_prefix[kPlanThreads];
-  __shared__ unsigned long long s_total;
-  __shared__ int s_max, s_slots, s_splits, s_bad;
+  __shared__ long long near_at[kPlanThreads];
+  __shared__ int heaviest, longest, bins[kPlanThreads];
   const int tid = threadIdx.x, span = 2 * a.tokens;
-  if (tid == 0) {
-    s_total = 0;
-    s_max = s_slots = s_splits = s_bad = 0;
-  }
-  for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
   pdl_launch();
+  if (tid == 0) heaviest = longest = 0;
+  bins[tid] = 0;
   pdl_wait();
   // pairs of tiles before each sequence
   const bool near = a.n <= kPlanThreads;
-  int pairs = 0;
+  int64_t pairs64 = 0;
   for (int base = 0; base < a.n; base += kPlanThreads) {
     const int s = base + tid;
     int q0, qlen = 0, k0, klen;
     if (s < a.n) seq_lengths(a, s, q0, qlen, k0, klen);
     int total;
-    const int before = pairs + block_scan((qlen + span - 1) / span, warp_sums, total);
-    if (s < a.n) (near ? near_prefix : w.prefix)[s] = before;
-    pairs += total;
+    const int before = block_scan((qlen + span - 1) / span, sums, total);
+    if (s < a.n) (near ? near_prefix : w.prefix)[s] = static_cast<int>(pairs64) + before;
+    pairs64 += total;
+    if (pairs64 > w.cap_pairs) break;  // (uniform) overlapping sequences: refused below
   }
   __syncthreads();
+  int pairs = static_cast<int>(pairs64);
+  if (pairs64 > w.cap_pairs) {
+    if (tid == 0) atomicCAS(&g_packed_err, 0, kPackedBadLengths);
+    pairs = 0;
+  }
   const int* prefix = near ? near_prefix : w.prefix;
-  // pair i belongs to the last sequence that begins at or before it
-  auto pair_of = [&](int i) {
-    int lo = 0, hi = a.n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (prefix[mid] <= i) lo = mid; else hi = mid - 1;
+  long long at = 0;
+  int most = 0, first_eh = 0;
+  for (int base = 0; base < pairs; base += kPlanThreads) {
+    const int i = base + tid;
+    PackedPair p = {};
+    if (i < pairs) {
+      int lo = 0, hi = a.n - 1;  // the last sequence that begins at or before pair i
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= i) lo = mid; else hi = mid - 1;
+      }
+      int q0, qlen, k0, klen;
+      seq_lengths(a, lo, q0, qlen, k0, klen);
+      const int tok0 = (i - prefix[lo]) * span;
+      p.q_row = q0 + tok0;
+      p.qn = qlen - tok0;
+      p.k_row = k0;
+      p.klen = klen;
+      p.pos0 = klen - qlen + tok0;
+      p.eh = seen_halves(qlen, klen, tok0 + span);
+      most = max(most, p.eh);
+      if (i == tid) first_eh = p.eh;
     }
-    PackedPair p;
-    seq_lengths(a, lo, p.q0, p.qlen, p.k0, p.klen);
-    p.tok0 = (i - prefix[lo]) * span;
-    p.e = seen_blocks(p.qlen, p.klen, p.tok0 + span);
-    return p;
-  };
-  PackedPair first = {};
-  if (tid < pairs) first = pair_of(tid);
-  unsigned long long mine = static_cast<unsigned long long>(first.e);
-  int most = first.e;
-  for (int i = tid + kPlanThreads; i < pairs; i += kPlanThreads) {
-    const int e = pair_of(i).e;
-    mine += static_cast<unsigned long long>(e);
-    most = max(most, e);
+    long long total;
+    p.at = at + block_scan(i < pairs ? static_cast<long long>(p.eh + kPackedItemCost) * a.subgroups : 0ll, sums64, total);
+    if (i < pairs) {
+      w.pairs[i] = p;
+      if (base == 0) near_at[tid] = p.at;
+    }
+    at += total;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-  }
-  if ((tid & 31) == 0 && most > 0) {
-    atomicAdd(&s_total, mine);
-    atomicMax(&s_max, most);
-  }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if ((tid & 31) == 0 && most > 0) atomicMax(&heaviest, most);
   __syncthreads();
-  // even share of the blocks, twice per SM; parts of at least kPackedMinPart blocks
-  const unsigned long long total = s_total * static_cast<unsigned long long>(a.hkv);
-  const unsigned long long even = (total + 2 * kSms - 1) / (2 * kSms);
-  int share = even > 0x7FFFFFFFull ? 0x7FFFFFFF : static_cast<int>(even);
-  if (share < kPackedMinPart) share = kPackedMinPart;
-  if (w.cap_slots == 0) share = 0x7FFFFFFF;
-  auto parts_of = [&](int e, int& len) {
-    len = e;
-    if (e <= share) return 1;
-    const int parts = (e + share - 1) / share;
-    len = (e + parts - 1) / parts;
-    return (e + len - 1) / len;
-  };
+  long long per = (at + a.groups - 1) / a.groups;
+  if (per < 2 * kPackedMinPart + kPackedItemCost) per = 2 * kPackedMinPart + kPackedItemCost;
+  if (tid < a.groups) {
+    const long long lo = tid * per;
+    int first = 0, last = pairs - 1;
+    while (first < last) {
+      const int mid = (first + last + 1) >> 1;
+      if ((pairs <= kPlanThreads ? near_at[mid] : w.pairs[mid].at) <= lo) first = mid; else last = mid - 1;
+    }
+    w.starts[tid] = first;
+  }
+  // heaviest first: counting sort by half blocks (the order within a bin is of no consequence)
   int shift = 0;
-  while ((min(s_max, share) >> shift) >= kBins) ++shift;
-  // longest first: counting sort by blocks (order within a bin is of no consequence)
-  for (int i = tid; i < pairs; i += kPlanThreads) {
-    const int e = i == tid ? first.e : pair_of(i).e;
-    int len;
-    const int parts = parts_of(e, len);
-    if (parts > 1) atomicAdd(&bins[kBins - 1 - (len >> shift)], parts - 1);
-    atomicAdd(&bins[kBins - 1 - ((e - (parts - 1) * len) >> shift)], 1);
-  }
+  while ((heaviest >> shift) >= kPlanThreads) ++shift;
+  for (int i = tid; i < pairs; i += kPlanThreads)
+    atomicAdd(&bins[kPlanThreads - 1 - ((i == tid ? first_eh : w.pairs[i].eh) >> shift)], 1);
   __syncthreads();
-  int count;
-  const int start = block_scan(bins[tid], warp_sums, count);
+  int total;
+  const int start = block_scan(bins[tid], sums, total);
   bins[tid] = start;
   __syncthreads();
+  int* sorted = near_prefix;  // (read for the last time above)
   for (int i = tid; i < pairs; i += kPlanThreads) {
-    const PackedPair p = i == tid ? first : pair_of(i);
-    int len;
-    const int parts = parts_of(p.e, len);
-    PackedEntry en;
-    en.q_row = p.q0 + p.tok0;
-    en.qn = p.qlen - p.tok0;
-    en.k_row = p.k0;
-    en.klen = p.klen;
-    en.pos0 = p.klen - p.qlen + p.tok0;
-    int slot = -1;
-    if (parts > 1) {
-      slot = atomicAdd(&s_slots, parts * 2 * a.hkv);
-      const int sp = atomicAdd(&s_splits, 1);
-      if (sp < w.cap_splits && slot + parts * 2 * a.hkv <= w.cap_slots) {
-        PackedSplit ps;
-        ps.q_row = en.q_row;
-        ps.qn = en.qn;
-        ps.pos0 = en.pos0;
-        ps.len = len;
-        ps.slot = slot;
-        w.splits[sp] = ps;
-      } else {
-        s_bad = 1;
-        continue;
-      }
-    }
-    for (int k = 0; k < parts; ++k) {
-      en.b0 = k * len;
-      en.b1 = min(p.e, en.b0 + len);
-      en.slot = parts > 1 ? slot + k * 2 * a.hkv : -1;
-      const int at = atomicAdd(&bins[kBins - 1 - ((en.b1 - en.b0) >> shift)], 1);
-      if (at < w.cap_entries)
-        w.entries[at] = en;
-      else
-        s_bad = 1;
-    }
+    const int eh = i == tid ? first_eh : w.pairs[i].eh, k = atomicAdd(&bins[kPlanThreads - 1 - (eh >> shift)], 1);
+    w.order[k] = i;
+    if (pairs <= kPlanThreads) sorted[k] = eh;
   }
   __syncthreads();
+  // whole pairs, dealt back and forth: the longest of the CTAs' shares, or a bound of it where there are many
+  if (pairs <= kPlanThreads) {
+    const int grid = a.groups * a.heads_abreast;
+    int share = 0;
+    if (tid < grid)
+      for (int t = 0;; ++t) {
+        const int i = t * grid + (t & 1 ? grid - 1 - tid : tid);
+        if (i / a.hkv >= pairs) break;
+        share += sorted[i / a.hkv] + kPackedItemCost;
+      }
+    share = __reduce_max_sync(0xFFFFFFFFu, share);
+    if ((tid & 31) == 0 && share > 0) atomicMax(&longest, share);
+    __syncthreads();
+  }
+  const bool whole = pairs <= kPlanThreads ? longest <= per + kPackedCutCost
+                                           : 2 * heaviest <= per && static_cast<long long>(pairs) * a.hkv < (1 << 30);
   if (tid == 0) {
-    // beyond the bounds of the workspace only with overlapping sequences, which are refused
-    if (s_bad) atomicCAS(&g_packed_err, 0, kPackedBadLengths);
-    w.head->entries = s_bad ? 0 : count;
-    w.head->splits = s_bad ? 0 : s_splits;
+    w.head->work = at;
+    w.head->per = per;
+    w.head->pairs = pairs;
+    w.head->whole = whole;
   }
 }
 
@@ -346,30 +332,79 @@ struct Item {
   __device__ bool both() const { return e0 > 2 * b0 && e1 > 2 * b0; }
 };
 
-// The k-th item of this CTA: the list in rounds of gridDim.x, every other round backwards.
-__device__ __forceinline__ bool item_at(const PackedArgs& a, const PackedWork& w, int total, int k, Item& it) {
-  const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-  const int64_t i = static_cast<int64_t>(k) * g + ((k & 1) ? g - 1 - c : c);
-  if (i >= total) return false;
-  const int en = static_cast<int>(i) / a.hkv;
-  it.hk = static_cast<int>(i) - en * a.hkv;
-  const int4* p = reinterpret_cast<const int4*>(w.entries + en);
-  const int4 u = p[0], v = p[1];
-  it.q_row = u.x;
-  it.qn = u.y;
-  it.k_row = u.z;
-  it.klen = u.w;
-  it.pos0 = v.x;
-  it.b0 = v.y;
-  it.slot = v.w < 0 ? -1 : v.w + 2 * it.hk;
-  // the last position that each tile's queries see
-  const int l0 = it.pos0 + min(a.tokens, it.qn) - 1, l1 = it.pos0 + min(2 * a.tokens, it.qn) - 1;
-  it.e0 = min(2 * v.z, l0 < 0 ? 0 : (l0 >> 6) + 1);
-  it.e1 = it.qn > a.tokens ? min(2 * v.z, l1 < 0 ? 0 : (l1 >> 6) + 1) : 0;
-  it.last = (max(it.e0, it.e1) + 1) >> 1;
-  if (it.last < it.b0) it.last = it.b0;
-  return true;
-}
+// This CTA's walk through the work: its group's range [lo, hi) in order, as items (pair, head subgroup); or, where
+// pairs stay whole, items (pair, head) in the plan's order, dealt back and forth.
+struct Walk {
+  int pair, sub;           // next item (whole: pair is the round of dealing, sub -1)
+  int cur_pair, cur_head;  // the one returned last
+
+  __device__ Walk(const PackedArgs& a, const PackedWork& w) {
+    pair = cur_pair = cur_head = 0;
+    sub = -1;
+    const int64_t lo = static_cast<int>(blockIdx.x) / a.heads_abreast * w.head->per;
+    if (!w.head->whole && lo < w.head->work) {
+      pair = w.starts[static_cast<int>(blockIdx.x) / a.heads_abreast];
+      sub = static_cast<int>((lo - w.pairs[pair].at) / (w.pairs[pair].eh + kPackedItemCost));
+    }
+  }
+
+  // Pair p of key head hk as far as it lies in the range; false if nothing of it does, with `end` if nothing after it does.
+  __device__ bool item(const PackedArgs& a, const PackedWork& w, int p, int hk, Item& it, bool& end) const {
+    const int4* entry = reinterpret_cast<const int4*>(w.pairs + p);
+    const int4 u = entry[0], v = entry[1];
+    const int eh = v.y, e = (eh + 1) >> 1, wide = eh + kPackedItemCost;
+    const int64_t at = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(v.z)) | (static_cast<uint64_t>(static_cast<uint32_t>(v.w)) << 32));
+    // (the range: read again, rather than kept in registers)
+    const int64_t lo = sub < 0 ? 0 : static_cast<int>(blockIdx.x) / a.heads_abreast * w.head->per;
+    const int64_t hi = sub < 0 ? w.head->work : lo + w.head->per;
+    const int64_t begin = at + static_cast<int64_t>(hk / a.heads_abreast) * wide;
+    end = begin >= hi;
+    if (end) return false;
+    const int b0 = begin >= lo ? 0 : cut_at(lo - begin, eh), b1 = begin + wide <= hi ? e : cut_at(hi - begin, eh);
+    if (b0 >= b1 && (e > 0 || begin < lo)) return false;  // (an item without blocks is its begin's)
+    it.hk = hk;
+    it.q_row = u.x;
+    it.qn = u.y;
+    it.k_row = u.z;
+    it.klen = u.w;
+    it.pos0 = v.x;
+    it.b0 = b0;
+    it.slot = b0 == 0 && b1 == e ? -1 : 4 * static_cast<int>(blockIdx.x) + (b0 > 0 ? 0 : 2);
+    // the last position that each tile's queries see
+    const int l0 = it.pos0 + min(a.tokens, it.qn) - 1, l1 = it.pos0 + min(2 * a.tokens, it.qn) - 1;
+    it.e0 = min(2 * b1, l0 < 0 ? 0 : (l0 >> 6) + 1);
+    it.e1 = it.qn > a.tokens ? min(2 * b1, l1 < 0 ? 0 : (l1 >> 6) + 1) : 0;
+    it.last = (max(it.e0, it.e1) + 1) >> 1;
+    if (it.last < it.b0) it.last = it.b0;
+    return true;
+  }
+
+  __device__ bool next(const PackedArgs& a, const PackedWork& w, Item& it) {
+    const int pairs = w.head->pairs;
+    while (true) {
+      if (sub < 0) {
+        const int grid = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+        const int i = pair * grid + (pair & 1 ? grid - 1 - cta : cta);  // (the plan keeps this within 32 bits)
+        ++pair;
+        const int at = i / a.hkv;
+        if (at >= pairs || !w.head->whole) return false;
+        cur_head = i - at * a.hkv;
+        cur_pair = w.order[at];
+      } else {
+        if (pair >= pairs) return false;
+        cur_pair = pair;
+        cur_head = sub * a.heads_abreast + static_cast<int>(blockIdx.x) % a.heads_abreast;
+        if (++sub == a.subgroups) {
+          sub = 0;
+          ++pair;
+        }
+      }
+      bool end;
+      if (item(a, w, cur_pair, cur_head, it, end)) return true;
+      if (end) return false;
+    }
+  }
+};
 
 __global__ void __launch_bounds__(kThreads, 1)
     packed_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -407,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = w.head->entries * a.hkv;
 
   if (warp < 4)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRoles));
@@ -425,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_bytes = static_cast<uint32_t>(a.tokens * a.group) * 128u;
       bool ok = true;
       Item it;
-      for (int k = 0; ok && item_at(a, w, total, k, it); ++k) {
+      Walk walk(a, w);
+      while (ok && walk.next(a, w, it)) {
         for (int x = 0; x < 2 && ok; ++x) {
           if (!it.active(x)) continue;
           // tile x's Q buffer is free once its previous item's last Q K^T has completed
@@ -478,9 +513,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- MMA issuer of tile x (the warp walks the work, one elected lane issues).  Scores are made
       // in half blocks of 64 keys, two of them in flight (buffers of 64 TMEM columns, P in the first 32), so that
       // the softmax of one runs while the tensor core makes the next: S of half blocks 0 and 1 first, then for
-      // each half block n P V of it and S of n + 2, in the same buffer.  In items where both tiles work the
-      // issuers alternate, half block by half block; a tile that has no work left passes its turn on.  Elsewhere
-      // the one with work needs no turn.
+      // each half block n P V of it and S of n + 2, in the same buffer.  The two issuers run freely, except that
+      // tile 1's first scores of an item wait for tile 0's, which sets the tiles half a step apart (16384-token prompt
+      // 1340 us; 1465 with the issuers taking turns throughout, 1355 with none; 8 ragged prompts 135, 139, 143).
       const uint32_t x = static_cast<uint32_t>(warp) - 1u;
       constexpr uint32_t kIdQK = idesc_bf16_f32(kBlk, 64, false, false);
       constexpr uint32_t kIdPV = idesc_bf16_f32(kBlk, kD, false, true);
@@ -488,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      dV0 = sdesc_sw128(sV, kHalf, 1024);
       const uint32_t tS = tmem_base + 128u * x, tO = tmem_base + 256u + 128u * x;
       const bool one = elect_one();
-      uint32_t gb = 0, nq = 0, np = 0, turns = 0;  // ring position; items and half blocks of this tile; turns received
+      uint32_t gb = 0, nq = 0, np = 0, turns = 0;  // ring position; items and half blocks of this tile; items of two tiles
       // S of half block h (of ring position gb) into the buffer of half block count n
       auto qk = [&](int h, uint32_t n) {
         const uint64_t dk = dK0 + ((static_cast<uint64_t>((gb + (static_cast<uint32_t>(h) >> 1)) & 1u) * kTile + (h & 1) * 8192u) >> 4);
@@ -505,21 +540,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_bf16_tmem_a(tO, tS + 64u * (n & 1u) + 8u * kk, dv + ((static_cast<uint64_t>(kk) * 2048u) >> 4), kIdPV,
                            static_cast<uint32_t>(!first || kk != 0));
       };
-      bool ok = true, shared_before = false;
-      auto take_turn = [&](bool needed) -> bool {
-        if (!needed) return true;
-        if (!mbar_wait(bar(B_TURN + x), turns & 1u, abort_flag, err, a.err_site + 4)) return false;
-        ++turns;
-        return true;
-      };
+      bool ok = true;
       auto k_ready = [&](int h) {
         const uint32_t r = gb + (static_cast<uint32_t>(h) >> 1);
         return mbar_wait(bar(B_K_FULL + (r & 1u)), (r >> 1) & 1u, abort_flag, err, a.err_site + 6);
       };
       Item it;
-      for (int k = 0; ok && item_at(a, w, total, k, it); ++k) {
+      Walk walk(a, w);
+      while (ok && walk.next(a, w, it)) {
         const bool two = it.both();
-        const int n = it.e(static_cast<int>(x)) - 2 * it.b0, most = max(it.e0, it.e1) - 2 * it.b0;  // half blocks: this tile's, all
+        const int n = it.e(static_cast<int>(x)) - 2 * it.b0;  // half blocks of this tile
         const uint32_t blocks = static_cast<uint32_t>(it.last - it.b0);
         if (n > 0) {
           // after S of half block h: its block is released once its last half block of this tile is done
@@ -528,9 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((h & 1) || h == n - 1) umma_commit(bar(B_K_EMPTY + 2 * x + ((gb + (static_cast<uint32_t>(h) >> 1)) & 1u)));
             if (h == n - 1) umma_commit(bar(B_Q_EMPTY + x));
           };
-          // the first turn ever is tile 0's
           if (!mbar_wait(bar(B_Q_FULL + x), nq & 1u, abort_flag, err, a.err_site + 5) || !k_ready(0) ||
-              !take_turn(two && (x == 1 || shared_before))) {
+              (two && x == 1 && !mbar_wait(bar(B_TURN + (turns & 1u)), (turns >> 1) & 1u, abort_flag, err, a.err_site + 4))) {
             ok = false;
             break;
           }
@@ -542,21 +571,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               qk(1, np + 1);
               made_s(1, np + 1);
             }
-            if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
+            // (tile 0 may be a whole item ahead, not two: the rings hold two blocks; hence two barriers)
+            if (two && x == 0) mbar_arrive(bar(B_TURN + (turns & 1u)));
           }
-          for (int h = 0; ok && h < most; ++h) {
-            if (h >= n) {  // the other tile alone
-              ok = take_turn(two);
-              if (ok && two && one) mbar_arrive(bar(B_TURN + (x ^ 1u)));
-              continue;
-            }
+          if (two) ++turns;
+          for (int h = 0; ok && h < n; ++h) {
             const uint32_t r = gb + (static_cast<uint32_t>(h) >> 1);
             // the waits that are usually over first, the softmax hand-off (the critical path) last
             if (!mbar_wait(bar(B_V_FULL + (r & 1u)), (r >> 1) & 1u, abort_flag, err, a.err_site + 7) ||
                 (h + 2 < n && !k_ready(h + 2)) ||
                 // the item's first P V overwrites O: the previous item's must be read
                 (h == 0 && nq > 0 && !mbar_wait(bar(B_O_FREE + x), (nq - 1) & 1u, abort_flag, err, a.err_site + 8)) ||
-                !take_turn(two) || !mbar_poll(bar(B_P_FULL + 2 * x + (np & 1u)), (np >> 1) & 1u, abort_flag, err, a.err_site + 9)) {
+                !mbar_poll(bar(B_P_FULL + 2 * x + (np & 1u)), (np >> 1) & 1u, abort_flag, err, a.err_site + 9)) {
               ok = false;
               break;
             }
@@ -569,13 +595,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 qk(h + 2, np);  // overwrites P only after the product above (issue order)
                 made_s(h + 2, np);
               }
-              if (two) mbar_arrive(bar(B_TURN + (x ^ 1u)));
             }
             ++np;
           }
           ++nq;
         }
-        shared_before |= two;
         gb += blocks;
       }
       if (one) umma_commit(bar(B_DRAIN + x));
@@ -598,7 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t cb = 0, gb = 0;  // half blocks this tile has processed; ring position
     bool ok = true;
     Item it;
-    for (int k = 0; ok && item_at(a, w, total, k, it); ++k) {
+    Walk walk(a, w);
+    while (ok && walk.next(a, w, it)) {
       const int e = it.e(x), first = 2 * it.b0, klen = it.klen;
       // the last key position that this row sees (none for rows outside)
       const int lim = row < rows && tok < it.qn - x * a.tokens ? min(it.pos0 + x * a.tokens + tok, klen - 1) : -1;
@@ -703,7 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(B_P_FULL + 2 * x + (cb & 1u)));
       }
       if (!ok) break;
-      item_at(a, w, total, k, it);  // again, rather than kept in registers through the blocks
+      bool end;
+      walk.item(a, w, walk.cur_pair, walk.cur_head, it, end);  // again, rather than kept in registers through the blocks
       gb += static_cast<uint32_t>(it.last - it.b0);
       const int live = min(a.tokens, it.qn - x * a.tokens);  // tokens of the tile that exist
       const bool row_ok = row < rows && tok < live;
@@ -809,30 +835,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- combine --------------------------------------------------------------------------------------
-// Block (split, key/value head, tile): with m = max m_p and c_p = 2^(m_p - m) over the parts p in order,
-// O = sum c_p O_p / sum c_p l_p, lse = ln 2 (m + log2(sum c_p l_p)).
+// Block (border, head of the group, tile and a quarter of O's columns), for the first border that cuts an item: with
+// m = max m_p and c_p = 2^(m_p - m) over the item's parts p in order, O = sum c_p O_p / sum c_p l_p, lse = ln 2 (m + log2(sum c_p l_p)).
 __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a, const PackedWork w) {
   pdl_launch();
   pdl_wait();
-  if (static_cast<int>(blockIdx.x) >= w.head->splits) return;
-  const PackedSplit s = w.splits[blockIdx.x];
-  const int hk = blockIdx.y, x = blockIdx.z;
-  const int live = min(a.tokens, s.qn - x * a.tokens);
+  const int g = static_cast<int>(blockIdx.x) + 1, j = blockIdx.y, x = blockIdx.z & 1, quarter = blockIdx.z >> 1;
+  const int64_t per = w.head->per;
+  if (g * per >= w.head->work || w.head->whole) return;
+  const PackedPair p = w.pairs[w.starts[g]];
+  const int blocks = (p.eh + 1) >> 1, wide = p.eh + kPackedItemCost, sub = static_cast<int>((g * per - p.at) / wide);
+  const int64_t begin = p.at + static_cast<int64_t>(sub) * wide;
+  auto border = [&](int k) { return k * per <= begin ? 0 : cut_at(k * per - begin, p.eh); };  // where border k cuts the item
+  const int b = border(g), before = border(g - 1);
+  if (b == 0 || b == blocks || before > 0) return;  // not cut here, or already before
+  const int live = min(a.tokens, p.qn - x * a.tokens);
   if (live <= 0) return;
-  const int last = s.pos0 + x * a.tokens + live - 1, e = last < 0 ? 0 : (last >> 7) + 1;
-  const int parts = (e + s.len - 1) / s.len, rows = live * a.group;
-  const int64_t step = 2 * a.hkv, first = s.slot + 2 * hk + x;
-  for (int i = threadIdx.x; i < rows * 32; i += 256) {
-    const int row = i % rows, c = i / rows;  // piece c: columns 4 c .. 4 c + 3
+  const int last = p.pos0 + x * a.tokens + live - 1, e = last < 0 ? 0 : (last >> 7) + 1;
+  // parts that hold some of the tile's blocks: the first is group g - 1's last, the k-th after it group (g - 1 + k)'s first
+  int parts = e > 0 ? 1 : 0;
+  while (parts > 0 && border(g - 1 + parts) < e) ++parts;
+  const int hk = sub * a.heads_abreast + j, rows = live * a.group;
+  auto slot = [&](int k) { return static_cast<int64_t>(4 * ((g - 1 + k) * a.heads_abreast + j) + (k == 0 ? 2 : 0) + x); };
+  for (int i = threadIdx.x; i < rows * 8; i += 256) {
+    const int row = i % rows, c = quarter * 8 + i / rows;  // piece c: columns 4 c .. 4 c + 3
     float m = -INFINITY;
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, w.ml[(first + p * step) * (2 * kBlk) + row]);
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) m = fmaxf(m, w.ml[slot(k) * (2 * kBlk) + row]);
     float l = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const float* ml = w.ml + (first + p * step) * (2 * kBlk);
+    for (int k = 0; k < parts; ++k) {
+      const float* ml = w.ml + slot(k) * (2 * kBlk);
       const float f = exp2f(ml[row] - base);
-      const float4 v = *reinterpret_cast<const float4*>(w.o + (first + p * step) * (kBlk * kD) + (c * kBlk + row) * 4);
+      const float4 v = *reinterpret_cast<const float4*>(w.o + slot(k) * (kBlk * kD) + (c * kBlk + row) * 4);
       l = fmaf(f, ml[kBlk + row], l);
       o0 = fmaf(f, v.x, o0);
       o1 = fmaf(f, v.y, o1);
@@ -842,7 +878,7 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a,
     const bool some = l > 0.0f || l != l;
     const float inv = some ? 1.0f / l : 0.0f;
     const int t = row / a.group;
-    const int64_t token = s.q_row + x * a.tokens + t;
+    const int64_t token = p.q_row + x * a.tokens + t;
     const int head = hk * a.group + row - t * a.group;
     *reinterpret_cast<uint2*>(a.O + token * a.ld_o + static_cast<int64_t>(head) * kD + c * 4) =
         make_uint2(pack_bf16x2(o0 * inv, o1 * inv), pack_bf16x2(o2 * inv, o3 * inv));
@@ -851,25 +887,32 @@ __global__ void __launch_bounds__(256) packed_combine_kernel(const PackedArgs a,
 }
 
 PackedWork packed_work(const PackedArgs& a, void* ws) {
-  const PackedLayout l = packed_layout(a.tq, a.n, a.tokens, a.hkv, a.tk);
+  const PackedLayout l = packed_layout(a.tq, a.n, a.tokens, a.tk);
   uint8_t* p = static_cast<uint8_t*>(ws);
   PackedWork w;
   w.head = reinterpret_cast<PackedHeader*>(p);
+  w.starts = reinterpret_cast<int*>(p + l.starts);
+  w.pairs = reinterpret_cast<PackedPair*>(p + l.pairs);
+  w.order = reinterpret_cast<int*>(p + l.order);
   w.prefix = reinterpret_cast<int*>(p + l.prefix);
-  w.entries = reinterpret_cast<PackedEntry*>(p + l.entries);
-  w.splits = reinterpret_cast<PackedSplit*>(p + l.splits);
   w.o = reinterpret_cast<float*>(p + l.o);
   w.ml = reinterpret_cast<float*>(p + l.ml);
-  w.cap_entries = l.cap_entries;
-  w.cap_splits = l.cap_splits;
-  w.cap_slots = l.cap_slots;
+  w.cap_pairs = l.cap_pairs;
   return w;
 }
 
 }  // namespace
 
 int64_t packed_scratch_bytes(int64_t tq, int64_t n, int hq, int hkv, int64_t tk) {
-  return packed_layout(tq, n, kBlk / (hq / hkv), hkv, tk).total;
+  return packed_layout(tq, n, kBlk / (hq / hkv), tk).total;
+}
+
+void packed_groups(PackedArgs* a, int sms) {
+  // the largest divisor of the key heads up to 8; at most 7 CTAs of a GPU stay idle for it
+  a->heads_abreast = 8;
+  while (a->hkv % a->heads_abreast != 0) --a->heads_abreast;
+  a->subgroups = a->hkv / a->heads_abreast;
+  a->groups = (sms < kSms ? sms : kSms) / a->heads_abreast;
 }
 
 cudaError_t launch_packed_plan(const PackedArgs& a, void* ws, cudaStream_t st) {
@@ -877,7 +920,7 @@ cudaError_t launch_packed_plan(const PackedArgs& a, void* ws, cudaStream_t st) {
 }
 
 cudaError_t launch_packed_attention(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                                    const PackedArgs& a, void* ws, int sms, cudaStream_t st) {
+                                    const PackedArgs& a, void* ws, cudaStream_t st) {
   static std::atomic<bool> ready_of[kMaxDevices];  // the shared-memory opt-in, per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -888,20 +931,15 @@ cudaError_t launch_packed_attention(const CUtensorMap& q, const CUtensorMap& k, 
     if (e != cudaSuccess) return e;
     ready_of[dev].store(true, std::memory_order_release);
   }
-  const PackedWork w = packed_work(a, ws);
-  const int64_t most = int64_t(w.cap_entries) * a.hkv;
-  const int grid = static_cast<int>(most < sms ? most : sms);
-  return launch_pdl(packed_attention_kernel, dim3(grid), dim3(kThreads), kSmem, 1, st, q, k, v, a, w);
+  return launch_pdl(packed_attention_kernel, dim3(static_cast<unsigned>(a.groups * a.heads_abreast)), dim3(kThreads), kSmem, 1, st, q,
+                    k, v, a, packed_work(a, ws));
 }
 
-bool packed_may_cut(const PackedArgs& a) {
-  return packed_layout(a.tq, a.n, a.tokens, a.hkv, a.tk).cap_splits > 0;
-}
+bool packed_may_cut(const PackedArgs& a) { return a.groups > 1 && packed_layout(a.tq, a.n, a.tokens, a.tk).slots > 0; }
 
 cudaError_t launch_packed_combine(const PackedArgs& a, void* ws, cudaStream_t st) {
-  const PackedWork w = packed_work(a, ws);
-  return launch_pdl(packed_combine_kernel, dim3(static_cast<unsigned>(w.cap_splits), static_cast<unsigned>(a.hkv), 2), dim3(256), 0, 1,
-                    st, a, w);
+  return launch_pdl(packed_combine_kernel, dim3(static_cast<unsigned>(a.groups - 1), static_cast<unsigned>(a.heads_abreast), 8), dim3(256),
+                    0, 1, st, a, packed_work(a, ws));
 }
 
 cudaError_t take_packed_error(int* code) {
