@@ -14,6 +14,7 @@
 // also cut along the reduction over the 2 or 4 pairs of a larger cluster, whose fp32 partials meet in
 // shared memory and are added in their order, each pair finishing a part of the rows.  No sum's
 // order depends on timing.
+#include "gelu2.cuh"
 #include "gemm.cuh"
 #include "ops.h"
 
@@ -88,8 +89,14 @@ __device__ __forceinline__ void lin_chunk(const LinArgs& a, const CUtensorMap* t
         const float z0 = __uint_as_float(r[8 * q + 2 * e]) + bf16lo(bw[e]);
         const float z1 = __uint_as_float(r[8 * q + 2 * e + 1]) + bf16hi(bw[e]);
         z[4 * q + e] = pack_bf16x2(z0, z1);
-        y[4 * q + e] = pack_bf16x2(act_fwd(decltype(act)::value, z0) + bf16lo(rw[e]),
-                                   act_fwd(decltype(act)::value, z1) + bf16hi(rw[e]));
+        float y0, y1;
+        if constexpr (decltype(act)::value == ACT_GELU) {
+          gelu_f2(z0, z1, y0, y1);
+        } else {
+          y0 = act_fwd(decltype(act)::value, z0);
+          y1 = act_fwd(decltype(act)::value, z1);
+        }
+        y[4 * q + e] = pack_bf16x2(y0 + bf16lo(rw[e]), y1 + bf16hi(rw[e]));
       }
     }
   };
@@ -461,8 +468,15 @@ __global__ void __launch_bounds__(256) lin_gz_kernel(const LinGzArgs a) {
           const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            v[2 * e] *= act_grad(ACT, bf16lo(zw[e]));
-            v[2 * e + 1] *= act_grad(ACT, bf16hi(zw[e]));
+            float d0, d1;
+            if constexpr (ACT == ACT_GELU) {
+              gelu_grad_f2(bf16lo(zw[e]), bf16hi(zw[e]), d0, d1);
+            } else {
+              d0 = act_grad(ACT, bf16lo(zw[e]));
+              d1 = act_grad(ACT, bf16hi(zw[e]));
+            }
+            v[2 * e] *= d0;
+            v[2 * e + 1] *= d1;
           }
           if (r + 8 * u < r1) store8_bf16(a.gZ + (r + 8 * u) * a.N + col, v);
         }
