@@ -52,7 +52,8 @@ constexpr int kSmem = 1024 + 1024 + 6 * static_cast<int>(kTile) + 8 * static_cas
 static_assert(kSmem <= 232448, "shared memory beyond the per-CTA limit");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kDrainNs = 200000000ull;
-constexpr int kPlanThreads = 1024;
+// The plan is a chain of short steps of one block: 512 threads take 0.8 us less than 1024, whose warps wait for issue slots.
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 
 // turn; per tile: Q, O free, drain; per ring slot: K, V; per tile and ring slot (2 x + slot): their releases; per tile and
 // score buffer (2 x + buffer, which half blocks use in turn): S, P, P V done.  (Two P V may be outstanding when a
@@ -157,16 +158,16 @@ __device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {  // exclu
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    T s = warp_sums[lane];
+    T s = lane < kPlanWarps ? warp_sums[lane] : T(0);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const T y = __shfl_up_sync(0xFFFFFFFFu, s, o);
       if (lane >= o) s += y;
     }
-    warp_sums[lane] = s;
+    if (lane < kPlanWarps) warp_sums[lane] = s;
   }
   __syncthreads();
-  total = warp_sums[31];
+  total = warp_sums[kPlanWarps - 1];
   return x - v + (warp > 0 ? warp_sums[warp - 1] : T(0));
 }
 
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
   __shared__ int near_prefix[kPlanThreads];
   __shared__ long long near_at[kPlanThreads];
   __shared__ int heaviest, longest, bins[kPlanThreads];
+  __shared__ int4 near_seq[kPlanThreads];  // first query, queries, first key, keys
   const int tid = threadIdx.x, span = 2 * a.tokens;
   pdl_launch();
   if (tid == 0) heaviest = longest = 0;
@@ -187,7 +189,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
   for (int base = 0; base < a.n; base += kPlanThreads) {
     const int s = base + tid;
     int q0, qlen = 0, k0, klen;
-    if (s < a.n) seq_lengths(a, s, q0, qlen, k0, klen);
+    if (s < a.n) {
+      seq_lengths(a, s, q0, qlen, k0, klen);
+      if (near) near_seq[s] = make_int4(q0, qlen, k0, klen);
+    }
     int total;
     const int before = block_scan((qlen + span - 1) / span, sums, total);
     if (s < a.n) (near ? near_prefix : w.prefix)[s] = static_cast<int>(pairs64) + before;
@@ -213,7 +218,12 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
         if (prefix[mid] <= i) lo = mid; else hi = mid - 1;
       }
       int q0, qlen, k0, klen;
-      seq_lengths(a, lo, q0, qlen, k0, klen);
+      if (near) {
+        const int4 v = near_seq[lo];
+        q0 = v.x, qlen = v.y, k0 = v.z, klen = v.w;
+      } else {
+        seq_lengths(a, lo, q0, qlen, k0, klen);
+      }
       const int tok0 = (i - prefix[lo]) * span;
       p.q_row = q0 + tok0;
       p.qn = qlen - tok0;
@@ -237,7 +247,47 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
   __syncthreads();
   long long per = (at + a.groups - 1) / a.groups;
   if (per < 2 * kPackedMinPart + kPackedItemCost) per = 2 * kPackedMinPart + kPackedItemCost;
-  if (tid < a.groups) {
+  // Whole pairs, dealt back and forth, where the longest of the CTAs' shares is near the mean (or, of many pairs, a
+  // bound of it); a pair heavier than that decides it at once.
+  const bool few = pairs <= kPlanThreads && a.hkv <= kPlanThreads;
+  bool whole = few ? heaviest + kPackedItemCost <= per + kPackedCutCost
+                   : 2ll * heaviest <= per && static_cast<long long>(pairs) * a.hkv < (1 << 30);
+  if (whole) {
+    // heaviest first: counting sort by half blocks (the order within a bin is of no consequence)
+    int shift = 0;
+    while ((heaviest >> shift) >= kPlanThreads) ++shift;
+    for (int i = tid; i < pairs; i += kPlanThreads)
+      atomicAdd(&bins[kPlanThreads - 1 - ((i == tid ? first_eh : w.pairs[i].eh) >> shift)], 1);
+    __syncthreads();
+    int total;
+    const int start = block_scan(bins[tid], sums, total);
+    bins[tid] = start;
+    __syncthreads();
+    int* sorted = near_prefix;  // (read for the last time above)
+    for (int i = tid; i < pairs; i += kPlanThreads) {
+      const int eh = i == tid ? first_eh : w.pairs[i].eh, k = atomicAdd(&bins[kPlanThreads - 1 - (eh >> shift)], 1);
+      w.order[k] = i;
+      if (few) sorted[k] = eh;
+    }
+    __syncthreads();
+    if (few) {
+      const int grid = a.groups * a.heads_abreast;
+      const float per_head = 1.0f / static_cast<float>(a.hkv);
+      int share = 0;
+      if (tid < grid)
+        for (int t = 0;; ++t) {
+          const int i = t * grid + (t & 1 ? grid - 1 - tid : tid);
+          const int k = static_cast<int>((static_cast<float>(i) + 0.5f) * per_head);  // i / hkv, exact below 2^21
+          if (k >= pairs) break;
+          share += sorted[k] + kPackedItemCost;
+        }
+      share = __reduce_max_sync(0xFFFFFFFFu, share);
+      if ((tid & 31) == 0 && share > 0) atomicMax(&longest, share);
+      __syncthreads();
+      whole = longest <= per + kPackedCutCost;
+    }
+  }
+  if (!whole && tid < a.groups) {
     const long long lo = tid * per;
     int first = 0, last = pairs - 1;
     while (first < last) {
@@ -246,39 +296,6 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
     }
     w.starts[tid] = first;
   }
-  // heaviest first: counting sort by half blocks (the order within a bin is of no consequence)
-  int shift = 0;
-  while ((heaviest >> shift) >= kPlanThreads) ++shift;
-  for (int i = tid; i < pairs; i += kPlanThreads)
-    atomicAdd(&bins[kPlanThreads - 1 - ((i == tid ? first_eh : w.pairs[i].eh) >> shift)], 1);
-  __syncthreads();
-  int total;
-  const int start = block_scan(bins[tid], sums, total);
-  bins[tid] = start;
-  __syncthreads();
-  int* sorted = near_prefix;  // (read for the last time above)
-  for (int i = tid; i < pairs; i += kPlanThreads) {
-    const int eh = i == tid ? first_eh : w.pairs[i].eh, k = atomicAdd(&bins[kPlanThreads - 1 - (eh >> shift)], 1);
-    w.order[k] = i;
-    if (pairs <= kPlanThreads) sorted[k] = eh;
-  }
-  __syncthreads();
-  // whole pairs, dealt back and forth: the longest of the CTAs' shares, or a bound of it where there are many
-  if (pairs <= kPlanThreads) {
-    const int grid = a.groups * a.heads_abreast;
-    int share = 0;
-    if (tid < grid)
-      for (int t = 0;; ++t) {
-        const int i = t * grid + (t & 1 ? grid - 1 - tid : tid);
-        if (i / a.hkv >= pairs) break;
-        share += sorted[i / a.hkv] + kPackedItemCost;
-      }
-    share = __reduce_max_sync(0xFFFFFFFFu, share);
-    if ((tid & 31) == 0 && share > 0) atomicMax(&longest, share);
-    __syncthreads();
-  }
-  const bool whole = pairs <= kPlanThreads ? longest <= per + kPackedCutCost
-                                           : 2 * heaviest <= per && static_cast<long long>(pairs) * a.hkv < (1 << 30);
   if (tid == 0) {
     w.head->work = at;
     w.head->per = per;

@@ -167,6 +167,26 @@ def test_many_sequences(ops):
         close(o[c:c + x], ro, so, what=f"sequence {i}")
 
 
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (16, 16), (22, 11), (24, 12)])
+@pytest.mark.parametrize("few", [False, True])
+def test_long_and_short_sequences_together(ops, hq, hkv, few):
+    """One sequence far longer than the mean share, cut over many ranges that lie across the heads' groups, among short ones,
+    fewer and more than the planning block has threads."""
+    seqs = [(1, 1 + i * 7 % 60) for i in range(20 if few else 700)]
+    seqs[11:11] = [(3, 9000), (0, 4000), (1, 0)]
+    b = Batch(seqs, hq, hkv, seed=hkv, gap=1)
+    o, lse = b.run(ops)
+    assert (o[~b.own_q] == 7.0).all()
+    for i in [*range(0, 16), len(seqs) - 1]:
+        (x, y), c, s = seqs[i], b.cu[i], b.start[i]
+        ro, rl, so, sl = attend64(b.q[c:c + x], b.k[s:s + y], b.v[s:s + y], D ** -0.5)
+        close(o[c:c + x], ro, so, what=f"sequence {i}")
+        if y >= x:
+            close(lse[c:c + x], rl, sl, rounding=0, what=f"lse of sequence {i}")
+    again = b.run(ops)
+    assert torch.equal(o, again[0]) and torch.equal(lse[b.own_q], again[1][b.own_q])
+
+
 def test_same_keys_for_several_sequences(ops):
     """A shared prefix: sequences may read the same cache rows."""
     q, kv = randn(6, 4, D, seed=1), randn(500, 2, 2, D, seed=2)
