@@ -130,6 +130,24 @@ __device__ __forceinline__ void lin_chunk(const LinArgs& a, const CUtensorMap* t
   ++n_stored;
 }
 
+// Output column n of rows m0 and m1 (none if negative) from the sums with bias z and the residuals r.
+__device__ __forceinline__ void few_put(const LinFewArgs& a, int n, bool live, int m0, int m1, float z0, float z1, float r0, float r1) {
+  float y0 = z0, y1 = z1;
+  if (a.act == ACT_GELU) {
+    gelu_f2(z0, z1, y0, y1);
+  } else if (a.act == ACT_RELU) {
+    y0 = fmaxf(z0, 0.0f);
+    y1 = fmaxf(z1, 0.0f);
+  }
+  if (!live) return;
+  const uint32_t y = pack_bf16x2(y0 + r0, y1 + r1), z = pack_bf16x2(z0, z1);
+  a.Y[m0 * a.ld_y + n] = static_cast<uint16_t>(y);
+  if (a.Z) a.Z[m0 * a.ld_z + n] = static_cast<uint16_t>(z);
+  if (m1 < 0) return;
+  a.Y[m1 * a.ld_y + n] = static_cast<uint16_t>(y >> 16);
+  if (a.Z) a.Z[m1 * a.ld_z + n] = static_cast<uint16_t>(z >> 16);
+}
+
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -429,6 +447,234 @@ cudaError_t launch_linear_t(const LinMaps& m, const LinArgs& a, cudaStream_t st)
                     m.a, m.b, m.y, m.z, a);
 }
 
+// ---- The layer on few rows: bound by the bytes of W, which every SM streams through its own tensor core.  W takes the
+// place of the wide operand (a tile is `height` <= 128 of its rows; the product's other lanes read what lies behind
+// them in the ring and are not used), X that of the narrow one (M rounded up to 16), so that a step costs shared
+// memory little more than W itself, and an output column is a lane: the epilogue is one column a thread, for all
+// rows of X.  Where N gives too few tiles, the CTAs of a cluster split the reduction and send their sums to the one
+// that finishes a row (row m by CTA m % parts), which adds them in the CTAs' order.  A stage is two swizzle panels,
+// 256 contiguous bytes of each row of W: with one panel 16384 x 4096 takes 23.1 us instead of 22.2 for one row and
+// 8192 x 8192 27.4 instead of 23.4.  The kernel for many rows takes 27.1 us for one row of 16384 x 4096 with GeLU
+// (this one 22.2; W at the copy rate 19.8), 28.3 for 64 rows (25.6); 28.4 and 31.3 for 4096 x 16384 (23.5, 30.4).
+constexpr int kFewPanels = 2;  // of 64 elements of the reduction a stage
+constexpr int kFewStages = 24, kFewRing = 196608, kFewJoin = kFewRows * 128 * 4;
+constexpr int kFewSmem = 1024 + kCtrlBytes + kFewRing + kFewJoin;
+static_assert(kFewSmem <= 232448, "shared memory beyond the per-CTA limit");
+static_assert(kFewJoin >= 128 * 128, "the last stage's unused lanes read past the ring");
+
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kLinThreads, 1)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinFewArgs a) {
+  constexpr int S = kFewStages, kFull = 0, kEmpty = S, kAccFull = 2 * S, kAccEmpty = 2 * S + 2, kDrain = 2 * S + 4;
+  static_assert(8 * (kDrain + 1) <= 512, "barriers overlap the TMEM slot");
+  static_assert(2 * kFewRows <= 128, "two accumulators");
+  constexpr uint32_t kCols = 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 512);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 516);
+  const uint32_t bar0 = smem_u32(smem), stage0 = smem_u32(smem + kCtrlBytes), join = stage0 + kFewRing;
+  auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  const uint32_t stages = static_cast<uint32_t>(a.stages), stage_bytes = static_cast<uint32_t>(a.stage_bytes),
+                 w_panel = static_cast<uint32_t>(a.height) * 128u, x_panel = static_cast<uint32_t>(a.x_rows) * 128u,
+                 x_at = kFewPanels * w_panel;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = static_cast<int>(cluster_ctarank());
+  const int unit = static_cast<int>(blockIdx.x) / a.parts, units = static_cast<int>(gridDim.x) / a.parts;
+  const int k_first = part * a.k_blocks / a.parts, k_last = (part + 1) * a.k_blocks / a.parts;
+  int* err = &g_gemm_err;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i <= kDrain; ++i) mbar_init(bar(i), i >= kAccEmpty && i < kDrain ? 8 : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&tmW);
+    tma_prefetch_map(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kCols);
+    tmem_relinquish();
+  }
+  pdl_launch();
+  tc_fence_before();
+  if (a.parts > 1)
+    cluster_sync();  // the others' shared memory may be written
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+
+  if (warp == 0) {
+    // ---------------- TMA producer
+    const bool one = elect_one();
+    uint32_t s = 0, ph = 0, issued = 0;
+    bool ok = true;
+    for (int tile = unit; ok && tile < a.tiles; tile += units) {
+      for (int kb = k_first; kb < k_last; ++kb) {
+        ok = mbar_wait(bar(kEmpty + s), ph ^ 1u, abort_flag, err, a.err_site + 1);
+        if (!ok) break;
+        if (one) {
+          const uint32_t sw = stage0 + s * stage_bytes;
+          mbar_arrive_expect_tx(bar(kFull + s), stage_bytes);
+#pragma unroll
+          for (int p = 0; p < kFewPanels; ++p)
+            tma_load_3d(sw + p * w_panel, &tmW, bar(kFull + s), (kb * kFewPanels + p) * kBK, tile * a.height, 0);
+#pragma unroll
+          for (int p = 0; p < kFewPanels; ++p)
+            tma_load_3d(sw + x_at + p * x_panel, &tmX, bar(kFull + s), (kb * kFewPanels + p) * kBK, 0, 0);
+        }
+        ++issued;
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (one && !ok) drain_ring(bar(kFull), stages, issued, issued, 0);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer
+    const bool one = elect_one();
+    uint32_t s = 0, ph = 0;
+    bool ok = true;
+    const uint32_t idesc = idesc_bf16_f32(128, a.x_rows, false, false);
+    const uint64_t w_desc = sdesc_sw128(stage0, 16, 1024), x_desc = sdesc_sw128(stage0 + x_at, 16, 1024);
+    int i = 0;
+    for (int tile = unit; ok && tile < a.tiles; tile += units, ++i) {
+      const int acc = i & 1;
+      ok = mbar_wait(bar(kAccEmpty + acc), ((static_cast<uint32_t>(i) >> 1) & 1u) ^ 1u, abort_flag, err, a.err_site + 2);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kFewRows);
+      for (int kb = k_first; kb < k_last; ++kb) {
+        ok = mbar_wait(bar(kFull + s), ph, abort_flag, err, a.err_site + 3);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t off = static_cast<uint64_t>(s * stage_bytes >> 4);
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < kFewPanels * kBK / 16; ++kk)
+            umma_bf16(d, w_desc + off + (kk >> 2) * (w_panel >> 4) + (kk & 3) * 2, x_desc + off + (kk >> 2) * (x_panel >> 4) + (kk & 3) * 2,
+                      idesc, static_cast<uint32_t>(kb != k_first || kk != 0));
+          umma_commit(bar(kEmpty + s));
+        }
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (one) umma_commit(bar(kAccFull + acc));
+    }
+    if (one) umma_commit(bar(kDrain));
+    __syncwarp();
+    mbar_wait_drain(bar(kDrain), 0);
+    __syncwarp();
+  }
+  if (a.parts == 1) {
+    if (warp >= 2) {
+      // ---------------- epilogue: one output column a thread, rows of X in chunks of 16 by its two warps in turn
+      const int quarter = warp & 3, half = (warp - 2) >> 2, lane_row = quarter * 32 + lane;
+      int i = 0;
+      for (int tile = unit; tile < a.tiles; tile += units, ++i) {
+        const int acc = i & 1, n = tile * a.height + lane_row;
+        const bool live = lane_row < a.height && n < a.N;
+        const float bias = live && a.bias ? bf16lo(a.bias[n]) : 0.0f;
+        float r[16];
+        auto residual = [&](int m0) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = live && a.R && m0 + j < a.M ? bf16lo(a.R[(m0 + j) * a.ld_r + n]) : 0.0f;
+        };
+        residual(16 * half);
+        const bool ok = mbar_wait(bar(kAccFull + acc), (static_cast<uint32_t>(i) >> 1) & 1u, abort_flag, err, a.err_site + 4);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        tc_fence_after();
+        const uint32_t t = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(acc * kFewRows);
+#pragma unroll 1
+        for (int m0 = 16 * half; m0 < a.M; m0 += 32) {
+          uint32_t d[16];
+          tmem_ld16(t + static_cast<uint32_t>(m0), d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            if (m0 + j >= a.M) break;
+            few_put(a, n, live, m0 + j, m0 + j + 1 < a.M ? m0 + j + 1 : -1, __uint_as_float(d[j]) + bias, __uint_as_float(d[j + 1]) + bias,
+                    r[j], r[j + 1]);
+          }
+          if (m0 + 32 < a.M) residual(m0 + 32);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kAccEmpty + acc));
+      }
+    }
+  } else {
+    // ---------------- one tile a cluster: sums to their finishing CTAs, [part][row / parts][column]
+    const int quarter = warp & 3, half = (warp - 2) >> 2, lane_row = quarter * 32 + lane, n = unit * a.height + lane_row;
+    const int depth = (kFewRows + a.parts - 1) / a.parts;
+    const bool live = lane_row < a.height && n < a.N;
+    if (warp >= 2) {
+      const bool got = mbar_wait(bar(kAccFull), 0, abort_flag, err, a.err_site + 4);
+      if (__all_sync(0xFFFFFFFFu, got)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int m0 = 16 * half; m0 < a.M; m0 += 32) {
+          uint32_t d[16];
+          tmem_ld16(tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(m0), d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int m = m0 + j, to = m & (a.parts - 1);
+            if (m < a.M && live)
+              st_shared_cluster_f32(mapa_shared(join, static_cast<uint32_t>(to)) + static_cast<uint32_t>(((part * depth + m / a.parts) * 128 + lane_row) * 4),
+                                    __uint_as_float(d[j]));
+          }
+        }
+        tc_fence_before();
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the sums have arrived (after an abort: whatever lies there is written to Y, and the error recorded)
+    if (warp >= 2 && live) {
+      const float bias = a.bias ? bf16lo(a.bias[n]) : 0.0f;
+#pragma unroll 1
+      for (int q = 2 * half; part + q * a.parts < a.M; q += 4) {
+        const int m = part + q * a.parts, m2 = m + a.parts < a.M ? m + a.parts : -1;
+        const float r0 = a.R ? bf16lo(a.R[m * a.ld_r + n]) : 0.0f, r1 = a.R && m2 >= 0 ? bf16lo(a.R[m2 * a.ld_r + n]) : 0.0f;
+        float z0 = 0.0f, z1 = 0.0f;
+        for (int p = 0; p < a.parts; ++p) {
+          const uint32_t at = join + static_cast<uint32_t>(((p * depth + q) * 128 + lane_row) * 4);
+          z0 += ld_shared_f32(at);
+          if (m2 >= 0) z1 += ld_shared_f32(at + 512);
+        }
+        few_put(a, n, true, m, m2, z0 + bias, z1 + bias, r0, r1);
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kCols);
+  }
+}
+
 // ---- gZ = gY act'(Z) and the columns' sums of gZ (before its rounding).  A block owns 256 columns
 // and a range of rows; lane l of each of its 8 warps owns columns 8 l .. 8 l + 7.  Bound by memory: 6 bytes an
 // element.  Two rows a warp at a time and four blocks an SM: 16384 x 16384 with GeLU in 281 us (5.7 TB/s), 4096 x 8192
@@ -559,6 +805,52 @@ cudaError_t launch_linear(int kind, const LinMaps& m, LinArgs a, cudaStream_t st
     case LIN_GW: return launch_linear_t<true, true>(m, a, st);
     default: return cudaErrorInvalidValue;
   }
+}
+
+// Estimated clocks: a stage (128 of the reduction) takes about 300 + 4.5 height + 2 x_rows, all of W 1765 elements a clock
+// from memory, joining 700 + 55 a row sent and 150 a row finished.  Taller tiles with a cut reduction against lower ones
+// without, us: one row, 4096 x 4096 7.6 (four parts) / 9.0 (two) / 11.4, 4096 x 16384 23.5 / 24.5 / 37.8, 6144 x 4096
+// 11.2 (two) / 12.4; 64 rows, 6144 x 4096 16.9 (two) / 14.9, 4096 x 4096 13.5 (four) / 15.3.
+void lin_few_plan(int64_t m, int64_t n, int64_t k, LinFewArgs* a) {
+  constexpr int kClusters[3] = {152, 76, 36};  // clusters of 1, 2 and 4 CTAs that a GB300 keeps resident
+  const int64_t kb = (k + 64 * kFewPanels - 1) / (64 * kFewPanels);
+  a->k_blocks = static_cast<int32_t>(kb);
+  a->x_rows = static_cast<int32_t>((m + 15) / 16 * 16);
+  double least = 1e300;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t parts = int64_t(1) << i, most = kClusters[i];
+    if (parts > 1 && (n > most * 128 || kb < 4 * parts)) break;
+    const int64_t rounds = (n + most * 128 - 1) / (most * 128), share = (n + most * rounds - 1) / (most * rounds);
+    const int64_t height = (share + 7) / 8 * 8, tiles = (n + height - 1) / height;
+    const double steps = double(rounds * ((kb + parts - 1) / parts)), dram = double(n) * double(k) / 1765.0;
+    double cost = steps * (300 + 4.5 * double(height) + 2.0 * double(a->x_rows));
+    if (cost < dram) cost = dram;
+    if (parts > 1) cost += 700.0 + double(m) * (55.0 + 150.0 / double(parts));
+    if (cost < least) {
+      least = cost;
+      a->height = static_cast<int32_t>(height);
+      a->parts = static_cast<int32_t>(parts);
+      a->tiles = static_cast<int32_t>(tiles);
+      a->units = static_cast<int32_t>(tiles < most ? tiles : most);
+    }
+  }
+}
+
+cudaError_t launch_linear_few(const CUtensorMap& w, const CUtensorMap& x, LinFewArgs a, cudaStream_t st) {
+  if (a.units == 0) return cudaSuccess;
+  static std::atomic<bool> ready_of[kMaxDevices];  // the shared-memory opt-in, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready_of[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(linear_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    if (e != cudaSuccess) return e;
+    ready_of[dev].store(true, std::memory_order_release);
+  }
+  a.stage_bytes = kFewPanels * (a.height + a.x_rows) * 128;  // both multiples of 8 rows: swizzle atoms stay aligned
+  a.stages = kFewRing / a.stage_bytes < kFewStages ? kFewRing / a.stage_bytes : kFewStages;
+  return launch_pdl(linear_few_kernel, dim3(static_cast<unsigned>(a.parts * a.units)), dim3(kLinThreads), kFewSmem, a.parts, st, w, x, a);
 }
 
 int lin_gz_row_blocks(int64_t m, int64_t n) {

@@ -122,6 +122,22 @@ struct LinArgs {
   int64_t ld_r;
 };
 cudaError_t launch_linear(int kind, const LinMaps& m, LinArgs a, cudaStream_t st);
+// The layer on few rows (at most kFewRows): tiles of `height` rows of W, split along the reduction over `parts` CTAs of a
+// cluster, by `units` clusters.  Maps (third dimension of one, 128-byte swizzle): w in boxes of 64 x height, x in
+// boxes of 64 x x_rows.
+constexpr int kFewRows = 64;
+struct LinFewArgs {
+  int32_t M, N, k_blocks, act, err_site;
+  int32_t height, parts, tiles, units, x_rows;  // lin_few_plan
+  int32_t stages, stage_bytes;                  // set by the launcher: the operand ring
+  const uint16_t* bias;                         // nullable
+  const uint16_t* R;                            // nullable
+  uint16_t* Y;
+  uint16_t* Z;                                  // nullable
+  int64_t ld_r, ld_y, ld_z;
+};
+void lin_few_plan(int64_t m, int64_t n, int64_t k, LinFewArgs* a);
+cudaError_t launch_linear_few(const CUtensorMap& w, const CUtensorMap& x, LinFewArgs a, cudaStream_t st);
 struct LinGzArgs {
   const uint16_t* gY;
   const uint16_t* Z;  // with an activation

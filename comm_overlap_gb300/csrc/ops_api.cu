@@ -249,6 +249,26 @@ domino_status domino_linear_fwd(domino_handle H, const uint16_t* X, int64_t ld_x
     DM_TRY(dm::check_handle(H));
     if (M == 0) return DOMINO_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M <= dm::kFewRows) {
+      dm::LinFewArgs a = {};
+      a.M = int32_t(M);
+      a.N = int32_t(N);
+      a.act = act;
+      a.err_site = 0x24 << 4;
+      a.bias = bias;
+      a.R = R;
+      a.Y = Y;
+      a.Z = Z;
+      a.ld_r = ld_r;
+      a.ld_y = ld_y;
+      a.ld_z = ld_z;
+      dm::lin_few_plan(M, N, K, &a);
+      CUtensorMap w, x;
+      DM_TRY(map2(&w, 2, W, K, N, K, 64, uint32_t(a.height), 128));
+      DM_TRY(map2(&x, 2, X, K, M, ld_x, 64, uint32_t(a.x_rows), 128));
+      return dm::launch_on(H, DOMINO_K_LINEAR_FWD, st, "linear layer launch (few rows)",
+                           [&] { return dm::launch_linear_few(w, x, a, st); });
+    }
     dm::LinMaps m = {};
     dm::LinArgs a;
     DM_TRY(linear_product(&m, &a, X, ld_x, false, W, K, false, M, N, K, 0x20));

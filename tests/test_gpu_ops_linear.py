@@ -131,6 +131,50 @@ def test_backward(ops, m, n, k, act):
     assert all(torch.equal(a, b) for a, b in zip(got, ops.linear_bwd(gy, x, w, z, act)))
 
 
+# few rows: whole and cut reductions (two and four parts), tiles of every height, several rounds of tiles, all of the 16-row
+# chunks, and the first count that the kernel for many rows takes
+FEW = [(1, 8, 4096), (2, 2560, 10240), (3, 6144, 4096), (7, 20000, 264), (16, 1024, 1096), (17, 4096, 2056), (47, 9728, 520),
+       (64, 4608, 2048), (64, 6144, 1032), (50, 39000, 72), (65, 4096, 1096)]
+
+
+@pytest.mark.parametrize("m,n,k", FEW)
+@pytest.mark.parametrize("act,bias,res,save", [("gelu", True, False, True), ("none", False, True, False), ("relu", True, True, True)])
+def test_few_rows(ops, m, n, k, act, bias, res, save):
+    """Strided inputs and outputs whose other columns and rows stay as they were; junk behind X's rows."""
+    x = torch.full((m + 3, k + 8), float("nan"), dtype=torch.bfloat16, device="cuda")[:m, :k]
+    x.copy_(randn(m, k, seed=1))
+    w = randn(n, k, seed=2, std=k ** -0.5)
+    b = randn(n, seed=3) if bias else None
+    r = randn(m, n + 8, seed=4)[:, :n] if res else None
+    y, z = ops.linear_fwd(x, w, b, act, r, save=save)
+    check_fwd(x, w, b, act, r, y, z)
+    again, _ = ops.linear_fwd(x, w, b, act, r, save=save)
+    assert torch.equal(y, again)
+
+
+def test_few_rows_and_outputs_of_ones_own(ops):
+    from comm_overlap_gb300 import domino as dm
+    m, n, k = 5, 264, 520
+    x, w, r = randn(m, k, seed=1), randn(n, k, seed=2, std=0.05), randn(m, n, seed=3)
+    want, _ = ops.linear_fwd(x, w, None, "gelu", r)
+    wide = torch.full((m + 2, n + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = wide[1:m + 1, 8:n + 8]
+    y.copy_(r)  # the residual's own place
+    h = dm.domino_create()
+    dm.domino_linear_fwd(h, x, k, w, None, dm.ACT_GELU, y, wide.stride(0), y, wide.stride(0), None, 0, m, n, k, stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    dm.domino_destroy(h)
+    assert torch.equal(y, want)
+    rest = wide.clone()
+    rest[1:m + 1, 8:n + 8] = 7.0
+    assert (rest == 7.0).all()
+    # a row of NaN stays a row of NaN
+    x[2] = float("nan")
+    got, _ = ops.linear_fwd(x, w, None, "gelu", r)
+    keep = [0, 1, 3, 4]
+    assert torch.equal(got[keep], want[keep]) and torch.isnan(got[2]).all()
+
+
 def test_parts_of_the_backward(ops):
     """Each gradient alone, and accumulation into fp32 buffers."""
     m, n, k = 333, 264, 1160
