@@ -930,6 +930,7 @@ void packed_groups(PackedArgs* a, int sms) {
   while (a->hkv % a->heads_abreast != 0) --a->heads_abreast;
   a->subgroups = a->hkv / a->heads_abreast;
   a->groups = (sms < kSms ? sms : kSms) / a->heads_abreast;
+  if (a->groups < 1) a->groups = 1;
 }
 
 cudaError_t launch_packed_plan(const PackedArgs& a, void* ws, cudaStream_t st) {

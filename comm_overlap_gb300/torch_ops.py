@@ -337,7 +337,7 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     query sees all of them, the one before all but the last, and so on (int32 tensors on the device, of n + 1,
     n and n values).  Without k_start and k_len the keys are the sequence's own rows, as in prompts.  The scale
     is 1 / sqrt(128) unless given.  Returns o, or (o, lse) with lse [tq, heads] fp32.  Rows that belong to no
-    sequence are left as they were in `out` (undefined without it).  Lengths that leave the tensors are not
+    sequence are left as they were in `out` (undefined without it), which may not overlap q, k or v.  Lengths that leave the tensors are not
     raised here: they are read on the device, and `device_status` reports them.  Forward only."""
     for name, x in (("q", q), ("k", k), ("v", v)):
         _check(name, x, q)

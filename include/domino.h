@@ -301,6 +301,7 @@ DOMINO_API domino_status domino_layernorm_bwd(domino_handle handle, const uint16
  *   X: M x K (row stride ld_x); W: N x K, contiguous (nn.Linear [out, in]); bias (nullable): N;
  *   R (nullable, the residual): M x N (row stride ld_r); Y: M x N (row stride ld_y; may be R).
  *   Z (nullable): M x N (row stride ld_z), the pre-activation that domino_linear_bwd needs.
+ * Otherwise Y and Z may not overlap the inputs or one another.
  * bf16 operands, fp32 accumulation; bias, activation and residual are applied in fp32 and Y and Z are
  * each rounded once.  act: NONE, RELU or GELU.  N and K are multiples of 8, at most 2^20; M >= 0.
  * The order of every sum depends on the sizes alone: equal inputs give equal bits. */
@@ -316,6 +317,7 @@ DOMINO_API domino_status domino_linear_fwd(domino_handle handle, const uint16_t*
  *   gW_main += gZ^T . X             (N x K fp32, the main_grad buffer; nullable)
  *   gbias = sum over rows of gZ     (N fp32, unrounded gZ; nullable), added to the buffer with
  *                                   accumulate = 1.
+ * gX, gW, gW_main and gbias may not overlap the inputs or one another.
  * Z is what the forward kept (unused with act = NONE); W is needed for gX, X for gW.  Workspace:
  * domino_linear_bwd_workspace_size() bytes. */
 DOMINO_API domino_status domino_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int32_t act,
@@ -337,9 +339,9 @@ DOMINO_API domino_status domino_linear_bwd(domino_handle handle, const uint16_t*
  *   O = softmax(scale Q K^T over the keys a query sees) V, P rounded to bf16 for its product, O once from
  *      fp32.  lse (nullable): tq x heads fp32, the logarithm of each softmax's denominator.  A query that
  *      sees no key (k_len < its position's need, or 0) gets zeros and -inf.
- * Rows of K and V outside a sequence's keys, and their values, have no effect on it.  Within a sequence a
- * NaN or infinity in V at a position that a query does not see may still reach it as NaN (0 x inf) when it
- * is in the query's last block of 128 keys.  Rows of O and lse that belong to no sequence keep what they
+ * Rows of K and V outside a sequence's keys, and their values, have no effect on it, nor has K at positions
+ * that a query does not see.  A NaN or infinity in V fewer than 192 positions after a query's own may still
+ * reach it as NaN (0 x inf).  Rows of O and lse that belong to no sequence keep what they
  * held.  Lengths are read on the device: a sequence whose rows leave the tensors is skipped and recorded
  * (domino_device_status gives DOMINO_ERR_INVALID_ARG); query rows shared by two sequences have undefined
  * results.  Equal inputs give equal bits.  O may not overlap Q, K or V.

@@ -187,6 +187,25 @@ def test_long_and_short_sequences_together(ops, hq, hkv, few):
     assert torch.equal(o, again[0]) and torch.equal(lse[b.own_q], again[1][b.own_q])
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 1)])
+@pytest.mark.parametrize("cached", [0, 1500])
+def test_nonfinite_keys_that_a_query_does_not_see(ops, hq, hkv, cached):
+    """Junk in K from a position on leaves the queries before it alone; junk in V those 192 and more before it."""
+    n, at = 700, 600
+    b = Batch([(n, cached + n)], hq, hkv, seed=21, junk=False)
+    clean, _ = b.run(ops)
+    c, s = b.cu[0], b.start[0] + cached
+    for t, reach in ((b.k, 0), (b.v, 191)):
+        keep = t[s + at:s + at + 40].clone()
+        for bad in (float("nan"), float("inf"), -float("inf")):
+            t[s + at:s + at + 40:3] = bad
+            o, _ = b.run(ops)
+            assert torch.equal(o[c:c + at - reach], clean[c:c + at - reach])
+            if bad != bad:
+                assert torch.isnan(o[c + at:c + n].float()).any(-1).all()
+        t[s + at:s + at + 40] = keep
+
+
 def test_same_keys_for_several_sequences(ops):
     """A shared prefix: sequences may read the same cache rows."""
     q, kv = randn(6, 4, D, seed=1), randn(500, 2, 2, D, seed=2)
