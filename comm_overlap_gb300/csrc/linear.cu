@@ -4,9 +4,9 @@
 // pass of the backward (gZ = gY act'(Z), bias gradient).
 //
 // The product runs on CTA pairs (tcgen05.mma.cta_group::2, tiles of 256 rows and `width` columns, 64
-// elements of the reduction a step through a 5-stage TMA ring):
-//   warp 0 (one lane)  TMA producer of this CTA's 128 rows of A and its width / 2 rows of B
-//   warp 1 (one lane of the leader)  MMA issuer, two 256-column accumulators in TMEM
+// elements of the reduction a step through a TMA ring of five stages or more):
+//   warp 0 (an elected lane)  TMA producer of this CTA's 128 rows of A and its width / 2 rows of B
+//   warp 1 (an elected lane of the leader)  MMA issuer, two 256-column accumulators in TMEM
 //   warps 2-9          epilogue, two per TMEM lane quarter taking alternate 32-column chunks, one row a
 //                      thread
 // The launcher lays the work over the GPU (lin_plan): pairs take tiles unit, unit + units, ...; the width
@@ -14,6 +14,10 @@
 // also cut along the reduction over the 2 or 4 pairs of a larger cluster, whose fp32 partials meet in
 // shared memory and are added in their order, each pair finishing a part of the rows.  No sum's
 // order depends on timing.
+//
+// Bound: the tensor core.  16384 x 16384 -> 4096 takes 1140 - 1250 us (0.91 - 1.0 of the measured burst rate; the power
+// cap decides), 777 x 2560 -> 10240 with GeLU and its pre-activation 39 us (21 at the burst rate): its last tile of
+// rows is three quarters padding, and tiles narrower than 256 run the tensor core below its rate (lin_plan).
 #include "gelu2.cuh"
 #include "gemm.cuh"
 #include "ops.h"
@@ -769,7 +773,9 @@ __global__ void __launch_bounds__(256) lin_gbias_kernel(const float* __restrict_
 }  // namespace
 
 // Estimated clocks of a product: a step of the reduction takes about 250 + 1.25 width (measured over two rounds
-// of 152 tiles with 32 and 64 steps: 333 at 64 columns, 399 at 128, 488 at 192, 575 at 256), a round's change
+// of 152 tiles with 32 and 64 steps: 333 at 64 columns, 399 at 128, 488 at 192, 575 at 256; the arithmetic takes 2
+// width.  L2 is not what slows narrow tiles: two pairs that shared their rows of A by multicast loads took the
+// same time), a round's change
 // of tiles 8 and the last epilogue 20 a column, the start 4500, and joining cut reductions as below.  The
 // choices it makes are within 5 % of the best of all widths and cuts at the shapes tried.
 LinPlan lin_plan(int64_t m, int64_t n, int64_t k) {

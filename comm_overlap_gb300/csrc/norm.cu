@@ -7,7 +7,9 @@
 // bias gradients in registers over all rows of the team.  Teams walk the rows with a fixed stride;
 // the next row's pieces are loaded before the current row is reduced, which keeps memory busy across
 // the reductions.  All arithmetic is fp32; the one rounding to bf16 is the output's.
-// Bound: memory (forward 4 bytes, backward 6, with a residual gradient 8 bytes an element).
+// Bound: memory (forward 4 bytes, backward 6, with a residual gradient 8 bytes an element).  32768 x 4096: forward 90 us
+// (79 at the copy rate), backward with a residual gradient 183 (158); 1237 x 2560 backward 12.8 (3.7: two launches and the
+// latency of a few rows a team); one row of 4096 forward 2.3.
 #include <atomic>
 
 #include "actfn.cuh"
