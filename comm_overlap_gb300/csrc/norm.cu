@@ -8,7 +8,7 @@
 // the next row's pieces are loaded before the current row is reduced, which keeps memory busy across
 // the reductions.  All arithmetic is fp32; the one rounding to bf16 is the output's.
 // Bound: memory (forward 4 bytes, backward 6, with a residual gradient 8 bytes an element).  32768 x 4096: forward 90 us
-// (79 at the copy rate), backward with a residual gradient 183 (158); 1237 x 2560 backward 12.8 (3.7: two launches and the
+// (79 at the copy rate), backward with a residual gradient 158 (158); 1237 x 2560 backward 11.7 (3.7: two launches and the
 // latency of a few rows a team); one row of 4096 forward 2.3.
 #include <atomic>
 
@@ -171,16 +171,26 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
 // bandwidth; the same copies without arithmetic take 86 us).
 __device__ int g_norm_err;
 
-__device__ __forceinline__ void bulk_load_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  mbar_arrive_expect_tx(bar, bytes);
+__device__ __forceinline__ void bulk_copy_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                : "memory");
+}
+__device__ __forceinline__ void bulk_load_row(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, bytes);
+  bulk_copy_row(dst, src, bytes, bar);
 }
 __device__ __forceinline__ void bulk_store_row(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(src),
                "r"(bytes)
                : "memory");
+}
+
+// After a wait that ran out: copies that other waits were for land before the block leaves.
+__device__ __forceinline__ void land_copies() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 100000ull) {
+  }
 }
 
 constexpr int kStreamMaxWarps = 16, kStreamMaxDepth = 3;
@@ -341,6 +351,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps) ln_fwd_stream_kernel(con
     }
   }
   if (tt == 0) bulk_wait_group_all();
+  if (*abort_flag) land_copies();
   __syncwarp();
 }
 
@@ -484,6 +495,180 @@ __global__ void __launch_bounds__(kTeamThreads) ln_bwd_kernel(const LnBwdArgs a,
   }
 }
 
+// ---- backward of many rows: as the forward's, teams of `wpr` warps stream gY, X and the residual's gradient (`ops` rows
+// a buffer set) through `depth` buffer sets of their own; a thread keeps its columns' sums (NPT pieces of eight) in
+// registers over all rows of its team.  Same arithmetic as ln_bwd_kernel up to the order of the sums.  Sixteen warps of
+// up to 128 registers: as few a row as four pieces a thread allow, because a row's reduction costs more than its
+// arithmetic (26715 x 4096: 115 us; with 24 warps of at most two pieces 162; with 8 of at most eight 114, but 59 instead
+// of 36 at 1024 columns).  32768 x 4096 with a residual's gradient 158 us, which is the copy rate; teams 183.
+template <int NPT>
+__global__ void __launch_bounds__(32 * kStreamMaxWarps)
+    ln_bwd_stream_kernel(const LnBwdArgs a, float* __restrict__ part, const int depth, const int wpr) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, teams = (blockDim.x >> 5) / wpr;
+  const int team = warp / wpr, wt = warp - team * wpr, tt = wt * 32 + lane, width = wpr * 32;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.h) * 2u, pitch = (row_bytes + 127u) & ~127u;
+  const uint32_t ops = a.gres ? 3u : 2u, set = ops * pitch;
+  const uint32_t bar0 = smem_u32(smem) + static_cast<uint32_t>(team * kStreamMaxDepth) * 8u;
+  float2* joint = reinterpret_cast<float2*>(smem + 512);  // a warp's sums of u and u n
+  const uint32_t sg = smem_u32(smem) + kStreamCtrl, ring = sg + pitch;
+  const uint32_t buf0 = ring + static_cast<uint32_t>(team * depth) * set;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kStreamCtrl - 4);
+  if (tt == 0) {
+    for (int d = 0; d < depth; ++d) mbar_init(bar0 + 8u * d, 1);
+    if (team == 0) *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_launch();
+  pdl_wait();
+  const int nv = static_cast<int>(a.h >> 3);
+  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+    const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.gamma) + v);
+    st_shared_v4(sg + 16u * v, g.x, g.y, g.z, g.w);
+  }
+  __syncthreads();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * teams, r0 = static_cast<int64_t>(blockIdx.x) * teams + team;
+  auto load = [&](int64_t r, int d) {
+    const uint32_t buf = buf0 + static_cast<uint32_t>(d) * set, bar = bar0 + 8u * d;
+    mbar_arrive_expect_tx(bar, ops * row_bytes);
+    bulk_copy_row(buf, a.gY + r * a.ld_gy, row_bytes, bar);
+    bulk_copy_row(buf + pitch, a.X + r * a.ld_x, row_bytes, bar);
+    if (a.gres) bulk_copy_row(buf + 2 * pitch, a.gres + r * a.ld_gres, row_bytes, bar);
+  };
+  if (tt == 0)
+    for (int d = 0; d < depth; ++d)
+      if (r0 + d * stride < a.rows) load(r0 + d * stride, d);
+  auto team_sync = [&] {
+    if (wpr > 1)
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(width) : "memory");
+    else
+      __syncwarp();
+  };
+  const float inv_h = 1.0f / static_cast<float>(a.h);
+  uint64_t ag[NPT][4], ab[NPT][4];
+#pragma unroll
+  for (int i = 0; i < NPT; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ag[i][e] = ab[i][e] = 0;
+  float mean = 0.0f, rstd = 0.0f;
+  if (r0 < a.rows) {
+    mean = __ldg(a.mean + r0);
+    rstd = __ldg(a.rstd + r0);
+  }
+  int d = 0;
+  uint32_t phase = 0;
+  for (int64_t r = r0; r < a.rows; r += stride) {
+    const uint32_t buf = buf0 + static_cast<uint32_t>(d) * set;
+    const bool more = r + stride < a.rows;
+    const float nmean = more ? __ldg(a.mean + r + stride) : 0.0f, nrstd = more ? __ldg(a.rstd + r + stride) : 0.0f;
+    const uint64_t neg = f2(-mean, -mean), scale = f2(rstd, rstd);
+    // (a wait that runs out raises the abort flag; the rows after it are neither loaded nor stored)
+    const bool ok = mbar_wait(bar0 + 8u * d, phase, abort_flag, &g_norm_err, 0x251);
+    uint64_t su = 0, sun = 0;
+#pragma unroll
+    for (int i = 0; i < NPT; ++i) {
+      const int v = tt + i * width;
+      if (v >= nv) continue;
+      uint64_t g[4], x[4], m[4];
+      unpack8(ld_shared_v4(buf + 16u * v), g);
+      unpack8(ld_shared_v4(buf + pitch + 16u * v), x);
+      unpack8(ld_shared_v4(sg + 16u * v), m);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t n = mul_f2(add_f2(x[e], neg), scale), u = mul_f2(g[e], m[e]);
+        su = add_f2(su, u);
+        sun = fma_f2(u, n, sun);
+        ag[i][e] = fma_f2(g[e], n, ag[i][e]);
+        ab[i][e] = add_f2(ab[i][e], g[e]);
+      }
+    }
+    float2 s;
+    {
+      float lo, hi;
+      f2_split(su, lo, hi);
+      s.x = lo + hi;
+      f2_split(sun, lo, hi);
+      s.y = lo + hi;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+      s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+    }
+    if (wpr > 1) {
+      if (lane == 0) joint[warp] = s;
+      team_sync();
+      s = joint[team * wpr];
+      for (int w = 1; w < wpr; ++w) {
+        const float2 o = joint[team * wpr + w];
+        s.x += o.x;
+        s.y += o.y;
+      }
+    }
+    const float mu = s.x * inv_h, mun = s.y * inv_h;
+    const uint64_t nmu = f2(-mu, -mu), nmun = f2(-mun, -mun);
+    uint4* out = reinterpret_cast<uint4*>(a.gX + r * a.ld_gx);
+#pragma unroll
+    for (int i = 0; i < NPT; ++i) {
+      const int v = tt + i * width;
+      if (v >= nv) continue;
+      uint64_t g[4], x[4], m[4], z[4] = {0, 0, 0, 0};
+      unpack8(ld_shared_v4(buf + 16u * v), g);
+      unpack8(ld_shared_v4(buf + pitch + 16u * v), x);
+      unpack8(ld_shared_v4(sg + 16u * v), m);
+      if (a.gres) unpack8(ld_shared_v4(buf + 2 * pitch + 16u * v), z);
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t n = mul_f2(add_f2(x[e], neg), scale), u = mul_f2(g[e], m[e]);
+        float lo, hi;
+        f2_split(fma_f2(scale, fma_f2(n, nmun, add_f2(u, nmu)), z[e]), lo, hi);
+        y[e] = pack_bf16x2(lo, hi);
+      }
+      if (ok) out[v] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    team_sync();  // the buffers and the joint sums are read
+    if (tt == 0 && ok && !*abort_flag && r + depth * stride < a.rows) load(r + depth * stride, d);
+    mean = nmean;
+    rstd = nrstd;
+    if (++d == depth) {
+      d = 0;
+      phase ^= 1u;
+    }
+  }
+  if (*abort_flag) land_copies();
+  // the teams' sums in team order
+  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * a.h;
+  float* cols = teams == 1 ? out : reinterpret_cast<float*>(smem + kStreamCtrl + pitch);
+  __syncthreads();  // every team is done with the ring
+#pragma unroll
+  for (int i = 0; i < NPT; ++i) {
+    const int c = (tt + i * width) * 8;
+    if (c >= a.h) continue;
+    float* to = cols + static_cast<int64_t>(team) * 2 * a.h + c;
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      float4 s;
+      f2_split(ag[i][e], s.x, s.y);
+      f2_split(ag[i][e + 1], s.z, s.w);
+      *reinterpret_cast<float4*>(to + 2 * e) = s;
+      f2_split(ab[i][e], s.x, s.y);
+      f2_split(ab[i][e + 1], s.z, s.w);
+      *reinterpret_cast<float4*>(to + a.h + 2 * e) = s;
+    }
+  }
+  if (teams == 1) return;
+  __syncthreads();
+  for (int64_t c = threadIdx.x * 4; c < 2 * a.h; c += blockDim.x * 4) {
+    float4 s = *reinterpret_cast<const float4*>(cols + c);
+    for (int k = 1; k < teams; ++k) {
+      const float4 o = *reinterpret_cast<const float4*>(cols + k * 2 * a.h + c);
+      s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+    }
+    *reinterpret_cast<float4*>(out + c) = s;
+  }
+}
+
 // Column sums of `parts` rows of 2 h floats, in a fixed order: 32 groups of rows per block, then the
 // groups in order.  Columns 0 .. h-1 go to ggamma, the others to gbeta (nullable).
 __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__ part, int parts, int64_t h,
@@ -519,16 +704,32 @@ __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__
 }
 
 constexpr int kMaxSmem = 232448;  // a CTA's
-// Rows are streamed from 768 columns and 2.2 M values on: at 1024 columns the two cross at about 1800 rows (3.2 us
-// teams, 4.3 streamed at 1216; 5.5 and 4.3 at 2432), at 4096 at 650 (11.0 and 6.5 at 1216); at 512 columns teams
-// stay ahead (20.9 and 27.8 us at 32768 rows).
-constexpr int64_t kStreamMinH = 768, kStreamMinValues = 2200000;
+// Forward: a row of up to 1024 columns is one warp's where there are rows to fill the GPU so (no barrier; 26715 rows of
+// 584: 18.3 us, with three warps a row 29.4, streamed 24.8; of 1024: 25.7, 32.6, 27.3), but several warps' where there
+// are few (64 rows of 904: 2.0 us, one warp a row 2.4).  Wider rows are streamed from 2.2 M values on: at 4096 columns
+// the two cross at 650 rows (11.0 and 6.5 us at 1216), at 1200 at 1800 (1000 rows: 3.3, streamed 4.4; 6648: 15.4 and 10.3).
+constexpr int64_t kNarrowMinRows = 512, kStreamMinH = 1032, kStreamMinValues = 2200000;
+// Backward: streamed from 1 M values on.  Teams and streamed, us, without a residual's gradient: 26715 rows of 584 41 and
+// 27, of 1576 82 and 60, of 2056 116 and 70, of 4096 127 and 115; 1000 rows of 1576 8.6 and 8.2, of 4096 12.5 and 12.4;
+// 8 rows of 1576 5.0 and 6.8.
+constexpr int64_t kStreamBwdMinValues = 1000000;
 int pieces_per_thread(int64_t h) { return h <= 2048 ? 1 : (h <= 8192 ? 2 : 4); }
 int team_threads(int64_t h, int npt) { return static_cast<int>(((h / 8 + npt - 1) / npt + 31) / 32 * 32); }
 
 }  // namespace
 
+namespace {
+bool ln_bwd_streams(int64_t rows, int64_t h) { return rows * h >= kStreamBwdMinValues; }
+// warps a row: at most four pieces of eight columns a thread
+int stream_bwd_warps(int64_t h) { return static_cast<int>((h + 1023) / 1024); }
+}  // namespace
+
 int ln_bwd_blocks(int64_t rows, int64_t h, int sms) {
+  if (ln_bwd_streams(rows, h)) {
+    const int teams = kStreamMaxWarps / stream_bwd_warps(h);
+    const int64_t need = (rows + teams - 1) / teams;
+    return static_cast<int>(need < sms ? need : sms);
+  }
   const int tpr = team_threads(h, pieces_per_thread(h)), teams = tpr >= 256 ? 1 : 256 / tpr;
   const int64_t need = (rows + 4 * teams - 1) / (4 * teams), most = 2 * int64_t(sms);
   return static_cast<int>(need < most ? need : most);
@@ -560,15 +761,44 @@ cudaError_t launch_ln_fwd_stream(const LnFwdArgs& a, int sms, cudaStream_t st) {
 cudaError_t launch_ln_fwd(const LnFwdArgs& a, int sms, cudaStream_t st) {
   if (a.rows == 0) return cudaSuccess;
   if (a.h >= kStreamMinH && a.rows * a.h >= kStreamMinValues) return launch_ln_fwd_stream(a, sms, st);
-  const int npt = pieces_per_thread(a.h), tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
+  const int npt = a.rows < kNarrowMinRows ? pieces_per_thread(a.h) : a.h <= 1024 ? static_cast<int>((a.h + 255) / 256)
+                                                                  : a.h <= 2048 ? 4 : pieces_per_thread(a.h);
+  const int tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
   const int64_t need = (a.rows + teams - 1) / teams, most = int64_t(sms) * (2048 / (teams * tpr));
   const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(static_cast<unsigned>(teams * tpr));
-  return launch_pdl(npt == 1 ? ln_fwd_kernel<1, true> : npt == 2 ? ln_fwd_kernel<2, true> : ln_fwd_kernel<4, true>, grid, block, 0, 1, st, a, tpr);
+  const auto fn = npt == 1 ? ln_fwd_kernel<1, true> : npt == 2 ? ln_fwd_kernel<2, true> : npt == 3 ? ln_fwd_kernel<3, true> : ln_fwd_kernel<4, true>;
+  return launch_pdl(fn, grid, block, 0, 1, st, a, tpr);
 }
+
+namespace {
+cudaError_t launch_ln_bwd_stream(const LnBwdArgs& a, float* part, int grid, cudaStream_t st) {
+  const int wpr = stream_bwd_warps(a.h), teams = kStreamMaxWarps / wpr;
+  const int npt = static_cast<int>((a.h / 8 + 32 * wpr - 1) / (32 * wpr));
+  const auto fn = npt == 1 ? ln_bwd_stream_kernel<1> : npt == 2 ? ln_bwd_stream_kernel<2> : npt == 3 ? ln_bwd_stream_kernel<3>
+                                                                                                 : ln_bwd_stream_kernel<4>;
+  static std::atomic<bool> ready_of[4][kMaxDevices];  // the shared-memory opt-in, per instance and device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready_of[npt - 1][dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    ready_of[npt - 1][dev].store(true, std::memory_order_release);
+  }
+  // two buffer sets always fit (at most 16384 columns a set), and hold the teams' sums at the end
+  const int64_t pitch = (a.h * 2 + 127) / 128 * 128, set = pitch * (a.gres ? 3 : 2) * teams;
+  const int64_t fit = (kMaxSmem - kStreamCtrl - pitch) / set;
+  const int depth = static_cast<int>(fit < kStreamMaxDepth ? fit : kStreamMaxDepth);
+  return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(32 * wpr * teams)), size_t(kStreamCtrl + pitch + depth * set), 1, st, a,
+                    part, depth, wpr);
+}
+}  // namespace
 
 cudaError_t launch_ln_bwd(const LnBwdArgs& a, float* part, int sms, cudaStream_t st) {
   const int grid = ln_bwd_blocks(a.rows, a.h, sms);
   if (grid == 0) return cudaSuccess;
+  if (ln_bwd_streams(a.rows, a.h)) return launch_ln_bwd_stream(a, part, grid, st);
   const int npt = pieces_per_thread(a.h), tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
   // several teams only for h <= 1024 (at most 8 teams x 2 h floats with teams x h <= 2048)
   const size_t smem = teams > 1 ? size_t(teams) * 2 * a.h * 4 : 0;

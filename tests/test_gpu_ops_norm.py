@@ -104,6 +104,59 @@ def test_backward(ops, rows, h, res):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+# many rows: one warp a row with one to four pieces a thread, two to sixteen warps a row, uneven last pieces, blocks with
+# spare warps, rows that do not divide among the teams
+MANY = [(8003, 136), (2100, 512), (3000, 760), (1200, 904), (701, 1576), (640, 2048), (501, 2056), (2500, 2560), (300, 4096),
+        (211, 5000), (130, 8200), (70, 16384)]
+
+
+@pytest.mark.parametrize("rows,h", MANY)
+@pytest.mark.parametrize("res", [True, False])
+def test_many_rows(ops, rows, h, res):
+    """Forward and backward of strided rows; sums added to buffers; junk between the rows."""
+    def strided(seed, **kw):
+        wide = torch.full((rows, h + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, :h] = randn(rows, h, seed=seed, **kw)
+        return wide[:, :h]
+
+    x, gy, w, b = strided(1, mean=0.5), strided(4), randn(h, seed=2, std=0.2, mean=1.0), randn(h, seed=3)
+    gres = strided(5) if res else None
+    fwd = ops.layer_norm_fwd(x, w, b)
+    check_fwd(x, w, b, 1e-5, fwd)
+    start = (randn(h, seed=6, dtype=torch.float32), randn(h, seed=7, dtype=torch.float32))
+    grads = tuple(t.clone() for t in start)
+    got = ops.layer_norm_bwd(gy, x, w, *fwd[1:], gres, grads=grads)
+    check_bwd(gy, x, w, *fwd[1:], gres, got, start)
+    plain = ops.layer_norm_bwd(gy, x, w, *fwd[1:], gres)
+    check_bwd(gy, x, w, *fwd[1:], gres, plain)
+    again = ops.layer_norm_bwd(gy, x, w, *fwd[1:], gres)
+    assert all(torch.equal(p, q) for p, q in zip(plain, again))
+
+
+def test_many_rows_in_place_and_apart(ops):
+    """gX in the place of gY or of the residual's gradient; a row of NaN leaves the other rows' gX alone."""
+    from comm_overlap_gb300 import domino as dm
+    rows, h = 900, 1576
+    x, gy, gres, w = (randn(rows, h, seed=i, mean=0.1) for i in (1, 2, 3, 4))
+    w = w[0].contiguous()
+    _, mean, rstd = ops.layer_norm_fwd(x, w)
+    want = ops.layer_norm_bwd(gy, x, w, mean, rstd, gres)
+    handle, stream = dm.domino_create(), torch.cuda.current_stream().cuda_stream
+    n = dm.domino_layernorm_bwd_workspace_size(rows, h)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for own in range(2):
+        g, r, gw, gb = gy.clone(), gres.clone(), torch.empty(h, device="cuda"), torch.empty(h, device="cuda")
+        gx = (g, r)[own]
+        dm.domino_layernorm_bwd(handle, g, h, x, h, w, mean, rstd, r, h, gx, h, gw, gb, 0, rows, h, ws, n, stream)
+        torch.cuda.synchronize()
+        assert torch.equal(gx, want[0]) and torch.equal(gw, want[1]) and torch.equal(gb, want[2])
+    dm.domino_destroy(handle)
+    gy[17] = float("nan")
+    got = ops.layer_norm_bwd(gy, x, w, mean, rstd, gres)
+    keep = torch.arange(rows, device="cuda") != 17
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.isnan(got[0][17]).all() and torch.isnan(got[1]).all()
+
+
 def test_strided_rows_and_accumulation(ops):
     rows, h = 37, 520
     wide, gwide = randn(rows, 3 * h, seed=1), randn(rows, 2 * h, seed=2)

@@ -57,8 +57,10 @@ def test_layernorm_backward(kw, code):
 
 def test_layernorm_workspace_size():
     assert dm.domino_layernorm_bwd_workspace_size(0, 64) == 0
-    # no more partial rows than two per SM, and never more rows than inputs
-    assert dm.domino_layernorm_bwd_workspace_size(1 << 20, 4096) == 304 * 2 * 4096 * 4
+    # a partial row per SM for many rows, no more than two per SM otherwise, and never more rows than inputs
+    assert dm.domino_layernorm_bwd_workspace_size(1 << 20, 4096) == 152 * 2 * 4096 * 4
+    assert all(0 < dm.domino_layernorm_bwd_workspace_size(rows, h) <= min(rows, 304) * 2 * h * 4
+               for rows in (1, 7, 300, 5000) for h in (8, 512, 2056, 16384))
     assert dm.domino_layernorm_bwd_workspace_size(1, 4096) == 2 * 4096 * 4
     assert status(dm.domino_layernorm_bwd_workspace_size, rows=1, h=12) == ALIGNMENT
 
