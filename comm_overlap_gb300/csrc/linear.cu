@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(256, 4) lin_gz_kernel(const LinGzArgs a) {
             v[2 * e] *= d0;
             v[2 * e + 1] *= d1;
           }
-          if (r + 8 * u < r1) store8_bf16(a.gZ + (r + 8 * u) * a.N + col, v);
+          if (r + 8 * u < r1) store8_bf16(a.gZ + (r + 8 * u) * a.ld_gz + col, v);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += v[e];

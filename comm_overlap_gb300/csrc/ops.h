@@ -141,9 +141,9 @@ cudaError_t launch_linear_few(const CUtensorMap& w, const CUtensorMap& x, LinFew
 struct LinGzArgs {
   const uint16_t* gY;
   const uint16_t* Z;  // with an activation
-  uint16_t* gZ;       // with an activation; contiguous
+  uint16_t* gZ;       // with an activation
   float* part;        // nullable: lin_gz_row_blocks() rows of N floats
-  int64_t M, N, ld_gy, ld_z;
+  int64_t M, N, ld_gy, ld_z, ld_gz;
   int32_t act;
 };
 int lin_gz_row_blocks(int64_t m, int64_t n);
