@@ -152,6 +152,22 @@ def test_few_rows(ops, m, n, k, act, bias, res, save):
     assert torch.equal(y, again)
 
 
+# rows of both operands that begin between 128-byte lines: pairs of tiles side by side, an odd count of tiles in either
+# direction, one to several rounds, fewer steps than the ring has stages, rows in the second half of the last tile alone
+@pytest.mark.parametrize("m,n,k", [(129, 520, 72), (400, 264, 1032), (385, 2568, 2568), (777, 2568, 520), (1300, 4104, 1032),
+                                   (5000, 1544, 328), (2049, 8200, 200)])
+@pytest.mark.parametrize("act", ["gelu", "none"])
+def test_rows_between_lines(ops, m, n, k, act):
+    x, w = randn(m, k, seed=1), randn(n, k, seed=2, std=k ** -0.5)
+    b, r, gy = randn(n, seed=3), randn(m, n, seed=4), randn(m, n, seed=5)
+    y, z = ops.linear_fwd(x, w, b, act, None if act == "gelu" else r, save=act == "gelu")
+    check_fwd(x, w, b, act, None if act == "gelu" else r, y, z)
+    got = ops.linear_bwd(gy, x, w, z, act)
+    check_bwd(gy, x, w, z, act, *got)
+    assert torch.equal(y, ops.linear_fwd(x, w, b, act, None if act == "gelu" else r)[0])
+    assert all(torch.equal(p, q) for p, q in zip(got, ops.linear_bwd(gy, x, w, z, act)))
+
+
 def test_few_rows_and_outputs_of_ones_own(ops):
     from comm_overlap_gb300 import domino as dm
     m, n, k = 5, 264, 520
