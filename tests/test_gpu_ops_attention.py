@@ -206,6 +206,21 @@ def test_nonfinite_keys_that_a_query_does_not_see(ops, hq, hkv, cached):
         t[s + at:s + at + 40] = keep
 
 
+def test_offsets_beyond_32_bits(ops):
+    """A cache whose rows pass 2^31 values and 2^32 bytes."""
+    tk, hkv, hq = 2300000, 8, 32
+    k, v = (torch.randn(tk, hkv, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    starts, lens = [0, 1048570, 2097140, 2099000, tk - 1000], [700, 40, 900, 3000, 1000]
+    q = randn(len(starts), hq, D, seed=1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o, lse = ops.packed_attention(q, k, v, torch.arange(len(starts) + 1, **i32), torch.tensor(starts, **i32),
+                                  torch.tensor(lens, **i32), return_lse=True)
+    for s, (a, n) in enumerate(zip(starts, lens)):
+        ro, rl, so, sl = attend64(q[s:s + 1], k[a:a + n], v[a:a + n], D ** -0.5)
+        close(o[s:s + 1], ro, so, what=f"O of sequence {s}")
+        close(lse[s:s + 1], rl, sl, rounding=0, what=f"lse of sequence {s}")
+
+
 def test_same_keys_for_several_sequences(ops):
     """A shared prefix: sequences may read the same cache rows."""
     q, kv = randn(6, 4, D, seed=1), randn(500, 2, 2, D, seed=2)

@@ -124,6 +124,34 @@ def test_serving_block(ops, hq, hkv):
         cached = [c + 1 for c in cached]
 
 
+def test_two_captured_steps_at_once(ops):
+    """Two captured steps of two blocks, replayed on two streams at the same time, and an eager one beside them."""
+    runs = []
+    for i in range(2):
+        block = Block(ops, 4, 2, 1032, 3, 2000)
+        queries, cached = [1, 1, 1], [1500 - i, 7, 1900]
+        block.k[:], block.v[:] = randn(*block.k.shape, seed=40 + i), randn(*block.v.shape, seed=50 + i)
+        rows, cu, start, length = block.lengths(queries, cached)
+        x = randn(3, block.h, seed=60 + i)
+        block.step(x, rows, cu, start, length)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = block.step(x, rows, cu, start, length)
+        want = {name: t.clone() for name, t in block.step(x, rows, cu, start, length).items()}
+        runs.append((block, graph, held, want, (x, rows, cu, start, length), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _, graph, _, _, _, stream in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        eager = runs[0][0].ops.linear_fwd(runs[0][4][0], runs[0][0].qkv.weight)[0]
+    torch.cuda.synchronize()
+    for _, _, held, want, _, _ in runs:
+        assert all(torch.equal(held[name], want[name]) for name in want)
+    lin.check_fwd(runs[0][4][0], runs[0][0].qkv.weight, None, "none", None, eager, None)
+
+
 @pytest.mark.parametrize("rows,h,f", [(1, 512, 1024), (300, 520, 1032), (777, 1024, 256)])
 def test_training_step(ops, rows, h, f):
     """y = x + down(gelu(up(LN(x)))): every gradient against its formula on the stages' own values, and the whole

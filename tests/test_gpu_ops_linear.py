@@ -168,6 +168,27 @@ def test_rows_between_lines(ops, m, n, k, act):
     assert all(torch.equal(p, q) for p, q in zip(got, ops.linear_bwd(gy, x, w, z, act)))
 
 
+def test_offsets_beyond_32_bits(ops):
+    """Outputs, residual, Z and gZ of more than 2^31 values."""
+    m, n, k = 270000, 8192, 72
+    big = dict(device="cuda", dtype=torch.bfloat16)
+    x, w, b, r = torch.randn(m, k, **big), randn(n, k, seed=2, std=0.1), randn(n, seed=3), torch.randn(m, n, **big)
+    y, z = ops.linear_fwd(x, w, b, "gelu", r, save=True)
+    rows = torch.tensor([0, 1, 131071, 131072, 262143, 262144, 262145, 267001, m - 1], device="cuda")
+    check_fwd(x[rows], w, b, "gelu", r[rows], y[rows], z[rows])
+    gx, _, _ = ops.linear_bwd(r, x, w, z, "gelu", weight_grad=False, bias_grad=False)
+    check_bwd(r[rows], x[rows], w, z[rows], "gelu", gx[rows], None, None)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1 << 20, 8), (1, 8, 1 << 20), (64, 8, 1 << 18), (100, 8, 1 << 18), (65, 1 << 17, 8), (300000, 8, 8)])
+def test_extreme_shapes(ops, m, n, k):
+    x, w = randn(m, k, seed=1), randn(n, k, seed=2, std=k ** -0.5)
+    y, _ = ops.linear_fwd(x, w)
+    check_fwd(x, w, None, "none", None, y, None)
+    gx, gw, _ = ops.linear_bwd(y, x, w, bias_grad=False)
+    check_bwd(y, x, w, None, "none", gx, gw, None)
+
+
 def test_few_rows_and_outputs_of_ones_own(ops):
     from comm_overlap_gb300 import domino as dm
     m, n, k = 5, 264, 520

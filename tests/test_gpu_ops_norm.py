@@ -157,6 +157,17 @@ def test_many_rows_in_place_and_apart(ops):
     assert torch.equal(got[0][keep], want[0][keep]) and torch.isnan(got[0][17]).all() and torch.isnan(got[1]).all()
 
 
+def test_offsets_beyond_32_bits(ops):
+    rows, h = 560000, 4096
+    x, w, b = torch.randn(rows, h, device="cuda", dtype=torch.bfloat16), randn(h, seed=2), randn(h, seed=3)
+    y, mean, rstd = ops.layer_norm_fwd(x, w, b)
+    some = torch.tensor([0, 262143, 262144, 524287, 524288, 524289, 550001, rows - 1], device="cuda")
+    check_fwd(x[some], w, b, 1e-5, (y[some], mean[some], rstd[some]))
+    gx, _, _ = ops.layer_norm_bwd(y, x, w, mean, rstd, x)
+    alone = ops.layer_norm_bwd(y[some], x[some], w, mean[some], rstd[some], x[some])
+    check_bwd(y[some], x[some], w, mean[some], rstd[some], x[some], (gx[some], *alone[1:]))
+
+
 def test_strided_rows_and_accumulation(ops):
     rows, h = 37, 520
     wide, gwide = randn(rows, 3 * h, seed=1), randn(rows, 2 * h, seed=2)
