@@ -85,9 +85,15 @@ def _matrix(name: str, x: torch.Tensor) -> None:
 
 # ---- LayerNorm -----------------------------------------------------------------------------------
 
-def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
+def _differentiated(*tensors: torch.Tensor | None) -> bool:
+    """Whether a backward pass may follow."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5,
+                   stats: bool = True):
     """LayerNorm of each row of x [rows, h] (bf16) with weight and bias (bf16): (y, mean, rstd), the last
-    two fp32, for `layer_norm_bwd`."""
+    two fp32, for `layer_norm_bwd` (None without `stats`)."""
     _matrix("x", x)
     rows, h = x.shape
     _check("weight", weight, x, (h,))
@@ -96,8 +102,8 @@ def layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | N
     x, ld = _rows(x)
     weight, bias = _vec(weight), _vec(bias)
     y = torch.empty((rows, h), dtype=_BF16, device=x.device)
-    mean = torch.empty(rows, dtype=_F32, device=x.device)
-    rstd = torch.empty(rows, dtype=_F32, device=x.device)
+    mean = torch.empty(rows, dtype=_F32, device=x.device) if stats else None
+    rstd = torch.empty(rows, dtype=_F32, device=x.device) if stats else None
     _call(dm.domino_layernorm_fwd, x, x, ld, weight, bias, eps, y, h, mean, rstd, rows, h)
     return y, mean, rstd
 
@@ -160,6 +166,8 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
     """Differentiable LayerNorm over the last dimension of x [..., h] (bf16)."""
     _check("x", x)
+    if not _differentiated(x, weight, bias):
+        return layer_norm_fwd(x.reshape(-1, x.shape[-1]), weight, bias, eps, stats=False)[0].view(x.shape)
     return _LayerNorm.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps).view(x.shape)
 
 
@@ -279,11 +287,14 @@ class _Linear(torch.autograd.Function):
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act="none",
            residual: torch.Tensor | None = None) -> torch.Tensor:
     """Differentiable y = act(x weight^T + bias) + residual for x [..., k] (bf16).  Where weight (bias)
-    has an fp32 `main_grad`, its gradient is accumulated there and its `.grad` stays None."""
+    has an fp32 `main_grad`, its gradient is accumulated there and its `.grad` stays None.  Where no
+    gradient is asked for, the pre-activation is not kept."""
     _check("x", x)
-    r = residual.reshape(-1, weight.shape[0]) if residual is not None else None
-    y = _Linear.apply(x.reshape(-1, x.shape[-1]), weight, bias, r, _act(act), getattr(weight, "main_grad", None),
-                      getattr(bias, "main_grad", None))
+    x2, r = x.reshape(-1, x.shape[-1]), residual.reshape(-1, weight.shape[0]) if residual is not None else None
+    if not _differentiated(x, weight, bias, residual):
+        y, _ = linear_fwd(x2, weight, bias, act, r)
+    else:
+        y = _Linear.apply(x2, weight, bias, r, _act(act), getattr(weight, "main_grad", None), getattr(bias, "main_grad", None))
     return y.view(*x.shape[:-1], weight.shape[0])
 
 

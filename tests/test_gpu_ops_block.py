@@ -124,6 +124,29 @@ def test_serving_block(ops, hq, hkv):
         cached = [c + 1 for c in cached]
 
 
+def test_modules_without_gradients(ops):
+    """The same bits with and without a backward pass to follow, and nothing kept for one without."""
+    ln, up = ops.DominoLayerNorm(520), ops.DominoLinear(520, 1032, act="gelu")
+    x, r = randn(3, 70, 520, seed=1), randn(3, 70, 1032, seed=2)
+    want = up(ln(x), r)
+    assert want.requires_grad and want.shape == (3, 70, 1032)
+    with torch.no_grad():
+        got = up(ln(x), r)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        held = up(ln(x), r)
+        # the two outputs alone, in the allocator's steps of 512 bytes, and the scratch that it has given back
+        assert torch.cuda.memory_allocated() - before <= held.numel() * 2 + 512
+    for p in (*ln.parameters(), *up.parameters()):
+        p.requires_grad_(False)
+    frozen = up(ln(x), r)
+    assert torch.equal(got, want) and torch.equal(frozen, want) and torch.equal(held, want)
+    assert not got.requires_grad and not frozen.requires_grad
+    x.requires_grad_()
+    up(ln(x), r).sum().backward()  # a frozen layer still passes the gradient on
+    assert x.grad is not None and torch.isfinite(x.grad).all()
+
+
 def test_two_captured_steps_at_once(ops):
     """Two captured steps of two blocks, replayed on two streams at the same time, and an eager one beside them."""
     runs = []
