@@ -13,6 +13,7 @@ per device serves all threads; a lock is held while a call enqueues its kernels.
 """
 from __future__ import annotations
 
+import functools
 import threading
 
 import torch
@@ -27,6 +28,9 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+# workspace sizes, functions of the shapes alone (a call through ctypes takes 1.3 us)
+_norm_scratch, _linear_scratch, _packed_scratch = (functools.lru_cache(4096)(f) for f in (
+    dm.domino_layernorm_bwd_workspace_size, dm.domino_linear_bwd_workspace_size, dm.domino_attn_packed_workspace_size))
 
 
 def _call(fn, x: torch.Tensor, *args) -> None:
@@ -140,7 +144,7 @@ def layer_norm_bwd(gy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean
         gres, ld_r = _rows(gres)
     weight, mean, rstd = _vec(weight), _vec(mean), _vec(rstd)
     gx = torch.empty((rows, h), dtype=_BF16, device=x.device)
-    n = dm.domino_layernorm_bwd_workspace_size(rows, h)
+    n = _norm_scratch(rows, h)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device)
     _call(dm.domino_layernorm_bwd, x, gy, ld_gy, x, ld_x, weight, mean, rstd, gres, ld_r, gx, h, gw, gb,
           int(grads is not None), rows, h, ws, n)
@@ -256,7 +260,7 @@ def linear_bwd(gy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, z: torch
     gb = bias_main_grad
     if gb is None and bias_grad:
         gb = torch.empty(n, dtype=_F32, device=x.device)
-    size = dm.domino_linear_bwd_workspace_size(m, n, k, act)
+    size = _linear_scratch(m, n, k, act)
     ws = torch.empty(size, dtype=torch.uint8, device=x.device) if size else None
     _call(dm.domino_linear_bwd, x, gy, ld_gy, x, ld_x, weight, z, ld_z, act, gx, k, gw,
           main_grad if weight_grad else None, gb, int(bias_main_grad is not None), m, n, k, ws, size)
@@ -387,7 +391,7 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
         if same is not out:
             raise ValueError("out must have contiguous, 16-byte aligned tokens that do not overlap")
     lse = torch.empty((tq, hq), dtype=torch.float32, device=q.device) if return_lse else None
-    size = dm.domino_attn_packed_workspace_size(tq, n, hq, hkv, tk)
+    size = _packed_scratch(tq, n, hq, hkv, tk)
     ws = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
     _call(dm.domino_attn_packed_fwd, q, q, ld_q, k, ld_k, v, ld_v, cu_q, k_start, k_len,
           HEAD_DIM ** -0.5 if scale is None else scale, out, ld_o, lse, tq, n, hq, hkv, tk, ws, size)
