@@ -74,7 +74,7 @@ __device__ __forceinline__ void load_row(uint4 (&w)[NPT], const uint16_t* p, int
 
 // mean and 1 / sqrt(var + eps) of the row (variance of the centred values, as a second pass over the
 // registers), y = (x - mean) rstd gamma + beta.
-template <int NPT, bool KEEP>
+template <int NPT>
 __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a, const int tpr) {
   pdl_launch();
   pdl_wait();
@@ -98,17 +98,15 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
     return v < nv && a.beta ? __ldg(reinterpret_cast<const uint4*>(a.beta) + v) : make_uint4(0u, 0u, 0u, 0u);
   };
   load_row<NPT>(w, a.X + r * a.ld_x, t, tpr, nv);
-  if constexpr (KEEP) {
 #pragma unroll
-    for (int i = 0; i < NPT; ++i) {
-      ga[i] = gamma_at(i);
-      be[i] = beta_at(i);
-    }
+  for (int i = 0; i < NPT; ++i) {
+    ga[i] = gamma_at(i);
+    be[i] = beta_at(i);
   }
   for (; r < a.rows; r += stride) {
     uint4 next[NPT];
     const bool more = r + stride < a.rows;
-    if (KEEP && more) load_row<NPT>(next, a.X + (r + stride) * a.ld_x, t, tpr, nv);
+    if (more) load_row<NPT>(next, a.X + (r + stride) * a.ld_x, t, tpr, nv);
     // mean and variance of the row times c
     auto stats = [&](float c, float& mean, float& var) {
       float s = 0.0f;
@@ -147,19 +145,15 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
       if (t + i * tpr >= nv) continue;
       float x[8], g[8], b[8];
       unpack8(w[i], x);
-      unpack8(KEEP ? ga[i] : gamma_at(i), g);
-      unpack8(KEEP ? be[i] : beta_at(i), b);
+      unpack8(ga[i], g);
+      unpack8(be[i], b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = fmaf((x[e] * c - mean) * rstd, g[e], b[e]);
       y[t + i * tpr] = pack8(x);
     }
     if (more) {
-      if constexpr (KEEP) {
 #pragma unroll
-        for (int i = 0; i < NPT; ++i) w[i] = next[i];
-      } else {
-        load_row<NPT>(w, a.X + (r + stride) * a.ld_x, t, tpr, nv);
-      }
+      for (int i = 0; i < NPT; ++i) w[i] = next[i];
     }
   }
 }
@@ -766,7 +760,7 @@ cudaError_t launch_ln_fwd(const LnFwdArgs& a, int sms, cudaStream_t st) {
   const int tpr = team_threads(a.h, npt), teams = tpr >= 256 ? 1 : 256 / tpr;
   const int64_t need = (a.rows + teams - 1) / teams, most = int64_t(sms) * (2048 / (teams * tpr));
   const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(static_cast<unsigned>(teams * tpr));
-  const auto fn = npt == 1 ? ln_fwd_kernel<1, true> : npt == 2 ? ln_fwd_kernel<2, true> : npt == 3 ? ln_fwd_kernel<3, true> : ln_fwd_kernel<4, true>;
+  const auto fn = npt == 1 ? ln_fwd_kernel<1> : npt == 2 ? ln_fwd_kernel<2> : npt == 3 ? ln_fwd_kernel<3> : ln_fwd_kernel<4>;
   return launch_pdl(fn, grid, block, 0, 1, st, a, tpr);
 }
 
