@@ -147,6 +147,50 @@ def test_modules_without_gradients(ops):
     assert x.grad is not None and torch.isfinite(x.grad).all()
 
 
+def test_threads_on_streams_of_their_own(ops):
+    """Four threads call the operators at once, each on its stream: the bits of one thread alone, and no memory kept."""
+    import threading
+
+    def work(i, times, stream):
+        m, h, f = 40 + 300 * (i % 2), 520, 1032
+        x, w, b = randn(m, h, seed=i), randn(f, h, seed=i + 10, std=0.05), randn(f, seed=i + 20)
+        g, q = randn(h, seed=i + 30, mean=1.0), randn(m, 3, D, seed=i + 40)
+        cu = torch.tensor([0, m // 3, m], dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            for _ in range(times):
+                n, mean, rstd = ops.layer_norm_fwd(x, g)
+                y, z = ops.linear_fwd(n, w, b, "gelu", save=True)
+                gx, gw, gb = ops.linear_bwd(y, n, w, z, "gelu")
+                out = (y, gx, gw, gb, *ops.layer_norm_bwd(gx, x, g, mean, rstd), ops.packed_attention(q, q[:, :1], q[:, 1:2], cu))
+            stream.synchronize()
+        return [t.clone() for t in out if t is not None]
+
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    want = [work(i, 1, streams[i]) for i in range(4)]
+    got, failures = [None] * 4, []
+
+    def run(i):
+        try:
+            got[i] = work(i, 50, streams[i])
+        except Exception as e:  # shown below: a thread's exception ends that thread alone
+            failures.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures, failures
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    del got, a, b
+    before = torch.cuda.memory_allocated()
+    work(0, 20, streams[0])
+    assert torch.cuda.memory_allocated() == before
+
+
 def test_two_captured_steps_at_once(ops):
     """Two captured steps of two blocks, replayed on two streams at the same time, and an eager one beside them."""
     runs = []
