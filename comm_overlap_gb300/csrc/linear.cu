@@ -13,8 +13,7 @@
 // (64 to 256 columns) is chosen so that the last round leaves few pairs idle; a product with few tiles is
 // also cut along the reduction over the 2 or 4 pairs of a larger cluster, whose fp32 partials meet in
 // shared memory and are added in their order, each pair finishing a part of the rows.  No sum's
-// order depends on timing.  Two pairs side by side (`quad`: a cluster of four CTAs, tiles of 256 x 2 width) load
-// half of their rows of A each, for both, by multicast.
+// order depends on timing.
 //
 // Bound: the tensor core.  16384 x 16384 -> 4096 takes 1140 - 1250 us (0.91 - 1.0 of the measured burst rate; the power
 // cap decides), 777 x 2560 -> 10240 with GeLU and its pre-activation 39 us (21 at the burst rate): its last tile of
@@ -46,12 +45,6 @@ __device__ __forceinline__ void lin_tile(const LinArgs& a, int tile, int& mt, in
 
 __device__ __forceinline__ void st_shared_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
 }
 
 // drain_pair_ring (gemm.cuh) for a ring of `stages` stages.
@@ -181,11 +174,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // CTA `crank` of the cluster: half `rank` of pair `part`, which computes part `part` of the reduction
   const uint32_t crank = cluster_ctarank(), rank = crank & 1u, lead = crank & ~1u;
-  const int part = a.quad ? 0 : static_cast<int>(crank >> 1), side = a.quad ? static_cast<int>(crank >> 1) : 0;
+  const int part = static_cast<int>(crank >> 1);
   const bool leader = rank == 0;
-  const int ctas = a.quad ? 4 : 2 * a.parts;
-  const int unit = static_cast<int>(blockIdx.x) / ctas, units = static_cast<int>(gridDim.x) / ctas;
-  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead), empty_mask = a.quad ? 0xF : pair_mask;
+  const int unit = static_cast<int>(blockIdx.x) / (2 * a.parts), units = static_cast<int>(gridDim.x) / (2 * a.parts);
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << lead);
   const int k_first = part * a.k_blocks / a.parts, k_last = (part + 1) * a.k_blocks / a.parts;
   const int tiles = a.m_tiles * a.n_tiles;
   int* err = &g_gemm_err;
@@ -193,7 +185,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(bar(kFull + s), 1);
-      mbar_init(bar(kEmpty + s), a.quad ? 2 : 1);  // products of each pair that reads the stage
+      mbar_init(bar(kEmpty + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kAccFull + i), 1);
@@ -237,8 +229,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int tile = unit; ok && tile < tiles; tile += units) {
         int mt, nt;
         lin_tile(a, tile, mt, nt);
-        const int m0 = mt * 256 + static_cast<int>(rank) * 128;
-        const int n0 = (a.quad ? 2 * nt + side : nt) * a.width + static_cast<int>(rank * b_rows);
+        const int m0 = mt * 256 + static_cast<int>(rank) * 128, n0 = nt * a.width + static_cast<int>(rank * b_rows);
         for (int kb = k_first; kb < k_last; ++kb) {
           ok = mbar_wait(bar(kEmpty + s), ph ^ 1u, abort_flag, err, a.err_site + 1);
           if (!ok) break;
@@ -247,15 +238,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           const int k0 = kb * kBK;
           if (one) {
           if (leader) mbar_arrive_expect_tx(bar(kFull + s), a_bytes + b_bytes + peer_bytes);
-          if (a.quad) {
-            // this CTA's 128 rows: the two pairs load 64 each, for both
-            const uint16_t mask = static_cast<uint16_t>(5u << rank);
-            const uint32_t half = sa + static_cast<uint32_t>(side) * 8192u;
-            if constexpr (!A_MN)
-              tma_load_3d_pair_multicast(half, &tmA, fb, k0, m0 + 64 * side, 0, mask);
-            else
-              tma_load_3d_pair_multicast(half, &tmA, fb, m0 + 64 * side, k0, 0, mask);
-          } else if (has_a) {
+          if (has_a) {
             if constexpr (!A_MN) {
               tma_load_3d_pair(sa, &tmA, fb, k0, m0, 0);
             } else {
@@ -277,8 +260,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
       }
-      // both CTAs' copies have landed before the pair leaves, also after an abort (gemm.cuh; four CTAs: below)
-      if (!one || a.quad) {
+      // both CTAs' copies have landed before the pair leaves, also after an abort (gemm.cuh)
+      if (!one) {
       } else if (!leader) {
         st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(peer_issued)), lead), issued);
         mbar_arrive_cluster(mapa_shared(bar(kPeerCount), lead));
@@ -325,7 +308,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             for (int kk = 0; kk < kBK / 16; ++kk)
               umma_bf16_pair(d, a_desc + off + (A_MN ? kk * 128 : kk * 2), b_desc + off + (B_MN ? kk * 128 : kk * 2), idesc,
                              static_cast<uint32_t>(kb != k_first || kk != 0));
-            umma_commit_pair_multicast(bar(kEmpty + s), empty_mask);
+            umma_commit_pair_multicast(bar(kEmpty + s), pair_mask);
           }
           if (++s == stages) {
             s = 0;
@@ -355,7 +338,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int tile = unit; tile < tiles; tile += units, ++i) {
         int mt, nt;
         lin_tile(a, tile, mt, nt);
-        if (a.quad) nt = 2 * nt + side;
         const int row0 = mt * 256 + static_cast<int>(rank) * 128 + quarter * 32;
         const int acc = i & 1;
         // a chunk's bias and residual are loaded before the previous one is finished (the first's while the
@@ -445,21 +427,6 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 
   tc_fence_before();
   cluster_sync();
-  if (a.quad) {
-    // Copies for both pairs come from both: each was waited for by the products that read it, unless a wait ran out
-    // somewhere in the cluster.  Then all four CTAs stay until copies in flight have landed.
-    if (warp == 0) {
-      uint32_t aborted = 0;
-      for (uint32_t c = 0; c < 4; ++c)
-        aborted |= ld_shared_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(abort_flag)), c));
-      if (aborted) {
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < kPeerCopyGraceNs) {
-        }
-      }
-    }
-    cluster_sync();
-  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -480,8 +447,7 @@ cudaError_t launch_linear_t(const LinMaps& m, const LinArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     ready_of[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(fn, dim3(static_cast<unsigned>((a.quad ? 4 : 2 * a.parts) * a.units)), dim3(kLinThreads), kLinSmem,
-                    a.quad ? 4 : 2 * a.parts, st,
+  return launch_pdl(fn, dim3(static_cast<unsigned>(2 * a.parts * a.units)), dim3(kLinThreads), kLinSmem, 2 * a.parts, st,
                     m.a, m.b, m.y, m.z, a);
 }
 
@@ -809,40 +775,24 @@ __global__ void __launch_bounds__(256) lin_gbias_kernel(const float* __restrict_
 // Estimated clocks of a product: a step of the reduction takes about 250 + 1.25 width (measured over two rounds
 // of 152 tiles with 32 and 64 steps: 333 at 64 columns, 399 at 128, 488 at 192, 575 at 256; the arithmetic takes 2
 // width), a round's change of tiles 8 and the last epilogue 20 a column, the start 4500, and joining cut reductions as
-// below.  Where the rows of both operands begin between lines (`split`), each 128-byte row of a box is two requests to
-// L2, 1.55 clocks a row of a pair's boxes or more: 781 for a step at 256 columns, and half the rows of A fewer with
-// two pairs side by side: 620 (4729 x 9368 -> 9032: 544 and 480 us; 777 x 2568 -> 10248: 47 and 42; 16384 x 4104 -> 4096:
-// 359 and 314).  With whole lines L2 is not the limit and pairs alone are ahead, because four SMs fit no cluster of
-// four (16384 x 16384 -> 4096: 1148 us, side by side 1184; 2048 x 2048 -> 8192: 42 and 44).
-// The choices it makes are within 5 % of the best of all widths and cuts at the shapes tried.
-LinPlan lin_plan(int64_t m, int64_t n, int64_t k, bool split) {
+// below.  Where the rows of both operands begin between lines, each 128-byte row of a box is two requests to L2 and a
+// step takes longer (781 at 256 columns).
+LinPlan lin_plan(int64_t m, int64_t n, int64_t k) {
   constexpr int kLinQuads = 36, kLinOctets = 15;  // clusters of 4 and 8 CTAs that a GB300 keeps resident
   const int64_t m_tiles = (m + 255) / 256, kb = (k + 63) / 64;
-  LinPlan best = {256, 1, 0, 0};
+  LinPlan best = {256, 1, 0};
   double least = 1e300;
-  auto step = [split](int width, int a_rows) {
-    const double products = 250 + 1.25 * width, requests = split ? 1.55 * (a_rows + width) : 0.0;
-    return products > requests ? products : requests;
-  };
   for (int width = 256; width >= 64; width -= 32) {
     const int64_t tiles = m_tiles * ((n + width - 1) / width);
     for (int parts = 1; parts <= 4; parts *= 2) {
       if (parts > 1 && (tiles > (parts == 2 ? kLinQuads : kLinOctets) || kb < 4 * parts)) break;
       const int64_t rounds = parts > 1 ? 1 : (tiles + kLinPairs - 1) / kLinPairs;
       const double steps = double((kb + parts - 1) / parts);
-      double cost = double(rounds) * (steps * step(width, 256) + 8.0 * width) + 20.0 * width;
+      double cost = double(rounds) * (steps * (250 + 1.25 * width) + 8.0 * width) + 20.0 * width;
       if (parts > 1) cost += (parts == 2 ? 1200.0 : 3000.0) + 45.0 * width * double(m < 256 ? m : 256) / 256;
       if (cost < least) {
         least = cost;
-        best = {width, parts, static_cast<int>(parts > 1 || tiles < kLinPairs ? tiles : kLinPairs), 0};
-      }
-    }
-    if (split && m > 128) {
-      const int64_t wide = m_tiles * ((n + 2 * width - 1) / (2 * width)), rounds = (wide + kLinQuads - 1) / kLinQuads;
-      const double cost = double(rounds) * (double(kb) * step(width, 128) + 8.0 * width) + 20.0 * width;
-      if (cost < least) {
-        least = cost;
-        best = {width, 1, static_cast<int>(wide < kLinQuads ? wide : kLinQuads), 1};
+        best = {width, parts, static_cast<int>(parts > 1 || tiles < kLinPairs ? tiles : kLinPairs)};
       }
     }
   }

@@ -104,10 +104,8 @@ enum LinKind : int {
 // reduction, by `units` pairs (groups of `parts` pairs).
 struct LinPlan {
   int width, parts, units;
-  int quad;  // two pairs side by side share their rows of A: `units` clusters of two pairs, tiles of 256 x 2 width
 };
-// `split`: rows of both operands begin between 128-byte lines.
-LinPlan lin_plan(int64_t m, int64_t n, int64_t k, bool split);
+LinPlan lin_plan(int64_t m, int64_t n, int64_t k);
 // Maps (all with a third dimension of one): operands in boxes of 64 (reduction) x a_rows, or x width / 2 for
 // B, or, contiguous along their rows, 64 (rows) x 64 (reduction), 128-byte swizzle; y, z (z only with save) in
 // boxes of 32 x 32, 64-byte swizzle.
@@ -116,7 +114,7 @@ struct LinMaps {
 };
 struct LinArgs {
   int32_t M, N, m_tiles, n_tiles, k_blocks, act, save, err_site;
-  int32_t width, parts, units, quad;  // lin_plan
+  int32_t width, parts, units;  // lin_plan
   int32_t a_rows;               // rows of a box of A: 128, or fewer when A is smaller
   int32_t stages, stage_bytes;  // set by the launcher: the operand ring
   const uint16_t* bias;         // nullable

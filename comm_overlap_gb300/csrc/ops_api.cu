@@ -130,21 +130,19 @@ domino_status check_packed(int64_t tq, int64_t n, int32_t heads, int32_t kv_head
 // reduction or (a_mn, b_mn) given as its transpose, with row strides ld_a, ld_b.
 domino_status linear_product(dm::LinMaps* maps, dm::LinArgs* a, const uint16_t* A, int64_t ld_a, bool a_mn,
                              const uint16_t* B, int64_t ld_b, bool b_mn, int64_t m, int64_t n, int64_t k, int site) {
-  auto between_lines = [](const uint16_t* p, int64_t ld) { return ((reinterpret_cast<uintptr_t>(p) | uint64_t(ld) * 2) & 127u) != 0; };
-  const dm::LinPlan p = dm::lin_plan(m, n, k, between_lines(A, ld_a) && between_lines(B, ld_b));
+  const dm::LinPlan p = dm::lin_plan(m, n, k);
   *a = {};
   a->M = int32_t(m);
   a->N = int32_t(n);
   a->m_tiles = int32_t((m + 255) / 256);
-  a->n_tiles = int32_t((n + p.width * (1 + p.quad) - 1) / (p.width * (1 + p.quad)));
+  a->n_tiles = int32_t((n + p.width - 1) / p.width);
   a->k_blocks = int32_t((k + 63) / 64);
   a->err_site = site << 4;
   a->width = p.width;
-  a->quad = p.quad;
   a->parts = p.parts;
   a->units = p.units;
   a->a_rows = a_mn || m >= 128 ? 128 : int32_t((m + 7) / 8 * 8);
-  DM_TRY(a_mn ? map2(&maps->a, 2, A, m, k, ld_a, 64, 64, 128) : map2(&maps->a, 2, A, k, m, ld_a, 64, uint32_t(p.quad ? 64 : a->a_rows), 128));
+  DM_TRY(a_mn ? map2(&maps->a, 2, A, m, k, ld_a, 64, 64, 128) : map2(&maps->a, 2, A, k, m, ld_a, 64, uint32_t(a->a_rows), 128));
   DM_TRY(b_mn ? map2(&maps->b, 2, B, n, k, ld_b, 64, 64, 128) : map2(&maps->b, 2, B, k, n, ld_b, 64, uint32_t(p.width / 2), 128));
   return DOMINO_OK;
 }

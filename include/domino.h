@@ -304,8 +304,7 @@ DOMINO_API domino_status domino_layernorm_bwd(domino_handle handle, const uint16
  * Otherwise Y and Z may not overlap the inputs or one another.
  * bf16 operands, fp32 accumulation; bias, activation and residual are applied in fp32 and Y and Z are
  * each rounded once.  act: NONE, RELU or GELU.  N and K are multiples of 8, at most 2^20; M >= 0.
- * The order of every sum depends on the sizes and on whether the operands' rows begin at multiples of 128
- * bytes, alone: equal inputs give equal bits. */
+ * The order of every sum depends on the sizes alone: equal inputs give equal bits. */
 DOMINO_API domino_status domino_linear_fwd(domino_handle handle, const uint16_t* X, int64_t ld_x, const uint16_t* W,
                                            const uint16_t* bias, int32_t act, const uint16_t* R, int64_t ld_r,
                                            uint16_t* Y, int64_t ld_y, uint16_t* Z, int64_t ld_z, int64_t M,
