@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(256, 4) lin_gz_kernel(const LinGzArgs a) {
 }
 
 // The row ranges' sums in order, written or added to gbias.
-__global__ void __launch_bounds__(256) lin_gbias_kernel(const float* __restrict__ part, int parts, int64_t n,
+__global__ void __launch_bounds__(256) lin_gbias_kernel(const float* part, int parts, int64_t n,
                                                         float* gbias, int accumulate) {
   pdl_launch();
   pdl_wait();

@@ -91,11 +91,11 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
   uint4 w[NPT], ga[NPT], be[NPT];
   auto gamma_at = [&](int i) {
     const int v = t + i * tpr;
-    return v < nv ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + v) : make_uint4(0u, 0u, 0u, 0u);
+    return v < nv ? reinterpret_cast<const uint4*>(a.gamma)[v] : make_uint4(0u, 0u, 0u, 0u);
   };
   auto beta_at = [&](int i) {
     const int v = t + i * tpr;
-    return v < nv && a.beta ? __ldg(reinterpret_cast<const uint4*>(a.beta) + v) : make_uint4(0u, 0u, 0u, 0u);
+    return v < nv && a.beta ? reinterpret_cast<const uint4*>(a.beta)[v] : make_uint4(0u, 0u, 0u, 0u);
   };
   load_row<NPT>(w, a.X + r * a.ld_x, t, tpr, nv);
 #pragma unroll
@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps) ln_fwd_stream_kernel(con
   pdl_wait();
   const int nv = static_cast<int>(a.h >> 3);
   for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-    const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.gamma) + v);
-    const uint4 b = a.beta ? __ldg(reinterpret_cast<const uint4*>(a.beta) + v) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 g = reinterpret_cast<const uint4*>(a.gamma)[v];
+    const uint4 b = a.beta ? reinterpret_cast<const uint4*>(a.beta)[v] : make_uint4(0u, 0u, 0u, 0u);
     st_shared_v4(sg + 16u * v, g.x, g.y, g.z, g.w);
     st_shared_v4(sb + 16u * v, b.x, b.y, b.z, b.w);
   }
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps) ln_fwd_stream_kernel(con
 // With u = gy gamma and n = (x - mean) rstd:  gx = rstd (u - mean(u) - n mean(u n)) (+ gres);
 // the columns' sums of gy n and gy over the block's rows go to row blockIdx.x of `part` (2 h floats).
 template <int NPT, bool PREFETCH>
-__global__ void __launch_bounds__(kTeamThreads) ln_bwd_kernel(const LnBwdArgs a, float* __restrict__ part,
+__global__ void __launch_bounds__(kTeamThreads) ln_bwd_kernel(const LnBwdArgs a, float* part,
                                                               const int tpr) {
   extern __shared__ float cols[];  // teams x 2 h (only with several teams)
   pdl_launch();
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kTeamThreads) ln_bwd_kernel(const LnBwdArgs a,
 // of 36 at 1024 columns).  32768 x 4096 with a residual's gradient 158 us, which is the copy rate; teams 183.
 template <int NPT>
 __global__ void __launch_bounds__(32 * kStreamMaxWarps)
-    ln_bwd_stream_kernel(const LnBwdArgs a, float* __restrict__ part, const int depth, const int wpr) {
+    ln_bwd_stream_kernel(const LnBwdArgs a, float* part, const int depth, const int wpr) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, teams = (blockDim.x >> 5) / wpr;
   const int team = warp / wpr, wt = warp - team * wpr, tt = wt * 32 + lane, width = wpr * 32;
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps)
   pdl_wait();
   const int nv = static_cast<int>(a.h >> 3);
   for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-    const uint4 g = __ldg(reinterpret_cast<const uint4*>(a.gamma) + v);
+    const uint4 g = reinterpret_cast<const uint4*>(a.gamma)[v];
     st_shared_v4(sg + 16u * v, g.x, g.y, g.z, g.w);
   }
   __syncthreads();
@@ -546,15 +546,15 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps)
     for (int e = 0; e < 4; ++e) ag[i][e] = ab[i][e] = 0;
   float mean = 0.0f, rstd = 0.0f;
   if (r0 < a.rows) {
-    mean = __ldg(a.mean + r0);
-    rstd = __ldg(a.rstd + r0);
+    mean = a.mean[r0];
+    rstd = a.rstd[r0];
   }
   int d = 0;
   uint32_t phase = 0;
   for (int64_t r = r0; r < a.rows; r += stride) {
     const uint32_t buf = buf0 + static_cast<uint32_t>(d) * set;
     const bool more = r + stride < a.rows;
-    const float nmean = more ? __ldg(a.mean + r + stride) : 0.0f, nrstd = more ? __ldg(a.rstd + r + stride) : 0.0f;
+    const float nmean = more ? a.mean[r + stride] : 0.0f, nrstd = more ? a.rstd[r + stride] : 0.0f;
     const uint64_t neg = f2(-mean, -mean), scale = f2(rstd, rstd);
     // (a wait that runs out raises the abort flag; the rows after it are neither loaded nor stored)
     const bool ok = mbar_wait(bar0 + 8u * d, phase, abort_flag, &g_norm_err, 0x251);
@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps)
 
 // Column sums of `parts` rows of 2 h floats, in a fixed order: 32 groups of rows per block, then the
 // groups in order.  Columns 0 .. h-1 go to ggamma, the others to gbeta (nullable).
-__global__ void __launch_bounds__(1024) ln_cols_kernel(const float* __restrict__ part, int parts, int64_t h,
+__global__ void __launch_bounds__(1024) ln_cols_kernel(const float* part, int parts, int64_t h,
                                                        float* ggamma, float* gbeta, int accumulate) {
   pdl_launch();
   pdl_wait();

@@ -24,7 +24,10 @@ domino_status launch_on(domino_handle H, int kind, cudaStream_t st, const char* 
 
 // ---- programmatic dependent launch: a kernel may be placed on SMs that its predecessor in the stream has left, and
 // sets itself up there; before it touches memory that others use it waits, in every thread's path, for the
-// predecessor's end (pdl_wait).  Saves 2 - 3 us between the short kernels of these operators.
+// predecessor's end (pdl_wait).  Saves 2 - 3 us between the short kernels of these operators.  The predecessor writes
+// while the kernel already runs, so no memory is read-only for the kernel's lifetime: such kernels read with ordinary
+// loads after the wait, never through __ldg, ld.global.nc or pointers declared __restrict__, which a compiler may move
+// before it.
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

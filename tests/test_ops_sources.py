@@ -22,3 +22,12 @@ def test_bulk_copies_are_not_multicast(path):
     for asm in re.findall(r"\basm\b[^;]*?\((.*?)\)\s*;", code(path), flags=re.S):
         text = "".join(re.findall(r'"((?:[^"\\]|\\.)*)"', asm))
         assert not ("cp.async.bulk" in text and ".multicast" in text), text
+
+
+@pytest.mark.parametrize("path", [f for f in FILES if "pdl_wait()" in code(f)], ids=os.path.basename)
+def test_dependent_kernels_read_with_ordinary_loads(path):
+    """A kernel that starts before its predecessor has ended may not declare what it reads read-only: such a load may
+    come from a stale line, or be moved before the wait."""
+    text = code(path)
+    for word in (r"\b__ldg\b", r"\b__restrict__\b", r"\.nc\b"):
+        assert not re.search(word, text), word
