@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps) ln_fwd_stream_kernel(con
         mean = __shfl_sync(0xFFFFFFFFu, mean, 0);
         m2 = __shfl_sync(0xFFFFFFFFu, m2, 0);
       }
-      var = fmaxf(m2 * inv_h, 0.0f);
+      // infinite or NaN: squares beyond fp32 (also as inf - inf above), or an infinity or NaN in the row
+      var = fabsf(m2) < INFINITY ? fmaxf(m2, 0.0f) * inv_h : NAN;
     };
     float c = 1.0f, mean, var;
     stats(1.0f, mean, var);
