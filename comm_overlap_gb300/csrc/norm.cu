@@ -73,7 +73,7 @@ __device__ __forceinline__ void load_row(uint4 (&w)[NPT], const uint16_t* p, int
 }
 
 // mean and 1 / sqrt(var + eps) of the row (variance of the centred values, as a second pass over the
-// registers), y = (x - mean) rstd gamma + beta.
+// registers), y = (x - mean) rstd gamma + beta.  Where the squares leave fp32's range, of the row times 2^-80.
 template <int NPT>
 __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a, const int tpr) {
   pdl_launch();
@@ -108,13 +108,14 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
     const bool more = r + stride < a.rows;
     if (more) load_row<NPT>(next, a.X + (r + stride) * a.ld_x, t, tpr, nv);
     // mean and variance of the row times c
-    auto stats = [&](float c, float& mean, float& var) {
+    float c = 1.0f, mean, var;
+    {
       float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < NPT; ++i) {
         float x[8];
         unpack8(w[i], x);  // pieces past the row are zero
-        s += ((x[0] * c + x[1] * c) + (x[2] * c + x[3] * c)) + ((x[4] * c + x[5] * c) + (x[6] * c + x[7] * c));
+        s += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
       }
       mean = team_sum(s, 0.0f, red, flip, warps, team).x * inv_h;
       float q = 0.0f;
@@ -124,20 +125,45 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
         float x[8];
         unpack8(w[i], x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(x[e] * c - mean, x[e] * c - mean, q);
+        for (int e = 0; e < 8; ++e) q = fmaf(x[e] - mean, x[e] - mean, q);
       }
       var = team_sum(q, 0.0f, red, flip, warps, team).x * inv_h;
-    };
-    float c = 1.0f, mean, var;
-    stats(1.0f, mean, var);
-    if (!(var < INFINITY)) {  // the squares' sum left fp32's range (or the row holds an infinity or NaN)
-      c = 0x1p-80f;
-      stats(c, mean, var);
     }
-    const float rstd = 1.0f / sqrtf(var + a.eps * c * c);
+    // Two kinds of rows are measured again (the same in the whole team), read once more: those whose squares or sums leave
+    // fp32's range (or with an infinity or NaN), in a smaller scale; and those whose values are all alike, or all but one
+    // (of 16384 values, one of them a bf16 step apart, the variance is 2^-30 of the mean's square), because there the error
+    // of the mean, a few units of its last place, counts against the spread.  The centred values' mean takes it away
+    // (all of it where they are alike).
+    if (!(var < INFINITY) || var < mean * mean * 0x1p-28f) {
+      c = var < INFINITY ? 1.0f : 0x1p-80f;
+      mean = 0.0f;
+      const uint4* again = reinterpret_cast<const uint4*>(a.X + r * a.ld_x);
+#pragma unroll 1
+      for (int k = 0; k < 3; ++k) {  // the mean, its correction, the variance
+        float s = 0.0f;
+#pragma unroll 1
+        for (int v = t; v < nv; v += tpr) {
+          float x[8];
+          unpack8(again[v], x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float z = fmaf(x[e], c, -mean);
+            s = k == 2 ? fmaf(z, z, s) : s + z;
+          }
+        }
+        s = team_sum(s, 0.0f, red, flip, warps, team).x * inv_h;
+        if (k == 2)
+          var = s;
+        else
+          mean += s;
+      }
+    }
+    // (the smaller scale leaves nothing of eps: a variance of zero there is a row of one value)
+    const bool alike = var == 0.0f && c != 1.0f;
+    const float rstd = alike ? 0.0f : 1.0f / sqrtf(var + a.eps * c * c);
     if (t == 0) {
       if (a.mean) a.mean[r] = mean / c;
-      if (a.rstd) a.rstd[r] = rstd * c;
+      if (a.rstd) a.rstd[r] = alike ? 1.0f / sqrtf(a.eps) : rstd * c;
     }
     uint4* y = reinterpret_cast<uint4*>(a.Y + r * a.ld_y);
 #pragma unroll
@@ -247,10 +273,10 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps) ln_fwd_stream_kernel(con
       if (tt < nv) {
         uint64_t x[4];
         unpack8(ld_shared_v4(buf + 16u * tt), x);
-        const uint64_t c2 = f2(c, c);
+        const uint64_t c2 = f2(c, c), c8 = f2(c * 0.125f, c * 0.125f);  // (an eighth of each: their sum may leave the range)
         float lo, hi;
-        f2_split(add_f2(add_f2(mul_f2(x[0], c2), mul_f2(x[1], c2)), add_f2(mul_f2(x[2], c2), mul_f2(x[3], c2))), lo, hi);
-        const float shift = (lo + hi) * 0.125f;
+        f2_split(add_f2(add_f2(mul_f2(x[0], c8), mul_f2(x[1], c8)), add_f2(mul_f2(x[2], c8), mul_f2(x[3], c8))), lo, hi);
+        const float shift = lo + hi;
         const uint64_t neg = f2(-shift, -shift);
         uint64_t s[2] = {0, 0}, q[2] = {0, 0};
 #pragma unroll 4
