@@ -17,6 +17,7 @@ import functools
 import threading
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from . import domino as dm
 
@@ -101,6 +102,14 @@ def _vec(x: torch.Tensor | None) -> torch.Tensor | None:
     if x is None or (x.is_contiguous() and x.data_ptr() % 16 == 0):
         return x
     return x.clone(memory_format=torch.contiguous_format)
+
+
+def _no_tangent(what: str, *tensors: torch.Tensor | None) -> None:
+    """Refuses tensors that carry a tangent: it would be lost, since the result is computed outside of autograd."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # outside of every dual level
+        return
+    if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{what} has no derivative in forward mode")
 
 
 def _matrix(name: str, x: torch.Tensor) -> None:
@@ -188,7 +197,8 @@ class _LayerNorm(torch.autograd.Function):
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-5):
-    """Differentiable LayerNorm over the last dimension of x [..., h] (bf16)."""
+    """Differentiable LayerNorm over the last dimension of x [..., h] (bf16); not in forward mode."""
+    _no_tangent("layer_norm", x, weight, bias)
     _check("x", x)
     if not _differentiated(x, weight, bias):
         return layer_norm_fwd(x.reshape(-1, x.shape[-1]), weight, bias, eps, stats=False)[0].view(x.shape)
@@ -311,7 +321,8 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
            residual: torch.Tensor | None = None) -> torch.Tensor:
     """Differentiable y = act(x weight^T + bias) + residual for x [..., k] (bf16).  Where weight (bias)
     has an fp32 `main_grad`, its gradient is accumulated there and its `.grad` stays None.  Where no
-    gradient is asked for, the pre-activation is not kept."""
+    gradient is asked for, the pre-activation is not kept.  Not differentiable in forward mode."""
+    _no_tangent("linear", x, weight, bias, residual)
     _check("x", x)
     x2, r = x.reshape(-1, x.shape[-1]), residual.reshape(-1, weight.shape[0]) if residual is not None else None
     if not _differentiated(x, weight, bias, residual):
@@ -375,6 +386,7 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     is 1 / sqrt(128) unless given.  Returns o, or (o, lse) with lse [tq, heads] fp32.  Rows that belong to no
     sequence are left as they were in `out` (undefined without it), which may not overlap q, k or v.  Lengths that leave the tensors are not
     raised here: they are read on the device, and `device_status` reports them.  Forward only."""
+    _no_tangent("packed_attention", q, k, v)
     for name, x in (("q", q), ("k", k), ("v", v)):
         _check(name, x, q)
         if x.dim() != 3 or x.shape[2] != HEAD_DIM:
