@@ -27,6 +27,13 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
+// max(a, b) that keeps NaN (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // g and e of u0, u1 >= 0.
 __device__ __forceinline__ void normal_tail_f2(float u0, float u1, uint64_t& g, uint64_t& e) {
   const uint64_t u = f2(u0, u1);

@@ -96,9 +96,12 @@ __device__ __forceinline__ void lin_chunk(const LinArgs& a, const CUtensorMap* t
         float y0, y1;
         if constexpr (decltype(act)::value == ACT_GELU) {
           gelu_f2(z0, z1, y0, y1);
+        } else if constexpr (decltype(act)::value == ACT_RELU) {
+          y0 = max_nan(z0, 0.0f);
+          y1 = max_nan(z1, 0.0f);
         } else {
-          y0 = act_fwd(decltype(act)::value, z0);
-          y1 = act_fwd(decltype(act)::value, z1);
+          y0 = z0;
+          y1 = z1;
         }
         y[4 * q + e] = pack_bf16x2(y0 + bf16lo(rw[e]), y1 + bf16hi(rw[e]));
       }
@@ -140,8 +143,8 @@ __device__ __forceinline__ void few_put(const LinFewArgs& a, int n, bool live, i
   if (a.act == ACT_GELU) {
     gelu_f2(z0, z1, y0, y1);
   } else if (a.act == ACT_RELU) {
-    y0 = fmaxf(z0, 0.0f);
-    y1 = fmaxf(z1, 0.0f);
+    y0 = max_nan(z0, 0.0f);
+    y1 = max_nan(z1, 0.0f);
   }
   if (!live) return;
   const uint32_t y = pack_bf16x2(y0 + r0, y1 + r1), z = pack_bf16x2(z0, z1);
