@@ -723,15 +723,16 @@ __global__ void __launch_bounds__(256, 4) lin_gz_kernel(const LinGzArgs a) {
           const uint32_t zw[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float d0, d1;
+            const float z0 = bf16lo(zw[e]), z1 = bf16hi(zw[e]);
             if constexpr (ACT == ACT_GELU) {
-              gelu_grad_f2(bf16lo(zw[e]), bf16hi(zw[e]), d0, d1);
-            } else {
-              d0 = act_grad(ACT, bf16lo(zw[e]));
-              d1 = act_grad(ACT, bf16hi(zw[e]));
+              float d0, d1;
+              gelu_grad_f2(z0, z1, d0, d1);
+              v[2 * e] *= d0;
+              v[2 * e + 1] *= d1;
+            } else {  // ReLU: a choice, so that an infinite gradient where z is cut has no effect
+              v[2 * e] = z0 > 0.0f ? v[2 * e] : 0.0f;
+              v[2 * e + 1] = z1 > 0.0f ? v[2 * e + 1] : 0.0f;
             }
-            v[2 * e] *= d0;
-            v[2 * e + 1] *= d1;
           }
           if (r + 8 * u < r1) store8_bf16(a.gZ + (r + 8 * u) * a.ld_gz + col, v);
         }

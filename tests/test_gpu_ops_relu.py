@@ -1,9 +1,10 @@
-"""The linear layer's ReLU at the values where fmaxf(z, 0) differs from the definition: NaN stays NaN."""
+"""The linear layer's ReLU at the values where fmaxf(z, 0) and a product with its derivative differ from the definition:
+NaN stays NaN, and a gradient is passed on where z > 0 and nowhere else."""
 import pytest
 import torch
 
 from ops_helpers import device_ok, randn
-from test_gpu_ops_linear import check_fwd
+from test_gpu_ops_linear import check_bwd, check_fwd
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,17 @@ def test_infinities_and_zeros(ops, m, n, k):
     check_fwd(x, w[2:], b[2:], "relu", None, y[:, 2:], None)
     y, _ = ops.linear_fwd(torch.zeros_like(x), w, None, "relu")
     assert not y.any()
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_gradients_pass_where_the_value_is_above_zero_alone(ops, m, n, k):
+    """Infinite and NaN output gradients at values that ReLU has cut have no effect: a choice, not a product with zero."""
+    x, w, gy, z = randn(m, k, seed=1), randn(n, k, seed=2, std=k ** -0.5), randn(m, n, seed=3), randn(m, n, seed=4)
+    z[0, 0], z[1, 1], z[1, 2], z[2, 3] = 0.0, -0.0, -float("inf"), float("nan")
+    cut = ~(z > 0)
+    assert cut[0, 0] and cut[1, 1] and cut[1, 2] and cut[2, 3]
+    want = ops.linear_bwd(torch.where(cut, torch.zeros_like(gy), gy), x, w, z, "relu")
+    check_bwd(gy, x, w, torch.where(z.isnan(), -torch.ones_like(z), z), "relu", *want)
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        got = ops.linear_bwd(torch.where(cut, torch.full_like(gy, bad), gy), x, w, z, "relu")
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), bad
