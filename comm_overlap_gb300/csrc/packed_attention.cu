@@ -254,23 +254,38 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedA
   bool whole = few ? heaviest + kPackedItemCost <= per + kPackedCutCost
                    : 2ll * heaviest <= per && static_cast<long long>(pairs) * a.hkv < (1 << 30);
   if (whole) {
-    // heaviest first: counting sort by half blocks (the order within a bin is of no consequence)
+    // heaviest first: counting sort by half blocks (the order within a bin, of the threads' arrival, changes neither a
+    // share nor a sum where a bin is one count)
     int shift = 0;
     while ((heaviest >> shift) >= kPlanThreads) ++shift;
-    for (int i = tid; i < pairs; i += kPlanThreads)
-      atomicAdd(&bins[kPlanThreads - 1 - ((i == tid ? first_eh : w.pairs[i].eh) >> shift)], 1);
-    __syncthreads();
-    int total;
-    const int start = block_scan(bins[tid], sums, total);
-    bins[tid] = start;
-    __syncthreads();
     int* sorted = near_prefix;  // (read for the last time above)
-    for (int i = tid; i < pairs; i += kPlanThreads) {
-      const int eh = i == tid ? first_eh : w.pairs[i].eh, k = atomicAdd(&bins[kPlanThreads - 1 - (eh >> shift)], 1);
-      w.order[k] = i;
-      if (few) sorted[k] = eh;
+    if (few && shift > 0) {
+      // Bins of several counts would leave the shares below, and with them whether pairs are cut, to chance: each pair
+      // counts those before it instead, the heavier and of equals the first.
+      bins[tid] = first_eh;
+      __syncthreads();
+      if (tid < pairs) {
+        int k = 0;
+        for (int i = 0; i < pairs; ++i) k += bins[i] > first_eh || (bins[i] == first_eh && i < tid);
+        w.order[k] = tid;
+        sorted[k] = first_eh;
+      }
+      __syncthreads();
+    } else {
+      for (int i = tid; i < pairs; i += kPlanThreads)
+        atomicAdd(&bins[kPlanThreads - 1 - ((i == tid ? first_eh : w.pairs[i].eh) >> shift)], 1);
+      __syncthreads();
+      int total;
+      const int start = block_scan(bins[tid], sums, total);
+      bins[tid] = start;
+      __syncthreads();
+      for (int i = tid; i < pairs; i += kPlanThreads) {
+        const int eh = i == tid ? first_eh : w.pairs[i].eh, k = atomicAdd(&bins[kPlanThreads - 1 - (eh >> shift)], 1);
+        w.order[k] = i;
+        if (few) sorted[k] = eh;
+      }
+      __syncthreads();
     }
-    __syncthreads();
     if (few) {
       const int grid = a.groups * a.heads_abreast;
       const float per_head = 1.0f / static_cast<float>(a.hkv);
