@@ -356,6 +356,27 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// As mbar_wait for a wait that may outlast any number of items: a tile that none of them uses waits for the next that
+// does.  The bound grows with the CTA's share of the work (4 us a half block of 64 keys, which takes 0.8 or less).
+__device__ __forceinline__ bool mbar_wait_share(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int site,
+                                                const PackedHeader* head) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitTimeoutNs + 4000ull * static_cast<uint64_t>(head->per)) {
+        *abort_flag = 1;
+        atomicCAS(err, 0, site);
+        return false;
+      }
+    }
+  }
+}
+
 struct Item {
   int hk, q_row, qn, k_row, klen, pos0, b0, slot;
   int e0, e1;   // tile x attends to half blocks (64 keys) 2 b0 .. e_x - 1 (none: e_x <= 2 b0)
@@ -591,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((h & 1) || h == n - 1) umma_commit(bar(B_K_EMPTY + 2 * x + ((gb + (static_cast<uint32_t>(h) >> 1)) & 1u)));
             if (h == n - 1) umma_commit(bar(B_Q_EMPTY + x));
           };
-          if (!mbar_wait(bar(B_Q_FULL + x), nq & 1u, abort_flag, err, a.err_site + 5) || !k_ready(0) ||
+          if (!mbar_wait_share(bar(B_Q_FULL + x), nq & 1u, abort_flag, err, a.err_site + 5, w.head) || !k_ready(0) ||
               (two && x == 1 && !mbar_wait(bar(B_TURN + (turns & 1u)), (turns >> 1) & 1u, abort_flag, err, a.err_site + 4))) {
             ok = false;
             break;
@@ -663,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_run = -INFINITY, l_run = 0.0f;
       for (int j = first; ok && j < e; ++j, ++cb) {
         const uint32_t tB = tS + 64u * (cb & 1u);
-        ok = mbar_wait(bar(B_S_FULL + 2 * x + (cb & 1u)), (cb >> 1) & 1u, abort_flag, err, a.err_site + 10);
+        ok = mbar_wait_share(bar(B_S_FULL + 2 * x + (cb & 1u)), (cb >> 1) & 1u, abort_flag, err, a.err_site + 10, w.head);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
