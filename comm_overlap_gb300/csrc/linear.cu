@@ -62,6 +62,9 @@ __device__ __forceinline__ void drain_ring(uint32_t full_bar0, uint32_t stages, 
   }
 }
 
+// Bound of the wait for a whole accumulator: the time of its steps (0.1 - 0.4 us each) comes on top of that for one step.
+__device__ __forceinline__ uint64_t acc_wait_ns(int steps) { return kWaitTimeoutNs + 4000ull * static_cast<uint64_t>(steps); }
+
 // Bias and residual of a 32-column chunk (first column col) for one row; zero outside D.
 struct LinIn {
   uint4 bias[4], res[4];
@@ -347,7 +350,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         // products run)
         LinIn in;
         in.load(a, row0 + lane, nt * a.width + 32 * half);
-        const bool ok = mbar_wait(bar(kAccFull + acc), (static_cast<uint32_t>(i) >> 1) & 1u, abort_flag, err, a.err_site + 4);
+        const bool ok = mbar_wait(bar(kAccFull + acc), (static_cast<uint32_t>(i) >> 1) & 1u, abort_flag, err, a.err_site + 4,
+                                  acc_wait_ns(k_last - k_first));
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         tc_fence_after();
         const uint32_t tacc = tq + static_cast<uint32_t>(acc * kBN);
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       const int row_cta = mt * 256 + static_cast<int>(rank) * 128, rows4 = 4 / a.parts;
       const uint32_t row_bytes = static_cast<uint32_t>(a.width) * 4u, key = static_cast<uint32_t>(lane) & 7u;
       const uint32_t block = static_cast<uint32_t>(rows4) * 32u * row_bytes;
-      const bool got = mbar_wait(bar(kAccFull), 0, abort_flag, err, a.err_site + 4);
+      const bool got = mbar_wait(bar(kAccFull), 0, abort_flag, err, a.err_site + 4, acc_wait_ns(k_last - k_first));
       const bool ok = __all_sync(0xFFFFFFFFu, got);
       tc_fence_after();
       cluster_sync();  // every ring of the cluster is idle (after an abort: nothing is sent or read)

@@ -99,6 +99,10 @@ domino_status check_linear(int64_t m, int64_t n, int64_t k, int32_t act) {
   return DOMINO_OK;
 }
 
+// Rows that one launch adds to gW_main: that kernel waits at most two seconds for a tile, whose 2^20 steps of 64 rows
+// take 0.3.
+constexpr int64_t kMainRows = int64_t(1) << 26;
+
 // Workspace of the backward: gZ, and the bias gradient's partial sums.  gZ's rows begin at multiples of 128 bytes, so
 // that a row of a TMA box is one line: with neither gZ nor the other operand so, the products of 4729 x 9032 and 9368
 // columns take 556 and 550 us, with gZ 468 and 447.
@@ -342,30 +346,33 @@ domino_status domino_linear_bwd(domino_handle H, const uint16_t* gY, int64_t ld_
       DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GX, st, "linear layer gX launch",
                            [&] { return dm::launch_linear(dm::LIN_GX, m, a, st); }));
     }
-    if (want_gw) {
+    if (gW) {
       dm::LinMaps m = {};
       dm::LinArgs a;
       DM_TRY(linear_product(&m, &a, gZ, ld_gz, true, X, ld_x, true, N, K, M, 0x22));
-      if (gW) {
-        DM_TRY(map2(&m.y, 2, gW, K, N, K, 32, 32, 64));
-        DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
-                             [&] { return dm::launch_linear(dm::LIN_GW, m, a, st); }));
-      } else {  // the MLP's weight-gradient product, tiles of 256 x 256
-        dm::GemmArgs g = {};
-        g.batches = 1;
-        g.m_tiles = a.m_tiles;
-        g.n_tiles = int32_t((K + 255) / 256);
-        g.k_blocks = a.k_blocks;
-        g.M = a.M;
-        g.N = a.N;
-        g.err_site = a.err_site;
-        g.alpha = g.out_scale = 1.0f;
-        g.out0 = gW_main;
-        g.ld0 = K;
-        const dm::EpiMaps none = {};
-        DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
-                             [&] { return dm::launch_gemm_bwd(dm::GV_WGRAD, m.a, m.b, none, g, st); }));
-      }
+      DM_TRY(map2(&m.y, 2, gW, K, N, K, 32, 32, 64));
+      DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
+                           [&] { return dm::launch_linear(dm::LIN_GW, m, a, st); }));
+    }
+    // gW_main: the MLP's weight-gradient product, tiles of 256 x 256, added up over ranges of rows
+    for (int64_t r = 0; gW_main && r < M; r += kMainRows) {
+      dm::LinMaps m = {};
+      dm::LinArgs a;
+      DM_TRY(linear_product(&m, &a, gZ + r * ld_gz, ld_gz, true, X + r * ld_x, ld_x, true, N, K, M - r < kMainRows ? M - r : kMainRows, 0x22));
+      dm::GemmArgs g = {};
+      g.batches = 1;
+      g.m_tiles = a.m_tiles;
+      g.n_tiles = int32_t((K + 255) / 256);
+      g.k_blocks = a.k_blocks;
+      g.M = a.M;
+      g.N = a.N;
+      g.err_site = a.err_site;
+      g.alpha = g.out_scale = 1.0f;
+      g.out0 = gW_main;
+      g.ld0 = K;
+      const dm::EpiMaps none = {};
+      DM_TRY(dm::launch_on(H, DOMINO_K_LINEAR_GW, st, "linear layer gW launch",
+                           [&] { return dm::launch_gemm_bwd(dm::GV_WGRAD, m.a, m.b, none, g, st); }));
     }
     return DOMINO_OK;
   });
