@@ -48,6 +48,13 @@ domino_status check_ld(int64_t ld, int64_t cols, const char* name) {
   return DOMINO_OK;
 }
 
+// An output in an input's place has its rows where the input's are, or a row written lies on rows still to be read.
+domino_status check_in_place(const void* out, int64_t ld_out, const void* in, int64_t ld_in, int64_t rows, const char* what) {
+  if (rows > 1 && in && out == in && ld_out != ld_in)
+    return refuse(DOMINO_ERR_INVALID_ARG, std::string(what) + " share their memory with different row strides");
+  return DOMINO_OK;
+}
+
 domino_status check_ws(void* ws, size_t bytes, size_t need) {
   if (need == 0) return DOMINO_OK;
   if (!ws) return refuse(DOMINO_ERR_WORKSPACE, "workspace is NULL");
@@ -170,6 +177,7 @@ domino_status domino_layernorm_fwd(domino_handle H, const uint16_t* X, int64_t l
       DM_TRY(check_ptr(Y, "Y"));
       DM_TRY(check_ptr(mean, "mean", true));
       DM_TRY(check_ptr(rstd, "rstd", true));
+      DM_TRY(check_in_place(Y, ld_y, X, ld_x, rows, "Y and X"));
     }
     DM_TRY(dm::check_handle(H));
     if (rows == 0) return DOMINO_OK;
@@ -211,6 +219,8 @@ domino_status domino_layernorm_bwd(domino_handle H, const uint16_t* gY, int64_t 
       DM_TRY(check_ptr(rstd, "rstd"));
       DM_TRY(check_ptr(gres, "gres", true));
       DM_TRY(check_ptr(gX, "gX"));
+      DM_TRY(check_in_place(gX, ld_gx, gY, ld_gy, rows, "gX and gY"));
+      DM_TRY(check_in_place(gX, ld_gx, gres, ld_gres, rows, "gX and gres"));
     }
     DM_TRY(check_ws(workspace, workspace_bytes, ln_bwd_bytes(rows, h)));
     DM_TRY(dm::check_handle(H));
@@ -252,6 +262,7 @@ domino_status domino_linear_fwd(domino_handle H, const uint16_t* X, int64_t ld_x
       DM_TRY(check_ptr(Y, "Y"));
       DM_TRY(check_ptr(R, "R", true));
       DM_TRY(check_ptr(Z, "Z", true));
+      DM_TRY(check_in_place(Y, ld_y, R, ld_r, M, "Y and R"));
     }
     DM_TRY(dm::check_handle(H));
     if (M == 0) return DOMINO_OK;

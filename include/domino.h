@@ -275,7 +275,7 @@ DOMINO_API domino_status domino_block_fwd(domino_handle handle, const domino_cfg
 /* LayerNorm with weight and bias, each row on its own:
  *   Y = (X - mean) rstd gamma + beta,  rstd = 1 / sqrt(var + eps)  (biased variance),
  * in fp32 with one rounding to bf16.  X, Y: rows x h with row strides ld_x, ld_y (elements, multiples
- * of 8); Y may be X.  gamma, beta: h bf16 (beta nullable: no bias).  mean, rstd (nullable): rows fp32
+ * of 8); Y may be X, with the same stride.  gamma, beta: h bf16 (beta nullable: no bias).  mean, rstd (nullable): rows fp32
  * each, what domino_layernorm_bwd needs.  h: a multiple of 8, at most 16384; rows may be 0. */
 DOMINO_API domino_status domino_layernorm_fwd(domino_handle handle, const uint16_t* X, int64_t ld_x,
                                               const uint16_t* gamma, const uint16_t* beta, float eps, uint16_t* Y,
@@ -284,7 +284,7 @@ DOMINO_API domino_status domino_layernorm_fwd(domino_handle handle, const uint16
 
 /* Backward of domino_layernorm_fwd.  With n = (X - mean) rstd and u = gY gamma:
  *   gX = bf16( gres + rstd (u - mean(u) - n mean(u n)) )   (gres, the gradient arriving through a
- *        residual connection, is nullable; gX may be gY or gres),
+ *        residual connection, is nullable; gX may be gY or gres, with the same stride),
  *   ggamma = sum over rows of gY n,  gbeta = sum over rows of gY   (fp32, h each; gbeta nullable),
  * written (accumulate = 0) or added to what the buffers hold (accumulate = 1).  The sums' order is
  * fixed: equal inputs give equal bits.  With rows = 0 the sums are zero.  Workspace:
@@ -299,7 +299,7 @@ DOMINO_API domino_status domino_layernorm_bwd(domino_handle handle, const uint16
 
 /* Linear layer:  Z = X . W^T + bias,  Y = act(Z) + R.
  *   X: M x K (row stride ld_x); W: N x K, contiguous (nn.Linear [out, in]); bias (nullable): N;
- *   R (nullable, the residual): M x N (row stride ld_r); Y: M x N (row stride ld_y; may be R).
+ *   R (nullable, the residual): M x N (row stride ld_r); Y: M x N (row stride ld_y; may be R, with the same stride).
  *   Z (nullable): M x N (row stride ld_z), the pre-activation that domino_linear_bwd needs.
  * Otherwise Y and Z may not overlap the inputs or one another.
  * bf16 operands, fp32 accumulation; bias, activation and residual are applied in fp32 and Y and Z are
