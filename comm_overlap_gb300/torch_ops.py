@@ -200,6 +200,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     """Differentiable LayerNorm over the last dimension of x [..., h] (bf16); not in forward mode."""
     _no_tangent("layer_norm", x, weight, bias)
     _check("x", x)
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dimension")
     if not _differentiated(x, weight, bias):
         return layer_norm_fwd(x.reshape(-1, x.shape[-1]), weight, bias, eps, stats=False)[0].view(x.shape)
     return _LayerNorm.apply(x.reshape(-1, x.shape[-1]), weight, bias, eps).view(x.shape)
@@ -215,7 +217,7 @@ class DominoLayerNorm(torch.nn.Module):
         self.bias = torch.nn.Parameter(torch.zeros(h, dtype=torch.bfloat16, device=device)) if bias else None
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        if x.shape[-1] != self.h:
+        if x.dim() == 0 or x.shape[-1] != self.h:
             raise ValueError(f"x must have {self.h} columns")
         return layer_norm(x, self.weight, self.bias, self.eps)
 
@@ -319,12 +321,22 @@ class _Linear(torch.autograd.Function):
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act="none",
            residual: torch.Tensor | None = None) -> torch.Tensor:
-    """Differentiable y = act(x weight^T + bias) + residual for x [..., k] (bf16).  Where weight (bias)
-    has an fp32 `main_grad`, its gradient is accumulated there and its `.grad` stays None.  Where no
-    gradient is asked for, the pre-activation is not kept.  Not differentiable in forward mode."""
+    """Differentiable y = act(x weight^T + bias) + residual for x [..., k] (bf16), the residual in y's shape or as its
+    rows.  Where weight (bias) has an fp32 `main_grad`, its gradient is accumulated there and its `.grad` stays None.
+    Where no gradient is asked for, the pre-activation is not kept.  Not differentiable in forward mode."""
     _no_tangent("linear", x, weight, bias, residual)
     _check("x", x)
-    x2, r = x.reshape(-1, x.shape[-1]), residual.reshape(-1, weight.shape[0]) if residual is not None else None
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dimension")
+    _matrix("weight", weight)
+    x2, r = x.reshape(-1, x.shape[-1]), residual
+    if r is not None:
+        _check("residual", r, x)
+        rows = (x2.shape[0], weight.shape[0])
+        if r.shape != rows:
+            if r.shape != (*x.shape[:-1], weight.shape[0]):
+                raise ValueError(f"residual must have the output's shape {(*x.shape[:-1], weight.shape[0])}, not {tuple(r.shape)}")
+            r = r.reshape(rows)
     if not _differentiated(x, weight, bias, residual):
         y, _ = linear_fwd(x2, weight, bias, act, r)
     else:
@@ -399,12 +411,12 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     tk, hkv, _ = k.shape
     if hkv == 0 or hq == 0 or hq % hkv:
         raise ValueError("the query heads must be a multiple of the key heads")
+    _check("cu_q", cu_q, q, None, torch.int32)
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must be a vector of n + 1 values")
     n = cu_q.numel() - 1
     if (k_start is None) != (k_len is None):
         raise ValueError("k_start and k_len go together")
-    _check("cu_q", cu_q, q, (n + 1,), torch.int32)
     if k_start is None:
         if tk != tq:
             raise ValueError("without k_start and k_len, q and k must have the same rows")
