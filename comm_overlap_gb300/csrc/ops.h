@@ -167,6 +167,8 @@ struct PackedArgs {
   int32_t n, tq, tk, hq, hkv, group, tokens;  // group = hq / hkv query heads share a key head; tokens = 128 / group
   int32_t heads_abreast, subgroups, groups;   // packed_groups: key heads of a group of CTAs, hkv / that, groups
   float scale_log2;        // scale x log2(e)
+  float scale_two;         // the power of two below it
+  float raise_by, huge;    // scores: 8 and 2^28 over scale_log2
   int32_t err_site;
 };
 // Maps, bf16 with 128-byte swizzle: q (128, group, hkv, tq) in boxes (64, group, 1, tokens); k, v (128, hkv,

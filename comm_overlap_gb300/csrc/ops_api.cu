@@ -444,6 +444,9 @@ domino_status domino_attn_packed_fwd(domino_handle H, const uint16_t* Q, int64_t
     a.group = heads / kv_heads;
     a.tokens = 128 / a.group;
     a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_two = std::ldexp(1.0f, std::ilogb(a.scale_log2));
+    a.raise_by = 8.0f / a.scale_log2;
+    a.huge = 0x1p28f / a.scale_log2;
     a.err_site = 0x23 << 4;
     dm::packed_groups(&a, op_sms(H));
     std::string err;

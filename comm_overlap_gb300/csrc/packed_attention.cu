@@ -708,18 +708,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
                                   __uint_as_float(sr[c >> 5][(c & 31) + 1]));
         const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-        // running maximum in the log2 domain, raised when some row of the warp would pass it by more than
-        // 8 (p <= 2^8 otherwise); O and the sum are then rescaled.  A row that has seen no key keeps
-        // -inf, and zero stands in for it so that its p are 0 and not NaN.
-        const float cand = fmaxf(m_run, top * a.scale_log2);
-        const bool raise = __any_sync(0xFFFFFFFFu, cand > m_run + 8.0f) || j == first;
+        // The running maximum is raised when some row of the warp would pass it by more than 8 in the log2 domain
+        // (p <= 2^8 otherwise); O and the sum are then rescaled.  A row that has seen no key keeps -inf, and zero
+        // stands in for it so that its p are 0 and not NaN.  Where the maximum's product with the scale has no binary
+        // places left (2^28), its rounding would be off by more than 2^ can take; scores that differ are then so far
+        // apart that one key has all the weight at any scale, and a power of two, which rounds nothing, stands in.
+        const float cand = fmaxf(m_run, top);
+        const bool raise = __any_sync(0xFFFFFFFFu, cand - m_run > a.raise_by) || j == first;
         const float mx = raise ? cand : m_run;
-        const float base = mx == -INFINITY ? 0.0f : mx;
-        const float alpha = raise ? ex2_approx(m_run - base) : 1.0f;
+        const float sc = fabsf(mx) < a.huge ? a.scale_log2 : a.scale_two;
+        const float base = mx == -INFINITY ? 0.0f : __fmul_rn(mx, sc);
+        const float alpha = raise ? ex2_approx(__fmul_rn(m_run, sc) - base) : 1.0f;
         uint64_t l4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) l4[i] = f2(0.0f, 0.0f);
-        const uint64_t sc2 = f2(a.scale_log2, a.scale_log2), nmx2 = f2(-base, -base);
+        const uint64_t sc2 = f2(sc, sc), nmx2 = f2(-base, -base);
         uint32_t pk[32];
         // p = 2^(score - maximum), two columns at a time
 #pragma unroll
@@ -822,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row_ok) {
           float* ml = w.ml + static_cast<int64_t>(it.slot + x) * (2 * kBlk);
-          ml[row] = m_run;
+          ml[row] = m_run * a.scale_log2;
           ml[kBlk + row] = l_run;
         }
         continue;
@@ -832,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l_run > 0.0f || l_run != l_run ? 1.0f / l_run : 0.0f;
       if (row_ok && a.lse)
         a.lse[static_cast<int64_t>(it.q_row + x * a.tokens + tok) * a.hq + it.hk * a.group + (row - tok * a.group)] =
-            l_run > 0.0f || l_run != l_run ? (m_run + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
+            l_run > 0.0f || l_run != l_run ? (__fmul_rn(m_run, a.scale_log2) + log2f(l_run)) * 0.69314718055994531f : -INFINITY;
 #pragma unroll 1
       for (int h2 = 0; h2 < 2; ++h2) {
         uint32_t o[2][32];
