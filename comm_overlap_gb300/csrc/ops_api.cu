@@ -406,7 +406,8 @@ domino_status domino_attn_packed_fwd(domino_handle H, const uint16_t* Q, int64_t
                                      void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() -> domino_status {
     DM_TRY(check_packed(tq, n, heads, kv_heads, tk));
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return refuse(DOMINO_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!(scale > 0.0f) || !std::isfinite(scale * 1.4426950408889634f))
+      return refuse(DOMINO_ERR_INVALID_ARG, "scale must be > 0, and finite in base 2 (at most 2.3e38)");
     DM_TRY(check_ld(ld_q, int64_t(heads) * 128, "ld_q"));
     DM_TRY(check_ld(ld_k, int64_t(kv_heads) * 128, "ld_k"));
     DM_TRY(check_ld(ld_v, int64_t(kv_heads) * 128, "ld_v"));
