@@ -17,7 +17,7 @@
 //
 // Bound: the tensor core.  16384 x 16384 -> 4096 takes 1140 - 1250 us (0.91 - 1.0 of the measured burst rate; the power
 // cap decides), 777 x 2560 -> 10240 with GeLU and its pre-activation 39 us (21 at the burst rate): its last tile of
-// rows is three quarters padding, and tiles narrower than 256 run the tensor core below its rate (lin_plan).
+// rows is nearly all padding, and every step is bound by staging its operands (lin_plan).
 #include "gelu2.cuh"
 #include "gemm.cuh"
 #include "ops.h"
@@ -782,7 +782,8 @@ __global__ void __launch_bounds__(256) lin_gbias_kernel(const float* part, int p
 
 // Estimated clocks of a product: a step of the reduction takes about 250 + 1.25 width (measured over two rounds
 // of 152 tiles with 32 and 64 steps: 333 at 64 columns, 399 at 128, 488 at 192, 575 at 256; the arithmetic takes 2
-// width), a round's change of tiles 8 and the last epilogue 20 a column, the start 4500, and joining cut reductions as
+// width; a CTA stages (128 + width / 2) x 128 bytes a step, 57 - 62 a clock at every width, and the shared memory that
+// they are written to and read from passes 128 a clock), a round's change of tiles 8 and the last epilogue 20 a column, the start 4500, and joining cut reductions as
 // below.  Where the rows of both operands begin between lines, each 128-byte row of a box is two requests to L2 and a
 // step takes longer (781 at 256 columns).
 LinPlan lin_plan(int64_t m, int64_t n, int64_t k) {

@@ -8,8 +8,8 @@
 // the next row's pieces are loaded before the current row is reduced, which keeps memory busy across
 // the reductions.  All arithmetic is fp32; the one rounding to bf16 is the output's.
 // Bound: memory (forward 4 bytes, backward 6, with a residual gradient 8 bytes an element).  32768 x 4096: forward 90 us
-// (79 at the copy rate), backward with a residual gradient 158 (158); 1237 x 2560 backward 11.7 (3.7: two launches and the
-// latency of a few rows a team); one row of 4096 forward 2.3.
+// (79 at the copy rate), backward with a residual gradient 158 (158); 1237 x 2560 backward 11.5 (3.7: two launches and the
+// latency of a few rows a team); one row of 4096 forward 2.4.
 #include <atomic>
 
 #include "actfn.cuh"
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kTeamThreads) ln_fwd_kernel(const LnFwdArgs a,
 // ---- forward of many rows: each team of `wpr` warps streams rows through its own `depth` buffers in shared memory
 // with bulk copies, so that memory never waits for a reduction and no team for another.  The row is
 // normalised in place and stored from there; a buffer is refilled one row after its store was issued.
-// Same arithmetic as above up to the order of the sums.  32768 x 4096: 135 us above, 88 us here (0.90 of the copy
+// Same arithmetic as above up to the order of the sums.  32768 x 4096: 135 us above, 90 us here (0.88 of the copy
 // bandwidth; the same copies without arithmetic take 86 us).
 __device__ int g_norm_err;
 
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(32 * kStreamMaxWarps) ln_fwd_stream_kernel(con
   const uint32_t row_bytes = static_cast<uint32_t>(a.h) * 2u, pitch = (row_bytes + 127u) & ~127u;
   const uint32_t bar0 = smem_u32(smem) + static_cast<uint32_t>(team * kStreamMaxDepth) * 8u;
   float* joint = reinterpret_cast<float*>(smem + 512);  // a team's warps: mean and sum of squares each
-  // gamma and beta in shared memory: beside buffers of this size L1 is too small to hold them (101 -> 88 us)
+  // gamma and beta in shared memory: beside buffers of this size L1 is too small to hold them (101 -> 90 us)
   const uint32_t sg = smem_u32(smem) + kStreamCtrl, sb = sg + pitch;
   const uint32_t buf0 = sg + (2u + static_cast<uint32_t>(team * depth)) * pitch;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kStreamCtrl - 4);
@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(1024) ln_cols_kernel(const float* part, int pa
 
 constexpr int kMaxSmem = 232448;  // a CTA's
 // Forward: a row of up to 1024 columns is one warp's where there are rows to fill the GPU so (no barrier; 26715 rows of
-// 584: 18.3 us, with three warps a row 29.4, streamed 24.8; of 1024: 25.7, 32.6, 27.3), but several warps' where there
+// 584: 18.1 us, with three warps a row 29.4, streamed 24.8; of 1024: 24.9, 32.6, 27.3), but several warps' where there
 // are few (64 rows of 904: 2.0 us, one warp a row 2.4).  Wider rows are streamed from 2.2 M values on: at 4096 columns
 // the two cross at 650 rows (11.0 and 6.5 us at 1216), at 1200 at 1800 (1000 rows: 3.3, streamed 4.4; 6648: 15.4 and 10.3).
 constexpr int64_t kNarrowMinRows = 512, kStreamMinH = 1032, kStreamMinValues = 2200000;

@@ -14,14 +14,14 @@
 //           CTAs are dealt whole pairs, heaviest first, back and forth.  Elsewhere (few long caches) the work is cut
 //           into equal ranges, one for each group of CTAs (one CTA for each of up to 8 heads, which read neighbouring
 //           cache rows at the same time); a range may begin and end inside a pair, at a block.  Whole / cut, us:
-//           eight prompts of 11000 tokens 140 / 165, 16 heads of four prompts 89 / 104, 64 cached tokens 196 / 188.
+//           eight prompts of 11000 tokens 140 / 165, 16 heads of four prompts 89 / 104, 64 cached tokens 196 / 190.
 //  combine  adds the parts of pairs that were cut: each left its unnormalised O, maximum and sum.
 // Only keys of the sequence count: scores of rows past its end are masked by position and its last value
 // tile is cleared past its end in shared memory, so whatever lies there (NaN included) has no effect.
 //
-// Bound: for prompts the tensor core and the exponentials, 1024 clocks each for a block of two tiles, of which a
-// 16384-token prompt with 32 and 8 heads reaches 0.85 (1310 - 1340 us, 1640 TFLOP/s of the products that count); memory
-// (K and V once per G heads) for single tokens: 64 over caches of up to 8064 keys in 189 us (0.90 of the copy rate).  A
+// Bound: for prompts the tensor core and the exponentials, 1024 clocks each for a half block of 64 keys of two tiles, of which a
+// 16384-token prompt with 32 and 8 heads reaches 0.85 (1300 - 1350 us, 1630 - 1690 TFLOP/s of the products that count); memory
+// (K and V once per G heads) for single tokens: 64 over caches of up to 8064 keys in 190 us (0.89 of the copy rate).  A
 // call's fixed part is about 13 us: the plan 5, the first loads and products of a CTA, its last output, the combination.
 #include <cuda_bf16.h>
 

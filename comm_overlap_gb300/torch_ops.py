@@ -4,8 +4,10 @@ The operators of a pre-LN block outside the sharded MLP: LayerNorm with weight a
 with bias, activation and residual, and causal attention over packed sequences with grouped heads.  The
 first two have plain functions that allocate their outputs and call the C ABI (`layer_norm_fwd`,
 `layer_norm_bwd`, `linear_fwd`, `linear_bwd`), a differentiable function (`layer_norm`, `linear`) and a
-module (`DominoLayerNorm`, `DominoLinear`); the attention (`packed_attention`) is forward only.  Every step of the
-computation runs in the library's kernels; tensors must be on one CUDA device, matrices bf16.
+module (`DominoLayerNorm`, `DominoLinear`); the attention (`packed_attention`) is forward only.  The operators run in the library's kernels;
+what PyTorch does beside them is to copy tensors that the library cannot stride over, to round the fp32 gradients of bf16
+parameters, and to take the sequences' lengths from `cu_q` where they are not given.  Tensors must be on one CUDA device,
+matrices bf16.
 
 Calls run on the current stream of the tensors' device.  Workspaces come from PyTorch's allocator for each
 call, so calls on several streams, and several captured graphs, share none.  One library handle per device

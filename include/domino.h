@@ -303,7 +303,7 @@ DOMINO_API domino_status domino_layernorm_bwd(domino_handle handle, const uint16
  *   Z (nullable): M x N (row stride ld_z), the pre-activation that domino_linear_bwd needs.
  * Otherwise Y and Z may not overlap the inputs or one another.
  * bf16 operands, fp32 accumulation; bias, activation and residual are applied in fp32 and Y and Z are
- * each rounded once.  act: NONE, RELU or GELU.  N and K are multiples of 8, at most 2^20; M >= 0.
+ * each rounded once.  act: NONE, RELU (which keeps NaN) or GELU.  N and K are multiples of 8, at most 2^20; M >= 0.
  * The order of every sum depends on the sizes alone: equal inputs give equal bits. */
 DOMINO_API domino_status domino_linear_fwd(domino_handle handle, const uint16_t* X, int64_t ld_x, const uint16_t* W,
                                            const uint16_t* bias, int32_t act, const uint16_t* R, int64_t ld_r,
@@ -311,7 +311,8 @@ DOMINO_API domino_status domino_linear_fwd(domino_handle handle, const uint16_t*
                                            int64_t N, int64_t K, void* stream);
 
 /* Backward of domino_linear_fwd (the residual's gradient is gY itself):
- *   gZ = gY act'(Z)                 (fp32; rounded to bf16 where it enters the products)
+ *   gZ = gY act'(Z)                 (fp32; rounded to bf16 where it enters the products; RELU: gY where Z > 0,
+ *                                    else 0, whatever gY holds there)
  *   gX = gZ . W                     (nullable; M x K, row stride ld_gx)
  *   gW = gZ^T . X                   (N x K; nullable) as bf16, rounded once, or instead
  *   gW_main += gZ^T . X             (N x K fp32, the main_grad buffer; nullable)
@@ -345,7 +346,8 @@ DOMINO_API domino_status domino_linear_bwd(domino_handle handle, const uint16_t*
  * held.  Lengths are read on the device: a sequence whose rows leave the tensors is skipped and recorded
  * (domino_device_status gives DOMINO_ERR_INVALID_ARG); query rows shared by two sequences have undefined
  * results.  Equal inputs give equal bits.  O may not overlap Q, K or V.
- * Workspace: domino_attn_packed_workspace_size() bytes, without initialisation. */
+ * Workspace: domino_attn_packed_workspace_size() bytes, without initialisation: the list of work (36 bytes a tile pair),
+ * and with tk > 896 another 40 MB for the partial results of cut sequences. */
 DOMINO_API domino_status domino_attn_packed_workspace_size(int64_t tq, int64_t n, int32_t heads, int32_t kv_heads,
                                                            int64_t tk, size_t* bytes);
 DOMINO_API domino_status domino_attn_packed_fwd(domino_handle handle, const uint16_t* Q, int64_t ld_q,
