@@ -1,6 +1,7 @@
 // ops.h -- host-side interface between the C ABI of the sublayer operators (ops_api.cu) and their
 // kernels: LayerNorm with parameters (norm.cu), the linear layer (linear.cu),
-// attention over packed sequences (packed_attention.cu).
+// attention over packed sequences (packed_attention.cu), norms and rotation of queries and keys and the
+// 8-bit cache (rotary.cu).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -181,5 +182,62 @@ cudaError_t launch_packed_attention(const CUtensorMap& q, const CUtensorMap& k, 
                                     const PackedArgs& a, void* ws, cudaStream_t st);
 cudaError_t launch_packed_combine(const PackedArgs& a, void* ws, cudaStream_t st);
 cudaError_t take_packed_error(int* code);
+
+// ---- norm and rotation of query and key heads, the 8-bit cache (rotary.cu), head dimension 128
+constexpr int kCacheExpMax = 51;  // the cache's powers of two lie between 2^-51 and 2^51
+struct RotaryArgs {
+  const uint16_t* Q;
+  const uint16_t* K;            // nullable with hkv = 0
+  const uint16_t* V;            // into the cache
+  const int32_t* positions;     // with rot > 0
+  const double* frequencies;    // with rot > 0: rot / 2, radians a position
+  const uint16_t* wq;           // nullable: no norm
+  const uint16_t* wk;
+  uint16_t* Yq;
+  uint16_t* Yk;                 // not into the cache
+  uint8_t* k8;                  // nullable: the cache, rows x hkv x 128 codes, and hkv rows of exponents + 127
+  uint8_t* v8;
+  uint8_t* k_exp;
+  uint8_t* v_exp;
+  const int32_t* rows;          // the cache row of each token; negative: not written
+  int64_t tokens, ld_q, ld_k, ld_v, ld_yq, ld_yk, ld_exp;
+  int32_t hq, hkv, rot, layout, cache_rows;  // layout: 0 half, 1 interleaved
+  float eps, amplitude, sign;   // sign -1: rotated back
+};
+struct RotaryBwdArgs {
+  const uint16_t* gYq;
+  const uint16_t* gYk;
+  const uint16_t* Q;
+  const uint16_t* K;
+  const int32_t* positions;
+  const double* frequencies;
+  const uint16_t* wq;
+  const uint16_t* wk;
+  uint16_t* gQ;
+  uint16_t* gK;
+  float* gwq;
+  float* gwk;                   // nullable with hkv = 0
+  int64_t tokens, ld_gyq, ld_gyk, ld_q, ld_k, ld_gq, ld_gk;
+  int32_t hq, hkv, rot, layout, accumulate;
+  float eps, amplitude;
+};
+struct CacheReadArgs {
+  const uint8_t* k8;
+  const uint8_t* v8;
+  const uint8_t* k_exp;
+  const uint8_t* v_exp;
+  const int32_t* rows;          // negative: zeros
+  uint16_t* K;
+  uint16_t* V;
+  int64_t tokens, ld_k, ld_v, ld_exp;
+  int32_t hkv, cache_rows;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int sms, cudaStream_t st);
+// `part`: rotary_bwd_blocks() rows of 256 floats, written by the backward and summed by launch_rotary_sums.
+int rotary_bwd_blocks(int64_t tokens, int hq, int hkv, int sms);
+cudaError_t launch_rotary_bwd(const RotaryBwdArgs& a, float* part, int sms, cudaStream_t st);
+cudaError_t launch_rotary_sums(const RotaryBwdArgs& a, const float* part, int sms, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheReadArgs& a, int sms, cudaStream_t st);
+cudaError_t take_rotary_error(int* code);
 
 }  // namespace dm

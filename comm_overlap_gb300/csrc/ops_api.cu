@@ -158,6 +158,64 @@ domino_status linear_product(dm::LinMaps* maps, dm::LinArgs* a, const uint16_t* 
   return DOMINO_OK;
 }
 
+domino_status check_list(const void* p, const char* name, uintptr_t align) {
+  if (!p) return refuse(DOMINO_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) & (align - 1))
+    return refuse(DOMINO_ERR_ALIGNMENT, std::string(name) + " is not " + std::to_string(align) + "-byte aligned");
+  return DOMINO_OK;
+}
+
+// Sizes and the rotation of the operators on query and key heads.
+domino_status check_heads(int64_t tokens, int32_t heads, int32_t kv_heads) {
+  if (tokens < 0 || heads < 0 || kv_heads < 0 || heads + kv_heads < 1)
+    return refuse(DOMINO_ERR_INVALID_ARG, "need tokens, heads and kv_heads >= 0, and a head");
+  if (tokens > (int64_t(1) << 31) - 1024 || heads > 4096 || kv_heads > 4096)
+    return refuse(DOMINO_ERR_UNSUPPORTED, "more tokens than 2^31 - 1024, or heads than 4096");
+  return DOMINO_OK;
+}
+domino_status check_rotation(int64_t tokens, const int32_t* positions, const double* frequencies, int32_t rot, int32_t layout,
+                             float amplitude) {
+  if (rot < 0) return refuse(DOMINO_ERR_INVALID_ARG, "rot must be >= 0");
+  if (rot > 128 || rot % 16 != 0) return refuse(DOMINO_ERR_UNSUPPORTED, "rot must be a multiple of 16, at most 128");
+  if (layout != DOMINO_ROTARY_HALF && layout != DOMINO_ROTARY_INTERLEAVED) return refuse(DOMINO_ERR_INVALID_ARG, "unknown layout");
+  if (!std::isfinite(amplitude)) return refuse(DOMINO_ERR_INVALID_ARG, "amplitude must be finite");
+  if (rot > 0 && tokens > 0) {
+    DM_TRY(check_list(positions, "positions", 4));
+    DM_TRY(check_list(frequencies, "frequencies", 8));
+  }
+  return DOMINO_OK;
+}
+domino_status check_weights(const uint16_t* wq, const uint16_t* wk, int32_t heads, int32_t kv_heads, float eps) {
+  if (!wq && !wk) return DOMINO_OK;
+  if (heads > 0) DM_TRY(check_ptr(wq, "wq"));
+  if (kv_heads > 0) DM_TRY(check_ptr(wk, "wk"));
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return refuse(DOMINO_ERR_INVALID_ARG, "eps must be finite and > 0");
+  return DOMINO_OK;
+}
+domino_status check_tokens(const void* p, const char* name, int64_t ld, const char* ld_name, int32_t heads, int64_t tokens) {
+  if (heads == 0) return DOMINO_OK;
+  DM_TRY(check_ld(ld, int64_t(heads) * 128, ld_name));
+  return tokens > 0 ? check_ptr(p, name) : DOMINO_OK;
+}
+size_t rotary_bwd_bytes(int64_t tokens, int32_t heads, int32_t kv_heads) {
+  return tokens == 0 ? 0 : size_t(dm::rotary_bwd_blocks(tokens, heads, kv_heads, kGb300Sms)) * 256 * 4;
+}
+domino_status check_cache(const void* k8, const void* v8, const void* k_exp, const void* v_exp, int64_t ld_exp, int64_t rows,
+                          int32_t kv_heads) {
+  if (rows < 0 || kv_heads < 1) return refuse(DOMINO_ERR_INVALID_ARG, "need cache_rows >= 0 and kv_heads >= 1");
+  if (rows > (int64_t(1) << 31) - 1024 || kv_heads > 4096)
+    return refuse(DOMINO_ERR_UNSUPPORTED, "cache rows beyond 2^31 - 1024, or more than 4096 heads");
+  if (ld_exp < rows) return refuse(DOMINO_ERR_INVALID_ARG, "ld_exp is smaller than the row it strides over");
+  if (ld_exp > (int64_t(1) << 32)) return refuse(DOMINO_ERR_UNSUPPORTED, "ld_exp beyond the supported range");
+  if (rows > 0) {
+    DM_TRY(check_ptr(k8, "k8"));
+    DM_TRY(check_ptr(v8, "v8"));
+    DM_TRY(check_list(k_exp, "k_exp", 1));
+    DM_TRY(check_list(v_exp, "v_exp", 1));
+  }
+  return DOMINO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -475,6 +533,163 @@ domino_status domino_attn_packed_fwd(domino_handle H, const uint16_t* Q, int64_t
       DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_PACKED, st, "packed attention combine launch",
                            [&] { return dm::launch_packed_combine(a, workspace, st); }));
     return DOMINO_OK;
+  });
+}
+
+domino_status domino_qk_rotary_fwd(domino_handle H, const uint16_t* Q, int64_t ld_q, const uint16_t* K, int64_t ld_k,
+                                   const int32_t* positions, const double* frequencies, int32_t rot, int32_t layout,
+                                   float amplitude, const uint16_t* wq, const uint16_t* wk, float eps, uint16_t* Yq,
+                                   int64_t ld_yq, uint16_t* Yk, int64_t ld_yk, int64_t tokens, int32_t heads,
+                                   int32_t kv_heads, void* stream) {
+  return guarded([&]() -> domino_status {
+    DM_TRY(check_heads(tokens, heads, kv_heads));
+    DM_TRY(check_rotation(tokens, positions, frequencies, rot, layout, amplitude));
+    DM_TRY(check_weights(wq, wk, heads, kv_heads, eps));
+    DM_TRY(check_tokens(Q, "Q", ld_q, "ld_q", heads, tokens));
+    DM_TRY(check_tokens(K, "K", ld_k, "ld_k", kv_heads, tokens));
+    DM_TRY(check_tokens(Yq, "Yq", ld_yq, "ld_yq", heads, tokens));
+    DM_TRY(check_tokens(Yk, "Yk", ld_yk, "ld_yk", kv_heads, tokens));
+    DM_TRY(check_in_place(Yq, ld_yq, Q, ld_q, tokens, "Yq and Q"));
+    DM_TRY(check_in_place(Yk, ld_yk, K, ld_k, tokens, "Yk and K"));
+    DM_TRY(dm::check_handle(H));
+    if (tokens == 0) return DOMINO_OK;
+    dm::RotaryArgs a = {};
+    a.Q = Q;
+    a.K = K;
+    a.positions = positions;
+    a.frequencies = frequencies;
+    a.wq = wq;
+    a.wk = wk;
+    a.Yq = Yq;
+    a.Yk = Yk;
+    a.tokens = tokens;
+    a.ld_q = ld_q;
+    a.ld_k = ld_k;
+    a.ld_yq = ld_yq;
+    a.ld_yk = ld_yk;
+    a.hq = heads;
+    a.hkv = kv_heads;
+    a.rot = rot;
+    a.layout = layout;
+    a.eps = eps;
+    a.amplitude = amplitude;
+    a.sign = 1.0f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dm::launch_on(H, DOMINO_K_ROTARY, st, "rotation launch", [&] { return dm::launch_rotary(a, op_sms(H), st); });
+  });
+}
+
+domino_status domino_qk_rotary_bwd_workspace_size(int64_t tokens, int32_t heads, int32_t kv_heads, size_t* bytes) {
+  return guarded([&]() -> domino_status {
+    if (!bytes) return refuse(DOMINO_ERR_INVALID_ARG, "bytes is NULL");
+    DM_TRY(check_heads(tokens, heads, kv_heads));
+    *bytes = rotary_bwd_bytes(tokens, heads, kv_heads);
+    return DOMINO_OK;
+  });
+}
+
+domino_status domino_qk_rotary_bwd(domino_handle H, const uint16_t* gYq, int64_t ld_gyq, const uint16_t* gYk, int64_t ld_gyk,
+                                   const uint16_t* Q, int64_t ld_q, const uint16_t* K, int64_t ld_k,
+                                   const int32_t* positions, const double* frequencies, int32_t rot, int32_t layout,
+                                   float amplitude, const uint16_t* wq, const uint16_t* wk, float eps, uint16_t* gQ,
+                                   int64_t ld_gq, uint16_t* gK, int64_t ld_gk, float* gwq, float* gwk,
+                                   int32_t accumulate, int64_t tokens, int32_t heads, int32_t kv_heads, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> domino_status {
+    DM_TRY(check_heads(tokens, heads, kv_heads));
+    if (accumulate != 0 && accumulate != 1) return refuse(DOMINO_ERR_INVALID_ARG, "accumulate must be 0 or 1");
+    DM_TRY(check_rotation(tokens, positions, frequencies, rot, layout, amplitude));
+    DM_TRY(check_weights(wq, wk, heads, kv_heads, eps));
+    const bool norm = wq || wk;
+    DM_TRY(check_tokens(gYq, "gYq", ld_gyq, "ld_gyq", heads, tokens));
+    DM_TRY(check_tokens(gYk, "gYk", ld_gyk, "ld_gyk", kv_heads, tokens));
+    DM_TRY(check_tokens(gQ, "gQ", ld_gq, "ld_gq", heads, tokens));
+    DM_TRY(check_tokens(gK, "gK", ld_gk, "ld_gk", kv_heads, tokens));
+    DM_TRY(check_in_place(gQ, ld_gq, gYq, ld_gyq, tokens, "gQ and gYq"));
+    DM_TRY(check_in_place(gK, ld_gk, gYk, ld_gyk, tokens, "gK and gYk"));
+    if (norm) {
+      DM_TRY(check_tokens(Q, "Q", ld_q, "ld_q", heads, tokens));
+      DM_TRY(check_tokens(K, "K", ld_k, "ld_k", kv_heads, tokens));
+      if (heads > 0) DM_TRY(check_ptr(gwq, "gwq"));
+      if (kv_heads > 0) DM_TRY(check_ptr(gwk, "gwk"));
+      DM_TRY(check_ws(workspace, workspace_bytes, rotary_bwd_bytes(tokens, heads, kv_heads)));
+    }
+    DM_TRY(dm::check_handle(H));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!norm) {  // the rotation alone: the forward's kernel, turned back
+      if (tokens == 0) return DOMINO_OK;
+      dm::RotaryArgs a = {};
+      a.Q = gYq;
+      a.K = gYk;
+      a.positions = positions;
+      a.frequencies = frequencies;
+      a.Yq = gQ;
+      a.Yk = gK;
+      a.tokens = tokens;
+      a.ld_q = ld_gyq;
+      a.ld_k = ld_gyk;
+      a.ld_yq = ld_gq;
+      a.ld_yk = ld_gk;
+      a.hq = heads;
+      a.hkv = kv_heads;
+      a.rot = rot;
+      a.layout = layout;
+      a.amplitude = amplitude;
+      a.sign = -1.0f;
+      return dm::launch_on(H, DOMINO_K_ROTARY, st, "rotation launch", [&] { return dm::launch_rotary(a, op_sms(H), st); });
+    }
+    const dm::RotaryBwdArgs a = {gYq, gYk, Q, K, positions, frequencies, wq, wk, gQ, gK, heads > 0 ? gwq : nullptr,
+                                 kv_heads > 0 ? gwk : nullptr, tokens, ld_gyq, ld_gyk, ld_q, ld_k, ld_gq, ld_gk, heads, kv_heads,
+                                 rot, layout, accumulate, eps, amplitude};
+    float* part = static_cast<float*>(workspace);
+    if (tokens > 0)
+      DM_TRY(dm::launch_on(H, DOMINO_K_ROTARY_BWD, st, "rotation backward launch",
+                           [&] { return dm::launch_rotary_bwd(a, part, op_sms(H), st); }));
+    return dm::launch_on(H, DOMINO_K_ROTARY_BWD, st, "norm gradient sums launch",
+                         [&] { return dm::launch_rotary_sums(a, part, op_sms(H), st); });
+  });
+}
+
+domino_status domino_cache_write(domino_handle H, const uint16_t* Q, int64_t ld_q, const uint16_t* K, int64_t ld_k,
+                                 const uint16_t* V, int64_t ld_v, const int32_t* positions, const double* frequencies,
+                                 int32_t rot, int32_t layout, float amplitude, const uint16_t* wq, const uint16_t* wk,
+                                 float eps, uint16_t* Yq, int64_t ld_yq, const int32_t* rows, uint8_t* k8, uint8_t* v8,
+                                 uint8_t* k_exp, uint8_t* v_exp, int64_t ld_exp, int64_t cache_rows, int64_t tokens,
+                                 int32_t heads, int32_t kv_heads, void* stream) {
+  return guarded([&]() -> domino_status {
+    DM_TRY(check_heads(tokens, heads, kv_heads));
+    DM_TRY(check_cache(k8, v8, k_exp, v_exp, ld_exp, cache_rows, kv_heads));
+    DM_TRY(check_rotation(tokens, positions, frequencies, rot, layout, amplitude));
+    DM_TRY(check_weights(wq, wk, heads, kv_heads, eps));
+    DM_TRY(check_tokens(Q, "Q", ld_q, "ld_q", heads, tokens));
+    DM_TRY(check_tokens(K, "K", ld_k, "ld_k", kv_heads, tokens));
+    DM_TRY(check_tokens(V, "V", ld_v, "ld_v", kv_heads, tokens));
+    DM_TRY(check_tokens(Yq, "Yq", ld_yq, "ld_yq", heads, tokens));
+    if (heads > 0) DM_TRY(check_in_place(Yq, ld_yq, Q, ld_q, tokens, "Yq and Q"));
+    if (tokens > 0) DM_TRY(check_list(rows, "rows", 4));
+    DM_TRY(dm::check_handle(H));
+    if (tokens == 0) return DOMINO_OK;
+    dm::RotaryArgs a = {Q, K, V, positions, frequencies, wq, wk, Yq, nullptr, k8, v8, k_exp, v_exp, rows, tokens, ld_q, ld_k, ld_v,
+                        ld_yq, 0, ld_exp, heads, kv_heads, rot, layout, int32_t(cache_rows), eps, amplitude, 1.0f};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dm::launch_on(H, DOMINO_K_CACHE_WRITE, st, "cache write launch", [&] { return dm::launch_rotary(a, op_sms(H), st); });
+  });
+}
+
+domino_status domino_cache_read(domino_handle H, const uint8_t* k8, const uint8_t* v8, const uint8_t* k_exp,
+                                const uint8_t* v_exp, int64_t ld_exp, int64_t cache_rows, const int32_t* rows, uint16_t* K,
+                                int64_t ld_k, uint16_t* V, int64_t ld_v, int64_t tokens, int32_t kv_heads, void* stream) {
+  return guarded([&]() -> domino_status {
+    DM_TRY(check_heads(tokens, 0, kv_heads));
+    DM_TRY(check_cache(k8, v8, k_exp, v_exp, ld_exp, cache_rows, kv_heads));
+    DM_TRY(check_tokens(K, "K", ld_k, "ld_k", kv_heads, tokens));
+    DM_TRY(check_tokens(V, "V", ld_v, "ld_v", kv_heads, tokens));
+    if (tokens > 0) DM_TRY(check_list(rows, "rows", 4));
+    DM_TRY(dm::check_handle(H));
+    if (tokens == 0) return DOMINO_OK;
+    const dm::CacheReadArgs a = {k8, v8, k_exp, v_exp, rows, K, V, tokens, ld_k, ld_v, ld_exp, kv_heads, int32_t(cache_rows)};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dm::launch_on(H, DOMINO_K_CACHE_READ, st, "cache read launch", [&] { return dm::launch_cache_read(a, op_sms(H), st); });
   });
 }
 

@@ -16,7 +16,9 @@ serves all threads; a lock is held while a call enqueues its kernels.
 from __future__ import annotations
 
 import functools
+import math
 import threading
+from typing import NamedTuple
 
 import torch
 import torch.autograd.forward_ad as forward_ad
@@ -26,14 +28,16 @@ from . import domino as dm
 _handles: dict[int, int] = {}
 _lock = threading.Lock()
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_F64, _U8, _FP8 = torch.float64, torch.uint8, torch.float8_e4m3fn
 # The current stream's handle as an integer and the current device, without the objects that torch.cuda builds
 # around them (3 us a call on a Grace core).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # workspace sizes, functions of the shapes alone (a call through ctypes takes 1.3 us)
-_norm_scratch, _linear_scratch, _packed_scratch = (functools.lru_cache(4096)(f) for f in (
-    dm.domino_layernorm_bwd_workspace_size, dm.domino_linear_bwd_workspace_size, dm.domino_attn_packed_workspace_size))
+_norm_scratch, _linear_scratch, _packed_scratch, _rotary_scratch = (functools.lru_cache(4096)(f) for f in (
+    dm.domino_layernorm_bwd_workspace_size, dm.domino_linear_bwd_workspace_size, dm.domino_attn_packed_workspace_size,
+    dm.domino_qk_rotary_bwd_workspace_size))
 
 
 # A workspace straight from PyTorch's allocator, on a stream as a tensor's memory would be, without a tensor around it
@@ -444,6 +448,307 @@ def packed_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: to
     return (out, lse) if return_lse else out
 
 
+# ---- norm and rotation of query and key heads -------------------------------------------------------
+
+LAYOUTS = {"half": dm.ROTARY_HALF, "interleaved": dm.ROTARY_INTERLEAVED}
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, original: int | None = None, slow: float = 1.0,
+                       fast: float = 4.0, device: str | torch.device = "cuda") -> torch.Tensor:
+    """Radians a position of the rot / 2 rotated pairs, base^(-2 i / rot), for `qk_rotary` and `cache_write` (fp64).  For
+    contexts `factor` times longer they are all divided by it; with `original`, the length trained on, only those
+    that turn fewer than `slow` times over it, while those that turn more than `fast` times stay, with a linear
+    ramp between."""
+    if rot < 2 or rot % 2:
+        raise ValueError("rot must be even and at least 2")
+    if not (base > 0 and factor > 0 and fast > slow):
+        raise ValueError("need base > 0, factor > 0 and fast > slow")
+    f = base ** (-torch.arange(rot // 2, dtype=_F64) * 2 / rot)
+    if original is None:
+        f = f / factor
+    else:
+        keep = ((original * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    return f.to(device)
+
+
+def _tokens(name: str, x: torch.Tensor, like: torch.Tensor, tokens: int) -> int:
+    """The heads of a [tokens, heads, 128] tensor."""
+    _check(name, x, like)
+    if x.dim() != 3 or x.shape[0] != tokens or x.shape[2] != HEAD_DIM or x.shape[1] == 0:
+        raise ValueError(f"{name} must have shape [{tokens}, heads, {HEAD_DIM}], not {tuple(x.shape)}")
+    return x.shape[1]
+
+
+def _rotation(x: torch.Tensor, positions, frequencies, layout, q_weight, k_weight, heads: int, kv_heads: int):
+    """Checked arguments of a norm and rotation: (positions, frequencies, rot, layout, q_weight, k_weight)."""
+    tokens = x.shape[0]
+    code = LAYOUTS.get(layout, layout)
+    if code not in LAYOUTS.values():
+        raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
+    if (positions is None) != (frequencies is None):
+        raise ValueError("positions and frequencies go together")
+    rot = 0
+    if frequencies is not None:
+        _check("frequencies", frequencies, x, None, _F64)
+        if frequencies.dim() != 1:
+            raise ValueError("frequencies must be a vector")
+        rot = 2 * frequencies.numel()
+        if rot > HEAD_DIM or rot % 16:
+            raise ValueError(f"there must be a multiple of 8 frequencies, at most {HEAD_DIM // 2}, not {rot // 2}")
+        _check("positions", positions, x, (tokens,), _I32)
+        positions, frequencies = positions.contiguous(), frequencies.contiguous()
+    if heads and kv_heads and (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if heads == 0 and q_weight is not None or kv_heads == 0 and k_weight is not None:
+        raise ValueError("a weight needs its heads")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _check(name, w, x, (HEAD_DIM,))
+    return positions, frequencies, rot, code, _vec(q_weight), _vec(k_weight)
+
+
+def _heads_out(name: str, out, like: torch.Tensor) -> tuple[torch.Tensor, int]:
+    """The output for [tokens, heads, 128] heads and its token stride: `out`, or a new one."""
+    if out is None:
+        return torch.empty(like.shape, dtype=_BF16, device=like.device), like.shape[1] * HEAD_DIM
+    _check(name, out, like, like.shape)
+    same, ld = _heads(name, out)
+    if same is not out:
+        raise ValueError(f"{name} must have contiguous, 16-byte aligned tokens that do not overlap")
+    return out, ld
+
+
+def qk_rotary_fwd(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None, frequencies: torch.Tensor | None,
+                  q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, layout="half", eps: float = 1e-6,
+                  amplitude: float = 1.0, out: tuple | None = None):
+    """RMS norm of each head of q [tokens, heads, 128] and k [tokens, kv_heads, 128] (bf16), with q_weight and k_weight
+    (128 values, bf16; no norm without them), and the rotation of the first 2 x len(frequencies) values of each head by
+    position x frequency, in one pass: (q', k').  positions: int32, one a token; frequencies: fp64 (`rotary_frequencies`),
+    or None for no rotation.  layout: "half" (value i pairs with i + len(frequencies)) or "interleaved" (2 i with 2 i + 1);
+    the rotated values are multiplied by `amplitude`.  q and k may be slices of a fused projection; k may be None.  `out`:
+    tensors for (q', k'), which may be q and k."""
+    _check("q", q)
+    if q.dim() != 3:
+        raise ValueError(f"q must have shape [tokens, heads, {HEAD_DIM}], not {tuple(q.shape)}")
+    tokens = q.shape[0]
+    hq = _tokens("q", q, q, tokens)
+    hkv = 0 if k is None else _tokens("k", k, q, tokens)
+    positions, frequencies, rot, code, q_weight, k_weight = _rotation(q, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
+    yq, ld_yq = _heads_out("out[0]", None if out is None else out[0], q)
+    q, ld_q = _heads("q", q)
+    yk, ld_k, ld_yk = None, 0, 0
+    if k is not None:
+        yk, ld_yk = _heads_out("out[1]", None if out is None else out[1], k)
+        k, ld_k = _heads("k", k)
+    _call(dm.domino_qk_rotary_fwd, q, q, ld_q, k, ld_k, positions, frequencies, rot, code, amplitude, q_weight, k_weight, eps, yq,
+          ld_yq, yk, ld_yk, tokens, hq, hkv)
+    return yq, yk
+
+
+def qk_rotary_bwd(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.Tensor | None, k: torch.Tensor | None,
+                  positions: torch.Tensor | None, frequencies: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                  k_weight: torch.Tensor | None = None, layout="half", eps: float = 1e-6, amplitude: float = 1.0,
+                  grads: tuple | None = None):
+    """Gradients of `qk_rotary_fwd` from those of its outputs: (gq, gk, gq_weight, gk_weight), the first two bf16, the others
+    fp32 (None without weights).  q and k, the forward's inputs, are needed with weights only.  `grads`, a pair of fp32
+    buffers for the weights' gradients, is added to instead of allocated."""
+    _check("gq", gq)
+    if gq.dim() != 3:
+        raise ValueError(f"gq must have shape [tokens, heads, {HEAD_DIM}], not {tuple(gq.shape)}")
+    tokens = gq.shape[0]
+    hq = _tokens("gq", gq, gq, tokens)
+    hkv = 0 if gk is None else _tokens("gk", gk, gq, tokens)
+    positions, frequencies, rot, code, q_weight, k_weight = _rotation(gq, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
+    norm = q_weight is not None
+    gwq = gwk = None
+    ld_q = ld_k = 0
+    if norm:
+        if q is None or (k is None) != (gk is None):
+            raise ValueError("the norm's gradient needs q and k")
+        _check("q", q, gq, gq.shape)
+        q, ld_q = _heads("q", q)
+        if hkv:
+            _check("k", k, gq, gk.shape)
+            k, ld_k = _heads("k", k)
+        if grads is not None:
+            gwq, gwk = grads
+            for name, g in (("gq_weight", gwq), ("gk_weight", gwk)):
+                if name == "gk_weight" and not hkv:
+                    continue
+                _check(f"the buffer of {name}", g, gq, (HEAD_DIM,), _F32)
+                if not g.is_contiguous() or g.data_ptr() % 16:
+                    raise ValueError(f"the buffer of {name} must be contiguous and 16-byte aligned")
+        else:
+            gwq = torch.empty(HEAD_DIM, dtype=_F32, device=gq.device)
+            gwk = torch.empty(HEAD_DIM, dtype=_F32, device=gq.device) if hkv else None
+    else:
+        q = k = None
+    gq, ld_gyq = _heads("gq", gq)
+    yq, ld_gq = _heads_out("gq", None, gq)
+    yk, ld_gyk, ld_gk = None, 0, 0
+    if hkv:
+        gk, ld_gyk = _heads("gk", gk)
+        yk, ld_gk = _heads_out("gk", None, gk)
+    _call(dm.domino_qk_rotary_bwd, gq, gq, ld_gyq, gk, ld_gyk, q, ld_q, k, ld_k, positions, frequencies, rot, code, amplitude,
+          q_weight, k_weight, eps, yq, ld_gq, yk, ld_gk, gwq, gwk, int(grads is not None), tokens, hq, hkv,
+          scratch=_rotary_scratch(tokens, hq, hkv) if norm else 0)
+    return yq, yk, gwq, gwk
+
+
+class _QKRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, frequencies, q_weight, k_weight, layout, eps, amplitude):
+        y = qk_rotary_fwd(q, k, positions, frequencies, q_weight, k_weight, layout, eps, amplitude)
+        norm = q_weight is not None
+        ctx.save_for_backward(q if norm else None, k if norm else None, positions, frequencies, q_weight, k_weight)
+        ctx.how = layout, eps, amplitude
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk):
+        q, k, positions, frequencies, wq, wk = ctx.saved_tensors
+        gq, gk, gwq, gwk = qk_rotary_bwd(gq, gk, q, k, positions, frequencies, wq, wk, *ctx.how)
+        return (gq, gk, None, None, gwq.to(wq.dtype) if gwq is not None else None, gwk.to(wk.dtype) if gwk is not None else None, None,
+                None, None)
+
+
+def qk_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None, frequencies: torch.Tensor | None,
+              q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, layout="half", eps: float = 1e-6,
+              amplitude: float = 1.0):
+    """Differentiable `qk_rotary_fwd`: (q', k'); not in forward mode, and not by the frequencies."""
+    _no_tangent("qk_rotary", q, k, q_weight, k_weight)
+    if not _differentiated(q, k, q_weight, k_weight):
+        return qk_rotary_fwd(q, k, positions, frequencies, q_weight, k_weight, layout, eps, amplitude)
+    return _QKRotary.apply(q, k, positions, frequencies, q_weight, k_weight, layout, eps, amplitude)
+
+
+class DominoQKRotary(torch.nn.Module):
+    """Norm of query and key heads (with `norm`: bf16 weights) and rotation of their first `rot` values; `scaling`: what
+    `rotary_frequencies` takes beyond rot and base."""
+
+    def __init__(self, rot: int = HEAD_DIM, base: float = 10000.0, layout="half", norm: bool = True, eps: float = 1e-6,
+                 amplitude: float = 1.0, device: str | torch.device = "cuda", **scaling):
+        super().__init__()
+        if layout not in LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
+        self.layout, self.eps, self.amplitude = layout, eps, amplitude
+        self.frequencies = rotary_frequencies(rot, base, device=device, **scaling)  # fp64 whatever the module is cast to
+        self.q_weight, self.k_weight = (
+            torch.nn.Parameter(torch.ones(HEAD_DIM, dtype=_BF16, device=device)) if norm else None for _ in range(2))
+
+    def _apply(self, fn, recurse=True):
+        super()._apply(fn, recurse)
+        moved = fn(self.frequencies)
+        self.frequencies = self.frequencies.to(moved.device)
+        return self
+
+    def forward(self, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor):
+        return qk_rotary(q, k, positions, self.frequencies, self.q_weight, self.k_weight, self.layout, self.eps, self.amplitude)
+
+    def write(self, cache: "QuantizedCache", rows: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+              positions: torch.Tensor) -> torch.Tensor:
+        """The same for serving: k and v into the cache (`cache_write`), q' returned."""
+        return cache_write(cache, rows, k, v, q, positions, self.frequencies, self.q_weight, self.k_weight, self.layout, self.eps,
+                           self.amplitude)
+
+
+# ---- the 8-bit cache of keys and values ---------------------------------------------------------------
+
+EXP_BIAS = 127
+
+
+class QuantizedCache(NamedTuple):
+    """Keys and values as E4M3 codes [rows, kv_heads, 128], each row and head with a power of two: its exponent + 127 in
+    k_exp and v_exp [kv_heads, rows].  Sequences lie in ranges of rows, as in the caches of `packed_attention`."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_exp: torch.Tensor
+    v_exp: torch.Tensor
+
+    @staticmethod
+    def empty(rows: int, kv_heads: int, device: str | torch.device = "cuda") -> "QuantizedCache":
+        codes = [torch.zeros((rows, kv_heads, HEAD_DIM), dtype=_U8, device=device).view(_FP8) for _ in range(2)]
+        return QuantizedCache(*codes, *(torch.full((kv_heads, rows), EXP_BIAS, dtype=_U8, device=device) for _ in range(2)))
+
+
+def _cache(cache: tuple, like: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, int, int, int]:
+    """Checked tensors of a cache, the row stride of its exponents, its rows and its heads."""
+    k, v, ke, ve = cache
+    _check("the cache's k", k, like, None, _FP8)
+    if k.dim() != 3 or k.shape[2] != HEAD_DIM or k.shape[1] == 0:
+        raise ValueError(f"the cache's k must have shape [rows, kv_heads, {HEAD_DIM}], not {tuple(k.shape)}")
+    rows, hkv, _ = k.shape
+    _check("the cache's v", v, like, k.shape, _FP8)
+    _check("the cache's k_exp", ke, like, (hkv, rows), _U8)
+    _check("the cache's v_exp", ve, like, (hkv, rows), _U8)
+    for name, x in (("k", k), ("v", v)):
+        if not x.is_contiguous() or x.data_ptr() % 16:
+            raise ValueError(f"the cache's {name} must be contiguous and 16-byte aligned")
+    ld = rows
+    if not (ke.is_contiguous() and ve.is_contiguous()):
+        ld = ke.stride(0)
+        if ke.stride() != ve.stride() or (rows > 1 and ke.stride(1) != 1) or (hkv > 1 and ld < rows):
+            raise ValueError("the cache's k_exp and v_exp must have contiguous rows that do not overlap, and the same strides")
+        ld = max(ld, rows)
+    return k, v, ke, ve, ld, rows, hkv
+
+
+def cache_write(cache: tuple, rows: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
+                positions: torch.Tensor | None = None, frequencies: torch.Tensor | None = None,
+                q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, layout="half", eps: float = 1e-6,
+                amplitude: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Writes the tokens of k and v [tokens, kv_heads, 128] (bf16) to the rows `rows` (int32, one a token) of the cache,
+    quantised: for each token and head the least power of two at which the largest value fits E4M3.  With weights or
+    frequencies the keys are normed and rotated before, as in `qk_rotary_fwd`, and so is q [tokens, heads, 128] in the same
+    pass, which is returned (`out`: a tensor for it, which may be q).  Negative rows are not written; rows beyond the cache
+    neither, and `device_status` reports them; a row must not be given twice.  No gradients."""
+    _no_tangent("cache_write", q, k, v, q_weight, k_weight)
+    if _differentiated(q, k, v, q_weight, k_weight):
+        raise ValueError("cache_write has no backward: call it under torch.no_grad(), or detach its inputs")
+    _check("k", k)
+    if k.dim() != 3:
+        raise ValueError(f"k must have shape [tokens, kv_heads, {HEAD_DIM}], not {tuple(k.shape)}")
+    tokens = k.shape[0]
+    hkv = _tokens("k", k, k, tokens)
+    hq = 0 if q is None else _tokens("q", q, k, tokens)
+    _check("v", v, k, k.shape)
+    k8, v8, ke, ve, ld_exp, cache_rows, cache_heads = _cache(cache, k)
+    if cache_heads != hkv:
+        raise ValueError(f"k has {hkv} heads, the cache {cache_heads}")
+    _check("rows", rows, k, (tokens,), _I32)
+    positions, frequencies, rot, code, q_weight, k_weight = _rotation(k, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
+    y, ld_q, ld_y = None, 0, 0
+    if q is not None:
+        y, ld_y = _heads_out("out", out, q)
+        q, ld_q = _heads("q", q)
+    k, ld_k = _heads("k", k)
+    v, ld_v = _heads("v", v)
+    _call(dm.domino_cache_write, k, q, ld_q, k, ld_k, v, ld_v, positions, frequencies, rot, code, amplitude, q_weight, k_weight, eps, y,
+          ld_y, rows.contiguous(), k8, v8, ke, ve, ld_exp, cache_rows, tokens, hq, hkv)
+    return y
+
+
+def cache_read(cache: tuple, rows: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """What the cache holds in the rows `rows` (int32): (k, v), each [len(rows), kv_heads, 128] in bf16, exact; zeros where a
+    row is negative, or beyond the cache, which `device_status` reports.  `out`: tensors for them."""
+    _check("rows", rows, None, None, _I32)
+    if rows.dim() != 1:
+        raise ValueError("rows must be a vector")
+    k8, v8, ke, ve, ld_exp, cache_rows, hkv = _cache(cache, rows)
+    tokens = rows.numel()
+    if out is None:
+        k, v = (torch.empty((tokens, hkv, HEAD_DIM), dtype=_BF16, device=rows.device) for _ in range(2))
+        ld_k = ld_v = hkv * HEAD_DIM
+    else:
+        for name, x in zip(("out[0]", "out[1]"), out):
+            _check(name, x, rows, (tokens, hkv, HEAD_DIM))
+        (k, ld_k), (v, ld_v) = (_heads_out(f"out[{i}]", x, x) for i, x in enumerate(out))
+    _call(dm.domino_cache_read, rows, k8, v8, ke, ve, ld_exp, cache_rows, rows.contiguous(), k, ld_k, v, ld_v, tokens, hkv)
+    return k, v
+
+
 def device_status(device: torch.device | int | None = None) -> None:
     """Synchronises the device and raises DominoError if a call of this module's since the last look ran out
     of a wait or met lengths that leave their tensors."""
@@ -456,6 +761,6 @@ def device_status(device: torch.device | int | None = None) -> None:
 
     _call(read, x)
     if status != dm.DOMINO_OK:
-        what = "packed_attention met lengths that leave its tensors" if site == dm.BAD_LENGTHS_SITE else \
+        what = "a call met lengths or rows that leave its tensors" if site == dm.BAD_LENGTHS_SITE else \
             f"a device-side wait ran out (site {site:#x})"
         raise dm.DominoError(status, what)

@@ -357,6 +357,66 @@ DOMINO_API domino_status domino_attn_packed_fwd(domino_handle handle, const uint
                                                 int64_t n, int32_t heads, int32_t kv_heads, int64_t tk,
                                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/* Norm and rotation of query and key heads, head dimension 128, in one pass:
+ *   n = x / sqrt(mean(x^2) + eps) w    for each head on its own (with wq, wk: 128 bf16 each, for all
+ *                                      heads; without them n = x; they go together),
+ *   (a, b) -> amplitude (a cos t - b sin t, a sin t + b cos t),  t = position frequency,
+ * for the rot / 2 pairs of the first rot values (rot a multiple of 16, at most 128; 0: none): values i and
+ * i + rot / 2 (layout DOMINO_ROTARY_HALF) or 2 i and 2 i + 1 (DOMINO_ROTARY_INTERLEAVED), i < rot / 2; the
+ * others stay.  fp32 arithmetic, one rounding to bf16.
+ *   Q, Yq: tokens x heads x 128, K, Yk: tokens x kv_heads x 128 (kv_heads = 0: no keys), row strides ld_* in
+ *   elements (multiples of 8), so that Q and K may be slices of a fused projection; Yq may be Q and Yk K,
+ *   with the same strides.  positions: tokens int32 (any value); frequencies: rot / 2 doubles, radians a
+ *   position, both on the device.  Angles are exact to fp32 whatever the position. */
+typedef enum { DOMINO_ROTARY_HALF = 0, DOMINO_ROTARY_INTERLEAVED = 1 } domino_rotary_layout;
+DOMINO_API domino_status domino_qk_rotary_fwd(domino_handle handle, const uint16_t* Q, int64_t ld_q, const uint16_t* K,
+                                              int64_t ld_k, const int32_t* positions, const double* frequencies,
+                                              int32_t rot, int32_t layout, float amplitude, const uint16_t* wq,
+                                              const uint16_t* wk, float eps, uint16_t* Yq, int64_t ld_yq, uint16_t* Yk,
+                                              int64_t ld_yk, int64_t tokens, int32_t heads, int32_t kv_heads,
+                                              void* stream);
+
+/* Backward of domino_qk_rotary_fwd.  With u the gradient rotated back and times amplitude, n = x rstd:
+ *   gQ, gK = rstd (u w - n mean(u w n))   (without weights: u; Q and K are then not read),
+ *   gwq, gwk = sums over tokens and heads of u n   (128 fp32 each; with weights),
+ * written (accumulate = 0) or added to what the buffers hold (accumulate = 1), in a fixed order: equal inputs
+ * give equal bits.  gQ may be gYq and gK may be gYk, with the same strides.  With tokens = 0 the sums are zero.
+ * Workspace (with weights): domino_qk_rotary_bwd_workspace_size() bytes. */
+DOMINO_API domino_status domino_qk_rotary_bwd_workspace_size(int64_t tokens, int32_t heads, int32_t kv_heads,
+                                                             size_t* bytes);
+DOMINO_API domino_status domino_qk_rotary_bwd(domino_handle handle, const uint16_t* gYq, int64_t ld_gyq,
+                                              const uint16_t* gYk, int64_t ld_gyk, const uint16_t* Q, int64_t ld_q,
+                                              const uint16_t* K, int64_t ld_k, const int32_t* positions,
+                                              const double* frequencies, int32_t rot, int32_t layout, float amplitude,
+                                              const uint16_t* wq, const uint16_t* wk, float eps, uint16_t* gQ,
+                                              int64_t ld_gq, uint16_t* gK, int64_t ld_gk, float* gwq, float* gwk,
+                                              int32_t accumulate, int64_t tokens, int32_t heads, int32_t kv_heads,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* The 8-bit cache: k8, v8 (cache_rows x kv_heads x 128, contiguous) hold E4M3 codes; k_exp, v_exp (kv_heads
+ * rows of cache_rows bytes, row stride ld_exp) for each row and head e + 127: the values are code x 2^e.
+ *
+ * domino_cache_write: token i's keys (with norm and rotation as in domino_qk_rotary_fwd, unrounded before this
+ * rounding; rot = 0 and no weights: as they are) and values go to cache row rows[i]:  e is the least integer
+ * with max |x| <= 448 2^e, in [-51, 51] (0 for a head of zeros), code = e4m3(x 2^-e), to nearest, ties to even,
+ * values beyond 448 2^51 saturating and infinities becoming NaN.  With heads > 0 the queries are normed and
+ * rotated into Yq in the same pass.  rows: tokens int32 on the device; negative: not written; from cache_rows on:
+ * not written, and recorded (domino_device_status).  A row that two tokens are written to has undefined values.
+ *
+ * domino_cache_read: the values of cache row rows[i] as token i of K and V (bf16, exact); zeros where rows[i] is
+ * negative, or from cache_rows on (recorded). */
+DOMINO_API domino_status domino_cache_write(domino_handle handle, const uint16_t* Q, int64_t ld_q, const uint16_t* K,
+                                            int64_t ld_k, const uint16_t* V, int64_t ld_v, const int32_t* positions,
+                                            const double* frequencies, int32_t rot, int32_t layout, float amplitude,
+                                            const uint16_t* wq, const uint16_t* wk, float eps, uint16_t* Yq,
+                                            int64_t ld_yq, const int32_t* rows, uint8_t* k8, uint8_t* v8,
+                                            uint8_t* k_exp, uint8_t* v_exp, int64_t ld_exp, int64_t cache_rows,
+                                            int64_t tokens, int32_t heads, int32_t kv_heads, void* stream);
+DOMINO_API domino_status domino_cache_read(domino_handle handle, const uint8_t* k8, const uint8_t* v8,
+                                           const uint8_t* k_exp, const uint8_t* v_exp, int64_t ld_exp,
+                                           int64_t cache_rows, const int32_t* rows, uint16_t* K, int64_t ld_k,
+                                           uint16_t* V, int64_t ld_v, int64_t tokens, int32_t kv_heads, void* stream);
+
 /* The reduction step alone (the AllReduce stand-in):
  *   Y[r, c] = bf16( (residual[r, c]) + (((P_0[r,c] + P_1[r,c]) + ...) + P_{t-1}[r,c]) )
  * P: t slices of rows x cols fp32, slice i at P + i*rows*cols, row stride cols.
@@ -374,8 +434,8 @@ DOMINO_API domino_status domino_act_eval(int32_t act, const float* a, const floa
                                          float* db, int64_t n, void* stream);
 
 /* Reads and clears the device error word of every kernel of this library.  *out is
- * DOMINO_OK, DOMINO_ERR_TIMEOUT, or DOMINO_ERR_INVALID_ARG when domino_attn_packed_fwd met lengths that
- * leave its tensors; *site (nullable) receives the code of the wait that expired (or
+ * DOMINO_OK, DOMINO_ERR_TIMEOUT, or DOMINO_ERR_INVALID_ARG when a call met lengths or rows that leave
+ * its tensors; *site (nullable) receives the code of the wait that expired (or
  * DOMINO_BAD_LENGTHS_SITE).  Synchronises the device. */
 #define DOMINO_BAD_LENGTHS_SITE 0x7E0
 DOMINO_API domino_status domino_device_status(domino_handle handle, domino_status* out, int32_t* site);
@@ -403,7 +463,11 @@ typedef enum {
   DOMINO_K_LINEAR_GX = 16,  /* domino_linear_bwd: gZ . W */
   DOMINO_K_LINEAR_GW = 17,  /* domino_linear_bwd: gZ^T . X */
   DOMINO_K_ATTN_PACKED = 18, /* domino_attn_packed_fwd (its two or three kernels) */
-  DOMINO_K_COUNT = 19
+  DOMINO_K_ROTARY = 19,     /* domino_qk_rotary_fwd, and the backward without norm */
+  DOMINO_K_ROTARY_BWD = 20, /* domino_qk_rotary_bwd (its two kernels) */
+  DOMINO_K_CACHE_WRITE = 21, /* domino_cache_write */
+  DOMINO_K_CACHE_READ = 22, /* domino_cache_read */
+  DOMINO_K_COUNT = 23
 } domino_kernel_kind;
 DOMINO_API domino_status domino_timing_enable(domino_handle handle, int32_t enable);
 DOMINO_API domino_status domino_timing_reset(domino_handle handle);
