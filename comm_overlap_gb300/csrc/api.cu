@@ -90,7 +90,7 @@ const char* kernel_kind_name(int kind) {
                                                      "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj",
                                                      "ln_affine", "ln_affine_bwd", "linear_fwd", "linear_gz", "linear_gx",
                                                      "linear_gw", "attn_packed", "rotary", "rotary_bwd", "cache_write",
-                                                     "cache_read"};
+                                                     "cache_read", "attn_cached"};
   return (kind >= 0 && kind < DOMINO_K_COUNT) ? names[kind] : "kernel";
 }
 
@@ -1378,7 +1378,7 @@ domino_status domino_device_status(domino_handle H, domino_status* out, int32_t*
   DM_TRY(ready(H));
   if (!out) return fail(DOMINO_ERR_INVALID_ARG, "out is NULL");
   DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
-  int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0, c7 = 0, c8 = 0;
+  int c1 = 0, c2 = 0, c3 = 0, c4 = 0, c5 = 0, c6 = 0, c7 = 0, c8 = 0, c9 = 0;
   DM_CUDA(dm::take_gemm_fwd_error(&c1), "reading the device error word");
   DM_CUDA(dm::take_gemm_bwd_error(&c2), "reading the device error word");
   DM_CUDA(dm::take_attn_error(&c3), "reading the device error word");
@@ -1387,7 +1387,8 @@ domino_status domino_device_status(domino_handle H, domino_status* out, int32_t*
   DM_CUDA(dm::take_packed_error(&c6), "reading the device error word");
   DM_CUDA(dm::take_norm_error(&c7), "reading the device error word");
   DM_CUDA(dm::take_rotary_error(&c8), "reading the device error word");
-  const int code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : (c4 ? c4 : (c5 ? c5 : (c6 ? c6 : (c7 ? c7 : c8))))));
+  DM_CUDA(dm::take_cached_error(&c9), "reading the device error word");
+  const int code = c1 ? c1 : (c2 ? c2 : (c3 ? c3 : (c4 ? c4 : (c5 ? c5 : (c6 ? c6 : (c7 ? c7 : (c8 ? c8 : c9)))))));
   *out = code == 0 ? DOMINO_OK : (code == dm::kPackedBadLengths ? DOMINO_ERR_INVALID_ARG : DOMINO_ERR_TIMEOUT);
   if (site) *site = code;
   return DOMINO_OK;

@@ -1,7 +1,7 @@
 // ops.h -- host-side interface between the C ABI of the sublayer operators (ops_api.cu) and their
 // kernels: LayerNorm with parameters (norm.cu), the linear layer (linear.cu),
 // attention over packed sequences (packed_attention.cu), norms and rotation of queries and keys and the
-// 8-bit cache (rotary.cu).
+// 8-bit cache (rotary.cu), attention over that cache (cached_attention.cu).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -239,5 +239,32 @@ cudaError_t launch_rotary_bwd(const RotaryBwdArgs& a, float* part, int sms, cuda
 cudaError_t launch_rotary_sums(const RotaryBwdArgs& a, const float* part, int sms, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheReadArgs& a, int sms, cudaStream_t st);
 cudaError_t take_rotary_error(int* code);
+
+// ---- attention of the last tokens of each sequence over the 8-bit cache (cached_attention.cu)
+struct CachedArgs {
+  const uint16_t* Q;
+  const uint8_t* k_exp;
+  const uint8_t* v_exp;
+  const int32_t* k_start;  // n
+  const int32_t* k_len;    // n
+  uint16_t* O;
+  float* lse;              // nullable
+  int64_t ld_q, ld_o, ld_exp;
+  int32_t n, t, hq, hkv, group, cache_rows;
+  int32_t causal, partial;               // query i of t sees len - t + i + 1 keys, or all; results stay in the workspace
+  int32_t share, rows_of_block, blocks;  // cached_shape: warps on the same tiles, rows that they hold, blocks of rows
+  float scale_log2;                      // scale x log2(e)
+  int32_t err_site;
+};
+// Maps of codes, 128-byte swizzle: (128, hkv, cache_rows) in boxes (128, 1, kCachedKeys).
+constexpr int kCachedKeys = 32;
+void cached_shape(CachedArgs* a);
+// `prefix` (nullable): the arguments of the rows that all sequences share, as one sequence of n x t tokens.
+int64_t cached_scratch_bytes(const CachedArgs& a, const CachedArgs* prefix);
+// `of`: the call's own arguments where `a` is its prefix.
+cudaError_t launch_cached_attention(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, const CachedArgs* of, void* ws,
+                                    int sms, cudaStream_t st);
+cudaError_t launch_cached_join(const CachedArgs& a, const CachedArgs* prefix, void* ws, cudaStream_t st);
+cudaError_t take_cached_error(int* code);
 
 }  // namespace dm

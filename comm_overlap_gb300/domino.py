@@ -23,11 +23,12 @@ PASS_FWD, PASS_BWD, PASS_STACK, PASS_STACK_BWD, PASS_ATTN, PASS_BLOCK, PASS_FWD_
 (K_GEMM_FWD1, K_GEMM_FWD2, K_SHARD_SUM, K_LAYERNORM, K_GEMM_DGRAD_H, K_GEMM_WGRAD_B, K_GEMM_DGRAD_X,
  K_GEMM_WGRAD_A, K_LN_BWD, K_GEMM_QKV, K_ATTN, K_GEMM_OPROJ, K_LN_AFFINE,
  K_LN_AFFINE_BWD, K_LINEAR_FWD, K_LINEAR_GZ, K_LINEAR_GX, K_LINEAR_GW,
- K_ATTN_PACKED, K_ROTARY, K_ROTARY_BWD, K_CACHE_WRITE, K_CACHE_READ) = range(23)
+ K_ATTN_PACKED, K_ROTARY, K_ROTARY_BWD, K_CACHE_WRITE, K_CACHE_READ,
+ K_ATTN_CACHED) = range(24)
 KERNEL_NAMES = ["gemm_fwd1", "gemm_fwd2", "shard_sum", "layernorm", "gemm_dgrad_h", "gemm_wgrad_b",
                 "gemm_dgrad_x", "gemm_wgrad_a", "layernorm_bwd", "gemm_qkv", "attention", "gemm_oproj",
                 "ln_affine", "ln_affine_bwd", "linear_fwd", "linear_gz", "linear_gx", "linear_gw",
-                "attn_packed", "rotary", "rotary_bwd", "cache_write", "cache_read"]
+                "attn_packed", "rotary", "rotary_bwd", "cache_write", "cache_read", "attn_cached"]
 ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 
 
@@ -96,6 +97,9 @@ _SIGS = {
     "domino_cache_write": [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _S, _S, _F, _P, _P, _F, _P, _I64, _P, _P, _P, _P,
                            _P, _I64, _I64, _I64, _S, _S, _P],
     "domino_cache_read": [_P, _P, _P, _P, _P, _I64, _I64, _P, _P, _I64, _P, _I64, _I64, _S, _P],
+    "domino_attn_cached_workspace_size": [_I64, _I64, _S, _S, _S, ctypes.POINTER(_N)],
+    "domino_attn_cached_fwd": [_P, _P, _I64, _P, _P, _P, _P, _I64, _I64, _P, _P, _P, _F, _P, _I64, _P, _I64, _I64, _S, _S,
+                               _P, _N, _P],
     "domino_act_eval": [ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_int64, _P],
     "domino_device_status": [_P, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)],
     "domino_timing_enable": [_P, ctypes.c_int32],
@@ -340,6 +344,20 @@ def domino_cache_read(handle, k8, v8, k_exp, v_exp, ld_exp, cache_rows, rows, K,
                       stream=None) -> None:
     _check(lib().domino_cache_read(handle, _ptr(k8), _ptr(v8), _ptr(k_exp), _ptr(v_exp), ld_exp, cache_rows, _ptr(rows),
                                    _ptr(K), ld_k, _ptr(V), ld_v, tokens, kv_heads, _stream(stream)))
+
+
+def domino_attn_cached_workspace_size(n, t, heads, kv_heads, prefix) -> int:
+    size = _N()
+    _check(lib().domino_attn_cached_workspace_size(n, t, heads, kv_heads, prefix, ctypes.byref(size)))
+    return size.value
+
+
+def domino_attn_cached_fwd(handle, Q, ld_q, k8, v8, k_exp, v_exp, ld_exp, cache_rows, k_start, k_len, prefix, scale, O, ld_o,
+                           lse, n, t, heads, kv_heads, workspace, workspace_bytes=None, stream=None) -> None:
+    _check(lib().domino_attn_cached_fwd(handle, _ptr(Q), ld_q, _ptr(k8), _ptr(v8), _ptr(k_exp), _ptr(v_exp), ld_exp,
+                                        cache_rows, _ptr(k_start), _ptr(k_len), _ptr(prefix), scale, _ptr(O), ld_o,
+                                        _ptr(lse), n, t, heads, kv_heads, _ptr(workspace),
+                                        _nbytes(workspace, workspace_bytes), _stream(stream)))
 
 
 def domino_act_eval(act, a, b, out, da, db, n, stream=None) -> None:

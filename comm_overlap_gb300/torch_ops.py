@@ -35,9 +35,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # workspace sizes, functions of the shapes alone (a call through ctypes takes 1.3 us)
-_norm_scratch, _linear_scratch, _packed_scratch, _rotary_scratch = (functools.lru_cache(4096)(f) for f in (
+_norm_scratch, _linear_scratch, _packed_scratch, _rotary_scratch, _cached_scratch = (functools.lru_cache(4096)(f) for f in (
     dm.domino_layernorm_bwd_workspace_size, dm.domino_linear_bwd_workspace_size, dm.domino_attn_packed_workspace_size,
-    dm.domino_qk_rotary_bwd_workspace_size))
+    dm.domino_qk_rotary_bwd_workspace_size, dm.domino_attn_cached_workspace_size))
 
 
 # A workspace straight from PyTorch's allocator, on a stream as a tensor's memory would be, without a tensor around it
@@ -747,6 +747,55 @@ def cache_read(cache: tuple, rows: torch.Tensor, out: tuple | None = None) -> tu
         (k, ld_k), (v, ld_v) = (_heads_out(f"out[{i}]", x, x) for i, x in enumerate(out))
     _call(dm.domino_cache_read, rows, k8, v8, ke, ve, ld_exp, cache_rows, rows.contiguous(), k, ld_k, v, ld_v, tokens, hkv)
     return k, v
+
+
+def cached_attention(q: torch.Tensor, cache: tuple, k_start: torch.Tensor, k_len: torch.Tensor,
+                     prefix: torch.Tensor | None = None, scale: float | None = None, return_lse: bool = False,
+                     out: torch.Tensor | None = None):
+    """Attention of the last tokens of n sequences over the 8-bit cache: q [n, heads, 128], one token a sequence, or
+    [n, t, heads, 128] (bf16).
+
+    Sequence s has the k_len[s] keys from cache row k_start[s] (int32, n each, on the device); its query i of t sees the
+    first k_len[s] - t + i + 1 of them.  `prefix`: int32 [first row, rows] on the device, keys that every query of every
+    sequence sees before its own; they are read once for all.  The scale is 1 / sqrt(128) unless given.  Returns o like q,
+    or (o, lse) with lse fp32, q without its last dimension.  A query that sees no key gets zeros and -inf.  `out` may not
+    overlap q.  Lengths that leave the cache are not raised here: they are read on the device, such a sequence has no keys,
+    and `device_status` reports them.  Forward only.  Made for few tokens a sequence: for long chunks, `cache_read` and
+    `packed_attention`."""
+    _no_tangent("cached_attention", q)
+    _check("q", q)
+    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
+        raise ValueError(f"q must have shape [n, heads, {HEAD_DIM}] or [n, t, heads, {HEAD_DIM}], not {tuple(q.shape)}")
+    if torch.is_grad_enabled() and q.requires_grad:
+        raise ValueError("cached_attention has no backward: call it under torch.no_grad(), or detach its inputs")
+    n, t, hq = q.shape[0], 1 if q.dim() == 3 else q.shape[1], q.shape[-2]
+    k8, v8, ke, ve, ld_exp, cache_rows, hkv = _cache(cache, q)
+    if hq == 0 or hq % hkv:
+        raise ValueError("the query heads must be a multiple of the cache's heads")
+    _check("k_start", k_start, q, (n,), _I32)
+    _check("k_len", k_len, q, (n,), _I32)
+    if prefix is not None:
+        _check("prefix", prefix, q, (2,), _I32)
+        prefix = prefix.contiguous()
+    shape = q.shape
+    q, ld_q = _heads("q", q.reshape(n * t, hq, HEAD_DIM))
+    if out is None:
+        o = out = torch.empty(shape, dtype=_BF16, device=q.device)
+        ld_o = hq * HEAD_DIM
+    else:
+        _check("out", out, q, shape)
+        try:
+            o = out.view(n * t, hq, HEAD_DIM)
+        except RuntimeError:
+            raise ValueError("out must have tokens at one stride") from None
+        same, ld_o = _heads("out", o)
+        if same is not o:
+            raise ValueError("out must have contiguous, 16-byte aligned tokens that do not overlap")
+    lse = torch.empty(shape[:-1], dtype=_F32, device=q.device) if return_lse else None
+    _call(dm.domino_attn_cached_fwd, q, q, ld_q, k8, v8, ke, ve, ld_exp, cache_rows, k_start.contiguous(), k_len.contiguous(), prefix,
+          HEAD_DIM ** -0.5 if scale is None else scale, o, ld_o, lse, n, t, hq, hkv,
+          scratch=_cached_scratch(n, t, hq, hkv, int(prefix is not None)))
+    return (out, lse) if return_lse else out
 
 
 def device_status(device: torch.device | int | None = None) -> None:

@@ -417,6 +417,32 @@ DOMINO_API domino_status domino_cache_read(domino_handle handle, const uint8_t* 
                                            int64_t cache_rows, const int32_t* rows, uint16_t* K, int64_t ld_k,
                                            uint16_t* V, int64_t ld_v, int64_t tokens, int32_t kv_heads, void* stream);
 
+/* Attention of the last t tokens of each of n sequences over the 8-bit cache, head dimension 128: one token a
+ * sequence in decoding, a few where drafted tokens are checked.
+ *   Q, O: n x t tokens x heads x 128, row strides ld_q, ld_o; sequence s has the keys in the cache rows k_start[s] ..
+ *      k_start[s] + k_len[s] - 1 (device int32, n each); its query i of t sees the first k_len[s] - t + i + 1 of
+ *      them.  heads is a multiple of kv_heads; query head j uses key head j / (heads / kv_heads).
+ *   prefix (nullable): 2 device int32, the first row and the number of rows that every query of every sequence
+ *      sees before its own keys; they are read once for all sequences.
+ *   O = softmax(scale Q K^T over the keys a query sees) V, weights rounded to f16 (times their value's power of
+ *      two) for the product, O once from fp32.  lse (nullable): n x t x heads fp32, the logarithm of each softmax's
+ *      denominator.  A query that sees no key gets zeros and -inf.
+ * Rows that a query does not see have no effect on it, whatever their codes and exponents.  Lengths are read on
+ * the device: a sequence (or prefix) whose rows leave the cache has no keys and is recorded (domino_device_status).
+ * Exponents are those of domino_cache_write (2^-51 to 2^51).  scale: > 0, at most 8192.  Equal inputs give equal
+ * bits.  O may not overlap Q.  Any t is taken, and rows (t x heads / kv_heads) beyond 128 read the keys again.
+ * Workspace: domino_attn_cached_workspace_size() bytes, without initialisation (10 or 20 MB, and with a prefix as
+ * much again and 1056 bytes a query and head). */
+DOMINO_API domino_status domino_attn_cached_workspace_size(int64_t n, int64_t t, int32_t heads, int32_t kv_heads,
+                                                           int32_t prefix, size_t* bytes);
+DOMINO_API domino_status domino_attn_cached_fwd(domino_handle handle, const uint16_t* Q, int64_t ld_q, const uint8_t* k8,
+                                                const uint8_t* v8, const uint8_t* k_exp, const uint8_t* v_exp,
+                                                int64_t ld_exp, int64_t cache_rows, const int32_t* k_start,
+                                                const int32_t* k_len, const int32_t* prefix, float scale, uint16_t* O,
+                                                int64_t ld_o, float* lse, int64_t n, int64_t t, int32_t heads,
+                                                int32_t kv_heads, void* workspace, size_t workspace_bytes,
+                                                void* stream);
+
 /* The reduction step alone (the AllReduce stand-in):
  *   Y[r, c] = bf16( (residual[r, c]) + (((P_0[r,c] + P_1[r,c]) + ...) + P_{t-1}[r,c]) )
  * P: t slices of rows x cols fp32, slice i at P + i*rows*cols, row stride cols.
@@ -467,7 +493,8 @@ typedef enum {
   DOMINO_K_ROTARY_BWD = 20, /* domino_qk_rotary_bwd (its two kernels) */
   DOMINO_K_CACHE_WRITE = 21, /* domino_cache_write */
   DOMINO_K_CACHE_READ = 22, /* domino_cache_read */
-  DOMINO_K_COUNT = 23
+  DOMINO_K_ATTN_CACHED = 23, /* domino_attn_cached_fwd (its two or three kernels) */
+  DOMINO_K_COUNT = 24
 } domino_kernel_kind;
 DOMINO_API domino_status domino_timing_enable(domino_handle handle, int32_t enable);
 DOMINO_API domino_status domino_timing_reset(domino_handle handle);
