@@ -2,24 +2,30 @@
 // rows that all sequences share.
 //
 // Keys and values are E4M3 codes with one power of two for each row and head, so K = k8 2^a and V = v8 2^b.  The scores are
-// products of the codes times 2^a; with t = scale log2(e) q k + b and the running maximum m of t, a key weighs w = 2^(t - m) <= 1,
-// which is its softmax weight times its value's 2^b: O = sum w v8, and the denominator is sum w 2^-b.  Codes convert to f16
-// without rounding; q is scaled by a power of two for each row so that its largest value lies in [2^14, 2^15) and keeps its
-// 8 bits down to 2^-24; w is rounded to f16 (11 bits), which is finer than the bf16 of the output.  Sums are fp32.
+// products of the codes times 2^a; with t = scale log2(e) q k + b and a reference m near the maximum of t, a key weighs w = 2^(t - m),
+// which is its softmax weight times its value's 2^b: O = sum w v8, and the denominator is sum w 2^-b.
 //
-// A row of scores is a token and one of the `group` query heads of a key head.  Products are computed transposed, keys x rows
-// (mma m16n8k16: 16 keys x 8 rows, then 16 elements x 8 rows), so that 8 rows, one token of up to 8 heads, fill an instruction,
-// and a warp converts each code once.  A warp holds NT x 8 rows; `share` warps read the same tiles of 32 keys for more.
-// tcgen05 would want 128 rows; here the conversions and memory bound the kernel, not the products.
+// Both products are transposed: a tile of 128 keys is the tensor core's 128 rows (S^T = K Q^T), then the 128 elements are (O^T = V^T
+// P^T), so that codes go from memory to the tensor core as they are and few queries make a narrow product.  The narrow operand is a
+// sum of two E4M3 terms, x1 + x2 / 16, in columns of their own: x1 is x rounded, x2 the rest.  For q, scaled by a power of two for
+// each row so that its largest value lies in [2^7, 2^8), they are exact down to 2^-14 of the largest, and off by at most 2^-21 of it
+// below.  For w, which is at most 448, they are good to 2^-8, as bf16 would be, or to 2^-20 of the row's largest weight.
+// (With mma.sync, 8 rows a warp, codes have to be converted to f16, 3 - 4 clocks for two: one sequence of 262001 keys and 8 heads
+// 130 us; its E4M3 form converts them too, 175.)
 //
-// The tiles of all sequences and key heads, laid end to end, are cut into equal ranges, one for each stream of warps on the GPU.
-// A stream loads its tiles by TMA into a ring of its own.  What covers all keys of a row is written out; parts leave their m,
-// denominator and O in the workspace, and a second kernel joins them in order.
+// A row is a token and one of the `group` query heads of a key head; R of them make 2 R columns, for each 8 rows the first terms, then
+// the second.  Warps of a block: one loads K and V by TMA into a ring, one issues the products, four hold the 128 keys (then
+// elements), one a thread, which TMEM lane by lane suits: no sums across threads but at an item's end.
+//
+// The tiles of all sequences, laid end to end, are cut into equal ranges, one for each group of `abreast` blocks, which take
+// neighbouring key heads and so read a row's heads at about the same time.  What covers all keys of a row is written out; parts leave
+// their m, denominator and O in the workspace, and a second kernel joins them in order.
 // Bound: memory, 2 x 129 bytes a key and key head.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <atomic>
-#include <type_traits>
+#include <climits>
 
 #include "actfn.cuh"
 #include "ops.h"
@@ -31,28 +37,43 @@ namespace {
 
 __device__ int g_cached_err;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kThreads = 192;                      // warps: 0 loads, 1 issues, 2 - 5 the keys of a tile
 constexpr int kKeys = kCachedKeys;                 // of a tile
-constexpr int kStages = 3;
 constexpr uint32_t kTile = kKeys * 128;            // bytes of K or V
-constexpr uint32_t kStage = 2 * kTile;
-constexpr uint32_t kCtrl = 2048;
-constexpr int kSmem = 1024 + static_cast<int>(kCtrl) + kWarps * kStages * static_cast<int>(kStage);
-static_assert(kSmem <= 232448, "shared memory beyond the per-CTA limit");
-constexpr int kSms = 152;                          // CTAs that the workspace is sized for, at most
+constexpr int kSms = 152;                          // SMs that the workspace is sized for, at most
+constexpr int kMaxAbreast = 8;
 constexpr int kPart = 132;                         // floats of a partial row: 128 of O, m, denominator, two unused
+constexpr int kJoinWarps = 8;
+constexpr uint64_t kDrainNs = 200000000ull;
 
-// ---- work: tiles of all items (sequence, block of rows, key head) in order
+// For R rows: blocks of an SM, slots of the ring (a tile of K or of V each), columns of TMEM (two buffers of scores, O).
+template <int R>
+struct Shape {
+  static constexpr int kBlocks = R <= 32 ? 2 : 1;
+  static constexpr uint32_t kSlots = R == 8 ? 6 : R == 16 ? 5 : R == 32 ? 4 : 8;
+  static constexpr uint32_t kCols = 2 * R;
+  static constexpr uint32_t kTmem = R == 8 ? 64 : R == 16 ? 128 : R == 32 ? 256 : 512;
+  static constexpr uint32_t kOperand = kCols * 128;                                // bytes of Q or P, two buffers each
+  static constexpr uint32_t kCtrl = 5120;
+  static constexpr int kSmem = 1024 + static_cast<int>(kCtrl + kSlots * kTile + 4 * kOperand);
+  static_assert(kBlocks * (kSmem + 1024 + 1700) <= 233472 && 3 * kCols <= kTmem && kBlocks * kTmem <= 512, "memory of an SM");
+};
+// Weights are 2^kRaise where t is the maximum that m was taken from; the maximum may rise by kBehind (in base 2) before O and the
+// denominator are brought to a new m, so that they stay below E4M3's 448 = 2^8.807.
+constexpr float kRaise = 6.0f, kBehind = 2.8f;
+constexpr float kTerm = 0.0625f;  // of the second terms
+
+// ---- work: tiles of all items (sequence, block of rows, `abreast` key heads) in order
 
 struct CachedHeader {
   int64_t tiles;    // of all items
-  int64_t streams;  // ranges that they are cut into
+  int64_t ranges;   // that they are cut into
 };
 
 struct CachedWork {
   CachedHeader* head;
   int64_t* base;    // tiles before each sequence
-  float* slots;     // two for each stream: `rows` partial rows each
+  float* slots;     // two for each range, of R partial rows for each head abreast
   float* whole;     // partial rows of items that were not cut, by token and head (with a shared prefix)
 };
 
@@ -68,88 +89,166 @@ __device__ __forceinline__ int sequence(const CachedArgs& a, int s, int& start) 
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kKeys - 1) / kKeys; }
 
-// Where stream i's range begins, and the stream that tile x belongs to.
-__device__ __forceinline__ int64_t range_begin(int64_t i, const CachedHeader& h) { return i * h.tiles / h.streams; }
-__device__ __forceinline__ int64_t stream_of(int64_t x, const CachedHeader& h) {
-  return ((x + 1) * h.streams + h.tiles - 1) / h.tiles - 1;
+// Where range i begins, and the range that tile x belongs to.
+__device__ __forceinline__ int64_t range_begin(int64_t i, const CachedHeader& h) { return i * h.tiles / h.ranges; }
+__device__ __forceinline__ int64_t range_of(int64_t x, const CachedHeader& h) {
+  return ((x + 1) * h.ranges + h.tiles - 1) / h.tiles - 1;
 }
 
-struct Cursor {
-  int s, start, len, tiles, item, tile;  // item: block of rows x hkv + key head, of sequence s
+// An item's part in a range: keys of tiles t0 .. t1 - 1 of sequence s.
+struct Piece {
+  int s, start, len, tiles;
+  int block, head;  // block of rows, first of the key heads abreast
+  int t0, t1;
+  int64_t at;       // t0 in the order of all tiles
 };
 
-__device__ __forceinline__ void next_sequence(const CachedArgs& a, Cursor& c) {
-  c.item = c.tile = 0;
-  do {
-    ++c.s;
-    c.len = c.s < a.n ? sequence(a, c.s, c.start) : 0;
-    c.tiles = tiles_of(c.len);
-  } while (c.tiles == 0 && c.s < a.n);
+// Sets t1; false where there is none (past the range, or, where lengths change while the kernel reads them, past the sequences).
+__device__ __forceinline__ bool close_piece(const CachedArgs& a, Piece& p, int64_t hi) {
+  if (p.at >= hi || p.s >= a.n) return false;
+  const int64_t left = hi - p.at;
+  p.t1 = p.tiles - p.t0 < left ? p.tiles : p.t0 + static_cast<int>(left);
+  return true;
 }
-__device__ __forceinline__ void next_item(const CachedArgs& a, Cursor& c) {
-  c.tile = 0;
-  if (++c.item == a.blocks * a.hkv) next_sequence(a, c);
+__device__ __forceinline__ bool next_piece(const CachedArgs& a, Piece& p, int64_t hi) {
+  p.at += p.t1 - p.t0;
+  p.t0 = 0;
+  p.head += a.abreast;
+  if (p.head >= a.hkv) {
+    p.head = 0;
+    if (++p.block >= a.blocks) {
+      p.block = 0;
+      do {
+        ++p.s;
+        p.len = p.s < a.n && p.at < hi ? sequence(a, p.s, p.start) : 0;
+        p.tiles = tiles_of(p.len);
+      } while (p.tiles == 0 && p.s < a.n && p.at < hi);
+    }
+  }
+  return close_piece(a, p, hi);
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+// ---- instructions
+
+// D[tmem] (+)= A . B^T, E4M3 operands in shared memory, fp32 accumulator, 32 of the reduction.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
-// The two codes in the lower, or upper, half of w as f16.
-__device__ __forceinline__ uint32_t f16_lower(uint32_t w) {
+// Descriptor of an operand without swizzle whose rows along the reduction are pieces of 16 bytes (16 columns), one after the other; the
+// next 16 columns `stride` bytes further.  (8 rows of 16 bytes are a unit; bits 16 - 29: the distance of units along the reduction, bits
+// 32 - 45: along the columns.)
+__device__ __forceinline__ uint64_t sdesc_pieces(uint32_t saddr, uint32_t stride) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128u >> 4) << 16 |
+         static_cast<uint64_t>((stride & 0x3FFFFu) >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void key_threads_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool key_threads_any(bool x) {
   uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-  return r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
 }
-__device__ __forceinline__ uint32_t f16_upper(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t transposed(uint32_t x) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ uint32_t has_nan(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ uint32_t has_nan(const uint4& v) { return has_nan(v.x) | has_nan(v.y) | has_nan(v.z) | has_nan(v.w); }
 
-// The tile's key that index x of an instruction's 8 stands for.  Of the rows of 128 bytes under the 128-byte swizzle (16-byte piece
-// p of row r lies at p ^ (r mod 8)), K's loads take pieces 0 - 3 or 4 - 7 of rows key(2 i) and key(2 i + 1) at once, V's pieces 2 i and
-// 2 i + 1 of rows key(0), key(2), key(4), key(6) or of the others: with this order neither meets a bank twice.
-__device__ __forceinline__ int key_of(int x) { return x & 1 ? ((x - 1) ^ 4) + 1 : x; }
+__device__ __forceinline__ uint16_t e4m3_of_f16(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
+  return r;
+}
+__device__ __forceinline__ __half2 f16_of_e4m3(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return *reinterpret_cast<const __half2*>(&r);
+}
+// The two terms of x and y (at most 448 in size; f16 holds 3 bits more than the terms do).
+__device__ __forceinline__ void two_terms(float x, float y, uint32_t& first, uint32_t& second) {
+  const __half2 v = __floats2half2_rn(x, y);
+  const uint16_t f = e4m3_of_f16(v);
+  first = f;
+  second = e4m3_of_f16(__hmul2(__hsub2(v, f16_of_e4m3(f)), __float2half2_rn(16.0f)));
+}
+// A byte of a list that is read on from there: memory brings 128 bytes at a time to L2, not 32.
+__device__ __forceinline__ int load_line(const uint8_t* p) {
+  uint32_t x;
+  asm volatile("ld.global.L2::128B.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return static_cast<int>(x);
+}
 
-template <int NT>
-__global__ void __launch_bounds__(kThreads, 1)
+// A row of an item, in shared memory
+struct __align__(16) Row {
+  float scale;   // of the scores of its q, in base 2
+  float base;    // m, or 0 while there is none
+  float above;   // beyond it m moves (-inf while there is none)
+  int limit;     // keys that it sees
+};
+
+enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_COUNT = 25 };
+// Control block: barriers, then 256: TMEM address, abort flag; 512: pieces; 1024: rows of two items; 3072: four warps' maxima or sums of
+// 64 rows; 4096: factors
+constexpr uint32_t kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 3072, kFactorsAt = 4096;
+static_assert(sizeof(Piece) * 2 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "control block");
+
+template <int R>
+__global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
     cached_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const CachedArgs a,
                             const CachedWork w) {
+  using S = Shape<R>;
+  constexpr uint32_t kSlots = S::kSlots;
+  constexpr int kChunks = R / 8;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  const uint32_t ctrl = (smem_u32(smem_raw) + 1023u) & ~1023u, ring0 = ctrl + kCtrl;
-  uint8_t* const ctrl_ptr = smem_raw + (ctrl - smem_u32(smem_raw));
+  uint8_t* const smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   __shared__ int64_t before[kThreads + 1];  // tiles of one item before each thread's sequences
-  __shared__ int64_t warp_sums[kWarps];
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl_ptr + kCtrl - 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int stream_slot = warp / a.share, member = warp - stream_slot * a.share, slots = kWarps / a.share;
-  const uint32_t bars = ctrl + 64u * static_cast<uint32_t>(stream_slot);
-  const uint32_t ring = ring0 + static_cast<uint32_t>(stream_slot * kStages) * kStage;
-  if (threadIdx.x == 0) *abort_flag = 0;
-  if (member == 0 && lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8u * i, 1);
+  __shared__ int64_t warp_sums[kThreads / 32];
+  const uint32_t bar0 = smem_u32(smem), ring = bar0 + S::kCtrl, q_at = ring + kSlots * kTile, p_at = q_at + 2 * S::kOperand;
+  auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 256);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 260);
+  Piece* pieces = reinterpret_cast<Piece*>(smem + kPiecesAt);
+  Row* all_rows = reinterpret_cast<Row*>(smem + kRowsAt);
+  float* sums = reinterpret_cast<float*>(smem + kSumsAt);
+  float* factors = reinterpret_cast<float*>(smem + kFactorsAt);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int* err = &g_cached_err;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_Q_FULL && i < B_PV_DONE && !(i >= B_S_FULL && i < B_P_FULL) ? 4 : 1);
+    *abort_flag = 0;
     fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), S::kTmem);
+    tmem_relinquish();
   }
   pdl_launch();
   pdl_wait();
 
-  // ---- the plan, by every block for itself: tiles before each thread's range of sequences
+  // ---- the plan, by every block for itself: tiles before each thread's sequences
   const int per = (a.n + kThreads - 1) / kThreads, s0 = min(static_cast<int>(threadIdx.x) * per, a.n), s1 = min(s0 + per, a.n);
   int64_t mine = 0;
   for (int s = s0; s < s1; ++s) {
@@ -166,19 +265,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < kThreads / 32; ++i) {
     if (i == warp) sum += total;
     total += warp_sums[i];
   }
   before[threadIdx.x] = sum - mine;
   if (threadIdx.x == 0) before[kThreads] = total;
+  tc_fence_before();
   __syncthreads();
-  const int64_t items = static_cast<int64_t>(a.blocks) * a.hkv;  // of a sequence
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t items = static_cast<int64_t>(a.blocks) * (a.hkv / a.abreast);  // of a sequence
   CachedHeader h;
   h.tiles = total * items;
   {
-    const int64_t most = static_cast<int64_t>(gridDim.x) * slots;
-    h.streams = h.tiles < most ? (h.tiles > 0 ? h.tiles : 1) : most;
+    const int64_t most = gridDim.x / a.abreast;
+    h.ranges = h.tiles < most ? (h.tiles > 0 ? h.tiles : 1) : most;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *w.head = h;
   if (threadIdx.x % gridDim.x == blockIdx.x) {  // for the second kernel
@@ -189,22 +291,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += static_cast<int64_t>(tiles_of(sequence(a, s, start))) * items;
     }
   }
-
-  const int64_t stream = static_cast<int64_t>(stream_slot) * gridDim.x + blockIdx.x;
-  if (stream >= h.streams || h.tiles == 0) return;  // (all warps of a stream)
-  const int64_t lo = range_begin(stream, h), hi = range_begin(stream + 1, h);
-  Cursor at;
-  {
-    // the thread whose sequences hold tile lo, then the sequence, 32 at a time
+  const int lane_head = blockIdx.x % a.abreast;  // of the heads abreast
+  const int64_t range = blockIdx.x / a.abreast;
+  const bool work = h.tiles > 0 && range < h.ranges;
+  const int64_t lo = work ? range_begin(range, h) : 0, hi = work ? range_begin(range + 1, h) : 0;
+  if (work && warp == 2) {  // the range's first piece: the thread whose sequences hold tile lo, then the sequence, 32 at a time
     int x = 0;
-    for (int step = kThreads / 2; step > 0; step >>= 1)
-      if (before[x + step] * items <= lo) x += step;
+    for (int step = 128; step > 0; step >>= 1)
+      if (x + step < kThreads && before[x + step] * items <= lo) x += step;
     int64_t done = before[x] * items;
-    at.s = min(x * per, a.n);
-    at.len = at.start = at.tiles = at.item = at.tile = 0;
-    for (; at.s < a.n; at.s += 32) {
+    Piece p = {};
+    p.at = lo;
+    p.s = min(x * per, a.n);
+    for (; p.s < a.n; p.s += 32) {
       int start = 0;
-      const int len = at.s + lane < a.n ? sequence(a, at.s + lane, start) : 0;
+      const int len = p.s + lane < a.n ? sequence(a, p.s + lane, start) : 0;
       int64_t upto = tiles_of(len);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -214,329 +315,405 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t past = __ballot_sync(0xFFFFFFFFu, done + upto * items > lo);
       if (past) {
         const int l = __ffs(past) - 1;
-        at.len = __shfl_sync(0xFFFFFFFFu, len, l);
-        at.start = __shfl_sync(0xFFFFFFFFu, start, l);
-        at.tiles = tiles_of(at.len);
-        done += (__shfl_sync(0xFFFFFFFFu, upto, l) - at.tiles) * items;
-        at.s += l;
+        p.len = __shfl_sync(0xFFFFFFFFu, len, l);
+        p.start = __shfl_sync(0xFFFFFFFFu, start, l);
+        p.tiles = tiles_of(p.len);
+        done += (__shfl_sync(0xFFFFFFFFu, upto, l) - p.tiles) * items;
+        p.s += l;
         break;
       }
       done += __shfl_sync(0xFFFFFFFFu, upto, 31) * items;
     }
-    if (at.tiles > 0) {
-      at.item = static_cast<int>((lo - done) / at.tiles);
-      at.tile = static_cast<int>((lo - done) - static_cast<int64_t>(at.item) * at.tiles);
+    if (p.tiles > 0) {
+      const int item = static_cast<int>((lo - done) / p.tiles), subs = a.hkv / a.abreast;
+      p.block = item / subs;
+      p.head = (item - p.block * subs) * a.abreast;
+      p.t0 = static_cast<int>((lo - done) - static_cast<int64_t>(item) * p.tiles);
     }
+    if (!close_piece(a, p, hi)) p.t1 = p.t0;  // (only where lengths change meanwhile)
+    if (lane == 0) pieces[0] = p;
   }
+  __syncthreads();
+  const int rows_of_sequence = a.t * a.group;
 
-  // ---- loads: tile by tile, kStages ahead; the lanes keep their key's two exponents
-  Cursor ahead = at;
-  int64_t loads_left = hi - lo;
-  int issued = 0;
-  int exps[kStages];
-  bool ok = true;
-  auto load = [&]() -> int {
-    if (loads_left == 0) return 0;
-    --loads_left;
-    const int head = ahead.item % a.hkv, row = ahead.start + ahead.tile * kKeys;
-    if (member == 0 && elect_one() && ok) {
-      const int stage = issued % kStages;
-      const uint32_t bar = bars + 8u * stage, to = ring + static_cast<uint32_t>(stage) * kStage;
-      mbar_arrive_expect_tx(bar, kStage);
-      tma_load_3d(to, &map_k, bar, 0, head, row);
-      tma_load_3d(to + kTile, &map_v, bar, 0, head, row);
-    }
-    ++issued;
-    int e = 0;
-    if (row + lane < a.cache_rows) {
-      const int64_t x = head * a.ld_exp + row + lane;
-      e = static_cast<int>(a.k_exp[x]) | static_cast<int>(a.v_exp[x]) << 8;
-    }
-    if (++ahead.tile == ahead.tiles) next_item(a, ahead);
-    return e;
-  };
+  if (work && warp == 0) {
+    // ---------------- loads: K and V of one tile after the other
+    Piece p = pieces[0];
+    uint32_t slot = 0, round = 0;
+    const bool one = elect_one();
+    bool ok = true, more = p.t1 > p.t0;
+    while (more && ok) {
+      for (int tile = p.t0; tile < p.t1 && ok; ++tile) {
+        const int row = p.start + tile * kKeys;
 #pragma unroll
-  for (int i = 0; i < kStages; ++i) exps[i] = load();
-
-  const int kg = key_of(g), ka = key_of(2 * c), kb = key_of(2 * c + 1);
-  const uint32_t k_lo = kg * 128 + ((c ^ kg) << 4), k_hi = kg * 128 + (((c + 4) ^ kg) << 4);
-  const uint32_t v_a = kTile + ka * 128 + ((g ^ ka) << 4), v_b = kTile + kb * 128 + ((g ^ kb) << 4);
-  auto release = [&] {  // the stream's warps have read a tile
-    if (a.share == 1)
+        for (int value = 0; value < 2; ++value) {
+          if (round > 0) ok = ok && mbar_wait(bar(B_EMPTY + slot), (round - 1) & 1u, abort_flag, err, a.err_site + 1);
+          if (ok && one) {
+            mbar_arrive_expect_tx(bar(B_FULL + slot), kTile);
+            tma_load_3d(ring + slot * kTile, value ? &map_v : &map_k, bar(B_FULL + slot), 0, p.head + lane_head, row);
+          }
+          if (++slot == kSlots) {
+            slot = 0;
+            ++round;
+          }
+        }
+      }
+      more = next_piece(a, p, hi);
+    }
+    if (!ok) {  // copies in flight land before the block leaves
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 100000ull) {
+      }
+    }
+  } else if (work && warp == 1) {
+    // ---------------- products: S of a tile while the one before it is weighed, then O += V^T P of that
+    const bool one = elect_one();
+    const uint64_t ring_desc = sdesc_sw128(ring, 16, 1024);
+    bool ok = true;
+    auto wait = [&](int b, uint32_t parity, int site) {  // the same in the whole warp
+      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(b), parity & 1u, abort_flag, err, a.err_site + site));
+    };
+    Piece p = pieces[0];
+    int tile = p.t0;
+    bool more = p.t1 > p.t0;
+    uint32_t item = 0, made = 0, slot_k = 0, round_k = 0, slot_v = 1, round_v = 0;
+    uint32_t columns = 0, columns_before = 0;  // of the last tile and of the one before it; bit 31: the item's first
+    auto advance = [](uint32_t& slot, uint32_t& round) {
+      slot += 2;
+      if (slot >= kSlots) {
+        slot -= kSlots;
+        ++round;
+      }
+    };
+    auto scores = [&] {
+      if (tile == p.t0) wait(B_Q_FULL + (item & 1u), item >> 1, 2);
+      wait(B_FULL + slot_k, round_k, 3);
+      columns_before = columns;
+      columns = 16u * static_cast<uint32_t>((min(R, rows_of_sequence - p.block * R) + 7) >> 3);
+      tc_fence_after();
+      if (ok && one) {
+        const uint32_t id = idesc_e4m3_f32(128, static_cast<int>(columns), false, false);
+        const uint64_t dk = ring_desc + ((slot_k * kTile) >> 4), dq = sdesc_sw128(q_at + (item & 1u) * S::kOperand, 16, 1024);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) umma_f8(tmem + (made & 1u) * S::kCols, dk + 2 * k, dq + 2 * k, id, k != 0);
+        umma_commit(bar(B_S_FULL + (made & 1u)));
+        umma_commit(bar(B_EMPTY + slot_k));
+      }
       __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(stream_slot + 1), "r"(a.share * 32) : "memory");
-  };
-  int consumed = 0;
-  for (int64_t x = lo; x < hi;) {
-    if (at.s >= a.n) {  // (only where lengths change while the kernel reads them)
-      for (; x < hi; ++x) release();
-      break;
+      if (tile == p.t0) columns |= 1u << 31;
+      advance(slot_k, round_k);
+      ++made;
+      if (++tile == p.t1) {
+        more = next_piece(a, p, hi);
+        tile = p.t0;
+        ++item;
+      }
+    };
+    if (more) scores();
+    for (uint32_t j = 0; j < made && ok; ++j) {
+      const bool last = !more;
+      if (!last) scores();
+      const uint32_t mine = last ? columns : columns_before;
+      wait(B_P_FULL + (j & 1u), j >> 1, 4);
+      wait(B_FULL + slot_v, round_v, 5);
+      tc_fence_after();
+      if (ok && one) {
+        const uint32_t id = idesc_e4m3_f32(128, static_cast<int>(mine & 0xFFFFu), true, true);
+        const uint64_t dv = ring_desc + ((slot_v * kTile) >> 4), dp = sdesc_pieces(p_at + (j & 1u) * S::kOperand, kKeys * 16);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+          umma_f8(tmem + 2 * S::kCols, dv + k * (4096u >> 4), dp + k * (512u >> 4), id, !(mine >> 31 && k == 0));
+        umma_commit(bar(B_PV_DONE + (j & 1u)));
+        umma_commit(bar(B_EMPTY + slot_v));
+      }
+      __syncwarp();
+      advance(slot_v, round_v);
     }
-    // ---- one item: rows block * rows .. of the sequence, keys of tiles at.tile .. last - 1
-    const int block = at.item / a.hkv, head = at.item - block * a.hkv;
-    const int last = static_cast<int>(min(static_cast<int64_t>(at.tiles), at.tile + (hi - x)));
-    const int row0 = (block * a.share + member) * NT * 8, rows = a.t * a.group;
-    const bool idle = row0 >= rows;
-    uint32_t q[NT][8][2];
-    float row_scale[NT][2];
-    int limit[NT][2];
-    int least = at.len;  // keys that every row of the warp sees
+    if (one) umma_commit(bar(B_DRAIN));
+    __syncwarp();
+    const uint64_t t0 = global_timer_ns();  // what was issued ends before the block frees its memory, whatever happened
+    while (!mbar_try_wait(bar(B_DRAIN), 0) && global_timer_ns() - t0 < kDrainNs) {
+    }
+  } else if (work) {
+    // ---------------- keys: a thread has one key of each tile, and one element of O, both the number of its TMEM lane.  After a wait
+    // that ran out these warps go on (every later one ends at once), so that they meet at their barriers, but write nothing.
+    const int x = threadIdx.x - 64, quarter = (warp & 3) * 32, me = quarter + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 16);
+    bool ok = true;
+    auto wait = [&](int b, uint32_t parity, int site) {
+      ok = mbar_wait(bar(b), parity & 1u, abort_flag, err, a.err_site + site) && ok;
+    };
+    // an item's rows: 16 threads a row have 8 values each, of 8 rows at a time
+    auto fetch = [&](const Piece& p, uint4 (&u)[kChunks]) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + g;
-      float v[2][16];
-      if (r < rows) {
-        const int token = r / a.group;
-        const uint16_t* p = a.Q + (static_cast<int64_t>(at.s) * a.t + token) * a.ld_q + (head * a.group + r - token * a.group) * 128;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint4* u = reinterpret_cast<const uint4*>(p + half * 64 + c * 16);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint4 y = u[i];
-            v[half][8 * i + 0] = bf16lo(y.x); v[half][8 * i + 1] = bf16hi(y.x);
-            v[half][8 * i + 2] = bf16lo(y.y); v[half][8 * i + 3] = bf16hi(y.y);
-            v[half][8 * i + 4] = bf16lo(y.z); v[half][8 * i + 5] = bf16hi(y.z);
-            v[half][8 * i + 6] = bf16lo(y.w); v[half][8 * i + 7] = bf16hi(y.w);
-          }
+      for (int c = 0; c < kChunks; ++c) {
+        const int r = p.block * R + c * 8 + (x >> 4);
+        u[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows_of_sequence) {
+          const int token = r / a.group;
+          const uint16_t* q = a.Q + (static_cast<int64_t>(p.s) * a.t + token) * a.ld_q +
+                              (static_cast<int64_t>(p.head + lane_head) * a.group + r - token * a.group) * 128;
+          u[c] = reinterpret_cast<const uint4*>(q)[x & 15];
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.0f;
       }
-      float amax = 0.0f;
+    };
+    // ... which go to shared memory in two terms
+    auto prepare = [&](const Piece& p, const uint4 (&u)[kChunks], uint32_t item) {
+      const uint32_t to = q_at + (item & 1u) * S::kOperand;
+      Row* rows = all_rows + (item & 1u) * R;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fmaxf(fabsf(v[0][i]), fabsf(v[1][i])));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-      // 2^up brings the largest into [2^14, 2^15) (an infinity stays one)
-      const int up = amax > 0.0f && amax < INFINITY ? min(14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120) : 0;
-      const float f = __int_as_float((up + 127) << 23);
+      for (int c = 0; c < kChunks; ++c) {
+        const int n = x >> 4, piece = x & 15, r = p.block * R + c * 8 + n;
+        const float v[8] = {bf16lo(u[c].x), bf16hi(u[c].x), bf16lo(u[c].y), bf16hi(u[c].y),
+                            bf16lo(u[c].z), bf16hi(u[c].z), bf16lo(u[c].w), bf16hi(u[c].w)};
+        float amax = 0.0f;
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        const float* y = v[s >> 2] + 4 * (s & 3);
-        q[nt][s][0] = pack_f16x2(y[0] * f, y[1] * f);
-        q[nt][s][1] = pack_f16x2(y[2] * f, y[3] * f);
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+        // 2^up brings the largest into [2^7, 2^8) (an infinity becomes NaN, as its scores would)
+        const int up = amax > 0.0f && amax < INFINITY ? min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120) : 0;
+        const float f = amax < INFINITY ? __int_as_float((up + 127) << 23) : NAN;
+        uint32_t one[4], two[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) two_terms(v[2 * i] * f, v[2 * i + 1] * f, one[i], two[i]);
+        // columns 16 c + n (first terms) and 16 c + 8 + n (second): rows of 128 bytes under the 128-byte swizzle
+        const uint32_t at = to + static_cast<uint32_t>(c * 2048 + n * 128 + (((piece >> 1) ^ n) << 4) + (piece & 1) * 8);
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
+        if (piece == 0) {
+          const int limit = r >= rows_of_sequence ? 0 : a.causal ? p.len - a.t + r / a.group + 1 : p.len;
+          rows[c * 8 + n] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, -INFINITY, limit};
+        }
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {  // this lane's columns: rows 2 c and 2 c + 1
-        const int rj = row0 + nt * 8 + 2 * c + j;
-        const int up_j = __shfl_sync(0xFFFFFFFFu, up, 4 * (2 * c + j));
-        row_scale[nt][j] = a.scale_log2 * __int_as_float((127 - up_j) << 23);
-        limit[nt][j] = a.causal && rj < rows ? at.len - a.t + rj / a.group + 1 : at.len;
-        least = min(least, limit[nt][j]);
-      }
-    }
-    least = __reduce_min_sync(0xFFFFFFFFu, least);
-    float o[8][NT][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.0f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        m[nt][j] = -INFINITY;
-        l[nt][j] = 0.0f;
-      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_Q_FULL + (item & 1u)));
+    };
+    auto exponents = [&](const Piece& p, int tile) -> int {
+      const int in = tile * kKeys + me;
+      if (in >= p.len) return 127 | 127 << 8;  // (what lies past the keys may be anything)
+      const int64_t i = (p.head + lane_head) * a.ld_exp + p.start + in;
+      return load_line(a.k_exp + i) | load_line(a.v_exp + i) << 8;
+    };
 
-    for (int tile = at.tile; tile < last; ++tile) {
-      const int stage = consumed % kStages;
-      const uint32_t kv = ring + static_cast<uint32_t>(stage) * kStage;
-      ok = mbar_wait(bars + 8u * stage, (consumed / kStages) & 1, abort_flag, &g_cached_err, a.err_site) && ok;
-      ++consumed;
-      if (!idle) {
-        const int key0 = tile * kKeys, e = key0 + lane < at.len ? exps[0] : 127 | 127 << 8;
-        float acc[2][NT][4], key_scale[2][2], bias[2][2], unbias[2][2];
+    uint4 u[kChunks];
+    Piece p = pieces[0], next = p;
+    bool more = p.t1 > p.t0, another = false;
+    int exps = 0;
+    if (more) {
+      exps = exponents(p, p.t0);
+      fetch(p, u);
+      prepare(p, u, 0);
+    }
+    uint32_t j = 0, slot_v = 1, round_v = 0;  // tiles so far; V's place in the ring
+    key_threads_sync();                       // the rows are there
+    for (uint32_t item = 0; more; ++item) {
+      Row* rows = all_rows + (item & 1u) * R;
+      const int count = min(R, rows_of_sequence - p.block * R), chunks = (count + 7) >> 3;
+      const int least = a.causal ? p.len - a.t + p.block * R / a.group + 1 : p.len;  // keys that every row sees
+      int nan_key = INT_MAX;  // the first key, of those that not all rows see, with NaN in this thread's element
+      float l[R];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.0f;
-          const uint32_t p = kv + mt * 2048u;
-          const uint4 x0 = ld_shared_v4(p + k_lo), x1 = ld_shared_v4(p + k_lo + 1024u);
-          const uint4 y0 = ld_shared_v4(p + k_hi), y1 = ld_shared_v4(p + k_hi + 1024u);
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            const uint32_t u = word_of(s < 4 ? x0 : y0, s & 3), v = word_of(s < 4 ? x1 : y1, s & 3);
-            const uint32_t a0 = f16_lower(u), a1 = f16_lower(v), a2 = f16_upper(u), a3 = f16_upper(v);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(acc[mt][nt], a0, a1, a2, a3, q[nt][s][0], q[nt][s][1]);
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {  // keys g and g + 8 of the instruction
-            const int both = __shfl_sync(0xFFFFFFFFu, e, mt * 16 + i * 8 + kg), b = both >> 8;
-            key_scale[mt][i] = __int_as_float((both & 255) << 23);
-            bias[mt][i] = static_cast<float>(b - 127);
-            unbias[mt][i] = __int_as_float((254 - b) << 23);
-          }
+      for (int r = 0; r < R; ++r) l[r] = 0.0f;
+
+      for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
+        const bool first = tile == p.t0, only = p.t1 == p.t0 + 1;
+        int next_exps = 0;
+        if (tile + 1 < p.t1)
+          next_exps = exponents(p, tile + 1);
+        else if (!first && another)
+          next_exps = exponents(next, next.t0);
+        if (first && x == 0) {  // one thread finds the next item, all take it from shared memory
+          Piece n = p;
+          if (!next_piece(a, n, hi)) n.t1 = n.t0;
+          pieces[(item + 1) & 1u] = n;
         }
+        const int key0 = tile * kKeys;
         const bool tail = key0 + kKeys > least;
+        const float key_scale = __int_as_float((exps & 255) << 23), bias = static_cast<float>((exps >> 8) - 127);
+        const float unbias = __int_as_float((254 - (exps >> 8)) << 23);
+        const uint32_t from = lanes + (j & 1u) * S::kCols;
+        wait(B_S_FULL + (j & 1u), j >> 1, 6);
+        tc_fence_after();
+        float t[R];
+        bool above = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float t = fmaf(acc[mt][nt][i] * key_scale[mt][i >> 1], row_scale[nt][i & 1], bias[mt][i >> 1]);
-              if (tail && key0 + mt * 16 + (i >> 1) * 8 + kg >= limit[nt][i & 1]) t = -INFINITY;
-              acc[mt][nt][i] = t;
-            }
-        // running maximum
-        bool moved = false;
-        float factor[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(fmaxf(acc[0][nt][j], acc[0][nt][2 + j]), fmaxf(acc[1][nt][j], acc[1][nt][2 + j]));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            top = fmaxf(top, m[nt][j]);
-            factor[nt][j] = top == m[nt][j] ? 1.0f : ex2_approx(m[nt][j] - top);
-            moved |= top != m[nt][j];
-            m[nt][j] = top;
-          }
-        if (__any_sync(0xFFFFFFFFu, moved)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            l[nt][0] *= factor[nt][0];
-            l[nt][1] *= factor[nt][1];
+        for (int c = 0; c < kChunks; ++c) {
+          if (c < chunks) {
+            uint32_t y[16];
+            tmem_ld16(from + 16u * c, y);
+            tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              o[i][nt][0] *= factor[nt][0];
-              o[i][nt][1] *= factor[nt][1];
-              o[i][nt][2] *= factor[nt][0];
-              o[i][nt][3] *= factor[nt][1];
+              const Row row = rows[8 * c + i];
+              float z = fmaf(fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i])) * key_scale, row.scale, bias);
+              if (tail && key0 + me >= row.limit) z = -INFINITY;
+              above |= z > row.above;
+              t[8 * c + i] = z;
             }
           }
         }
-        uint32_t p[2][NT][2];  // weights in f16, rows 2 c and 2 c + 1, of keys g and g + 8
+        if (key_threads_any(above)) {
+          // the rows' maxima; where one is well above m, m moves
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+          for (int c = 0; c < kChunks; ++c)
+            if (c < chunks) {
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float w0 = ex2_approx(acc[mt][nt][2 * i] - m0), w1 = ex2_approx(acc[mt][nt][2 * i + 1] - m1);
-              l[nt][0] = fmaf(w0, unbias[mt][i], l[nt][0]);
-              l[nt][1] = fmaf(w1, unbias[mt][i], l[nt][1]);
-              p[mt][nt][i] = pack_f16x2(w0, w1);
+              for (int i = 0; i < 8; ++i) {
+                const float z = t[8 * c + i];
+                const int bits = __float_as_int(z == z ? z : -INFINITY);
+                const int top = __reduce_max_sync(0xFFFFFFFFu, bits ^ ((bits >> 31) & 0x7FFFFFFF));  // (ordered as the floats are)
+                if (lane == 0) sums[(warp & 3) * R + 8 * c + i] = __int_as_float(top ^ ((top >> 31) & 0x7FFFFFFF));
+              }
             }
-        }
-        // O += V^T P; `only`: for the rows that see `sees` keys alone (a weight of zero times NaN must not reach the others)
-        auto add_values = [&](int mt, const uint4& xa, const uint4& xb, const uint4& ya, const uint4& yb, auto only, int sees) {
-          uint32_t b[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            b[nt][0] = transposed(p[mt][nt][0]);
-            b[nt][1] = transposed(p[mt][nt][1]);
+          key_threads_sync();
+          if (x < 8 * chunks) {
+            const float top = fmaxf(fmaxf(sums[x], sums[R + x]), fmaxf(sums[2 * R + x], sums[3 * R + x]));
+            Row row = rows[x];
+            float f = 1.0f;
+            if (top > row.above) {
+              f = row.above == -INFINITY ? 0.0f : ex2_approx(row.base - (top - kRaise));
+              row.base = top - kRaise;
+              row.above = top + kBehind;
+              rows[x] = row;
+            }
+            factors[x] = f;
           }
+          key_threads_sync();
+          if (!first) {
+            wait(B_PV_DONE + ((j - 1) & 1u), (j - 1) >> 1, 7);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (c < chunks) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) l[8 * c + i] *= factors[8 * c + i];
+              if (!first) {
+                uint32_t y[16];
+                tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float f = factors[8 * c + i];
+                  y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                  y[8 + i] = __float_as_uint(__uint_as_float(y[8 + i]) * f);
+                }
+                tmem_st16(lanes + 2 * S::kCols + 16u * c, y);
+              }
+            }
+          if (!first) tmem_st_wait();
+        }
+        // weights, in two terms: 16 bytes a key for 8 rows
+        if (j >= 2) wait(B_PV_DONE + (j & 1u), (j - 2) >> 1, 8);
+        const uint32_t to = p_at + (j & 1u) * S::kOperand + static_cast<uint32_t>(me) * 16u;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (c < chunks) {
+            uint32_t one[4], two[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * c + 2 * i;
+              const float w0 = ex2_approx(t[r] - rows[r].base), w1 = ex2_approx(t[r + 1] - rows[r + 1].base);
+              l[r] = fmaf(w0, unbias, l[r]);
+              l[r + 1] = fmaf(w1, unbias, l[r + 1]);
+              two_terms(w0, w1, one[i], two[i]);
+            }
+            st_shared_v4(to + c * (kKeys * 16u), one[0] | one[1] << 16, one[2] | one[3] << 16, two[0] | two[1] << 16, two[2] | two[3] << 16);
+          }
+        if (tail) {
+          // values past the sequence's keys count as zero, NaN included; so does NaN among keys that some rows do not see, and the
+          // rows that do get it at the item's end
+          wait(B_FULL + slot_v, round_v, 9);
+          const uint32_t v_at = ring + slot_v * kTile;
+          const int end = p.len - key0;
+          for (int r = max(end, 0) + (x >> 3); r < kKeys; r += 16) st_shared_v4(v_at + static_cast<uint32_t>(r * 128 + (x & 7) * 16), 0u, 0u, 0u, 0u);
+          for (int r = max(least - key0, 0); r < min(end, kKeys); ++r) {
+            const uint32_t at = v_at + static_cast<uint32_t>(r * 128 + (((me >> 4) ^ (r & 7)) << 4) + (me & 15));
+            uint16_t code;
+            asm volatile("{\n\t.reg .b32 v;\n\tld.shared.u8 v, [%1];\n\tcvt.u16.u32 %0, v;\n\t}" : "=h"(code) : "r"(at) : "memory");
+            if ((code & 0x7F) == 0x7F) {
+              nan_key = min(nan_key, key0 + r);
+              asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(0u) : "memory");
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P_FULL + (j & 1u)));
+        slot_v += 2;
+        if (slot_v >= kSlots) {
+          slot_v -= kSlots;
+          ++round_v;
+        }
+        if (first) {
+          next = pieces[(item + 1) & 1u];
+          another = next.t1 > next.t0;
+          if (another) {
+            fetch(next, u);
+            if (only) next_exps = exponents(next, next.t0);
+          }
+        }
+        if (another && (only || tile == p.t0 + 1)) prepare(next, u, item + 1);
+        exps = next_exps;
+      }
+
+      // ---- what the piece's keys came to
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        if (c < chunks) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t sel = i & 1 ? 0x7362u : 0x5140u;
-            const uint32_t u = __byte_perm(word_of(xa, i >> 1), word_of(xb, i >> 1), sel);
-            const uint32_t v = __byte_perm(word_of(ya, i >> 1), word_of(yb, i >> 1), sel);
-            const uint32_t a0 = f16_lower(u), a1 = f16_upper(u), a2 = f16_lower(v), a3 = f16_upper(v);
+            float v = l[8 * c + i];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float k0 = o[i][nt][0], k1 = o[i][nt][1], k2 = o[i][nt][2], k3 = o[i][nt][3];
-              mma16816(o[i][nt], a0, a1, a2, a3, b[nt][0], b[nt][1]);
-              if (decltype(only)::value) {
-                if (limit[nt][0] != sees) {
-                  o[i][nt][0] = k0;
-                  o[i][nt][2] = k2;
-                }
-                if (limit[nt][1] != sees) {
-                  o[i][nt][1] = k1;
-                  o[i][nt][3] = k3;
-                }
-              }
-            }
-          }
-        };
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          const uint32_t at_v = kv + mt * 2048u;
-          uint4 xa = ld_shared_v4(at_v + v_a), xb = ld_shared_v4(at_v + v_b);
-          uint4 ya = ld_shared_v4(at_v + v_a + 1024u), yb = ld_shared_v4(at_v + v_b + 1024u);
-          if (tail) {
-            const int k0 = key0 + mt * 16;
-            if (k0 + ka >= at.len) xa = zero;  // what lies past the sequence's keys has no effect, NaN included
-            if (k0 + kb >= at.len) xb = zero;
-            if (k0 + ka + 8 >= at.len) ya = zero;
-            if (k0 + kb + 8 >= at.len) yb = zero;
-            // NaN among values that some rows see and some do not: each token's rows by themselves
-            if (least < at.len && __any_sync(0xFFFFFFFFu, has_nan(xa) | has_nan(xb) | has_nan(ya) | has_nan(yb))) {
-              const int first = row0 / a.group, end = (min(row0 + NT * 8, rows) - 1) / a.group;
-              for (int token = first; token <= end; ++token) {
-                const int sees = at.len - a.t + token + 1;
-                add_values(mt, k0 + ka < sees ? xa : zero, k0 + kb < sees ? xb : zero, k0 + ka + 8 < sees ? ya : zero,
-                           k0 + kb + 8 < sees ? yb : zero, std::true_type(), sees);
-              }
-              continue;
-            }
-          }
-          add_values(mt, xa, xb, ya, yb, std::false_type(), 0);
-        }
-      }
-      release();  // the tile's place takes the next one
-#pragma unroll
-      for (int i = 0; i + 1 < kStages; ++i) exps[i] = exps[i + 1];
-      exps[kStages - 1] = load();
-    }
-
-    // ---- what the item's keys came to
-    const bool all = at.tile == 0 && last == at.tiles;
-    x += last - at.tile;
-    if (!idle && ok) {
-      const int64_t begin = x - last;  // the item's first tile
-      float* slot = w.slots + (2 * stream + (begin > lo ? 1 : 0)) * (static_cast<int64_t>(a.share) * NT * 8 * kPart);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float den = l[nt][j];
-          den += __shfl_xor_sync(0xFFFFFFFFu, den, 4);
-          den += __shfl_xor_sync(0xFFFFFFFFu, den, 8);
-          den += __shfl_xor_sync(0xFFFFFFFFu, den, 16);
-          const int in_warp = nt * 8 + 2 * c + j, r = row0 + in_warp;
-          if (r >= rows) continue;
-          const int token = r / a.group;
-          const int64_t row = static_cast<int64_t>(at.s) * a.t + token;
-          const int qh = head * a.group + r - token * a.group;
-          if (all && !a.partial) {
-            const bool some = den > 0.0f || den != den;
-            const float inv = some ? 1.0f / den : 0.0f;
-            uint4* y = reinterpret_cast<uint4*>(a.O + row * a.ld_o + static_cast<int64_t>(qh) * 128 + 16 * g);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              y[i] = make_uint4(pack_bf16x2(o[4 * i][nt][j] * inv, o[4 * i][nt][2 + j] * inv),
-                                pack_bf16x2(o[4 * i + 1][nt][j] * inv, o[4 * i + 1][nt][2 + j] * inv),
-                                pack_bf16x2(o[4 * i + 2][nt][j] * inv, o[4 * i + 2][nt][2 + j] * inv),
-                                pack_bf16x2(o[4 * i + 3][nt][j] * inv, o[4 * i + 3][nt][2 + j] * inv));
-            if (g == 0 && a.lse) a.lse[row * a.hq + qh] = some ? (m[nt][j] + log2f(den)) * 0.69314718055994531f : -INFINITY;
-          } else {
-            float* y = all ? w.whole + (row * a.hq + qh) * kPart : slot + (member * NT * 8 + in_warp) * kPart;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(y + 16 * g + 4 * i) =
-                  make_float4(o[2 * i][nt][j], o[2 * i][nt][2 + j], o[2 * i + 1][nt][j], o[2 * i + 1][nt][2 + j]);
-            if (g == 0) *reinterpret_cast<float2*>(y + 128) = make_float2(m[nt][j], den);
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (lane == 0) sums[(warp & 3) * R + 8 * c + i] = v;
           }
         }
+      key_threads_sync();
+      wait(B_PV_DONE + ((j - 1) & 1u), (j - 1) >> 1, 10);
+      tc_fence_after();
+      const bool all = p.t0 == 0 && p.t1 == p.tiles, out = all && !a.partial;
+      const int64_t begin = p.at - p.t0;  // the item's first tile
+      float* slot = w.slots + ((2 * range + (begin > lo ? 1 : 0)) * a.abreast + lane_head) * static_cast<int64_t>(R * kPart);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        if (c < chunks) {
+          uint32_t y[16];
+          tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int in = 8 * c + i, r = p.block * R + in;
+            if (in >= count || !ok) continue;
+            const float den = (sums[in] + sums[R + in]) + (sums[2 * R + in] + sums[3 * R + in]);
+            const float m = rows[in].above == -INFINITY ? -INFINITY : rows[in].base;
+            float o = fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i]));
+            if (rows[in].limit > nan_key) o = NAN;
+            const int token = r / a.group, qh = (p.head + lane_head) * a.group + r - token * a.group;
+            const int64_t row = static_cast<int64_t>(p.s) * a.t + token;
+            if (out) {
+              const bool some = den > 0.0f || den != den;
+              a.O[row * a.ld_o + static_cast<int64_t>(qh) * 128 + me] = static_cast<uint16_t>(pack_bf16x2(some ? o / den : 0.0f, 0.0f));
+              if (x == 0 && a.lse) a.lse[row * a.hq + qh] = some ? (m + log2f(den)) * 0.69314718055994531f : -INFINITY;
+            } else {
+              float* part = all ? w.whole + (row * a.hq + qh) * kPart : slot + in * kPart;
+              part[me] = o;
+              if (x == 0) *reinterpret_cast<float2*>(part + 128) = make_float2(m, den);
+            }
+          }
+        }
+      p = next;
+      more = another;
     }
-    at.tile = last;
-    if (last == at.tiles) next_item(a, at);
   }
-  if (!ok) {  // after a wait that ran out: copies in flight land before the block leaves
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 100000ull) {
-    }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmem);
   }
 }
 
@@ -559,38 +736,49 @@ struct Joined {
   }
 };
 
-// Parts of row r (of the sequence's rows) of key head `head` under one plan; true if there is one that covers all keys.
+// Parts of row r (of the sequence's rows) of key head `head` under one plan, every `warps`-th of them; true if one covers all keys.
 __device__ __forceinline__ bool join_parts(const CachedArgs& a, const CachedWork& w, int s, int head, int r, const float* whole, int lane,
-                                           Joined& j) {
+                                           int warp, int warps, Joined& j) {
   int start;
   const int tiles = tiles_of(sequence(a, s, start));
   if (tiles == 0) return false;
   const CachedHeader h = *w.head;
-  const int rows = a.rows_of_block, block = r / rows;
-  const int64_t begin = w.base[s] + static_cast<int64_t>(block * a.hkv + head) * tiles;
-  const int64_t first = stream_of(begin, h), last = stream_of(begin + tiles - 1, h);
+  const int rows = a.rows_of_block, block = r / rows, sub = head / a.abreast;
+  const int64_t begin = w.base[s] + static_cast<int64_t>(block * (a.hkv / a.abreast) + sub) * tiles;
+  const int64_t first = range_of(begin, h), last = range_of(begin + tiles - 1, h);
   if (first == last) {
-    if (a.partial) j.add(whole, lane);
+    if (a.partial && warp == 0) j.add(whole, lane);
     return true;
   }
+  const int64_t slot = static_cast<int64_t>(rows) * kPart;
+  const float* row = w.slots + (head - sub * a.abreast) * slot + static_cast<int64_t>(r - block * rows) * kPart;
+  if (warp == 0) j.add(row + (2 * first + (begin > range_begin(first, h) ? 1 : 0)) * a.abreast * slot, lane);
 #pragma unroll 4
-  for (int64_t i = first; i <= last; ++i)
-    j.add(w.slots + ((2 * i + (begin > range_begin(i, h) ? 1 : 0)) * rows + (r - block * rows)) * kPart, lane);
+  for (int64_t i = first + 1 + warp; i <= last; i += warps) j.add(row + 2 * i * a.abreast * slot, lane);  // (these begin within the item)
   return false;
 }
 
-__global__ void __launch_bounds__(128) cached_join_kernel(const CachedArgs a, const CachedWork w, const CachedArgs pa, const CachedWork pw) {
+// A block for each row, of `warps` warps that share its parts.
+__global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const CachedArgs a, const CachedWork w, const CachedArgs pa,
+                                                               const CachedWork pw) {
+  __shared__ __align__(16) float parts[kJoinWarps][kPart];
   pdl_launch();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (i >= static_cast<int64_t>(a.n) * a.t * a.hq) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t i = blockIdx.x;
   const int64_t token = i / a.hq;
   const int qh = static_cast<int>(i - token * a.hq), head = qh / a.group, in_group = qh - head * a.group;
   const int s = static_cast<int>(token / a.t), t = static_cast<int>(token - static_cast<int64_t>(s) * a.t);
   Joined j;
-  if (a.partial) join_parts(pa, pw, 0, head, static_cast<int>(token) * a.group + in_group, pw.whole + i * kPart, lane, j);
-  if (join_parts(a, w, s, head, t * a.group + in_group, w.whole + i * kPart, lane, j) && !a.partial) return;
+  if (a.partial) join_parts(pa, pw, 0, head, static_cast<int>(token) * a.group + in_group, pw.whole + i * kPart, lane, warp, warps, j);
+  if (join_parts(a, w, s, head, t * a.group + in_group, w.whole + i * kPart, lane, warp, warps, j) && !a.partial) return;
+  if (warps > 1) {
+    *reinterpret_cast<float4*>(&parts[warp][4 * lane]) = j.o;
+    if (lane == 0) *reinterpret_cast<float2*>(&parts[warp][128]) = make_float2(j.m, j.l);
+    __syncthreads();
+    if (warp != 0) return;
+    for (int x = 1; x < warps; ++x) j.add(parts[x], lane);
+  }
   const bool some = j.l > 0.0f || j.l != j.l;
   const float inv = some ? 1.0f / j.l : 0.0f;
   *reinterpret_cast<uint2*>(a.O + token * a.ld_o + static_cast<int64_t>(qh) * 128 + 4 * lane) =
@@ -602,16 +790,18 @@ __global__ void __launch_bounds__(128) cached_join_kernel(const CachedArgs a, co
 
 __host__ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
+int blocks_of_sm(int rows_of_block) { return rows_of_block <= 32 ? 2 : 1; }
+
 struct Region {
   int64_t head, base, slots, whole, total;
 };
 // of one plan, from `at` on
-__host__ Region region(int64_t at, int64_t n, int share, int rows_of_block, int64_t whole_rows) {
+Region region(int64_t at, const CachedArgs& a, int64_t whole_rows) {
   Region r;
   r.head = at;
   r.base = up256(r.head + static_cast<int64_t>(sizeof(CachedHeader)));
-  r.slots = up256(r.base + n * 8);
-  r.whole = up256(r.slots + int64_t(2) * kSms * (kWarps / share) * rows_of_block * kPart * 4);
+  r.slots = up256(r.base + a.n * int64_t(8));
+  r.whole = up256(r.slots + int64_t(2) * kSms * blocks_of_sm(a.rows_of_block) * a.rows_of_block * kPart * 4);
   r.total = up256(r.whole + whole_rows * kPart * 4);
   return r;
 }
@@ -624,28 +814,34 @@ CachedWork work_at(void* ws, const Region& r) {
   w.whole = reinterpret_cast<float*>(p + r.whole);
   return w;
 }
+Region own_region(const CachedArgs& a) { return region(0, a, a.partial ? int64_t(a.n) * a.t * a.hq : 0); }
+Region prefix_region(const CachedArgs& a, const CachedArgs& p) { return region(own_region(a).total, p, int64_t(a.n) * a.t * a.hq); }
 
-// Warps that share tiles: as few as hold the rows, 8 or 16 each.
-void shape_of(int64_t rows, int* nt, int* share) {
-  *nt = rows <= 8 ? 1 : 2;
-  *share = 1;
-  while (*share < kWarps && *share * 16 < rows) *share *= 2;
-}
-
-Region own_region(const CachedArgs& a) {
-  return region(0, a.n, a.share, a.rows_of_block, a.partial ? int64_t(a.n) * a.t * a.hq : 0);
-}
-Region prefix_region(const CachedArgs& a, const CachedArgs& p) {
-  return region(own_region(a).total, 1, p.share, p.rows_of_block, int64_t(a.n) * a.t * a.hq);
+template <int R>
+cudaError_t launch_rows(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, const CachedWork& w, int sms, cudaStream_t st) {
+  static std::atomic<bool> ready_of[kMaxDevices];  // the shared-memory opt-in, per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!ready_of[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(cached_attention_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<R>::kSmem);
+    if (e != cudaSuccess) return e;
+    ready_of[dev].store(true, std::memory_order_release);
+  }
+  const dim3 grid(static_cast<unsigned>((sms < kSms ? sms : kSms) * Shape<R>::kBlocks));
+  return launch_pdl(cached_attention_kernel<R>, grid, dim3(kThreads), Shape<R>::kSmem, 1, st, k, v, a, w);
 }
 
 }  // namespace
 
 void cached_shape(CachedArgs* a) {
-  int nt;
-  shape_of(int64_t(a->t) * a->group, &nt, &a->share);
-  a->rows_of_block = 8 * nt * a->share;
-  a->blocks = static_cast<int32_t>((int64_t(a->t) * a->group + a->rows_of_block - 1) / a->rows_of_block);
+  const int64_t rows = int64_t(a->t) * a->group;
+  a->rows_of_block = 8;
+  while (a->rows_of_block < 64 && a->rows_of_block < rows) a->rows_of_block *= 2;
+  a->blocks = static_cast<int32_t>((rows + a->rows_of_block - 1) / a->rows_of_block);
+  a->abreast = kMaxAbreast;
+  while (a->hkv % a->abreast != 0) --a->abreast;
 }
 
 int64_t cached_scratch_bytes(const CachedArgs& a, const CachedArgs* prefix) {
@@ -654,27 +850,25 @@ int64_t cached_scratch_bytes(const CachedArgs& a, const CachedArgs* prefix) {
 
 cudaError_t launch_cached_attention(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, const CachedArgs* of, void* ws,
                                     int sms, cudaStream_t st) {
-  static std::atomic<bool> ready_of[kMaxDevices];  // the shared-memory opt-in, per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (!ready_of[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(cached_attention_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(cached_attention_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    ready_of[dev].store(true, std::memory_order_release);
-  }
   const CachedWork w = work_at(ws, of ? prefix_region(*of, a) : own_region(a));
-  const dim3 grid(static_cast<unsigned>(sms < kSms ? sms : kSms));
-  return a.rows_of_block == 8 * a.share ? launch_pdl(cached_attention_kernel<1>, grid, dim3(kThreads), kSmem, 1, st, k, v, a, w)
-                                        : launch_pdl(cached_attention_kernel<2>, grid, dim3(kThreads), kSmem, 1, st, k, v, a, w);
+  switch (a.rows_of_block) {
+    case 8: return launch_rows<8>(k, v, a, w, sms, st);
+    case 16: return launch_rows<16>(k, v, a, w, sms, st);
+    case 32: return launch_rows<32>(k, v, a, w, sms, st);
+    default: return launch_rows<64>(k, v, a, w, sms, st);
+  }
 }
 
 cudaError_t launch_cached_join(const CachedArgs& a, const CachedArgs* prefix, void* ws, cudaStream_t st) {
   const int64_t rows = int64_t(a.n) * a.t * a.hq;
   const CachedWork w = work_at(ws, own_region(a)), pw = prefix ? work_at(ws, prefix_region(a, *prefix)) : w;
-  return launch_pdl(cached_join_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, 1, st, a, w, prefix ? *prefix : a, pw);
+  // warps for a row: with few items each is cut into many parts
+  const CachedArgs& b = prefix ? *prefix : a;
+  const int64_t items = int64_t(b.hkv) * b.n * b.blocks;
+  int warps = 1;
+  while (warps < kJoinWarps && items * warps * 4 < kSms * blocks_of_sm(b.rows_of_block)) warps *= 2;
+  return launch_pdl(cached_join_kernel, dim3(static_cast<unsigned>(rows)), dim3(static_cast<unsigned>(32 * warps)), 0, 1, st, a, w,
+                    prefix ? *prefix : a, pw);
 }
 
 cudaError_t take_cached_error(int* code) {

@@ -150,9 +150,11 @@ cudaError_t launch_layernorm_bwd(const uint16_t* gN, const uint16_t* N, const fl
 
 // Tensor maps (zero fill out of bounds).  dims[0] is innermost; strides_bytes[i] is the stride of
 // dims[i+1].  elem_bytes: 1 = 8-bit codes, 2 = bf16, 4 = fp32.  swizzle_bytes: 128 or 64.
+// l2_bytes: what L2 fetches at a time, 256 or 128.
 bool tma_encoder_ready(std::string* err);
 bool make_map(CUtensorMap* map, int elem_bytes, const void* base, int rank, const uint64_t* dims,
-              const uint64_t* strides_bytes, const uint32_t* box, std::string* err, int swizzle_bytes = 128);
+              const uint64_t* strides_bytes, const uint32_t* box, std::string* err, int swizzle_bytes = 128,
+              int l2_bytes = 256);
 inline bool make_map_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                           const uint64_t* strides_bytes, const uint32_t* box, std::string* err) {
   return make_map(map, 2, base, rank, dims, strides_bytes, box, err);

@@ -252,12 +252,13 @@ struct CachedArgs {
   int64_t ld_q, ld_o, ld_exp;
   int32_t n, t, hq, hkv, group, cache_rows;
   int32_t causal, partial;               // query i of t sees len - t + i + 1 keys, or all; results stay in the workspace
-  int32_t share, rows_of_block, blocks;  // cached_shape: warps on the same tiles, rows that they hold, blocks of rows
+  int32_t rows_of_block, blocks;         // cached_shape: rows (tokens x group) of a block, blocks of rows,
+  int32_t abreast;                       // neighbouring key heads that blocks take at the same time
   float scale_log2;                      // scale x log2(e)
   int32_t err_site;
 };
 // Maps of codes, 128-byte swizzle: (128, hkv, cache_rows) in boxes (128, 1, kCachedKeys).
-constexpr int kCachedKeys = 32;
+constexpr int kCachedKeys = 128;
 void cached_shape(CachedArgs* a);
 // `prefix` (nullable): the arguments of the rows that all sequences share, as one sequence of n x t tokens.
 int64_t cached_scratch_bytes(const CachedArgs& a, const CachedArgs* prefix);

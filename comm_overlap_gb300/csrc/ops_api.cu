@@ -760,7 +760,7 @@ domino_status domino_attn_cached_fwd(domino_handle H, const uint16_t* Q, int64_t
       const uint64_t strides[2] = {128, uint64_t(kv_heads) * 128};
       const uint32_t box[3] = {128, 1, uint32_t(dm::kCachedKeys)};
       const void* base = cache_rows > 0 ? (i ? static_cast<const void*>(v8) : k8) : Q;
-      if (!dm::make_map(i ? &mv : &mk, 1, base, 3, dims, strides, box, &err)) return refuse(DOMINO_ERR_CUDA, err);
+      if (!dm::make_map(i ? &mv : &mk, 1, base, 3, dims, strides, box, &err, 128, 128)) return refuse(DOMINO_ERR_CUDA, err);
     }
     for (dm::CachedArgs* x : {&a, &p}) {
       x->Q = Q;
