@@ -9,13 +9,14 @@
 // P^T), so that codes go from memory to the tensor core as they are and few queries make a narrow product.  The narrow operand is a
 // sum of two E4M3 terms, x1 + x2 / 16, in columns of their own: x1 is x rounded, x2 the rest.  For q, scaled by a power of two for
 // each row so that its largest value lies in [2^7, 2^8), they are exact down to 2^-14 of the largest, and off by at most 2^-21 of it
-// below.  For w, which is at most 448, they are good to 2^-8, as bf16 would be, or to 2^-20 of the row's largest weight.
+// below.  For w, which is at most 448, they are good to 2^-8, as bf16 would be, or to 2^-18 of the row's largest weight.
 // (With mma.sync, 8 rows a warp, codes have to be converted to f16, 3 - 4 clocks for two: one sequence of 262001 keys and 8 heads
 // 130 us; its E4M3 form converts them too, 175.)
 //
 // A row is a token and one of the `group` query heads of a key head; R of them make 2 R columns, for each 8 rows the first terms, then
-// the second.  Warps of a block: one loads K and V by TMA into a ring, one issues the products, four hold the 128 keys (then
-// elements), one a thread, which TMEM lane by lane suits: no sums across threads but at an item's end.
+// the second.  Warps of a block: one loads K and V by TMA into a ring, one issues the products, and four for each 16 rows hold the 128
+// keys (then elements), one a thread, which TMEM lane by lane suits: no sums across threads but at an item's end.  (What an item
+// needs once is kept short: instructions that run once come from memory each time.)
 //
 // The tiles of all sequences, laid end to end, are cut into equal ranges, one for each group of `abreast` blocks, which take
 // neighbouring key heads and so read a row's heads at about the same time.  What covers all keys of a row is written out; parts leave
@@ -37,7 +38,6 @@ namespace {
 
 __device__ int g_cached_err;
 
-constexpr int kThreads = 192;                      // warps: 0 loads, 1 issues, 2 - 5 the keys of a tile
 constexpr int kKeys = kCachedKeys;                 // of a tile
 constexpr uint32_t kTile = kKeys * 128;            // bytes of K or V
 constexpr int kSms = 152;                          // SMs that the workspace is sized for, at most
@@ -50,24 +50,28 @@ constexpr uint64_t kDrainNs = 200000000ull;
 template <int R>
 struct Shape {
   static constexpr int kBlocks = R <= 32 ? 2 : 1;
+  static constexpr int kRows = R < 16 ? R : 16, kGroups = R / kRows;  // groups of 128 threads that hold keys, and the rows of each
+  static constexpr int kThreads = 64 + 128 * kGroups;                 // warps: 0 loads, 1 issues, from 2 on keys
   static constexpr uint32_t kSlots = R == 8 ? 6 : R == 16 ? 5 : R == 32 ? 4 : 8;
   static constexpr uint32_t kCols = 2 * R;
   static constexpr uint32_t kTmem = R == 8 ? 64 : R == 16 ? 128 : R == 32 ? 256 : 512;
   static constexpr uint32_t kOperand = kCols * 128;                                // bytes of Q or P, two buffers each
-  static constexpr uint32_t kCtrl = 5120;
+  static constexpr uint32_t kCtrl = 5120;                                          // control block
   static constexpr int kSmem = 1024 + static_cast<int>(kCtrl + kSlots * kTile + 4 * kOperand);
-  static_assert(kBlocks * (kSmem + 1024 + 1700) <= 233472 && 3 * kCols <= kTmem && kBlocks * kTmem <= 512, "memory of an SM");
+  static_assert(kBlocks * (kSmem + 1024 + 8 * kThreads + 512) <= 233472 && 3 * kCols <= kTmem && kBlocks * kTmem <= 512, "memory of an SM");
 };
 // Weights are 2^kRaise where t is the maximum that m was taken from; the maximum may rise by kBehind (in base 2) before O and the
-// denominator are brought to a new m, so that they stay below E4M3's 448 = 2^8.807.
-constexpr float kRaise = 6.0f, kBehind = 2.8f;
+// denominator are brought to a new m, so that they stay below E4M3's 448 = 2^8.807.  (With 6 and 2.8 m moved in nearly every tile of 64
+// rows.)
+constexpr float kRaise = 4.0f, kBehind = 4.8f;
 constexpr float kTerm = 0.0625f;  // of the second terms
 
 // ---- work: tiles of all items (sequence, block of rows, `abreast` key heads) in order
 
 struct CachedHeader {
-  int64_t tiles;    // of all items
-  int64_t ranges;   // that they are cut into
+  int64_t tiles;       // of all items
+  int64_t each;        // of a range; the first `rest` ranges have one more
+  int32_t rest, ranges;
 };
 
 struct CachedWork {
@@ -89,10 +93,15 @@ __device__ __forceinline__ int sequence(const CachedArgs& a, int s, int& start) 
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kKeys - 1) / kKeys; }
 
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {  // x, y >= 0; nearly always within 32 bits
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
 // Where range i begins, and the range that tile x belongs to.
-__device__ __forceinline__ int64_t range_begin(int64_t i, const CachedHeader& h) { return i * h.tiles / h.ranges; }
+__device__ __forceinline__ int64_t range_begin(int64_t i, const CachedHeader& h) { return i * h.each + (i < h.rest ? i : h.rest); }
 __device__ __forceinline__ int64_t range_of(int64_t x, const CachedHeader& h) {
-  return ((x + 1) * h.ranges + h.tiles - 1) / h.tiles - 1;
+  const int64_t longer = h.rest * (h.each + 1);
+  return x < longer ? divide(x, h.each + 1) : h.rest + divide(x - longer, h.each);
 }
 
 // An item's part in a range: keys of tiles t0 .. t1 - 1 of sequence s.
@@ -163,16 +172,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void key_threads_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool key_threads_any(bool x) {
+// The threads that hold a group's keys meet.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
+__device__ __forceinline__ bool group_any(int group, bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "setp.ne.b32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x))
+      : "r"(group + 1), "r"(static_cast<uint32_t>(x))
       : "memory");
   return r != 0;
 }
@@ -204,24 +214,93 @@ __device__ __forceinline__ int load_line(const uint8_t* p) {
 // A row of an item, in shared memory
 struct __align__(16) Row {
   float scale;   // of the scores of its q, in base 2
-  float base;    // m, or 0 while there is none
-  float above;   // beyond it m moves (-inf while there is none)
+  float base;    // m (0 while there is none)
   int limit;     // keys that it sees
+  int begun;     // whether there is an m
+};
+
+// ... and, at the item's end, where its results go
+struct __align__(16) OutRow {
+  int64_t at;    // of O, the partial results or the whole ones
+  float factor;
+  int limit;
 };
 
 enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_COUNT = 25 };
-// Control block: barriers, then 256: TMEM address, abort flag; 512: pieces; 1024: rows of two items; 3072: four warps' maxima or sums of
-// 64 rows; 4096: factors
-constexpr uint32_t kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 3072, kFactorsAt = 4096;
+// Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces; 1024: rows of two items; 3072:
+// four warps' maxima or sums of 64 rows; 4096: by how much m moved, and the factor for what was added up before
+constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 3072, kMovesAt = 4096;
 static_assert(sizeof(Piece) * 2 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "control block");
 
+// An item's rows (8 x CHUNKS from row r0 of the sequence on) to shared memory, in two terms, 16 threads a row: columns 16 c + n (first
+// terms) and 16 c + 8 + n (second) of the product's narrow operand, rows of 128 bytes under the 128-byte swizzle.
+template <int CHUNKS>
+__device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, int head, int r0, uint32_t to, Row* rows, int x) {
+  uint4 u[CHUNKS];
+  const int n = x >> 4, piece = x & 15, count = a.t * a.group;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int r = r0 + c * 8 + n;
+    u[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < count) {
+      const int token = r / a.group;
+      const uint16_t* q =
+          a.Q + (static_cast<int64_t>(s) * a.t + token) * a.ld_q + (static_cast<int64_t>(head) * a.group + r - token * a.group) * 128;
+      u[c] = reinterpret_cast<const uint4*>(q)[piece];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int r = r0 + c * 8 + n;
+    const float v[8] = {bf16lo(u[c].x), bf16hi(u[c].x), bf16lo(u[c].y), bf16hi(u[c].y),
+                        bf16lo(u[c].z), bf16hi(u[c].z), bf16lo(u[c].w), bf16hi(u[c].w)};
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    // 2^up brings the largest into [2^7, 2^8) (an infinity becomes NaN, as its scores would)
+    const int up = amax > 0.0f && amax < INFINITY ? min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120) : 0;
+    const float f = amax < INFINITY ? __int_as_float((up + 127) << 23) : NAN;
+    uint32_t one[4], two[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) two_terms(v[2 * i] * f, v[2 * i + 1] * f, one[i], two[i]);
+    const uint32_t at = to + static_cast<uint32_t>(c * 2048 + n * 128 + (((piece >> 1) ^ n) << 4) + (piece & 1) * 8);
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
+    if (piece == 0) {
+      const int limit = r >= count ? 0 : a.causal ? len - a.t + r / a.group + 1 : len;
+      rows[c * 8 + n] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, limit, 0};
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+// Sums over the warp of each of ROWS values: lane i gets that of row i / (32 / ROWS).
+template <int ROWS>
+__device__ __forceinline__ float row_sums(float (&v)[ROWS], int lane) {
+  int o = 16;
+#pragma unroll
+  for (int half = ROWS / 2; half > 0; half >>= 1, o >>= 1) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = upper ? v[i + half] : v[i], give = upper ? v[i] : v[i + half];
+      v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+    }
+  }
+  float sum = v[0];
+  for (; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  return sum;
+}
+
 template <int R>
-__global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
-    cached_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const CachedArgs a,
-                            const CachedWork w) {
+__global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
+    cached_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                            const __grid_constant__ CachedArgs a, const CachedWork w) {
   using S = Shape<R>;
   constexpr uint32_t kSlots = S::kSlots;
-  constexpr int kChunks = R / 8;
+  constexpr int kThreads = S::kThreads, kRows = S::kRows, kChunks = kRows / 8;  // rows and chunks of 8 of a group
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   __shared__ int64_t before[kThreads + 1];  // tiles of one item before each thread's sequences
@@ -233,11 +312,12 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
   Piece* pieces = reinterpret_cast<Piece*>(smem + kPiecesAt);
   Row* all_rows = reinterpret_cast<Row*>(smem + kRowsAt);
   float* sums = reinterpret_cast<float*>(smem + kSumsAt);
-  float* factors = reinterpret_cast<float*>(smem + kFactorsAt);
+  float2* moves = reinterpret_cast<float2*>(smem + kMovesAt);
+  volatile uint32_t* flags_of = reinterpret_cast<volatile uint32_t*>(smem + kFlagsAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = &g_cached_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_Q_FULL && i < B_PV_DONE && !(i >= B_S_FULL && i < B_P_FULL) ? 4 : 1);
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_Q_FULL || i == B_Q_FULL + 1 || i == B_P_FULL || i == B_P_FULL + 1 ? 4 * S::kGroups : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -279,8 +359,10 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
   CachedHeader h;
   h.tiles = total * items;
   {
-    const int64_t most = gridDim.x / a.abreast;
-    h.ranges = h.tiles < most ? (h.tiles > 0 ? h.tiles : 1) : most;
+    const int most = static_cast<int>(gridDim.x) / a.abreast;
+    h.ranges = h.tiles < most ? (h.tiles > 0 ? static_cast<int>(h.tiles) : 1) : most;
+    h.each = divide(h.tiles, h.ranges);
+    h.rest = static_cast<int>(h.tiles - h.each * h.ranges);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *w.head = h;
   if (threadIdx.x % gridDim.x == blockIdx.x) {  // for the second kernel
@@ -297,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
   const int64_t lo = work ? range_begin(range, h) : 0, hi = work ? range_begin(range + 1, h) : 0;
   if (work && warp == 2) {  // the range's first piece: the thread whose sequences hold tile lo, then the sequence, 32 at a time
     int x = 0;
-    for (int step = 128; step > 0; step >>= 1)
+    for (int step = 512; step > 0; step >>= 1)
       if (x + step < kThreads && before[x + step] * items <= lo) x += step;
     int64_t done = before[x] * items;
     Piece p = {};
@@ -325,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
       done += __shfl_sync(0xFFFFFFFFu, upto, 31) * items;
     }
     if (p.tiles > 0) {
-      const int item = static_cast<int>((lo - done) / p.tiles), subs = a.hkv / a.abreast;
+      const int item = static_cast<int>(divide(lo - done, p.tiles)), subs = a.hkv / a.abreast;
       p.block = item / subs;
       p.head = (item - p.block * subs) * a.abreast;
       p.t0 = static_cast<int>((lo - done) - static_cast<int64_t>(item) * p.tiles);
@@ -435,58 +517,25 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
     while (!mbar_try_wait(bar(B_DRAIN), 0) && global_timer_ns() - t0 < kDrainNs) {
     }
   } else if (work) {
-    // ---------------- keys: a thread has one key of each tile, and one element of O, both the number of its TMEM lane.  After a wait
-    // that ran out these warps go on (every later one ends at once), so that they meet at their barriers, but write nothing.
-    const int x = threadIdx.x - 64, quarter = (warp & 3) * 32, me = quarter + lane;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 16);
+    // ---------------- keys: a thread has one key of each tile, and one element of O, both the number of its TMEM lane, for its group's
+    // rows.  After a wait that ran out these warps go on (every later one ends at once), so that they meet at their barriers, but write
+    // nothing.
+    const int group = (threadIdx.x - 64) >> 7, x = (threadIdx.x - 64) & 127, quarter = (warp & 3) * 32, me = quarter + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 16) + static_cast<uint32_t>(group * 2 * kRows);
+    sums += group * 4 * kRows;
+    moves += group * kRows;
+    flags_of += group * 4;
+    auto groups_sync = [&] {
+      if (S::kGroups > 1) asm volatile("bar.sync %0, %1;" ::"n"(S::kGroups + 1), "n"(128 * S::kGroups) : "memory");
+    };
     bool ok = true;
     auto wait = [&](int b, uint32_t parity, int site) {
       ok = mbar_wait(bar(b), parity & 1u, abort_flag, err, a.err_site + site) && ok;
     };
-    // an item's rows: 16 threads a row have 8 values each, of 8 rows at a time
-    auto fetch = [&](const Piece& p, uint4 (&u)[kChunks]) {
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int r = p.block * R + c * 8 + (x >> 4);
-        u[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows_of_sequence) {
-          const int token = r / a.group;
-          const uint16_t* q = a.Q + (static_cast<int64_t>(p.s) * a.t + token) * a.ld_q +
-                              (static_cast<int64_t>(p.head + lane_head) * a.group + r - token * a.group) * 128;
-          u[c] = reinterpret_cast<const uint4*>(q)[x & 15];
-        }
-      }
-    };
-    // ... which go to shared memory in two terms
-    auto prepare = [&](const Piece& p, const uint4 (&u)[kChunks], uint32_t item) {
-      const uint32_t to = q_at + (item & 1u) * S::kOperand;
-      Row* rows = all_rows + (item & 1u) * R;
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int n = x >> 4, piece = x & 15, r = p.block * R + c * 8 + n;
-        const float v[8] = {bf16lo(u[c].x), bf16hi(u[c].x), bf16lo(u[c].y), bf16hi(u[c].y),
-                            bf16lo(u[c].z), bf16hi(u[c].z), bf16lo(u[c].w), bf16hi(u[c].w)};
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        // 2^up brings the largest into [2^7, 2^8) (an infinity becomes NaN, as its scores would)
-        const int up = amax > 0.0f && amax < INFINITY ? min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120) : 0;
-        const float f = amax < INFINITY ? __int_as_float((up + 127) << 23) : NAN;
-        uint32_t one[4], two[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) two_terms(v[2 * i] * f, v[2 * i + 1] * f, one[i], two[i]);
-        // columns 16 c + n (first terms) and 16 c + 8 + n (second): rows of 128 bytes under the 128-byte swizzle
-        const uint32_t at = to + static_cast<uint32_t>(c * 2048 + n * 128 + (((piece >> 1) ^ n) << 4) + (piece & 1) * 8);
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
-        if (piece == 0) {
-          const int limit = r >= rows_of_sequence ? 0 : a.causal ? p.len - a.t + r / a.group + 1 : p.len;
-          rows[c * 8 + n] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, -INFINITY, limit};
-        }
-      }
-      fence_proxy_async_smem();
+    auto prepare = [&](const Piece& p, uint32_t item) {
+      prepare_rows<kChunks>(a, p.s, p.len, p.head + lane_head, p.block * R + group * kRows,
+                            q_at + (item & 1u) * S::kOperand + static_cast<uint32_t>(group * kChunks) * 2048u,
+                            all_rows + (item & 1u) * R + group * kRows, x);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_Q_FULL + (item & 1u)));
     };
@@ -497,25 +546,24 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
       return load_line(a.k_exp + i) | load_line(a.v_exp + i) << 8;
     };
 
-    uint4 u[kChunks];
     Piece p = pieces[0], next = p;
     bool more = p.t1 > p.t0, another = false;
     int exps = 0;
     if (more) {
       exps = exponents(p, p.t0);
-      fetch(p, u);
-      prepare(p, u, 0);
+      prepare(p, 0);
     }
     uint32_t j = 0, slot_v = 1, round_v = 0;  // tiles so far; V's place in the ring
-    key_threads_sync();                       // the rows are there
+    group_sync(group);                        // the rows are there
     for (uint32_t item = 0; more; ++item) {
-      Row* rows = all_rows + (item & 1u) * R;
-      const int count = min(R, rows_of_sequence - p.block * R), chunks = (count + 7) >> 3;
+      Row* rows = all_rows + (item & 1u) * R + group * kRows;
+      const int count = min(kRows, rows_of_sequence - p.block * R - group * kRows), chunks = (count + 7) >> 3;  // (none: below 0)
       const int least = a.causal ? p.len - a.t + p.block * R / a.group + 1 : p.len;  // keys that every row sees
       int nan_key = INT_MAX;  // the first key, of those that not all rows see, with NaN in this thread's element
-      float l[R];
+      float l[kRows];
 #pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = 0.0f;
+      for (int r = 0; r < kRows; ++r) l[r] = 0.0f;
+      bool force = true;  // rows without an m
 
       for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
         const bool first = tile == p.t0, only = p.t1 == p.t0 + 1;
@@ -524,10 +572,13 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
           next_exps = exponents(p, tile + 1);
         else if (!first && another)
           next_exps = exponents(next, next.t0);
-        if (first && x == 0) {  // one thread finds the next item, all take it from shared memory
-          Piece n = p;
-          if (!next_piece(a, n, hi)) n.t1 = n.t0;
-          pieces[(item + 1) & 1u] = n;
+        if (first) {  // one thread finds the next item, all take it from shared memory (after they have met below)
+          if (threadIdx.x == 64) {
+            Piece n = p;
+            if (!next_piece(a, n, hi)) n.t1 = n.t0;
+            pieces[(item + 1) & 1u] = n;
+          }
+          groups_sync();
         }
         const int key0 = tile * kKeys;
         const bool tail = key0 + kKeys > least;
@@ -536,78 +587,99 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
         const uint32_t from = lanes + (j & 1u) * S::kCols;
         wait(B_S_FULL + (j & 1u), j >> 1, 6);
         tc_fence_after();
-        float t[R];
-        bool above = false;
+        float d[kRows];  // t - m
+        uint32_t flags = 0;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
           if (c < chunks) {
             uint32_t y[16];
             tmem_ld16(from + 16u * c, y);
             tmem_ld_wait();
+            float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const Row row = rows[8 * c + i];
-              float z = fmaf(fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i])) * key_scale, row.scale, bias);
-              if (tail && key0 + me >= row.limit) z = -INFINITY;
-              above |= z > row.above;
-              t[8 * c + i] = z;
+              const float2 row = *reinterpret_cast<const float2*>(rows + 8 * c + i);
+              const float z = fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i])) * key_scale;
+              d[8 * c + i] = fmaf(z, row.x, bias - row.y);
             }
+            if (tail) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (key0 + me >= rows[8 * c + i].limit) d[8 * c + i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, d[8 * c + i]);
+            flags |= static_cast<uint32_t>(top > kRaise + kBehind) << c;
           }
         }
-        if (key_threads_any(above)) {
+        if (kChunks == 1) {
+          flags = group_any(group, flags != 0) ? 1u : 0u;
+        } else {
+          flags = __reduce_or_sync(0xFFFFFFFFu, flags);
+          if (lane == 0) flags_of[warp & 3] = flags;
+          group_sync(group);
+          flags = (flags_of[0] | flags_of[1]) | (flags_of[2] | flags_of[3]);
+        }
+        if (force) flags = chunks > 0 ? (1u << chunks) - 1u : 0u;
+        if (flags) {
           // the rows' maxima; where one is well above m, m moves
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
-            if (c < chunks) {
+            if (c < chunks && (flags >> c & 1u)) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const float z = t[8 * c + i];
+                const float z = d[8 * c + i];
                 const int bits = __float_as_int(z == z ? z : -INFINITY);
                 const int top = __reduce_max_sync(0xFFFFFFFFu, bits ^ ((bits >> 31) & 0x7FFFFFFF));  // (ordered as the floats are)
-                if (lane == 0) sums[(warp & 3) * R + 8 * c + i] = __int_as_float(top ^ ((top >> 31) & 0x7FFFFFFF));
+                if (lane == 0) sums[(warp & 3) * kRows + 8 * c + i] = __int_as_float(top ^ ((top >> 31) & 0x7FFFFFFF));
               }
             }
-          key_threads_sync();
-          if (x < 8 * chunks) {
-            const float top = fmaxf(fmaxf(sums[x], sums[R + x]), fmaxf(sums[2 * R + x], sums[3 * R + x]));
+          group_sync(group);
+          bool without = false;
+          if (x < 8 * chunks && (flags >> (x >> 3) & 1u)) {
+            const float top = fmaxf(fmaxf(sums[x], sums[kRows + x]), fmaxf(sums[2 * kRows + x], sums[3 * kRows + x]));
             Row row = rows[x];
-            float f = 1.0f;
-            if (top > row.above) {
-              f = row.above == -INFINITY ? 0.0f : ex2_approx(row.base - (top - kRaise));
-              row.base = top - kRaise;
-              row.above = top + kBehind;
+            float2 move = make_float2(0.0f, 1.0f);
+            if (row.begun ? top > kRaise + kBehind : top > -INFINITY) {
+              move = make_float2(top - kRaise, row.begun ? ex2_approx(kRaise - top) : 0.0f);
+              row.base += move.x;
+              row.begun = 1;
               rows[x] = row;
             }
-            factors[x] = f;
+            moves[x] = move;
+            without = !row.begun && x < count;
           }
-          key_threads_sync();
+          force = group_any(group, without);
           if (!first) {
             wait(B_PV_DONE + ((j - 1) & 1u), (j - 1) >> 1, 7);
             tc_fence_after();
           }
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            if (c < chunks) {
+          for (int r = 0; r < kRows; ++r)
+            if (flags >> (r >> 3) & 1u) {
+              const float2 move = moves[r];
+              d[r] -= move.x;
+              l[r] *= move.y;
+            }
+#pragma unroll 1
+          for (int c = 0; c < chunks && !first; ++c)
+            if (flags >> c & 1u) {
+              uint32_t y[16];
+              tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
+              tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) l[8 * c + i] *= factors[8 * c + i];
-              if (!first) {
-                uint32_t y[16];
-                tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const float f = factors[8 * c + i];
-                  y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-                  y[8 + i] = __float_as_uint(__uint_as_float(y[8 + i]) * f);
-                }
-                tmem_st16(lanes + 2 * S::kCols + 16u * c, y);
+              for (int i = 0; i < 8; ++i) {
+                const float f = moves[8 * c + i].y;
+                y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                y[8 + i] = __float_as_uint(__uint_as_float(y[8 + i]) * f);
               }
+              tmem_st16(lanes + 2 * S::kCols + 16u * c, y);
             }
           if (!first) tmem_st_wait();
         }
         // weights, in two terms: 16 bytes a key for 8 rows
         if (j >= 2) wait(B_PV_DONE + (j & 1u), (j - 2) >> 1, 8);
-        const uint32_t to = p_at + (j & 1u) * S::kOperand + static_cast<uint32_t>(me) * 16u;
+        const uint32_t to = p_at + (j & 1u) * S::kOperand + static_cast<uint32_t>(group * kChunks) * (kKeys * 16u) + static_cast<uint32_t>(me) * 16u;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
           if (c < chunks) {
@@ -615,29 +687,38 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int r = 8 * c + 2 * i;
-              const float w0 = ex2_approx(t[r] - rows[r].base), w1 = ex2_approx(t[r + 1] - rows[r + 1].base);
+              const float w0 = ex2_approx(d[r]), w1 = ex2_approx(d[r + 1]);
               l[r] = fmaf(w0, unbias, l[r]);
               l[r + 1] = fmaf(w1, unbias, l[r + 1]);
               two_terms(w0, w1, one[i], two[i]);
             }
             st_shared_v4(to + c * (kKeys * 16u), one[0] | one[1] << 16, one[2] | one[3] << 16, two[0] | two[1] << 16, two[2] | two[3] << 16);
           }
-        if (tail) {
-          // values past the sequence's keys count as zero, NaN included; so does NaN among keys that some rows do not see, and the
-          // rows that do get it at the item's end
+        if (tail && group == 0) {
+          // values past the sequence's keys count as zero, NaN included
           wait(B_FULL + slot_v, round_v, 9);
           const uint32_t v_at = ring + slot_v * kTile;
-          const int end = p.len - key0;
-          for (int r = max(end, 0) + (x >> 3); r < kKeys; r += 16) st_shared_v4(v_at + static_cast<uint32_t>(r * 128 + (x & 7) * 16), 0u, 0u, 0u, 0u);
-          for (int r = max(least - key0, 0); r < min(end, kKeys); ++r) {
-            const uint32_t at = v_at + static_cast<uint32_t>(r * 128 + (((me >> 4) ^ (r & 7)) << 4) + (me & 15));
-            uint16_t code;
-            asm volatile("{\n\t.reg .b32 v;\n\tld.shared.u8 v, [%1];\n\tcvt.u16.u32 %0, v;\n\t}" : "=h"(code) : "r"(at) : "memory");
-            if ((code & 0x7F) == 0x7F) {
-              nan_key = min(nan_key, key0 + r);
-              asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(0u) : "memory");
-            }
-          }
+          for (int r = max(p.len - key0, 0) + (x >> 3); r < kKeys; r += 16)
+            st_shared_v4(v_at + static_cast<uint32_t>(r * 128 + (x & 7) * 16), 0u, 0u, 0u, 0u);
+        }
+        if (tail && least < p.len) {
+          // so does NaN among keys that some rows do not see, and the rows that do get it at the item's end.  (Each group looks before one
+          // clears them.)
+          wait(B_FULL + slot_v, round_v, 9);
+          const uint32_t v_at = ring + slot_v * kTile;
+          const int r0 = max(least - key0, 0), r1 = min(p.len - key0, kKeys);
+          auto place = [&](int r) { return v_at + static_cast<uint32_t>(r * 128 + (((me >> 4) ^ (r & 7)) << 4) + (me & 15)); };
+          auto is_nan = [&](int r) {
+            uint32_t code;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(place(r)) : "memory");
+            return (code & 0x7Fu) == 0x7Fu;
+          };
+          for (int r = r0; r < r1; ++r)
+            if (is_nan(r)) nan_key = min(nan_key, key0 + r);
+          groups_sync();
+          if (group == 0)
+            for (int r = r0; r < r1; ++r)
+              if (is_nan(r)) asm volatile("st.shared.u8 [%0], %1;" ::"r"(place(r)), "r"(0u) : "memory");
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -652,59 +733,61 @@ __global__ void __launch_bounds__(kThreads, Shape<R>::kBlocks)
           next = pieces[(item + 1) & 1u];
           another = next.t1 > next.t0;
           if (another) {
-            fetch(next, u);
             if (only) next_exps = exponents(next, next.t0);
+            prepare(next, item + 1);
           }
         }
-        if (another && (only || tile == p.t0 + 1)) prepare(next, u, item + 1);
         exps = next_exps;
       }
 
       // ---- what the piece's keys came to
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        if (c < chunks) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float v = l[8 * c + i];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0) sums[(warp & 3) * R + 8 * c + i] = v;
-          }
+      {
+        const float sum = row_sums<kRows>(l, lane);
+        if ((lane & (32 / kRows - 1)) == 0) sums[(warp & 3) * kRows + lane / (32 / kRows)] = sum;
+      }
+      group_sync(group);
+      const bool all = p.t0 == 0 && p.t1 == p.tiles, out = all && !a.partial;
+      if (x < count) {
+        const float den = (sums[x] + sums[kRows + x]) + (sums[2 * kRows + x] + sums[3 * kRows + x]);
+        const Row row = rows[x];
+        const float m = row.begun ? row.base : -INFINITY;
+        const int in = group * kRows + x, r = p.block * R + in, token = r / a.group;
+        const int64_t place = (static_cast<int64_t>(p.s) * a.t + token) * a.hq + (p.head + lane_head) * a.group + r - token * a.group;
+        OutRow to;
+        to.limit = row.limit;
+        to.factor = 1.0f;
+        if (out) {
+          const bool some = den > 0.0f || den != den;
+          to.factor = some ? 1.0f / den : 0.0f;
+          to.at = (static_cast<int64_t>(p.s) * a.t + token) * a.ld_o + (static_cast<int64_t>(p.head + lane_head) * a.group + r - token * a.group) * 128;
+          if (a.lse && ok) a.lse[place] = some ? (m + log2f(den)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          const int64_t slot = (2 * range + (p.at - p.t0 > lo ? 1 : 0)) * a.abreast + lane_head;  // (the item begins within the range)
+          to.at = all ? place * kPart : (slot * R + in) * kPart;
+          if (ok) *reinterpret_cast<float2*>((all ? w.whole : w.slots) + to.at + 128) = make_float2(m, den);
         }
-      key_threads_sync();
+        *reinterpret_cast<OutRow*>(rows + x) = to;
+      }
       wait(B_PV_DONE + ((j - 1) & 1u), (j - 1) >> 1, 10);
       tc_fence_after();
-      const bool all = p.t0 == 0 && p.t1 == p.tiles, out = all && !a.partial;
-      const int64_t begin = p.at - p.t0;  // the item's first tile
-      float* slot = w.slots + ((2 * range + (begin > lo ? 1 : 0)) * a.abreast + lane_head) * static_cast<int64_t>(R * kPart);
+      group_sync(group);
+      float* parts = all ? w.whole : w.slots;
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        uint32_t y[16];
+        tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
+        tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        if (c < chunks) {
-          uint32_t y[16];
-          tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int in = 8 * c + i, r = p.block * R + in;
-            if (in >= count || !ok) continue;
-            const float den = (sums[in] + sums[R + in]) + (sums[2 * R + in] + sums[3 * R + in]);
-            const float m = rows[in].above == -INFINITY ? -INFINITY : rows[in].base;
-            float o = fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i]));
-            if (rows[in].limit > nan_key) o = NAN;
-            const int token = r / a.group, qh = (p.head + lane_head) * a.group + r - token * a.group;
-            const int64_t row = static_cast<int64_t>(p.s) * a.t + token;
-            if (out) {
-              const bool some = den > 0.0f || den != den;
-              a.O[row * a.ld_o + static_cast<int64_t>(qh) * 128 + me] = static_cast<uint16_t>(pack_bf16x2(some ? o / den : 0.0f, 0.0f));
-              if (x == 0 && a.lse) a.lse[row * a.hq + qh] = some ? (m + log2f(den)) * 0.69314718055994531f : -INFINITY;
-            } else {
-              float* part = all ? w.whole + (row * a.hq + qh) * kPart : slot + in * kPart;
-              part[me] = o;
-              if (x == 0) *reinterpret_cast<float2*>(part + 128) = make_float2(m, den);
-            }
-          }
+        for (int i = 0; i < 8; ++i) {
+          if (8 * c + i >= count || !ok) break;
+          const OutRow to = *reinterpret_cast<const OutRow*>(rows + 8 * c + i);
+          const float o = to.limit > nan_key ? NAN : fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i])) * to.factor;
+          if (out)
+            a.O[to.at + me] = static_cast<uint16_t>(pack_bf16x2(o, 0.0f));
+          else
+            parts[to.at + me] = o;
         }
+      }
       p = next;
       more = another;
     }
@@ -740,11 +823,12 @@ struct Joined {
 __device__ __forceinline__ bool join_parts(const CachedArgs& a, const CachedWork& w, int s, int head, int r, const float* whole, int lane,
                                            int warp, int warps, Joined& j) {
   int start;
+  const CachedHeader h = *w.head;
+  const int64_t base = w.base[s];
   const int tiles = tiles_of(sequence(a, s, start));
   if (tiles == 0) return false;
-  const CachedHeader h = *w.head;
   const int rows = a.rows_of_block, block = r / rows, sub = head / a.abreast;
-  const int64_t begin = w.base[s] + static_cast<int64_t>(block * (a.hkv / a.abreast) + sub) * tiles;
+  const int64_t begin = base + static_cast<int64_t>(block * (a.hkv / a.abreast) + sub) * tiles;
   const int64_t first = range_of(begin, h), last = range_of(begin + tiles - 1, h);
   if (first == last) {
     if (a.partial && warp == 0) j.add(whole, lane);
@@ -830,7 +914,7 @@ cudaError_t launch_rows(const CUtensorMap& k, const CUtensorMap& v, const Cached
     ready_of[dev].store(true, std::memory_order_release);
   }
   const dim3 grid(static_cast<unsigned>((sms < kSms ? sms : kSms) * Shape<R>::kBlocks));
-  return launch_pdl(cached_attention_kernel<R>, grid, dim3(kThreads), Shape<R>::kSmem, 1, st, k, v, a, w);
+  return launch_pdl(cached_attention_kernel<R>, grid, dim3(Shape<R>::kThreads), Shape<R>::kSmem, 1, st, k, v, a, w);
 }
 
 }  // namespace

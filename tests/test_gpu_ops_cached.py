@@ -4,12 +4,12 @@ in 64 bits on the values that the cache stands for.
 What the kernel rounds, for a row with keys j: q, as two terms, is off by at most 2^-21 of its largest value, an element, which is
 2^-21 max |q| sum |k|; the score's 2 x 128 products are summed in fp32 by 8 instructions, each off by at most 5 U32 of its terms'
 sizes (at most 1 + 2^-3 times sum |q k|), joined and scaled (4 roundings), and so is the logarithm t = s log2 e + b, and t - m: delta =
-scale (2^-21 max |q| sum |k| + 50 U32 sum |q k|) + 6 U32 |t|; the exponential adds 2^-22, the weight's two terms 2^-8 of it, or 2^-20 of the
-row's largest weight (the second term's smallest step is 2^-9, half of that counts a sixteenth, the largest weight is at least 2^6).  Sums
+scale (2^-21 max |q| sum |k| + 50 U32 sum |q k|) + 6 U32 |t|; the exponential adds 2^-22, the weight's two terms 2^-8 of it, or 2^-18 of the
+row's largest weight (the second term's smallest step is 2^-9, half of that counts a sixteenth, the largest weight is at least 2^4).  Sums
 over n keys: an instruction for 32 of them for each term, 5 U32 of their sizes each time, and the
 denominator at most n / 4 + 64 roundings: n + 64 covers both.  So O is off by at most sum_j p_j |v_j| (2^-8 + 2 delta + 2^-21 + 2 (n + 64) U32)
 (delta, the exponential and the sums once for the numerator and once for the denominator, which the weight's rounding does not
-enter) and 2^-20 sum_j |v8_j| / l."""
+enter) and 2^-18 sum_j |v8_j| / l."""
 import math
 
 import pytest
@@ -71,7 +71,7 @@ def reference(q, cache, starts, lens, prefix=None, scale=None):
             m = tt.amax(-1, keepdim=True)
             den = torch.exp2(tt - bias - m).sum(-1, keepdim=True)
             v8 = v[:seen].abs() / torch.exp2(b[:seen])[..., None]
-            so[s, i] = (torch.einsum("hgk,khd->hgd", p * each, v[:seen].abs()) + 2.0 ** -20 * v8.sum(0)[:, None] / den).view(hq, D)
+            so[s, i] = (torch.einsum("hgk,khd->hgd", p * each, v[:seen].abs()) + 2.0 ** -18 * v8.sum(0)[:, None] / den).view(hq, D)
             sl[s, i] = (delta[..., 0] + 2.0 ** -21 + (seen + 64) * U32).view(-1) + 8 * U32 * (lse[s, i].abs() + 60)
     return o, so, lse, sl
 
