@@ -472,51 +472,83 @@ def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, ori
     return f.to(device)
 
 
-def _tokens(name: str, x: torch.Tensor, like: torch.Tensor, tokens: int) -> int:
-    """The heads of a [tokens, heads, 128] tensor."""
+# The functions below hand device addresses to the binding, and look at each property of a tensor once: a Grace core takes
+# 0.1 - 0.4 us for one.
+
+def _device_index(name: str, x: torch.Tensor) -> int:
+    if not isinstance(x, torch.Tensor) or x.get_device() < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return x.get_device()
+
+
+def _head_tensor(name: str, x: torch.Tensor, like: torch.Tensor, index: int, tokens: int | None = None, copy: bool = True):
+    """(tensor, address, tokens, heads, token stride) of [tokens, heads, 128] bf16 heads one after the other, of a copy where
+    they are not (with `copy`; else refused).  Hold the tensor until the call is enqueued."""
+    if isinstance(x, torch.Tensor) and x.dtype is _BF16 and x.get_device() == index:
+        shape = x.shape
+        if len(shape) == 3 and shape[2] == HEAD_DIM and (tokens is None or shape[0] == tokens) and shape[1]:
+            t, h, d = shape
+            a, b, c = x.stride()
+            p = x.data_ptr()
+            if c == 1 and not p & 15 and (b == d or h == 1):
+                if t <= 1:
+                    return x, p, t, h, h * d
+                if a >= h * d and not a & 7:
+                    return x, p, t, h, a
+            if not copy:
+                if t == 0:
+                    return x, p, t, h, h * d
+                raise ValueError(f"{name} must have contiguous, 16-byte aligned tokens that do not overlap")
+            x = x.clone(memory_format=torch.contiguous_format)
+            return x, x.data_ptr(), t, h, h * d
     _check(name, x, like)
-    if x.dim() != 3 or x.shape[0] != tokens or x.shape[2] != HEAD_DIM or x.shape[1] == 0:
-        raise ValueError(f"{name} must have shape [{tokens}, heads, {HEAD_DIM}], not {tuple(x.shape)}")
-    return x.shape[1]
+    raise ValueError(f"{name} must have shape [{'tokens' if tokens is None else tokens}, heads, {HEAD_DIM}], not {tuple(x.shape)}")
 
 
-def _rotation(x: torch.Tensor, positions, frequencies, layout, q_weight, k_weight, heads: int, kv_heads: int):
-    """Checked arguments of a norm and rotation: (positions, frequencies, rot, layout, q_weight, k_weight)."""
-    tokens = x.shape[0]
+def _list(name: str, x: torch.Tensor, like: torch.Tensor, index: int, n: int, dtype) -> tuple[torch.Tensor, int]:
+    """(tensor, address) of a contiguous vector of n values, a copy where it is not."""
+    if not (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == index and x.shape == (n,)):
+        _check(name, x, like, (n,), dtype)
+    if not x.is_contiguous():
+        x = x.contiguous()
+    return x, x.data_ptr()
+
+
+def _rotation(x: torch.Tensor, index: int, tokens: int, positions, frequencies, layout, q_weight, k_weight, heads: int, kv_heads: int):
+    """Checked arguments of a norm and rotation: addresses of positions, frequencies and the weights, rot, the layout's code, and
+    the tensors to hold."""
     code = LAYOUTS.get(layout, layout)
-    if code not in LAYOUTS.values():
+    if code not in (dm.ROTARY_HALF, dm.ROTARY_INTERLEAVED):
         raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
-    if (positions is None) != (frequencies is None):
-        raise ValueError("positions and frequencies go together")
-    rot = 0
-    if frequencies is not None:
+    rot, at, by, wq, wk = 0, None, None, None, None
+    if frequencies is not None and positions is not None:
         _check("frequencies", frequencies, x, None, _F64)
         if frequencies.dim() != 1:
             raise ValueError("frequencies must be a vector")
-        rot = 2 * frequencies.numel()
+        rot = 2 * frequencies.shape[0]
         if rot > HEAD_DIM or rot % 16:
             raise ValueError(f"there must be a multiple of 8 frequencies, at most {HEAD_DIM // 2}, not {rot // 2}")
-        _check("positions", positions, x, (tokens,), _I32)
-        positions, frequencies = positions.contiguous(), frequencies.contiguous()
-    if heads and kv_heads and (q_weight is None) != (k_weight is None):
-        raise ValueError("q_weight and k_weight go together")
-    if heads == 0 and q_weight is not None or kv_heads == 0 and k_weight is not None:
-        raise ValueError("a weight needs its heads")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _check(name, w, x, (HEAD_DIM,))
-    return positions, frequencies, rot, code, _vec(q_weight), _vec(k_weight)
+        frequencies, by = _list("frequencies", frequencies, x, index, rot // 2, _F64)
+        positions, at = _list("positions", positions, x, index, tokens, _I32)
+    elif frequencies is not None or positions is not None:
+        raise ValueError("positions and frequencies go together")
+    if q_weight is not None or k_weight is not None:
+        if heads and kv_heads and (q_weight is None or k_weight is None):
+            raise ValueError("q_weight and k_weight go together")
+        if q_weight is not None and not heads or k_weight is not None and not kv_heads:
+            raise ValueError("a weight needs its heads")
+        if q_weight is not None:
+            _check("q_weight", q_weight, x, _WEIGHT)
+            q_weight = _vec(q_weight)
+            wq = q_weight.data_ptr()
+        if k_weight is not None:
+            _check("k_weight", k_weight, x, _WEIGHT)
+            k_weight = _vec(k_weight)
+            wk = k_weight.data_ptr()
+    return at, by, rot, code, wq, wk, (positions, frequencies, q_weight, k_weight)
 
 
-def _heads_out(name: str, out, like: torch.Tensor) -> tuple[torch.Tensor, int]:
-    """The output for [tokens, heads, 128] heads and its token stride: `out`, or a new one."""
-    if out is None:
-        return torch.empty(like.shape, dtype=_BF16, device=like.device), like.shape[1] * HEAD_DIM
-    _check(name, out, like, like.shape)
-    same, ld = _heads(name, out)
-    if same is not out:
-        raise ValueError(f"{name} must have contiguous, 16-byte aligned tokens that do not overlap")
-    return out, ld
+_WEIGHT = (HEAD_DIM,)
 
 
 def qk_rotary_fwd(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor | None, frequencies: torch.Tensor | None,
@@ -528,21 +560,26 @@ def qk_rotary_fwd(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tens
     or None for no rotation.  layout: "half" (value i pairs with i + len(frequencies)) or "interleaved" (2 i with 2 i + 1);
     the rotated values are multiplied by `amplitude`.  q and k may be slices of a fused projection; k may be None.  `out`:
     tensors for (q', k'), which may be q and k."""
-    _check("q", q)
-    if q.dim() != 3:
-        raise ValueError(f"q must have shape [tokens, heads, {HEAD_DIM}], not {tuple(q.shape)}")
-    tokens = q.shape[0]
-    hq = _tokens("q", q, q, tokens)
-    hkv = 0 if k is None else _tokens("k", k, q, tokens)
-    positions, frequencies, rot, code, q_weight, k_weight = _rotation(q, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
-    yq, ld_yq = _heads_out("out[0]", None if out is None else out[0], q)
-    q, ld_q = _heads("q", q)
-    yk, ld_k, ld_yk = None, 0, 0
+    index = _device_index("q", q)
+    q, pq, tokens, hq, ld_q = _head_tensor("q", q, q, index)
+    pk, hkv, ld_k, yk, pyk, ld_yk = None, 0, 0, None, None, 0
     if k is not None:
-        yk, ld_yk = _heads_out("out[1]", None if out is None else out[1], k)
-        k, ld_k = _heads("k", k)
-    _call(dm.domino_qk_rotary_fwd, q, q, ld_q, k, ld_k, positions, frequencies, rot, code, amplitude, q_weight, k_weight, eps, yq,
-          ld_yq, yk, ld_yk, tokens, hq, hkv)
+        k, pk, _, hkv, ld_k = _head_tensor("k", k, q, index, tokens)
+    at, by, rot, code, wq, wk, held = _rotation(q, index, tokens, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
+    if out is None:
+        yq = torch.empty((tokens, hq, HEAD_DIM), dtype=_BF16, device=q.device)
+        pyq, ld_yq = yq.data_ptr(), hq * HEAD_DIM
+        if hkv:
+            yk = torch.empty((tokens, hkv, HEAD_DIM), dtype=_BF16, device=q.device)
+            pyk, ld_yk = yk.data_ptr(), hkv * HEAD_DIM
+    else:
+        yq, pyq, _, h, ld_yq = _head_tensor("out[0]", out[0], q, index, tokens, copy=False)
+        if hkv:
+            yk, pyk, _, h2, ld_yk = _head_tensor("out[1]", out[1], q, index, tokens, copy=False)
+        if h != hq or hkv and h2 != hkv:
+            raise ValueError("out must have as many heads as q and k")
+    _call(dm.domino_qk_rotary_fwd, q, pq, ld_q, pk, ld_k, at, by, rot, code, amplitude, wq, wk, eps, pyq, ld_yq, pyk, ld_yk, tokens,
+          hq, hkv)
     return yq, yk
 
 
@@ -553,46 +590,41 @@ def qk_rotary_bwd(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.Tensor | N
     """Gradients of `qk_rotary_fwd` from those of its outputs: (gq, gk, gq_weight, gk_weight), the first two bf16, the others
     fp32 (None without weights).  q and k, the forward's inputs, are needed with weights only.  `grads`, a pair of fp32
     buffers for the weights' gradients, is added to instead of allocated."""
-    _check("gq", gq)
-    if gq.dim() != 3:
-        raise ValueError(f"gq must have shape [tokens, heads, {HEAD_DIM}], not {tuple(gq.shape)}")
-    tokens = gq.shape[0]
-    hq = _tokens("gq", gq, gq, tokens)
-    hkv = 0 if gk is None else _tokens("gk", gk, gq, tokens)
-    positions, frequencies, rot, code, q_weight, k_weight = _rotation(gq, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
-    norm = q_weight is not None
-    gwq = gwk = None
+    index = _device_index("gq", gq)
+    gq, pgq, tokens, hq, ld_gyq = _head_tensor("gq", gq, gq, index)
+    pgk, hkv, ld_gyk, yk, pyk = None, 0, 0, None, None
+    if gk is not None:
+        gk, pgk, _, hkv, ld_gyk = _head_tensor("gk", gk, gq, index, tokens)
+    at, by, rot, code, wq, wk, held = _rotation(gq, index, tokens, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
+    gwq = gwk = pq = pk = None
     ld_q = ld_k = 0
-    if norm:
+    if wq is not None:
         if q is None or (k is None) != (gk is None):
             raise ValueError("the norm's gradient needs q and k")
-        _check("q", q, gq, gq.shape)
-        q, ld_q = _heads("q", q)
+        q, pq, _, h, ld_q = _head_tensor("q", q, gq, index, tokens)
+        h2 = hkv
         if hkv:
-            _check("k", k, gq, gk.shape)
-            k, ld_k = _heads("k", k)
+            k, pk, _, h2, ld_k = _head_tensor("k", k, gq, index, tokens)
+        if h != hq or h2 != hkv:
+            raise ValueError("q and k must have as many heads as their gradients")
         if grads is not None:
             gwq, gwk = grads
             for name, g in (("gq_weight", gwq), ("gk_weight", gwk)):
                 if name == "gk_weight" and not hkv:
                     continue
-                _check(f"the buffer of {name}", g, gq, (HEAD_DIM,), _F32)
+                _check(f"the buffer of {name}", g, gq, _WEIGHT, _F32)
                 if not g.is_contiguous() or g.data_ptr() % 16:
                     raise ValueError(f"the buffer of {name} must be contiguous and 16-byte aligned")
         else:
             gwq = torch.empty(HEAD_DIM, dtype=_F32, device=gq.device)
             gwk = torch.empty(HEAD_DIM, dtype=_F32, device=gq.device) if hkv else None
-    else:
-        q = k = None
-    gq, ld_gyq = _heads("gq", gq)
-    yq, ld_gq = _heads_out("gq", None, gq)
-    yk, ld_gyk, ld_gk = None, 0, 0
+    yq = torch.empty((tokens, hq, HEAD_DIM), dtype=_BF16, device=gq.device)
     if hkv:
-        gk, ld_gyk = _heads("gk", gk)
-        yk, ld_gk = _heads_out("gk", None, gk)
-    _call(dm.domino_qk_rotary_bwd, gq, gq, ld_gyq, gk, ld_gyk, q, ld_q, k, ld_k, positions, frequencies, rot, code, amplitude,
-          q_weight, k_weight, eps, yq, ld_gq, yk, ld_gk, gwq, gwk, int(grads is not None), tokens, hq, hkv,
-          scratch=_rotary_scratch(tokens, hq, hkv) if norm else 0)
+        yk = torch.empty((tokens, hkv, HEAD_DIM), dtype=_BF16, device=gq.device)
+        pyk = yk.data_ptr()
+    _call(dm.domino_qk_rotary_bwd, gq, pgq, ld_gyq, pgk, ld_gyk, pq, ld_q, pk, ld_k, at, by, rot, code, amplitude, wq, wk, eps,
+          yq.data_ptr(), hq * HEAD_DIM, pyk, hkv * HEAD_DIM, gwq, gwk, int(grads is not None), tokens, hq, hkv,
+          scratch=_rotary_scratch(tokens, hq, hkv) if wq is not None else 0)
     return yq, yk, gwq, gwk
 
 
@@ -673,26 +705,27 @@ class QuantizedCache(NamedTuple):
         return QuantizedCache(*codes, *(torch.full((kv_heads, rows), EXP_BIAS, dtype=_U8, device=device) for _ in range(2)))
 
 
-def _cache(cache: tuple, like: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, int, int, int]:
-    """Checked tensors of a cache, the row stride of its exponents, its rows and its heads."""
+def _cache(cache: tuple, like: torch.Tensor, index: int):
+    """(k, v, k_exp, v_exp) addresses of a cache, the row stride of its exponents, its rows and its heads."""
     k, v, ke, ve = cache
-    _check("the cache's k", k, like, None, _FP8)
-    if k.dim() != 3 or k.shape[2] != HEAD_DIM or k.shape[1] == 0:
-        raise ValueError(f"the cache's k must have shape [rows, kv_heads, {HEAD_DIM}], not {tuple(k.shape)}")
-    rows, hkv, _ = k.shape
-    _check("the cache's v", v, like, k.shape, _FP8)
+    shape = k.shape if isinstance(k, torch.Tensor) else ()
+    if not (len(shape) == 3 and k.dtype is _FP8 and k.get_device() == index and shape[2] == HEAD_DIM and shape[1]):
+        _check("the cache's k", k, like, None, _FP8)
+        raise ValueError(f"the cache's k must have shape [rows, kv_heads, {HEAD_DIM}], not {tuple(shape)}")
+    rows, hkv, _ = shape
+    _check("the cache's v", v, like, shape, _FP8)
     _check("the cache's k_exp", ke, like, (hkv, rows), _U8)
     _check("the cache's v_exp", ve, like, (hkv, rows), _U8)
-    for name, x in (("k", k), ("v", v)):
-        if not x.is_contiguous() or x.data_ptr() % 16:
-            raise ValueError(f"the cache's {name} must be contiguous and 16-byte aligned")
+    pk, pv = k.data_ptr(), v.data_ptr()
+    if not (k.is_contiguous() and v.is_contiguous()) or pk & 15 or pv & 15:
+        raise ValueError("the cache's k and v must be contiguous and 16-byte aligned")
     ld = rows
     if not (ke.is_contiguous() and ve.is_contiguous()):
         ld = ke.stride(0)
         if ke.stride() != ve.stride() or (rows > 1 and ke.stride(1) != 1) or (hkv > 1 and ld < rows):
             raise ValueError("the cache's k_exp and v_exp must have contiguous rows that do not overlap, and the same strides")
         ld = max(ld, rows)
-    return k, v, ke, ve, ld, rows, hkv
+    return (pk, pv, ke.data_ptr(), ve.data_ptr()), ld, rows, hkv
 
 
 def cache_write(cache: tuple, rows: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor | None = None,
@@ -707,45 +740,49 @@ def cache_write(cache: tuple, rows: torch.Tensor, k: torch.Tensor, v: torch.Tens
     _no_tangent("cache_write", q, k, v, q_weight, k_weight)
     if _differentiated(q, k, v, q_weight, k_weight):
         raise ValueError("cache_write has no backward: call it under torch.no_grad(), or detach its inputs")
-    _check("k", k)
-    if k.dim() != 3:
-        raise ValueError(f"k must have shape [tokens, kv_heads, {HEAD_DIM}], not {tuple(k.shape)}")
-    tokens = k.shape[0]
-    hkv = _tokens("k", k, k, tokens)
-    hq = 0 if q is None else _tokens("q", q, k, tokens)
-    _check("v", v, k, k.shape)
-    k8, v8, ke, ve, ld_exp, cache_rows, cache_heads = _cache(cache, k)
-    if cache_heads != hkv:
-        raise ValueError(f"k has {hkv} heads, the cache {cache_heads}")
-    _check("rows", rows, k, (tokens,), _I32)
-    positions, frequencies, rot, code, q_weight, k_weight = _rotation(k, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
-    y, ld_q, ld_y = None, 0, 0
+    index = _device_index("k", k)
+    k, pk, tokens, hkv, ld_k = _head_tensor("k", k, k, index)
+    v, pv, _, h, ld_v = _head_tensor("v", v, k, index, tokens)
+    if h != hkv:
+        raise ValueError(f"v has {h} heads, k {hkv}")
+    codes, ld_exp, cache_rows, h = _cache(cache, k, index)
+    if h != hkv:
+        raise ValueError(f"k has {hkv} heads, the cache {h}")
+    rows, at_rows = _list("rows", rows, k, index, tokens, _I32)
+    pq, hq, ld_q, y, py, ld_y = None, 0, 0, None, None, 0
     if q is not None:
-        y, ld_y = _heads_out("out", out, q)
-        q, ld_q = _heads("q", q)
-    k, ld_k = _heads("k", k)
-    v, ld_v = _heads("v", v)
-    _call(dm.domino_cache_write, k, q, ld_q, k, ld_k, v, ld_v, positions, frequencies, rot, code, amplitude, q_weight, k_weight, eps, y,
-          ld_y, rows.contiguous(), k8, v8, ke, ve, ld_exp, cache_rows, tokens, hq, hkv)
+        q, pq, _, hq, ld_q = _head_tensor("q", q, k, index, tokens)
+    at, by, rot, code, wq, wk, held = _rotation(k, index, tokens, positions, frequencies, layout, q_weight, k_weight, hq, hkv)
+    if hq and out is None:
+        y = torch.empty((tokens, hq, HEAD_DIM), dtype=_BF16, device=k.device)
+        py, ld_y = y.data_ptr(), hq * HEAD_DIM
+    elif hq:
+        y, py, _, h, ld_y = _head_tensor("out", out, k, index, tokens, copy=False)
+        if h != hq:
+            raise ValueError("out must have as many heads as q")
+    _call(dm.domino_cache_write, k, pq, ld_q, pk, ld_k, pv, ld_v, at, by, rot, code, amplitude, wq, wk, eps, py, ld_y, at_rows, *codes,
+          ld_exp, cache_rows, tokens, hq, hkv)
     return y
 
 
 def cache_read(cache: tuple, rows: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """What the cache holds in the rows `rows` (int32): (k, v), each [len(rows), kv_heads, 128] in bf16, exact; zeros where a
     row is negative, or beyond the cache, which `device_status` reports.  `out`: tensors for them."""
-    _check("rows", rows, None, None, _I32)
+    index = _device_index("rows", rows)
     if rows.dim() != 1:
         raise ValueError("rows must be a vector")
-    k8, v8, ke, ve, ld_exp, cache_rows, hkv = _cache(cache, rows)
-    tokens = rows.numel()
+    tokens = rows.shape[0]
+    rows, at_rows = _list("rows", rows, rows, index, tokens, _I32)
+    codes, ld_exp, cache_rows, hkv = _cache(cache, rows, index)
     if out is None:
         k, v = (torch.empty((tokens, hkv, HEAD_DIM), dtype=_BF16, device=rows.device) for _ in range(2))
-        ld_k = ld_v = hkv * HEAD_DIM
+        pk, pv, ld_k, ld_v = k.data_ptr(), v.data_ptr(), hkv * HEAD_DIM, hkv * HEAD_DIM
     else:
-        for name, x in zip(("out[0]", "out[1]"), out):
-            _check(name, x, rows, (tokens, hkv, HEAD_DIM))
-        (k, ld_k), (v, ld_v) = (_heads_out(f"out[{i}]", x, x) for i, x in enumerate(out))
-    _call(dm.domino_cache_read, rows, k8, v8, ke, ve, ld_exp, cache_rows, rows.contiguous(), k, ld_k, v, ld_v, tokens, hkv)
+        k, pk, _, h, ld_k = _head_tensor("out[0]", out[0], rows, index, tokens, copy=False)
+        v, pv, _, h2, ld_v = _head_tensor("out[1]", out[1], rows, index, tokens, copy=False)
+        if h != hkv or h2 != hkv:
+            raise ValueError("out must have as many heads as the cache")
+    _call(dm.domino_cache_read, rows, *codes, ld_exp, cache_rows, at_rows, pk, ld_k, pv, ld_v, tokens, hkv)
     return k, v
 
 
@@ -763,37 +800,38 @@ def cached_attention(q: torch.Tensor, cache: tuple, k_start: torch.Tensor, k_len
     and `device_status` reports them.  Forward only.  Made for few tokens a sequence: for long chunks, `cache_read` and
     `packed_attention`."""
     _no_tangent("cached_attention", q)
-    _check("q", q)
-    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
-        raise ValueError(f"q must have shape [n, heads, {HEAD_DIM}] or [n, t, heads, {HEAD_DIM}], not {tuple(q.shape)}")
-    if torch.is_grad_enabled() and q.requires_grad:
-        raise ValueError("cached_attention has no backward: call it under torch.no_grad(), or detach its inputs")
-    n, t, hq = q.shape[0], 1 if q.dim() == 3 else q.shape[1], q.shape[-2]
-    k8, v8, ke, ve, ld_exp, cache_rows, hkv = _cache(cache, q)
-    if hq == 0 or hq % hkv:
-        raise ValueError("the query heads must be a multiple of the cache's heads")
-    _check("k_start", k_start, q, (n,), _I32)
-    _check("k_len", k_len, q, (n,), _I32)
-    if prefix is not None:
-        _check("prefix", prefix, q, (2,), _I32)
-        prefix = prefix.contiguous()
+    index = _device_index("q", q)
     shape = q.shape
-    q, ld_q = _heads("q", q.reshape(n * t, hq, HEAD_DIM))
+    if len(shape) not in (3, 4) or shape[-1] != HEAD_DIM:
+        raise ValueError(f"q must have shape [n, heads, {HEAD_DIM}] or [n, t, heads, {HEAD_DIM}], not {tuple(shape)}")
+    if q.requires_grad and torch.is_grad_enabled():
+        raise ValueError("cached_attention has no backward: call it under torch.no_grad(), or detach its inputs")
+    codes, ld_exp, cache_rows, hkv = _cache(cache, q, index)
+    n, t = shape[0], 1
+    if len(shape) == 4:
+        t = shape[1]
+        q = q.reshape(n * t, shape[2], HEAD_DIM)
+    q, pq, tokens, hq, ld_q = _head_tensor("q", q, q, index)
+    if hq % hkv:
+        raise ValueError("the query heads must be a multiple of the cache's heads")
+    k_start, at_start = _list("k_start", k_start, q, index, n, _I32)
+    k_len, at_len = _list("k_len", k_len, q, index, n, _I32)
+    at_prefix = None
+    if prefix is not None:
+        prefix, at_prefix = _list("prefix", prefix, q, index, 2, _I32)
     if out is None:
-        o = out = torch.empty(shape, dtype=_BF16, device=q.device)
-        ld_o = hq * HEAD_DIM
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        po, ld_o = out.data_ptr(), hq * HEAD_DIM
     else:
         _check("out", out, q, shape)
         try:
-            o = out.view(n * t, hq, HEAD_DIM)
+            o = out.view(tokens, hq, HEAD_DIM)
         except RuntimeError:
             raise ValueError("out must have tokens at one stride") from None
-        same, ld_o = _heads("out", o)
-        if same is not o:
-            raise ValueError("out must have contiguous, 16-byte aligned tokens that do not overlap")
+        _, po, _, _, ld_o = _head_tensor("out", o, q, index, tokens, copy=False)
     lse = torch.empty(shape[:-1], dtype=_F32, device=q.device) if return_lse else None
-    _call(dm.domino_attn_cached_fwd, q, q, ld_q, k8, v8, ke, ve, ld_exp, cache_rows, k_start.contiguous(), k_len.contiguous(), prefix,
-          HEAD_DIM ** -0.5 if scale is None else scale, o, ld_o, lse, n, t, hq, hkv,
+    _call(dm.domino_attn_cached_fwd, q, pq, ld_q, *codes, ld_exp, cache_rows, at_start, at_len, at_prefix,
+          HEAD_DIM ** -0.5 if scale is None else scale, po, ld_o, lse, n, t, hq, hkv,
           scratch=_cached_scratch(n, t, hq, hkv, int(prefix is not None)))
     return (out, lse) if return_lse else out
 
