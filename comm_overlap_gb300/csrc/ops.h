@@ -233,7 +233,7 @@ struct CacheReadArgs {
   int32_t hkv, cache_rows;
 };
 cudaError_t launch_rotary(const RotaryArgs& a, int sms, cudaStream_t st);
-// `part`: rotary_bwd_blocks() rows of 256 floats, written by the backward and summed by launch_rotary_sums.
+// `part`: rotary_bwd_blocks() rows of 128 floats, written by the backward and summed by launch_rotary_sums.
 int rotary_bwd_blocks(int64_t tokens, int hq, int hkv, int sms);
 cudaError_t launch_rotary_bwd(const RotaryBwdArgs& a, float* part, int sms, cudaStream_t st);
 cudaError_t launch_rotary_sums(const RotaryBwdArgs& a, const float* part, int sms, cudaStream_t st);

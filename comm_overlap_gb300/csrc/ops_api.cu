@@ -198,7 +198,7 @@ domino_status check_tokens(const void* p, const char* name, int64_t ld, const ch
   return tokens > 0 ? check_ptr(p, name) : DOMINO_OK;
 }
 size_t rotary_bwd_bytes(int64_t tokens, int32_t heads, int32_t kv_heads) {
-  return tokens == 0 ? 0 : size_t(dm::rotary_bwd_blocks(tokens, heads, kv_heads, kGb300Sms)) * 256 * 4;
+  return tokens == 0 ? 0 : size_t(dm::rotary_bwd_blocks(tokens, heads, kv_heads, kGb300Sms)) * 128 * 4;
 }
 domino_status check_cache(const void* k8, const void* v8, const void* k_exp, const void* v_exp, int64_t ld_exp, int64_t rows,
                           int32_t kv_heads) {

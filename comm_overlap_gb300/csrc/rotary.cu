@@ -4,16 +4,22 @@
 // A head's 128 values are held by 8 lanes of a warp, two 16-byte pieces each, chosen so that a rotated pair always lies in one
 // lane: with rot = 16 m rotated values, lane j < m holds pieces j and j + m (half layout: value i pairs with i + rot / 2, which
 // is m pieces further; interleaved: 2 i with 2 i + 1, in one piece), the lanes from m on two neighbouring pieces of the rest.
-// A warp takes four heads at a time, all of one token, whose cosines and sines it computes once.
+// A warp takes twice four heads at a time, all of one token, whose cosines and sines it computes once.  Steps come through a ring in
+// shared memory of each warp, several ahead, whatever token they belong to; it waits for no other warp.  Blocks are dealt to the kinds of
+// heads by their bytes: forward, queries and keys have the same blocks and values others; backward each kind has its own, so that a
+// lane keeps one kind's weight and sums in registers.
 //
 // Angles: a position turns pair i by position x frequency.  The frequency is kept as a 64-bit fraction of a turn, so the
 // product's low 64 bits are the angle's fraction of a turn without any rounding by the position's size; its upper 32 bits go to
 // sincospif.
 //
 // Bound: memory.  Forward 4 bytes a value, backward 6 (4 without norm), cache 3.
-#include <atomic>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "actfn.cuh"
+#include "f32x2.cuh"
 #include "ops.h"
 #include "ptx.cuh"
 
@@ -23,15 +29,33 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kHeadsAbreast = 4;  // heads of a warp's step
+constexpr int kReadAbreast = 2;
+// Blocks of an SM and steps in flight of a warp.
+constexpr int kFwdBlocks = 3, kFwdDepth = 8, kWriteBlocks = 4, kWriteDepth = 3, kBwdBlocks = 3, kBwdDepth = 4;
+// Blocks of two kinds of heads, and the warps that share a token's steps.
+struct RotaryShares {
+  int blocks[2], split[2];
+};
+__host__ __device__ constexpr int steps_of(int heads) { return (heads + 2 * kHeadsAbreast - 1) / (2 * kHeadsAbreast); }
 
 __device__ int g_rotary_err;
 
-__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
-  v[0] = bf16lo(w.x); v[1] = bf16hi(w.x); v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
-  v[4] = bf16lo(w.z); v[5] = bf16hi(w.z); v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
+__device__ __forceinline__ void unpack8(const uint4& w, uint64_t (&v)[4]) {
+  v[0] = f2(bf16lo(w.x), bf16hi(w.x));
+  v[1] = f2(bf16lo(w.y), bf16hi(w.y));
+  v[2] = f2(bf16lo(w.z), bf16hi(w.z));
+  v[3] = f2(bf16lo(w.w), bf16hi(w.w));
 }
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
+__device__ __forceinline__ float sum2(uint64_t v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return lo + hi;
 }
 
 // Frequency (radians a position) as a fraction of a turn, in units of 2^-64 turns.
@@ -57,12 +81,10 @@ __device__ __forceinline__ Place place_of(int lane, int rot) {
   return p;
 }
 
-// Cosines and sines of a token's angles, times the amplitude: computed by the warp's lanes, two pairs each, and read back from
-// shared memory (64 float2 a warp) in the order of the lane's own pairs: half layout 8 j + e for (a[e], b[e]); interleaved
-// 4 ca + i for (a[2 i], a[2 i + 1]) and 4 cb + i for b's.
-template <bool HALF>
-__device__ __forceinline__ void token_angles(float2* mine, const unsigned long long* turns, int position, int rot, float amplitude,
-                                             int lane, const Place& p, float (&c)[8], float (&s)[8]) {
+// Cosines and sines of a token's angles, times the amplitude (and sines times `sign`), computed by the warp's lanes, two pairs each,
+// to shared memory (64 of each a warp).
+__device__ __forceinline__ void token_angles(float* cosines, float* sines, const unsigned long long* turns, int position, int rot,
+                                             float amplitude, float sign, int lane) {
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -71,39 +93,51 @@ __device__ __forceinline__ void token_angles(float2* mine, const unsigned long l
       const unsigned long long at = turns[i] * static_cast<unsigned long long>(static_cast<long long>(position));
       float sn, cs;
       sincospif(static_cast<float>(static_cast<int>(at >> 32)) * 0x1p-31f, &sn, &cs);
-      mine[i] = make_float2(cs * amplitude, sn * amplitude);
+      cosines[i] = cs * amplitude;
+      sines[i] = sn * (amplitude * sign);
     }
   }
   __syncwarp();
-  if (p.turns) {
-    const int first = HALF ? 8 * p.j : 4 * p.ca, second = HALF ? 8 * p.j + 4 : 4 * p.cb;
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const float4 x = *reinterpret_cast<const float4*>(mine + first + i), y = *reinterpret_cast<const float4*>(mine + second + i);
-      c[i] = x.x; s[i] = x.y; c[i + 1] = x.z; s[i + 1] = x.w;
-      c[i + 4] = y.x; s[i + 4] = y.y; c[i + 5] = y.z; s[i + 5] = y.w;
-    }
-  }
+}
+// Those of the lane's own pairs: half layout 8 j + e for (a[e], b[e]); interleaved 4 ca + i for (a[2 i], a[2 i + 1]) and 4 cb + i for b's.
+template <bool HALF>
+__device__ __forceinline__ void own_pairs(const float* v, const Place& p, uint64_t (&x)[4]) {
+  const int first = HALF ? 8 * p.j : 4 * p.ca, second = HALF ? 8 * p.j + 4 : 4 * p.cb;
+  const float4 y = *reinterpret_cast<const float4*>(v + first), z = *reinterpret_cast<const float4*>(v + second);
+  x[0] = f2(y.x, y.y);
+  x[1] = f2(y.z, y.w);
+  x[2] = f2(z.x, z.y);
+  x[3] = f2(z.z, z.w);
 }
 
+// (a, b) -> (a cos - b sin, a sin + b cos): half layout two pairs at a time, interleaved within each two values.
 template <bool HALF>
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const float (&c)[8], const float (&s)[8], float sign) {
+__device__ __forceinline__ void rotate(uint64_t (&a)[4], uint64_t (&b)[4], const uint64_t (&c)[4], const uint64_t (&s)[4]) {
   if (HALF) {
+    const uint64_t minus = f2(-1.0f, -1.0f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = a[e], y = b[e], sn = s[e] * sign;
-      a[e] = fmaf(x, c[e], -y * sn);
-      b[e] = fmaf(x, sn, y * c[e]);
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t x = a[e], y = b[e], ys = mul_f2(y, s[e]);
+      a[e] = fma_f2(ys, minus, mul_f2(x, c[e]));
+      b[e] = fma_f2(x, s[e], mul_f2(y, c[e]));
     }
   } else {
+    auto turn = [](uint64_t& v, float cs, float sn) {
+      float x, y;
+      f2_split(v, x, y);
+      v = f2(fmaf(x, cs, -y * sn), fmaf(x, sn, y * cs));
+    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = a[2 * i], y = a[2 * i + 1], sn = s[i] * sign;
-      a[2 * i] = fmaf(x, c[i], -y * sn);
-      a[2 * i + 1] = fmaf(x, sn, y * c[i]);
-      const float z = b[2 * i], w = b[2 * i + 1], sm = s[i + 4] * sign;
-      b[2 * i] = fmaf(z, c[i + 4], -w * sm);
-      b[2 * i + 1] = fmaf(z, sm, w * c[i + 4]);
+    for (int i = 0; i < 2; ++i) {
+      float c0, c1, s0, s1;
+      f2_split(c[i], c0, c1);
+      f2_split(s[i], s0, s1);
+      turn(a[2 * i], c0, s0);
+      turn(a[2 * i + 1], c1, s1);
+      f2_split(c[i + 2], c0, c1);
+      f2_split(s[i + 2], s0, s1);
+      turn(b[2 * i], c0, s0);
+      turn(b[2 * i + 1], c1, s1);
     }
   }
 }
@@ -119,40 +153,34 @@ __device__ __forceinline__ float head_max(float v) {
   return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
 }
 
-__device__ __forceinline__ float squares(const float (&a)[8], const float (&b)[8]) {
-  float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    s0 = fmaf(a[e], a[e], s0);
-    s1 = fmaf(b[e], b[e], s1);
-  }
-  return s0 + s1;
-}
-
 constexpr float kInvD = 1.0f / 128.0f;
 // Heads whose squares leave fp32's range are measured times this.
 constexpr float kSmaller = 0x1p-80f;
 
-// x / sqrt(mean(x^2) + eps) times the weight (bf16 pieces wa, wb).
-__device__ __forceinline__ void normalise(float (&a)[8], float (&b)[8], const uint4& wa, const uint4& wb, float eps) {
-  float ss = head_sum(squares(a, b)), c = 1.0f;
-  if (__any_sync(0xFFFFFFFFu, !(ss < INFINITY))) {
-    c = ss < INFINITY ? 1.0f : kSmaller;
+// 1 / sqrt(mean(x^2) + eps) of the head, whose values are brought into range: x was multiplied by `small`, and so is the result.
+__device__ __forceinline__ float head_rstd(uint64_t (&a)[4], uint64_t (&b)[4], float eps, float& small) {
+  auto squares = [&] {
+    uint64_t s0 = mul_f2(a[0], a[0]), s1 = mul_f2(b[0], b[0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] *= c;
-      b[e] *= c;
+    for (int e = 1; e < 4; ++e) {
+      s0 = fma_f2(a[e], a[e], s0);
+      s1 = fma_f2(b[e], b[e], s1);
     }
-    ss = head_sum(squares(a, b));
+    return head_sum(sum2(add_f2(s0, s1)));
+  };
+  float ss = squares();
+  small = 1.0f;
+  if (__any_sync(0xFFFFFFFFu, !(ss < INFINITY))) {
+    small = ss < INFINITY ? 1.0f : kSmaller;
+    const uint64_t f = f2(small, small);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = mul_f2(a[e], f);
+      b[e] = mul_f2(b[e], f);
+    }
+    ss = squares();
   }
-  const float rstd = rsqrtf(fmaf(ss, kInvD, eps * c * c));
-  float w[8];
-  unpack8(wa, w);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) a[e] *= rstd * w[e];
-  unpack8(wb, w);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) b[e] *= rstd * w[e];
+  return rsqrtf(fmaf(ss, kInvD, eps * small * small));
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -169,18 +197,23 @@ __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e 
 
 // E4M3 codes of a head: the least e with amax <= 448 x 2^e (1.75 x 2^8), in [-kCacheExpMax, kCacheExpMax] (0 for a head of
 // zeros), then x 2^-e, which is exact, rounded once.  An infinity becomes NaN, and counts no more than one for e.
-__device__ __forceinline__ int quantise(float (&a)[8], float (&b)[8], uint2& qa, uint2& qb) {
-  float amax = 0.0f;
+__device__ __forceinline__ int quantise(const uint64_t (&a)[4], const uint64_t (&b)[4], uint2& qa, uint2& qb) {
+  float x[8], y[8], amax = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(a[e]), fabsf(b[e])));
+  for (int e = 0; e < 4; ++e) {
+    f2_split(a[e], x[2 * e], x[2 * e + 1]);
+    f2_split(b[e], y[2 * e], y[2 * e + 1]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
   amax = head_max(amax);
   if (__any_sync(0xFFFFFFFFu, !(amax < INFINITY))) {
     amax = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      a[e] = fabsf(a[e]) < INFINITY ? a[e] : NAN;
-      b[e] = fabsf(b[e]) < INFINITY ? b[e] : NAN;
-      amax = fmaxf(amax, fmaxf(fabsf(a[e]), fabsf(b[e])));  // (NaN is passed over)
+      x[e] = fabsf(x[e]) < INFINITY ? x[e] : NAN;
+      y[e] = fabsf(y[e]) < INFINITY ? y[e] : NAN;
+      amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));  // (NaN is passed over)
     }
     amax = head_max(amax);
   }
@@ -188,287 +221,522 @@ __device__ __forceinline__ int quantise(float (&a)[8], float (&b)[8], uint2& qa,
   int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u);
   e = amax > 0.0f ? min(max(e, -kCacheExpMax), kCacheExpMax) : 0;
   const float f = power_of_two(-e);
-  qa = make_uint2(e4m3x4(a[0] * f, a[1] * f, a[2] * f, a[3] * f), e4m3x4(a[4] * f, a[5] * f, a[6] * f, a[7] * f));
-  qb = make_uint2(e4m3x4(b[0] * f, b[1] * f, b[2] * f, b[3] * f), e4m3x4(b[4] * f, b[5] * f, b[6] * f, b[7] * f));
+  qa = make_uint2(e4m3x4(x[0] * f, x[1] * f, x[2] * f, x[3] * f), e4m3x4(x[4] * f, x[5] * f, x[6] * f, x[7] * f));
+  qb = make_uint2(e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f), e4m3x4(y[4] * f, y[5] * f, y[6] * f, y[7] * f));
   return e;
 }
 
-// ---- forward: a unit is a token's part of its groups of four heads (queries, then keys, then, into the cache, values)
-template <bool NORM, bool HALF, bool CACHE>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, const int split) {
-  __shared__ unsigned long long turns[64];
-  __shared__ float2 angles[kWarps][64];
-  pdl_launch();
-  pdl_wait();
-  if (static_cast<int>(threadIdx.x) < (a.rot >> 1)) turns[threadIdx.x] = turn_fraction(a.frequencies[threadIdx.x]);
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Place p = place_of(lane, a.rot);
-  const int gq = (a.hq + kHeadsAbreast - 1) / kHeadsAbreast, gk = (a.hkv + kHeadsAbreast - 1) / kHeadsAbreast;
-  const int groups = gq + gk + (CACHE ? gk : 0);
-  uint4 wqa = {}, wqb = {}, wka = {}, wkb = {};
-  if (NORM) {
-    wqa = reinterpret_cast<const uint4*>(a.wq)[p.ca];
-    wqb = reinterpret_cast<const uint4*>(a.wq)[p.cb];
-    if (a.wk) {
-      wka = reinterpret_cast<const uint4*>(a.wk)[p.ca];
-      wkb = reinterpret_cast<const uint4*>(a.wk)[p.cb];
+// 16 bytes from memory to shared memory, zeros unless `there`; each lane reads back only what it asked for itself.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ int64_t divide(int64_t x, int y) {  // x >= 0; nearly always within 32 bits
+  if ((x >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+// A warp's way through its units: a unit is a token's steps (of twice four heads), or, with few tokens, every split-th of them.
+struct Walk {
+  int64_t unit, token;
+  int step;
+  __device__ __forceinline__ void enter(int64_t u, int64_t units, int split) {
+    unit = u;
+    if (u >= units) return;
+    token = split == 1 ? u : divide(u, split);
+    step = static_cast<int>(u - token * split);
+  }
+  // The next step; true where a unit begins.
+  __device__ __forceinline__ bool next(int steps, int split, int64_t stride, int64_t units) {
+    step += split;
+    if (step < steps) return false;
+    enter(unit + stride, units, split);
+    return true;
+  }
+};
+
+// What a lane multiplies its values with: half layout a' = a[..] A - b[..] B, b' = a C + b D, two pairs at a time (without norm A = D and
+// B = C); interleaved the same for the two values of a pair, a's four pairs in the first two of each array.  Lanes that do not turn: a A
+// and b D alone.
+template <bool HALF>
+__device__ __forceinline__ void turn_pairs(uint64_t (&a)[4], uint64_t (&b)[4], const uint64_t (&A)[4], const uint64_t (&B)[4],
+                                           const uint64_t (&C)[4], const uint64_t (&D)[4]) {
+  if (HALF) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t x = a[e], y = b[e];
+      a[e] = fma_f2(x, A[e], mul_f2(y, B[e]));  // (B is negative)
+      b[e] = fma_f2(x, C[e], mul_f2(y, D[e]));
+    }
+  } else {
+    auto turn = [](uint64_t& v, uint64_t A, uint64_t B, uint64_t C, uint64_t D, int half) {
+      float x, y, k[4][2];
+      f2_split(v, x, y);
+      f2_split(A, k[0][0], k[0][1]);
+      f2_split(B, k[1][0], k[1][1]);
+      f2_split(C, k[2][0], k[2][1]);
+      f2_split(D, k[3][0], k[3][1]);
+      v = f2(fmaf(x, k[0][half], y * k[1][half]), fmaf(x, k[2][half], y * k[3][half]));
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      turn(a[2 * i], A[i], B[i], C[i], D[i], 0);
+      turn(a[2 * i + 1], A[i], B[i], C[i], D[i], 1);
+      turn(b[2 * i], A[i + 2], B[i + 2], C[i + 2], D[i + 2], 0);
+      turn(b[2 * i + 1], A[i + 2], B[i + 2], C[i + 2], D[i + 2], 1);
     }
   }
-  const int64_t units = a.tokens * split, stride = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units; u += stride) {
-    const int64_t token = split == 1 ? u : u / split;
-    const int part = static_cast<int>(u - token * split);
-    int row = 0;
-    bool write = true;
-    if (CACHE) {
-      row = a.rows[token];
-      write = row >= 0 && row < a.cache_rows;
-      if (row >= a.cache_rows && lane == 0) atomicCAS(&g_rotary_err, 0, kPackedBadLengths);
-    }
-    // the head of this lane in a group, and its pieces in memory (null past the last head)
-    auto source = [&](int group) -> const uint16_t* {
-      const int which = group < gq ? 0 : group < gq + gk ? 1 : 2;
-      const int head = (group - (which == 0 ? 0 : which == 1 ? gq : gq + gk)) * kHeadsAbreast + p.slot;
-      if (head >= (which == 0 ? a.hq : a.hkv)) return nullptr;
-      return (which == 0 ? a.Q + token * a.ld_q : which == 1 ? a.K + token * a.ld_k : a.V + token * a.ld_v) + head * 128;
-    };
-    auto load = [&](int group, uint4& xa, uint4& xb) {
-      const uint16_t* x = group < groups ? source(group) : nullptr;
-      xa = x ? __ldcs(reinterpret_cast<const uint4*>(x) + p.ca) : make_uint4(0u, 0u, 0u, 0u);
-      xb = x ? __ldcs(reinterpret_cast<const uint4*>(x) + p.cb) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    // two groups in flight, in registers of their own each (moved from one to the other they were waited for: 69 us for 16384
-    // tokens of 32 + 8 heads)
-    uint4 xa, xb, ya, yb;
-    load(part, xa, xb);
-    load(part + split, ya, yb);
-    float c[8], s[8];
-    if (a.rot > 0)
-      token_angles<HALF>(angles[warp], turns, a.positions[token], a.rot, a.amplitude, lane, p, c, s);
-    auto step = [&](int group, uint4& wa, uint4& wb) {
-      float va[8], vb[8];
-      unpack8(wa, va);
-      unpack8(wb, vb);
-      load(group + 2 * split, wa, wb);
-      const bool query = group < gq, value = CACHE && group >= gq + gk;
-      if (!value) {
-        if (NORM) normalise(va, vb, query ? wqa : wka, query ? wqb : wkb, a.eps);
-        if (p.turns) rotate<HALF>(va, vb, c, s, a.sign);
+}
+
+// ---- forward
+template <bool NORM, bool HALF, bool CACHE>
+__global__ void __launch_bounds__(kThreads, CACHE ? kWriteBlocks : kFwdBlocks) rotary_kernel(const RotaryArgs a, const RotaryShares shares) {
+  constexpr int kDepth = CACHE ? kWriteDepth : kFwdDepth;
+  extern __shared__ __align__(16) uint8_t ring_all[];  // of each warp, kDepth steps of 2048 bytes
+  __shared__ unsigned long long turns[64];
+  __shared__ __align__(16) float cosines[kWarps][64], sines[kWarps][64];
+  pdl_launch();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool value = CACHE && static_cast<int>(blockIdx.x) >= shares.blocks[0];  // blocks of values come after the others
+  const int place = static_cast<int>(blockIdx.x) - (value ? shares.blocks[0] : 0), split = shares.split[value];
+  if (!value && static_cast<int>(threadIdx.x) < (a.rot >> 1)) turns[threadIdx.x] = turn_fraction(a.frequencies[threadIdx.x]);
+  __syncthreads();
+  const Place p = place_of(lane, a.rot);
+  // steps of a token: of queries, then keys (or of values alone)
+  const int q_steps = value ? 0 : steps_of(a.hq), steps = q_steps + steps_of(a.hkv);
+  const int64_t units = a.tokens * split, stride = static_cast<int64_t>(shares.blocks[value]) * kWarps;
+  Walk now, ahead;
+  now.enter(static_cast<int64_t>(place) * kWarps + warp, units, split);
+  if (now.unit >= units) return;
+  ahead = now;
+  const uint16_t* const k_from = (value ? a.V : a.K) + p.slot * 128;
+  const int64_t k_ld = value ? a.ld_v : a.ld_k;
+  const uint32_t ring = smem_u32(ring_all) + warp * (kDepth * 2048u) + lane * 16u;
+  uint32_t fill = 0, take = 0;
+  auto load = [&] {
+    if (ahead.unit < units) {
+      const bool query = ahead.step < q_steps;
+      const int head = (ahead.step - (query ? 0 : q_steps)) * (2 * kHeadsAbreast) + p.slot, left = (query ? a.hq : a.hkv) - head;
+      const uint16_t* x = query ? a.Q + ahead.token * a.ld_q + p.slot * 128 : k_from + ahead.token * k_ld;
+      if (left > 0) x += (head - p.slot) * 128;  // (past the last head nothing is read)
+      const uint4* v = reinterpret_cast<const uint4*>(x);
+      const uint32_t to = ring + fill;
+      copy16(to, v + p.ca, left > 0);
+      copy16(to + 512u, v + p.cb, left > 0);
+      if (left > kHeadsAbreast) {
+        copy16(to + 1024u, v + kHeadsAbreast * 16 + p.ca, true);
+        copy16(to + 1536u, v + kHeadsAbreast * 16 + p.cb, true);
       }
-      const int head = (group - (query ? 0 : value ? gq + gk : gq)) * kHeadsAbreast + p.slot;
+      ahead.next(steps, split, stride, units);
+    }
+    copies_commit();
+    fill = fill + 2048u == kDepth * 2048u ? 0u : fill + 2048u;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kDepth - 1; ++i) load();
+  // a token's position and cache row, loaded a unit before they are needed
+  const bool turned = a.rot > 0 && !value;
+  int position = 0, row = 0, to_row = 0;
+  auto look = [&](int64_t unit) {
+    if (unit >= units) return;
+    const int64_t token = split == 1 ? unit : divide(unit, split);
+    if (turned) position = a.positions[token];
+    if (CACHE) row = a.rows[token];
+  };
+  look(now.unit);
+  bool begins = true, was_query = false;
+  uint64_t A[4], B[4], C[4], D[4];
+  while (now.unit < units) {
+    const bool query = now.step < q_steps;
+    if (begins) {
+      if (turned) token_angles(cosines[warp], sines[warp], turns, position, a.rot, a.amplitude, a.sign, lane);
+      if (CACHE) {
+        to_row = row;
+        if (to_row >= a.cache_rows) {
+          if (lane == 0) atomicCAS(&g_rotary_err, 0, kPackedBadLengths);
+          to_row = -1;
+        }
+      }
+      look(now.unit + stride);
+    }
+    if (!value && (begins || (NORM && query != was_query))) {
+      // cosines and sines times the weights of what they are multiplied with
+      if (p.turns) {
+        own_pairs<HALF>(cosines[warp], p, A);
+        own_pairs<HALF>(sines[warp], p, C);
+        const uint64_t minus = f2(-1.0f, -1.0f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          D[e] = A[e];
+          B[e] = mul_f2(C[e], minus);
+        }
+      }
+      if (NORM) {
+        const uint4* w = reinterpret_cast<const uint4*>(query ? a.wq : a.wk);
+        uint64_t wa[4], wb[4];
+        unpack8(w[p.ca], wa);
+        unpack8(w[p.cb], wb);
+        if (!p.turns) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            A[e] = wa[e];
+            D[e] = wb[e];
+          }
+        } else if (HALF) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            A[e] = mul_f2(A[e], wa[e]);
+            C[e] = mul_f2(C[e], wa[e]);
+            B[e] = mul_f2(B[e], wb[e]);
+            D[e] = mul_f2(D[e], wb[e]);
+          }
+        } else {  // the two weights of a pair lie side by side
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x0, y0, x1, y1;
+            f2_split(e < 2 ? wa[2 * (e & 1)] : wb[2 * (e & 1)], x0, y0);
+            f2_split(e < 2 ? wa[2 * (e & 1) + 1] : wb[2 * (e & 1) + 1], x1, y1);
+            const uint64_t wx = f2(x0, x1), wy = f2(y0, y1);
+            A[e] = mul_f2(A[e], wx);
+            C[e] = mul_f2(C[e], wx);
+            B[e] = mul_f2(B[e], wy);
+            D[e] = mul_f2(D[e], wy);
+          }
+        }
+      }
+      was_query = query;
+    }
+    load();
+    copies_wait<kDepth - 1>();
+    const int heads = query ? a.hq : a.hkv, head0 = (now.step - (query ? 0 : q_steps)) * (2 * kHeadsAbreast) + p.slot;
+    const uint32_t from = ring + take;
+    take = take + 2048u == kDepth * 2048u ? 0u : take + 2048u;
+    uint16_t* y = nullptr;
+    if (!CACHE || query) y = (query ? a.Yq + now.token * a.ld_yq : a.Yk + now.token * a.ld_yk) + head0 * 128;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int head = head0 + half * kHeadsAbreast;
+      if (half == 1 && head - p.slot >= heads) break;  // (the same in the whole warp)
+      uint64_t va[4], vb[4];
+      unpack8(ld_shared_v4(from + half * 1024u), va);
+      unpack8(ld_shared_v4(from + half * 1024u + 512u), vb);
+      if (!value) {
+        float rstd = 1.0f;
+        if (NORM) {
+          float small;
+          rstd = head_rstd(va, vb, a.eps, small);
+        }
+        if (p.turns) {
+          turn_pairs<HALF>(va, vb, A, B, C, D);
+        } else if (NORM) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            va[e] = mul_f2(va[e], A[e]);
+            vb[e] = mul_f2(vb[e], D[e]);
+          }
+        }
+        if (NORM) {
+          const uint64_t r = f2(rstd, rstd);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            va[e] = mul_f2(va[e], r);
+            vb[e] = mul_f2(vb[e], r);
+          }
+        }
+      }
       if (CACHE && !query) {
         uint2 qa, qb;
         const int e = quantise(va, vb, qa, qb);
-        if (write && head < a.hkv) {
-          uint8_t* codes = (value ? a.v8 : a.k8) + (static_cast<int64_t>(row) * a.hkv + head) * 128;
+        if (to_row >= 0 && head < heads) {
+          uint8_t* codes = (value ? a.v8 : a.k8) + (static_cast<int64_t>(to_row) * a.hkv + head) * 128;
           reinterpret_cast<uint2*>(codes)[p.ca] = qa;
           reinterpret_cast<uint2*>(codes)[p.cb] = qb;
-          if (p.j == 0) (value ? a.v_exp : a.k_exp)[head * a.ld_exp + row] = static_cast<uint8_t>(e + 127);
+          if (p.j == 0) (value ? a.v_exp : a.k_exp)[head * a.ld_exp + to_row] = static_cast<uint8_t>(e + 127);
         }
-      } else if (head < (query ? a.hq : a.hkv)) {
-        uint16_t* y = (query ? a.Yq + token * a.ld_yq : a.Yk + token * a.ld_yk) + head * 128;
-        reinterpret_cast<uint4*>(y)[p.ca] = pack8(va);
-        reinterpret_cast<uint4*>(y)[p.cb] = pack8(vb);
+      } else if (head < heads) {
+        uint4* to = reinterpret_cast<uint4*>(y + half * (kHeadsAbreast * 128));
+        to[p.ca] = pack8(va);
+        to[p.cb] = pack8(vb);
       }
-    };
-    for (int group = part; group < groups; group += 2 * split) {
-      step(group, xa, xb);
-      if (group + split < groups) step(group + split, ya, yb);
     }
+    begins = now.next(steps, split, stride, units);
   }
+  copies_wait<0>();
 }
 
 // ---- backward with norm.  With u = amplitude R^T gy, n = x rstd: gx = rstd (u w - n mean(u w n)), gw = sum of u n over tokens
-// and heads.  Each lane adds up its values' gw in registers over all its heads; a block leaves 256 sums (queries', keys').
+// and heads.  Each lane adds up its values' gw in registers over all its heads; a block leaves the 128 sums of its kind.
 template <bool HALF>
-__global__ void __launch_bounds__(kThreads) rotary_bwd_kernel(const RotaryBwdArgs a, float* part, const int split) {
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) rotary_bwd_kernel(const RotaryBwdArgs a, float* part, const RotaryShares shares) {
+  extern __shared__ __align__(16) uint8_t ring_all[];  // of each warp, kBwdDepth steps of 4096 bytes
   __shared__ unsigned long long turns[64];
-  __shared__ float2 angles[kWarps][64];
-  __shared__ float sums[kWarps][256];
+  __shared__ __align__(16) float cosines[kWarps][64], sines[kWarps][64];
+  __shared__ float sums[kWarps][128];
   pdl_launch();
   pdl_wait();
   if (static_cast<int>(threadIdx.x) < (a.rot >> 1)) turns[threadIdx.x] = turn_fraction(a.frequencies[threadIdx.x]);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kind = static_cast<int>(blockIdx.x) >= shares.blocks[0];  // 0 queries, 1 keys
+  const int place = static_cast<int>(blockIdx.x) - (kind ? shares.blocks[0] : 0), split = shares.split[kind];
   const Place p = place_of(lane, a.rot);
-  const int gq = (a.hq + kHeadsAbreast - 1) / kHeadsAbreast, groups = gq + (a.hkv + kHeadsAbreast - 1) / kHeadsAbreast;
-  float acc[2][16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) acc[0][e] = acc[1][e] = 0.0f;
-  const int64_t units = a.tokens * split, stride = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < units; unit += stride) {
-    const int64_t token = split == 1 ? unit : unit / split;
-    const int first = static_cast<int>(unit - token * split);
-    auto load = [&](int group, uint4 (&x)[4]) {
-      const bool query = group < gq;
-      const int head = (group - (query ? 0 : gq)) * kHeadsAbreast + p.slot;
-      if (group < groups && head < (query ? a.hq : a.hkv)) {
-        const uint4* g = reinterpret_cast<const uint4*>((query ? a.gYq + token * a.ld_gyq : a.gYk + token * a.ld_gyk) + head * 128);
-        const uint4* v = reinterpret_cast<const uint4*>((query ? a.Q + token * a.ld_q : a.K + token * a.ld_k) + head * 128);
-        x[0] = __ldcs(g + p.ca);
-        x[1] = __ldcs(g + p.cb);
-        x[2] = __ldcs(v + p.ca);
-        x[3] = __ldcs(v + p.cb);
-      } else {
-        x[0] = x[1] = x[2] = x[3] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    uint4 x0[4], x1[4];
-    load(first, x0);
-    load(first + split, x1);
-    float c[8], s[8];
-    if (a.rot > 0) token_angles<HALF>(angles[warp], turns, a.positions[token], a.rot, a.amplitude, lane, p, c, s);
-    auto step = [&](int group, uint4 (&now)[4]) {
-      const bool query = group < gq;
-      const uint16_t* weight = query ? a.wq : a.wk;
-      float ua[8], ub[8], xa[8], xb[8], wa[8], wb[8];
-      unpack8(now[0], ua);
-      unpack8(now[1], ub);
-      unpack8(now[2], xa);
-      unpack8(now[3], xb);
-      load(group + 2 * split, now);
-      unpack8(reinterpret_cast<const uint4*>(weight)[p.ca], wa);
-      unpack8(reinterpret_cast<const uint4*>(weight)[p.cb], wb);
-      if (p.turns) rotate<HALF>(ua, ub, c, s, -1.0f);
-      float small = 1.0f, ss = head_sum(squares(xa, xb));
-      if (__any_sync(0xFFFFFFFFu, !(ss < INFINITY))) {  // as in normalise
-        small = ss < INFINITY ? 1.0f : kSmaller;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xa[e] *= small;
-          xb[e] *= small;
-        }
-        ss = head_sum(squares(xa, xb));
-      }
-      const float rstd = rsqrtf(fmaf(ss, kInvD, a.eps * small * small));
-      float dot = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        xa[e] *= rstd;
-        xb[e] *= rstd;
-        if (query) {
-          acc[0][e] = fmaf(ua[e], xa[e], acc[0][e]);
-          acc[0][8 + e] = fmaf(ub[e], xb[e], acc[0][8 + e]);
-        } else {
-          acc[1][e] = fmaf(ua[e], xa[e], acc[1][e]);
-          acc[1][8 + e] = fmaf(ub[e], xb[e], acc[1][8 + e]);
-        }
-        ua[e] *= wa[e];
-        ub[e] *= wb[e];
-        dot = fmaf(ua[e], xa[e], dot);
-        dot = fmaf(ub[e], xb[e], dot);
-      }
-      const float m = head_sum(dot) * kInvD, r = rstd * small;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ua[e] = r * fmaf(-xa[e], m, ua[e]);
-        ub[e] = r * fmaf(-xb[e], m, ub[e]);
-      }
-      const int head = (group - (query ? 0 : gq)) * kHeadsAbreast + p.slot;
-      if (head < (query ? a.hq : a.hkv)) {
-        uint16_t* y = (query ? a.gQ + token * a.ld_gq : a.gK + token * a.ld_gk) + head * 128;
-        reinterpret_cast<uint4*>(y)[p.ca] = pack8(ua);
-        reinterpret_cast<uint4*>(y)[p.cb] = pack8(ub);
-      }
-    };
-    for (int group = first; group < groups; group += 2 * split) {
-      step(group, x0);
-      if (group + split < groups) step(group + split, x1);
-    }
+  const int heads = kind == 0 ? a.hq : a.hkv, steps = steps_of(heads);
+  const uint16_t* const gy = (kind == 0 ? a.gYq : a.gYk) + p.slot * 128;
+  const uint16_t* const x = (kind == 0 ? a.Q : a.K) + p.slot * 128;
+  uint16_t* const gx = (kind == 0 ? a.gQ : a.gK) + p.slot * 128;
+  const int64_t ld_gy = kind == 0 ? a.ld_gyq : a.ld_gyk, ld_x = kind == 0 ? a.ld_q : a.ld_k, ld_gx = kind == 0 ? a.ld_gq : a.ld_gk;
+  uint64_t wa[4], wb[4], acc[8];
+  {
+    const uint4* w = reinterpret_cast<const uint4*>(kind == 0 ? a.wq : a.wk);
+    unpack8(w[p.ca], wa);
+    unpack8(w[p.cb], wb);
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0;
+  const int64_t units = a.tokens * split, stride = static_cast<int64_t>(shares.blocks[kind]) * kWarps;
+  Walk now, ahead;
+  now.enter(static_cast<int64_t>(place) * kWarps + warp, units, split);
+  ahead = now;
+  const uint32_t ring = smem_u32(ring_all) + warp * (kBwdDepth * 4096u) + lane * 16u;
+  uint32_t fill = 0, take = 0;
+  auto load = [&] {
+    if (ahead.unit < units) {
+      const int head = ahead.step * (2 * kHeadsAbreast) + p.slot, left = heads - head;
+      const int64_t in = left > 0 ? ahead.step * (2 * kHeadsAbreast * 128) : 0;
+      const uint4* g = reinterpret_cast<const uint4*>(gy + ahead.token * ld_gy + in);
+      const uint4* v = reinterpret_cast<const uint4*>(x + ahead.token * ld_x + in);
+      const uint32_t to = ring + fill;
+      copy16(to, g + p.ca, left > 0);
+      copy16(to + 512u, g + p.cb, left > 0);
+      copy16(to + 1024u, v + p.ca, left > 0);
+      copy16(to + 1536u, v + p.cb, left > 0);
+      if (left > kHeadsAbreast) {
+        copy16(to + 2048u, g + kHeadsAbreast * 16 + p.ca, true);
+        copy16(to + 2560u, g + kHeadsAbreast * 16 + p.cb, true);
+        copy16(to + 3072u, v + kHeadsAbreast * 16 + p.ca, true);
+        copy16(to + 3584u, v + kHeadsAbreast * 16 + p.cb, true);
+      } else if (heads - (head - p.slot) > kHeadsAbreast) {  // others of the warp have a head there: zeros for the sums
+        st_shared_v4(to + 2048u, 0u, 0u, 0u, 0u);
+        st_shared_v4(to + 2560u, 0u, 0u, 0u, 0u);
+        st_shared_v4(to + 3072u, 0u, 0u, 0u, 0u);
+        st_shared_v4(to + 3584u, 0u, 0u, 0u, 0u);
+      }
+      ahead.next(steps, split, stride, units);
+    }
+    copies_commit();
+    fill = fill + 4096u == kBwdDepth * 4096u ? 0u : fill + 4096u;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kBwdDepth - 1; ++i) load();
+  int position = 0;
+  auto look = [&](int64_t unit) {
+    if (a.rot > 0 && unit < units) position = a.positions[split == 1 ? unit : divide(unit, split)];
+  };
+  look(now.unit);
+  bool begins = true;
+  uint64_t c[4], s[4];
+  while (now.unit < units) {
+    if (begins) {
+      if (a.rot > 0) {
+        token_angles(cosines[warp], sines[warp], turns, position, a.rot, a.amplitude, -1.0f, lane);
+        if (p.turns) {
+          own_pairs<HALF>(cosines[warp], p, c);
+          own_pairs<HALF>(sines[warp], p, s);
+        }
+      }
+      look(now.unit + stride);
+    }
+    load();
+    copies_wait<kBwdDepth - 1>();
+    const uint32_t from = ring + take;
+    take = take + 4096u == kBwdDepth * 4096u ? 0u : take + 4096u;
+    const int head0 = now.step * (2 * kHeadsAbreast) + p.slot;
+    uint16_t* const y = gx + now.token * ld_gx + now.step * (2 * kHeadsAbreast * 128);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int head = head0 + half * kHeadsAbreast;
+      if (half == 1 && head - p.slot >= heads) break;  // (the same in the whole warp)
+      uint64_t ua[4], ub[4], xa[4], xb[4];
+      unpack8(ld_shared_v4(from + half * 2048u), ua);
+      unpack8(ld_shared_v4(from + half * 2048u + 512u), ub);
+      unpack8(ld_shared_v4(from + half * 2048u + 1024u), xa);
+      unpack8(ld_shared_v4(from + half * 2048u + 1536u), xb);
+      if (p.turns) rotate<HALF>(ua, ub, c, s);
+      float small;
+      const float rstd = head_rstd(xa, xb, a.eps, small);
+      const uint64_t r = f2(rstd, rstd);
+      uint64_t dot = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        xa[e] = mul_f2(xa[e], r);
+        xb[e] = mul_f2(xb[e], r);
+        acc[e] = fma_f2(ua[e], xa[e], acc[e]);
+        acc[4 + e] = fma_f2(ub[e], xb[e], acc[4 + e]);
+        ua[e] = mul_f2(ua[e], wa[e]);
+        ub[e] = mul_f2(ub[e], wb[e]);
+        dot = fma_f2(ua[e], xa[e], dot);
+        dot = fma_f2(ub[e], xb[e], dot);
+      }
+      const float m = -head_sum(sum2(dot)) * kInvD, f = rstd * small;
+      const uint64_t mm = f2(m, m), ff = f2(f, f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ua[e] = mul_f2(ff, fma_f2(xa[e], mm, ua[e]));
+        ub[e] = mul_f2(ff, fma_f2(xb[e], mm, ub[e]));
+      }
+      if (head < heads) {
+        uint4* to = reinterpret_cast<uint4*>(y + half * (kHeadsAbreast * 128));
+        to[p.ca] = pack8(ua);
+        to[p.cb] = pack8(ub);
+      }
+    }
+    begins = now.next(steps, split, stride, units);
+  }
+  copies_wait<0>();
   // over the warp's four heads, then the block's warps in order
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int e = 0; e < 8; ++e) {
+    float v[2];
+    f2_split(acc[e], v[0], v[1]);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      float v = acc[k][e];
-      v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
-      v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
-      if (p.slot == 0) sums[warp][128 * k + 8 * (e < 8 ? p.ca : p.cb) + (e & 7)] = v;
+    for (int i = 0; i < 2; ++i) {
+      v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 8);
+      v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], 16);
+      if (p.slot == 0) sums[warp][8 * (e < 4 ? p.ca : p.cb) + 2 * (e & 3) + i] = v[i];
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 256; i += kThreads) {
-    float v = sums[0][i];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) v += sums[w][i];
-    part[static_cast<int64_t>(blockIdx.x) * 256 + i] = v;
   }
+  __syncthreads();
+  float v = sums[0][threadIdx.x];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) v += sums[w][threadIdx.x];
+  part[static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x] = v;
 }
 
-// The blocks' sums, added up in order by 8 rows of threads and then across them; one block for 32 columns.
-__global__ void __launch_bounds__(256) rotary_sums_kernel(const RotaryBwdArgs a, const float* part, const int blocks) {
-  __shared__ float rows[8][32];
+// The blocks' sums of a kind, added up in order by 32 rows of threads and then across them; one block for 32 columns of a kind.
+__global__ void __launch_bounds__(1024) rotary_sums_kernel(const RotaryBwdArgs a, const float* part, const RotaryShares shares) {
+  __shared__ float rows[32][33];
   pdl_launch();
   pdl_wait();
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, kind = blockIdx.x >> 2, first_col = (blockIdx.x & 3) * 32;
+  const int first = kind == 0 ? 0 : shares.blocks[0], last = first + shares.blocks[kind];
   float v = 0.0f;
-#pragma unroll 4
-  for (int b = y; b < blocks; b += 8) v += part[static_cast<int64_t>(b) * 256 + col];
+#pragma unroll 8
+  for (int b = first + y; b < last; b += 32) v += part[static_cast<int64_t>(b) * 128 + first_col + x];
   rows[y][x] = v;
   __syncthreads();
-  if (y != 0) return;
+  v = rows[x][y];  // column y of the block's: its 32 partial sums lie in a warp
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v += rows[i][x];
-  float* to = col < 128 ? a.gwq + col : a.gwk ? a.gwk + (col - 128) : nullptr;
-  if (to) *to = a.accumulate ? *to + v : v;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  float* to = kind == 0 ? a.gwq : a.gwk;
+  if (x == 0 && to) to[first_col + y] = a.accumulate ? to[first_col + y] + v : v;
 }
 
-// ---- cache, read back: a thread takes 16 codes
-__device__ __forceinline__ uint32_t half2_of_e4m3x2(uint32_t two) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(two));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t two, float f) {
+// ---- cache, read back: a warp takes a token, a lane 8 codes of up to kReadAbreast pieces at a time
+__device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint16_t two, float f) {
   float lo, hi;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+  asm("{\n\t.reg .b32 x;\n\t.reg .b16 l, h;\n\tcvt.rn.f16x2.e4m3x2 x, %2;\n\tmov.b32 {l, h}, x;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
       : "=f"(lo), "=f"(hi)
-      : "r"(half2_of_e4m3x2(two)));
+      : "h"(two));
   return pack_bf16x2(lo * f, hi * f);  // (exact)
 }
 __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadArgs a) {
   pdl_launch();
   pdl_wait();
-  const int per = a.hkv * 8;  // pieces of a token in one of K and V
-  const int64_t pieces = a.tokens * per * 2, stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += stride) {
-    const int64_t token = i / (2 * per);
-    int piece = static_cast<int>(i - token * (2 * per));
-    const bool value = piece >= per;
-    piece -= value ? per : 0;
-    const int row = a.rows[token];
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    float f = 1.0f;
-    if (row >= 0 && row < a.cache_rows) {
-      w = __ldcs(reinterpret_cast<const uint4*>((value ? a.v8 : a.k8) + static_cast<int64_t>(row) * a.hkv * 128) + piece);
-      f = power_of_two(static_cast<int>((value ? a.v_exp : a.k_exp)[(piece >> 3) * a.ld_exp + row]) - 127);
-    } else if (row >= a.cache_rows) {
-      atomicCAS(&g_rotary_err, 0, kPackedBadLengths);
+  const int lane = threadIdx.x & 31, per = a.hkv * 16;  // pieces of a token in one of K and V
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  int64_t token = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  int row = token < a.tokens ? a.rows[token] : 0;
+  for (; token < a.tokens; token += stride) {
+    const int next = token + stride < a.tokens ? a.rows[token + stride] : 0;
+    const bool there = row >= 0 && row < a.cache_rows;
+    if (row >= a.cache_rows && lane == 0) atomicCAS(&g_rotary_err, 0, kPackedBadLengths);
+    const uint8_t* k8 = a.k8 + static_cast<int64_t>(row) * a.hkv * 128;
+    const uint8_t* v8 = a.v8 + static_cast<int64_t>(row) * a.hkv * 128;
+    for (int first = lane; first < 2 * per; first += 32 * kReadAbreast) {
+      uint2 w[kReadAbreast];
+      int e[kReadAbreast];
+#pragma unroll
+      for (int i = 0; i < kReadAbreast; ++i) {
+        const int at = first + 32 * i, piece = at < per ? at : at - per;
+        w[i] = make_uint2(0u, 0u);
+        e[i] = 127;
+        if (there && at < 2 * per) {
+          w[i] = __ldcs(reinterpret_cast<const uint2*>(at < per ? k8 : v8) + piece);
+          e[i] = (at < per ? a.k_exp : a.v_exp)[(piece >> 4) * a.ld_exp + row];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kReadAbreast; ++i) {
+        const int at = first + 32 * i, piece = at < per ? at : at - per;
+        if (at >= 2 * per) break;
+        const float f = power_of_two(e[i] - 127);
+        reinterpret_cast<uint4*>(at < per ? a.K + token * a.ld_k : a.V + token * a.ld_v)[piece] =
+            make_uint4(bf16x2_of_e4m3x2(static_cast<uint16_t>(w[i].x), f), bf16x2_of_e4m3x2(static_cast<uint16_t>(w[i].x >> 16), f),
+                       bf16x2_of_e4m3x2(static_cast<uint16_t>(w[i].y), f), bf16x2_of_e4m3x2(static_cast<uint16_t>(w[i].y >> 16), f));
+      }
     }
-    uint4* y = reinterpret_cast<uint4*>(value ? a.V + token * a.ld_v : a.K + token * a.ld_k) + 2 * piece;
-    y[0] = make_uint4(bf16x2_of_e4m3x2(w.x, f), bf16x2_of_e4m3x2(w.x >> 16, f), bf16x2_of_e4m3x2(w.y, f), bf16x2_of_e4m3x2(w.y >> 16, f));
-    y[1] = make_uint4(bf16x2_of_e4m3x2(w.z, f), bf16x2_of_e4m3x2(w.z >> 16, f), bf16x2_of_e4m3x2(w.w, f), bf16x2_of_e4m3x2(w.w >> 16, f));
+    row = next;
   }
 }
 
-// Warps that share a token's groups of heads: one, or with few tokens as many as fill the GPU.
-int token_split(int64_t tokens, int groups, int sms) {
-  const int64_t want = (static_cast<int64_t>(sms) * 32 + tokens - 1) / (tokens > 0 ? tokens : 1);
-  return static_cast<int>(want < 1 ? 1 : want > groups ? groups : want);
+// Two kinds of blocks with so many steps a token each: by their steps, at most sms x blocks_of_sm altogether; one warp takes a token's
+// steps, or with few tokens as many as fill the GPU.
+RotaryShares shares_of(int64_t tokens, int steps0, int steps1, int sms, int blocks_of_sm) {
+  const int steps[2] = {steps0, steps1}, most = sms * blocks_of_sm;
+  RotaryShares s = {};
+  int left = most;
+  for (int i = 1; i >= 0; --i) {
+    if (steps[i] == 0 || tokens == 0) continue;
+    const int64_t want = (int64_t(sms) * 16 + tokens - 1) / tokens;
+    s.split[i] = static_cast<int>(want > steps[i] ? steps[i] : want);
+    const int64_t units = (tokens * s.split[i] + kWarps - 1) / kWarps;
+    int share = i == 0 ? left : static_cast<int>((int64_t(most) * steps1 + (steps0 + steps1) / 2) / (steps0 + steps1));
+    if (share < 1) share = 1;
+    if (i == 1 && steps0 > 0 && share >= most) share = most - 1;
+    s.blocks[i] = static_cast<int>(units < share ? units : share);
+    left -= s.blocks[i];
+  }
+  return s;
 }
-int groups_of(int heads) { return (heads + kHeadsAbreast - 1) / kHeadsAbreast; }
+// The opt-in to more than 48 KB of shared memory, once for each kernel and device.
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes) {
+  static std::mutex lock;
+  static std::set<std::pair<const void*, int>> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> hold(lock);
+  const std::pair<const void*, int> key(reinterpret_cast<const void*>(kernel), dev);
+  if (done.count(key)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.insert(key);
+  return e;
+}
 
-constexpr int kFwdBlocks = 8, kBwdBlocks = 4;  // blocks of an SM, at most
+RotaryShares fwd_shares(int64_t tokens, int hq, int hkv, bool values, int sms) {
+  return shares_of(tokens, steps_of(hq) + steps_of(hkv), values ? steps_of(hkv) : 0, sms, values ? kWriteBlocks : kFwdBlocks);
+}
+RotaryShares bwd_shares(int64_t tokens, int hq, int hkv, int sms) {
+  return shares_of(tokens, steps_of(hq), steps_of(hkv), sms, kBwdBlocks);
+}
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, int sms, cudaStream_t st) {
   const bool cache = a.rows != nullptr, norm = a.wq != nullptr || a.wk != nullptr, half = a.layout == 0;
-  const int split = token_split(a.tokens, groups_of(a.hq) + (cache ? 2 : 1) * groups_of(a.hkv), sms);
-  const int64_t blocks = (a.tokens * split + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * kFwdBlocks;
-  const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
-  auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kThreads), 0, 1, st, a, split); };
+  const RotaryShares s = fwd_shares(a.tokens, a.hq, a.hkv, cache, sms);
+  const dim3 grid(static_cast<unsigned>(s.blocks[0] + s.blocks[1]));
+  auto go = [&](auto kernel) {
+    const int bytes = kWarps * 2048 * (cache ? kWriteDepth : kFwdDepth);
+    const cudaError_t e = allow_smem(kernel, bytes);
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kThreads), size_t(bytes), 1, st, a, s);
+  };
   if (cache)
     return norm ? (half ? go(rotary_kernel<true, true, true>) : go(rotary_kernel<true, false, true>))
                 : (half ? go(rotary_kernel<false, true, true>) : go(rotary_kernel<false, false, true>));
@@ -477,25 +745,28 @@ cudaError_t launch_rotary(const RotaryArgs& a, int sms, cudaStream_t st) {
 }
 
 int rotary_bwd_blocks(int64_t tokens, int hq, int hkv, int sms) {
-  const int split = token_split(tokens, groups_of(hq) + groups_of(hkv), sms);
-  const int64_t blocks = (tokens * split + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * kBwdBlocks;
-  return static_cast<int>(blocks < most ? blocks : most);
+  const RotaryShares s = bwd_shares(tokens, hq, hkv, sms);
+  return s.blocks[0] + s.blocks[1];
 }
 
 cudaError_t launch_rotary_bwd(const RotaryBwdArgs& a, float* part, int sms, cudaStream_t st) {
-  const int split = token_split(a.tokens, groups_of(a.hq) + groups_of(a.hkv), sms);
-  const dim3 grid(static_cast<unsigned>(rotary_bwd_blocks(a.tokens, a.hq, a.hkv, sms)));
-  return a.layout == 0 ? launch_pdl(rotary_bwd_kernel<true>, grid, dim3(kThreads), 0, 1, st, a, part, split)
-                       : launch_pdl(rotary_bwd_kernel<false>, grid, dim3(kThreads), 0, 1, st, a, part, split);
+  const RotaryShares s = bwd_shares(a.tokens, a.hq, a.hkv, sms);
+  const dim3 grid(static_cast<unsigned>(s.blocks[0] + s.blocks[1]));
+  auto go = [&](auto kernel) {
+    const int bytes = kWarps * 4096 * kBwdDepth;
+    const cudaError_t e = allow_smem(kernel, bytes);
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kThreads), size_t(bytes), 1, st, a, part, s);
+  };
+  return a.layout == 0 ? go(rotary_bwd_kernel<true>) : go(rotary_bwd_kernel<false>);
 }
 
 cudaError_t launch_rotary_sums(const RotaryBwdArgs& a, const float* part, int sms, cudaStream_t st) {
-  const int blocks = a.tokens > 0 ? rotary_bwd_blocks(a.tokens, a.hq, a.hkv, sms) : 0;
-  return launch_pdl(rotary_sums_kernel, dim3(8), dim3(256), 0, 1, st, a, part, blocks);
+  const RotaryShares s = bwd_shares(a.tokens, a.hq, a.hkv, sms);
+  return launch_pdl(rotary_sums_kernel, dim3(8), dim3(1024), 0, 1, st, a, part, s);
 }
 
 cudaError_t launch_cache_read(const CacheReadArgs& a, int sms, cudaStream_t st) {
-  const int64_t blocks = (a.tokens * a.hkv * 16 + 255) / 256, most = static_cast<int64_t>(sms) * 8;
+  const int64_t blocks = (a.tokens + 7) / 8, most = (int64_t(1) << 31) - 1;
   return launch_pdl(cache_read_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, 1, st, a);
 }
 
