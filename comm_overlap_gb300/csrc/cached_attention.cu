@@ -46,19 +46,20 @@ constexpr int kPart = 132;                         // floats of a partial row: 1
 constexpr int kJoinWarps = 8;
 constexpr uint64_t kDrainNs = 200000000ull;
 
-// For R rows: blocks of an SM, slots of the ring (a tile of K or of V each), columns of TMEM (two buffers of scores, O).
+constexpr int kBlocks = 2;  // of an SM
+
+// For R rows: slots of the ring (a tile of K or of V each), columns of TMEM (two buffers of scores, O).
 template <int R>
 struct Shape {
-  static constexpr int kBlocks = R <= 32 ? 2 : 1;
   static constexpr int kRows = R < 16 ? R : 16, kGroups = R / kRows;  // groups of 128 threads that hold keys, and the rows of each
   static constexpr int kThreads = 64 + 128 * kGroups;                 // warps: 0 loads, 1 issues, from 2 on keys
-  static constexpr uint32_t kSlots = R == 8 ? 6 : R == 16 ? 5 : R == 32 ? 4 : 8;
+  static constexpr uint32_t kSlots = R == 8 ? 6 : R == 16 ? 5 : 4;
   static constexpr uint32_t kCols = 2 * R;
-  static constexpr uint32_t kTmem = R == 8 ? 64 : R == 16 ? 128 : R == 32 ? 256 : 512;
-  static constexpr uint32_t kOperand = kCols * 128;                                // bytes of Q or P, two buffers each
-  static constexpr uint32_t kCtrl = 5120;                                          // control block
+  static constexpr uint32_t kTmem = R == 8 ? 64 : R == 16 ? 128 : 256;
+  static constexpr uint32_t kOperand = kCols * 128;  // bytes of Q or P, two buffers each
+  static constexpr uint32_t kCtrl = 4096;            // control block
   static constexpr int kSmem = 1024 + static_cast<int>(kCtrl + kSlots * kTile + 4 * kOperand);
-  static_assert(kBlocks * (kSmem + 1024 + 8 * kThreads + 512) <= 233472 && 3 * kCols <= kTmem && kBlocks * kTmem <= 512, "memory of an SM");
+  static_assert(kBlocks * (kSmem + 1024 + 512) <= 233472 && 3 * kCols <= kTmem && kBlocks * kTmem <= 512, "memory of an SM");
 };
 // Weights are 2^kRaise where t is the maximum that m was taken from; the maximum may rise by kBehind (in base 2) before O and the
 // denominator are brought to a new m, so that they stay below E4M3's 448 = 2^8.807.  (With 6 and 2.8 m moved in nearly every tile of 64
@@ -81,10 +82,18 @@ struct CachedWork {
   float* whole;     // partial rows of items that were not cut, by token and head (with a shared prefix)
 };
 
-// First row and length of a sequence; one whose rows leave the cache gets none and is recorded.
+// The list of work: the rows that all sequences share, where there are some (entry 0, whose rows are all tokens'), then the sequences.
+__device__ __forceinline__ bool is_shared(const CachedArgs& a, int s) { return s < a.shared; }
+__device__ __forceinline__ int rows_of(const CachedArgs& a, int s) { return is_shared(a, s) ? a.shared_rows : a.rows; }
+__device__ __forceinline__ int blocks_of(const CachedArgs& a, int s) { return is_shared(a, s) ? a.shared_blocks : a.blocks; }
+__device__ __forceinline__ int64_t first_token(const CachedArgs& a, int s) {
+  return is_shared(a, s) ? 0 : static_cast<int64_t>(s - a.shared) * a.t;
+}
+
+// First row and length of an entry; one whose rows leave the cache gets none and is recorded.
 __device__ __forceinline__ int sequence(const CachedArgs& a, int s, int& start) {
-  start = a.k_start[s];
-  int len = a.k_len[s];
+  start = is_shared(a, s) ? a.prefix[0] : a.k_start[s - a.shared];
+  int len = is_shared(a, s) ? a.prefix[1] : a.k_len[s - a.shared];
   if (start < 0 || len < 0 || len > a.cache_rows || start > a.cache_rows - len) {
     atomicCAS(&g_cached_err, 0, kPackedBadLengths);
     start = len = 0;
@@ -104,7 +113,7 @@ __device__ __forceinline__ int64_t range_of(int64_t x, const CachedHeader& h) {
   return x < longer ? divide(x, h.each + 1) : h.rest + divide(x - longer, h.each);
 }
 
-// An item's part in a range: keys of tiles t0 .. t1 - 1 of sequence s.
+// An item's part in a range: keys of tiles t0 .. t1 - 1 of entry s.
 struct Piece {
   int s, start, len, tiles;
   int block, head;  // block of rows, first of the key heads abreast
@@ -114,7 +123,7 @@ struct Piece {
 
 // Sets t1; false where there is none (past the range, or, where lengths change while the kernel reads them, past the sequences).
 __device__ __forceinline__ bool close_piece(const CachedArgs& a, Piece& p, int64_t hi) {
-  if (p.at >= hi || p.s >= a.n) return false;
+  if (p.at >= hi || p.s >= a.n + a.shared) return false;
   const int64_t left = hi - p.at;
   p.t1 = p.tiles - p.t0 < left ? p.tiles : p.t0 + static_cast<int>(left);
   return true;
@@ -125,13 +134,13 @@ __device__ __forceinline__ bool next_piece(const CachedArgs& a, Piece& p, int64_
   p.head += a.abreast;
   if (p.head >= a.hkv) {
     p.head = 0;
-    if (++p.block >= a.blocks) {
+    if (++p.block >= blocks_of(a, p.s)) {
       p.block = 0;
       do {
         ++p.s;
-        p.len = p.s < a.n && p.at < hi ? sequence(a, p.s, p.start) : 0;
+        p.len = p.s < a.n + a.shared && p.at < hi ? sequence(a, p.s, p.start) : 0;
         p.tiles = tiles_of(p.len);
-      } while (p.tiles == 0 && p.s < a.n && p.at < hi);
+      } while (p.tiles == 0 && p.s < a.n + a.shared && p.at < hi);
     }
   }
   return close_piece(a, p, hi);
@@ -227,9 +236,9 @@ struct __align__(16) OutRow {
 };
 
 enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_COUNT = 25 };
-// Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces; 1024: rows of two items; 3072:
-// four warps' maxima or sums of 64 rows; 4096: by how much m moved, and the factor for what was added up before
-constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 3072, kMovesAt = 4096;
+// Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces; 1024: rows of two items; 2048: four warps'
+// maxima or sums of 32 rows; 2560: by how much m moved, and the factor for what was added up before
+constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 2048, kMovesAt = 2560;
 static_assert(sizeof(Piece) * 2 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "control block");
 
 // An item's rows (8 x CHUNKS from row r0 of the sequence on) to shared memory, in two terms, 16 threads a row: columns 16 c + n (first
@@ -237,7 +246,7 @@ static_assert(sizeof(Piece) * 2 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "c
 template <int CHUNKS>
 __device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, int head, int r0, uint32_t to, Row* rows, int x) {
   uint4 u[CHUNKS];
-  const int n = x >> 4, piece = x & 15, count = a.t * a.group;
+  const int n = x >> 4, piece = x & 15, count = rows_of(a, s);
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
     const int r = r0 + c * 8 + n;
@@ -245,7 +254,7 @@ __device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, i
     if (r < count) {
       const int token = r / a.group;
       const uint16_t* q =
-          a.Q + (static_cast<int64_t>(s) * a.t + token) * a.ld_q + (static_cast<int64_t>(head) * a.group + r - token * a.group) * 128;
+          a.Q + (first_token(a, s) + token) * a.ld_q + (static_cast<int64_t>(head) * a.group + r - token * a.group) * 128;
       u[c] = reinterpret_cast<const uint4*>(q)[piece];
     }
   }
@@ -269,7 +278,7 @@ __device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, i
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
     if (piece == 0) {
-      const int limit = r >= count ? 0 : a.causal ? len - a.t + r / a.group + 1 : len;
+      const int limit = r >= count ? 0 : is_shared(a, s) ? len : len - a.t + r / a.group + 1;
       rows[c * 8 + n] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, limit, 0};
     }
   }
@@ -295,7 +304,7 @@ __device__ __forceinline__ float row_sums(float (&v)[ROWS], int lane) {
 }
 
 template <int R>
-__global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
+__global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     cached_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                             const __grid_constant__ CachedArgs a, const CachedWork w) {
   using S = Shape<R>;
@@ -303,7 +312,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
   constexpr int kThreads = S::kThreads, kRows = S::kRows, kChunks = kRows / 8;  // rows and chunks of 8 of a group
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
-  __shared__ int64_t before[kThreads + 1];  // tiles of one item before each thread's sequences
   __shared__ int64_t warp_sums[kThreads / 32];
   const uint32_t bar0 = smem_u32(smem), ring = bar0 + S::kCtrl, q_at = ring + kSlots * kTile, p_at = q_at + 2 * S::kOperand;
   auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
@@ -328,12 +336,14 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
   pdl_launch();
   pdl_wait();
 
-  // ---- the plan, by every block for itself: tiles before each thread's sequences
-  const int per = (a.n + kThreads - 1) / kThreads, s0 = min(static_cast<int>(threadIdx.x) * per, a.n), s1 = min(s0 + per, a.n);
+  // ---- the plan, by every block for itself: tiles (times blocks of rows) before each thread's entries
+  const int entries = a.n + a.shared, subs = a.hkv / a.abreast;
+  const int per = (entries + kThreads - 1) / kThreads, s0 = min(static_cast<int>(threadIdx.x) * per, entries), s1 = min(s0 + per, entries);
   int64_t mine = 0;
+  int start0 = 0, len0 = 0;  // of the thread's last entry
   for (int s = s0; s < s1; ++s) {
-    int start;
-    mine += tiles_of(sequence(a, s, start));
+    len0 = sequence(a, s, start0);
+    mine += static_cast<int64_t>(tiles_of(len0)) * blocks_of(a, s);
   }
   int64_t sum = mine;
 #pragma unroll
@@ -342,81 +352,65 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
     if (lane >= o) sum += v;
   }
   if (lane == 31) warp_sums[warp] = sum;
+  if (threadIdx.x == 0) pieces[0] = Piece{};
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   int64_t total = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) {
     if (i == warp) sum += total;
     total += warp_sums[i];
   }
-  before[threadIdx.x] = sum - mine;
-  if (threadIdx.x == 0) before[kThreads] = total;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int64_t items = static_cast<int64_t>(a.blocks) * (a.hkv / a.abreast);  // of a sequence
   CachedHeader h;
-  h.tiles = total * items;
+  h.tiles = total * subs;
   {
     const int most = static_cast<int>(gridDim.x) / a.abreast;
     h.ranges = h.tiles < most ? (h.tiles > 0 ? static_cast<int>(h.tiles) : 1) : most;
     h.each = divide(h.tiles, h.ranges);
     h.rest = static_cast<int>(h.tiles - h.each * h.ranges);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) *w.head = h;
-  if (threadIdx.x % gridDim.x == blockIdx.x) {  // for the second kernel
-    int64_t at = (sum - mine) * items;
-    for (int s = s0; s < s1; ++s) {
-      int start;
-      w.base[s] = at;
-      at += static_cast<int64_t>(tiles_of(sequence(a, s, start))) * items;
-    }
-  }
   const int lane_head = blockIdx.x % a.abreast;  // of the heads abreast
   const int64_t range = blockIdx.x / a.abreast;
   const bool work = h.tiles > 0 && range < h.ranges;
   const int64_t lo = work ? range_begin(range, h) : 0, hi = work ? range_begin(range + 1, h) : 0;
-  if (work && warp == 2) {  // the range's first piece: the thread whose sequences hold tile lo, then the sequence, 32 at a time
-    int x = 0;
-    for (int step = 512; step > 0; step >>= 1)
-      if (x + step < kThreads && before[x + step] * items <= lo) x += step;
-    int64_t done = before[x] * items;
-    Piece p = {};
+  // the range's first piece: tile lo is tile lo - done of entry p.s
+  auto enter = [&](Piece p, int64_t done) {
+    const int item = static_cast<int>(divide(lo - done, p.tiles));
     p.at = lo;
-    p.s = min(x * per, a.n);
-    for (; p.s < a.n; p.s += 32) {
-      int start = 0;
-      const int len = p.s + lane < a.n ? sequence(a, p.s + lane, start) : 0;
-      int64_t upto = tiles_of(len);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-        if (lane >= o) upto += v;
-      }
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, done + upto * items > lo);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        p.len = __shfl_sync(0xFFFFFFFFu, len, l);
-        p.start = __shfl_sync(0xFFFFFFFFu, start, l);
-        p.tiles = tiles_of(p.len);
-        done += (__shfl_sync(0xFFFFFFFFu, upto, l) - p.tiles) * items;
-        p.s += l;
-        break;
-      }
-      done += __shfl_sync(0xFFFFFFFFu, upto, 31) * items;
+    p.block = item / subs;
+    p.head = (item - p.block * subs) * a.abreast;
+    p.t0 = static_cast<int>((lo - done) - static_cast<int64_t>(item) * p.tiles);
+    if (close_piece(a, p, hi)) pieces[0] = p;
+  };
+  const int64_t mine_at = (sum - mine) * subs;
+  if (work && mine_at <= lo && lo < mine_at + mine * subs) {
+    // one thread has it; with several entries a thread it passes over those before
+    Piece p = {};
+    p.s = s0;
+    int64_t done = mine_at;
+    p.start = start0;
+    p.len = len0;
+    for (;; ++p.s) {
+      if (per > 1) p.len = p.s < s1 ? sequence(a, p.s, p.start) : 0;
+      p.tiles = tiles_of(p.len);
+      const int64_t all = static_cast<int64_t>(p.tiles) * blocks_of(a, p.s) * subs;
+      if (lo < done + all || p.s >= s1) break;
+      done += all;
     }
-    if (p.tiles > 0) {
-      const int item = static_cast<int>(divide(lo - done, p.tiles)), subs = a.hkv / a.abreast;
-      p.block = item / subs;
-      p.head = (item - p.block * subs) * a.abreast;
-      p.t0 = static_cast<int>((lo - done) - static_cast<int64_t>(item) * p.tiles);
+    if (p.tiles > 0) enter(p, done);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *w.head = h;
+  if (threadIdx.x % gridDim.x == blockIdx.x) {  // for the second kernel
+    int64_t at = mine_at;
+    for (int s = s0; s < s1; ++s) {
+      int start;
+      w.base[s] = at;
+      at += static_cast<int64_t>(tiles_of(sequence(a, s, start))) * blocks_of(a, s) * subs;
     }
-    if (!close_piece(a, p, hi)) p.t1 = p.t0;  // (only where lengths change meanwhile)
-    if (lane == 0) pieces[0] = p;
   }
   __syncthreads();
-  const int rows_of_sequence = a.t * a.group;
 
   if (work && warp == 0) {
     // ---------------- loads: K and V of one tile after the other
@@ -471,7 +465,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
       if (tile == p.t0) wait(B_Q_FULL + (item & 1u), item >> 1, 2);
       wait(B_FULL + slot_k, round_k, 3);
       columns_before = columns;
-      columns = 16u * static_cast<uint32_t>((min(R, rows_of_sequence - p.block * R) + 7) >> 3);
+      columns = 16u * static_cast<uint32_t>((min(R, rows_of(a, p.s) - p.block * R) + 7) >> 3);
       tc_fence_after();
       if (ok && one) {
         const uint32_t id = idesc_e4m3_f32(128, static_cast<int>(columns), false, false);
@@ -557,8 +551,8 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
     group_sync(group);                        // the rows are there
     for (uint32_t item = 0; more; ++item) {
       Row* rows = all_rows + (item & 1u) * R + group * kRows;
-      const int count = min(kRows, rows_of_sequence - p.block * R - group * kRows), chunks = (count + 7) >> 3;  // (none: below 0)
-      const int least = a.causal ? p.len - a.t + p.block * R / a.group + 1 : p.len;  // keys that every row sees
+      const int count = min(kRows, rows_of(a, p.s) - p.block * R - group * kRows), chunks = (count + 7) >> 3;  // (none: below 0)
+      const int least = is_shared(a, p.s) ? p.len : p.len - a.t + p.block * R / a.group + 1;  // keys that every row sees
       int nan_key = INT_MAX;  // the first key, of those that not all rows see, with NaN in this thread's element
       float l[kRows];
 #pragma unroll
@@ -746,24 +740,24 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, Shape<R>::kBlocks)
         if ((lane & (32 / kRows - 1)) == 0) sums[(warp & 3) * kRows + lane / (32 / kRows)] = sum;
       }
       group_sync(group);
-      const bool all = p.t0 == 0 && p.t1 == p.tiles, out = all && !a.partial;
+      const bool all = p.t0 == 0 && p.t1 == p.tiles, out = all && a.shared == 0;
       if (x < count) {
         const float den = (sums[x] + sums[kRows + x]) + (sums[2 * kRows + x] + sums[3 * kRows + x]);
         const Row row = rows[x];
         const float m = row.begun ? row.base : -INFINITY;
         const int in = group * kRows + x, r = p.block * R + in, token = r / a.group;
-        const int64_t place = (static_cast<int64_t>(p.s) * a.t + token) * a.hq + (p.head + lane_head) * a.group + r - token * a.group;
+        const int64_t row_at = first_token(a, p.s) + token, place = row_at * a.hq + (p.head + lane_head) * a.group + r - token * a.group;
         OutRow to;
         to.limit = row.limit;
         to.factor = 1.0f;
         if (out) {
           const bool some = den > 0.0f || den != den;
           to.factor = some ? 1.0f / den : 0.0f;
-          to.at = (static_cast<int64_t>(p.s) * a.t + token) * a.ld_o + (static_cast<int64_t>(p.head + lane_head) * a.group + r - token * a.group) * 128;
+          to.at = row_at * a.ld_o + (static_cast<int64_t>(p.head + lane_head) * a.group + r - token * a.group) * 128;
           if (a.lse && ok) a.lse[place] = some ? (m + log2f(den)) * 0.69314718055994531f : -INFINITY;
         } else {
           const int64_t slot = (2 * range + (p.at - p.t0 > lo ? 1 : 0)) * a.abreast + lane_head;  // (the item begins within the range)
-          to.at = all ? place * kPart : (slot * R + in) * kPart;
+          to.at = all ? (place + (is_shared(a, p.s) ? a.whole_rows : 0)) * kPart : (slot * R + in) * kPart;
           if (ok) *reinterpret_cast<float2*>((all ? w.whole : w.slots) + to.at + 128) = make_float2(m, den);
         }
         *reinterpret_cast<OutRow*>(rows + x) = to;
@@ -819,7 +813,7 @@ struct Joined {
   }
 };
 
-// Parts of row r (of the sequence's rows) of key head `head` under one plan, every `warps`-th of them; true if one covers all keys.
+// Parts of row r of entry s for key head `head`, every `warps`-th of them; true if one covers all keys.
 __device__ __forceinline__ bool join_parts(const CachedArgs& a, const CachedWork& w, int s, int head, int r, const float* whole, int lane,
                                            int warp, int warps, Joined& j) {
   int start;
@@ -831,7 +825,7 @@ __device__ __forceinline__ bool join_parts(const CachedArgs& a, const CachedWork
   const int64_t begin = base + static_cast<int64_t>(block * (a.hkv / a.abreast) + sub) * tiles;
   const int64_t first = range_of(begin, h), last = range_of(begin + tiles - 1, h);
   if (first == last) {
-    if (a.partial && warp == 0) j.add(whole, lane);
+    if (a.shared && warp == 0) j.add(whole, lane);
     return true;
   }
   const int64_t slot = static_cast<int64_t>(rows) * kPart;
@@ -843,8 +837,7 @@ __device__ __forceinline__ bool join_parts(const CachedArgs& a, const CachedWork
 }
 
 // A block for each row, of `warps` warps that share its parts.
-__global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const CachedArgs a, const CachedWork w, const CachedArgs pa,
-                                                               const CachedWork pw) {
+__global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const CachedArgs a, const CachedWork w) {
   __shared__ __align__(16) float parts[kJoinWarps][kPart];
   pdl_launch();
   pdl_wait();
@@ -854,8 +847,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const Cach
   const int qh = static_cast<int>(i - token * a.hq), head = qh / a.group, in_group = qh - head * a.group;
   const int s = static_cast<int>(token / a.t), t = static_cast<int>(token - static_cast<int64_t>(s) * a.t);
   Joined j;
-  if (a.partial) join_parts(pa, pw, 0, head, static_cast<int>(token) * a.group + in_group, pw.whole + i * kPart, lane, warp, warps, j);
-  if (join_parts(a, w, s, head, t * a.group + in_group, w.whole + i * kPart, lane, warp, warps, j) && !a.partial) return;
+  if (a.shared)
+    join_parts(a, w, 0, head, static_cast<int>(token) * a.group + in_group, w.whole + (a.whole_rows + i) * kPart, lane, warp, warps, j);
+  if (join_parts(a, w, s + a.shared, head, t * a.group + in_group, w.whole + i * kPart, lane, warp, warps, j) && !a.shared) return;
   if (warps > 1) {
     *reinterpret_cast<float4*>(&parts[warp][4 * lane]) = j.o;
     if (lane == 0) *reinterpret_cast<float2*>(&parts[warp][128]) = make_float2(j.m, j.l);
@@ -874,32 +868,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cached_join_kernel(const Cach
 
 __host__ int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
 
-int blocks_of_sm(int rows_of_block) { return rows_of_block <= 32 ? 2 : 1; }
-
 struct Region {
-  int64_t head, base, slots, whole, total;
+  int64_t base, slots, whole, total;
 };
-// of one plan, from `at` on
-Region region(int64_t at, const CachedArgs& a, int64_t whole_rows) {
+Region region(const CachedArgs& a) {
   Region r;
-  r.head = at;
-  r.base = up256(r.head + static_cast<int64_t>(sizeof(CachedHeader)));
-  r.slots = up256(r.base + a.n * int64_t(8));
-  r.whole = up256(r.slots + int64_t(2) * kSms * blocks_of_sm(a.rows_of_block) * a.rows_of_block * kPart * 4);
-  r.total = up256(r.whole + whole_rows * kPart * 4);
+  r.base = up256(static_cast<int64_t>(sizeof(CachedHeader)));
+  r.slots = up256(r.base + (a.n + a.shared) * int64_t(8));
+  r.whole = up256(r.slots + int64_t(2) * kSms * kBlocks * a.rows_of_block * kPart * 4);
+  r.total = up256(r.whole + (a.shared ? 2 * a.whole_rows : 0) * kPart * 4);
   return r;
 }
-CachedWork work_at(void* ws, const Region& r) {
+CachedWork work_at(void* ws, const CachedArgs& a) {
+  const Region r = region(a);
   uint8_t* p = static_cast<uint8_t*>(ws);
   CachedWork w;
-  w.head = reinterpret_cast<CachedHeader*>(p + r.head);
+  w.head = reinterpret_cast<CachedHeader*>(p);
   w.base = reinterpret_cast<int64_t*>(p + r.base);
   w.slots = reinterpret_cast<float*>(p + r.slots);
   w.whole = reinterpret_cast<float*>(p + r.whole);
   return w;
 }
-Region own_region(const CachedArgs& a) { return region(0, a, a.partial ? int64_t(a.n) * a.t * a.hq : 0); }
-Region prefix_region(const CachedArgs& a, const CachedArgs& p) { return region(own_region(a).total, p, int64_t(a.n) * a.t * a.hq); }
 
 template <int R>
 cudaError_t launch_rows(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, const CachedWork& w, int sms, cudaStream_t st) {
@@ -913,46 +902,44 @@ cudaError_t launch_rows(const CUtensorMap& k, const CUtensorMap& v, const Cached
     if (e != cudaSuccess) return e;
     ready_of[dev].store(true, std::memory_order_release);
   }
-  const dim3 grid(static_cast<unsigned>((sms < kSms ? sms : kSms) * Shape<R>::kBlocks));
+  const dim3 grid(static_cast<unsigned>((sms < kSms ? sms : kSms) * kBlocks));
   return launch_pdl(cached_attention_kernel<R>, grid, dim3(Shape<R>::kThreads), Shape<R>::kSmem, 1, st, k, v, a, w);
 }
 
 }  // namespace
 
 void cached_shape(CachedArgs* a) {
-  const int64_t rows = int64_t(a->t) * a->group;
+  a->rows = a->t * a->group;
+  a->whole_rows = int64_t(a->n) * a->t * a->hq;
+  a->shared_rows = a->shared ? a->n * a->rows : 0;
+  const int most = a->shared ? a->shared_rows : a->rows;
   a->rows_of_block = 8;
-  while (a->rows_of_block < 64 && a->rows_of_block < rows) a->rows_of_block *= 2;
-  a->blocks = static_cast<int32_t>((rows + a->rows_of_block - 1) / a->rows_of_block);
+  while (a->rows_of_block < 32 && a->rows_of_block < most) a->rows_of_block *= 2;
+  auto blocks = [&](int rows) { return static_cast<int32_t>((int64_t(rows) + a->rows_of_block - 1) / a->rows_of_block); };
+  a->blocks = blocks(a->rows);
+  a->shared_blocks = blocks(a->shared_rows);
   a->abreast = kMaxAbreast;
   while (a->hkv % a->abreast != 0) --a->abreast;
 }
 
-int64_t cached_scratch_bytes(const CachedArgs& a, const CachedArgs* prefix) {
-  return prefix ? prefix_region(a, *prefix).total : own_region(a).total;
-}
+int64_t cached_scratch_bytes(const CachedArgs& a) { return region(a).total; }
 
-cudaError_t launch_cached_attention(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, const CachedArgs* of, void* ws,
-                                    int sms, cudaStream_t st) {
-  const CachedWork w = work_at(ws, of ? prefix_region(*of, a) : own_region(a));
+cudaError_t launch_cached_attention(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, void* ws, int sms, cudaStream_t st) {
+  const CachedWork w = work_at(ws, a);
   switch (a.rows_of_block) {
     case 8: return launch_rows<8>(k, v, a, w, sms, st);
     case 16: return launch_rows<16>(k, v, a, w, sms, st);
-    case 32: return launch_rows<32>(k, v, a, w, sms, st);
-    default: return launch_rows<64>(k, v, a, w, sms, st);
+    default: return launch_rows<32>(k, v, a, w, sms, st);
   }
 }
 
-cudaError_t launch_cached_join(const CachedArgs& a, const CachedArgs* prefix, void* ws, cudaStream_t st) {
-  const int64_t rows = int64_t(a.n) * a.t * a.hq;
-  const CachedWork w = work_at(ws, own_region(a)), pw = prefix ? work_at(ws, prefix_region(a, *prefix)) : w;
+cudaError_t launch_cached_join(const CachedArgs& a, void* ws, cudaStream_t st) {
   // warps for a row: with few items each is cut into many parts
-  const CachedArgs& b = prefix ? *prefix : a;
-  const int64_t items = int64_t(b.hkv) * b.n * b.blocks;
+  const int64_t items = int64_t(a.hkv) * (int64_t(a.n) * a.blocks + a.shared_blocks);
   int warps = 1;
-  while (warps < kJoinWarps && items * warps * 4 < kSms * blocks_of_sm(b.rows_of_block)) warps *= 2;
-  return launch_pdl(cached_join_kernel, dim3(static_cast<unsigned>(rows)), dim3(static_cast<unsigned>(32 * warps)), 0, 1, st, a, w,
-                    prefix ? *prefix : a, pw);
+  while (warps < kJoinWarps && items * warps * 4 < kSms * kBlocks) warps *= 2;
+  return launch_pdl(cached_join_kernel, dim3(static_cast<unsigned>(a.whole_rows)), dim3(static_cast<unsigned>(32 * warps)), 0, 1, st, a,
+                    work_at(ws, a));
 }
 
 cudaError_t take_cached_error(int* code) {

@@ -250,22 +250,21 @@ struct CachedArgs {
   uint16_t* O;
   float* lse;              // nullable
   int64_t ld_q, ld_o, ld_exp;
-  int32_t n, t, hq, hkv, group, cache_rows;
-  int32_t causal, partial;               // query i of t sees len - t + i + 1 keys, or all; results stay in the workspace
-  int32_t rows_of_block, blocks;         // cached_shape: rows (tokens x group) of a block, blocks of rows,
+  const int32_t* prefix;                 // nullable: first row and number of the rows that all sequences see
+  int64_t whole_rows;                    // cached_shape, as the next two lines: n x t x hq
+  int32_t rows, rows_of_block, blocks;   // rows (tokens x group) of a sequence and key head, in blocks
+  int32_t shared_rows, shared_blocks;    // those of all sequences together, over the shared rows
   int32_t abreast;                       // neighbouring key heads that blocks take at the same time
+  int32_t n, t, hq, hkv, group, cache_rows, shared;  // query i of t sees k_len - t + i + 1 keys; shared: 1 with a prefix
   float scale_log2;                      // scale x log2(e)
   int32_t err_site;
 };
 // Maps of codes, 128-byte swizzle: (128, hkv, cache_rows) in boxes (128, 1, kCachedKeys).
 constexpr int kCachedKeys = 128;
 void cached_shape(CachedArgs* a);
-// `prefix` (nullable): the arguments of the rows that all sequences share, as one sequence of n x t tokens.
-int64_t cached_scratch_bytes(const CachedArgs& a, const CachedArgs* prefix);
-// `of`: the call's own arguments where `a` is its prefix.
-cudaError_t launch_cached_attention(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, const CachedArgs* of, void* ws,
-                                    int sms, cudaStream_t st);
-cudaError_t launch_cached_join(const CachedArgs& a, const CachedArgs* prefix, void* ws, cudaStream_t st);
+int64_t cached_scratch_bytes(const CachedArgs& a);
+cudaError_t launch_cached_attention(const CUtensorMap& k, const CUtensorMap& v, const CachedArgs& a, void* ws, int sms, cudaStream_t st);
+cudaError_t launch_cached_join(const CachedArgs& a, void* ws, cudaStream_t st);
 cudaError_t take_cached_error(int* code);
 
 }  // namespace dm

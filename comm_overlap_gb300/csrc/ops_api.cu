@@ -217,7 +217,7 @@ domino_status check_cache(const void* k8, const void* v8, const void* k_exp, con
 }
 
 // Sizes of the attention over the 8-bit cache, and the shape of its work.
-domino_status cached_args(int64_t n, int64_t t, int32_t heads, int32_t kv_heads, bool prefix, dm::CachedArgs* a, dm::CachedArgs* p) {
+domino_status cached_args(int64_t n, int64_t t, int32_t heads, int32_t kv_heads, bool prefix, dm::CachedArgs* a) {
   if (n < 0 || t < 0 || heads < 1 || kv_heads < 1)
     return refuse(DOMINO_ERR_INVALID_ARG, "need n, t >= 0, heads >= 1 and kv_heads >= 1");
   if (heads % kv_heads != 0) return refuse(DOMINO_ERR_INVALID_ARG, "heads must be a multiple of kv_heads");
@@ -230,14 +230,8 @@ domino_status cached_args(int64_t n, int64_t t, int32_t heads, int32_t kv_heads,
   a->hq = heads;
   a->hkv = kv_heads;
   a->group = heads / kv_heads;
-  a->causal = 1;
-  a->partial = prefix;
-  *p = *a;
-  p->n = 1;
-  p->t = int32_t(n * t);
-  p->causal = 0;
+  a->shared = prefix;
   dm::cached_shape(a);
-  dm::cached_shape(p);
   return DOMINO_OK;
 }
 
@@ -722,9 +716,9 @@ domino_status domino_attn_cached_workspace_size(int64_t n, int64_t t, int32_t he
                                                 size_t* bytes) {
   return guarded([&]() -> domino_status {
     if (!bytes) return refuse(DOMINO_ERR_INVALID_ARG, "bytes is NULL");
-    dm::CachedArgs a, p;
-    DM_TRY(cached_args(n, t, heads, kv_heads, prefix != 0, &a, &p));
-    *bytes = n == 0 || t == 0 ? 0 : size_t(dm::cached_scratch_bytes(a, prefix != 0 ? &p : nullptr));
+    dm::CachedArgs a;
+    DM_TRY(cached_args(n, t, heads, kv_heads, prefix != 0, &a));
+    *bytes = n == 0 || t == 0 ? 0 : size_t(dm::cached_scratch_bytes(a));
     return DOMINO_OK;
   });
 }
@@ -735,8 +729,8 @@ domino_status domino_attn_cached_fwd(domino_handle H, const uint16_t* Q, int64_t
                                      uint16_t* O, int64_t ld_o, float* lse, int64_t n, int64_t t, int32_t heads,
                                      int32_t kv_heads, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() -> domino_status {
-    dm::CachedArgs a, p;
-    DM_TRY(cached_args(n, t, heads, kv_heads, prefix != nullptr, &a, &p));
+    dm::CachedArgs a;
+    DM_TRY(cached_args(n, t, heads, kv_heads, prefix != nullptr, &a));
     DM_TRY(check_cache(k8, v8, k_exp, v_exp, ld_exp, cache_rows, kv_heads));
     if (!(scale > 0.0f) || !(scale <= 8192.0f)) return refuse(DOMINO_ERR_INVALID_ARG, "scale must be > 0 and at most 8192");
     const int64_t tokens = n * t;
@@ -748,7 +742,7 @@ domino_status domino_attn_cached_fwd(domino_handle H, const uint16_t* Q, int64_t
       DM_TRY(check_list(k_len, "k_len", 4));
       if (prefix) DM_TRY(check_list(prefix, "prefix", 4));
       if (O == Q) return refuse(DOMINO_ERR_INVALID_ARG, "O may not be Q");
-      DM_TRY(check_ws(workspace, workspace_bytes, size_t(dm::cached_scratch_bytes(a, prefix ? &p : nullptr))));
+      DM_TRY(check_ws(workspace, workspace_bytes, size_t(dm::cached_scratch_bytes(a))));
     }
     DM_TRY(dm::check_handle(H));
     if (tokens == 0) return DOMINO_OK;
@@ -762,29 +756,25 @@ domino_status domino_attn_cached_fwd(domino_handle H, const uint16_t* Q, int64_t
       const void* base = cache_rows > 0 ? (i ? static_cast<const void*>(v8) : k8) : Q;
       if (!dm::make_map(i ? &mv : &mk, 1, base, 3, dims, strides, box, &err, 128, 128)) return refuse(DOMINO_ERR_CUDA, err);
     }
-    for (dm::CachedArgs* x : {&a, &p}) {
-      x->Q = Q;
-      x->k_exp = k_exp;
-      x->v_exp = v_exp;
-      x->k_start = x == &a ? k_start : prefix;
-      x->k_len = x == &a ? k_len : prefix + 1;
-      x->O = O;
-      x->lse = lse;
-      x->ld_q = ld_q;
-      x->ld_o = ld_o;
-      x->ld_exp = ld_exp;
-      x->cache_rows = int32_t(cache_rows);
-      x->scale_log2 = scale * 1.4426950408889634f;
-      x->err_site = 0x26 << 4;
-    }
+    a.Q = Q;
+    a.k_exp = k_exp;
+    a.v_exp = v_exp;
+    a.k_start = k_start;
+    a.k_len = k_len;
+    a.prefix = prefix;
+    a.O = O;
+    a.lse = lse;
+    a.ld_q = ld_q;
+    a.ld_o = ld_o;
+    a.ld_exp = ld_exp;
+    a.cache_rows = int32_t(cache_rows);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.err_site = 0x26 << 4;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (prefix)
-      DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_CACHED, st, "cached attention launch (prefix)",
-                           [&] { return dm::launch_cached_attention(mk, mv, p, &a, workspace, op_sms(H), st); }));
     DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_CACHED, st, "cached attention launch",
-                         [&] { return dm::launch_cached_attention(mk, mv, a, nullptr, workspace, op_sms(H), st); }));
+                         [&] { return dm::launch_cached_attention(mk, mv, a, workspace, op_sms(H), st); }));
     return dm::launch_on(H, DOMINO_K_ATTN_CACHED, st, "cached attention join launch",
-                         [&] { return dm::launch_cached_join(a, prefix ? &p : nullptr, workspace, st); });
+                         [&] { return dm::launch_cached_join(a, workspace, st); });
   });
 }
 

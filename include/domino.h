@@ -493,7 +493,7 @@ typedef enum {
   DOMINO_K_ROTARY_BWD = 20, /* domino_qk_rotary_bwd (its two kernels) */
   DOMINO_K_CACHE_WRITE = 21, /* domino_cache_write */
   DOMINO_K_CACHE_READ = 22, /* domino_cache_read */
-  DOMINO_K_ATTN_CACHED = 23, /* domino_attn_cached_fwd (its two or three kernels) */
+  DOMINO_K_ATTN_CACHED = 23, /* domino_attn_cached_fwd (its two kernels) */
   DOMINO_K_COUNT = 24
 } domino_kernel_kind;
 DOMINO_API domino_status domino_timing_enable(domino_handle handle, int32_t enable);
