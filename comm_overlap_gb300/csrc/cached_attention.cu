@@ -235,10 +235,11 @@ struct __align__(16) OutRow {
   int limit;
 };
 
-enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_COUNT = 25 };
+enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_EXPS = 25, B_COUNT = 29 };
 // Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces; 1024: rows of two items; 2048: four warps'
-// maxima or sums of 32 rows; 2560: by how much m moved, and the factor for what was added up before
-constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 2048, kMovesAt = 2560;
+// maxima or sums of 32 rows; 2560: by how much m moved, and the factor for what was added up before; 3072: exponents of four tiles' keys
+constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 2048, kMovesAt = 2560, kExpsAt = 3072;
+constexpr uint32_t kExpTiles = 4;
 static_assert(sizeof(Piece) * 2 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "control block");
 
 // An item's rows (8 x CHUNKS from row r0 of the sequence on) to shared memory, in two terms, 16 threads a row: columns 16 c + n (first
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = &g_cached_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_Q_FULL || i == B_Q_FULL + 1 || i == B_P_FULL || i == B_P_FULL + 1 ? 4 * S::kGroups : 1);
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_Q_FULL || i == B_Q_FULL + 1 || i == B_P_FULL || i == B_P_FULL + 1 ? 4 * S::kGroups : i >= B_EXPS ? 32 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -413,13 +414,25 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
   __syncthreads();
 
   if (work && warp == 0) {
-    // ---------------- loads: K and V of one tile after the other
+    // ---------------- loads: K and V of one tile after the other, and its keys' exponents, which the lanes load (four keys each) and
+    // store a tile later, before anything that may wait.  (Loaded by the threads that use them, a tile ahead, they were waited for:
+    // 64 sequences of up to 8000 keys 101 us.)  Four tiles of them are kept: V of the third tile before is read by then.
     Piece p = pieces[0];
-    uint32_t slot = 0, round = 0;
+    uint32_t slot = 0, round = 0, made = 0;
     const bool one = elect_one();
     bool ok = true, more = p.t1 > p.t0;
+    int exps[4];
+    auto store = [&] {  // those of tile made - 1
+      const uint32_t to = bar0 + kExpsAt + ((made - 1) & (kExpTiles - 1)) * (2u * kKeys) + 2u * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 64u * i), "h"(static_cast<unsigned short>(exps[i])) : "memory");
+      mbar_arrive(bar(B_EXPS + ((made - 1) & (kExpTiles - 1))));
+    };
     while (more && ok) {
+      const int64_t list = (p.head + lane_head) * a.ld_exp + p.start;
       for (int tile = p.t0; tile < p.t1 && ok; ++tile) {
+        if (made > 0) store();
         const int row = p.start + tile * kKeys;
 #pragma unroll
         for (int value = 0; value < 2; ++value) {
@@ -433,9 +446,17 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
             ++round;
           }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int in = tile * kKeys + 32 * i + lane;
+          exps[i] = 127 | 127 << 8;  // (what lies past the keys may be anything)
+          if (in < p.len) exps[i] = load_line(a.k_exp + list + in) | load_line(a.v_exp + list + in) << 8;
+        }
+        ++made;
       }
       more = next_piece(a, p, hi);
     }
+    if (made > 0 && ok) store();
     if (!ok) {  // copies in flight land before the block leaves
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 100000ull) {
@@ -533,20 +554,9 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_Q_FULL + (item & 1u)));
     };
-    auto exponents = [&](const Piece& p, int tile) -> int {
-      const int in = tile * kKeys + me;
-      if (in >= p.len) return 127 | 127 << 8;  // (what lies past the keys may be anything)
-      const int64_t i = (p.head + lane_head) * a.ld_exp + p.start + in;
-      return load_line(a.k_exp + i) | load_line(a.v_exp + i) << 8;
-    };
-
     Piece p = pieces[0], next = p;
     bool more = p.t1 > p.t0, another = false;
-    int exps = 0;
-    if (more) {
-      exps = exponents(p, p.t0);
-      prepare(p, 0);
-    }
+    if (more) prepare(p, 0);
     uint32_t j = 0, slot_v = 1, round_v = 0;  // tiles so far; V's place in the ring
     group_sync(group);                        // the rows are there
     for (uint32_t item = 0; more; ++item) {
@@ -560,12 +570,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
       bool force = true;  // rows without an m
 
       for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
-        const bool first = tile == p.t0, only = p.t1 == p.t0 + 1;
-        int next_exps = 0;
-        if (tile + 1 < p.t1)
-          next_exps = exponents(p, tile + 1);
-        else if (!first && another)
-          next_exps = exponents(next, next.t0);
+        const bool first = tile == p.t0;
         if (first) {  // one thread finds the next item, all take it from shared memory (after they have met below)
           if (threadIdx.x == 64) {
             Piece n = p;
@@ -576,6 +581,10 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         }
         const int key0 = tile * kKeys;
         const bool tail = key0 + kKeys > least;
+        wait(B_EXPS + (j & (kExpTiles - 1)), j / kExpTiles, 11);
+        unsigned short packed;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(packed) : "r"(bar0 + kExpsAt + (j & (kExpTiles - 1)) * (2u * kKeys) + 2u * me) : "memory");
+        const int exps = packed;
         const float key_scale = __int_as_float((exps & 255) << 23), bias = static_cast<float>((exps >> 8) - 127);
         const float unbias = __int_as_float((254 - (exps >> 8)) << 23);
         const uint32_t from = lanes + (j & 1u) * S::kCols;
@@ -726,12 +735,8 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         if (first) {
           next = pieces[(item + 1) & 1u];
           another = next.t1 > next.t0;
-          if (another) {
-            if (only) next_exps = exponents(next, next.t0);
-            prepare(next, item + 1);
-          }
+          if (another) prepare(next, item + 1);
         }
-        exps = next_exps;
       }
 
       // ---- what the piece's keys came to
