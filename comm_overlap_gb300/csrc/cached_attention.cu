@@ -196,6 +196,15 @@ __device__ __forceinline__ bool group_any(int group, bool x) {
   return r != 0;
 }
 
+// mbar_wait with all but its first look out of the way: the loop over tiles is long as it is, and instructions that it passes over cost
+// it their fetching.
+__device__ __noinline__ bool arrival_awaited(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int site) {
+  return mbar_wait(bar, parity, abort_flag, err, site);
+}
+__device__ __forceinline__ bool arrival(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int site) {
+  return mbar_try_wait(bar, parity) || arrival_awaited(bar, parity, abort_flag, err, site);
+}
+
 __device__ __forceinline__ uint16_t e4m3_of_f16(__half2 x) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&x)));
@@ -235,52 +244,58 @@ struct __align__(16) OutRow {
   int limit;
 };
 
-enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_EXPS = 25, B_COUNT = 29 };
-// Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces; 1024: rows of two items; 2048: four warps'
+enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_EXPS = 25,
+             B_Q_EMPTY = 29, B_COUNT = 31 };
+// Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces (two items', the range's first); 1024: rows of two items; 2048: four warps'
 // maxima or sums of 32 rows; 2560: by how much m moved, and the factor for what was added up before; 3072: exponents of four tiles' keys
 constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 2048, kMovesAt = 2560, kExpsAt = 3072;
 constexpr uint32_t kExpTiles = 4;
-static_assert(sizeof(Piece) * 2 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "control block");
+static_assert(sizeof(Piece) * 3 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "control block");
 
-// An item's rows (8 x CHUNKS from row r0 of the sequence on) to shared memory, in two terms, 16 threads a row: columns 16 c + n (first
-// terms) and 16 c + 8 + n (second) of the product's narrow operand, rows of 128 bytes under the 128-byte swizzle.
-template <int CHUNKS>
-__device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, int head, int r0, uint32_t to, Row* rows, int x) {
-  uint4 u[CHUNKS];
-  const int n = x >> 4, piece = x & 15, count = rows_of(a, s);
+// An item's rows to shared memory, in two terms, by warps whose lanes take 16 a row: this one rows first, first + step, ...  Rows 16 c + n
+// (first terms) and 16 c + 8 + n (second) of the product's narrow operand are row 8 c + n of the item, 128 bytes each under the
+// 128-byte swizzle.
+__device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, int head, int r0, uint32_t to, Row* rows, int lane,
+                                          int first, int step) {
+  const int piece = lane & 15, all = rows_of(a, s), top = (min(a.rows_of_block, all - r0) + 7) & ~7;
+#pragma unroll 1
+  for (first += lane >> 4; first < top; first += 4 * step) {
+    uint4 u[4];
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) {
-    const int r = r0 + c * 8 + n;
-    u[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < count) {
-      const int token = r / a.group;
-      const uint16_t* q =
-          a.Q + (first_token(a, s) + token) * a.ld_q + (static_cast<int64_t>(head) * a.group + r - token * a.group) * 128;
-      u[c] = reinterpret_cast<const uint4*>(q)[piece];
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + first + step * i;
+      u[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (first + step * i < top && r < all) {
+        const int token = r / a.group;
+        const uint16_t* q =
+            a.Q + (first_token(a, s) + token) * a.ld_q + (static_cast<int64_t>(head) * a.group + r - token * a.group) * 128;
+        u[i] = reinterpret_cast<const uint4*>(q)[piece];
+      }
     }
-  }
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) {
-    const int r = r0 + c * 8 + n;
-    const float v[8] = {bf16lo(u[c].x), bf16hi(u[c].x), bf16lo(u[c].y), bf16hi(u[c].y),
-                        bf16lo(u[c].z), bf16hi(u[c].z), bf16lo(u[c].w), bf16hi(u[c].w)};
-    float amax = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const int in = first + step * i, c = in >> 3, n = in & 7, r = r0 + in;
+      if (in >= top) break;  // (the same in the whole warp: its two rows are of the same eight)
+      const float v[8] = {bf16lo(u[i].x), bf16hi(u[i].x), bf16lo(u[i].y), bf16hi(u[i].y),
+                          bf16lo(u[i].z), bf16hi(u[i].z), bf16lo(u[i].w), bf16hi(u[i].w)};
+      float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    // 2^up brings the largest into [2^7, 2^8) (an infinity becomes NaN, as its scores would)
-    const int up = amax > 0.0f && amax < INFINITY ? min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120) : 0;
-    const float f = amax < INFINITY ? __int_as_float((up + 127) << 23) : NAN;
-    uint32_t one[4], two[4];
+      for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+      // 2^up brings the largest into [2^7, 2^8) (an infinity becomes NaN, as its scores would)
+      const int up = amax > 0.0f && amax < INFINITY ? min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120) : 0;
+      const float f = amax < INFINITY ? __int_as_float((up + 127) << 23) : NAN;
+      uint32_t one[4], two[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) two_terms(v[2 * i] * f, v[2 * i + 1] * f, one[i], two[i]);
-    const uint32_t at = to + static_cast<uint32_t>(c * 2048 + n * 128 + (((piece >> 1) ^ n) << 4) + (piece & 1) * 8);
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
-    if (piece == 0) {
-      const int limit = r >= count ? 0 : is_shared(a, s) ? len : len - a.t + r / a.group + 1;
-      rows[c * 8 + n] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, limit, 0};
+      for (int e = 0; e < 4; ++e) two_terms(v[2 * e] * f, v[2 * e + 1] * f, one[e], two[e]);
+      const uint32_t at = to + static_cast<uint32_t>(c * 2048 + n * 128 + (((piece >> 1) ^ n) << 4) + (piece & 1) * 8);
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
+      if (piece == 0) {
+        const int limit = r >= all ? 0 : is_shared(a, s) ? len : len - a.t + r / a.group + 1;
+        rows[in] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, limit, 0};
+      }
     }
   }
   fence_proxy_async_smem();
@@ -326,7 +341,9 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = &g_cached_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_Q_FULL || i == B_Q_FULL + 1 || i == B_P_FULL || i == B_P_FULL + 1 ? 4 * S::kGroups : i >= B_EXPS ? 32 : 1);
+    for (int i = 0; i < B_COUNT; ++i)
+      mbar_init(bar(i), i == B_P_FULL || i == B_P_FULL + 1 ? 4 * S::kGroups : i >= B_Q_EMPTY ? 4 * S::kGroups + 1
+                        : i >= B_EXPS || i == B_Q_FULL || i == B_Q_FULL + 1 ? 32 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     if (lane >= o) sum += v;
   }
   if (lane == 31) warp_sums[warp] = sum;
-  if (threadIdx.x == 0) pieces[0] = Piece{};
+  if (threadIdx.x == 0) pieces[2] = Piece{};
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -383,7 +400,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     p.block = item / subs;
     p.head = (item - p.block * subs) * a.abreast;
     p.t0 = static_cast<int>((lo - done) - static_cast<int64_t>(item) * p.tiles);
-    if (close_piece(a, p, hi)) pieces[0] = p;
+    if (close_piece(a, p, hi)) pieces[2] = p;
   };
   const int64_t mine_at = (sum - mine) * subs;
   if (work && mine_at <= lo && lo < mine_at + mine * subs) {
@@ -414,47 +431,65 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
   __syncthreads();
 
   if (work && warp == 0) {
-    // ---------------- loads: K and V of one tile after the other, and its keys' exponents, which the lanes load (four keys each) and
-    // store a tile later, before anything that may wait.  (Loaded by the threads that use them, a tile ahead, they were waited for:
+    // ---------------- loads: K and V of one tile after the other, and its keys' exponents, which the lanes ask for (four keys each)
+    // before they wait for the tile's places, and store before the next tile.  (Loaded by the threads that use them, a tile ahead, they were waited for:
     // 64 sequences of up to 8000 keys 101 us.)  Four tiles of them are kept: V of the third tile before is read by then.
-    Piece p = pieces[0];
-    uint32_t slot = 0, round = 0, made = 0;
+    // It also prepares each item but the first: its piece and rows for the others, two items at a time.
+    Piece p = pieces[2];
+    uint32_t slot = 0, round = 0, made = 0, item = 0;
     const bool one = elect_one();
     bool ok = true, more = p.t1 > p.t0;
-    int exps[4];
+    int of_keys[4], of_values[4];  // (joined where they are stored, so that nothing waits for them before)
     auto store = [&] {  // those of tile made - 1
       const uint32_t to = bar0 + kExpsAt + ((made - 1) & (kExpTiles - 1)) * (2u * kKeys) + 2u * lane;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 64u * i), "h"(static_cast<unsigned short>(exps[i])) : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(to + 64u * i), "h"(static_cast<unsigned short>(of_keys[i] | of_values[i] << 8)) : "memory");
       mbar_arrive(bar(B_EXPS + ((made - 1) & (kExpTiles - 1))));
     };
-    while (more && ok) {
-      const int64_t list = (p.head + lane_head) * a.ld_exp + p.start;
-      for (int tile = p.t0; tile < p.t1 && ok; ++tile) {
-        if (made > 0) store();
-        const int row = p.start + tile * kKeys;
+    auto wait = [&](int b, uint32_t parity, int site) {  // the same in the whole warp
+      ok = __all_sync(0xFFFFFFFFu, ok && arrival(bar(b), parity & 1u, abort_flag, err, a.err_site + site));
+    };
+    for (;; ++item) {
+      for (int tile = p.t0; tile <= p.t1; ++tile) {
+        if (tile < p.t1) {
+          if (made > 0 && ok) store();
+          const int row = p.start + tile * kKeys;
+          const int64_t list = (p.head + lane_head) * a.ld_exp + row;
 #pragma unroll
-        for (int value = 0; value < 2; ++value) {
-          if (round > 0) ok = ok && mbar_wait(bar(B_EMPTY + slot), (round - 1) & 1u, abort_flag, err, a.err_site + 1);
-          if (ok && one) {
-            mbar_arrive_expect_tx(bar(B_FULL + slot), kTile);
-            tma_load_3d(ring + slot * kTile, value ? &map_v : &map_k, bar(B_FULL + slot), 0, p.head + lane_head, row);
+          for (int i = 0; i < 4; ++i) {
+            const int in = 32 * i + lane;
+            of_keys[i] = of_values[i] = 127;  // (what lies past the keys may be anything)
+            if (tile * kKeys + in < p.len) {
+              of_keys[i] = load_line(a.k_exp + list + in);
+              of_values[i] = load_line(a.v_exp + list + in);
+            }
           }
-          if (++slot == kSlots) {
-            slot = 0;
-            ++round;
-          }
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int in = tile * kKeys + 32 * i + lane;
-          exps[i] = 127 | 127 << 8;  // (what lies past the keys may be anything)
-          if (in < p.len) exps[i] = load_line(a.k_exp + list + in) | load_line(a.v_exp + list + in) << 8;
+          for (int value = 0; value < 2; ++value) {
+            if (round > 0) wait(B_EMPTY + slot, round - 1, 1);
+            if (ok && one) {
+              mbar_arrive_expect_tx(bar(B_FULL + slot), kTile);
+              tma_load_3d(ring + slot * kTile, value ? &map_v : &map_k, bar(B_FULL + slot), 0, p.head + lane_head, row);
+            }
+            if (++slot == kSlots) {
+              slot = 0;
+              ++round;
+            }
+          }
+          ++made;
         }
-        ++made;
+        if (tile == p.t0 && item > 0) {  // (or there is no item, and the others learn it)
+          if (item >= 2) wait(B_Q_EMPTY + (item & 1u), (item >> 1) + 1, 12);
+          if (lane == 0) pieces[item & 1u] = p;
+          if (more) prepare_rows(a, p.s, p.len, p.head + lane_head, p.block * R, q_at + (item & 1u) * S::kOperand, all_rows + (item & 1u) * R, lane, 0, 2);
+          mbar_arrive(bar(B_Q_FULL + (item & 1u)));
+        }
+        if (!ok || !more) break;
       }
+      if (!ok || !more) break;
       more = next_piece(a, p, hi);
+      if (!more) p.t1 = p.t0;
     }
     if (made > 0 && ok) store();
     if (!ok) {  // copies in flight land before the block leaves
@@ -468,12 +503,19 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     const uint64_t ring_desc = sdesc_sw128(ring, 16, 1024);
     bool ok = true;
     auto wait = [&](int b, uint32_t parity, int site) {  // the same in the whole warp
-      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(b), parity & 1u, abort_flag, err, a.err_site + site));
+      ok = __all_sync(0xFFFFFFFFu, ok && arrival(bar(b), parity & 1u, abort_flag, err, a.err_site + site));
     };
-    Piece p = pieces[0];
-    int tile = p.t0;
-    bool more = p.t1 > p.t0;
-    uint32_t item = 0, made = 0, slot_k = 0, round_k = 0, slot_v = 1, round_v = 0;
+    int tile = 0, tile0 = 0, tile1 = 0;
+    bool more = false;
+    uint32_t item = 0, made = 0, slot_k = 0, round_k = 0, slot_v = 1, round_v = 0, item_columns = 0;
+    auto enter = [&] {
+      wait(B_Q_FULL + (item & 1u), item >> 1, 2);
+      const Piece& p = pieces[item & 1u];
+      tile = tile0 = p.t0;
+      tile1 = p.t1;
+      item_columns = 16u * static_cast<uint32_t>((min(R, rows_of(a, p.s) - p.block * R) + 7) >> 3);
+      more = ok && tile1 > tile0;
+    };
     uint32_t columns = 0, columns_before = 0;  // of the last tile and of the one before it; bit 31: the item's first
     auto advance = [](uint32_t& slot, uint32_t& round) {
       slot += 2;
@@ -483,10 +525,9 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
       }
     };
     auto scores = [&] {
-      if (tile == p.t0) wait(B_Q_FULL + (item & 1u), item >> 1, 2);
       wait(B_FULL + slot_k, round_k, 3);
       columns_before = columns;
-      columns = 16u * static_cast<uint32_t>((min(R, rows_of(a, p.s) - p.block * R) + 7) >> 3);
+      columns = item_columns;
       tc_fence_after();
       if (ok && one) {
         const uint32_t id = idesc_e4m3_f32(128, static_cast<int>(columns), false, false);
@@ -495,20 +536,18 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         for (uint32_t k = 0; k < 4; ++k) umma_f8(tmem + (made & 1u) * S::kCols, dk + 2 * k, dq + 2 * k, id, k != 0);
         umma_commit(bar(B_S_FULL + (made & 1u)));
         umma_commit(bar(B_EMPTY + slot_k));
+        if (tile + 1 == tile1) umma_commit(bar(B_Q_EMPTY + (item & 1u)));
       }
       __syncwarp();
-      if (tile == p.t0) columns |= 1u << 31;
+      if (tile == tile0) columns |= 1u << 31;
       advance(slot_k, round_k);
       ++made;
-      if (++tile == p.t1) {
-        more = next_piece(a, p, hi);
-        tile = p.t0;
-        ++item;
-      }
+      ++tile;
     };
+    enter();
     if (more) scores();
     for (uint32_t j = 0; j < made && ok; ++j) {
-      const bool last = !more;
+      const bool last = tile == tile1;  // of its item
       if (!last) scores();
       const uint32_t mine = last ? columns : columns_before;
       wait(B_P_FULL + (j & 1u), j >> 1, 4);
@@ -525,6 +564,11 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
       }
       __syncwarp();
       advance(slot_v, round_v);
+      if (last) {  // (the next item's rows may have to wait for what the last product goes to)
+        ++item;
+        enter();
+        if (more) scores();
+      }
     }
     if (one) umma_commit(bar(B_DRAIN));
     __syncwarp();
@@ -543,23 +587,35 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     auto groups_sync = [&] {
       if (S::kGroups > 1) asm volatile("bar.sync %0, %1;" ::"n"(S::kGroups + 1), "n"(128 * S::kGroups) : "memory");
     };
+    auto keys_any = [&](bool x) {
+      uint32_t r;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.b32 p, %3, 0;\n\t"
+          "bar.red.or.pred q, %1, %2, p;\n\t"
+          "selp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(r)
+          : "n"(S::kGroups + 1), "n"(128 * S::kGroups), "r"(static_cast<uint32_t>(x))
+          : "memory");
+      return r != 0;
+    };
     bool ok = true;
     auto wait = [&](int b, uint32_t parity, int site) {
-      ok = mbar_wait(bar(b), parity & 1u, abort_flag, err, a.err_site + site) && ok;
+      ok = arrival(bar(b), parity & 1u, abort_flag, err, a.err_site + site) && ok;
     };
-    auto prepare = [&](const Piece& p, uint32_t item) {
-      prepare_rows<kChunks>(a, p.s, p.len, p.head + lane_head, p.block * R + group * kRows,
-                            q_at + (item & 1u) * S::kOperand + static_cast<uint32_t>(group * kChunks) * 2048u,
-                            all_rows + (item & 1u) * R + group * kRows, x);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_Q_FULL + (item & 1u)));
-    };
-    Piece p = pieces[0], next = p;
-    bool more = p.t1 > p.t0, another = false;
-    if (more) prepare(p, 0);
+    // the range's first item, by all
+    {
+      const Piece p = pieces[2];
+      prepare_rows(a, p.s, p.len, p.head + lane_head, p.block * R, q_at, all_rows, lane, 2 * (warp - 2), 8 * S::kGroups);
+      if (threadIdx.x == 64) pieces[0] = p;
+    }
+    keys_any(false);
+    if (warp == 2) mbar_arrive(bar(B_Q_FULL));
     uint32_t j = 0, slot_v = 1, round_v = 0;  // tiles so far; V's place in the ring
-    group_sync(group);                        // the rows are there
-    for (uint32_t item = 0; more; ++item) {
+    for (uint32_t item = 0;; ++item) {
+      wait(B_Q_FULL + (item & 1u), item >> 1, 13);
+      const Piece p = pieces[item & 1u];
+      if (keys_any(!ok) || p.t1 <= p.t0) break;  // (the same for all: nobody is left at a barrier)
       Row* rows = all_rows + (item & 1u) * R + group * kRows;
       const int count = min(kRows, rows_of(a, p.s) - p.block * R - group * kRows), chunks = (count + 7) >> 3;  // (none: below 0)
       const int least = is_shared(a, p.s) ? p.len : p.len - a.t + p.block * R / a.group + 1;  // keys that every row sees
@@ -571,14 +627,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
 
       for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
         const bool first = tile == p.t0;
-        if (first) {  // one thread finds the next item, all take it from shared memory (after they have met below)
-          if (threadIdx.x == 64) {
-            Piece n = p;
-            if (!next_piece(a, n, hi)) n.t1 = n.t0;
-            pieces[(item + 1) & 1u] = n;
-          }
-          groups_sync();
-        }
         const int key0 = tile * kKeys;
         const bool tail = key0 + kKeys > least;
         wait(B_EXPS + (j & (kExpTiles - 1)), j / kExpTiles, 11);
@@ -605,7 +653,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
               const float z = fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i])) * key_scale;
               d[8 * c + i] = fmaf(z, row.x, bias - row.y);
             }
-            if (tail) {
+            if (__builtin_expect(tail, 0)) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 if (key0 + me >= rows[8 * c + i].limit) d[8 * c + i] = -INFINITY;
@@ -624,7 +672,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
           flags = (flags_of[0] | flags_of[1]) | (flags_of[2] | flags_of[3]);
         }
         if (force) flags = chunks > 0 ? (1u << chunks) - 1u : 0u;
-        if (flags) {
+        if (__builtin_expect(flags != 0, 0)) {
           // the rows' maxima; where one is well above m, m moves
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
@@ -697,14 +745,14 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
             }
             st_shared_v4(to + c * (kKeys * 16u), one[0] | one[1] << 16, one[2] | one[3] << 16, two[0] | two[1] << 16, two[2] | two[3] << 16);
           }
-        if (tail && group == 0) {
+        if (__builtin_expect(tail && group == 0, 0)) {
           // values past the sequence's keys count as zero, NaN included
           wait(B_FULL + slot_v, round_v, 9);
           const uint32_t v_at = ring + slot_v * kTile;
           for (int r = max(p.len - key0, 0) + (x >> 3); r < kKeys; r += 16)
             st_shared_v4(v_at + static_cast<uint32_t>(r * 128 + (x & 7) * 16), 0u, 0u, 0u, 0u);
         }
-        if (tail && least < p.len) {
+        if (__builtin_expect(tail && least < p.len, 0)) {
           // so does NaN among keys that some rows do not see, and the rows that do get it at the item's end.  (Each group looks before one
           // clears them.)
           wait(B_FULL + slot_v, round_v, 9);
@@ -731,11 +779,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         if (slot_v >= kSlots) {
           slot_v -= kSlots;
           ++round_v;
-        }
-        if (first) {
-          next = pieces[(item + 1) & 1u];
-          another = next.t1 > next.t0;
-          if (another) prepare(next, item + 1);
         }
       }
 
@@ -787,8 +830,10 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
             parts[to.at + me] = o;
         }
       }
-      p = next;
-      more = another;
+      // the item's rows and O are read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_Q_EMPTY + (item & 1u)));
     }
   }
   tc_fence_before();
