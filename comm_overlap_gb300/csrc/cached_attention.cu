@@ -667,9 +667,11 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
           flags = group_any(group, flags != 0) ? 1u : 0u;
         } else {
           flags = __reduce_or_sync(0xFFFFFFFFu, flags);
-          if (lane == 0) flags_of[warp & 3] = flags;
+          // (in turn in two places: a warp may write the next tile's before another has read this one's)
+          volatile uint32_t* of = flags_of + (j & 1u) * (4 * S::kGroups);
+          if (lane == 0) of[warp & 3] = flags;
           group_sync(group);
-          flags = (flags_of[0] | flags_of[1]) | (flags_of[2] | flags_of[3]);
+          flags = (of[0] | of[1]) | (of[2] | of[3]);
         }
         if (force) flags = chunks > 0 ? (1u << chunks) - 1u : 0u;
         if (__builtin_expect(flags != 0, 0)) {

@@ -10,8 +10,8 @@
 // lane keeps one kind's weight and sums in registers.
 //
 // Angles: a position turns pair i by position x frequency.  The frequency is kept as a 64-bit fraction of a turn, so the
-// product's low 64 bits are the angle's fraction of a turn without any rounding by the position's size; its upper 32 bits go to
-// sincospif.
+// product's low 64 bits are the angle's fraction of a turn without any rounding by the position's size; what its upper 32 bits are off
+// the nearest quarter turn goes to sincospif.
 //
 // Bound: memory.  Forward 4 bytes a value, backward 6 (4 without norm), cache 3.
 #include <mutex>
@@ -91,8 +91,12 @@ __device__ __forceinline__ void token_angles(float* cosines, float* sines, const
     const int i = lane + 32 * k;
     if (i < (rot >> 1)) {
       const unsigned long long at = turns[i] * static_cast<unsigned long long>(static_cast<long long>(position));
-      float sn, cs;
-      sincospif(static_cast<float>(static_cast<int>(at >> 32)) * 0x1p-31f, &sn, &cs);
+      // the nearest quarter turn, and the rest, which is small enough to keep its digits in fp32
+      const uint32_t turn = static_cast<uint32_t>(at >> 32), quarter = (turn + 0x20000000u) >> 30;
+      float x, y;
+      sincospif(static_cast<float>(static_cast<int>(turn - (quarter << 30))) * 0x1p-31f, &y, &x);
+      const float cs = quarter & 1 ? (quarter & 2 ? y : -y) : (quarter & 2 ? -x : x);
+      const float sn = quarter & 1 ? (quarter & 2 ? -x : x) : (quarter & 2 ? -y : y);
       cosines[i] = cs * amplitude;
       sines[i] = sn * (amplitude * sign);
     }
@@ -157,8 +161,9 @@ constexpr float kInvD = 1.0f / 128.0f;
 // Heads whose squares leave fp32's range are measured times this.
 constexpr float kSmaller = 0x1p-80f;
 
-// 1 / sqrt(mean(x^2) + eps) of the head, whose values are brought into range: x was multiplied by `small`, and so is the result.
-__device__ __forceinline__ float head_rstd(uint64_t (&a)[4], uint64_t (&b)[4], float eps, float& small) {
+// 1 / sqrt(mean(x^2) + eps) of the head, whose values are brought into range: x was multiplied by `small`, and so is the result.  To the
+// nearest for what goes to 8 bits, where the last bit of fp32 can turn a value over to the next step.
+__device__ __forceinline__ float head_rstd(uint64_t (&a)[4], uint64_t (&b)[4], float eps, float& small, bool nearest = false) {
   auto squares = [&] {
     uint64_t s0 = mul_f2(a[0], a[0]), s1 = mul_f2(b[0], b[0]);
 #pragma unroll
@@ -180,7 +185,12 @@ __device__ __forceinline__ float head_rstd(uint64_t (&a)[4], uint64_t (&b)[4], f
     }
     ss = squares();
   }
-  return rsqrtf(fmaf(ss, kInvD, eps * small * small));
+  const float mean = fmaf(ss, kInvD, eps * small * small);
+  const float r = rsqrtf(mean);
+  if (!nearest) return r;
+  // a step of Newton's method, its residual 1 - mean r^2 from products without rounding
+  const float h = mean * r, l = fmaf(mean, r, -h), e = fmaf(-l, r, fmaf(-h, r, 1.0f));
+  return e == e ? fmaf(0.5f * r, e, r) : r;  // (an infinity has none)
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -429,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, CACHE ? kWriteBlocks : kFwdBlocks) r
         float rstd = 1.0f;
         if (NORM) {
           float small;
-          rstd = head_rstd(va, vb, a.eps, small);
+          rstd = head_rstd(va, vb, a.eps, small, CACHE && !query);
         }
         if (p.turns) {
           turn_pairs<HALF>(va, vb, A, B, C, D);
