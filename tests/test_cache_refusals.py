@@ -166,3 +166,28 @@ def test_functions_refuse_what_they_cannot_take():
     with pytest.raises(ValueError, match="layout"):
         ops.DominoQKRotary(128, layout="diagonal", device="cpu")
     assert cache.k.dtype == torch.float8_e4m3fn and cache.k.shape == (10, 8, 128) and cache.k_exp.shape == (8, 10)
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_tangents_are_refused(grad):
+    import torch.autograd.forward_ad as forward_ad
+    x, w = torch.randn(4, 2, 128).bfloat16(), torch.ones(128).bfloat16()
+    at, cache = torch.zeros(4, dtype=torch.int32), ops.QuantizedCache.empty(10, 2, device="cpu")
+    f = ops.rotary_frequencies(128, device="cpu")
+    for name, args, call in (("qk_rotary", (x, x, w, w), lambda q, k, a, b: ops.qk_rotary(q, k, at, f, a, b)),
+                             ("cache_write", (x, x, x, w, w), lambda k, v, q, a, b: ops.cache_write(cache, at, k, v, q, at, f, a, b)),
+                             ("cached_attention", (x,), lambda q: ops.cached_attention(q, cache, at, at))):
+        for i in range(len(args)):
+            with torch.set_grad_enabled(grad), forward_ad.dual_level():
+                dual = list(args)
+                dual[i] = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
+                with pytest.raises(NotImplementedError, match=name):
+                    call(*dual)
+
+
+def test_no_backward_is_refused():
+    x = torch.zeros(4, 2, 128, dtype=torch.bfloat16, requires_grad=True)
+    y, at, cache = x.detach(), torch.zeros(4, dtype=torch.int32), ops.QuantizedCache.empty(10, 2, device="cpu")
+    for call in (lambda: ops.cache_write(cache, at, x, y), lambda: ops.cache_write(cache, at, y, x), lambda: ops.cache_write(cache, at, y, y, x)):
+        with pytest.raises(ValueError, match="no backward"):
+            call()
