@@ -67,17 +67,20 @@ struct Shape {
 constexpr float kRaise = 4.0f, kBehind = 4.8f;
 constexpr float kTerm = 0.0625f;  // of the second terms
 
-// ---- work: tiles of all items (sequence, block of rows, `abreast` key heads) in order
+// ---- work: tiles of all items (sequence, block of rows, `abreast` key heads) in order.  What an item costs beside its tiles counts as
+// kItem of them, before its first: units.  (16 sequences of up to 3001 keys, 35 rows each for 4 heads: 32.3 us without, 29.7 so, 29.8 with
+// two.)
+constexpr int kItem = 1;
 
 struct CachedHeader {
-  int64_t tiles;       // of all items
+  int64_t units;       // of all items
   int64_t each;        // of a range; the first `rest` ranges have one more
   int32_t rest, ranges;
 };
 
 struct CachedWork {
   CachedHeader* head;
-  int64_t* base;    // tiles before each sequence
+  int64_t* base;    // units before each sequence
   float* slots;     // two for each range, of R partial rows for each head abreast
   float* whole;     // partial rows of items that were not cut, by token and head (with a shared prefix)
 };
@@ -91,22 +94,30 @@ __device__ __forceinline__ int64_t first_token(const CachedArgs& a, int s) {
 }
 
 // First row and length of an entry; one whose rows leave the cache gets none and is recorded.
-__device__ __forceinline__ int sequence(const CachedArgs& a, int s, int& start) {
+__device__ __forceinline__ void given_rows(const CachedArgs& a, int s, int& start, int& len) {
   start = is_shared(a, s) ? a.prefix[0] : a.k_start[s - a.shared];
-  int len = is_shared(a, s) ? a.prefix[1] : a.k_len[s - a.shared];
+  len = is_shared(a, s) ? a.prefix[1] : a.k_len[s - a.shared];
+}
+__device__ __forceinline__ int checked(const CachedArgs& a, int& start, int len) {
   if (start < 0 || len < 0 || len > a.cache_rows || start > a.cache_rows - len) {
     atomicCAS(&g_cached_err, 0, kPackedBadLengths);
     start = len = 0;
   }
   return len;
 }
+__device__ __forceinline__ int sequence(const CachedArgs& a, int s, int& start) {
+  int len;
+  given_rows(a, s, start, len);
+  return checked(a, start, len);
+}
 __device__ __forceinline__ int tiles_of(int len) { return (len + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kItem : 0; }
 
 __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {  // x, y >= 0; nearly always within 32 bits
   if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
   return x / y;
 }
-// Where range i begins, and the range that tile x belongs to.
+// Where range i begins, and the range that unit x belongs to.
 __device__ __forceinline__ int64_t range_begin(int64_t i, const CachedHeader& h) { return i * h.each + (i < h.rest ? i : h.rest); }
 __device__ __forceinline__ int64_t range_of(int64_t x, const CachedHeader& h) {
   const int64_t longer = h.rest * (h.each + 1);
@@ -118,29 +129,32 @@ struct Piece {
   int s, start, len, tiles;
   int block, head;  // block of rows, first of the key heads abreast
   int t0, t1;
-  int64_t at;       // t0 in the order of all tiles
+  int64_t at;       // the item's first unit
 };
 
 // Sets t1; false where there is none (past the range, or, where lengths change while the kernel reads them, past the sequences).
 __device__ __forceinline__ bool close_piece(const CachedArgs& a, Piece& p, int64_t hi) {
-  if (p.at >= hi || p.s >= a.n + a.shared) return false;
-  const int64_t left = hi - p.at;
-  p.t1 = p.tiles - p.t0 < left ? p.tiles : p.t0 + static_cast<int>(left);
-  return true;
+  const int64_t left = hi - p.at - kItem;
+  p.t1 = p.tiles < left ? p.tiles : static_cast<int>(left);
+  return p.t1 > p.t0 && p.s < a.n + a.shared;
 }
-__device__ __forceinline__ bool next_piece(const CachedArgs& a, Piece& p, int64_t hi) {
-  p.at += p.t1 - p.t0;
+// (next_start, next_len: those of the entry behind p's, loaded by the call before, so that none waits for them.)
+__device__ __forceinline__ bool next_piece(const CachedArgs& a, Piece& p, int64_t hi, int& next_start, int& next_len) {
+  p.at += units_of(p.tiles);
   p.t0 = 0;
   p.head += a.abreast;
   if (p.head >= a.hkv) {
     p.head = 0;
     if (++p.block >= blocks_of(a, p.s)) {
       p.block = 0;
+      const int entries = a.n + a.shared;
       do {
         ++p.s;
-        p.len = p.s < a.n + a.shared && p.at < hi ? sequence(a, p.s, p.start) : 0;
+        p.start = next_start;
+        p.len = p.s < entries && p.at < hi ? checked(a, p.start, next_len) : 0;
         p.tiles = tiles_of(p.len);
-      } while (p.tiles == 0 && p.s < a.n + a.shared && p.at < hi);
+        if (p.s + 1 < entries) given_rows(a, p.s + 1, next_start, next_len);
+      } while (p.tiles == 0 && p.s < entries && p.at < hi);
     }
   }
   return close_piece(a, p, hi);
@@ -196,6 +210,18 @@ __device__ __forceinline__ bool group_any(int group, bool x) {
   return r != 0;
 }
 
+// Whether the phase has completed, without any wait.
+__device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // mbar_wait with all but its first look out of the way: the loop over tiles is long as it is, and instructions that it passes over cost
 // it their fetching.
 __device__ __noinline__ bool arrival_awaited(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int site) {
@@ -245,7 +271,7 @@ struct __align__(16) OutRow {
 };
 
 enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_EXPS = 25,
-             B_Q_EMPTY = 29, B_COUNT = 31 };
+             B_Q_EMPTY = 29, B_READY = 31, B_COUNT = 32 };
 // Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces (two items', the range's first); 1024: rows of two items; 2048: four warps'
 // maxima or sums of 32 rows; 2560: by how much m moved, and the factor for what was added up before; 3072: exponents of four tiles' keys
 constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 2048, kMovesAt = 2560, kExpsAt = 3072;
@@ -259,46 +285,64 @@ __device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, i
                                           int first, int step) {
   const int piece = lane & 15, all = rows_of(a, s), top = (min(a.rows_of_block, all - r0) + 7) & ~7;
 #pragma unroll 1
-  for (first += lane >> 4; first < top; first += 4 * step) {
+  for (first += lane >> 4; first - (lane >> 4) < top; first += 4 * step) {
     uint4 u[4];
+    float amax[4];
+    int token[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = r0 + first + step * i;
       u[i] = make_uint4(0u, 0u, 0u, 0u);
+      token[i] = static_cast<int>(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.group));
       if (first + step * i < top && r < all) {
-        const int token = r / a.group;
         const uint16_t* q =
-            a.Q + (first_token(a, s) + token) * a.ld_q + (static_cast<int64_t>(head) * a.group + r - token * a.group) * 128;
+            a.Q + (first_token(a, s) + token[i]) * a.ld_q + (static_cast<int64_t>(head) * a.group + r - token[i] * a.group) * 128;
         u[i] = reinterpret_cast<const uint4*>(q)[piece];
       }
     }
+    auto value = [&](int i, int e) {
+      const uint32_t x = e < 2 ? u[i].x : e < 4 ? u[i].y : e < 6 ? u[i].z : u[i].w;
+      return e & 1 ? bf16hi(x) : bf16lo(x);
+    };
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int in = first + step * i, c = in >> 3, n = in & 7, r = r0 + in;
-      if (in >= top) break;  // (the same in the whole warp: its two rows are of the same eight)
-      const float v[8] = {bf16lo(u[i].x), bf16hi(u[i].x), bf16lo(u[i].y), bf16hi(u[i].y),
-                          bf16lo(u[i].z), bf16hi(u[i].z), bf16lo(u[i].w), bf16hi(u[i].w)};
-      float amax = 0.0f;
+      amax[i] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[e]));
+      for (int e = 0; e < 8; ++e) amax[i] = fmaxf(amax[i], fabsf(value(i, e)));
+    }
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+    for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xFFFFFFFFu, amax[i], o));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int in = first + step * i, c = in >> 3, n = in & 7;
       // 2^up brings the largest into [2^7, 2^8) (an infinity becomes NaN, as its scores would)
-      const int up = amax > 0.0f && amax < INFINITY ? min(7 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), 120) : 0;
-      const float f = amax < INFINITY ? __int_as_float((up + 127) << 23) : NAN;
+      const int up = amax[i] > 0.0f && amax[i] < INFINITY ? min(7 + 127 - static_cast<int>(__float_as_uint(amax[i]) >> 23), 120) : 0;
+      const float f = amax[i] < INFINITY ? __int_as_float((up + 127) << 23) : NAN;
       uint32_t one[4], two[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) two_terms(v[2 * e] * f, v[2 * e + 1] * f, one[e], two[e]);
-      const uint32_t at = to + static_cast<uint32_t>(c * 2048 + n * 128 + (((piece >> 1) ^ n) << 4) + (piece & 1) * 8);
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
-      if (piece == 0) {
-        const int limit = r >= all ? 0 : is_shared(a, s) ? len : len - a.t + r / a.group + 1;
-        rows[in] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, limit, 0};
+      for (int e = 0; e < 4; ++e) two_terms(value(i, 2 * e) * f, value(i, 2 * e + 1) * f, one[e], two[e]);
+      if (in < top) {
+        const uint32_t at = to + static_cast<uint32_t>(c * 2048 + n * 128 + (((piece >> 1) ^ n) << 4) + (piece & 1) * 8);
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(one[0] | one[1] << 16), "r"(one[2] | one[3] << 16) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 1024u), "r"(two[0] | two[1] << 16), "r"(two[2] | two[3] << 16) : "memory");
+        if (piece == 0) {
+          const int limit = r0 + in >= all ? 0 : is_shared(a, s) ? len : len - a.t + token[i] + 1;
+          rows[in] = {a.scale_log2 * __int_as_float((127 - up) << 23), 0.0f, limit, 0};
+        }
       }
     }
   }
   fence_proxy_async_smem();
+}
+
+// Whether the threads that hold the keys prepare an item's rows (the range's first they always do).  The loading warp takes 2.5 us for
+// eight, while the others work on the item before, but ten for 32: 16 sequences of up to 3001 keys, 35 rows each for 4 heads 29.7 us if it
+// prepares all, 27.4 so.
+template <int R>
+__device__ __forceinline__ bool keys_prepare(const CachedArgs& a, const Piece& p) {
+  return R > 8 && rows_of(a, p.s) - p.block * R > 8;
 }
 
 // Sums over the warp of each of ROWS values: lane i gets that of row i / (32 / ROWS).
@@ -342,7 +386,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
   int* err = &g_cached_err;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i)
-      mbar_init(bar(i), i == B_P_FULL || i == B_P_FULL + 1 ? 4 * S::kGroups : i >= B_Q_EMPTY ? 4 * S::kGroups + 1
+      mbar_init(bar(i), i == B_P_FULL || i == B_P_FULL + 1 || i == B_READY ? 4 * S::kGroups : i >= B_Q_EMPTY ? 4 * S::kGroups + 1
                         : i >= B_EXPS || i == B_Q_FULL || i == B_Q_FULL + 1 ? 32 : 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -361,7 +405,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
   int start0 = 0, len0 = 0;  // of the thread's last entry
   for (int s = s0; s < s1; ++s) {
     len0 = sequence(a, s, start0);
-    mine += static_cast<int64_t>(tiles_of(len0)) * blocks_of(a, s);
+    mine += static_cast<int64_t>(units_of(tiles_of(len0))) * blocks_of(a, s);
   }
   int64_t sum = mine;
 #pragma unroll
@@ -382,24 +426,24 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     total += warp_sums[i];
   }
   CachedHeader h;
-  h.tiles = total * subs;
+  h.units = total * subs;
   {
     const int most = static_cast<int>(gridDim.x) / a.abreast;
-    h.ranges = h.tiles < most ? (h.tiles > 0 ? static_cast<int>(h.tiles) : 1) : most;
-    h.each = divide(h.tiles, h.ranges);
-    h.rest = static_cast<int>(h.tiles - h.each * h.ranges);
+    h.ranges = h.units < most ? (h.units > 0 ? static_cast<int>(h.units) : 1) : most;
+    h.each = divide(h.units, h.ranges);
+    h.rest = static_cast<int>(h.units - h.each * h.ranges);
   }
   const int lane_head = blockIdx.x % a.abreast;  // of the heads abreast
   const int64_t range = blockIdx.x / a.abreast;
-  const bool work = h.tiles > 0 && range < h.ranges;
+  const bool work = h.units > 0 && range < h.ranges;
   const int64_t lo = work ? range_begin(range, h) : 0, hi = work ? range_begin(range + 1, h) : 0;
-  // the range's first piece: tile lo is tile lo - done of entry p.s
+  // the range's first piece: unit lo is unit lo - done of entry p.s
   auto enter = [&](Piece p, int64_t done) {
-    const int item = static_cast<int>(divide(lo - done, p.tiles));
-    p.at = lo;
+    const int units = units_of(p.tiles), item = static_cast<int>(divide(lo - done, units));
+    p.at = done + static_cast<int64_t>(item) * units;
     p.block = item / subs;
     p.head = (item - p.block * subs) * a.abreast;
-    p.t0 = static_cast<int>((lo - done) - static_cast<int64_t>(item) * p.tiles);
+    p.t0 = max(static_cast<int>(lo - p.at) - kItem, 0);
     if (close_piece(a, p, hi)) pieces[2] = p;
   };
   const int64_t mine_at = (sum - mine) * subs;
@@ -413,7 +457,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     for (;; ++p.s) {
       if (per > 1) p.len = p.s < s1 ? sequence(a, p.s, p.start) : 0;
       p.tiles = tiles_of(p.len);
-      const int64_t all = static_cast<int64_t>(p.tiles) * blocks_of(a, p.s) * subs;
+      const int64_t all = static_cast<int64_t>(units_of(p.tiles)) * blocks_of(a, p.s) * subs;
       if (lo < done + all || p.s >= s1) break;
       done += all;
     }
@@ -425,7 +469,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     for (int s = s0; s < s1; ++s) {
       int start;
       w.base[s] = at;
-      at += static_cast<int64_t>(tiles_of(sequence(a, s, start))) * blocks_of(a, s) * subs;
+      at += static_cast<int64_t>(units_of(tiles_of(sequence(a, s, start)))) * blocks_of(a, s) * subs;
     }
   }
   __syncthreads();
@@ -434,11 +478,13 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     // ---------------- loads: K and V of one tile after the other, and its keys' exponents, which the lanes ask for (four keys each)
     // before they wait for the tile's places, and store before the next tile.  (Loaded by the threads that use them, a tile ahead, they were waited for:
     // 64 sequences of up to 8000 keys 101 us.)  Four tiles of them are kept: V of the third tile before is read by then.
-    // It also prepares each item but the first: its piece and rows for the others, two items at a time.
+    // It also prepares each item but the first: its piece and (few) rows for the others, two items at a time.
     Piece p = pieces[2];
     uint32_t slot = 0, round = 0, made = 0, item = 0;
     const bool one = elect_one();
     bool ok = true, more = p.t1 > p.t0;
+    int next_start = 0, next_len = 0;
+    if (p.s + 1 < entries) given_rows(a, p.s + 1, next_start, next_len);
     int of_keys[4], of_values[4];  // (joined where they are stored, so that nothing waits for them before)
     auto store = [&] {  // those of tile made - 1
       const uint32_t to = bar0 + kExpsAt + ((made - 1) & (kExpTiles - 1)) * (2u * kKeys) + 2u * lane;
@@ -482,13 +528,14 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         if (tile == p.t0 && item > 0) {  // (or there is no item, and the others learn it)
           if (item >= 2) wait(B_Q_EMPTY + (item & 1u), (item >> 1) + 1, 12);
           if (lane == 0) pieces[item & 1u] = p;
-          if (more) prepare_rows(a, p.s, p.len, p.head + lane_head, p.block * R, q_at + (item & 1u) * S::kOperand, all_rows + (item & 1u) * R, lane, 0, 2);
+          if (more && !keys_prepare<R>(a, p))
+            prepare_rows(a, p.s, p.len, p.head + lane_head, p.block * R, q_at + (item & 1u) * S::kOperand, all_rows + (item & 1u) * R, lane, 0, 2);
           mbar_arrive(bar(B_Q_FULL + (item & 1u)));
         }
         if (!ok || !more) break;
       }
       if (!ok || !more) break;
-      more = next_piece(a, p, hi);
+      more = next_piece(a, p, hi, next_start, next_len);
       if (!more) p.t1 = p.t0;
     }
     if (made > 0 && ok) store();
@@ -507,14 +554,19 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     };
     int tile = 0, tile0 = 0, tile1 = 0;
     bool more = false;
-    uint32_t item = 0, made = 0, slot_k = 0, round_k = 0, slot_v = 1, round_v = 0, item_columns = 0;
-    auto enter = [&] {
+    uint32_t item = 0, made = 0, slot_k = 0, round_k = 0, slot_v = 1, round_v = 0, item_columns = 0, readied = 0;
+    auto enter = [&] {  // item `item`
       wait(B_Q_FULL + (item & 1u), item >> 1, 2);
       const Piece& p = pieces[item & 1u];
       tile = tile0 = p.t0;
       tile1 = p.t1;
       item_columns = 16u * static_cast<uint32_t>((min(R, rows_of(a, p.s) - p.block * R) + 7) >> 3);
       more = ok && tile1 > tile0;
+      if (more && item > 0 && keys_prepare<R>(a, p)) wait(B_READY, readied++, 14);
+    };
+    auto next_ready = [&] {  // whether there is no more to wait for before the next item (what the keys' threads prepare comes after its turn)
+      const uint32_t next = item + 1;
+      return __all_sync(0xFFFFFFFFu, arrived(bar(B_Q_FULL + (next & 1u)), (next >> 1) & 1u) && !keys_prepare<R>(a, pieces[next & 1u]));
     };
     uint32_t columns = 0, columns_before = 0;  // of the last tile and of the one before it; bit 31: the item's first
     auto advance = [](uint32_t& slot, uint32_t& round) {
@@ -547,9 +599,15 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     enter();
     if (more) scores();
     for (uint32_t j = 0; j < made && ok; ++j) {
-      const bool last = tile == tile1;  // of its item
-      if (!last) scores();
-      const uint32_t mine = last ? columns : columns_before;
+      bool last = tile == tile1;  // of its item
+      if (last && next_ready()) {
+        ++item;
+        enter();
+        last = false;
+      }
+      const bool ahead = !last && more;
+      if (ahead) scores();
+      const uint32_t mine = ahead ? columns_before : columns;
       wait(B_P_FULL + (j & 1u), j >> 1, 4);
       wait(B_FULL + slot_v, round_v, 5);
       tc_fence_after();
@@ -611,11 +669,19 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     }
     keys_any(false);
     if (warp == 2) mbar_arrive(bar(B_Q_FULL));
+    uint32_t readied = 0;
     uint32_t j = 0, slot_v = 1, round_v = 0;  // tiles so far; V's place in the ring
     for (uint32_t item = 0;; ++item) {
       wait(B_Q_FULL + (item & 1u), item >> 1, 13);
       const Piece p = pieces[item & 1u];
       if (keys_any(!ok) || p.t1 <= p.t0) break;  // (the same for all: nobody is left at a barrier)
+      if (item > 0 && keys_prepare<R>(a, p)) {
+        prepare_rows(a, p.s, p.len, p.head + lane_head, p.block * R, q_at + (item & 1u) * S::kOperand, all_rows + (item & 1u) * R, lane,
+                     2 * (warp - 2), 8 * S::kGroups);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_READY));
+        wait(B_READY, readied++, 14);
+      }
       Row* rows = all_rows + (item & 1u) * R + group * kRows;
       const int count = min(kRows, rows_of(a, p.s) - p.block * R - group * kRows), chunks = (count + 7) >> 3;  // (none: below 0)
       const int least = is_shared(a, p.s) ? p.len : p.len - a.t + p.block * R / a.group + 1;  // keys that every row sees
@@ -663,7 +729,9 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
             flags |= static_cast<uint32_t>(top > kRaise + kBehind) << c;
           }
         }
-        if (kChunks == 1) {
+        if (force) {
+          flags = chunks > 0 ? (1u << chunks) - 1u : 0u;
+        } else if (kChunks == 1) {
           flags = group_any(group, flags != 0) ? 1u : 0u;
         } else {
           flags = __reduce_or_sync(0xFFFFFFFFu, flags);
@@ -673,7 +741,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
           group_sync(group);
           flags = (of[0] | of[1]) | (of[2] | of[3]);
         }
-        if (force) flags = chunks > 0 ? (1u << chunks) - 1u : 0u;
         if (__builtin_expect(flags != 0, 0)) {
           // the rows' maxima; where one is well above m, m moves
 #pragma unroll
@@ -806,7 +873,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
           to.at = row_at * a.ld_o + (static_cast<int64_t>(p.head + lane_head) * a.group + r - token * a.group) * 128;
           if (a.lse && ok) a.lse[place] = some ? (m + log2f(den)) * 0.69314718055994531f : -INFINITY;
         } else {
-          const int64_t slot = (2 * range + (p.at - p.t0 > lo ? 1 : 0)) * a.abreast + lane_head;  // (the item begins within the range)
+          const int64_t slot = (2 * range + (p.at > lo ? 1 : 0)) * a.abreast + lane_head;  // (the item begins within the range)
           to.at = all ? (place + (is_shared(a, p.s) ? a.whole_rows : 0)) * kPart : (slot * R + in) * kPart;
           if (ok) *reinterpret_cast<float2*>((all ? w.whole : w.slots) + to.at + 128) = make_float2(m, den);
         }
@@ -874,8 +941,9 @@ __device__ __forceinline__ bool join_parts(const CachedArgs& a, const CachedWork
   const int tiles = tiles_of(sequence(a, s, start));
   if (tiles == 0) return false;
   const int rows = a.rows_of_block, block = r / rows, sub = head / a.abreast;
-  const int64_t begin = base + static_cast<int64_t>(block * (a.hkv / a.abreast) + sub) * tiles;
-  const int64_t first = range_of(begin, h), last = range_of(begin + tiles - 1, h);
+  const int64_t begin = base + static_cast<int64_t>(block * (a.hkv / a.abreast) + sub) * units_of(tiles), tile0 = begin + kItem;
+  // (within the workspace also where lengths have changed since the other kernel read them)
+  const int64_t most = h.ranges - 1, first = min(range_of(tile0, h), most), last = min(range_of(tile0 + tiles - 1, h), most);
   if (first == last) {
     if (a.shared && warp == 0) j.add(whole, lane);
     return true;
