@@ -4,7 +4,11 @@ The operators of a pre-LN block outside the sharded MLP: LayerNorm with weight a
 with bias, activation and residual, and causal attention over packed sequences with grouped heads.  The
 first two have plain functions that allocate their outputs and call the C ABI (`layer_norm_fwd`,
 `layer_norm_bwd`, `linear_fwd`, `linear_bwd`), a differentiable function (`layer_norm`, `linear`) and a
-module (`DominoLayerNorm`, `DominoLinear`); the attention (`packed_attention`) is forward only.  The operators run in the library's kernels;
+module (`DominoLayerNorm`, `DominoLinear`); the attention (`packed_attention`) is forward only.  Between the
+projection and the attention stand the norm and rotation of query and key heads (`qk_rotary_fwd`, `qk_rotary_bwd`,
+`qk_rotary`, `DominoQKRotary`); for serving, `cache_write` does the same and writes keys and values to an 8-bit cache
+(`QuantizedCache`), which `cached_attention` reads for single tokens and drafts and `cache_read` gives back in bf16 for
+`packed_attention`.  The operators run in the library's kernels;
 what PyTorch does beside them is to copy tensors that the library cannot stride over, to round the fp32 gradients of bf16
 parameters, and to take the sequences' lengths from `cu_q` where they are not given.  Tensors must be on one CUDA device,
 matrices bf16.
@@ -15,9 +19,11 @@ serves all threads; a lock is held while a call enqueues its kernels.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 import math
 import threading
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -49,6 +55,27 @@ if _take is None or _give is None:
     _take = functools.partial(lambda alloc, size, stream: alloc(size, stream=stream), _take)
 
 
+# The short way of the last section's functions (csrc/torch_calls.cpp): outputs, or None where something is not of the plain
+# form or is to be refused.  There from a device's first call on, if it could be built.
+_short = None
+
+
+def _shorten(index: int, handle: int) -> None:
+    global _short
+    try:
+        from . import torch_calls
+    except ImportError as e:
+        warnings.warn(f"calls of the rotation and the 8-bit cache take 10 us longer each: torch_calls is not there ({e})", stacklevel=4)
+        return
+    torch_calls.use_handle(index, handle)
+    if _short is None:
+        L = dm.lib()
+        torch_calls.use(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+            "domino_qk_rotary_fwd", "domino_qk_rotary_bwd", "domino_qk_rotary_bwd_workspace_size", "domino_cache_write",
+            "domino_cache_read", "domino_attn_cached_fwd", "domino_attn_cached_workspace_size")), _lock)
+        _short = torch_calls
+
+
 def _call(fn, x: torch.Tensor, *args, scratch: int | None = None) -> None:
     """fn(handle, *args, stream) on the device of `x` and its current stream, under the lock; with `scratch`, a
     workspace of so many bytes and its size follow the arguments."""
@@ -60,6 +87,7 @@ def _call(fn, x: torch.Tensor, *args, scratch: int | None = None) -> None:
         handle = _handles.get(index)
         if handle is None:
             handle = _handles[index] = dm.domino_create()
+            _shorten(index, handle)
         stream = _raw_stream(index)
         if scratch is None:
             fn(handle, *args, stream=stream)
@@ -472,8 +500,8 @@ def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, ori
     return f.to(device)
 
 
-# The functions below hand device addresses to the binding, and look at each property of a tensor once: a Grace core takes
-# 0.1 - 0.4 us for one.
+# The functions below try the short way first.  What it leaves is checked here, each property of a tensor looked at once: a Grace
+# core takes 0.1 - 0.4 us for one.
 
 def _device_index(name: str, x: torch.Tensor) -> int:
     if not isinstance(x, torch.Tensor) or x.get_device() < 0:
@@ -560,6 +588,10 @@ def qk_rotary_fwd(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tens
     or None for no rotation.  layout: "half" (value i pairs with i + len(frequencies)) or "interleaved" (2 i with 2 i + 1);
     the rotated values are multiplied by `amplitude`.  q and k may be slices of a fused projection; k may be None.  `out`:
     tensors for (q', k'), which may be q and k."""
+    if _short is not None and out is None:
+        y = _short.qk_rotary_fwd(q, k, positions, frequencies, q_weight, k_weight, LAYOUTS.get(layout, layout), eps, amplitude)
+        if y is not None:
+            return y
     index = _device_index("q", q)
     q, pq, tokens, hq, ld_q = _head_tensor("q", q, q, index)
     pk, hkv, ld_k, yk, pyk, ld_yk = None, 0, 0, None, None, 0
@@ -590,6 +622,10 @@ def qk_rotary_bwd(gq: torch.Tensor, gk: torch.Tensor | None, q: torch.Tensor | N
     """Gradients of `qk_rotary_fwd` from those of its outputs: (gq, gk, gq_weight, gk_weight), the first two bf16, the others
     fp32 (None without weights).  q and k, the forward's inputs, are needed with weights only.  `grads`, a pair of fp32
     buffers for the weights' gradients, is added to instead of allocated."""
+    if _short is not None and grads is None:
+        g = _short.qk_rotary_bwd(gq, gk, q, k, positions, frequencies, q_weight, k_weight, LAYOUTS.get(layout, layout), eps, amplitude)
+        if g is not None:
+            return g
     index = _device_index("gq", gq)
     gq, pgq, tokens, hq, ld_gyq = _head_tensor("gq", gq, gq, index)
     pgk, hkv, ld_gyk, yk, pyk = None, 0, 0, None, None
@@ -738,6 +774,10 @@ def cache_write(cache: tuple, rows: torch.Tensor, k: torch.Tensor, v: torch.Tens
     pass, which is returned (`out`: a tensor for it, which may be q).  Negative rows are not written; rows beyond the cache
     neither, and `device_status` reports them; a row must not be given twice.  No gradients."""
     _no_tangent("cache_write", q, k, v, q_weight, k_weight)
+    if _short is not None and out is None:
+        y = _short.cache_write(cache, rows, k, v, q, positions, frequencies, q_weight, k_weight, LAYOUTS.get(layout, layout), eps, amplitude)
+        if y is not None:
+            return y[0]
     if _differentiated(q, k, v, q_weight, k_weight):
         raise ValueError("cache_write has no backward: call it under torch.no_grad(), or detach its inputs")
     index = _device_index("k", k)
@@ -768,6 +808,10 @@ def cache_write(cache: tuple, rows: torch.Tensor, k: torch.Tensor, v: torch.Tens
 def cache_read(cache: tuple, rows: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """What the cache holds in the rows `rows` (int32): (k, v), each [len(rows), kv_heads, 128] in bf16, exact; zeros where a
     row is negative, or beyond the cache, which `device_status` reports.  `out`: tensors for them."""
+    if _short is not None and out is None:
+        x = _short.cache_read(cache, rows)
+        if x is not None:
+            return x
     index = _device_index("rows", rows)
     if rows.dim() != 1:
         raise ValueError("rows must be a vector")
@@ -800,6 +844,12 @@ def cached_attention(q: torch.Tensor, cache: tuple, k_start: torch.Tensor, k_len
     and `device_status` reports them.  Forward only.  Made for few tokens a sequence: for long chunks, `cache_read` and
     `packed_attention`."""
     _no_tangent("cached_attention", q)
+    if scale is None:
+        scale = HEAD_DIM ** -0.5
+    if _short is not None and out is None:
+        y = _short.cached_attention(q, cache, k_start, k_len, prefix, scale, return_lse)
+        if y is not None:
+            return y if return_lse else y[0]
     index = _device_index("q", q)
     shape = q.shape
     if len(shape) not in (3, 4) or shape[-1] != HEAD_DIM:
@@ -831,7 +881,7 @@ def cached_attention(q: torch.Tensor, cache: tuple, k_start: torch.Tensor, k_len
         _, po, _, _, ld_o = _head_tensor("out", o, q, index, tokens, copy=False)
     lse = torch.empty(shape[:-1], dtype=_F32, device=q.device) if return_lse else None
     _call(dm.domino_attn_cached_fwd, q, pq, ld_q, *codes, ld_exp, cache_rows, at_start, at_len, at_prefix,
-          HEAD_DIM ** -0.5 if scale is None else scale, po, ld_o, lse, n, t, hq, hkv,
+          scale, po, ld_o, lse, n, t, hq, hkv,
           scratch=_cached_scratch(n, t, hq, hkv, int(prefix is not None)))
     return (out, lse) if return_lse else out
 

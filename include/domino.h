@@ -424,15 +424,17 @@ DOMINO_API domino_status domino_cache_read(domino_handle handle, const uint8_t* 
  *      them.  heads is a multiple of kv_heads; query head j uses key head j / (heads / kv_heads).
  *   prefix (nullable): 2 device int32, the first row and the number of rows that every query of every sequence
  *      sees before its own keys; they are read once for all sequences.
- *   O = softmax(scale Q K^T over the keys a query sees) V, weights rounded to f16 (times their value's power of
- *      two) for the product, O once from fp32.  lse (nullable): n x t x heads fp32, the logarithm of each softmax's
- *      denominator.  A query that sees no key gets zeros and -inf.
+ *   O = softmax(scale Q K^T over the keys a query sees) V.  Queries, and weights (times their value's power of two),
+ *      enter the products as two E4M3 terms: queries good to 2^-21 of their row's largest element, weights to 2^-8 or
+ *      to 2^-18 of the row's largest.  O is rounded once from fp32.  lse (nullable): n x t x heads fp32, the logarithm
+ *      of each softmax's denominator.  A query that sees no key gets zeros and -inf.
  * Rows that a query does not see have no effect on it, whatever their codes and exponents.  Lengths are read on
  * the device: a sequence (or prefix) whose rows leave the cache has no keys and is recorded (domino_device_status).
  * Exponents are those of domino_cache_write (2^-51 to 2^51).  scale: > 0, at most 8192.  Equal inputs give equal
- * bits.  O may not overlap Q.  Any t is taken, and rows (t x heads / kv_heads) beyond 128 read the keys again.
- * Workspace: domino_attn_cached_workspace_size() bytes, without initialisation (10 or 20 MB, and with a prefix as
- * much again and 1056 bytes a query and head). */
+ * bits.  O may not overlap Q.  Any t is taken; every further 32 rows (t x heads / kv_heads, with a prefix those of all
+ * sequences together) read the keys again.
+ * Workspace: domino_attn_cached_workspace_size() bytes, without initialisation (2.6 to 10.3 MB, and with a prefix 1056
+ * bytes a query and head). */
 DOMINO_API domino_status domino_attn_cached_workspace_size(int64_t n, int64_t t, int32_t heads, int32_t kv_heads,
                                                            int32_t prefix, size_t* bytes);
 DOMINO_API domino_status domino_attn_cached_fwd(domino_handle handle, const uint16_t* Q, int64_t ld_q, const uint8_t* k8,
