@@ -742,7 +742,8 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
           flags = (of[0] | of[1]) | (of[2] | of[3]);
         }
         if (__builtin_expect(flags != 0, 0)) {
-          // the rows' maxima; where one is well above m, m moves
+          // the rows' maxima.  Where one is well above m, m moves, and with it those of its eight rows that have risen at all: what costs is
+          // the visit (1 us; 18 of 100 tiles of 48 rows over 16001 keys had one, 64.5 us, now 62.5), not the row.
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks && (flags >> c & 1u)) {
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
             const float top = fmaxf(fmaxf(sums[x], sums[kRows + x]), fmaxf(sums[2 * kRows + x], sums[3 * kRows + x]));
             Row row = rows[x];
             float2 move = make_float2(0.0f, 1.0f);
-            if (row.begun ? top > kRaise + kBehind : top > -INFINITY) {
+            if (row.begun ? top > kRaise : top > -INFINITY) {
               move = make_float2(top - kRaise, row.begun ? ex2_approx(kRaise - top) : 0.0f);
               row.base += move.x;
               row.begun = 1;
