@@ -2,8 +2,8 @@
 definitions in 64 bits.
 
 fp32 slop (in units U32 of the magnitudes): a norm's factor is a sum of 128 squares (each lane 8 + 8 in two chains, 3
-shuffles: at most 13 roundings), rsqrt (2 ulp = 4 halves) and two products: under 24; an angle is rounded to 24 bits of half a
-turn and sincospif is good to 2 ulp: under pi + 4 units of the pair's size, the rotation itself 3.  40 covers them.  The backward
+shuffles: at most 13 roundings), rsqrt (2 ulp = 4 halves) and two products: under 24; an angle's distance from a quarter turn is
+rounded to 24 bits, pi / 4 units of the pair's size at most, and sincospif is good to 2 ulp: under pi + 4, the rotation itself 3.  40 covers them.  The backward
 adds a dot product of 128 terms (19 roundings) and three products to each side: 80."""
 import pytest
 import torch
