@@ -1023,7 +1023,8 @@ cudaError_t launch_rows(const CUtensorMap& k, const CUtensorMap& v, const Cached
     if (e != cudaSuccess) return e;
     ready_of[dev].store(true, std::memory_order_release);
   }
-  const dim3 grid(static_cast<unsigned>((sms < kSms ? sms : kSms) * kBlocks));
+  const int blocks = (sms < kSms ? sms : kSms) * kBlocks;
+  const dim3 grid(static_cast<unsigned>(blocks < a.abreast ? a.abreast : blocks));  // (a range of blocks at least)
   return launch_pdl(cached_attention_kernel<R>, grid, dim3(Shape<R>::kThreads), Shape<R>::kSmem, 1, st, k, v, a, w);
 }
 

@@ -179,6 +179,47 @@ def test_autograd_module_and_accumulation(ops):
     assert none is None and x.grad is not None
 
 
+def test_offsets_beyond_32_bits(ops):
+    """Three tokens 1.2e9 elements apart in inputs and outputs."""
+    step, far = 1_200_000_000, 2_400_000_000 + 4096
+    big, out = (torch.empty(far, dtype=BF, device="cuda") for _ in range(2))
+    view = lambda t, at, h: t.as_strided((3, h, D), (step, D, 1), at)
+    q, k, pos, freq = randn(3, 16, D, seed=1), randn(3, 4, D, seed=2), torch.tensor([5, 70000, 3], dtype=torch.int32, device="cuda"), ops.rotary_frequencies(128)
+    wq, wk = randn(D, seed=3, mean=1.0), randn(D, seed=4, mean=1.0)
+    view(big, 0, 16).copy_(q), view(big, 2048, 4).copy_(k)
+    want = ops.qk_rotary_fwd(q, k, pos, freq, wq, wk)
+    got = ops.qk_rotary_fwd(view(big, 0, 16), view(big, 2048, 4), pos, freq, wq, wk, out=(view(out, 0, 16), view(out, 2048, 4)))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    got = ops.qk_rotary_bwd(*got, view(big, 0, 16), view(big, 2048, 4), pos, freq, wq, wk)
+    again = ops.qk_rotary_bwd(*ops.qk_rotary_fwd(q, k, pos, freq, wq, wk), q, k, pos, freq, wq, wk)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    cache, other = ops.QuantizedCache.empty(3, 4), ops.QuantizedCache.empty(3, 4)
+    rows = torch.arange(3, dtype=torch.int32, device="cuda")
+    y = ops.cache_write(cache, rows, view(big, 2048, 4), view(big, 2048, 4), view(big, 0, 16), pos, freq, wq, wk)
+    assert torch.equal(y, ops.cache_write(other, rows, k, k, q, pos, freq, wq, wk))
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(cache, other))
+    kk, vv = ops.cache_read(cache, rows, out=(view(out, 0, 4), view(out, 2048, 4)))
+    assert all(torch.equal(a, b) for a, b in zip((kk, vv), ops.cache_read(other, rows)))
+    device_ok()
+
+
+def test_gradients_of_one_value(ops):
+    """Gradients that are one value everywhere, without strides, and outputs of which one alone is used."""
+    q, k = randn(9, 4, D, seed=1).requires_grad_(), randn(9, 2, D, seed=2).requires_grad_()
+    m, pos = ops.DominoQKRotary(64), torch.arange(9, dtype=torch.int32, device="cuda")
+    yq, yk = m(q, k, pos)
+    yq.sum().backward()
+    want = ops.qk_rotary_bwd(torch.ones(9, 4, D, dtype=BF, device="cuda"), torch.zeros(9, 2, D, dtype=BF, device="cuda"), q.detach(), k.detach(),
+                             pos, m.frequencies, m.q_weight.detach(), m.k_weight.detach())
+    assert torch.equal(q.grad, want[0]) and not k.grad.any() and torch.equal(m.q_weight.grad, want[2].to(BF)) and not m.k_weight.grad.any()
+    with torch.no_grad():
+        assert not m(q, k, pos)[0].requires_grad
+    q.grad = None
+    x, _ = ops.qk_rotary(q, None, pos, m.frequencies, m.q_weight)
+    x.backward(torch.ones_like(x))
+    assert torch.equal(q.grad, want[0])
+
+
 def test_no_tokens(ops):
     q, freq, w = torch.empty(0, 4, D, dtype=BF, device="cuda"), ops.rotary_frequencies(128), randn(D)
     pos = torch.empty(0, dtype=torch.int32, device="cuda")
