@@ -273,8 +273,8 @@ struct __align__(16) OutRow {
 enum : int { B_FULL = 0, B_EMPTY = 8, B_Q_FULL = 16, B_S_FULL = 18, B_P_FULL = 20, B_PV_DONE = 22, B_DRAIN = 24, B_EXPS = 25,
              B_Q_EMPTY = 29, B_READY = 31, B_COUNT = 32 };
 // Control block: barriers, then 256: TMEM address, abort flag, flags of warps; 512: pieces (two items', the range's first); 1024: rows of two items; 2048: four warps'
-// maxima or sums of 32 rows; 2560: by how much m moved, and the factor for what was added up before; 3072: exponents of four tiles' keys
-constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 2048, kMovesAt = 2560, kExpsAt = 3072;
+// maxima or sums of 32 rows; 2560: by how much m moved, and the factor for what was added up before; then the exponents of four tiles' keys
+constexpr uint32_t kFlagsAt = 288, kPiecesAt = 512, kRowsAt = 1024, kSumsAt = 2048, kMovesAt = 2560, kExpsAt = kMovesAt + 512;
 constexpr uint32_t kExpTiles = 4;
 static_assert(sizeof(Piece) * 3 <= kRowsAt - kPiecesAt && 8 * B_COUNT <= 256, "control block");
 

@@ -529,12 +529,12 @@ __global__ void __launch_bounds__(kThreads, kBwdBlocks) rotary_bwd_kernel(const 
       if (left > kHeadsAbreast) {
         copy16(to + 2048u, g + kHeadsAbreast * 16 + p.ca, true);
         copy16(to + 2560u, g + kHeadsAbreast * 16 + p.cb, true);
-        copy16(to + 3072u, v + kHeadsAbreast * 16 + p.ca, true);
+        copy16(to + 3u * 1024u, v + kHeadsAbreast * 16 + p.ca, true);
         copy16(to + 3584u, v + kHeadsAbreast * 16 + p.cb, true);
       } else if (heads - (head - p.slot) > kHeadsAbreast) {  // others of the warp have a head there: zeros for the sums
         st_shared_v4(to + 2048u, 0u, 0u, 0u, 0u);
         st_shared_v4(to + 2560u, 0u, 0u, 0u, 0u);
-        st_shared_v4(to + 3072u, 0u, 0u, 0u, 0u);
+        st_shared_v4(to + 3u * 1024u, 0u, 0u, 0u, 0u);
         st_shared_v4(to + 3584u, 0u, 0u, 0u, 0u);
       }
       ahead.next(steps, split, stride, units);
