@@ -191,3 +191,20 @@ def test_no_backward_is_refused():
     for call in (lambda: ops.cache_write(cache, at, x, y), lambda: ops.cache_write(cache, at, y, x), lambda: ops.cache_write(cache, at, y, y, x)):
         with pytest.raises(ValueError, match="no backward"):
             call()
+
+
+def test_the_short_way_leaves_what_is_not_on_a_gpu():
+    """torch_calls is built beside the library; without a handle, and for tensors of the CPU, it takes nothing."""
+    from comm_overlap_gb300 import torch_calls as t
+    x, at, f = torch.zeros(4, 2, 128, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32), ops.rotary_frequencies(128, device="cpu")
+    cache = ops.QuantizedCache.empty(10, 2, device="cpu")
+    assert t.qk_rotary_fwd(x, x, at, f, None, None, 0, 1e-6, 1.0) is None
+    assert t.qk_rotary_bwd(x, x, None, None, at, f, None, None, 0, 1e-6, 1.0) is None
+    assert t.cache_write(cache, at, x, x, None, None, None, None, None, 0, 1e-6, 1.0) is None
+    assert t.cache_read(cache, at) is None and t.cached_attention(x, cache, at, at, None, 0.1, False) is None
+    for args in ((), (1, 2, 3), (None,) * 12):
+        assert t.qk_rotary_fwd(*args) is None and t.cache_read(*args) is None and t.cached_attention(*args) is None
+    with pytest.raises(TypeError):
+        t.use(1)
+    with pytest.raises(TypeError):
+        t.use_handle("device", 0)
