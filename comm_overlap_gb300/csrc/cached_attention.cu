@@ -47,6 +47,8 @@ constexpr int kJoinWarps = 8;
 constexpr uint64_t kDrainNs = 200000000ull;
 
 constexpr int kBlocks = 2;  // of an SM
+constexpr int kErrSite = 0x26 << 4;  // of the waits, in the device error word
+constexpr uint32_t kAbortAt = 260;  // in the control block
 
 // For R rows: slots of the ring (a tile of K or of V each), columns of TMEM (two buffers of scores, O).
 template <int R>
@@ -223,12 +225,13 @@ __device__ __forceinline__ bool arrived(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // mbar_wait with all but its first look out of the way: the loop over tiles is long as it is, and instructions that it passes over cost
-// it their fetching.
-__device__ __noinline__ bool arrival_awaited(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int site) {
-  return mbar_wait(bar, parity, abort_flag, err, site);
+// it their fetching and the registers of their arguments.  (The barriers lie at the start of the control block, which is aligned to 1024 bytes.)
+__device__ __noinline__ bool arrival_awaited(uint32_t bar, uint32_t parity, int site) {
+  volatile int* abort_flag = static_cast<volatile int*>(__cvta_shared_to_generic((bar & ~1023u) + kAbortAt));
+  return mbar_wait(bar, parity, abort_flag, &g_cached_err, kErrSite + site);
 }
-__device__ __forceinline__ bool arrival(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int site) {
-  return mbar_try_wait(bar, parity) || arrival_awaited(bar, parity, abort_flag, err, site);
+__device__ __forceinline__ bool arrival(uint32_t bar, uint32_t parity, int site) {
+  return mbar_try_wait(bar, parity) || arrival_awaited(bar, parity, site);
 }
 
 __device__ __forceinline__ uint16_t e4m3_of_f16(__half2 x) {
@@ -376,19 +379,17 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
   const uint32_t bar0 = smem_u32(smem), ring = bar0 + S::kCtrl, q_at = ring + kSlots * kTile, p_at = q_at + 2 * S::kOperand;
   auto bar = [bar0](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 256);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 260);
   Piece* pieces = reinterpret_cast<Piece*>(smem + kPiecesAt);
   Row* all_rows = reinterpret_cast<Row*>(smem + kRowsAt);
   float* sums = reinterpret_cast<float*>(smem + kSumsAt);
   float2* moves = reinterpret_cast<float2*>(smem + kMovesAt);
   volatile uint32_t* flags_of = reinterpret_cast<volatile uint32_t*>(smem + kFlagsAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int* err = &g_cached_err;
   if (threadIdx.x == 0) {
     for (int i = 0; i < B_COUNT; ++i)
       mbar_init(bar(i), i == B_P_FULL || i == B_P_FULL + 1 || i == B_READY ? 4 * S::kGroups : i >= B_Q_EMPTY ? 4 * S::kGroups + 1
                         : i >= B_EXPS || i == B_Q_FULL || i == B_Q_FULL + 1 ? 32 : 1);
-    *abort_flag = 0;
+    *reinterpret_cast<volatile int*>(smem + kAbortAt) = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
       mbar_arrive(bar(B_EXPS + ((made - 1) & (kExpTiles - 1))));
     };
     auto wait = [&](int b, uint32_t parity, int site) {  // the same in the whole warp
-      ok = __all_sync(0xFFFFFFFFu, ok && arrival(bar(b), parity & 1u, abort_flag, err, a.err_site + site));
+      ok = __all_sync(0xFFFFFFFFu, ok && arrival(bar(b), parity & 1u, site));
     };
     for (;; ++item) {
       for (int tile = p.t0; tile <= p.t1; ++tile) {
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     const uint64_t ring_desc = sdesc_sw128(ring, 16, 1024);
     bool ok = true;
     auto wait = [&](int b, uint32_t parity, int site) {  // the same in the whole warp
-      ok = __all_sync(0xFFFFFFFFu, ok && arrival(bar(b), parity & 1u, abort_flag, err, a.err_site + site));
+      ok = __all_sync(0xFFFFFFFFu, ok && arrival(bar(b), parity & 1u, site));
     };
     int tile = 0, tile0 = 0, tile1 = 0;
     bool more = false;
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     };
     bool ok = true;
     auto wait = [&](int b, uint32_t parity, int site) {
-      ok = arrival(bar(b), parity & 1u, abort_flag, err, a.err_site + site) && ok;
+      ok = arrival(bar(b), parity & 1u, site) && ok;
     };
     // the range's first item, by all
     {
@@ -670,29 +671,36 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     keys_any(false);
     if (warp == 2) mbar_arrive(bar(B_Q_FULL));
     uint32_t readied = 0;
-    uint32_t j = 0, slot_v = 1, round_v = 0;  // tiles so far; V's place in the ring
+    uint32_t j = 0;  // tiles so far
     for (uint32_t item = 0;; ++item) {
       wait(B_Q_FULL + (item & 1u), item >> 1, 13);
-      const Piece p = pieces[item & 1u];
-      if (keys_any(!ok) || p.t1 <= p.t0) break;  // (the same for all: nobody is left at a barrier)
-      if (item > 0 && keys_prepare<R>(a, p)) {
-        prepare_rows(a, p.s, p.len, p.head + lane_head, p.block * R, q_at + (item & 1u) * S::kOperand, all_rows + (item & 1u) * R, lane,
-                     2 * (warp - 2), 8 * S::kGroups);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_READY));
-        wait(B_READY, readied++, 14);
+      // (The rest of the piece is read again where it is needed: with two groups registers are short, and 48 sequences behind 16001 shared
+      // rows took 62.5 us with more of them held, 59 so.)
+      int tile, end, count, least;
+      {
+        const Piece p = pieces[item & 1u];
+        if (keys_any(!ok) || p.t1 <= p.t0) break;  // (the same for all: nobody is left at a barrier)
+        if (item > 0 && keys_prepare<R>(a, p)) {
+          prepare_rows(a, p.s, p.len, p.head + lane_head, p.block * R, q_at + (item & 1u) * S::kOperand, all_rows + (item & 1u) * R, lane,
+                       2 * (warp - 2), 8 * S::kGroups);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_READY));
+          wait(B_READY, readied++, 14);
+        }
+        tile = p.t0;
+        end = p.t1;
+        count = min(kRows, rows_of(a, p.s) - p.block * R - group * kRows);
+        least = is_shared(a, p.s) ? p.len : p.len - a.t + p.block * R / a.group + 1;  // keys that every row sees
       }
+      const int chunks = (count + 7) >> 3;  // (none: below 0)
       Row* rows = all_rows + (item & 1u) * R + group * kRows;
-      const int count = min(kRows, rows_of(a, p.s) - p.block * R - group * kRows), chunks = (count + 7) >> 3;  // (none: below 0)
-      const int least = is_shared(a, p.s) ? p.len : p.len - a.t + p.block * R / a.group + 1;  // keys that every row sees
       int nan_key = INT_MAX;  // the first key, of those that not all rows see, with NaN in this thread's element
       float l[kRows];
 #pragma unroll
       for (int r = 0; r < kRows; ++r) l[r] = 0.0f;
       bool force = true;  // rows without an m
 
-      for (int tile = p.t0; tile < p.t1; ++tile, ++j) {
-        const bool first = tile == p.t0;
+      for (bool first = true; tile < end; ++tile, ++j, first = false) {
         const int key0 = tile * kKeys;
         const bool tail = key0 + kKeys > least;
         wait(B_EXPS + (j & (kExpTiles - 1)), j / kExpTiles, 11);
@@ -817,17 +825,18 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
           }
         if (__builtin_expect(tail && group == 0, 0)) {
           // values past the sequence's keys count as zero, NaN included
-          wait(B_FULL + slot_v, round_v, 9);
-          const uint32_t v_at = ring + slot_v * kTile;
-          for (int r = max(p.len - key0, 0) + (x >> 3); r < kKeys; r += 16)
+          const uint32_t slot_v = (2 * j + 1) % kSlots, v_at = ring + slot_v * kTile;
+          wait(B_FULL + slot_v, (2 * j + 1) / kSlots, 9);
+          const int len = pieces[item & 1u].len;
+          for (int r = max(len - key0, 0) + (x >> 3); r < kKeys; r += 16)
             st_shared_v4(v_at + static_cast<uint32_t>(r * 128 + (x & 7) * 16), 0u, 0u, 0u, 0u);
         }
-        if (__builtin_expect(tail && least < p.len, 0)) {
+        if (__builtin_expect(tail && least < pieces[item & 1u].len, 0)) {
           // so does NaN among keys that some rows do not see, and the rows that do get it at the item's end.  (Each group looks before one
           // clears them.)
-          wait(B_FULL + slot_v, round_v, 9);
-          const uint32_t v_at = ring + slot_v * kTile;
-          const int r0 = max(least - key0, 0), r1 = min(p.len - key0, kKeys);
+          const uint32_t slot_v = (2 * j + 1) % kSlots, v_at = ring + slot_v * kTile;
+          wait(B_FULL + slot_v, (2 * j + 1) / kSlots, 9);
+          const int r0 = max(least - key0, 0), r1 = min(pieces[item & 1u].len - key0, kKeys);
           auto place = [&](int r) { return v_at + static_cast<uint32_t>(r * 128 + (((me >> 4) ^ (r & 7)) << 4) + (me & 15)); };
           auto is_nan = [&](int r) {
             uint32_t code;
@@ -845,11 +854,6 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_P_FULL + (j & 1u)));
-        slot_v += 2;
-        if (slot_v >= kSlots) {
-          slot_v -= kSlots;
-          ++round_v;
-        }
       }
 
       // ---- what the piece's keys came to
@@ -858,6 +862,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         if ((lane & (32 / kRows - 1)) == 0) sums[(warp & 3) * kRows + lane / (32 / kRows)] = sum;
       }
       group_sync(group);
+      const Piece p = pieces[item & 1u];
       const bool all = p.t0 == 0 && p.t1 == p.tiles, out = all && a.shared == 0;
       if (x < count) {
         const float den = (sums[x] + sums[kRows + x]) + (sums[2 * kRows + x] + sums[3 * kRows + x]);

@@ -257,7 +257,6 @@ struct CachedArgs {
   int32_t abreast;                       // neighbouring key heads that blocks take at the same time
   int32_t n, t, hq, hkv, group, cache_rows, shared;  // query i of t sees k_len - t + i + 1 keys; shared: 1 with a prefix
   float scale_log2;                      // scale x log2(e)
-  int32_t err_site;
 };
 // Maps of codes, 128-byte swizzle: (128, hkv, cache_rows) in boxes (128, 1, kCachedKeys).
 constexpr int kCachedKeys = 128;

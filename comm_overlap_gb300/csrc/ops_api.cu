@@ -769,7 +769,6 @@ domino_status domino_attn_cached_fwd(domino_handle H, const uint16_t* Q, int64_t
     a.ld_exp = ld_exp;
     a.cache_rows = int32_t(cache_rows);
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.err_site = 0x26 << 4;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     DM_TRY(dm::launch_on(H, DOMINO_K_ATTN_CACHED, st, "cached attention launch",
                          [&] { return dm::launch_cached_attention(mk, mv, a, workspace, op_sms(H), st); }));
