@@ -14,7 +14,7 @@
 // the nearest quarter turn goes to sincospif.
 //
 // Bound: memory.  Forward 4 bytes a value, backward 6 (4 without norm), cache 3.  16384 tokens of 32 query and 8 key heads with norm: forward
-// 57.4 us (5.8 TB/s, as a copy of the same bytes; 69 with loads into registers a step ahead), backward 94 (5.3), into the cache 64.6 (369 MB, 5.7);
+// 57.4 us (5.8 TB/s, as a copy of the same bytes; 69 with loads into registers a step ahead), backward 86 (5.9), into the cache 64.6 (369 MB, 5.7);
 // 147456 rows of 8 heads read back 141.6 (906 MB, 6.4).
 #include <atomic>
 
@@ -696,9 +696,13 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const CacheReadArgs a) 
 }
 
 // Two kinds of blocks with so many steps a token each: by their steps, at most sms x blocks_of_sm altogether; one warp takes a token's
-// steps, or with few tokens as many as fill the GPU.
-RotaryShares shares_of(int64_t tokens, int steps0, int steps1, int sms, int blocks_of_sm) {
+// steps, or with few tokens as many as fill the GPU.  Both kinds should end together.  Backward both compute a token's angles, which counts as
+// `more` halves of a step (16384 tokens of 32 query and 8 key heads 86 us; 96 without, 89 with a quarter, 88 with three).  Into the cache
+// values go through the tokens beside the queries and keys of the same rows, by their steps alone: 65 us, with a tenth more or fewer
+// blocks 67 - 71.
+RotaryShares shares_of(int64_t tokens, int steps0, int steps1, int more, int sms, int blocks_of_sm) {
   const int steps[2] = {steps0, steps1}, most = sms * blocks_of_sm;
+  const int cost0 = steps0 ? 2 * steps0 + more : 0, cost1 = steps1 ? 2 * steps1 + more : 0;
   RotaryShares s = {};
   int left = most;
   for (int i = 1; i >= 0; --i) {
@@ -706,7 +710,7 @@ RotaryShares shares_of(int64_t tokens, int steps0, int steps1, int sms, int bloc
     const int64_t want = (int64_t(sms) * 16 + tokens - 1) / tokens;
     s.split[i] = static_cast<int>(want > steps[i] ? steps[i] : want);
     const int64_t units = (tokens * s.split[i] + kWarps - 1) / kWarps;
-    int share = i == 0 ? left : static_cast<int>((int64_t(most) * steps1 + (steps0 + steps1) / 2) / (steps0 + steps1));
+    int share = i == 0 ? left : static_cast<int>((int64_t(most) * cost1 + (cost0 + cost1) / 2) / (cost0 + cost1));
     if (share < 1) share = 1;
     if (i == 1 && steps0 > 0 && share >= most) share = most - 1;
     s.blocks[i] = static_cast<int>(units < share ? units : share);
@@ -727,10 +731,10 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<bool> (&ready)
 }
 
 RotaryShares fwd_shares(int64_t tokens, int hq, int hkv, bool values, int sms) {
-  return shares_of(tokens, steps_of(hq) + steps_of(hkv), values ? steps_of(hkv) : 0, sms, values ? kWriteBlocks : kFwdBlocks);
+  return shares_of(tokens, steps_of(hq) + steps_of(hkv), values ? steps_of(hkv) : 0, 0, sms, values ? kWriteBlocks : kFwdBlocks);
 }
 RotaryShares bwd_shares(int64_t tokens, int hq, int hkv, int sms) {
-  return shares_of(tokens, steps_of(hq), steps_of(hkv), sms, kBwdBlocks);
+  return shares_of(tokens, steps_of(hq), steps_of(hkv), 1, sms, kBwdBlocks);
 }
 
 template <bool NORM, bool HALF, bool CACHE>
