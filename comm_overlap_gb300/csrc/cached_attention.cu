@@ -7,16 +7,19 @@
 //
 // Both products are transposed: a tile of 128 keys is the tensor core's 128 rows (S^T = K Q^T), then the 128 elements are (O^T = V^T
 // P^T), so that codes go from memory to the tensor core as they are and few queries make a narrow product.  The narrow operand is a
-// sum of two E4M3 terms, x1 + x2 / 16, in columns of their own: x1 is x rounded, x2 the rest.  For q, scaled by a power of two for
-// each row so that its largest value lies in [2^7, 2^8), they are exact down to 2^-14 of the largest, and off by at most 2^-21 of it
-// below.  For w, which is at most 448, they are good to 2^-8, as bf16 would be, or to 2^-18 of the row's largest weight.
+// sum of terms of 8 bits in columns of their own.  q, scaled by a power of two for each row so that its largest value lies in [2^7,
+// 2^8), is x1 + x2 / 16 in E4M3, x1 rounded and x2 the rest: exact down to 2^-14 of the largest, off by at most 2^-21 of it below.
+// w is y1 + y2 / 8 + y3 / 32 in E5M2, three bits of fp16's eleven each: good to 2^-8, as bf16 would be, down to 2^-13, and to 2^-21.8
+// below, 2^-30.8 of the row's largest weight.  (A key with most of the weight may stand before very many with 2^-20 of it each, which
+// count together: two E4M3 terms, good to 2^-18 of the largest, lost 262143 keys 13 nats below the first, 8 % of O.)
 // (With mma.sync, 8 rows a warp, codes have to be converted to f16, 3 - 4 clocks for two: one sequence of 262001 keys and 8 heads
 // 130 us; its E4M3 form converts them too, 175.)
 //
-// A row is a token and one of the `group` query heads of a key head; R of them make 2 R columns, for each 8 rows the first terms, then
-// the second.  Warps of a block: one loads K and V by TMA into a ring, one issues the products, and four for each 16 rows hold the 128
-// keys (then elements), one a thread, which TMEM lane by lane suits: no sums across threads but at an item's end.  (What an item
-// needs once is kept short: instructions that run once come from memory each time.)
+// A row is a token and one of the `group` query heads of a key head; R of them make 2 R columns of scores, for each 8 rows the first
+// terms, then the second, and 3 R of O, for each 16 rows (or the only 8) one term after the other.  Warps of a block: one loads K and
+// V by TMA into a ring, one issues the products, and four for each 16 rows hold the 128 keys (then elements), one a thread, which TMEM
+// lane by lane suits: no sums across threads but at an item's end.  (What an item needs once is kept short: instructions that run once
+// come from memory each time.)
 //
 // The tiles of all sequences, laid end to end, are cut into equal ranges, one for each group of `abreast` blocks, which take
 // neighbouring key heads and so read a row's heads at about the same time.  What covers all keys of a row is written out; parts leave
@@ -55,19 +58,21 @@ template <int R>
 struct Shape {
   static constexpr int kRows = R < 16 ? R : 16, kGroups = R / kRows;  // groups of 128 threads that hold keys, and the rows of each
   static constexpr int kThreads = 64 + 128 * kGroups;                 // warps: 0 loads, 1 issues, from 2 on keys
-  static constexpr uint32_t kSlots = R == 8 ? 6 : R == 16 ? 5 : 4;
-  static constexpr uint32_t kCols = 2 * R;
+  static constexpr uint32_t kSlots = R < 32 ? 5 : 4;                  // (six for 8 rows: 64 sequences of up to 8000 keys 98 us, five 92)
+  static constexpr uint32_t kCols = 2 * R, kTerms = kRows;            // columns of scores; of one term of a group's O
+  static constexpr uint32_t kOutCols = R == 8 ? 32 : 3 * R;           // of O (a product has a multiple of 16: 8 unused)
   static constexpr uint32_t kTmem = R == 8 ? 64 : R == 16 ? 128 : 256;
-  static constexpr uint32_t kOperand = kCols * 128;  // bytes of Q or P, two buffers each
-  static constexpr uint32_t kCtrl = 4096;            // control block
-  static constexpr int kSmem = 1024 + static_cast<int>(kCtrl + kSlots * kTile + 4 * kOperand);
-  static_assert(kBlocks * (kSmem + 1024 + 512) <= 233472 && 3 * kCols <= kTmem && kBlocks * kTmem <= 512, "memory of an SM");
+  static constexpr uint32_t kOperand = kCols * 128, kWeights = kOutCols * 128;  // bytes of Q and of P, two buffers each
+  static constexpr uint32_t kCtrl = 4096;                                       // control block
+  static constexpr int kSmem = 1024 + static_cast<int>(kCtrl + kSlots * kTile + 2 * kOperand + 2 * kWeights);
+  static_assert(kBlocks * (kSmem + 1024 + 512) <= 233472 && 2 * kCols + kOutCols <= kTmem && kBlocks * kTmem <= 512, "memory of an SM");
 };
 // Weights are 2^kRaise where t is the maximum that m was taken from; the maximum may rise by kBehind (in base 2) before O and the
-// denominator are brought to a new m, so that they stay below E4M3's 448 = 2^8.807.  (With 6 and 2.8 m moved in nearly every tile of 64
-// rows.)
-constexpr float kRaise = 4.0f, kBehind = 4.8f;
-constexpr float kTerm = 0.0625f;  // of the second terms
+// denominator are brought to a new m, so that they stay below E5M2's 57344 = 2^15.807.  (With less to rise m moves more often, at 1 us a
+// time; with a lower start more of the small weights is lost.)
+constexpr float kRaise = 9.0f, kBehind = 6.75f;
+constexpr float kTerm = 0.0625f;                      // of q's second terms
+constexpr float kSecond = 0.125f, kThird = 0.03125f;  // of the weights' terms
 
 // ---- work: tiles of all items (sequence, block of rows, `abreast` key heads) in order.  What an item costs beside its tiles counts as
 // kItem of them, before its first: units.  (16 sequences of up to 3001 keys, 35 rows each for 4 heads: 32.3 us without, 29.7 so, 29.8 with
@@ -164,7 +169,7 @@ __device__ __forceinline__ bool next_piece(const CachedArgs& a, Piece& p, int64_
 
 // ---- instructions
 
-// D[tmem] (+)= A . B^T, E4M3 operands in shared memory, fp32 accumulator, 32 of the reduction.
+// D[tmem] (+)= A . B^T, operands of 8 bits in shared memory, fp32 accumulator, 32 of the reduction.
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -173,6 +178,7 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+constexpr uint32_t kE5m2Columns = 1u << 10;  // of the instruction's descriptor: B's format
 // Descriptor of an operand without swizzle whose rows along the reduction are pieces of 16 bytes (16 columns), one after the other; the
 // next 16 columns `stride` bytes further.  (8 rows of 16 bytes are a unit; bits 16 - 29: the distance of units along the reduction, bits
 // 32 - 45: along the columns.)
@@ -189,13 +195,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // A tile of codes to shared memory, the first to leave L2 again: they are read once, or by blocks that run at about the same time (64
 // sequences of up to 8000 keys 98.8 us, 100.4 without).
@@ -265,6 +274,21 @@ __device__ __forceinline__ void two_terms(float x, float y, uint32_t& first, uin
   first = f;
   second = e4m3_of_f16(__hmul2(__hsub2(v, f16_of_e4m3(f)), __float2half2_rn(16.0f)));
 }
+// The three terms of weights x and y (at most 2^15.75; fp16's upper byte is the E5M2 value next to zero): the first two in the upper
+// bytes of the halves, the third, rounded, in two bytes.  All but the two roundings is exact.  NaN stays in the first.
+__device__ __forceinline__ void three_terms(float x, float y, uint32_t& first, uint32_t& second, uint16_t& third) {
+  auto upper = [](uint32_t v) {
+    v &= 0xFF00FF00u;
+    return *reinterpret_cast<const __half2*>(&v);
+  };
+  const __half2 v = __floats2half2_rn(x, y);
+  first = *reinterpret_cast<const uint32_t*>(&v);
+  const __half2 rest = __hmul2(__hsub2(v, upper(first)), __float2half2_rn(8.0f));
+  second = *reinterpret_cast<const uint32_t*>(&rest);
+  const __half2 last = __hmul2(__hsub2(rest, upper(second)), __float2half2_rn(4.0f));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(third) : "r"(*reinterpret_cast<const uint32_t*>(&last)));
+}
+__device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
 // A byte of a list that is read on from there: memory brings 128 bytes at a time to L2, not 32.
 __device__ __forceinline__ int load_line(const uint8_t* p) {
   uint32_t x;
@@ -628,8 +652,10 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
       wait(B_FULL + slot_v, round_v, 5);
       tc_fence_after();
       if (ok && one) {
-        const uint32_t id = idesc_e4m3_f32(128, static_cast<int>(mine & 0xFFFFu), true, true);
-        const uint64_t dv = ring_desc + ((slot_v * kTile) >> 4), dp = sdesc_pieces(p_at + (j & 1u) * S::kOperand, kKeys * 16);
+        // (groups of 16 rows; scores have 16 columns for 8)
+        const uint32_t out_columns = S::kGroups > 1 && (mine & 0xFFFFu) <= 32 ? S::kOutCols / S::kGroups : S::kOutCols;
+        const uint32_t id = idesc_e4m3_f32(128, static_cast<int>(out_columns), true, true) | kE5m2Columns;
+        const uint64_t dv = ring_desc + ((slot_v * kTile) >> 4), dp = sdesc_pieces(p_at + (j & 1u) * S::kWeights, kKeys * 16);
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k)
           umma_f8(tmem + 2 * S::kCols, dv + k * (4096u >> 4), dp + k * (512u >> 4), id, !(mine >> 31 && k == 0));
@@ -655,6 +681,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
     // nothing.
     const int group = (threadIdx.x - 64) >> 7, x = (threadIdx.x - 64) & 127, quarter = (warp & 3) * 32, me = quarter + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter) << 16) + static_cast<uint32_t>(group * 2 * kRows);
+    const uint32_t out_lanes = lanes + 2 * S::kCols + static_cast<uint32_t>(group * kRows);  // (three terms of its rows, where scores have two)
     sums += group * 4 * kRows;
     moves += group * kRows;
     flags_of += group * 4;
@@ -808,36 +835,51 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
 #pragma unroll 1
           for (int c = 0; c < chunks && !first; ++c)
             if (flags >> c & 1u) {
-              uint32_t y[16];
-              tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
-              tmem_ld_wait();
+#pragma unroll 1
+              for (uint32_t at = out_lanes + 8u * c; at < out_lanes + 3 * S::kTerms; at += S::kTerms) {
+                uint32_t y[8];
+                tmem_ld8(at, y);
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float f = moves[8 * c + i].y;
-                y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-                y[8 + i] = __float_as_uint(__uint_as_float(y[8 + i]) * f);
+                for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * moves[8 * c + i].y);
+                tmem_st8(at, y);
               }
-              tmem_st16(lanes + 2 * S::kCols + 16u * c, y);
             }
           if (!first) tmem_st_wait();
         }
-        // weights, in two terms: 16 bytes a key for 8 rows
+        // weights, in three terms: 16 bytes a key and term for 16 rows, or for 8 the first two together
         if (j >= 2) wait(B_PV_DONE + (j & 1u), (j - 2) >> 1, 8);
-        const uint32_t to = p_at + (j & 1u) * S::kOperand + static_cast<uint32_t>(group * kChunks) * (kKeys * 16u) + static_cast<uint32_t>(me) * 16u;
+        const uint32_t to = p_at + (j & 1u) * S::kWeights + static_cast<uint32_t>(group) * (3u * kKeys * 16u) + static_cast<uint32_t>(me) * 16u;
+        if (chunks > 0) {
+          uint32_t term[3][4] = {};
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (c < chunks) {
-            uint32_t one[4], two[4];
+          for (int c = 0; c < kChunks; ++c)
+            if (c < chunks) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 8 * c + 2 * i;
-              const float w0 = ex2_approx(d[r]), w1 = ex2_approx(d[r + 1]);
-              l[r] = fmaf(w0, unbias, l[r]);
-              l[r + 1] = fmaf(w1, unbias, l[r + 1]);
-              two_terms(w0, w1, one[i], two[i]);
+              for (int i = 0; i < 2; ++i) {  // four rows
+                uint32_t one[2], two[2];
+                uint16_t three[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int r = 8 * c + 4 * i + 2 * h;
+                  const float w0 = ex2_approx(d[r]), w1 = ex2_approx(d[r + 1]);
+                  l[r] = fmaf(w0, unbias, l[r]);
+                  l[r + 1] = fmaf(w1, unbias, l[r + 1]);
+                  three_terms(w0, w1, one[h], two[h], three[h]);
+                }
+                term[0][2 * c + i] = upper_bytes(one[0], one[1]);
+                term[1][2 * c + i] = upper_bytes(two[0], two[1]);
+                term[2][2 * c + i] = static_cast<uint32_t>(three[0]) | static_cast<uint32_t>(three[1]) << 16;
+              }
             }
-            st_shared_v4(to + c * (kKeys * 16u), one[0] | one[1] << 16, one[2] | one[3] << 16, two[0] | two[1] << 16, two[2] | two[3] << 16);
+          if (kChunks == 1) {
+            st_shared_v4(to, term[0][0], term[0][1], term[1][0], term[1][1]);
+            st_shared_v4(to + kKeys * 16u, term[2][0], term[2][1], 0u, 0u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) st_shared_v4(to + k * (kKeys * 16u), term[k][0], term[k][1], term[k][2], term[k][3]);
           }
+        }
         if (__builtin_expect(tail && group == 0, 0)) {
           // values past the sequence's keys count as zero, NaN included
           const uint32_t slot_v = (2 * j + 1) % kSlots, v_at = ring + slot_v * kTile;
@@ -906,14 +948,16 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
       float* parts = all ? w.whole : w.slots;
 #pragma unroll 1
       for (int c = 0; c < chunks; ++c) {
-        uint32_t y[16];
-        tmem_ld16(lanes + 2 * S::kCols + 16u * c, y);
+        uint32_t y[3][8];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) tmem_ld8(out_lanes + k * S::kTerms + 8u * c, y[k]);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (8 * c + i >= count || !ok) break;
           const OutRow to = *reinterpret_cast<const OutRow*>(rows + 8 * c + i);
-          const float o = to.limit > nan_key ? NAN : fmaf(__uint_as_float(y[8 + i]), kTerm, __uint_as_float(y[i])) * to.factor;
+          const float sum = fmaf(__uint_as_float(y[2][i]), kThird, fmaf(__uint_as_float(y[1][i]), kSecond, __uint_as_float(y[0][i])));
+          const float o = to.limit > nan_key ? NAN : sum * to.factor;
           if (out)
             a.O[to.at + me] = static_cast<uint16_t>(pack_bf16x2(o, 0.0f));
           else

@@ -424,10 +424,11 @@ DOMINO_API domino_status domino_cache_read(domino_handle handle, const uint8_t* 
  *      them.  heads is a multiple of kv_heads; query head j uses key head j / (heads / kv_heads).
  *   prefix (nullable): 2 device int32, the first row and the number of rows that every query of every sequence
  *      sees before its own keys; they are read once for all sequences.
- *   O = softmax(scale Q K^T over the keys a query sees) V.  Queries, and weights (times their value's power of two),
- *      enter the products as two E4M3 terms: queries good to 2^-21 of their row's largest element, weights to 2^-8 or
- *      to 2^-18 of the row's largest.  O is rounded once from fp32.  lse (nullable): n x t x heads fp32, the logarithm
- *      of each softmax's denominator.  A query that sees no key gets zeros and -inf.
+ *   O = softmax(scale Q K^T over the keys a query sees) V.  Queries enter the products as two E4M3 terms, good to
+ *      2^-21 of their row's largest element; weights (times their value's power of two) as three E5M2 terms, each good
+ *      to 2^-8 of itself, or to 2^-30 of the row's largest: of O, n keys lose at most 2^-8 of sum w |v|, and n 2^-30 of
+ *      the largest term.  O is rounded once from fp32.  lse (nullable): n x t x heads fp32, the logarithm of each
+ *      softmax's denominator.  A query that sees no key gets zeros and -inf.
  * Rows that a query does not see have no effect on it, whatever their codes and exponents.  Lengths are read on
  * the device: a sequence (or prefix) whose rows leave the cache has no keys and is recorded (domino_device_status).
  * Exponents are those of domino_cache_write (2^-51 to 2^51).  scale: > 0, at most 8192.  Equal inputs give equal
