@@ -427,7 +427,7 @@ DOMINO_API domino_status domino_cache_read(domino_handle handle, const uint8_t* 
  *   O = softmax(scale Q K^T over the keys a query sees) V.  Queries enter the products as two E4M3 terms, good to
  *      2^-21 of their row's largest element; weights (times their value's power of two) as three E5M2 terms, each good
  *      to 2^-8 of itself, or to 2^-30 of the row's largest: of O, n keys lose at most 2^-8 of sum w |v|, and n 2^-30 of
- *      the largest term.  O is rounded once from fp32.  lse (nullable): n x t x heads fp32, the logarithm of each
+ *      the largest term (where a value of zeros counts as one of 2^-51).  O is rounded once from fp32.  lse (nullable): n x t x heads fp32, the logarithm of each
  *      softmax's denominator.  A query that sees no key gets zeros and -inf.
  * Rows that a query does not see have no effect on it, whatever their codes and exponents.  Lengths are read on
  * the device: a sequence (or prefix) whose rows leave the cache has no keys and is recorded (domino_device_status).

@@ -1,4 +1,5 @@
-"""Attention over the 8-bit cache where the softmax's weights differ widely: one key that holds most of them before a long rest.
+"""Attention over the 8-bit cache where the softmax's weights differ widely: one key that holds most of them before a long rest, and
+rows whose value is zero.
 
 The bound is one of an attention whose weights are rounded, each for itself: with p the weights in 64 bits, O is off by its own rounding
 to bf16, 2^-8 |O|, and by sum_j p_j |v_j| times
@@ -136,3 +137,55 @@ def test_one_key_of_the_shared_rows(ops, shape, share):
     k, v = randn(n + own, hkv, D, seed=2).float(), randn(n + own, hkv, D, seed=3).float() + 0.5
     k[3] = u * (math.log(n * math.exp(0.5) * share / (1 - share)) / math.sqrt(D))
     check(ops, queries(count, t, hq, u), filled(ops, k, v), n, own, (0, n))
+
+
+@pytest.mark.parametrize("gap", [0.0, 3.0, 5.0, 8.0, 30.0])
+@pytest.mark.parametrize("size", [1.0, 0.05, 1e-4])
+@pytest.mark.parametrize("place", ["first", "middle", "last"])
+def test_a_row_without_value(ops, place, size, gap):
+    """A key whose value is zero, so many nats above the others, takes from the others' weight and adds nothing, whatever their size."""
+    n, u = 1000, signs(1)
+    for count, t, hq, hkv in ((2, 1, 4, 2), (1, 2, 16, 2), (40, 3, 32, 8)):
+        k, v = randn(n, hkv, D, seed=2).float(), (randn(n, hkv, D, seed=3).float() + 0.5) * size
+        at = dict(first=0, middle=n // 2, last=n - 1)[place]
+        k[at], v[at] = u * (gap / math.sqrt(D)), 0
+        check(ops, queries(count, t, hq, u), filled(ops, k, v), 0, n)
+
+
+def test_a_row_without_value_in_a_long_range(ops):
+    for n, gap in ((8192, 8.0), (8192, 9.0), (100000, 12.0)):
+        u = signs(1)
+        k, v = randn(n, 1, D, seed=2).float(), randn(n, 1, D, seed=3).float() + 0.5
+        k[0], v[0] = u * (gap / math.sqrt(D)), 0
+        check(ops, queries(310, 1, 4, u), filled(ops, k, v), 0, n)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 4, 2), (3, 2, 16, 2), (48, 1, 32, 8)], ids=str)
+def test_rows_left_empty(ops, shape):
+    """Rows of the cache that nothing was written to, among small values; also in front of others and shared."""
+    count, t, hq, hkv = shape
+    n, u = 3001, signs(1)
+    k, v = randn(n, hkv, D, seed=2).float(), (randn(n, hkv, D, seed=3).float() + 0.5) * 1e-3
+    empty = torch.rand(n, generator=torch.Generator().manual_seed(5)) < 0.3
+    empty[:200] = True
+    k[empty], v[empty] = 0, 0
+    check(ops, queries(count, t, hq, u), filled(ops, k, v), 0, n)
+    check(ops, queries(count, t, hq, u), filled(ops, k, v), 2000, 1001, (0, 2000))
+    v[:] = 0
+    check(ops, queries(count, t, hq, u), filled(ops, k, v), 0, n)
+
+
+def test_a_row_of_zeros_and_nan(ops):
+    """A value of zeros and a NaN is NaN there, and elsewhere as one of zeros."""
+    n, u = 1000, signs(1)
+    for count, t, hq, hkv in ((2, 1, 4, 2), (40, 3, 32, 8)):
+        k, v = randn(n, hkv, D, seed=2).float(), (randn(n, hkv, D, seed=3).float() + 0.5) * 0.01
+        k[100], v[100] = u * (5 / math.sqrt(D)), 0
+        q, one = queries(count, t, hq, u), torch.ones(count, dtype=torch.int32, device="cuda")
+        want = ops.cached_attention(q, filled(ops, k, v), 0 * one, n * one)
+        v[100, :, 7] = float("inf")
+        got = ops.cached_attention(q, filled(ops, k, v), 0 * one, n * one)
+        assert got[..., 7].isnan().all()
+        got[..., 7] = want[..., 7]
+        assert torch.equal(got, want)
+    device_ok()
