@@ -10,8 +10,8 @@
 // lane keeps one kind's weight and sums in registers.
 //
 // Angles: a position turns pair i by position x frequency.  The frequency is kept as a 64-bit fraction of a turn, so the
-// product's low 64 bits are the angle's fraction of a turn without any rounding by the position's size; what its upper 32 bits are off
-// the nearest quarter turn goes to sincospif.
+// product's low 64 bits are the angle's fraction of a turn without any rounding by the position's size; what they are off the
+// nearest quarter turn goes to sincospif.
 //
 // Bound: memory.  Forward 4 bytes a value, backward 6 (4 without norm), cache 3.  16384 tokens of 32 query and 8 key heads with norm: forward
 // 57.4 us (5.8 TB/s, as a copy of the same bytes; 69 with loads into registers a step ahead), backward 86 (5.9), into the cache 64.6 (369 MB, 5.7);
@@ -92,10 +92,10 @@ __device__ __forceinline__ void token_angles(float* cosines, float* sines, const
     const int i = lane + 32 * k;
     if (i < (rot >> 1)) {
       const unsigned long long at = turns[i] * static_cast<unsigned long long>(static_cast<long long>(position));
-      // the nearest quarter turn, and the rest, which is small enough to keep its digits in fp32
-      const uint32_t turn = static_cast<uint32_t>(at >> 32), quarter = (turn + 0x20000000u) >> 30;
+      // the nearest quarter turn, and the rest, all of its 64 bits: an angle next to a quarter turn (or to none) keeps fp32's digits for itself
+      const uint32_t quarter = static_cast<uint32_t>((at + (1ull << 61)) >> 62);
       float x, y;
-      sincospif(static_cast<float>(static_cast<int>(turn - (quarter << 30))) * 0x1p-31f, &y, &x);
+      sincospif(static_cast<float>(static_cast<long long>(at - (static_cast<unsigned long long>(quarter) << 62))) * 0x1p-63f, &y, &x);
       const float cs = quarter & 1 ? (quarter & 2 ? y : -y) : (quarter & 2 ? -x : x);
       const float sn = quarter & 1 ? (quarter & 2 ? -x : x) : (quarter & 2 ? -y : y);
       cosines[i] = cs * amplitude;

@@ -367,7 +367,8 @@ DOMINO_API domino_status domino_attn_packed_fwd(domino_handle handle, const uint
  *   Q, Yq: tokens x heads x 128, K, Yk: tokens x kv_heads x 128 (kv_heads = 0: no keys), row strides ld_* in
  *   elements (multiples of 8), so that Q and K may be slices of a fused projection; Yq may be Q and Yk K,
  *   with the same strides.  positions: tokens int32 (any value); frequencies: rot / 2 doubles, radians a
- *   position, both on the device.  Angles are exact to fp32 whatever the position. */
+ *   position, both on the device.  Cosines and sines are good to fp32, each to its own size, for the frequency as a
+ *   multiple of 2^-64 turns, which takes it to 53 bits: an angle is off by at most 2^-52 of itself and |position| 2^-62. */
 typedef enum { DOMINO_ROTARY_HALF = 0, DOMINO_ROTARY_INTERLEAVED = 1 } domino_rotary_layout;
 DOMINO_API domino_status domino_qk_rotary_fwd(domino_handle handle, const uint16_t* Q, int64_t ld_q, const uint16_t* K,
                                               int64_t ld_k, const int32_t* positions, const double* frequencies,
