@@ -66,6 +66,19 @@ __device__ __forceinline__ unsigned long long turn_fraction(double f) {
   return __double2ull_rn(t * 18446744073709551616.0);
 }
 
+// The rotated pairs' turns a position, and 1 for each (NaN for a frequency that is not finite), by the first rot / 2 threads.
+struct Turns {
+  unsigned long long of[64];
+  float one[64];
+  __device__ __forceinline__ void load(const double* frequencies, int rot) {
+    const int i = static_cast<int>(threadIdx.x);
+    if (i >= (rot >> 1)) return;
+    const double f = frequencies[i];
+    of[i] = turn_fraction(f);
+    one[i] = f - f == 0.0 ? 1.0f : NAN;
+  }
+};
+
 // The lanes' places in a head: pieces ca and cb, and whether they are rotated.
 struct Place {
   int slot, j, ca, cb;
@@ -84,22 +97,23 @@ __device__ __forceinline__ Place place_of(int lane, int rot) {
 
 // Cosines and sines of a token's angles, times the amplitude (and sines times `sign`), computed by the warp's lanes, two pairs each,
 // to shared memory (64 of each a warp).
-__device__ __forceinline__ void token_angles(float* cosines, float* sines, const unsigned long long* turns, int position, int rot,
-                                             float amplitude, float sign, int lane) {
+__device__ __forceinline__ void token_angles(float* cosines, float* sines, const Turns& turns, int position, int rot, float amplitude,
+                                             float sign, int lane) {
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int i = lane + 32 * k;
     if (i < (rot >> 1)) {
-      const unsigned long long at = turns[i] * static_cast<unsigned long long>(static_cast<long long>(position));
+      const unsigned long long at = turns.of[i] * static_cast<unsigned long long>(static_cast<long long>(position));
       // the nearest quarter turn, and the rest, all of its 64 bits: an angle next to a quarter turn (or to none) keeps fp32's digits for itself
       const uint32_t quarter = static_cast<uint32_t>((at + (1ull << 61)) >> 62);
       float x, y;
       sincospif(static_cast<float>(static_cast<long long>(at - (static_cast<unsigned long long>(quarter) << 62))) * 0x1p-63f, &y, &x);
       const float cs = quarter & 1 ? (quarter & 2 ? y : -y) : (quarter & 2 ? -x : x);
       const float sn = quarter & 1 ? (quarter & 2 ? -x : x) : (quarter & 2 ? -y : y);
-      cosines[i] = cs * amplitude;
-      sines[i] = sn * (amplitude * sign);
+      const float size = amplitude * turns.one[i];
+      cosines[i] = cs * size;
+      sines[i] = sn * (size * sign);
     }
   }
   __syncwarp();
@@ -308,14 +322,14 @@ template <bool NORM, bool HALF, bool CACHE>
 __global__ void __launch_bounds__(kThreads, CACHE ? kWriteBlocks : kFwdBlocks) rotary_kernel(const RotaryArgs a, const RotaryShares shares) {
   constexpr int kDepth = CACHE ? kWriteDepth : kFwdDepth;
   extern __shared__ __align__(16) uint8_t ring_all[];  // of each warp, kDepth steps of 2048 bytes
-  __shared__ unsigned long long turns[64];
+  __shared__ Turns turns;
   __shared__ __align__(16) float cosines[kWarps][64], sines[kWarps][64];
   pdl_launch();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool value = CACHE && static_cast<int>(blockIdx.x) >= shares.blocks[0];  // blocks of values come after the others
   const int place = static_cast<int>(blockIdx.x) - (value ? shares.blocks[0] : 0), split = shares.split[value];
-  if (!value && static_cast<int>(threadIdx.x) < (a.rot >> 1)) turns[threadIdx.x] = turn_fraction(a.frequencies[threadIdx.x]);
+  if (!value) turns.load(a.frequencies, a.rot);
   __syncthreads();
   const Place p = place_of(lane, a.rot);
   // steps of a token: of queries, then keys (or of values alone)
@@ -485,12 +499,12 @@ __global__ void __launch_bounds__(kThreads, CACHE ? kWriteBlocks : kFwdBlocks) r
 template <bool HALF>
 __global__ void __launch_bounds__(kThreads, kBwdBlocks) rotary_bwd_kernel(const RotaryBwdArgs a, float* part, const RotaryShares shares) {
   extern __shared__ __align__(16) uint8_t ring_all[];  // of each warp, kBwdDepth steps of 4096 bytes
-  __shared__ unsigned long long turns[64];
+  __shared__ Turns turns;
   __shared__ __align__(16) float cosines[kWarps][64], sines[kWarps][64];
   __shared__ float sums[kWarps][128];
   pdl_launch();
   pdl_wait();
-  if (static_cast<int>(threadIdx.x) < (a.rot >> 1)) turns[threadIdx.x] = turn_fraction(a.frequencies[threadIdx.x]);
+  turns.load(a.frequencies, a.rot);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kind = static_cast<int>(blockIdx.x) >= shares.blocks[0];  // 0 queries, 1 keys

@@ -69,3 +69,27 @@ def test_next_to_quarter_turns(ops, quarter):
         # the turns are rounded to 53 bits, which is 2^-53 of `quarter` quarter turns
         assert ((x - ref).abs() <= BF16 * ref.abs() + (1 + BF16) * (2.0 ** -20 * ref.abs() + 2.0 ** -51 * abs(quarter) * math.pi / 2)).all()
     device_ok()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_frequencies_that_are_not_finite(ops, layout):
+    """Their pairs are NaN at every position, forward and back, and no others."""
+    f = ops.rotary_frequencies(D)
+    broken = f.clone()
+    broken[3], broken[17], broken[63] = float("nan"), float("inf"), -float("inf")
+    hit = torch.zeros(64, dtype=torch.bool, device="cuda")
+    hit[[3, 17, 63]] = True
+    positions = torch.tensor([0, 1, -5, 100000], dtype=torch.int32, device="cuda")
+    for way in ("forward", "back"):
+        for got, want in zip(parts(ops, positions, broken, layout, way), parts(ops, positions, f, layout, way)):
+            assert got[:, hit].isnan().all() and torch.equal(got[:, ~hit], want[:, ~hit])
+    x, w = torch.ones(4, 2, D, dtype=BF, device="cuda"), torch.ones(D, dtype=BF, device="cuda")
+    g, _, gw, _ = ops.qk_rotary_bwd(x, None, x, None, positions, broken, w, layout=layout)
+    gw = gw.view(2, 64).t() if layout == "half" else gw.view(64, 2)
+    assert g.isnan().all() and gw[hit].isnan().all() and gw[~hit].isfinite().all()
+    cache = ops.QuantizedCache.empty(4, 2)
+    ops.cache_write(cache, torch.arange(4, dtype=torch.int32, device="cuda"), x, x, None, positions, broken, layout=layout)
+    k, v = ops.cache_read(cache, torch.arange(4, dtype=torch.int32, device="cuda"))
+    k = k.unflatten(-1, (2, 64)).movedim(-2, -1) if layout == "half" else k.unflatten(-1, (64, 2))
+    assert k[:, :, hit].isnan().all() and k[:, :, ~hit].isfinite().all() and torch.equal(v, x)
+    device_ok()
