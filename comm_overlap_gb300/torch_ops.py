@@ -847,7 +847,7 @@ def cached_attention(q: torch.Tensor, cache: tuple, k_start: torch.Tensor, k_len
     if scale is None:
         scale = HEAD_DIM ** -0.5
     if _short is not None and out is None:
-        y = _short.cached_attention(q, cache, k_start, k_len, prefix, scale, return_lse)
+        y = _short.cached_attention(q, cache, k_start, k_len, prefix, scale, bool(return_lse))
         if y is not None:
             return y if return_lse else y[0]
     index = _device_index("q", q)
