@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -21,6 +22,7 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdomino.so")
 CALLS = os.path.join(HERE, "torch_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS_FOR = os.path.join(OBJ, "torch_calls.for")  # the PyTorch that it was built for
 HEADER = os.path.join(ROOT, "include", "domino.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -63,9 +65,17 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _torch_version() -> str:
+    return importlib.metadata.version("torch")
+
+
 def _calls_need_build() -> bool:
+    """Also for another PyTorch, whose tensors may be laid out in another way."""
     t = os.path.getmtime(CALLS) if os.path.exists(CALLS) else 0
-    return any(os.path.getmtime(p) > t for p in (CALLS_SRC, HEADER, __file__))
+    if any(os.path.getmtime(p) > t for p in (CALLS_SRC, HEADER, __file__)) or not os.path.exists(CALLS_FOR):
+        return True
+    with open(CALLS_FOR, encoding="utf-8") as f:
+        return f.read() != _torch_version()
 
 
 def _build_calls() -> None:
@@ -84,6 +94,9 @@ def _build_calls() -> None:
         sys.stderr.write(f"torch_calls is not built, calls of the cache's operators will take longer:\n{r.stderr[-2000:]}\n")
         return
     os.replace(tmp, CALLS)
+    os.makedirs(OBJ, exist_ok=True)
+    with open(CALLS_FOR, "w", encoding="utf-8") as f:
+        f.write(_torch_version())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -8,6 +8,7 @@
 #include <Python.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
@@ -427,4 +428,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "torch_calls", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit_torch_calls() { return PyModule_Create(&module); }
+// `built_for`: the PyTorch whose headers lay out the tensors that are read here.
+PyMODINIT_FUNC PyInit_torch_calls() {
+  PyObject* const m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -64,7 +64,10 @@ def _shorten(index: int, handle: int) -> None:
     global _short
     try:
         from . import torch_calls
-    except ImportError as e:
+        built, here = torch_calls.built_for, torch.__version__.split("+")[0]
+        if built != here:  # it reads tensors as that version lays them out
+            raise ImportError(f"it was built for PyTorch {built}, this is {here}")
+    except (ImportError, AttributeError) as e:
         warnings.warn(f"calls of the rotation and the 8-bit cache take 10 us longer each: torch_calls is not there ({e})", stacklevel=4)
         return
     torch_calls.use_handle(index, handle)

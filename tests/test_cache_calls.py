@@ -1,6 +1,11 @@
 """The PyTorch functions of the 8-bit cache's attention and the rotation around their short way, without a GPU."""
+import sys
+import types
+
+import pytest
 import torch
 
+from comm_overlap_gb300 import build
 from comm_overlap_gb300 import torch_ops as ops
 
 
@@ -17,3 +22,32 @@ def test_any_true_value_asks_for_the_logarithms(monkeypatch):
     monkeypatch.setattr(ops, "_short", Noted())
     for asked, want in ((True, ("o", "lse")), (1, ("o", "lse")), (torch.tensor(True), ("o", "lse")), (False, "o"), (0, "o"), (None, "o")):
         assert ops.cached_attention(torch.zeros(1), None, None, None, return_lse=asked) == want
+
+
+def test_the_short_way_is_built_again_for_another_pytorch(monkeypatch, tmp_path):
+    build.build()
+    assert not build._calls_need_build()
+    monkeypatch.setattr(build, "_torch_version", lambda: "1.0")
+    assert build._calls_need_build()
+    monkeypatch.undo()
+    monkeypatch.setattr(build, "CALLS_FOR", str(tmp_path / "none"))
+    assert build._calls_need_build()
+
+
+@pytest.mark.parametrize("built", ["1.0", None])
+def test_the_short_way_of_another_pytorch_is_not_taken(monkeypatch, built):
+    """It reads fields of tensors, which lie elsewhere in another version."""
+    import comm_overlap_gb300
+    build.build()
+    from comm_overlap_gb300 import torch_calls
+    assert torch_calls.built_for == torch.__version__.split("+")[0]
+    other = types.ModuleType("comm_overlap_gb300.torch_calls")
+    if built:
+        other.built_for = built
+    other.use = other.use_handle = lambda *a: pytest.fail("it is used")
+    monkeypatch.setitem(sys.modules, "comm_overlap_gb300.torch_calls", other)
+    monkeypatch.setattr(comm_overlap_gb300, "torch_calls", other)
+    monkeypatch.setattr(ops, "_short", None)
+    with pytest.warns(UserWarning, match="torch_calls"):
+        ops._shorten(0, 1)
+    assert ops._short is None
