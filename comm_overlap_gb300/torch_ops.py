@@ -705,14 +705,19 @@ class DominoQKRotary(torch.nn.Module):
         if layout not in LAYOUTS:
             raise ValueError(f"layout must be one of {sorted(LAYOUTS)}")
         self.layout, self.eps, self.amplitude = layout, eps, amplitude
+        self._how = rot, base, scaling
         self.frequencies = rotary_frequencies(rot, base, device=device, **scaling)  # fp64 whatever the module is cast to
         self.q_weight, self.k_weight = (
             torch.nn.Parameter(torch.ones(HEAD_DIM, dtype=_BF16, device=device)) if norm else None for _ in range(2))
 
     def _apply(self, fn, recurse=True):
         super()._apply(fn, recurse)
-        moved = fn(self.frequencies)
-        self.frequencies = self.frequencies.to(moved.device)
+        device = fn(self.frequencies).device
+        if self.frequencies.is_meta and device.type != "meta":  # built without memory, which it gets now
+            rot, base, scaling = self._how
+            self.frequencies = rotary_frequencies(rot, base, device=device, **scaling)
+        else:
+            self.frequencies = self.frequencies.to(device)
         return self
 
     def forward(self, q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor):

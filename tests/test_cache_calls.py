@@ -51,3 +51,18 @@ def test_the_short_way_of_another_pytorch_is_not_taken(monkeypatch, built):
     with pytest.warns(UserWarning, match="torch_calls"):
         ops._shorten(0, 1)
     assert ops._short is None
+
+
+def test_a_module_built_without_memory_gets_its_frequencies():
+    want = ops.DominoQKRotary(64, 5e5, device="cpu", factor=4.0, original=1000)
+    module = ops.DominoQKRotary(64, 5e5, device="meta", factor=4.0, original=1000)
+    assert module.frequencies.is_meta and module.half().frequencies.is_meta
+    module = module.bfloat16().to_empty(device="cpu")
+    assert torch.equal(module.frequencies, want.frequencies) and module.frequencies.dtype == torch.float64
+    module.load_state_dict(want.state_dict())
+    assert torch.equal(module.q_weight, want.q_weight) and module.q_weight.dtype == torch.bfloat16
+    assert torch.equal(module.float().frequencies, want.frequencies)
+    # what a user has put there stays through a cast
+    module.frequencies = want.frequencies * 2
+    assert torch.equal(module.bfloat16().frequencies, want.frequencies * 2)
+    assert module.to("meta").frequencies.is_meta
