@@ -1,6 +1,8 @@
 // ops_api.cu -- the C ABI of the sublayer operators (include/domino.h): argument validation,
 // workspace layout and launches.
+#include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <new>
 
 #include "ops.h"
@@ -52,6 +54,28 @@ domino_status check_ld(int64_t ld, int64_t cols, const char* name) {
 domino_status check_in_place(const void* out, int64_t ld_out, const void* in, int64_t ld_in, int64_t rows, const char* what) {
   if (rows > 1 && in && out == in && ld_out != ld_in)
     return refuse(DOMINO_ERR_INVALID_ARG, std::string(what) + " share their memory with different row strides");
+  return DOMINO_OK;
+}
+
+// Whether rows x cols values of bf16 at `a` and `b` have one in common, where that can be told from one row (equal row strides, or one
+// row); tensors of different strides may lie in each other's gaps and pass.
+bool in_common(const void* a, int64_t cols_a, int64_t ld_a, const void* b, int64_t cols_b, int64_t ld_b, int64_t rows) {
+  if (!a || !b || rows < 1 || cols_a < 1 || cols_b < 1 || (rows > 1 && ld_a != ld_b)) return false;
+  const int64_t ld = (rows > 1 ? ld_a : std::max(cols_a, cols_b)) * 2;
+  const int64_t apart = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b)) - static_cast<int64_t>(reinterpret_cast<uintptr_t>(a));
+  int64_t row = apart / ld, in = apart % ld;  // b's row i begins `in` bytes into a's row i + row
+  if (in < 0) {
+    in += ld;
+    --row;
+  }
+  return (std::abs(row) < rows && in < cols_a * 2) || (std::abs(row + 1) < rows && ld - in < cols_b * 2);
+}
+// An output may not overlap an input, unless (in_place) it is just that.
+domino_status check_apart(const void* out, int32_t heads_out, int64_t ld_out, const void* in, int32_t heads_in, int64_t ld_in, int64_t rows,
+                          bool in_place, const char* what) {
+  if (in_place && out == in) return DOMINO_OK;
+  if (in_common(out, int64_t(heads_out) * 128, ld_out, in, int64_t(heads_in) * 128, ld_in, rows))
+    return refuse(DOMINO_ERR_INVALID_ARG, std::string(what) + " overlap");
   return DOMINO_OK;
 }
 
@@ -570,6 +594,10 @@ domino_status domino_qk_rotary_fwd(domino_handle H, const uint16_t* Q, int64_t l
     DM_TRY(check_tokens(Yk, "Yk", ld_yk, "ld_yk", kv_heads, tokens));
     DM_TRY(check_in_place(Yq, ld_yq, Q, ld_q, tokens, "Yq and Q"));
     DM_TRY(check_in_place(Yk, ld_yk, K, ld_k, tokens, "Yk and K"));
+    DM_TRY(check_apart(Yq, heads, ld_yq, Q, heads, ld_q, tokens, true, "Yq and Q"));
+    DM_TRY(check_apart(Yk, kv_heads, ld_yk, K, kv_heads, ld_k, tokens, true, "Yk and K"));
+    DM_TRY(check_apart(Yq, heads, ld_yq, K, kv_heads, ld_k, tokens, false, "Yq and K"));
+    DM_TRY(check_apart(Yk, kv_heads, ld_yk, Q, heads, ld_q, tokens, false, "Yk and Q"));
     DM_TRY(dm::check_handle(H));
     if (tokens == 0) return DOMINO_OK;
     dm::RotaryArgs a = {};
@@ -632,7 +660,15 @@ domino_status domino_qk_rotary_bwd(domino_handle H, const uint16_t* gYq, int64_t
       if (heads > 0) DM_TRY(check_ptr(gwq, "gwq"));
       if (kv_heads > 0) DM_TRY(check_ptr(gwk, "gwk"));
       DM_TRY(check_ws(workspace, workspace_bytes, rotary_bwd_bytes(tokens, heads, kv_heads)));
+      DM_TRY(check_apart(gQ, heads, ld_gq, Q, heads, ld_q, tokens, true, "gQ and Q"));
+      DM_TRY(check_apart(gK, kv_heads, ld_gk, K, kv_heads, ld_k, tokens, true, "gK and K"));
+      DM_TRY(check_apart(gQ, heads, ld_gq, K, kv_heads, ld_k, tokens, false, "gQ and K"));
+      DM_TRY(check_apart(gK, kv_heads, ld_gk, Q, heads, ld_q, tokens, false, "gK and Q"));
     }
+    DM_TRY(check_apart(gQ, heads, ld_gq, gYq, heads, ld_gyq, tokens, true, "gQ and gYq"));
+    DM_TRY(check_apart(gK, kv_heads, ld_gk, gYk, kv_heads, ld_gyk, tokens, true, "gK and gYk"));
+    DM_TRY(check_apart(gQ, heads, ld_gq, gYk, kv_heads, ld_gyk, tokens, false, "gQ and gYk"));
+    DM_TRY(check_apart(gK, kv_heads, ld_gk, gYq, heads, ld_gyq, tokens, false, "gK and gYq"));
     DM_TRY(dm::check_handle(H));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!norm) {  // the rotation alone: the forward's kernel, turned back
@@ -686,6 +722,9 @@ domino_status domino_cache_write(domino_handle H, const uint16_t* Q, int64_t ld_
     DM_TRY(check_tokens(Yq, "Yq", ld_yq, "ld_yq", heads, tokens));
     if (heads > 0) DM_TRY(check_in_place(Yq, ld_yq, Q, ld_q, tokens, "Yq and Q"));
     if (tokens > 0) DM_TRY(check_list(rows, "rows", 4));
+    DM_TRY(check_apart(Yq, heads, ld_yq, Q, heads, ld_q, tokens, true, "Yq and Q"));
+    DM_TRY(check_apart(Yq, heads, ld_yq, K, kv_heads, ld_k, tokens, false, "Yq and K"));
+    DM_TRY(check_apart(Yq, heads, ld_yq, V, kv_heads, ld_v, tokens, false, "Yq and V"));
     DM_TRY(dm::check_handle(H));
     if (tokens == 0) return DOMINO_OK;
     dm::RotaryArgs a = {Q, K, V, positions, frequencies, wq, wk, Yq, nullptr, k8, v8, k_exp, v_exp, rows, tokens, ld_q, ld_k, ld_v,
@@ -742,6 +781,7 @@ domino_status domino_attn_cached_fwd(domino_handle H, const uint16_t* Q, int64_t
       DM_TRY(check_list(k_len, "k_len", 4));
       if (prefix) DM_TRY(check_list(prefix, "prefix", 4));
       if (O == Q) return refuse(DOMINO_ERR_INVALID_ARG, "O may not be Q");
+      DM_TRY(check_apart(O, heads, ld_o, Q, heads, ld_q, tokens, false, "O and Q"));
       DM_TRY(check_ws(workspace, workspace_bytes, size_t(dm::cached_scratch_bytes(a))));
     }
     DM_TRY(dm::check_handle(H));

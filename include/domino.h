@@ -365,10 +365,12 @@ DOMINO_API domino_status domino_attn_packed_fwd(domino_handle handle, const uint
  * i + rot / 2 (layout DOMINO_ROTARY_HALF) or 2 i and 2 i + 1 (DOMINO_ROTARY_INTERLEAVED), i < rot / 2; the
  * others stay.  fp32 arithmetic, one rounding to bf16.
  *   Q, Yq: tokens x heads x 128, K, Yk: tokens x kv_heads x 128 (kv_heads = 0: no keys), row strides ld_* in
- *   elements (multiples of 8), so that Q and K may be slices of a fused projection; Yq may be Q and Yk K,
- *   with the same strides.  positions: tokens int32 (any value); frequencies: rot / 2 doubles, radians a
- *   position, both on the device.  Cosines and sines are good to fp32, each to its own size, for the frequency as a
- *   multiple of 2^-64 turns, which takes it to 53 bits: an angle is off by at most 2^-52 of itself and |position| 2^-62. */
+ *   elements (multiples of 8), so that Q and K may be slices of a fused projection; Yq may be Q and Yk K, with the
+ *   same strides.  No other overlap of an output with an input is allowed, here and in the two calls below; it is
+ *   refused where the row strides are equal.  positions: tokens int32 (any value); frequencies: rot / 2 doubles,
+ *   radians a position, both on the device.  Cosines and sines are good to fp32, each to its own size, for the frequency
+ *   as a multiple of 2^-64 turns, which takes it to 53 bits: an angle is off by at most 2^-52 of itself and
+ *   |position| 2^-62.  A frequency that is not finite gives NaN. */
 typedef enum { DOMINO_ROTARY_HALF = 0, DOMINO_ROTARY_INTERLEAVED = 1 } domino_rotary_layout;
 DOMINO_API domino_status domino_qk_rotary_fwd(domino_handle handle, const uint16_t* Q, int64_t ld_q, const uint16_t* K,
                                               int64_t ld_k, const int32_t* positions, const double* frequencies,
@@ -433,7 +435,7 @@ DOMINO_API domino_status domino_cache_read(domino_handle handle, const uint8_t* 
  * Rows that a query does not see have no effect on it, whatever their codes and exponents.  Lengths are read on
  * the device: a sequence (or prefix) whose rows leave the cache has no keys and is recorded (domino_device_status).
  * Exponents are those of domino_cache_write (2^-51 to 2^51).  scale: > 0, at most 8192.  Equal inputs give equal
- * bits.  O may not overlap Q.  Any t is taken; every further 32 rows (t x heads / kv_heads, with a prefix those of all
+ * bits.  O may not overlap Q (refused where the row strides are equal).  Any t is taken; every further 32 rows (t x heads / kv_heads, with a prefix those of all
  * sequences together) read the keys again.
  * Workspace: domino_attn_cached_workspace_size() bytes, without initialisation (2.6 to 10.3 MB, and with a prefix 1056
  * bytes a query and head). */
