@@ -58,7 +58,7 @@ template <int R>
 struct Shape {
   static constexpr int kRows = R < 16 ? R : 16, kGroups = R / kRows;  // groups of 128 threads that hold keys, and the rows of each
   static constexpr int kThreads = 64 + 128 * kGroups;                 // warps: 0 loads, 1 issues, from 2 on keys
-  static constexpr uint32_t kSlots = R < 32 ? 5 : 4;                  // (six for 8 rows: 64 sequences of up to 8000 keys 98 us, five 92)
+  static constexpr uint32_t kSlots = R < 32 ? 5 : 4;                  // (six for 8 rows: 64 sequences of up to 8000 keys 91.6 us, five 88.4)
   static constexpr uint32_t kCols = 2 * R, kTerms = kRows;            // columns of scores; of one term of a group's O
   static constexpr uint32_t kOutCols = R == 8 ? 32 : 3 * R;           // of O (a product has a multiple of 16: 8 unused)
   static constexpr uint32_t kTmem = R == 8 ? 64 : R == 16 ? 128 : 256;
@@ -69,14 +69,14 @@ struct Shape {
 };
 // Weights are 2^kRaise where t is the maximum that m was taken from; the maximum may rise by kBehind (in base 2) before O and the
 // denominator are brought to a new m, so that they stay below E5M2's 57344 = 2^15.807.  (With less to rise m moves more often, at 1 us a
-// time; with a lower start more of the small weights is lost.)
+// time: 48 sequences behind 16001 shared rows 66.2 us with 4.8, 63.1 so; with a lower start more of the small weights is lost.)
 constexpr float kRaise = 9.0f, kBehind = 6.75f;
 constexpr float kTerm = 0.0625f;                      // of q's second terms
 constexpr float kSecond = 0.125f, kThird = 0.03125f;  // of the weights' terms
 
 // ---- work: tiles of all items (sequence, block of rows, `abreast` key heads) in order.  What an item costs beside its tiles counts as
-// kItem of them, before its first: units.  (16 sequences of up to 3001 keys, 35 rows each for 4 heads: 32.3 us without, 29.7 so, 29.8 with
-// two.)
+// kItem of them, before its first: units.  (256 tokens over up to 1000 keys of one head 22.7 us without, 19.4 so, 18.5 with two; 48 sequences
+// behind 16001 shared rows 71.8, 63.1, 65.0.)
 constexpr int kItem = 1;
 
 struct CachedHeader {
@@ -207,7 +207,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 // A tile of codes to shared memory, the first to leave L2 again: they are read once, or by blocks that run at about the same time (64
-// sequences of up to 8000 keys 98.8 us, 100.4 without).
+// sequences of up to 8000 keys 88.4 us, 92.2 without).
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t policy;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
@@ -379,8 +379,8 @@ __device__ __noinline__ void prepare_rows(const CachedArgs& a, int s, int len, i
 }
 
 // Whether the threads that hold the keys prepare an item's rows (the range's first they always do).  The loading warp takes 2.5 us for
-// eight, while the others work on the item before, but ten for 32: 16 sequences of up to 3001 keys, 35 rows each for 4 heads 29.7 us if it
-// prepares all, 27.4 so.
+// eight, while the others work on the item before, but ten for 32: 16 sequences of up to 3001 keys, 35 rows each for 4 heads 32.0 us if it
+// prepares all, 28.8 so.
 template <int R>
 __device__ __forceinline__ bool keys_prepare(const CachedArgs& a, const Piece& p) {
   return R > 8 && rows_of(a, p.s) - p.block * R > 8;
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
             }
           }
           // the rows' maxima.  Where one is well above m, m moves, and with it those of its eight rows that have risen at all: what costs is
-          // the visit (1 us; 18 of 100 tiles of 48 rows over 16001 keys had one, 64.5 us, now 62.5), not the row.
+          // the visit (1 us; when 4.8 were left to rise, 18 of 100 tiles of 48 rows over 16001 keys had one, and 64.5 us became 62.5), not the row.
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if (c < chunks && (flags >> c & 1u)) {

@@ -30,8 +30,9 @@ namespace {
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kHeadsAbreast = 4;  // a warp's step has twice as many: with one four at a time the address and loop work weighs as much as the heads'
 constexpr int kReadAbreast = 2;   // pieces of a lane in flight: with 4 a token of 8 heads leaves half the lanes idle
-// Blocks of an SM and steps in flight of a warp: the registers that two halves of a step take, and 200 KB of copies in flight on an SM (72 KB
-// for the cache, whose blocks wait less for memory than for the conversions).
+// Blocks of an SM and steps in the ring of a warp: the registers that two halves of a step take, and rings of 192 KB on an SM, of which one
+// step is being read and 168 KB (backward 144) are in flight (96 KB and 64 for the cache, whose blocks wait less for memory than for the
+// conversions).
 constexpr int kFwdBlocks = 3, kFwdDepth = 8, kWriteBlocks = 4, kWriteDepth = 3, kBwdBlocks = 3, kBwdDepth = 4;
 // Blocks of two kinds of heads, and the warps that share a token's steps.
 struct RotaryShares {
@@ -75,7 +76,7 @@ struct Turns {
     if (i >= (rot >> 1)) return;
     const double f = frequencies[i];
     of[i] = turn_fraction(f);
-    one[i] = f - f == 0.0 ? 1.0f : NAN;
+    one[i] = (__double2hiint(f) & 0x7FF00000) != 0x7FF00000 ? 1.0f : NAN;  // (fp64 arithmetic is slow here, and the blocks wait for it)
   }
 };
 
