@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(Shape<R>::kThreads, kBlocks)
         if (__builtin_expect(flags != 0, 0)) {
           // A value of zeros adds nothing to O, so it may not set the m of those that do (the cache gives it 2^0, and values of size 0.05 have
           // 2^-11): its power of two counts as the least.  So does that of zeros and NaN, which is NaN with any weight.  (Looked at where m moves
-          // alone, so that only items' first tiles wait for their values: 48 sequences behind 16001 shared rows 62.5 us, 61.5 without.)
+          // alone, so that only items' first tiles wait for their values: 48 sequences behind 16001 shared rows 63.2 us, 61.4 without.)
           {
             const uint32_t slot_v = (2 * j + 1) % kSlots, v_at = ring + slot_v * kTile;
             wait(B_FULL + slot_v, (2 * j + 1) / kSlots, 15);

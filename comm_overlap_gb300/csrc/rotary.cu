@@ -14,8 +14,8 @@
 // nearest quarter turn goes to sincospif.
 //
 // Bound: memory.  Forward 4 bytes a value, backward 6 (4 without norm), cache 3.  16384 tokens of 32 query and 8 key heads with norm: forward
-// 57.4 us (5.8 TB/s, as a copy of the same bytes; 69 with loads into registers a step ahead), backward 86 (5.9), into the cache 64.6 (369 MB, 5.7);
-// 147456 rows of 8 heads read back 141.6 (906 MB, 6.4).
+// 57.7 us (5.8 TB/s, as a copy of the same bytes; 69 with loads into registers a step ahead), backward 82.6 (6.1), into the cache 64.9 (369 MB, 5.7);
+// 147456 rows of 8 heads read back 142.5 (906 MB, 6.4).
 #include <atomic>
 
 #include "actfn.cuh"
