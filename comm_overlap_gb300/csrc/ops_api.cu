@@ -660,6 +660,8 @@ domino_status domino_qk_rotary_bwd(domino_handle H, const uint16_t* gYq, int64_t
       if (heads > 0) DM_TRY(check_ptr(gwq, "gwq"));
       if (kv_heads > 0) DM_TRY(check_ptr(gwk, "gwk"));
       DM_TRY(check_ws(workspace, workspace_bytes, rotary_bwd_bytes(tokens, heads, kv_heads)));
+      DM_TRY(check_in_place(gQ, ld_gq, Q, ld_q, tokens, "gQ and Q"));
+      DM_TRY(check_in_place(gK, ld_gk, K, ld_k, tokens, "gK and K"));
       DM_TRY(check_apart(gQ, heads, ld_gq, Q, heads, ld_q, tokens, true, "gQ and Q"));
       DM_TRY(check_apart(gK, kv_heads, ld_gk, K, kv_heads, ld_k, tokens, true, "gK and K"));
       DM_TRY(check_apart(gQ, heads, ld_gq, K, kv_heads, ld_k, tokens, false, "gQ and K"));

@@ -75,3 +75,4 @@ def test_in_place_and_crosswise():
     assert "gQ and gYk overlap" in backward(gQ=P + 9 * HEAD) and "gK and gYq overlap" in backward(gK=P + 6 * HEAD)
     assert "gK and K overlap" in backward(gK=2 * FAR + 9 * HEAD)
     assert "Yq and K overlap" in write(Yq=P + 9 * HEAD) and "Yq and V overlap" in write(Yq=P + 11 * HEAD)
+    assert "different row strides" in backward(gQ=2 * FAR, ld_gq=2 * LD) and "different row strides" in backward(gK=2 * FAR + 8 * HEAD, ld_gk=2 * LD)
