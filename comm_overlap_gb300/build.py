@@ -66,7 +66,11 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def _torch_version() -> str:
-    return importlib.metadata.version("torch")
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # one that runs from its sources
+        import torch
+        return torch.__version__
 
 
 def _calls_need_build() -> bool:

@@ -22,6 +22,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import re
 import threading
 import warnings
 from typing import NamedTuple
@@ -64,9 +65,9 @@ def _shorten(index: int, handle: int) -> None:
     global _short
     try:
         from . import torch_calls
-        built, here = torch_calls.built_for, torch.__version__.split("+")[0]
-        if built != here:  # it reads tensors as that version lays them out
-            raise ImportError(f"it was built for PyTorch {built}, this is {here}")
+        built = torch_calls.built_for  # three numbers; what follows them here names the build
+        if re.match(r"\d+\.\d+\.\d+", torch.__version__).group() != built:  # it reads tensors as that version lays them out
+            raise ImportError(f"it was built for PyTorch {built}, this is {torch.__version__}")
     except (ImportError, AttributeError) as e:
         warnings.warn(f"calls of the rotation and the 8-bit cache take 10 us longer each: torch_calls is not there ({e})", stacklevel=4)
         return

@@ -32,6 +32,25 @@ def test_the_short_way_is_built_again_for_another_pytorch(monkeypatch, tmp_path)
     monkeypatch.undo()
     monkeypatch.setattr(build, "CALLS_FOR", str(tmp_path / "none"))
     assert build._calls_need_build()
+    monkeypatch.undo()
+
+    def unknown(name):
+        raise build.importlib.metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(build.importlib.metadata, "version", unknown)
+    assert build._torch_version() == torch.__version__
+
+
+def test_the_short_way_is_taken_in_any_build_of_its_version(monkeypatch):
+    build.build()
+    from comm_overlap_gb300 import torch_calls
+    monkeypatch.setattr(ops, "_short", None)
+    monkeypatch.setattr(torch, "__version__", torch_calls.built_for + "a0+145a3a7.other")
+    used = []
+    monkeypatch.setattr(torch_calls, "use", lambda *a: used.append(a))
+    monkeypatch.setattr(torch_calls, "use_handle", lambda *a: None)
+    ops._shorten(0, 0)
+    assert ops._short is torch_calls and used
 
 
 @pytest.mark.parametrize("built", ["1.0", None])
@@ -40,7 +59,7 @@ def test_the_short_way_of_another_pytorch_is_not_taken(monkeypatch, built):
     import comm_overlap_gb300
     build.build()
     from comm_overlap_gb300 import torch_calls
-    assert torch_calls.built_for == torch.__version__.split("+")[0]
+    assert torch.__version__.startswith(torch_calls.built_for)
     other = types.ModuleType("comm_overlap_gb300.torch_calls")
     if built:
         other.built_for = built
